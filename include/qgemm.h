@@ -60,15 +60,19 @@ struct CUstream_st; /* the same type as cudaStream_t */
 typedef enum {
     QG_OK = 0,
     QG_ERR_INVALID_ARG = 1,       /* null pointer, negative size, ld < row length */
-    QG_ERR_UNSUPPORTED_SHAPE = 2, /* M > 32 (65536 for W8A8), K % 16 (FP8, W8A8), K % 128 (LUT3)
-                                     or K % 8 (BF16) != 0 */
+    QG_ERR_UNSUPPORTED_SHAPE = 2, /* M > 32 (65536 for W8A8, INT8), K % 16 (FP8, W8A8, INT8), K % 128 (LUT3)
+                                     or K % 8 (BF16) != 0; log probabilities: V == 0, top_k > V or
+                                     > QG_MAX_TOP_K */
     QG_ERR_MISALIGNED = 3,        /* a pointer or row stride breaks the 16-byte rule */
     QG_ERR_CUDA = 4,              /* a CUDA runtime call or kernel launch failed */
     QG_ERR_TIMEOUT = 5,           /* a bounded in-kernel wait ran out */
     QG_ERR_WORKSPACE = 6          /* workspace missing or smaller than qg_workspace_bytes */
 } qg_status;
 
-enum { QG_KIND_FP8_BLOCK = 0, QG_KIND_LUT3 = 1, QG_KIND_BF16 = 2, QG_KIND_W8A8 = 3 };
+enum { QG_KIND_FP8_BLOCK = 0, QG_KIND_LUT3 = 1, QG_KIND_BF16 = 2, QG_KIND_W8A8 = 3, QG_KIND_INT8 = 4 };
+
+/* Element types of the entry points that take one as an argument. */
+enum { QG_BF16 = 0, QG_FP16 = 1, QG_FP32 = 2 };
 
 /*
  * Bytes of device workspace a call of the given kind and shape needs on the
@@ -82,6 +86,12 @@ enum { QG_KIND_FP8_BLOCK = 0, QG_KIND_LUT3 = 1, QG_KIND_BF16 = 2, QG_KIND_W8A8 =
  * without clearing.  The W8A8 kind lays its workspace out differently (wider
  * partial sums): a workspace serves either QG_KIND_W8A8 calls or calls of
  * the other kinds, not both, unless it is zero-filled again in between.
+ * QG_KIND_INT8 has a layout of its own too: 16384 bytes of arrival counters
+ * (at the front for every shape), the activations expanded to FP16 (2 M K
+ * bytes rounded up to 256), then the partial sums of a schedule that splits
+ * tiles (two slots of 512 R bytes for each CTA, R = the rows of a tile: 16,
+ * 32, 64 or 128); its workspace serves INT8 calls of any shape, and no other
+ * kind.
  */
 size_t qg_workspace_bytes(int kind, int M, int N, int K);
 
@@ -290,6 +300,89 @@ qg_status qgemm_w8a8_block(const uint8_t *Xq, int64_t ldxq, const float *X_scale
                            struct CUstream_st *stream);
 
 /*
+ * 8-bit integer activation quantiser, one scale per token (an addition of
+ * this library, with no counterpart in the paper).  For every row m, in FP32:
+ *   a          = max_k |X[m, k]|
+ *   X_scale[m] = a / 127
+ *   Xq[m, k]   = X[m, k] * (127 * (1 / a)), rounded half to even (-127 .. 127)
+ * and a row with a < 2^-100 has codes 0 and scale 1.  Bit-exact: the same FP32
+ * operations, each rounded to nearest (per row two divisions and a product,
+ * per element one product), on every device.
+ *   X        device, QG_BF16 or QG_FP16 [M, ldx], 16-byte aligned, ldx >= K,
+ *            ldx % 8 == 0
+ *   Xq       device, int8 [M, ldxq], 16-byte aligned, ldxq >= K, ldxq % 16 == 0
+ *   X_scale  device, FP32 [M]
+ *   M, K     0 <= M <= 65536, K % 16 == 0 (nothing is written when K == 0)
+ * Finite inputs only (the codes of a row with Inf or NaN are unspecified).
+ */
+qg_status qg_quantize_act_int8(const void *X, int x_type, int64_t ldx, int8_t *Xq, int64_t ldxq,
+                               float *X_scale, int M, int K, struct CUstream_st *stream);
+
+/*
+ * 8-bit integer GEMM with one scale per token and one per channel (an
+ * addition of this library, with no counterpart in the paper):
+ *   Y[m, n] = X_scale[m] * W_scale[n] * sum_k Xq[m, k] * W[n, k] + bias[n]
+ * The products and their sum are exact integers while every partial sum
+ * stays below 2^24 in magnitude (always for K <= 1024); a sum beyond that is
+ * rounded in FP32.  The scales and the bias are applied in FP32, then Y is
+ * rounded once to its type.
+ *   Xq       device, int8 [M, ldxq] (all of -128 .. 127), 16-byte aligned,
+ *            ldxq >= K, ldxq % 16 == 0
+ *   X_scale  device, FP32 [M]
+ *   W        device, int8 [N, K] row-major (row stride K bytes), 16-byte
+ *            aligned
+ *   W_scale  device, FP32 [N]
+ *   bias     device, FP32 [N], or NULL for none
+ *   Y        device, [M, ldy] of y_type (QG_BF16, QG_FP16 or QG_FP32),
+ *            aligned to its element, ldy >= N
+ *   M, N, K  1 <= M <= 65536, N >= 1, K % 16 == 0; K == 0 writes the bias
+ *            (or zeros) to every row
+ *   workspace  at least qg_workspace_bytes(QG_KIND_INT8, M, N, K) bytes,
+ *            zero-filled before its first use, 256-byte aligned (every
+ *            INT8 call needs one: it holds the activations as FP16)
+ * A call launches two kernels: the expansion of the activations, and the
+ * GEMM, whose weight stream starts under it.
+ */
+qg_status qgemm_w8a8_int8(const int8_t *Xq, int64_t ldxq, const float *X_scale,
+                          const int8_t *W, const float *W_scale, const float *bias,
+                          void *Y, int y_type, int64_t ldy,
+                          int M, int N, int K,
+                          void *workspace, size_t workspace_bytes,
+                          struct CUstream_st *stream);
+
+/*
+ * Log probabilities of given tokens, entropy and top alternatives over rows
+ * of logits, such as an lm_head's output (an addition of this library, with
+ * no counterpart in the paper).  With x = logits[m, 0 .. V-1] and
+ * p = softmax(x), in FP32 and natural logarithms:
+ *   token_logprobs[m * T + t] = ln p[tokens[m * ldt + t]]
+ *   entropy[m]                = - sum_v p[v] ln p[v]   (0 ln 0 = 0)
+ *   top_ids[m * top_k + j], top_logprobs[m * top_k + j]
+ *                             = the j-th largest logit's index and ln p; equal
+ *                               logits go by the lower index
+ *   logits   device, [M, ld] of `type` (QG_BF16, QG_FP16 or QG_FP32), aligned
+ *            to its element, ld >= V (any row may start at any element)
+ *   tokens   device, int64 [M, ldt], ldt >= T; T >= 0 tokens asked in each row
+ *   entropy  device, FP32 [M], or NULL; top_k 0 .. QG_MAX_TOP_K and <= V (the
+ *            outputs of a part not asked for may be NULL)
+ *   M, V     M >= 0 rows (M == 0 is a no-op), V >= 1
+ * A masked token is one whose logit is -inf: its log probability is -inf and
+ * it comes after every other alternative.  A row that is all -inf has no
+ * distribution: all its log probabilities are -inf, its entropy is 0 and its
+ * alternatives are the tokens 0, 1, ...  A token outside 0 .. V-1 has log
+ * probability -inf.  A row holding a NaN or +inf has NaN for its entropy and
+ * for the log probability of every token within 0 .. V-1; its alternatives
+ * are ordered with NaN above +inf.
+ */
+#define QG_MAX_TOP_K 32
+
+qg_status qg_logprobs(const void *logits, int type, int64_t ld,
+                      const int64_t *tokens, int64_t ldt, int T,
+                      float *token_logprobs, float *entropy,
+                      int top_k, int64_t *top_ids, float *top_logprobs,
+                      int M, int V, struct CUstream_st *stream);
+
+/*
  * Packed size, in bytes, of an [N, K] 3-bit code matrix:
  * ceil(N/128) * ceil(K/256) * 16384.
  */
@@ -357,7 +450,8 @@ qg_status qg_dequant_lut3(const void *Wq, const void *qmap, const void *scales,
  *
  * qg_dispatch_set: ctas in 1 .. SM count of the current device sets the
  *   entry (a grid larger than the shape's work units is cut to their
- *   number); ctas == 0 removes it.  M in 1..32 (1..65536 for QG_KIND_W8A8).
+ *   number); ctas == 0 removes it.  M in 1..32 (1..65536 for QG_KIND_W8A8
+ *   and QG_KIND_INT8).
  * qg_dispatch_get: the grid the next call of the shape launches on the
  *   current device (0 for invalid arguments).
  * qg_dispatch_rule: the grid the built-in cost rule picks for the shape on

@@ -1,0 +1,274 @@
+"""Log probabilities, entropy and top alternatives against 64-bit arithmetic.
+
+Bounds (u = 2^-24, D = the row's range of finite logits, at most 104 where a
+term still counts): each exponential is off by 4 u from the instruction and by
+at most D u from its argument, a thread's running sums by one u per term and
+the joining trees by 32 u, so the sums are off by
+    R = (4 + 2 min(D, 104) + V / 128 + 32) u
+relatively; a log probability by R plus 4 u of its size (and of D), the
+entropy by R (2 + 2 ln V + 2 H)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import qg
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+INF = float("inf")
+
+
+def _reference(x, tokens, k):
+    """x: float64 [M, V] on the CPU."""
+    M, V = x.shape
+    lp = np.full((M, V), -np.inf)
+    H = np.zeros(M)
+    for m in range(M):
+        r = x[m]
+        if np.isnan(r).any() or (r == np.inf).any():
+            lp[m] = np.nan
+            H[m] = np.nan
+            continue
+        mx = r.max()
+        if mx == -np.inf:
+            continue
+        d = r - mx
+        s = np.exp(d).sum()
+        lp[m] = d - math.log(s)
+        p = np.exp(lp[m])
+        H[m] = -(p[p > 0] * lp[m][p > 0]).sum()
+    key = np.where(np.isnan(x), np.inf, x)
+    ids = np.empty((M, k), np.int64)
+    for m in range(M):
+        order = np.lexsort((np.arange(V), -key[m], ~np.isnan(x[m])))
+        ids[m] = order[:k]
+    tok = np.array([[lp[m, t] if 0 <= t < V else -np.inf for t in tokens[m]] for m in range(M)])
+    return lp, tok.reshape(M, -1), H, ids
+
+
+def _check(logits, tokens, k):
+    q = qg()
+    M, V = logits.shape
+    r = q.logprobs(logits, torch.from_numpy(tokens).cuda(), top_k=k, entropy=True)
+    assert q.last_device_status() == 0
+    x = logits.double().cpu().numpy()
+    lp, tok, H, ids = _reference(x, tokens, k)
+    fin = np.where(np.isfinite(x), x, np.nan)
+    with np.errstate(all="ignore"):
+        D = np.nan_to_num(np.nanmax(np.where(np.isfinite(fin), fin, -1e300), axis=1) -
+                          np.nanmin(np.where(np.isfinite(fin), fin, 1e300), axis=1), nan=0.0)
+    R = (4 + 2 * np.minimum(np.maximum(D, 0), 104) + V / 128 + 32) * U
+
+    def close(got, want, tol):
+        same = (got == want) | (np.isnan(got) & np.isnan(want))
+        with np.errstate(all="ignore"):
+            ok = same | (np.isfinite(want) & (np.abs(got - want) <= tol))
+        assert ok.all(), (np.argwhere(~ok)[:4].tolist(), got[~ok][:4], want[~ok][:4])
+
+    with np.errstate(all="ignore"):
+        got = r.token_logprobs.double().cpu().numpy().reshape(M, -1)
+        close(got, tok, R[:, None] + 4 * U * np.abs(tok))
+        close(r.entropy.double().cpu().numpy(), H, R * (2 + 2 * math.log(max(V, 2)) + 2 * np.abs(H)))
+        if k:
+            assert np.array_equal(r.top_ids.cpu().numpy(), ids)
+            want = np.take_along_axis(lp, ids, axis=1)
+            close(r.top_logprobs.double().cpu().numpy(), want, R[:, None] + 4 * U * np.abs(want))
+    return r
+
+
+def _logits(M, V, dtype, seed, pad=0, offset=0, scale=2.5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    buf = torch.full((M * (V + pad) + offset,), 1e4, dtype=DT[dtype], device="cuda")   # a large value if read by mistake
+    rows = buf[offset:].view(M, V + pad)[:, :V]
+    rows.copy_(torch.randn(M, V, generator=g, device="cuda") * scale)
+    return rows
+
+
+def _tokens(M, T, V, seed=1):
+    return np.random.default_rng(seed).integers(0, V, size=(M, T))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,V,T,k,pad,offset", [
+    (1, 1, 1, 1, 0, 0), (1, 2, 1, 2, 0, 1), (3, 7, 2, 7, 3, 1), (2, 31, 1, 31, 0, 3), (5, 33, 1, 32, 0, 1),
+    (1, 1000, 1, 5, 0, 0), (7, 1003, 3, 20, 0, 1), (4, 4099, 1, 8, 13, 5), (33, 32768, 1, 5, 0, 0),
+    (2, 50021, 4, 20, 27, 7), (1, 131072, 1, 20, 0, 0), (9, 100003, 1, 32, 0, 3), (300, 2050, 1, 1, 2, 1),
+    (700, 517, 1, 3, 0, 0),
+])
+def test_matches_64_bits(dtype, M, V, T, k, pad, offset):
+    _check(_logits(M, V, dtype, M + V, pad, offset), _tokens(M, T, V), k)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_masked_and_empty_rows(dtype):
+    """Masks as -inf: all but one token, fewer tokens than alternatives asked,
+    scattered, one contiguous run, and nothing left."""
+    V = 20011
+    x = _logits(8, V, dtype, 5)
+    keep = torch.zeros(8, V, dtype=torch.bool, device="cuda")
+    keep[0, 777] = True
+    keep[1, [3, 9000, 20010]] = True
+    keep[2, ::97] = True
+    keep[3, 4096:4200] = True
+    keep[5] = True
+    keep[5, :8192] = False
+    keep[6, :5] = True
+    keep[7] = torch.rand(V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)) < 0.5
+    x.masked_fill_(~keep, -INF)
+    tokens = _tokens(8, 3, V)
+    tokens[0, 0], tokens[1, 1], tokens[4, 0] = 777, 9000, 0
+    r = _check(x, tokens, 20)
+    assert r.top_ids[4].tolist() == list(range(20)) and float(r.entropy[4]) == 0.0
+    assert r.top_ids[0, :3].tolist() == [777, 0, 1]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_lowest_value_masks(dtype):
+    """Masks as the type's lowest value; a row of nothing else is uniform."""
+    V = 5003
+    low = torch.finfo(DT[dtype]).min
+    x = _logits(4, V, dtype, 6)
+    x[0] = low
+    x[1, 10:] = low
+    x[2, ::2] = low
+    x[3] = low
+    x[3, 5:4000] = -INF
+    r = _check(x, _tokens(4, 2, V), 12)
+    assert abs(float(r.entropy[0]) - math.log(V)) < 1e-4
+    assert r.top_ids[3].tolist()[:6] == [0, 1, 2, 3, 4, 4000]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_ties_go_to_the_lower_index(dtype):
+    V = 30011
+    x = _logits(5, V, dtype, 8)
+    x[0] = 1.5
+    x[1] = torch.arange(V, device="cuda") % 3
+    x[2, 100::64] = 30.0
+    x[3] = torch.where(torch.arange(V, device="cuda") % 2 == 0, 0.0, -0.0)
+    x[4] = (x[4] * 2).round() / 2
+    _check(x, _tokens(5, 1, V), 32)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_nan_and_infinity(dtype):
+    V = 9001
+    x = _logits(5, V, dtype, 9)
+    x[0, 17] = float("nan")
+    x[1, 8000] = INF
+    x[2, 3] = INF
+    x[2, 4000] = float("nan")
+    x[2, 9000] = -float("nan")
+    x[3, 0] = -INF
+    tokens = _tokens(5, 2, V)
+    tokens[0, 0] = -1
+    tokens[4] = (V, -100)
+    r = _check(x, tokens, 4)
+    assert r.top_ids[2].tolist()[:3] == [4000, 9000, 3]
+    assert r.token_logprobs[4].tolist() == [-INF, -INF]
+    assert float(r.token_logprobs[0, 0]) == -INF
+
+
+@pytest.mark.parametrize("shift", [3e3, -4e4, 1e9, -3e12, 1e30])
+def test_large_offsets(shift):
+    """A row far from zero: its differences are what 32 bits hold of them."""
+    V = 4001
+    x = _logits(3, V, "fp32", 10) + shift
+    _check(x, _tokens(3, 1, V), 10)
+
+
+def test_peaked_and_rising_rows():
+    """A maximum that keeps moving (ascending logits), and one token that
+    holds all the probability."""
+    V = 70000
+    x = torch.empty(3, V, device="cuda")
+    x[0] = torch.linspace(-50, 50, V, device="cuda")
+    x[1] = torch.linspace(50, -50, V, device="cuda")
+    x[2] = 0.0
+    x[2, 61234] = 90.0
+    _check(x, np.array([[V - 1, 0], [0, 5], [61234, 1]]), 20)
+
+
+def test_more_rows_than_64_thousand():
+    V = 40
+    x = _logits(70001, V, "bf16", 12)
+    q = qg()
+    r = q.logprobs(x, top_k=2)
+    ref = torch.log_softmax(x.double(), dim=1)
+    top = ref.max(dim=1).values
+    assert float((r.top_logprobs[:, 0].double() - top).abs().max()) < 1e-5
+    assert r.entropy is None and r.token_logprobs is None
+
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie beyond 2^32 bytes and 2^31 elements."""
+    V = 131075
+    M = (1 << 31) // V + 3
+    x = torch.zeros(M, V, dtype=torch.bfloat16, device="cuda")
+    x[M - 1, V - 1] = 3.0
+    x[M - 2, 5] = 2.0
+    q = qg()
+    r = q.logprobs(x, torch.full((M,), V - 1, dtype=torch.int64, device="cuda"), top_k=1, entropy=True)
+    assert r.top_ids[M - 1, 0].item() == V - 1 and r.top_ids[M - 2, 0].item() == 5 and r.top_ids[0, 0].item() == 0
+    want = 3.0 - math.log(V - 1 + math.exp(3.0))
+    assert abs(r.token_logprobs[M - 1].item() - want) < 1e-4
+    del x
+    torch.cuda.empty_cache()
+
+
+def test_parts_on_their_own_and_other_streams():
+    q = qg()
+    V = 33333
+    x = _logits(6, V, "bf16", 13)
+    tok = torch.from_numpy(_tokens(6, 1, V)).cuda()
+    full = q.logprobs(x, tok, top_k=7, entropy=True)
+    assert torch.equal(q.logprobs(x, tok[:, 0]).token_logprobs, full.token_logprobs[:, 0])
+    assert torch.equal(q.logprobs(x, entropy=True).entropy, full.entropy)
+    part = q.logprobs(x, top_k=7)
+    assert torch.equal(part.top_ids, full.top_ids) and torch.equal(part.top_logprobs, full.top_logprobs)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        other = q.logprobs(x, tok, top_k=7, entropy=True)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, full))
+    # strided tokens and an expanded column of them
+    wide = torch.zeros(6, 5, dtype=torch.int64, device="cuda")
+    wide[:, 2] = tok[:, 0]
+    assert torch.equal(q.logprobs(x, wide[:, 2]).token_logprobs, full.token_logprobs[:, 0])
+    same = torch.full((1, 1), 9, dtype=torch.int64, device="cuda").expand(6, 3)
+    one = q.logprobs(x, torch.full((6,), 9, dtype=torch.int64, device="cuda")).token_logprobs
+    assert torch.equal(q.logprobs(x, same).token_logprobs, one[:, None].expand(6, 3))
+
+
+def test_results_do_not_depend_on_the_batch():
+    """The same row gives the same bits alone and among others."""
+    q = qg()
+    x = _logits(40, 32768, "bf16", 14)
+    a = q.logprobs(x, top_k=5, entropy=True)
+    again = q.logprobs(x, top_k=5, entropy=True)
+    assert all(torch.equal(u, v) for u, v in zip(a[1:], again[1:]))
+    ids = q.logprobs(x[7:8], top_k=5).top_ids
+    assert torch.equal(ids, a.top_ids[7:8])
+
+
+def test_refusals():
+    q = qg()
+    x = torch.zeros(3, 16, device="cuda")
+    for bad in (lambda: q.logprobs(x.double()), lambda: q.logprobs(x.t()), lambda: q.logprobs(x.cpu(), entropy=True),
+                lambda: q.logprobs(x, torch.zeros(3, dtype=torch.int32, device="cuda")),
+                lambda: q.logprobs(x, torch.zeros(4, dtype=torch.int64, device="cuda")),
+                lambda: q.logprobs(x, torch.zeros(3, dtype=torch.int64))):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    for k in (17, 33):
+        with pytest.raises(q.QgemmError) as e:
+            q.logprobs(torch.zeros(3, 40 if k == 33 else 16, device="cuda"), top_k=k)
+        assert e.value.code == 2
+    with pytest.raises(q.QgemmError):
+        q.logprobs(x, top_k=-1)
+    assert q.logprobs(torch.zeros(0, 16, device="cuda"), top_k=2).top_ids.shape == (0, 2)

@@ -1,0 +1,99 @@
+"""Host-side checks of the 8-bit integer and log-probability entry points (no
+GPU): arguments are refused before anything is enqueued."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def qg():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    import weight_only_quantized_qgemm_gb300 as q
+    return q
+
+
+FAKE = 0x100000  # never dereferenced: every call below ends in its checks
+
+
+@pytest.mark.parametrize("args,expect", [
+    # Xq, ldxq, Sx, W, Sw, bias, Y, y_type, ldy, M, N, K
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 0, 256, 512), 0),        # M == 0: no-op
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 4, 0, 512), 0),          # N == 0: no-op
+    ((None, 512, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 4, 256, 512), 1),
+    ((FAKE, 512, None, FAKE, FAKE, None, FAKE, 0, 256, 4, 256, 512), 1),
+    ((FAKE, 512, FAKE, None, FAKE, None, FAKE, 0, 256, 4, 256, 512), 1),
+    ((FAKE, 512, FAKE, FAKE, None, None, FAKE, 0, 256, 4, 256, 512), 1),
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, None, 0, 256, 4, 256, 512), 1),
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, None, 0, 256, 4, 256, 0), 1),          # K == 0 writes Y too
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE, 3, 256, 4, 256, 512), 1),        # no such type
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE, 0, 256, -1, 256, 512), 1),
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 65537, 256, 512), 2),    # M > 65536
+    ((FAKE, 520, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 4, 256, 520), 2),        # K % 16
+    ((FAKE, 256, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 4, 256, 512), 1),        # ldxq < K
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE, 0, 255, 4, 256, 512), 1),        # ldy < N
+    ((FAKE + 8, 512, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 4, 256, 512), 3),
+    ((FAKE, 520, FAKE, FAKE, FAKE, None, FAKE, 0, 256, 4, 256, 512), 3),        # ldxq % 16
+    ((FAKE, 512, FAKE, FAKE + 8, FAKE, None, FAKE, 0, 256, 4, 256, 512), 3),
+    ((FAKE, 512, FAKE + 2, FAKE, FAKE, None, FAKE, 0, 256, 4, 256, 512), 3),
+    ((FAKE, 512, FAKE, FAKE, FAKE, FAKE + 1, FAKE, 0, 256, 4, 256, 512), 3),
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE + 2, 2, 256, 4, 256, 512), 3),    # FP32 Y
+    ((FAKE, 512, FAKE, FAKE, FAKE, None, FAKE + 1, 1, 256, 4, 256, 512), 3),
+])
+def test_gemm_argument_validation(qg, args, expect):
+    assert qg.lib.qgemm_w8a8_int8(*args, None, 0, None) == expect
+
+
+@pytest.mark.parametrize("args,expect", [
+    # X, x_type, ldx, Xq, ldxq, Sx, M, K
+    ((FAKE, 0, 512, FAKE, 512, FAKE, 0, 512), 0),
+    ((FAKE, 0, 512, FAKE, 512, FAKE, 4, 0), 0),
+    ((None, 0, 512, FAKE, 512, FAKE, 4, 512), 1),
+    ((FAKE, 0, 512, None, 512, FAKE, 4, 512), 1),
+    ((FAKE, 0, 512, FAKE, 512, None, 4, 512), 1),
+    ((FAKE, 2, 512, FAKE, 512, FAKE, 4, 512), 1),      # FP32 X
+    ((FAKE, 0, 512, FAKE, 512, FAKE, 4, 504), 2),      # K % 16
+    ((FAKE, 0, 512, FAKE, 512, FAKE, 65537, 512), 2),
+    ((FAKE, 0, 504, FAKE, 512, FAKE, 4, 512), 1),
+    ((FAKE, 0, 512, FAKE, 496, FAKE, 4, 512), 1),
+    ((FAKE, 0, 516, FAKE, 512, FAKE, 4, 512), 3),
+    ((FAKE, 1, 512, FAKE, 520, FAKE, 4, 512), 3),
+    ((FAKE + 8, 1, 512, FAKE, 512, FAKE, 4, 512), 3),
+    ((FAKE, 1, 512, FAKE, 512, FAKE + 2, 4, 512), 3),
+])
+def test_quantiser_argument_validation(qg, args, expect):
+    assert qg.lib.qg_quantize_act_int8(*args, None) == expect
+
+
+@pytest.mark.parametrize("args,expect", [
+    # logits, type, ld, tokens, ldt, T, token_lp, entropy, top_k, top_ids, top_lp, M, V
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 0, 100), 0),       # M == 0: no-op
+    ((None, 0, 100, None, 0, 0, None, None, 0, None, None, 3, 100), 0),       # nothing asked
+    ((None, 0, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),
+    ((FAKE, 0, 100, None, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),
+    ((FAKE, 0, 100, FAKE, 1, 1, None, FAKE, 4, FAKE, FAKE, 3, 100), 1),
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, None, 4, None, FAKE, 3, 100), 1),
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, None, 4, FAKE, None, 3, 100), 1),
+    ((FAKE, 5, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),
+    ((FAKE, 0, 100, FAKE, 1, -1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, -1, FAKE, FAKE, 3, 100), 1),
+    ((FAKE, 0, 99, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),        # ld < V
+    ((FAKE, 0, 100, FAKE, 1, 2, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),       # ldt < T
+    ((FAKE, 0, 0, FAKE, 1, 1, FAKE, FAKE, 0, FAKE, FAKE, 3, 0), 2),           # V == 0
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, 33, FAKE, FAKE, 3, 100), 2),      # top_k > 32
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, 9, FAKE, FAKE, 3, 8), 2),         # top_k > V
+    ((FAKE + 1, 0, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 3),
+    ((FAKE + 2, 2, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 3),
+    ((FAKE, 0, 100, FAKE + 4, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 3),
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE + 2, FAKE, 4, FAKE, FAKE, 3, 100), 3),
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE + 2, 4, FAKE, FAKE, 3, 100), 3),
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE + 4, FAKE, 3, 100), 3),
+    ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE + 2, 3, 100), 3),
+])
+def test_logprobs_argument_validation(qg, args, expect):
+    assert qg.lib.qg_logprobs(*args, None) == expect
+
+
+def test_dispatch_rule_covers_the_kind(qg):
+    assert qg.dispatch_rule(qg.KIND_INT8, 16, 17408, 5120, 152) in range(1, 153)
+    assert qg.dispatch_rule(qg.KIND_INT8, 65536, 17408, 5120, 152) in range(1, 153)
+    assert qg.dispatch_rule(qg.KIND_INT8, 65537, 17408, 5120, 152) == 0
+    assert qg.dispatch_rule(qg.KIND_INT8, 1, 1, 16, 152) == 1

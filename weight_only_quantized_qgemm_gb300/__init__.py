@@ -21,6 +21,11 @@ The names follow the C ABI in ``include/qgemm.h``:
   larger batches: BF16 activations quantised to E4M3 per (row, 128-wide K
   block) with FP32 scales, then an E4M3 x E4M3 block-scaled GEMM
   (:func:`qgemm_w8a8` runs both).
+* :func:`quantize_act_int8` / :func:`qgemm_w8a8_int8` -- 8-bit integer
+  activations (one scale per token) and weights (one scale per channel), BF16,
+  FP16 or FP32 output, optional bias.
+* :func:`logprobs` -- over rows of logits: log probabilities of given tokens,
+  entropy and the top alternatives.
 * :func:`pack_lut3` / :func:`unpack_lut3` -- offline nibble packer (host).
 * :func:`debug_fp8_split` / :func:`dequant_lut3` -- test aids: the FP8
   kernel's activation split and the LUT3 kernel's dequantiser on their own,
@@ -30,6 +35,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 import numpy as np
 
@@ -41,6 +47,7 @@ __all__ = [
     "debug_schedule", "tune_fp8", "tune_lut3", "workspace_bytes_max", "qgemm_bf16", "KIND_BF16", "KIND_FP8_BLOCK", "KIND_LUT3", "STATUS",
     "quantize_act_e4m3", "qgemm_w8a8_block", "qgemm_w8a8", "KIND_W8A8", "MAX_M_W8A8",
     "tune_bf16", "tune_w8a8", "workspace_bytes_max_w8a8",
+    "quantize_act_int8", "qgemm_w8a8_int8", "KIND_INT8", "logprobs", "LogProbs", "MAX_TOP_K",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -50,6 +57,7 @@ KIND_FP8_BLOCK = 0
 KIND_LUT3 = 1
 KIND_BF16 = 2
 KIND_W8A8 = 3
+KIND_INT8 = 4
 MAX_M_W8A8 = 65536
 STATUS = {
     0: "QG_OK", 1: "QG_ERR_INVALID_ARG", 2: "QG_ERR_UNSUPPORTED_SHAPE", 3: "QG_ERR_MISALIGNED",
@@ -83,6 +91,9 @@ _SIGS = {
     "qgemm_bf16": (_I, [_P, _L, _P, _P, _L, _I, _I, _I, _P, _S, _P]),
     "qg_quantize_act_e4m3": (_I, [_P, _L, _P, _L, _P, _L, _I, _I, _P]),
     "qgemm_w8a8_block": (_I, [_P, _L, _P, _L, _P, _P, _P, _L, _I, _I, _I, _P, _S, _P]),
+    "qg_quantize_act_int8": (_I, [_P, _I, _L, _P, _L, _P, _I, _I, _P]),
+    "qgemm_w8a8_int8": (_I, [_P, _L, _P, _P, _P, _P, _P, _I, _L, _I, _I, _I, _P, _S, _P]),
+    "qg_logprobs": (_I, [_P, _I, _L, _P, _L, _I, _P, _P, _I, _P, _P, _I, _I, _P]),
     "qg_lut3_packed_bytes": (_S, [_I, _I]),
     "pack_lut3": (_I, [_P, _P, _I, _I]),
     "unpack_lut3": (_I, [_P, _P, _I, _I]),
@@ -183,8 +194,8 @@ def _workspace_for(kind, M, N, K, workspace, device, stream=None):
         return None, 0
     if workspace is None:
         # one default buffer per device, stream (calls on different streams may
-        # overlap) and layout family (the W8A8 kind's differs from the others')
-        key = (device, _stream_ptr(stream), kind == KIND_W8A8)
+        # overlap) and layout family (the W8A8 and INT8 kinds' differ from the others')
+        key = (device, _stream_ptr(stream), kind if kind in (KIND_W8A8, KIND_INT8) else None)
         workspace = _default_ws.get(key)
         if workspace is None:
             workspace = _default_ws[key] = Workspace(device)
@@ -388,6 +399,151 @@ def qgemm_w8a8(X, W, W_scale, Y=None, workspace=None, stream=None):
     :func:`qgemm_w8a8_block` (two launches on one stream)."""
     Xq, X_scale = quantize_act_e4m3(X, stream=stream)
     return qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=Y, workspace=workspace, stream=stream)
+
+
+_dtype_codes = {}
+
+
+def _dtype_code(dtype):
+    """QG_BF16, QG_FP16 or QG_FP32 of a torch dtype, None for any other."""
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    return _dtype_codes.get(dtype)
+
+
+def _row_ld(t) -> int:
+    """_ld, with the row length for a lone row (whose stride is arbitrary)."""
+    ld = _ld(t)
+    return t.shape[1] if t.shape[0] <= 1 else ld
+
+
+def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
+    """8-bit integer codes and one FP32 scale per row of BF16 or FP16
+    activations: scale = max |x| / 127, code = x * (127 * (1 / max |x|)) rounded
+    half to even (a row whose largest |x| is below 2^-100 has codes 0, scale 1).
+
+    X: CUDA [M, K] (row stride a multiple of 8, K % 16 == 0).  Returns (Xq
+    int8 [M, K], X_scale float32 [M]).  Xq and X_scale (optional) are written
+    in place.
+    """
+    torch = _torch()
+    code = _dtype_code(X.dtype)
+    if code not in (0, 1):
+        raise TypeError("X must be bfloat16 or float16")
+    M, K = X.shape
+    if Xq is None:
+        Xq = torch.empty((M, K), dtype=torch.int8, device=X.device)
+    if X_scale is None:
+        X_scale = torch.empty((M,), dtype=torch.float32, device=X.device)
+    if Xq.dtype != torch.int8 or X_scale.dtype != torch.float32 or not X_scale.is_contiguous():
+        raise TypeError("Xq must be int8, X_scale contiguous float32")
+    if Xq.shape != X.shape or tuple(X_scale.shape) != (M,):
+        raise ValueError("shape mismatch between X, Xq and X_scale")
+    if not (X.is_cuda and Xq.device == X.device and X_scale.device == X.device):
+        raise ValueError("X, Xq and X_scale must be on one CUDA device")
+    _check(lib.qg_quantize_act_int8(X.data_ptr(), code, _row_ld(X), Xq.data_ptr(), _row_ld(Xq), X_scale.data_ptr(), M, K,
+                                    _stream_ptr(stream)), "qg_quantize_act_int8")
+    return Xq, X_scale
+
+
+def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, workspace=None, stream=None):
+    """Y[m, n] = X_scale[m] * W_scale[n] * (Xq[m] . W[n]) (+ bias[n]): 8-bit
+    integer activations with one scale per token, 8-bit integer weights with
+    one scale per channel.
+
+    Xq: int8 CUDA [M, K] (row stride a multiple of 16), X_scale: float32 [M] as
+    :func:`quantize_act_int8` returns them; W: int8 [N, K] contiguous; W_scale:
+    float32 [N]; bias (optional): float32 [N].  Y (optional): [M, N] with unit
+    column stride, in bfloat16 (the default), float16 or float32 (out_dtype).
+    """
+    torch = _torch()
+    if Xq.dtype != torch.int8 or W.dtype != torch.int8:
+        raise TypeError("Xq and W must be int8")
+    if X_scale.dtype != torch.float32 or W_scale.dtype != torch.float32 or \
+            (bias is not None and bias.dtype != torch.float32):
+        raise TypeError("X_scale, W_scale and bias must be float32")
+    if not (W.is_contiguous() and X_scale.is_contiguous() and W_scale.is_contiguous()) or \
+            (bias is not None and not bias.is_contiguous()):
+        raise TypeError("W, the scales and bias must be contiguous")
+    M, K = Xq.shape
+    N = W.shape[0]
+    if W.shape[1] != K or tuple(X_scale.shape) != (M,) or tuple(W_scale.shape) != (N,) or \
+            (bias is not None and tuple(bias.shape) != (N,)):
+        raise ValueError("shape mismatch between Xq, X_scale, W, W_scale and bias")
+    if Y is None:
+        Y = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=Xq.device)
+    elif tuple(Y.shape) != (M, N) or (out_dtype is not None and Y.dtype != out_dtype):
+        raise ValueError("Y must be [M, N] of out_dtype")
+    code = _dtype_code(Y.dtype)
+    if code is None:
+        raise TypeError("the output must be bfloat16, float16 or float32")
+    if not Xq.is_cuda or any(t is not None and t.device != Xq.device for t in (X_scale, W, W_scale, bias, Y)):
+        raise ValueError("all tensors must be on one CUDA device")
+    ws, wsb = _workspace_for(KIND_INT8, M, N, K, workspace, Xq.device, stream)
+    _check(lib.qgemm_w8a8_int8(Xq.data_ptr(), _row_ld(Xq), X_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(),
+                               bias.data_ptr() if bias is not None else None, Y.data_ptr(), code, _row_ld(Y), M, N, K,
+                               ws, wsb, _stream_ptr(stream)), "qgemm_w8a8_int8")
+    return Y
+
+
+MAX_TOP_K = 32
+
+
+class LogProbs(NamedTuple):
+    """What :func:`logprobs` returns; a part not asked for is None."""
+    token_logprobs: Any   # float32, shaped like tokens
+    entropy: Any          # float32 [M], nats
+    top_ids: Any          # int64 [M, top_k]
+    top_logprobs: Any     # float32 [M, top_k]
+
+
+def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=None) -> LogProbs:
+    """Over the softmax of every row of logits: the log probabilities of given
+    tokens, the entropy, and the top alternatives (by value, then by lower
+    index).
+
+    logits: bf16, fp16 or fp32 CUDA [M, V] with unit column stride; tokens
+    (optional): int64 [M] or [M, T]; top_k: 0 .. MAX_TOP_K and <= V.  A logit
+    of -inf is a masked token; a row with nothing left has log probabilities
+    of -inf and entropy 0; a token outside the vocabulary has -inf; a row with
+    a NaN or +inf gives NaN (see include/qgemm.h).
+    """
+    torch = _torch()
+    code = _dtype_code(logits.dtype)
+    if code is None:
+        raise TypeError("logits must be bfloat16, float16 or float32")
+    ld = _row_ld(logits)
+    M, V = logits.shape
+    dev = logits.device
+    if not logits.is_cuda or (tokens is not None and tokens.device != dev):
+        raise ValueError("logits and tokens must be on one CUDA device")
+    T = ldt = 0
+    tok = token_lp = ent = ids = top = None
+    if tokens is not None:
+        if tokens.dtype != torch.int64:
+            raise TypeError("tokens must be int64")
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
+            raise ValueError("tokens must be [M] or [M, T]")
+        T = tokens.shape[1] if tokens.dim() == 2 else 1
+        if T > 1 and tokens.stride(1) != 1:
+            tokens = tokens.contiguous()
+        ldt = max(tokens.stride(0), T)
+        if M > 1 and tokens.stride(0) < T:   # an expanded row
+            tokens = tokens.contiguous()
+            ldt = T
+        tok = tokens.data_ptr()
+        token_lp = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+    if entropy:
+        ent = torch.empty((M,), dtype=torch.float32, device=dev)
+    if top_k > 0:   # a negative one is refused by the library
+        ids = torch.empty((M, top_k), dtype=torch.int64, device=dev)
+        top = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+    _check(lib.qg_logprobs(logits.data_ptr(), code, ld, tok, ldt, T,
+                           token_lp.data_ptr() if token_lp is not None else None,
+                           ent.data_ptr() if entropy else None, top_k, ids.data_ptr() if ids is not None else None,
+                           top.data_ptr() if top is not None else None, M, V, _stream_ptr(stream)), "qg_logprobs")
+    return LogProbs(token_lp, ent, ids, top)
 
 
 def qgemm_bf16(X, W, Y=None, workspace=None, stream=None):

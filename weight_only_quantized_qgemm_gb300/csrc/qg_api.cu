@@ -11,7 +11,9 @@
 
 #include "../../include/qgemm.h"
 #include "qg_gemm.cuh"
+#include "qg_int8.h"
 #include "qg_internal.h"
+#include "qg_logprobs.h"
 #include "qg_w8a8.h"
 
 namespace qg {
@@ -163,13 +165,14 @@ int table_lookup(int kind, int M, int N, int K) {
 // The schedule of a shape on `sms` SMs, with `forced` > 0 a dispatch-table grid.
 Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
     Schedule s;
-    s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : M <= 16 ? 16 : 32;
-    // W8A8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
-    s.T = (N + 127) / 128 * (kind == QG_KIND_W8A8 ? (M + s.nmma - 1) / s.nmma : 1);
+    s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : kind == QG_KIND_INT8 ? int8_tile_rows(M) : M <= 16 ? 16 : 32;
+    // W8A8 and INT8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
+    s.T = (N + 127) / 128 * (kind == QG_KIND_W8A8 || kind == QG_KIND_INT8 ? (M + s.nmma - 1) / s.nmma : 1);
     // one unit = 128 rows x one 128-wide K block (W8A8: two blocks)
     s.KU = kind == QG_KIND_W8A8 ? (K + 255) / 256 : (K + 127) / 128;
     s.U = static_cast<long long>(s.T) * s.KU;
-    const bool unit_bound = kind == QG_KIND_W8A8 || (kind == QG_KIND_FP8_BLOCK && M > 16);
+    const bool unit_bound =
+        kind == QG_KIND_W8A8 || (kind == QG_KIND_FP8_BLOCK && M > 16) || (kind == QG_KIND_INT8 && M > 64);
     long long g = sms;
     if (forced > 0) {
         g = forced;
@@ -244,7 +247,9 @@ const SchedEntry& cached_schedule(int kind, int M, int N, int K, int sms) {
     e.sms = sms;
     e.gen = gen;
     e.s = choose_schedule(kind, M, N, K, sms);
-    e.ws = kind == QG_KIND_W8A8 ? w8a8_workspace_bytes(e.s, schedule_splits(e.s)) : workspace_bytes_uncached(e.s);
+    e.ws = kind == QG_KIND_W8A8   ? w8a8_workspace_bytes(e.s, schedule_splits(e.s))
+           : kind == QG_KIND_INT8 ? int8_workspace_bytes(e.s, M, K, schedule_splits(e.s))
+                                  : workspace_bytes_uncached(e.s);
     return e;
 }
 
@@ -262,7 +267,8 @@ int max_m(int kind) {
         case QG_KIND_FP8_BLOCK:
         case QG_KIND_LUT3:
         case QG_KIND_BF16: return 32;
-        case QG_KIND_W8A8: return kMaxMW8a8;
+        case QG_KIND_W8A8:
+        case QG_KIND_INT8: return kMaxMW8a8;
     }
     return 0;
 }
@@ -328,6 +334,10 @@ void workspace_counters(int kind, int M, int N, int K, size_t* offset, size_t* b
     const Schedule& s = e.s;
     const size_t total = e.ws;
     if (total == 0) return;
+    if (kind == QG_KIND_INT8) {
+        *bytes = kInt8CounterBytes;
+        return;
+    }
     *offset = kind == QG_KIND_W8A8 ? w8a8_partial_bytes(s) : workspace_partial_bytes(s);
     *bytes = total - *offset;
 }
@@ -684,6 +694,92 @@ qg_status qgemm_w8a8_block(const uint8_t* Xq, int64_t ldxq, const float* X_scale
               make_tmap(&a.tmY, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<uint64_t>(N),
                         static_cast<uint64_t>(M), static_cast<uint64_t>(ldy) * 2, 32, 16, CU_TENSOR_MAP_SWIZZLE_NONE);
     return launch_w8a8(a, s, *tmW, tmX, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+qg_status qg_quantize_act_int8(const void* X, int x_type, int64_t ldx, int8_t* Xq, int64_t ldxq, float* X_scale, int M,
+                               int K, cudaStream_t stream) {
+    if (M < 0 || K < 0 || (x_type != QG_BF16 && x_type != QG_FP16)) return QG_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return QG_OK;
+    if (!X || !Xq || !X_scale) return QG_ERR_INVALID_ARG;
+    if (M > kMaxMW8a8 || K % 16 != 0) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (ldx < K || ldxq < K) return QG_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(Xq) || ldx % 8 != 0 || ldxq % 16 != 0 ||
+        (reinterpret_cast<uintptr_t>(X_scale) & 3u) != 0)
+        return QG_ERR_MISALIGNED;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    return launch_quantize_int8(X, x_type, ldx, Xq, ldxq, X_scale, M, K, launch_ctl(d), stream) == cudaSuccess
+               ? QG_OK
+               : QG_ERR_CUDA;
+}
+
+qg_status qgemm_w8a8_int8(const int8_t* Xq, int64_t ldxq, const float* X_scale, const int8_t* W, const float* W_scale,
+                          const float* bias, void* Y, int y_type, int64_t ldy, int M, int N, int K, void* workspace,
+                          size_t workspace_bytes_, cudaStream_t stream) {
+    if (M < 0 || N < 0 || K < 0 || (y_type != QG_BF16 && y_type != QG_FP16 && y_type != QG_FP32))
+        return QG_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return QG_OK;
+    if (!Y || (K > 0 && (!Xq || !X_scale || !W || !W_scale))) return QG_ERR_INVALID_ARG;
+    if (M > kMaxMW8a8 || K % 16 != 0) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (ldxq < K || ldy < N) return QG_ERR_INVALID_ARG;
+    const uintptr_t y_mask = y_type == QG_FP32 ? 3u : 1u;
+    // without a K there is nothing of Xq and W to be aligned
+    if ((K > 0 && (!aligned16(Xq) || !aligned16(W) || ldxq % 16 != 0)) ||
+        (reinterpret_cast<uintptr_t>(X_scale) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(W_scale) & 3u) != 0 || (reinterpret_cast<uintptr_t>(bias) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(Y) & y_mask) != 0)
+        return QG_ERR_MISALIGNED;
+    // tiles are indexed by int
+    if ((static_cast<int64_t>(N) + 127) / 128 * ((M + 15) / 16) > (int64_t(1) << 29)) return QG_ERR_UNSUPPORTED_SHAPE;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    Int8Args a{};
+    a.Xq = Xq;
+    a.ldxq = ldxq;
+    a.Sx = X_scale;
+    a.Sw = W_scale;
+    a.bias = bias;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.y_type = y_type;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    if (K == 0) return launch_int8_bias_rows(a, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+    const SchedEntry& se = cached_schedule(QG_KIND_INT8, M, N, K, d->sms);
+    const Schedule s = se.s;
+    if (!workspace || workspace_bytes_ < se.ws || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return QG_ERR_WORKSPACE;
+    a.ws = workspace;
+    CUtensorMap tmW, tmX;
+    if (!make_tmap(&tmW, W, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<uint64_t>(K), static_cast<uint64_t>(N),
+                   static_cast<uint64_t>(K), 128, 128) ||
+        !make_tmap(&tmX, static_cast<uint8_t*>(workspace) + kInt8CounterBytes, CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                   static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K) * 2, 64,
+                   static_cast<uint32_t>(s.nmma)))
+        return QG_ERR_CUDA;
+    return launch_int8(a, s, tmW, tmX, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+qg_status qg_logprobs(const void* logits, int type, int64_t ld, const int64_t* tokens, int64_t ldt, int T,
+                      float* token_logprobs, float* entropy, int top_k, int64_t* top_ids, float* top_logprobs, int M,
+                      int V, cudaStream_t stream) {
+    if (M < 0 || V < 0 || T < 0 || top_k < 0 || (type != QG_BF16 && type != QG_FP16 && type != QG_FP32))
+        return QG_ERR_INVALID_ARG;
+    if (M == 0 || (T == 0 && !entropy && top_k == 0)) return QG_OK;
+    if (!logits || (T > 0 && (!tokens || !token_logprobs)) || (top_k > 0 && (!top_ids || !top_logprobs)))
+        return QG_ERR_INVALID_ARG;
+    if (V == 0 || top_k > QG_MAX_TOP_K || top_k > V) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (ld < V || ldt < T) return QG_ERR_INVALID_ARG;
+    const uintptr_t mask = type == QG_FP32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(logits) & mask) || (reinterpret_cast<uintptr_t>(tokens) & 7u) ||
+        (reinterpret_cast<uintptr_t>(token_logprobs) & 3u) || (reinterpret_cast<uintptr_t>(entropy) & 3u) ||
+        (reinterpret_cast<uintptr_t>(top_ids) & 7u) || (reinterpret_cast<uintptr_t>(top_logprobs) & 3u))
+        return QG_ERR_MISALIGNED;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    const LogprobArgs a{logits, type, ld, tokens, ldt, T, token_logprobs, entropy, top_k, top_ids, top_logprobs, M, V};
+    return launch_logprobs(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
 qg_status qgemm_lut3(const void* X, int64_t ldx, const void* Wq, const void* qmap, const void* scales, void* Y,

@@ -1,0 +1,614 @@
+// 8-bit integer GEMM with one scale per token and per channel, and the
+// activation quantiser in front of it, for sm_103a.
+//
+//   Y[m, n] = sx[m] * sw[n] * sum_k xq[m, k] * w[n, k] (+ bias[n])
+//
+// sm_103a has no integer kind of tcgen05.mma, so the products run as
+// kind::f16: every value of -128..127 is an FP16 number, every product an
+// integer of at most 2^14, and the FP32 accumulator adds integers exactly
+// while the partial sums stay below 2^24 (always for K <= 1024; beyond that a
+// sum that leaves the range rounds at 2^-24 of its size, far under the output
+// types' steps).  The floor is therefore the FP16 tensor rate for large M and
+// the weight bytes, read once as stored, for small M.
+//
+// The output is tiled in 128 weight rows x NA activation rows (NA = the MMA's
+// N side); a unit is one tile x one 128-wide K block.  Weights stay 8-bit up
+// to the SM: TMA brings a unit's 128 x 128 bytes into a shared-memory ring
+// (128-byte swizzle), the convert warps turn each row's bytes into FP16 in
+// registers (XOR 0x80, a byte permute under the exponent of 1024, one packed
+// subtract: five instructions for four values) and store them to TMEM, from
+// where the MMA takes its A operand.  Activations are expanded to FP16 once
+// per call by a small kernel in front (they are read by every weight tile;
+// converting them in each CTA would cost NA/128 of the weight conversion and
+// twice the shared memory traffic) and arrive by TMA as the B operand.
+//
+// One persistent CTA per SM; warps by role:
+//   warp 0        weight producer (TMA, one 16 KB box per unit)
+//   warp 1        activation producer (TMA, boxes of 64 K x NA rows), after
+//                 the expansion kernel's completion
+//   warp 2        MMA issuer: 8 tcgen05.mma (M = 128, N = NA, K = 16) a unit
+//   warps 4-      epilogue: one per TMEM lane quadrant (two for NA >= 128)
+//   the last 8    convert: two groups of four warps taking alternate units
+//
+// Units are split evenly over the CTAs in tile-major order; a tile shared by
+// several CTAs is summed, in ascending K order of its pieces, by the last to
+// arrive, as in the other kernels.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qg_gemm.cuh"
+#include "qg_int8.h"
+
+namespace qg {
+namespace {
+
+using gemm::Cursor;
+using gemm::Params;
+using gemm::Ring;
+
+constexpr int kWarpWProd = 0, kWarpXProd = 1, kWarpMma = 2, kWarpEpi0 = 4;
+constexpr int kGroups = 2;   // convert groups of four warps
+
+template <int NA>
+struct I8Layout {
+    static constexpr int kEpi = NA >= 128 ? 8 : 4;
+    static constexpr int kEpiCols = NA / (kEpi / 4);            // columns per epilogue warp
+    static constexpr int kWarpConv0 = kWarpEpi0 + kEpi;
+    static constexpr int kThreads = 32 * (kWarpConv0 + 4 * kGroups);
+    static constexpr int kWBytes = 128 * 128;
+    static constexpr int kXSlot = NA * 128;                     // 64 K of FP16
+    static constexpr int kXStages = NA == 128 ? 6 : NA == 64 ? 8 : 12;
+    static constexpr int kWFit = (232448 - 2048 - kXStages * kXSlot) / kWBytes;
+    static constexpr int kWStages = (kWFit < 12 ? kWFit : 12) / kGroups * kGroups;
+    static constexpr int kNA = 4;                               // A buffers in TMEM, 64 columns each
+    static constexpr int kD = 2;                                // accumulators, NA columns each
+    static constexpr int kDCol0 = kNA * 64;
+    static constexpr int kXOff = kWStages * kWBytes;
+    static constexpr int kBarOff = kXOff + kXStages * kXSlot;
+    static constexpr int kNumBars = 2 * kWStages + 2 * kXStages + 2 * kNA + 2 * kD;
+    static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+    static constexpr int kSmemBytes = kMiscOff + 64 + 1024;     // + alignment slack
+    static_assert(kDCol0 + kD * NA <= 512, "TMEM columns");
+    static_assert(kSmemBytes <= 232448, "shared memory");
+    static_assert(kXSlot % 1024 == 0, "keep the 1024-byte swizzle alignment");
+    // a weight stage and an A buffer always belong to one convert group, so
+    // that its parity waits are for the phase after one it has seen
+    static_assert(kWStages % kGroups == 0 && kNA % kGroups == 0, "ring ownership");
+    static_assert(kEpiCols % 16 == 0, "epilogue chunks");
+};
+
+struct Out {
+    const float* sx;
+    const float* sw;
+    const float* bias;
+    int y_type;
+    int tm_count;   // activation row blocks; tile t = (weight tile t / tm_count, block t % tm_count)
+};
+
+// Four signed bytes of w -> two FP16x2 words, exactly: u = byte + 128 under
+// the exponent of 1024 is 1024 + u, minus 1152 is the byte's value.
+__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = prmt(u, 0x64646464u, 0x4140u);
+    const uint32_t b = prmt(u, 0x64646464u, 0x4342u);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+}
+
+// 16 output columns (activation rows m0 ..) of weight row n.  sxl: lane l's
+// scale of row m0 + l (l < 16).
+__device__ __forceinline__ void store16(const Params& p, const Out& o, int n, int m0, float sxl, float sw, float b,
+                                        const float (&v)[16]) {
+    const int64_t ldy = p.seg[0].ldy;
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        y[j] = __fmaf_rn(__fmul_rn(v[j], __shfl_sync(0xffffffffu, sxl, j)), sw, b);
+    if (n >= p.N) return;
+    const int64_t at = static_cast<int64_t>(m0) * ldy + n;
+    const int rows = p.M - m0;
+    if (o.y_type == QG_FP32) {
+        float* Y = static_cast<float*>(p.seg[0].Y) + at;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < rows) Y[j * ldy] = y[j];
+    } else if (o.y_type == QG_BF16) {
+        __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.seg[0].Y) + at;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < rows) Y[j * ldy] = __float2bfloat16_rn(y[j]);
+    } else {
+        __half* Y = static_cast<__half*>(p.seg[0].Y) + at;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < rows) Y[j * ldy] = __float2half_rn(y[j]);
+    }
+}
+
+template <int NA>
+__device__ __forceinline__ float4* part_slot(const Params& p, int cta, int which) {
+    return reinterpret_cast<float4*>(p.part) + (static_cast<size_t>(cta) * 2 + which) * (NA / 4) * 128;
+}
+
+template <int NA>
+__global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
+    int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p,
+                const Out o) {
+    using L = I8Layout<NA>;
+    constexpr int kWStages = L::kWStages, kXStages = L::kXStages, kNA = L::kNA, kD = L::kD;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw);
+
+    const uint32_t bar0 = base + L::kBarOff;
+    auto wfull = [&](int s) { return bar0 + 8u * s; };
+    auto wempty = [&](int s) { return bar0 + 8u * (kWStages + s); };
+    auto xfull = [&](int s) { return bar0 + 8u * (2 * kWStages + s); };
+    auto xempty = [&](int s) { return bar0 + 8u * (2 * kWStages + kXStages + s); };
+    constexpr int kBarA = 2 * kWStages + 2 * kXStages;
+    auto afull = [&](int a) { return bar0 + 8u * (kBarA + a); };
+    auto afree = [&](int a) { return bar0 + 8u * (kBarA + kNA + a); };
+    auto dfull = [&](int b) { return bar0 + 8u * (kBarA + 2 * kNA + b); };
+    auto dempty = [&](int b) { return bar0 + 8u * (kBarA + 2 * kNA + kD + b); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    const long long u0 = gemm::unit_begin(cta, p.U, p.G);
+    const long long u1 = gemm::unit_begin(cta + 1, p.U, p.G);
+    const int nunits = static_cast<int>(u1 - u0);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kWStages; ++s) {
+            mbar_init(wfull(s), 1);
+            mbar_init(wempty(s), 4);   // the four warps of the convert group
+        }
+        for (int s = 0; s < kXStages; ++s) {
+            mbar_init(xfull(s), 1);
+            mbar_init(xempty(s), 1);   // commit
+        }
+        for (int a = 0; a < kNA; ++a) {
+            mbar_init(afull(a), 4);
+            mbar_init(afree(a), 1);    // commit
+        }
+        for (int b = 0; b < kD; ++b) {
+            mbar_init(dfull(b), 1);    // commit: the piece's MMAs are complete
+            mbar_init(dempty(b), L::kEpi);
+        }
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const WaitCtl wc{p.timeout_ns, p.status, abort_flag};
+    grid_dependents_launch();
+
+    if (warp == kWarpWProd) {
+        if (lane == 0) {
+            prefetch_tmap(&tmW);
+            // a weight tile serves tm_count tiles in a row: keep it for their re-reads
+            const uint64_t pol = o.tm_count > 1 ? policy_evict_last() : policy_evict_first();
+            int issued = 0;
+            Cursor cur(u0, p.KB);
+            Ring<kWStages> rw(0);
+            for (int i = 0; i < nunits; ++i, cur.step(p.KB), rw.step(1)) {
+                if (i >= kWStages && !wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
+                issued = i + 1;
+                if (cta == 0 && i == p.fault_unit) continue;   // failure-path test hook
+                mbar_arrive_expect_tx(wfull(rw.slot), L::kWBytes);
+                tma_load_2d(base + rw.slot * L::kWBytes, &tmW, wfull(rw.slot), cur.kr * 128,
+                            cur.tile / o.tm_count * 128, pol);
+            }
+            for (int i = issued - kWStages < 0 ? 0 : issued - kWStages; i < issued; ++i) {
+                if (cta == 0 && i == p.fault_unit) continue;
+                gemm::drain_wait(wfull(i % kWStages), (i / kWStages) & 1, p.timeout_ns);
+            }
+        }
+    } else if (warp == kWarpXProd) {
+        if (lane == 0) {
+            prefetch_tmap(&tmX);
+            grid_dependency_wait();   // the expansion kernel's output
+            const uint64_t pol = policy_evict_last();
+            int issued = 0;
+            Cursor cur(u0, p.KB);
+            Ring<kXStages> rx(0);
+            for (int i = 0; i < 2 * nunits; ++i, rx.step(1)) {
+                if (i >= kXStages && !wait_bounded(xempty(rx.slot), rx.phase ^ 1u, wc)) break;
+                mbar_arrive_expect_tx(xfull(rx.slot), L::kXSlot);
+                tma_load_2d(base + L::kXOff + rx.slot * L::kXSlot, &tmX, xfull(rx.slot), cur.kr * 128 + (i & 1) * 64,
+                            cur.tile % o.tm_count * NA, pol);
+                issued = i + 1;
+                if (i & 1) cur.step(p.KB);
+            }
+            for (int i = issued - kXStages < 0 ? 0 : issued - kXStages; i < issued; ++i)
+                gemm::drain_wait(xfull(i % kXStages), (i / kXStages) & 1, p.timeout_ns);
+        }
+    } else if (warp == kWarpMma) {
+        const bool elected = elect_one();
+        constexpr uint32_t idesc = idesc_f16(NA, false);
+        const uint64_t dx0 = smem_desc_sw128(base + L::kXOff);
+        Cursor cur(u0, p.KB);
+        Ring<kXStages> rx(0);
+        Ring<kNA> ra(0);
+        int piece = 0;
+        int last_a = -1;
+        uint32_t last_ph = 0;
+        bool fresh = true;   // the next MMA starts a piece
+        bool ok = true;
+        for (int i = 0; i < nunits && ok; ++i, ra.step(1)) {
+            const int b = piece % kD;
+            if (fresh && piece >= kD && !gemm::warp_wait(dempty(b), ((piece / kD) - 1) & 1, wc)) break;
+            if (!gemm::warp_wait(afull(ra.slot), ra.phase, wc)) break;
+            const uint32_t dt = tmem + L::kDCol0 + b * NA;
+            const uint32_t at = tmem + ra.slot * 64;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ok = gemm::warp_wait(xfull(rx.slot), rx.phase, wc);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t xd = dx0 + static_cast<uint64_t>((rx.slot * L::kXSlot) >> 4);
+                if (elected) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_ts_f16(dt, at + h * 32 + j * 8, xd + 2 * j, idesc, (h > 0 || j > 0 || !fresh) ? 1u : 0u);
+                    tc_commit(xempty(rx.slot));
+                }
+                __syncwarp();
+                rx.step(1);
+            }
+            const bool closes = i == nunits - 1 || cur.kb == p.KB - 1;
+            if (elected) {
+                tc_commit(afree(ra.slot));
+                if (closes && ok) tc_commit(dfull(b));
+            }
+            __syncwarp();
+            last_a = ra.slot;
+            last_ph = ra.phase;
+            fresh = closes;
+            if (closes) ++piece;
+            cur.step(p.KB);
+        }
+        if (last_a >= 0 && elected) gemm::drain_wait(afree(last_a), last_ph, p.timeout_ns);
+    } else if (warp >= L::kWarpConv0) {
+        const int q = warp & 3;
+        const int grp = (warp - L::kWarpConv0) >> 2;
+        const int row = q * 32 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        Ring<kWStages> rw(grp);
+        Ring<kNA> ra(grp);
+        for (int i = grp; i < nunits; i += kGroups, rw.step(kGroups), ra.step(kGroups)) {
+            if (!gemm::warp_wait(wfull(rw.slot), rw.phase, wc)) break;
+            const uint8_t* src = gbase + rw.slot * L::kWBytes + row * 128;
+            uint4 c[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
+            if (i >= kNA && !gemm::warp_wait(afree(ra.slot), ra.phase ^ 1u, wc)) break;
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                uint32_t f[16];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 w = c[2 * t + e];
+                    s8x4_to_f16(w.x, f[8 * e + 0], f[8 * e + 1]);
+                    s8x4_to_f16(w.y, f[8 * e + 2], f[8 * e + 3]);
+                    s8x4_to_f16(w.z, f[8 * e + 4], f[8 * e + 5]);
+                    s8x4_to_f16(w.w, f[8 * e + 6], f[8 * e + 7]);
+                }
+                tmem_st_x16(tl + ra.slot * 64 + t * 16, f);
+            }
+            // the loads have returned: the TMEM stores above needed them
+            __syncwarp();
+            if (lane == 0) mbar_arrive(wempty(rw.slot));
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(afull(ra.slot));
+        }
+    } else if (warp >= kWarpEpi0) {
+        const int ew = warp - kWarpEpi0;
+        const int q = warp & 3;
+        const int col0 = (ew >> 2) * L::kEpiCols;
+        const int row = q * 32 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + L::kDCol0 + col0;
+        const int first_tile = static_cast<int>(u0 / p.KB);
+        const int split_info = gemm::split_info_lane(p, u0, u1, lane);
+        // the scales, Y and the workspace may be in use by the preceding grid
+        grid_dependency_wait();
+        int ps = 0;
+        int kb0 = static_cast<int>(u0 % p.KB);
+        for (int pc = 0; ps < nunits; ++pc) {
+            const int tile = first_tile + pc;
+            const int b = pc % kD;
+            int pe = ps + (p.KB - kb0) - 1;
+            if (pe > nunits - 1) pe = nunits - 1;
+            const bool whole = kb0 == 0 && pe - ps == p.KB - 1;
+            const int tn = tile / o.tm_count;
+            const int n = tn * 128 + row;
+            const int m0 = (tile - tn * o.tm_count) * NA + col0;
+            const float sw = n < p.N ? o.sw[n] : 0.0f;
+            const float bias = o.bias != nullptr && n < p.N ? o.bias[n] : 0.0f;
+            auto scale_of = [&](int m) { return lane < 16 && m + lane < p.M ? o.sx[m + lane] : 0.0f; };
+            if (!gemm::warp_wait(dfull(b), (pc / kD) & 1, wc)) break;
+            tc_fence_after();
+            const int which = tile == first_tile ? 0 : 1;
+            float4* mine = part_slot<NA>(p, cta, which) + (col0 / 4) * 128 + row;
+#pragma unroll 1
+            for (int c = 0; c < L::kEpiCols / 16; ++c) {
+                uint32_t v[16];
+                const float sxl = scale_of(m0 + 16 * c);
+                tmem_ld_x16(tl + b * NA + 16 * c, v);
+                tmem_wait_ld();
+                float f[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+                if (whole) {
+                    store16(p, o, n, m0 + 16 * c, sxl, sw, bias, f);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        __stcg(mine + (4 * c + g) * 128,
+                               make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dempty(b));
+            if (!whole) {
+                // every lane's partial visible GPU-wide before lane 0's arrival.  A
+                // split tile's counter is indexed by the CTA that holds its first
+                // unit: that CTA's last tile, so no other tile shares it.
+                const int cf = __shfl_sync(0xffffffffu, split_info, 3 * which);
+                const int cl = __shfl_sync(0xffffffffu, split_info, 3 * which + 1);
+                const int w_first = __shfl_sync(0xffffffffu, split_info, 3 * which + 2);
+                uint32_t* cnt = p.cnt + cf * 8 + ew;
+                __threadfence();
+                __syncwarp();
+                uint32_t prev = 0;
+                if (lane == 0) prev = atomicAdd(cnt, 1u);
+                prev = __shfl_sync(0xffffffffu, prev, 0);
+                if (static_cast<int>(prev) == cl - cf) {
+                    __threadfence();
+#pragma unroll 1
+                    for (int c = 0; c < L::kEpiCols / 16; ++c) {
+                        const float sxl = scale_of(m0 + 16 * c);
+                        float acc[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
+#pragma unroll 4
+                        for (int c2 = cf; c2 <= cl; ++c2) {
+                            const float4* src = part_slot<NA>(p, c2, c2 == cf ? w_first : 0) + (col0 / 4 + 4 * c) * 128 + row;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                const float4 x = __ldcg(src + g * 128);
+                                acc[4 * g + 0] = __fadd_rn(acc[4 * g + 0], x.x);
+                                acc[4 * g + 1] = __fadd_rn(acc[4 * g + 1], x.y);
+                                acc[4 * g + 2] = __fadd_rn(acc[4 * g + 2], x.z);
+                                acc[4 * g + 3] = __fadd_rn(acc[4 * g + 3], x.w);
+                            }
+                        }
+                        store16(p, o, n, m0 + 16 * c, sxl, sw, bias, acc);
+                    }
+                    __syncwarp();
+                    if (lane == 0) *cnt = 0u;   // ready for the next call
+                }
+            }
+            ps = pe + 1;
+            kb0 = 0;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The activations as FP16 [M, K]: 16 codes (K % 16 == 0) a thread.
+__global__ void __launch_bounds__(256) expand_kernel(const int8_t* __restrict__ Xq, int64_t ldxq,
+                                                     uint4* __restrict__ out, int M, int K16) {
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int64_t total = static_cast<int64_t>(M) * K16;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total;
+         t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t m = t / K16;
+        const uint4 c = *reinterpret_cast<const uint4*>(Xq + m * ldxq + (t - m * K16) * 16);
+        uint4 a, b;
+        s8x4_to_f16(c.x, a.x, a.y);
+        s8x4_to_f16(c.y, a.z, a.w);
+        s8x4_to_f16(c.z, b.x, b.y);
+        s8x4_to_f16(c.w, b.z, b.w);
+        out[2 * t] = a;
+        out[2 * t + 1] = b;
+    }
+}
+
+// ----------------------------------------------------------------- quantiser
+// Row maximum below this: the row counts as zero (codes 0, scale 1), so that
+// 1 / max stays finite.
+constexpr float kTinyMax = 7.888609052210118e-31f;   // 2^-100
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+    if (kBf16) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        a = f.x;
+        b = f.y;
+    }
+}
+
+// Code of x * inv, round half to even, as a byte.
+__device__ __forceinline__ uint32_t code_of(float x, float inv) {
+    return static_cast<uint32_t>(__float2int_rn(__fmul_rn(x, inv))) & 0xFFu;
+}
+
+// One CTA per row; the row is read once for its maximum and again (from L1 or
+// L2) for its codes.
+template <bool kBf16>
+__global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+                                                            int8_t* __restrict__ Xq, int64_t ldxq,
+                                                            float* __restrict__ Sx, int K) {
+    __shared__ float warp_max[8];
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int64_t m = blockIdx.x;
+    const uint4* x = reinterpret_cast<const uint4*>(X + m * ldx);
+    const int nv = K / 8;
+    float amax = 0.0f;
+    for (int v = threadIdx.x; v < nv; v += 256) {
+        const uint4 w = x[v];
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            unpack2<kBf16>(u[j], a, b);
+            amax = fmaxf(amax, fmaxf(fabsf(a), fabsf(b)));
+        }
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, warp_max[j]);
+    const bool live = amax >= kTinyMax;
+    const float inv = live ? __fmul_rn(127.0f, __frcp_rn(amax)) : 0.0f;
+    if (threadIdx.x == 0) Sx[m] = live ? __fdiv_rn(amax, 127.0f) : 1.0f;
+    uint2* q = reinterpret_cast<uint2*>(Xq + m * ldxq);
+    for (int v = threadIdx.x; v < nv; v += 256) {
+        const uint4 w = x[v];
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            unpack2<kBf16>(u[j], a, b);
+            h[j] = code_of(a, inv) | (code_of(b, inv) << 8);
+        }
+        q[v] = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    }
+}
+
+__global__ void bias_rows_kernel(const float* bias, void* Y, int64_t ldy, int y_type, int M, int N) {
+    const int64_t total = static_cast<int64_t>(M) * N;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total;
+         t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t m = t / N;
+        const int64_t n = t - m * N;
+        const float b = bias ? bias[n] : 0.0f;
+        if (y_type == QG_FP32) static_cast<float*>(Y)[m * ldy + n] = b;
+        else if (y_type == QG_BF16) static_cast<__nv_bfloat16*>(Y)[m * ldy + n] = __float2bfloat16_rn(b);
+        else static_cast<__half*>(Y)[m * ldy + n] = __float2half_rn(b);
+    }
+}
+
+template <int NA>
+cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                           const LaunchCtl& c, cudaStream_t st) {
+    using L = I8Layout<NA>;
+    cudaError_t e =
+        cudaFuncSetAttribute(int8_kernel<NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    Params p = gemm::base_params(s, a.Y, a.ldy, a.M, a.N, a.K, nullptr, c);
+    uint8_t* w = static_cast<uint8_t*>(a.ws);
+    p.cnt = reinterpret_cast<uint32_t*>(w);
+    p.part = reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(a.M, a.K));
+    const Out o{a.Sx, a.Sw, a.bias, a.y_type, (a.M + NA - 1) / NA};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(s.G));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kSmemBytes;
+    cfg.stream = st;
+    // always overlapped with the expansion kernel in front, which is part of
+    // this call: the weight stream starts under it
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, int8_kernel<NA>, tmW, tmX, p, o);
+}
+
+}  // namespace
+
+int int8_tile_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+size_t int8_expanded_bytes(int M, int K) {
+    return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255);
+}
+
+size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split) {
+    const size_t part = split ? static_cast<size_t>(s.G) * 2 * 128 * s.nmma * sizeof(float) : 0;
+    return kInt8CounterBytes + int8_expanded_bytes(M, K) + part;
+}
+
+cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                        const LaunchCtl& c, cudaStream_t st) {
+    if (static_cast<size_t>(s.G) * 8 * sizeof(uint32_t) > kInt8CounterBytes) return cudaErrorInvalidValue;
+    const int K16 = a.K / 16;
+    int64_t blocks = (static_cast<int64_t>(a.M) * K16 + 255) / 256;
+    if (blocks > 4 * c.num_sms) blocks = 4 * c.num_sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    if (c.overlap) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    uint4* xf = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.ws) + kInt8CounterBytes);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel, a.Xq, a.ldxq, xf, a.M, K16);
+    if (e != cudaSuccess) return e;
+    switch (s.nmma) {
+        case 16: return launch_int8_na<16>(a, s, tmW, tmX, c, st);
+        case 32: return launch_int8_na<32>(a, s, tmW, tmX, c, st);
+        case 64: return launch_int8_na<64>(a, s, tmW, tmX, c, st);
+        case 128: return launch_int8_na<128>(a, s, tmW, tmX, c, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_quantize_int8(const void* X, int x_type, int64_t ldx, int8_t* Xq, int64_t ldxq, float* Sx, int M,
+                                 int K, const LaunchCtl& c, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(M));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    if (c.overlap) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    const uint16_t* x = static_cast<const uint16_t*>(X);
+    if (x_type == QG_BF16) return cudaLaunchKernelEx(&cfg, quantize_int8_kernel<true>, x, ldx, Xq, ldxq, Sx, K);
+    return cudaLaunchKernelEx(&cfg, quantize_int8_kernel<false>, x, ldx, Xq, ldxq, Sx, K);
+}
+
+cudaError_t launch_int8_bias_rows(const Int8Args& a, cudaStream_t st) {
+    const int64_t total = static_cast<int64_t>(a.M) * a.N;
+    const int64_t blocks = total / 256 + 1 < 4096 ? total / 256 + 1 : 4096;
+    bias_rows_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(a.bias, a.Y, a.ldy, a.y_type, a.M, a.N);
+    return cudaGetLastError();
+}
+
+}  // namespace qg

@@ -1,0 +1,41 @@
+// Internal interface of the 8-bit integer kernels (qg_int8.cu) for the C ABI.
+#pragma once
+
+#include "qg_internal.h"
+
+namespace qg {
+
+struct Int8Args {
+    const int8_t* Xq;    // [M, ldxq]
+    int64_t ldxq;
+    const float* Sx;     // [M]
+    const float* Sw;     // [N]
+    const float* bias;   // [N] or null
+    void* Y;             // [M, ldy] of y_type
+    int64_t ldy;
+    int y_type;          // QG_BF16, QG_FP16 or QG_FP32
+    int M, N, K;
+    void* ws;
+};
+
+// Activation rows per tile (the MMA's N side) for a batch size.
+int int8_tile_rows(int M);
+
+// Workspace of a schedule (s.nmma = the tile's activation rows): the arrival
+// counters (kInt8CounterBytes, zero between calls, at offset 0 for every
+// shape), the activations as FP16 [M, K], then the split-K partial sums of a
+// schedule that splits tiles (two slots of 128 x s.nmma FP32 per CTA).
+constexpr size_t kInt8CounterBytes = 16384;
+size_t int8_expanded_bytes(int M, int K);
+size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split);
+
+// tmW: the weight map ([N, K] bytes, 128 x 128 boxes, 128-byte swizzle);
+// tmX: the expanded activations ([M, K] FP16, boxes of 64 K x s.nmma rows).
+cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                        const LaunchCtl& c, cudaStream_t st);
+cudaError_t launch_quantize_int8(const void* X, int x_type, int64_t ldx, int8_t* Xq, int64_t ldxq, float* Sx, int M,
+                                 int K, const LaunchCtl& c, cudaStream_t st);
+// Y = bias (or zeros) in every row: the K = 0 product.
+cudaError_t launch_int8_bias_rows(const Int8Args& a, cudaStream_t st);
+
+}  // namespace qg
