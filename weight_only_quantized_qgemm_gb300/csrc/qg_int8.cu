@@ -24,8 +24,8 @@
 //
 // One persistent CTA per SM; warps by role:
 //   warp 0        weight producer (TMA, one 16 KB box per unit)
-//   warp 1        activation producer (TMA, boxes of 64 K x NA rows), after
-//                 the expansion kernel's completion
+//   warp 1        activation producer (TMA, two boxes of 64 K x NA rows a unit),
+//                 after the expansion kernel's completion
 //   warp 2        MMA issuer: 8 tcgen05.mma (M = 128, N = NA, K = 16) a unit
 //   warps 4-      epilogue: one per TMEM lane quadrant (two for NA >= 128)
 //   the last 8    convert: two groups of four warps taking alternate units
@@ -56,24 +56,30 @@ struct I8Layout {
     static constexpr int kWarpConv0 = kWarpEpi0 + kEpi;
     static constexpr int kThreads = 32 * (kWarpConv0 + 4 * kGroups);
     static constexpr int kWBytes = 128 * 128;
-    static constexpr int kXSlot = NA * 128;                     // 64 K of FP16
-    static constexpr int kXStages = NA == 128 ? 6 : NA == 64 ? 8 : 12;
-    static constexpr int kWFit = (232448 - 2048 - kXStages * kXSlot) / kWBytes;
+    // The operand ring: a slot is one unit's A buffer in TMEM (64 columns) and
+    // its activations in shared memory (two boxes of 64 K).  One barrier says
+    // that both are there, one that the unit's MMAs have read them, so that
+    // the MMA warp passes one wait and one commit per unit: each costs it
+    // 0.05 to 0.1 us even when nothing is late (with separate rings, three
+    // waits and three commits a unit, gate/up at 16 rows took 28.0 us).
+    static constexpr int kSlots = 4;
+    static constexpr int kXBox = NA * 128;
+    static constexpr int kXSlot = 2 * kXBox;
+    static constexpr int kWFit = (232448 - 2048 - kSlots * kXSlot) / kWBytes;
     static constexpr int kWStages = (kWFit < 12 ? kWFit : 12) / kGroups * kGroups;
-    static constexpr int kNA = 4;                               // A buffers in TMEM, 64 columns each
     static constexpr int kD = 2;                                // accumulators, NA columns each
-    static constexpr int kDCol0 = kNA * 64;
+    static constexpr int kDCol0 = kSlots * 64;
     static constexpr int kXOff = kWStages * kWBytes;
-    static constexpr int kBarOff = kXOff + kXStages * kXSlot;
-    static constexpr int kNumBars = 2 * kWStages + 2 * kXStages + 2 * kNA + 2 * kD;
+    static constexpr int kBarOff = kXOff + kSlots * kXSlot;
+    static constexpr int kNumBars = 2 * kWStages + 2 * kSlots + 2 * kD;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmemBytes = kMiscOff + 64 + 1024;     // + alignment slack
     static_assert(kDCol0 + kD * NA <= 512, "TMEM columns");
     static_assert(kSmemBytes <= 232448, "shared memory");
-    static_assert(kXSlot % 1024 == 0, "keep the 1024-byte swizzle alignment");
-    // a weight stage and an A buffer always belong to one convert group, so
-    // that its parity waits are for the phase after one it has seen
-    static_assert(kWStages % kGroups == 0 && kNA % kGroups == 0, "ring ownership");
+    static_assert(kXBox % 1024 == 0, "keep the 1024-byte swizzle alignment");
+    // a weight stage and a slot always belong to one convert group, so that
+    // its parity waits are for the phase after one it has seen
+    static_assert(kWStages % kGroups == 0 && kSlots % kGroups == 0, "ring ownership");
     static_assert(kEpiCols % 16 == 0, "epilogue chunks");
 };
 
@@ -135,7 +141,7 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
     int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p,
                 const Out o) {
     using L = I8Layout<NA>;
-    constexpr int kWStages = L::kWStages, kXStages = L::kXStages, kNA = L::kNA, kD = L::kD;
+    constexpr int kWStages = L::kWStages, kSlots = L::kSlots, kD = L::kD;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -144,13 +150,11 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
     const uint32_t bar0 = base + L::kBarOff;
     auto wfull = [&](int s) { return bar0 + 8u * s; };
     auto wempty = [&](int s) { return bar0 + 8u * (kWStages + s); };
-    auto xfull = [&](int s) { return bar0 + 8u * (2 * kWStages + s); };
-    auto xempty = [&](int s) { return bar0 + 8u * (2 * kWStages + kXStages + s); };
-    constexpr int kBarA = 2 * kWStages + 2 * kXStages;
-    auto afull = [&](int a) { return bar0 + 8u * (kBarA + a); };
-    auto afree = [&](int a) { return bar0 + 8u * (kBarA + kNA + a); };
-    auto dfull = [&](int b) { return bar0 + 8u * (kBarA + 2 * kNA + b); };
-    auto dempty = [&](int b) { return bar0 + 8u * (kBarA + 2 * kNA + kD + b); };
+    auto ofull = [&](int a) { return bar0 + 8u * (2 * kWStages + a); };
+    auto ofree = [&](int a) { return bar0 + 8u * (2 * kWStages + kSlots + a); };
+    constexpr int kBarD = 2 * kWStages + 2 * kSlots;
+    auto dfull = [&](int b) { return bar0 + 8u * (kBarD + b); };
+    auto dempty = [&](int b) { return bar0 + 8u * (kBarD + kD + b); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kMiscOff);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMiscOff + 4);
 
@@ -161,18 +165,24 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
     const long long u1 = gemm::unit_begin(cta + 1, p.U, p.G);
     const int nunits = static_cast<int>(u1 - u0);
 
+    // a weight tile serves tm_count tiles in a row: keep it for their re-reads
+    auto load_w = [&](int s, const Cursor& cur) {
+        mbar_arrive_expect_tx(wfull(s), L::kWBytes);
+        tma_load_2d(base + s * L::kWBytes, &tmW, wfull(s), cur.kr * 128, cur.tile / o.tm_count * 128,
+                    o.tm_count > 1 ? policy_evict_last() : policy_evict_first());
+    };
+    auto skipped = [&](int i) { return cta == 0 && i == p.fault_unit; };   // failure-path test hook
+    Cursor wcur(u0, p.KB);   // the weight producer's place
+    int wissued = 0;
     if (threadIdx.x == 0) {
+        prefetch_tmap(&tmW);
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(wfull(s), 1);
             mbar_init(wempty(s), 4);   // the four warps of the convert group
         }
-        for (int s = 0; s < kXStages; ++s) {
-            mbar_init(xfull(s), 1);
-            mbar_init(xempty(s), 1);   // commit
-        }
-        for (int a = 0; a < kNA; ++a) {
-            mbar_init(afull(a), 4);
-            mbar_init(afree(a), 1);    // commit
+        for (int a = 0; a < kSlots; ++a) {
+            mbar_init(ofull(a), 5);    // the convert group's four warps, the activations' copies
+            mbar_init(ofree(a), 1);    // commit
         }
         for (int b = 0; b < kD; ++b) {
             mbar_init(dfull(b), 1);    // commit: the piece's MMAs are complete
@@ -180,9 +190,13 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
         }
         *abort_flag = 0;
         fence_barrier_init();
+        // the first turn of the weight ring, before the CTA has met: it needs
+        // nothing but the barriers just set up
+        for (; wissued < kWStages && wissued < nunits; ++wissued, wcur.step(p.KB))
+            if (!skipped(wissued)) load_w(wissued, wcur);
     }
     __syncwarp();
-    if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
+    if (warp == kWarpMma) tmem_alloc(smem_u32(tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -192,24 +206,13 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
 
     if (warp == kWarpWProd) {
         if (lane == 0) {
-            prefetch_tmap(&tmW);
-            // a weight tile serves tm_count tiles in a row: keep it for their re-reads
-            const uint64_t pol = o.tm_count > 1 ? policy_evict_last() : policy_evict_first();
-            int issued = 0;
-            Cursor cur(u0, p.KB);
-            Ring<kWStages> rw(0);
-            for (int i = 0; i < nunits; ++i, cur.step(p.KB), rw.step(1)) {
-                if (i >= kWStages && !wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
-                issued = i + 1;
-                if (cta == 0 && i == p.fault_unit) continue;   // failure-path test hook
-                mbar_arrive_expect_tx(wfull(rw.slot), L::kWBytes);
-                tma_load_2d(base + rw.slot * L::kWBytes, &tmW, wfull(rw.slot), cur.kr * 128,
-                            cur.tile / o.tm_count * 128, pol);
+            Ring<kWStages> rw(wissued);
+            for (; wissued < nunits; ++wissued, wcur.step(p.KB), rw.step(1)) {
+                if (!wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
+                if (!skipped(wissued)) load_w(rw.slot, wcur);
             }
-            for (int i = issued - kWStages < 0 ? 0 : issued - kWStages; i < issued; ++i) {
-                if (cta == 0 && i == p.fault_unit) continue;
-                gemm::drain_wait(wfull(i % kWStages), (i / kWStages) & 1, p.timeout_ns);
-            }
+            for (int i = wissued - kWStages < 0 ? 0 : wissued - kWStages; i < wissued; ++i)
+                if (!skipped(i)) gemm::drain_wait(wfull(i % kWStages), (i / kWStages) & 1, p.timeout_ns);
         }
     } else if (warp == kWarpXProd) {
         if (lane == 0) {
@@ -218,78 +221,70 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             const uint64_t pol = policy_evict_last();
             int issued = 0;
             Cursor cur(u0, p.KB);
-            Ring<kXStages> rx(0);
-            for (int i = 0; i < 2 * nunits; ++i, rx.step(1)) {
-                if (i >= kXStages && !wait_bounded(xempty(rx.slot), rx.phase ^ 1u, wc)) break;
-                mbar_arrive_expect_tx(xfull(rx.slot), L::kXSlot);
-                tma_load_2d(base + L::kXOff + rx.slot * L::kXSlot, &tmX, xfull(rx.slot), cur.kr * 128 + (i & 1) * 64,
-                            cur.tile % o.tm_count * NA, pol);
+            Ring<kSlots> ro(0);
+            for (int i = 0; i < nunits; ++i, cur.step(p.KB), ro.step(1)) {
+                if (i >= kSlots && !wait_bounded(ofree(ro.slot), ro.phase ^ 1u, wc)) break;
+                const uint32_t dst = base + L::kXOff + ro.slot * L::kXSlot;
+                const int m0 = cur.tile % o.tm_count * NA;
+                mbar_arrive_expect_tx(ofull(ro.slot), L::kXSlot);
+                tma_load_2d(dst, &tmX, ofull(ro.slot), cur.kr * 128, m0, pol);
+                tma_load_2d(dst + L::kXBox, &tmX, ofull(ro.slot), cur.kr * 128 + 64, m0, pol);
                 issued = i + 1;
-                if (i & 1) cur.step(p.KB);
             }
-            for (int i = issued - kXStages < 0 ? 0 : issued - kXStages; i < issued; ++i)
-                gemm::drain_wait(xfull(i % kXStages), (i / kXStages) & 1, p.timeout_ns);
+            // a slot's barrier completes with its weights too: after a wait
+            // that gave up they may be missing, and the drain gives up as well
+            for (int i = issued - kSlots < 0 ? 0 : issued - kSlots; i < issued; ++i)
+                gemm::drain_wait(ofull(i % kSlots), (i / kSlots) & 1, p.timeout_ns);
         }
     } else if (warp == kWarpMma) {
         const bool elected = elect_one();
         constexpr uint32_t idesc = idesc_f16(NA, false);
         const uint64_t dx0 = smem_desc_sw128(base + L::kXOff);
         Cursor cur(u0, p.KB);
-        Ring<kXStages> rx(0);
-        Ring<kNA> ra(0);
+        Ring<kSlots> ro(0);
         int piece = 0;
         int last_a = -1;
         uint32_t last_ph = 0;
         bool fresh = true;   // the next MMA starts a piece
-        bool ok = true;
-        for (int i = 0; i < nunits && ok; ++i, ra.step(1)) {
+        for (int i = 0; i < nunits; ++i, ro.step(1)) {
             const int b = piece % kD;
             if (fresh && piece >= kD && !gemm::warp_wait(dempty(b), ((piece / kD) - 1) & 1, wc)) break;
-            if (!gemm::warp_wait(afull(ra.slot), ra.phase, wc)) break;
+            if (!gemm::warp_wait(ofull(ro.slot), ro.phase, wc)) break;
+            tc_fence_after();
             const uint32_t dt = tmem + L::kDCol0 + b * NA;
-            const uint32_t at = tmem + ra.slot * 64;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ok = gemm::warp_wait(xfull(rx.slot), rx.phase, wc);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t xd = dx0 + static_cast<uint64_t>((rx.slot * L::kXSlot) >> 4);
-                if (elected) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_ts_f16(dt, at + h * 32 + j * 8, xd + 2 * j, idesc, (h > 0 || j > 0 || !fresh) ? 1u : 0u);
-                    tc_commit(xempty(rx.slot));
-                }
-                __syncwarp();
-                rx.step(1);
-            }
+            const uint32_t at = tmem + ro.slot * 64;
+            const uint64_t xd = dx0 + static_cast<uint64_t>((ro.slot * L::kXSlot) >> 4);
             const bool closes = i == nunits - 1 || cur.kb == p.KB - 1;
             if (elected) {
-                tc_commit(afree(ra.slot));
-                if (closes && ok) tc_commit(dfull(b));
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    mma_ts_f16(dt, at + j * 8, xd + (((j >> 2) * L::kXBox + (j & 3) * 32) >> 4), idesc,
+                               (j > 0 || !fresh) ? 1u : 0u);
+                tc_commit(ofree(ro.slot));
+                if (closes) tc_commit(dfull(b));
             }
             __syncwarp();
-            last_a = ra.slot;
-            last_ph = ra.phase;
+            last_a = ro.slot;
+            last_ph = ro.phase;
             fresh = closes;
             if (closes) ++piece;
             cur.step(p.KB);
         }
-        if (last_a >= 0 && elected) gemm::drain_wait(afree(last_a), last_ph, p.timeout_ns);
+        if (last_a >= 0 && elected) gemm::drain_wait(ofree(last_a), last_ph, p.timeout_ns);
     } else if (warp >= L::kWarpConv0) {
         const int q = warp & 3;
         const int grp = (warp - L::kWarpConv0) >> 2;
         const int row = q * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
         Ring<kWStages> rw(grp);
-        Ring<kNA> ra(grp);
-        for (int i = grp; i < nunits; i += kGroups, rw.step(kGroups), ra.step(kGroups)) {
+        Ring<kSlots> ro(grp);
+        for (int i = grp; i < nunits; i += kGroups, rw.step(kGroups), ro.step(kGroups)) {
             if (!gemm::warp_wait(wfull(rw.slot), rw.phase, wc)) break;
             const uint8_t* src = gbase + rw.slot * L::kWBytes + row * 128;
             uint4 c[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
-            if (i >= kNA && !gemm::warp_wait(afree(ra.slot), ra.phase ^ 1u, wc)) break;
+            if (i >= kSlots && !gemm::warp_wait(ofree(ro.slot), ro.phase ^ 1u, wc)) break;
             __syncwarp();
             tc_fence_after();
 #pragma unroll
@@ -303,7 +298,7 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
                     s8x4_to_f16(w.z, f[8 * e + 4], f[8 * e + 5]);
                     s8x4_to_f16(w.w, f[8 * e + 6], f[8 * e + 7]);
                 }
-                tmem_st_x16(tl + ra.slot * 64 + t * 16, f);
+                tmem_st_x16(tl + ro.slot * 64 + t * 16, f);
             }
             // the loads have returned: the TMEM stores above needed them
             __syncwarp();
@@ -311,7 +306,7 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(afull(ra.slot));
+            if (lane == 0) mbar_arrive(ofull(ro.slot));
         }
     } else if (warp >= kWarpEpi0) {
         const int ew = warp - kWarpEpi0;
@@ -408,7 +403,7 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == kWarpMma) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
