@@ -168,6 +168,13 @@ Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
     s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : kind == QG_KIND_INT8 ? int8_tile_rows(M) : M <= 16 ? 16 : 32;
     // W8A8 and INT8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
     s.T = (N + 127) / 128 * (kind == QG_KIND_W8A8 || kind == QG_KIND_INT8 ? (M + s.nmma - 1) / s.nmma : 1);
+    // INT8 tiles on CTA pairs are 256 weight rows; the grid counts pairs below
+    const int ctas = kind == QG_KIND_INT8 ? int8_ctas(s.nmma) : 1;
+    if (ctas == 2) {
+        s.T = (N + 255) / 256 * ((M + s.nmma - 1) / s.nmma);
+        sms = sms > 1 ? sms / 2 : 1;
+        forced = forced > 0 ? (forced + 1) / 2 : 0;
+    }
     // one unit = 128 rows x one 128-wide K block (W8A8: two blocks)
     s.KU = kind == QG_KIND_W8A8 ? (K + 255) / 256 : (K + 127) / 128;
     s.U = static_cast<long long>(s.T) * s.KU;
@@ -208,6 +215,9 @@ Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
     s.max_ctas = sms > s.G ? sms : s.G;
     return s;
 }
+
+// CTAs of the launch per G of the schedule (2 where G counts CTA pairs).
+int schedule_ctas(int kind, const Schedule& s) { return kind == QG_KIND_INT8 ? int8_ctas(s.nmma) : 1; }
 
 Schedule choose_schedule(int kind, int M, int N, int K, int sms) {
     return schedule_for(kind, M, N, K, sms, table_lookup(kind, M, N, K));
@@ -756,7 +766,7 @@ qg_status qgemm_w8a8_int8(const int8_t* Xq, int64_t ldxq, const float* X_scale, 
                    static_cast<uint64_t>(K), 128, 128) ||
         !make_tmap(&tmX, static_cast<uint8_t*>(workspace) + kInt8CounterBytes, CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                    static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K) * 2, 64,
-                   static_cast<uint32_t>(s.nmma)))
+                   static_cast<uint32_t>(s.nmma / int8_ctas(s.nmma))))
         return QG_ERR_CUDA;
     return launch_int8(a, s, tmW, tmX, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
@@ -951,12 +961,14 @@ int qg_dispatch_get(int kind, int M, int N, int K) {
     if (M < 1 || M > max_m(kind) || N < 1 || K < 1) return 0;
     DeviceInfo* d = device_info();
     if (!d) return 0;
-    return cached_schedule(kind, M, N, K, d->sms).s.G;
+    const Schedule& s = cached_schedule(kind, M, N, K, d->sms).s;
+    return s.G * schedule_ctas(kind, s);
 }
 
 int qg_dispatch_rule(int kind, int M, int N, int K, int sms) {
     if (max_m(kind) == 0 || M < 1 || M > max_m(kind) || N < 1 || K < 1 || sms < 1) return 0;
-    return schedule_for(kind, M, N, K, sms, 0).G;
+    const Schedule s = schedule_for(kind, M, N, K, sms, 0);
+    return s.G * schedule_ctas(kind, s);
 }
 
 void qg_dispatch_clear(void) {

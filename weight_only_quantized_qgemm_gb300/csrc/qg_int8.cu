@@ -49,8 +49,10 @@ using gemm::Ring;
 constexpr int kWarpWProd = 0, kWarpXProd = 1, kWarpMma = 2, kWarpEpi0 = 4;
 constexpr int kGroups = 2;   // convert groups of four warps
 
-template <int NA>
+// NA activation rows a tile; kPair: a tile is 256 weight rows on a CTA pair.
+template <int NA, bool kPair>
 struct I8Layout {
+    static constexpr int kCtas = kPair ? 2 : 1;
     static constexpr int kEpi = NA >= 128 ? 8 : 4;
     static constexpr int kEpiCols = NA / (kEpi / 4);            // columns per epilogue warp
     static constexpr int kWarpConv0 = kWarpEpi0 + kEpi;
@@ -63,11 +65,12 @@ struct I8Layout {
     // 0.05 to 0.1 us even when nothing is late (with separate rings, three
     // waits and three commits a unit, gate/up at 16 rows took 28.0 us).
     static constexpr int kSlots = 4;
-    static constexpr int kXBox = NA * 128;
+    static constexpr int kXRows = NA / kCtas;                   // of the tile, in this CTA's shared memory
+    static constexpr int kXBox = kXRows * 128;
     static constexpr int kXSlot = 2 * kXBox;
     static constexpr int kWFit = (232448 - 2048 - kSlots * kXSlot) / kWBytes;
     static constexpr int kWStages = (kWFit < 12 ? kWFit : 12) / kGroups * kGroups;
-    static constexpr int kD = 2;                                // accumulators, NA columns each
+    static constexpr int kD = NA > 128 ? 1 : 2;                 // accumulators, NA columns each
     static constexpr int kDCol0 = kSlots * 64;
     static constexpr int kXOff = kWStages * kWBytes;
     static constexpr int kBarOff = kXOff + kSlots * kXSlot;
@@ -136,11 +139,11 @@ __device__ __forceinline__ float4* part_slot(const Params& p, int cta, int which
     return reinterpret_cast<float4*>(p.part) + (static_cast<size_t>(cta) * 2 + which) * (NA / 4) * 128;
 }
 
-template <int NA>
-__global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
+template <int NA, bool kPair>
+__global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p,
                 const Out o) {
-    using L = I8Layout<NA>;
+    using L = I8Layout<NA, kPair>;
     constexpr int kWStages = L::kWStages, kSlots = L::kSlots, kD = L::kD;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -161,14 +164,19 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
-    const long long u0 = gemm::unit_begin(cta, p.U, p.G);
-    const long long u1 = gemm::unit_begin(cta + 1, p.U, p.G);
+    // the units of a worker: a CTA, or a pair (both CTAs walk the same ones)
+    const int worker = cta / L::kCtas;
+    const uint32_t rank = kPair ? cluster_cta_rank() : 0u;
+    const bool leader = rank == 0;
+    const long long u0 = gemm::unit_begin(worker, p.U, p.G);
+    const long long u1 = gemm::unit_begin(worker + 1, p.U, p.G);
     const int nunits = static_cast<int>(u1 - u0);
 
     // a weight tile serves tm_count tiles in a row: keep it for their re-reads
     auto load_w = [&](int s, const Cursor& cur) {
         mbar_arrive_expect_tx(wfull(s), L::kWBytes);
-        tma_load_2d(base + s * L::kWBytes, &tmW, wfull(s), cur.kr * 128, cur.tile / o.tm_count * 128,
+        tma_load_2d(base + s * L::kWBytes, &tmW, wfull(s), cur.kr * 128,
+                    (cur.tile / o.tm_count * L::kCtas + static_cast<int>(rank)) * 128,
                     o.tm_count > 1 ? policy_evict_last() : policy_evict_first());
     };
     auto skipped = [&](int i) { return cta == 0 && i == p.fault_unit; };   // failure-path test hook
@@ -181,12 +189,14 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             mbar_init(wempty(s), 4);   // the four warps of the convert group
         }
         for (int a = 0; a < kSlots; ++a) {
-            mbar_init(ofull(a), 5);    // the convert group's four warps, the activations' copies
+            // each CTA's four convert warps, and the activations' copies (the
+            // leader's barrier counts for the pair)
+            mbar_init(ofull(a), 4 * L::kCtas + 1);
             mbar_init(ofree(a), 1);    // commit
         }
         for (int b = 0; b < kD; ++b) {
             mbar_init(dfull(b), 1);    // commit: the piece's MMAs are complete
-            mbar_init(dempty(b), L::kEpi);
+            mbar_init(dempty(b), L::kEpi * L::kCtas);
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -196,9 +206,13 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             if (!skipped(wissued)) load_w(wissued, wcur);
     }
     __syncwarp();
-    if (warp == kWarpMma) tmem_alloc(smem_u32(tmem_slot), 512);
+    if (warp == kWarpMma) {
+        if constexpr (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+        else tmem_alloc(smem_u32(tmem_slot), 512);
+    }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (kPair) cluster_sync_all();   // the peer's barriers are set up too
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const WaitCtl wc{p.timeout_ns, p.status, abort_flag};
@@ -225,21 +239,35 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             for (int i = 0; i < nunits; ++i, cur.step(p.KB), ro.step(1)) {
                 if (i >= kSlots && !wait_bounded(ofree(ro.slot), ro.phase ^ 1u, wc)) break;
                 const uint32_t dst = base + L::kXOff + ro.slot * L::kXSlot;
-                const int m0 = cur.tile % o.tm_count * NA;
-                mbar_arrive_expect_tx(ofull(ro.slot), L::kXSlot);
-                tma_load_2d(dst, &tmX, ofull(ro.slot), cur.kr * 128, m0, pol);
-                tma_load_2d(dst + L::kXBox, &tmX, ofull(ro.slot), cur.kr * 128 + 64, m0, pol);
+                const int m0 = cur.tile % o.tm_count * NA + static_cast<int>(rank) * L::kXRows;
+                if (leader) mbar_arrive_expect_tx(ofull(ro.slot), L::kXSlot * L::kCtas);
+                if constexpr (kPair) {
+                    const uint32_t bar = map_to_cta(ofull(ro.slot), 0);
+                    tma_load_2d_pair(dst, &tmX, bar, cur.kr * 128, m0, pol);
+                    tma_load_2d_pair(dst + L::kXBox, &tmX, bar, cur.kr * 128 + 64, m0, pol);
+                } else {
+                    tma_load_2d(dst, &tmX, ofull(ro.slot), cur.kr * 128, m0, pol);
+                    tma_load_2d(dst + L::kXBox, &tmX, ofull(ro.slot), cur.kr * 128 + 64, m0, pol);
+                }
                 issued = i + 1;
             }
-            // a slot's barrier completes with its weights too: after a wait
-            // that gave up they may be missing, and the drain gives up as well
+            // a unit whose MMAs are complete has its copies; after a wait that
+            // gave up some never run, and the drain gives up as well
             for (int i = issued - kSlots < 0 ? 0 : issued - kSlots; i < issued; ++i)
-                gemm::drain_wait(ofull(i % kSlots), (i / kSlots) & 1, p.timeout_ns);
+                gemm::drain_wait(ofree(i % kSlots), (i / kSlots) & 1, p.timeout_ns);
         }
-    } else if (warp == kWarpMma) {
+    } else if (warp == kWarpMma && leader) {
         const bool elected = elect_one();
-        constexpr uint32_t idesc = idesc_f16(NA, false);
+        constexpr uint32_t idesc = idesc_f16(NA, false, 128 * L::kCtas);
         const uint64_t dx0 = smem_desc_sw128(base + L::kXOff);
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if constexpr (kPair) return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, wc)) != 0;
+            else return gemm::warp_wait(bar, parity, wc);
+        };
+        auto commit = [&](uint32_t bar) {
+            if constexpr (kPair) tc_commit_pair(bar);
+            else tc_commit(bar);
+        };
         Cursor cur(u0, p.KB);
         Ring<kSlots> ro(0);
         int piece = 0;
@@ -248,8 +276,8 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
         bool fresh = true;   // the next MMA starts a piece
         for (int i = 0; i < nunits; ++i, ro.step(1)) {
             const int b = piece % kD;
-            if (fresh && piece >= kD && !gemm::warp_wait(dempty(b), ((piece / kD) - 1) & 1, wc)) break;
-            if (!gemm::warp_wait(ofull(ro.slot), ro.phase, wc)) break;
+            if (fresh && piece >= kD && !wait(dempty(b), ((piece / kD) - 1) & 1)) break;
+            if (!wait(ofull(ro.slot), ro.phase)) break;
             tc_fence_after();
             const uint32_t dt = tmem + L::kDCol0 + b * NA;
             const uint32_t at = tmem + ro.slot * 64;
@@ -257,11 +285,13 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             const bool closes = i == nunits - 1 || cur.kb == p.KB - 1;
             if (elected) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    mma_ts_f16(dt, at + j * 8, xd + (((j >> 2) * L::kXBox + (j & 3) * 32) >> 4), idesc,
-                               (j > 0 || !fresh) ? 1u : 0u);
-                tc_commit(ofree(ro.slot));
-                if (closes) tc_commit(dfull(b));
+                for (int j = 0; j < 8; ++j) {
+                    const uint64_t bd = xd + (((j >> 2) * L::kXBox + (j & 3) * 32) >> 4);
+                    if constexpr (kPair) mma_ts_f16_pair(dt, at + j * 8, bd, idesc, (j > 0 || !fresh) ? 1u : 0u);
+                    else mma_ts_f16(dt, at + j * 8, bd, idesc, (j > 0 || !fresh) ? 1u : 0u);
+                }
+                commit(ofree(ro.slot));
+                if (closes) commit(dfull(b));
             }
             __syncwarp();
             last_a = ro.slot;
@@ -306,7 +336,10 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(ofull(ro.slot));
+            if (lane == 0) {
+                if (kPair && !leader) mbar_arrive_cluster(map_to_cta(ofull(ro.slot), 0));
+                else mbar_arrive(ofull(ro.slot));
+            }
         }
     } else if (warp >= kWarpEpi0) {
         const int ew = warp - kWarpEpi0;
@@ -327,7 +360,7 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             if (pe > nunits - 1) pe = nunits - 1;
             const bool whole = kb0 == 0 && pe - ps == p.KB - 1;
             const int tn = tile / o.tm_count;
-            const int n = tn * 128 + row;
+            const int n = (tn * L::kCtas + static_cast<int>(rank)) * 128 + row;
             const int m0 = (tile - tn * o.tm_count) * NA + col0;
             const float sw = n < p.N ? o.sw[n] : 0.0f;
             const float bias = o.bias != nullptr && n < p.N ? o.bias[n] : 0.0f;
@@ -356,15 +389,19 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(dempty(b));
+            if (lane == 0) {
+                if (kPair && !leader) mbar_arrive_cluster(map_to_cta(dempty(b), 0));
+                else mbar_arrive(dempty(b));
+            }
             if (!whole) {
                 // every lane's partial visible GPU-wide before lane 0's arrival.  A
                 // split tile's counter is indexed by the CTA that holds its first
-                // unit: that CTA's last tile, so no other tile shares it.
+                // unit: that CTA's last tile, so no other tile shares it (a pair's
+                // CTAs keep partial sums and counters of their own).
                 const int cf = __shfl_sync(0xffffffffu, split_info, 3 * which);
                 const int cl = __shfl_sync(0xffffffffu, split_info, 3 * which + 1);
                 const int w_first = __shfl_sync(0xffffffffu, split_info, 3 * which + 2);
-                uint32_t* cnt = p.cnt + cf * 8 + ew;
+                uint32_t* cnt = p.cnt + (cf * L::kCtas + static_cast<int>(rank)) * 8 + ew;
                 __threadfence();
                 __syncwarp();
                 uint32_t prev = 0;
@@ -380,7 +417,9 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
                         for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
 #pragma unroll 4
                         for (int c2 = cf; c2 <= cl; ++c2) {
-                            const float4* src = part_slot<NA>(p, c2, c2 == cf ? w_first : 0) + (col0 / 4 + 4 * c) * 128 + row;
+                            const float4* src =
+                                part_slot<NA>(p, c2 * L::kCtas + static_cast<int>(rank), c2 == cf ? w_first : 0) +
+                                (col0 / 4 + 4 * c) * 128 + row;
 #pragma unroll
                             for (int g = 0; g < 4; ++g) {
                                 const float4 x = __ldcg(src + g * 128);
@@ -402,11 +441,16 @@ __global__ void __launch_bounds__(I8Layout<NA>::kThreads, 1)
     }
 
     tc_fence_before();
-    __syncthreads();
+    // a pair leaves together: the leader's MMAs read both CTAs' operands, and
+    // either's threads arrive on the other's barriers
+    __syncwarp();
+    if constexpr (kPair) cluster_sync_all();
+    else __syncthreads();
     if (warp == kWarpMma) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if constexpr (kPair) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
     }
 }
 
@@ -512,12 +556,12 @@ __global__ void bias_rows_kernel(const float* bias, void* Y, int64_t ldy, int y_
     }
 }
 
-template <int NA>
+template <int NA, bool kPair>
 cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                            const LaunchCtl& c, cudaStream_t st) {
-    using L = I8Layout<NA>;
+    using L = I8Layout<NA, kPair>;
     cudaError_t e =
-        cudaFuncSetAttribute(int8_kernel<NA>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+        cudaFuncSetAttribute(int8_kernel<NA, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     Params p = gemm::base_params(s, a.Y, a.ldy, a.M, a.N, a.K, nullptr, c);
     uint8_t* w = static_cast<uint8_t*>(a.ws);
@@ -525,36 +569,40 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
     p.part = reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(a.M, a.K));
     const Out o{a.Sx, a.Sw, a.bias, a.y_type, (a.M + NA - 1) / NA};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(s.G));
+    cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
     cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kSmemBytes;
     cfg.stream = st;
     // always overlapped with the expansion kernel in front, which is part of
     // this call: the weight stream starts under it
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, int8_kernel<NA>, tmW, tmX, p, o);
+    cfg.numAttrs = kPair ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, int8_kernel<NA, kPair>, tmW, tmX, p, o);
 }
 
 }  // namespace
 
-int int8_tile_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+int int8_tile_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
 
 size_t int8_expanded_bytes(int M, int K) {
     return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255);
 }
 
 size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split) {
-    const size_t part = split ? static_cast<size_t>(s.G) * 2 * 128 * s.nmma * sizeof(float) : 0;
+    const size_t part = split ? static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 2 * 128 * s.nmma * sizeof(float) : 0;
     return kInt8CounterBytes + int8_expanded_bytes(M, K) + part;
 }
 
 cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                         const LaunchCtl& c, cudaStream_t st) {
-    if (static_cast<size_t>(s.G) * 8 * sizeof(uint32_t) > kInt8CounterBytes) return cudaErrorInvalidValue;
+    if (static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 8 * sizeof(uint32_t) > kInt8CounterBytes) return cudaErrorInvalidValue;
     const int K16 = a.K / 16;
     int64_t blocks = (static_cast<int64_t>(a.M) * K16 + 255) / 256;
     if (blocks > 4 * c.num_sms) blocks = 4 * c.num_sms;
@@ -573,10 +621,11 @@ cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap&
     cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel, a.Xq, a.ldxq, xf, a.M, K16);
     if (e != cudaSuccess) return e;
     switch (s.nmma) {
-        case 16: return launch_int8_na<16>(a, s, tmW, tmX, c, st);
-        case 32: return launch_int8_na<32>(a, s, tmW, tmX, c, st);
-        case 64: return launch_int8_na<64>(a, s, tmW, tmX, c, st);
-        case 128: return launch_int8_na<128>(a, s, tmW, tmX, c, st);
+        case 16: return launch_int8_na<16, false>(a, s, tmW, tmX, c, st);
+        case 32: return launch_int8_na<32, false>(a, s, tmW, tmX, c, st);
+        case 64: return launch_int8_na<64, false>(a, s, tmW, tmX, c, st);
+        case 128: return launch_int8_na<128, false>(a, s, tmW, tmX, c, st);
+        case 256: return launch_int8_na<256, true>(a, s, tmW, tmX, c, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -18,8 +18,11 @@ struct Int8Args {
     void* ws;
 };
 
-// Activation rows per tile (the MMA's N side) for a batch size.
+// Activation rows per tile (the MMA's N side) for a batch size, and the CTAs
+// that work on a tile together (2: a CTA pair with a tile of 256 weight rows;
+// a schedule's G then counts pairs).
 int int8_tile_rows(int M);
+inline int int8_ctas(int tile_rows) { return tile_rows > 128 ? 2 : 1; }
 
 // Workspace of a schedule (s.nmma = the tile's activation rows): the arrival
 // counters (kInt8CounterBytes, zero between calls, at offset 0 for every
@@ -30,7 +33,8 @@ size_t int8_expanded_bytes(int M, int K);
 size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split);
 
 // tmW: the weight map ([N, K] bytes, 128 x 128 boxes, 128-byte swizzle);
-// tmX: the expanded activations ([M, K] FP16, boxes of 64 K x s.nmma rows).
+// tmX: the expanded activations ([M, K] FP16, boxes of 64 K x the rows of a
+// tile that one CTA holds, s.nmma / int8_ctas).
 cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                         const LaunchCtl& c, cudaStream_t st);
 cudaError_t launch_quantize_int8(const void* X, int x_type, int64_t ldx, int8_t* Xq, int64_t ldxq, float* Sx, int M,
