@@ -57,6 +57,8 @@ struct I8Layout {
     static constexpr int kEpiCols = NA / (kEpi / 4);            // columns per epilogue warp
     static constexpr int kWarpConv0 = kWarpEpi0 + kEpi;
     static constexpr int kThreads = 32 * (kWarpConv0 + 4 * kGroups);
+    // per epilogue warp, the activation scales of the columns at hand
+    static constexpr int kScaleCols = kEpiCols < 64 ? kEpiCols : 64;
     static constexpr int kWBytes = 128 * 128;
     // The operand ring: a slot is one unit's A buffer in TMEM (64 columns) and
     // its activations in shared memory (two boxes of 64 K).  One barrier says
@@ -68,7 +70,7 @@ struct I8Layout {
     static constexpr int kXRows = NA / kCtas;                   // of the tile, in this CTA's shared memory
     static constexpr int kXBox = kXRows * 128;
     static constexpr int kXSlot = 2 * kXBox;
-    static constexpr int kWFit = (232448 - 2048 - kSlots * kXSlot) / kWBytes;
+    static constexpr int kWFit = (232448 - 512 - kEpi * kScaleCols * 4 - kSlots * kXSlot) / kWBytes;
     static constexpr int kWStages = (kWFit < 12 ? kWFit : 12) / kGroups * kGroups;
     static constexpr int kD = NA > 128 ? 1 : 2;                 // accumulators, NA columns each
     static constexpr int kDCol0 = kSlots * 64;
@@ -76,7 +78,8 @@ struct I8Layout {
     static constexpr int kBarOff = kXOff + kSlots * kXSlot;
     static constexpr int kNumBars = 2 * kWStages + 2 * kSlots + 2 * kD;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kSmemBytes = kMiscOff + 64 + 1024;     // + alignment slack
+    static constexpr int kScaleOff = (kMiscOff + 16 + 15) / 16 * 16;
+    static constexpr int kSmemBytes = kScaleOff + kEpi * kScaleCols * 4;
     static_assert(kDCol0 + kD * NA <= 512, "TMEM columns");
     static_assert(kSmemBytes <= 232448, "shared memory");
     static_assert(kXBox % 1024 == 0, "keep the 1024-byte swizzle alignment");
@@ -91,6 +94,7 @@ struct Out {
     const float* sw;
     const float* bias;
     int y_type;
+    int y_pairs;    // a 16-bit Y that takes 32-bit stores of two neighbouring columns
     int tm_count;   // activation row blocks; tile t = (weight tile t / tm_count, block t % tm_count)
 };
 
@@ -104,18 +108,47 @@ __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& 
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
-// 16 output columns (activation rows m0 ..) of weight row n.  sxl: lane l's
-// scale of row m0 + l (l < 16).
-__device__ __forceinline__ void store16(const Params& p, const Out& o, int n, int m0, float sxl, float sw, float b,
+// Two neighbouring weight rows' outputs as one 32-bit store: for activation
+// rows m and m + 1 the even lane of a pair writes (n, n + 1) of row m and the
+// odd lane (n - 1, n) of row m + 1, which halves the stores of a tile.
+template <class T2, class T>
+__device__ __forceinline__ void store_pairs(T* Y, int64_t ldy, int n, int N, int rows, const float (&y)[16]) {
+    const int odd = threadIdx.x & 1;
+    T* at = Y + odd * ldy - odd;
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        const float other = __shfl_xor_sync(0xffffffffu, odd ? y[j] : y[j + 1], 1);
+        T2 v;
+        v.x = T(odd ? other : y[j]);
+        v.y = T(odd ? y[j + 1] : other);
+        if (n < N && j + odd < rows) *reinterpret_cast<T2*>(at + j * ldy) = v;
+    }
+}
+
+// 16 output columns (activation rows m0 ..) of weight row n; sx: their scales
+// in shared memory.
+__device__ __forceinline__ void store16(const Params& p, const Out& o, int n, int m0, const float* sx, float sw, float b,
                                         const float (&v)[16]) {
     const int64_t ldy = p.seg[0].ldy;
     float y[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-        y[j] = __fmaf_rn(__fmul_rn(v[j], __shfl_sync(0xffffffffu, sxl, j)), sw, b);
-    if (n >= p.N) return;
+    for (int g = 0; g < 4; ++g) {
+        const float4 s = reinterpret_cast<const float4*>(sx)[g];
+        y[4 * g + 0] = __fmaf_rn(__fmul_rn(v[4 * g + 0], s.x), sw, b);
+        y[4 * g + 1] = __fmaf_rn(__fmul_rn(v[4 * g + 1], s.y), sw, b);
+        y[4 * g + 2] = __fmaf_rn(__fmul_rn(v[4 * g + 2], s.z), sw, b);
+        y[4 * g + 3] = __fmaf_rn(__fmul_rn(v[4 * g + 3], s.w), sw, b);
+    }
     const int64_t at = static_cast<int64_t>(m0) * ldy + n;
     const int rows = p.M - m0;
+    if (o.y_pairs) {
+        if (o.y_type == QG_BF16)
+            store_pairs<__nv_bfloat162>(static_cast<__nv_bfloat16*>(p.seg[0].Y) + at, ldy, n, p.N, rows, y);
+        else
+            store_pairs<__half2>(static_cast<__half*>(p.seg[0].Y) + at, ldy, n, p.N, rows, y);
+        return;
+    }
+    if (n >= p.N) return;
     if (o.y_type == QG_FP32) {
         float* Y = static_cast<float*>(p.seg[0].Y) + at;
 #pragma unroll
@@ -145,10 +178,12 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 const Out o) {
     using L = I8Layout<NA, kPair>;
     constexpr int kWStages = L::kWStages, kSlots = L::kSlots, kD = L::kD;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t* gbase = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t gbase[];
+    const uint32_t base = smem_u32(gbase);
+    if (base & 1023u) {   // the swizzle needs the alignment asked for above
+        if (threadIdx.x == 0) atomicOr(p.status, kDevTimeout);
+        return;
+    }
 
     const uint32_t bar0 = base + L::kBarOff;
     auto wfull = [&](int s) { return bar0 + 8u * s; };
@@ -349,6 +384,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + L::kDCol0 + col0;
         const int first_tile = static_cast<int>(u0 / p.KB);
         const int split_info = gemm::split_info_lane(p, u0, u1, lane);
+        float* sxs = reinterpret_cast<float*>(gbase + L::kScaleOff) + ew * L::kScaleCols;
         // the scales, Y and the workspace may be in use by the preceding grid
         grid_dependency_wait();
         int ps = 0;
@@ -364,7 +400,28 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             const int m0 = (tile - tn * o.tm_count) * NA + col0;
             const float sw = n < p.N ? o.sw[n] : 0.0f;
             const float bias = o.bias != nullptr && n < p.N ? o.bias[n] : 0.0f;
-            auto scale_of = [&](int m) { return lane < 16 && m + lane < p.M ? o.sx[m + lane] : 0.0f; };
+            // the tile's activation scales, fetched while its MMAs run: lane l
+            // holds columns l, l + 32, ...; they reach the other lanes through
+            // the warp's own shared memory, kScaleCols at a time
+            constexpr int kHeld = (L::kEpiCols + 31) / 32;
+            float held[kHeld];
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h) {
+                const int c = 32 * h + lane;
+                held[h] = c < L::kEpiCols && m0 + c < p.M ? o.sx[m0 + c] : 0.0f;
+            }
+            auto scales_from = [&](int c) {   // of the 16 columns from 16 c (c in ascending order)
+                if ((16 * c) % L::kScaleCols == 0) {
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < kHeld; ++h) {
+                        const int at = 32 * h + lane - 16 * c;
+                        if (at >= 0 && at < L::kScaleCols) sxs[at] = held[h];
+                    }
+                    __syncwarp();
+                }
+                return sxs + (16 * c) % L::kScaleCols;
+            };
             if (!gemm::warp_wait(dfull(b), (pc / kD) & 1, wc)) break;
             tc_fence_after();
             const int which = tile == first_tile ? 0 : 1;
@@ -372,14 +429,13 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < L::kEpiCols / 16; ++c) {
                 uint32_t v[16];
-                const float sxl = scale_of(m0 + 16 * c);
                 tmem_ld_x16(tl + b * NA + 16 * c, v);
                 tmem_wait_ld();
                 float f[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
                 if (whole) {
-                    store16(p, o, n, m0 + 16 * c, sxl, sw, bias, f);
+                    store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, f);
                 } else {
 #pragma unroll
                     for (int g = 0; g < 4; ++g)
@@ -411,7 +467,6 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                     __threadfence();
 #pragma unroll 1
                     for (int c = 0; c < L::kEpiCols / 16; ++c) {
-                        const float sxl = scale_of(m0 + 16 * c);
                         float acc[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
@@ -429,7 +484,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                                 acc[4 * g + 3] = __fadd_rn(acc[4 * g + 3], x.w);
                             }
                         }
-                        store16(p, o, n, m0 + 16 * c, sxl, sw, bias, acc);
+                        store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, acc);
                     }
                     __syncwarp();
                     if (lane == 0) *cnt = 0u;   // ready for the next call
@@ -567,7 +622,9 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
     uint8_t* w = static_cast<uint8_t*>(a.ws);
     p.cnt = reinterpret_cast<uint32_t*>(w);
     p.part = reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(a.M, a.K));
-    const Out o{a.Sx, a.Sw, a.bias, a.y_type, (a.M + NA - 1) / NA};
+    const int y_pairs = a.y_type != QG_FP32 && a.N % 2 == 0 && a.ldy % 2 == 0 &&
+                        (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
+    const Out o{a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.M + NA - 1) / NA};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
     cfg.blockDim = dim3(L::kThreads);
