@@ -108,29 +108,8 @@ __device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& 
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
-// Two neighbouring weight rows' outputs as one 32-bit store: for activation
-// rows m and m + 1 the even lane of a pair writes (n, n + 1) of row m and the
-// odd lane (n - 1, n) of row m + 1, which halves the stores of a tile.
-template <class T2, class T>
-__device__ __forceinline__ void store_pairs(T* Y, int64_t ldy, int n, int N, int rows, const float (&y)[16]) {
-    const int odd = threadIdx.x & 1;
-    T* at = Y + odd * ldy - odd;
-#pragma unroll
-    for (int j = 0; j < 16; j += 2) {
-        const float other = __shfl_xor_sync(0xffffffffu, odd ? y[j] : y[j + 1], 1);
-        T2 v;
-        v.x = T(odd ? other : y[j]);
-        v.y = T(odd ? y[j + 1] : other);
-        if (n < N && j + odd < rows) *reinterpret_cast<T2*>(at + j * ldy) = v;
-    }
-}
-
-// 16 output columns (activation rows m0 ..) of weight row n; sx: their scales
-// in shared memory.
-__device__ __forceinline__ void store16(const Params& p, const Out& o, int n, int m0, const float* sx, float sw, float b,
-                                        const float (&v)[16]) {
-    const int64_t ldy = p.seg[0].ldy;
-    float y[16];
+// 16 accumulators of one weight row (activation rows in order), scaled.
+__device__ __forceinline__ void scale16(const float (&v)[16], const float* sx, float sw, float b, float (&y)[16]) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         const float4 s = reinterpret_cast<const float4*>(sx)[g];
@@ -139,16 +118,60 @@ __device__ __forceinline__ void store16(const Params& p, const Out& o, int n, in
         y[4 * g + 2] = __fmaf_rn(__fmul_rn(v[4 * g + 2], s.z), sw, b);
         y[4 * g + 3] = __fmaf_rn(__fmul_rn(v[4 * g + 3], s.w), sw, b);
     }
-    const int64_t at = static_cast<int64_t>(m0) * ldy + n;
-    const int rows = p.M - m0;
+}
+
+// The same as 16-bit values, two activation rows to a word.
+__device__ __forceinline__ void pack16(const float (&v)[16], const float* sx, float sw, float b, int y_type,
+                                       uint32_t* w) {
+    float y[16];
+    scale16(v, sx, sw, b, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (y_type == QG_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(y[2 * j], y[2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+}
+
+// Stores COLS packed columns (activation rows m0 ..) of weight row n, two
+// neighbouring weight rows to a 32-bit store: of activation rows m and m + 1
+// the even lane of a pair writes (n, n + 1) of row m and the odd lane (n - 1,
+// n) of row m + 1, which halves the stores of a tile.
+template <int COLS>
+__device__ __forceinline__ void store_packed(const Params& p, int n, int m0, const uint32_t* w) {
+    const int odd = threadIdx.x & 1;
+    const uint32_t sel = odd ? 0x3276u : 0x5410u;
+    const int64_t ldy = p.seg[0].ldy;
+    uint16_t* at = static_cast<uint16_t*>(p.seg[0].Y) + (static_cast<int64_t>(m0) + odd) * ldy + (n - odd);
+    const int rows = n < p.N ? p.M - m0 - odd : 0;   // of this lane's; N is even
+#pragma unroll
+    for (int j = 0; j < COLS / 2; ++j) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 1);
+        if (2 * j < rows) *reinterpret_cast<uint32_t*>(at) = prmt(w[j], other, sel);
+        at += 2 * ldy;
+    }
+}
+
+// 16 output columns (activation rows m0 ..) of weight row n; sx: their scales
+// in shared memory.
+__device__ __forceinline__ void store16(const Params& p, const Out& o, int n, int m0, const float* sx, float sw, float b,
+                                        const float (&v)[16]) {
     if (o.y_pairs) {
-        if (o.y_type == QG_BF16)
-            store_pairs<__nv_bfloat162>(static_cast<__nv_bfloat16*>(p.seg[0].Y) + at, ldy, n, p.N, rows, y);
-        else
-            store_pairs<__half2>(static_cast<__half*>(p.seg[0].Y) + at, ldy, n, p.N, rows, y);
+        uint32_t w[8];
+        pack16(v, sx, sw, b, o.y_type, w);
+        store_packed<16>(p, n, m0, w);
         return;
     }
+    float y[16];
+    scale16(v, sx, sw, b, y);
     if (n >= p.N) return;
+    const int64_t ldy = p.seg[0].ldy;
+    const int64_t at = static_cast<int64_t>(m0) * ldy + n;
+    const int rows = p.M - m0;
     if (o.y_type == QG_FP32) {
         float* Y = static_cast<float*>(p.seg[0].Y) + at;
 #pragma unroll
@@ -425,29 +448,50 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             if (!gemm::warp_wait(dfull(b), (pc / kD) & 1, wc)) break;
             tc_fence_after();
             const int which = tile == first_tile ? 0 : 1;
-            float4* mine = part_slot<NA>(p, cta, which) + (col0 / 4) * 128 + row;
-#pragma unroll 1
-            for (int c = 0; c < L::kEpiCols / 16; ++c) {
+            auto release = [&]() {   // the accumulator has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (kPair && !leader) mbar_arrive_cluster(map_to_cta(dempty(b), 0));
+                    else mbar_arrive(dempty(b));
+                }
+            };
+            auto load16 = [&](int c, float (&f)[16]) {
                 uint32_t v[16];
                 tmem_ld_x16(tl + b * NA + 16 * c, v);
                 tmem_wait_ld();
-                float f[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
-                if (whole) {
-                    store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, f);
-                } else {
+            };
+            if (whole && o.y_pairs) {
+                // all columns into registers, packed, so that the next tile's
+                // MMAs run under the stores (with one accumulator per pair the
+                // stores held them for 5 us of each tile's 38)
+                uint32_t w[L::kEpiCols / 2];
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        __stcg(mine + (4 * c + g) * 128,
-                               make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
+                for (int c = 0; c < L::kEpiCols / 16; ++c) {
+                    float f[16];
+                    load16(c, f);
+                    pack16(f, scales_from(c), sw, bias, o.y_type, w + 8 * c);
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (kPair && !leader) mbar_arrive_cluster(map_to_cta(dempty(b), 0));
-                else mbar_arrive(dempty(b));
+                release();
+                store_packed<L::kEpiCols>(p, n, m0, w);
+            } else {
+                float4* mine = part_slot<NA>(p, cta, which) + (col0 / 4) * 128 + row;
+#pragma unroll 1
+                for (int c = 0; c < L::kEpiCols / 16; ++c) {
+                    float f[16];
+                    load16(c, f);
+                    if (whole) {
+                        store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, f);
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g)
+                            __stcg(mine + (4 * c + g) * 128,
+                                   make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
+                    }
+                }
+                release();
             }
             if (!whole) {
                 // every lane's partial visible GPU-wide before lane 0's arrival.  A
