@@ -541,7 +541,9 @@ qg_status qg_tune_w8a8(const uint8_t *Xq, int64_t ldxq, const float *X_scale, in
  *                              and last CTA holding units of the tile and the
  *                              partial-sum slot (0 or 1) of the first one
  *   info[6g+3 .. 6g+5]         the same for its last tile
- * capacity: the number of CTAs the arrays hold.
+ * capacity: the number of CTAs the arrays hold.  QG_KIND_INT8, whose CTAs run
+ * whole tiles side by side before they share the rest, is refused
+ * (QG_ERR_INVALID_ARG).
  */
 qg_status qg_debug_schedule(int kind, int M, int N, int K, int *ctas, int64_t *ranges, int *info, int capacity,
                             struct CUstream_st *stream);

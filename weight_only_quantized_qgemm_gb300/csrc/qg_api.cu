@@ -164,22 +164,15 @@ int table_lookup(int kind, int M, int N, int K) {
 
 // The schedule of a shape on `sms` SMs, with `forced` > 0 a dispatch-table grid.
 Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
+    if (kind == QG_KIND_INT8) return int8_schedule(M, N, K, sms, forced);
     Schedule s;
-    s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : kind == QG_KIND_INT8 ? int8_tile_rows(M) : M <= 16 ? 16 : 32;
-    // W8A8 and INT8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
-    s.T = (N + 127) / 128 * (kind == QG_KIND_W8A8 || kind == QG_KIND_INT8 ? (M + s.nmma - 1) / s.nmma : 1);
-    // INT8 tiles on CTA pairs are 256 weight rows; the grid counts pairs below
-    const int ctas = kind == QG_KIND_INT8 ? int8_ctas(s.nmma) : 1;
-    if (ctas == 2) {
-        s.T = (N + 255) / 256 * ((M + s.nmma - 1) / s.nmma);
-        sms = sms > 1 ? sms / 2 : 1;
-        forced = forced > 0 ? (forced + 1) / 2 : 0;
-    }
+    s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : M <= 16 ? 16 : 32;
+    // W8A8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
+    s.T = (N + 127) / 128 * (kind == QG_KIND_W8A8 ? (M + s.nmma - 1) / s.nmma : 1);
     // one unit = 128 rows x one 128-wide K block (W8A8: two blocks)
     s.KU = kind == QG_KIND_W8A8 ? (K + 255) / 256 : (K + 127) / 128;
     s.U = static_cast<long long>(s.T) * s.KU;
-    const bool unit_bound =
-        kind == QG_KIND_W8A8 || (kind == QG_KIND_FP8_BLOCK && M > 16) || (kind == QG_KIND_INT8 && M > 64);
+    const bool unit_bound = kind == QG_KIND_W8A8 || (kind == QG_KIND_FP8_BLOCK && M > 16);
     long long g = sms;
     if (forced > 0) {
         g = forced;
@@ -258,7 +251,7 @@ const SchedEntry& cached_schedule(int kind, int M, int N, int K, int sms) {
     e.gen = gen;
     e.s = choose_schedule(kind, M, N, K, sms);
     e.ws = kind == QG_KIND_W8A8   ? w8a8_workspace_bytes(e.s, schedule_splits(e.s))
-           : kind == QG_KIND_INT8 ? int8_workspace_bytes(e.s, M, K, schedule_splits(e.s))
+           : kind == QG_KIND_INT8 ? int8_workspace_bytes(e.s, M, K, e.s.split)
                                   : workspace_bytes_uncached(e.s);
     return e;
 }
@@ -917,7 +910,7 @@ qg_status qg_dequant_lut3(const void* Wq, const void* qmap, const void* scales, 
 
 qg_status qg_debug_schedule(int kind, int M, int N, int K, int* ctas, int64_t* ranges, int* info, int capacity,
                             cudaStream_t stream) {
-    if (max_m(kind) == 0) return QG_ERR_INVALID_ARG;
+    if (max_m(kind) == 0 || kind == QG_KIND_INT8) return QG_ERR_INVALID_ARG;   // INT8: not a plain split of T * KU units
     if (M < 1 || M > max_m(kind) || N < 1 || K < 1 || !ctas) return QG_ERR_INVALID_ARG;
     if (K % k_multiple(kind) != 0) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();

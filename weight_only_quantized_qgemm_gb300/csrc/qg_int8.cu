@@ -30,9 +30,11 @@
 //   warps 4-      epilogue: one per TMEM lane quadrant (two for NA >= 128)
 //   the last 8    convert: two groups of four warps taking alternate units
 //
-// Units are split evenly over the CTAs in tile-major order; a tile shared by
-// several CTAs is summed, in ascending K order of its pieces, by the last to
-// arrive, as in the other kernels.
+// Each worker (a CTA, or beyond 128 rows a pair of them) first runs the same
+// number of whole tiles, the workers side by side so that the tiles in flight
+// share their operands in L2; the tiles that are left are cut over the workers
+// at any K block, and a tile shared by several is summed, in ascending K order
+// of its pieces, by the last to arrive, as in the other kernels.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -95,7 +97,59 @@ struct Out {
     const float* bias;
     int y_type;
     int y_pairs;    // a 16-bit Y that takes 32-bit stores of two neighbouring columns
-    int tm_count;   // activation row blocks; tile t = (weight tile t / tm_count, block t % tm_count)
+    int tn_count, tm_count;   // weight tiles, activation row blocks
+    int workers;              // CTAs or CTA pairs
+    int nfull;                // whole tiles each worker runs before its part of the tail
+};
+
+// Where tile t lies: bands of kBand activation row blocks, in a band weight
+// tile by weight tile.  The tiles in flight at a time then share a few weight
+// tiles and one band of activations, which L2 holds.
+constexpr int kBand = 16;
+__device__ __forceinline__ void place_of(const Out& o, int t, int& tn, int& tm) {
+    const int band = t / (o.tn_count * kBand);
+    const int r = t - band * o.tn_count * kBand;
+    int width = o.tm_count - band * kBand;
+    width = width > kBand ? kBand : width < 1 ? 1 : width;   // < 1: a place past the last tile, not used
+    tn = r / width;
+    tm = band * kBand + r - tn * width;
+}
+
+// A worker's units in order: whole tiles worker, worker + workers, ... (nfull
+// of them), then units [u0, u1) of the tail, the tiles from nfull * workers on,
+// which are cut over the tail's workers (Params U and G) at any K block.  kr is
+// the K block a unit covers: tiles start at different ones (see Cursor).
+struct Walk {
+    int tile, kb, kr, tn, tm;
+    int full;                 // whole tiles left, this one included; 0 in the tail
+    int tail_tile, tail_kb;
+    __device__ Walk(const Params& p, const Out& o, int worker, long long u0)
+        : full(o.nfull),
+          tail_tile(o.nfull * o.workers + static_cast<int>(u0 / p.KB)),
+          tail_kb(static_cast<int>(u0 % p.KB)) {
+        if (full > 0) enter(p, o, worker, 0);
+        else enter(p, o, tail_tile, tail_kb);
+    }
+    __device__ void enter(const Params& p, const Out& o, int t, int k) {
+        tile = t;
+        kb = k;
+        kr = k + Cursor::first_block(t, p.KB);
+        if (kr >= p.KB) kr -= p.KB;
+        place_of(o, t, tn, tm);
+    }
+    __device__ void step(const Params& p, const Out& o) {
+        if (++kr == p.KB) kr = 0;
+        if (++kb < p.KB) return;
+        if (full > 1) {
+            --full;
+            enter(p, o, tile + o.workers, 0);
+        } else if (full == 1) {
+            full = 0;
+            enter(p, o, tail_tile, tail_kb);
+        } else {
+            enter(p, o, tile + 1, 0);
+        }
+    }
 };
 
 // Four signed bytes of w -> two FP16x2 words, exactly: u = byte + 128 under
@@ -226,19 +280,19 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     const int worker = cta / L::kCtas;
     const uint32_t rank = kPair ? cluster_cta_rank() : 0u;
     const bool leader = rank == 0;
-    const long long u0 = gemm::unit_begin(worker, p.U, p.G);
-    const long long u1 = gemm::unit_begin(worker + 1, p.U, p.G);
-    const int nunits = static_cast<int>(u1 - u0);
+    const long long u0 = worker < p.G ? gemm::unit_begin(worker, p.U, p.G) : p.U;
+    const long long u1 = worker < p.G ? gemm::unit_begin(worker + 1, p.U, p.G) : p.U;
+    const int nunits = o.nfull * p.KB + static_cast<int>(u1 - u0);
 
     // a weight tile serves tm_count tiles in a row: keep it for their re-reads
-    auto load_w = [&](int s, const Cursor& cur) {
+    auto load_w = [&](int s, const Walk& cur) {
         mbar_arrive_expect_tx(wfull(s), L::kWBytes);
         tma_load_2d(base + s * L::kWBytes, &tmW, wfull(s), cur.kr * 128,
-                    (cur.tile / o.tm_count * L::kCtas + static_cast<int>(rank)) * 128,
+                    (cur.tn * L::kCtas + static_cast<int>(rank)) * 128,
                     o.tm_count > 1 ? policy_evict_last() : policy_evict_first());
     };
     auto skipped = [&](int i) { return cta == 0 && i == p.fault_unit; };   // failure-path test hook
-    Cursor wcur(u0, p.KB);   // the weight producer's place
+    Walk wcur(p, o, worker, u0);   // the weight producer's place
     int wissued = 0;
     if (threadIdx.x == 0) {
         prefetch_tmap(&tmW);
@@ -260,7 +314,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         fence_barrier_init();
         // the first turn of the weight ring, before the CTA has met: it needs
         // nothing but the barriers just set up
-        for (; wissued < kWStages && wissued < nunits; ++wissued, wcur.step(p.KB))
+        for (; wissued < kWStages && wissued < nunits; ++wissued, wcur.step(p, o))
             if (!skipped(wissued)) load_w(wissued, wcur);
     }
     __syncwarp();
@@ -279,7 +333,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     if (warp == kWarpWProd) {
         if (lane == 0) {
             Ring<kWStages> rw(wissued);
-            for (; wissued < nunits; ++wissued, wcur.step(p.KB), rw.step(1)) {
+            for (; wissued < nunits; ++wissued, wcur.step(p, o), rw.step(1)) {
                 if (!wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
                 if (!skipped(wissued)) load_w(rw.slot, wcur);
             }
@@ -292,12 +346,12 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             grid_dependency_wait();   // the expansion kernel's output
             const uint64_t pol = policy_evict_last();
             int issued = 0;
-            Cursor cur(u0, p.KB);
+            Walk cur(p, o, worker, u0);
             Ring<kSlots> ro(0);
-            for (int i = 0; i < nunits; ++i, cur.step(p.KB), ro.step(1)) {
+            for (int i = 0; i < nunits; ++i, cur.step(p, o), ro.step(1)) {
                 if (i >= kSlots && !wait_bounded(ofree(ro.slot), ro.phase ^ 1u, wc)) break;
                 const uint32_t dst = base + L::kXOff + ro.slot * L::kXSlot;
-                const int m0 = cur.tile % o.tm_count * NA + static_cast<int>(rank) * L::kXRows;
+                const int m0 = cur.tm * NA + static_cast<int>(rank) * L::kXRows;
                 if (leader) mbar_arrive_expect_tx(ofull(ro.slot), L::kXSlot * L::kCtas);
                 if constexpr (kPair) {
                     const uint32_t bar = map_to_cta(ofull(ro.slot), 0);
@@ -326,7 +380,8 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             if constexpr (kPair) tc_commit_pair(bar);
             else tc_commit(bar);
         };
-        Cursor cur(u0, p.KB);
+        // the K block within a tile: whole tiles, then the tail from its first
+        int kb = o.nfull > 0 ? 0 : static_cast<int>(u0 % p.KB);
         Ring<kSlots> ro(0);
         int piece = 0;
         int last_a = -1;
@@ -340,7 +395,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             const uint32_t dt = tmem + L::kDCol0 + b * NA;
             const uint32_t at = tmem + ro.slot * 64;
             const uint64_t xd = dx0 + static_cast<uint64_t>((ro.slot * L::kXSlot) >> 4);
-            const bool closes = i == nunits - 1 || cur.kb == p.KB - 1;
+            const bool closes = i == nunits - 1 || kb == p.KB - 1;
             if (elected) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -356,7 +411,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             last_ph = ro.phase;
             fresh = closes;
             if (closes) ++piece;
-            cur.step(p.KB);
+            if (++kb == p.KB) kb = i + 1 == o.nfull * p.KB ? static_cast<int>(u0 % p.KB) : 0;
         }
         if (last_a >= 0 && elected) gemm::drain_wait(ofree(last_a), last_ph, p.timeout_ns);
     } else if (warp >= L::kWarpConv0) {
@@ -405,22 +460,24 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         const int col0 = (ew >> 2) * L::kEpiCols;
         const int row = q * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + L::kDCol0 + col0;
-        const int first_tile = static_cast<int>(u0 / p.KB);
-        const int split_info = gemm::split_info_lane(p, u0, u1, lane);
+        const int tail_tile = o.nfull * o.workers + static_cast<int>(u0 / p.KB);
+        const int split_info = u1 > u0 ? gemm::split_info_lane(p, u0, u1, lane) : 0;
         float* sxs = reinterpret_cast<float*>(gbase + L::kScaleOff) + ew * L::kScaleCols;
         // the scales, Y and the workspace may be in use by the preceding grid
         grid_dependency_wait();
         int ps = 0;
-        int kb0 = static_cast<int>(u0 % p.KB);
         for (int pc = 0; ps < nunits; ++pc) {
-            const int tile = first_tile + pc;
+            const bool full = pc < o.nfull;
+            const int kb0 = pc == o.nfull ? static_cast<int>(u0 % p.KB) : 0;
+            const int tile = full ? worker + pc * o.workers : tail_tile + pc - o.nfull;
             const int b = pc % kD;
             int pe = ps + (p.KB - kb0) - 1;
             if (pe > nunits - 1) pe = nunits - 1;
             const bool whole = kb0 == 0 && pe - ps == p.KB - 1;
-            const int tn = tile / o.tm_count;
+            int tn, tm;
+            place_of(o, tile, tn, tm);
             const int n = (tn * L::kCtas + static_cast<int>(rank)) * 128 + row;
-            const int m0 = (tile - tn * o.tm_count) * NA + col0;
+            const int m0 = tm * NA + col0;
             const float sw = n < p.N ? o.sw[n] : 0.0f;
             const float bias = o.bias != nullptr && n < p.N ? o.bias[n] : 0.0f;
             // the tile's activation scales, fetched while its MMAs run: lane l
@@ -447,7 +504,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             };
             if (!gemm::warp_wait(dfull(b), (pc / kD) & 1, wc)) break;
             tc_fence_after();
-            const int which = tile == first_tile ? 0 : 1;
+            const int which = pc == o.nfull ? 0 : 1;   // of the tail's first and last tile
             auto release = [&]() {   // the accumulator has been read
                 tc_fence_before();
                 __syncwarp();
@@ -514,19 +571,29 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                         float acc[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-#pragma unroll 4
-                        for (int c2 = cf; c2 <= cl; ++c2) {
-                            const float4* src =
-                                part_slot<NA>(p, c2 * L::kCtas + static_cast<int>(rank), c2 == cf ? w_first : 0) +
-                                (col0 / 4 + 4 * c) * 128 + row;
+                        // four pieces' loads in flight at a time
+#pragma unroll 1
+                        for (int c4 = cf; c4 <= cl; c4 += 4) {
+                            float4 x[4][4];
 #pragma unroll
-                            for (int g = 0; g < 4; ++g) {
-                                const float4 x = __ldcg(src + g * 128);
-                                acc[4 * g + 0] = __fadd_rn(acc[4 * g + 0], x.x);
-                                acc[4 * g + 1] = __fadd_rn(acc[4 * g + 1], x.y);
-                                acc[4 * g + 2] = __fadd_rn(acc[4 * g + 2], x.z);
-                                acc[4 * g + 3] = __fadd_rn(acc[4 * g + 3], x.w);
+                            for (int e = 0; e < 4; ++e) {
+                                const int c2 = c4 + e;
+                                const float4* src =
+                                    part_slot<NA>(p, c2 * L::kCtas + static_cast<int>(rank), c2 == cf ? w_first : 0) +
+                                    (col0 / 4 + 4 * c) * 128 + row;
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    x[e][g] = c2 <= cl ? __ldcg(src + g * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                             }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) {
+                                    acc[4 * g + 0] = __fadd_rn(acc[4 * g + 0], x[e][g].x);
+                                    acc[4 * g + 1] = __fadd_rn(acc[4 * g + 1], x[e][g].y);
+                                    acc[4 * g + 2] = __fadd_rn(acc[4 * g + 2], x[e][g].z);
+                                    acc[4 * g + 3] = __fadd_rn(acc[4 * g + 3], x[e][g].w);
+                                }
                         }
                         store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, acc);
                     }
@@ -535,7 +602,6 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 }
             }
             ps = pe + 1;
-            kb0 = 0;
         }
     }
 
@@ -663,12 +729,14 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
         cudaFuncSetAttribute(int8_kernel<NA, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     Params p = gemm::base_params(s, a.Y, a.ldy, a.M, a.N, a.K, nullptr, c);
+    p.U = static_cast<long long>(s.T - s.nfull * s.G) * s.KU;   // the tail
+    p.G = s.tail_g;
     uint8_t* w = static_cast<uint8_t*>(a.ws);
     p.cnt = reinterpret_cast<uint32_t*>(w);
     p.part = reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(a.M, a.K));
     const int y_pairs = a.y_type != QG_FP32 && a.N % 2 == 0 && a.ldy % 2 == 0 &&
                         (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
-    const Out o{a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.M + NA - 1) / NA};
+    const Out o{a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
     cfg.blockDim = dim3(L::kThreads);
@@ -691,6 +759,58 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
 }  // namespace
 
 int int8_tile_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
+
+// The cost of a grid is the units (a tile x 128 of K) of its busiest worker.
+// The whole tiles cost floor(T / workers) tiles; for the tail of r tiles the
+// rule takes the cheapest of
+//   - one worker a tile: KU units
+//   - k = floor(workers / r) equal pieces of every tile: ceil(KU / k), plus
+//     kSplitUnits for storing, counting and summing partial results
+//   - all workers, pieces that straddle tiles: ceil(r KU / workers), plus
+//     kSplitUnits + kStraddleUnits
+constexpr long long kSplitUnits = 10, kStraddleUnits = 5;
+constexpr int kMostPieces = 8;
+
+Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
+    Schedule s;
+    s.nmma = int8_tile_rows(M);
+    const int ctas = int8_ctas(s.nmma);
+    const long long tn = (N + 128ll * ctas - 1) / (128 * ctas);
+    s.T = static_cast<int>(tn * ((M + s.nmma - 1) / s.nmma));
+    s.KU = (K + 127) / 128;
+    s.U = static_cast<long long>(s.T) * s.KU;
+    long long w = forced > 0 ? (forced + ctas - 1) / ctas : sms / ctas;
+    if (w < 1) w = 1;
+    s.max_ctas = static_cast<int>(w * ctas);
+    if (w > s.U) w = s.U;
+    s.nfull = static_cast<int>(s.T / w);
+    const long long r = s.T - s.nfull * w;
+    long long g = 0;
+    if (r > 0) {
+        const long long all = w < r * s.KU ? w : r * s.KU;
+        if (forced > 0) {
+            g = all;
+        } else {
+            auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+            long long best = s.KU;
+            g = r;
+            long long k = w / r;
+            if (k > kMostPieces) k = kMostPieces;
+            if (k > s.KU) k = s.KU;
+            if (k > 1 && up(s.KU, k) + kSplitUnits < best) {
+                best = up(s.KU, k) + kSplitUnits;
+                g = k * r;
+            }
+            if (up(r * s.KU, all) + kSplitUnits + kStraddleUnits < best) g = all;
+        }
+    }
+    s.tail_g = static_cast<int>(g);
+    s.G = static_cast<int>(s.nfull > 0 ? w : g);
+    // splits: some worker's part of the tail begins inside a tile
+    s.split = false;
+    for (long long c = 1; c < g && !s.split; ++c) s.split = c * (r * s.KU) / g % s.KU != 0;
+    return s;
+}
 
 size_t int8_expanded_bytes(int M, int K) {
     return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255);

@@ -24,6 +24,10 @@ struct Int8Args {
 int int8_tile_rows(int M);
 inline int int8_ctas(int tile_rows) { return tile_rows > 128 ? 2 : 1; }
 
+// The schedule of a shape on `sms` SMs (forced > 0: with that many CTAs, the
+// tail cut evenly over all of them).
+Schedule int8_schedule(int M, int N, int K, int sms, int forced);
+
 // Workspace of a schedule (s.nmma = the tile's activation rows): the arrival
 // counters (kInt8CounterBytes, zero between calls, at offset 0 for every
 // shape), the activations as FP16 [M, K], then the split-K partial sums of a

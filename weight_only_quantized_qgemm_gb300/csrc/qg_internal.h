@@ -23,6 +23,11 @@ struct Schedule {
     int G = 0;        // CTAs
     int nmma = 16;    // MMA N (16 or 32)
     int max_ctas = 0; // CTAs the device holds at once (one per SM): bounds G
+    // INT8 schedules only (qg_int8.cu): G workers run nfull whole tiles each,
+    // then tail_g of them share the units of the other T - nfull G tiles
+    int nfull = 0;
+    int tail_g = 0;
+    bool split = false;   // the tail cuts a tile
 };
 
 // Workspace layout for a schedule that splits tiles: split-K partial sums
