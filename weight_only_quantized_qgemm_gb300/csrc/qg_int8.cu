@@ -100,6 +100,9 @@ struct Out {
     int tn_count, tm_count;   // weight tiles, activation row blocks
     int workers;              // CTAs or CTA pairs
     int nfull;                // whole tiles each worker runs before its part of the tail
+    int tail_q, tail_r;       // the tail's units = tail_q G + tail_r
+    // where worker c's part of the tail begins: floor(c U / G), in 32 bits
+    __device__ int tail_begin(const Params& p, int c) const { return c * tail_q + c * tail_r / p.G; }
 };
 
 // Where tile t lies: bands of kBand activation row blocks, in a band weight
@@ -123,10 +126,8 @@ struct Walk {
     int tile, kb, kr, tn, tm;
     int full;                 // whole tiles left, this one included; 0 in the tail
     int tail_tile, tail_kb;
-    __device__ Walk(const Params& p, const Out& o, int worker, long long u0)
-        : full(o.nfull),
-          tail_tile(o.nfull * o.workers + static_cast<int>(u0 / p.KB)),
-          tail_kb(static_cast<int>(u0 % p.KB)) {
+    __device__ Walk(const Params& p, const Out& o, int worker, int u0)
+        : full(o.nfull), tail_tile(o.nfull * o.workers + u0 / p.KB), tail_kb(u0 % p.KB) {
         if (full > 0) enter(p, o, worker, 0);
         else enter(p, o, tail_tile, tail_kb);
     }
@@ -280,69 +281,81 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     const int worker = cta / L::kCtas;
     const uint32_t rank = kPair ? cluster_cta_rank() : 0u;
     const bool leader = rank == 0;
-    const long long u0 = worker < p.G ? gemm::unit_begin(worker, p.U, p.G) : p.U;
-    const long long u1 = worker < p.G ? gemm::unit_begin(worker + 1, p.U, p.G) : p.U;
-    const int nunits = o.nfull * p.KB + static_cast<int>(u1 - u0);
-
-    // a weight tile serves tm_count tiles in a row: keep it for their re-reads
-    auto load_w = [&](int s, const Walk& cur) {
-        mbar_arrive_expect_tx(wfull(s), L::kWBytes);
-        tma_load_2d(base + s * L::kWBytes, &tmW, wfull(s), cur.kr * 128,
-                    (cur.tn * L::kCtas + static_cast<int>(rank)) * 128,
-                    o.tm_count > 1 ? policy_evict_last() : policy_evict_first());
-    };
-    auto skipped = [&](int i) { return cta == 0 && i == p.fault_unit; };   // failure-path test hook
-    Walk wcur(p, o, worker, u0);   // the weight producer's place
-    int wissued = 0;
-    if (threadIdx.x == 0) {
-        prefetch_tmap(&tmW);
-        for (int s = 0; s < kWStages; ++s) {
-            mbar_init(wfull(s), 1);
-            mbar_init(wempty(s), 4);   // the four warps of the convert group
-        }
-        for (int a = 0; a < kSlots; ++a) {
-            // each CTA's four convert warps, and the activations' copies (the
-            // leader's barrier counts for the pair)
-            mbar_init(ofull(a), 4 * L::kCtas + 1);
-            mbar_init(ofree(a), 1);    // commit
-        }
-        for (int b = 0; b < kD; ++b) {
-            mbar_init(dfull(b), 1);    // commit: the piece's MMAs are complete
-            mbar_init(dempty(b), L::kEpi * L::kCtas);
-        }
-        *abort_flag = 0;
-        fence_barrier_init();
-        // the first turn of the weight ring, before the CTA has met: it needs
-        // nothing but the barriers just set up
-        for (; wissued < kWStages && wissued < nunits; ++wissued, wcur.step(p, o))
-            if (!skipped(wissued)) load_w(wissued, wcur);
-    }
-    __syncwarp();
-    if (warp == kWarpMma) {
-        if constexpr (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 512);
-        else tmem_alloc(smem_u32(tmem_slot), 512);
-    }
-    tc_fence_before();
-    if constexpr (kPair) cluster_sync_all();   // the peer's barriers are set up too
-    else __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const int u0 = worker < p.G ? o.tail_begin(p, worker) : 0;
+    const int u1 = worker < p.G ? o.tail_begin(p, worker + 1) : 0;
+    const int nunits = o.nfull * p.KB + u1 - u0;
     const WaitCtl wc{p.timeout_ns, p.status, abort_flag};
-    grid_dependents_launch();
 
     if (warp == kWarpWProd) {
+        // Sets the barriers up, announces them and starts the weight stream at
+        // once: it needs nothing else of the CTA's set-up (with the first turn
+        // of the ring ahead of the CTA's meeting the other warps met 2.7 us
+        // after the launch, now 1 us).
         if (lane == 0) {
-            Ring<kWStages> rw(wissued);
-            for (; wissued < nunits; ++wissued, wcur.step(p, o), rw.step(1)) {
-                if (!wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
-                if (!skipped(wissued)) load_w(rw.slot, wcur);
+            prefetch_tmap(&tmW);
+            for (int s = 0; s < kWStages; ++s) {
+                mbar_init(wfull(s), 1);
+                mbar_init(wempty(s), 4);   // the four warps of the convert group
             }
-            for (int i = wissued - kWStages < 0 ? 0 : wissued - kWStages; i < wissued; ++i)
+            for (int a = 0; a < kSlots; ++a) {
+                // each CTA's four convert warps, and the activations' copies (the
+                // leader's barrier counts for the pair)
+                mbar_init(ofull(a), 4 * L::kCtas + 1);
+                mbar_init(ofree(a), 1);    // commit
+            }
+            for (int b = 0; b < kD; ++b) {
+                mbar_init(dfull(b), 1);    // commit: the piece's MMAs are complete
+                mbar_init(dempty(b), L::kEpi * L::kCtas);
+            }
+            *abort_flag = 0;
+            fence_barrier_init();
+        }
+        __syncwarp();
+        if constexpr (kPair) cluster_arrive_all();
+        else named_bar_arrive(1, L::kThreads);
+        grid_dependents_launch();
+        // a weight tile serves tm_count tiles: keep it for their re-reads
+        const uint64_t pol = o.tm_count > 1 ? policy_evict_last() : policy_evict_first();
+        auto skipped = [&](int i) { return cta == 0 && i == p.fault_unit; };   // failure-path test hook
+        Walk cur(p, o, worker, u0);
+        Ring<kWStages> rw(0);
+        int issued = 0;
+        auto load_w = [&]() {
+            if (skipped(issued)) return;
+            mbar_arrive_expect_tx(wfull(rw.slot), L::kWBytes);
+            tma_load_2d(base + rw.slot * L::kWBytes, &tmW, wfull(rw.slot), cur.kr * 128,
+                        (cur.tn * L::kCtas + static_cast<int>(rank)) * 128, pol);
+        };
+        if (lane == 0)
+            for (; issued < nunits && issued < kWStages; ++issued, cur.step(p, o), rw.step(1)) load_w();
+        __syncwarp();
+        if constexpr (kPair) cluster_wait_all();   // of the arrival above
+        if (lane == 0) {
+            for (; issued < nunits; ++issued, cur.step(p, o), rw.step(1)) {
+                if (!wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
+                load_w();
+            }
+            for (int i = issued - kWStages < 0 ? 0 : issued - kWStages; i < issued; ++i)
                 if (!skipped(i)) gemm::drain_wait(wfull(i % kWStages), (i / kWStages) & 1, p.timeout_ns);
         }
+    } else {
+        if (warp == kWarpMma) {
+            if constexpr (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 512);
+            else tmem_alloc(smem_u32(tmem_slot), 512);
+        }
+        if (warp == kWarpXProd && lane == 0) prefetch_tmap(&tmX);
+        tc_fence_before();
+        __syncwarp();
+        if constexpr (kPair) cluster_sync_all();   // the peer's barriers are set up too
+        else named_bar_sync(1, L::kThreads);
+        tc_fence_after();
+    }
+    const uint32_t tmem = *tmem_slot;   // not of the weight producer's business, which has not met the others
+
+    if (warp == kWarpWProd) {
+        // done above
     } else if (warp == kWarpXProd) {
         if (lane == 0) {
-            prefetch_tmap(&tmX);
             grid_dependency_wait();   // the expansion kernel's output
             const uint64_t pol = policy_evict_last();
             int issued = 0;
@@ -381,7 +394,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             else tc_commit(bar);
         };
         // the K block within a tile: whole tiles, then the tail from its first
-        int kb = o.nfull > 0 ? 0 : static_cast<int>(u0 % p.KB);
+        int kb = o.nfull > 0 ? 0 : u0 % p.KB;
         Ring<kSlots> ro(0);
         int piece = 0;
         int last_a = -1;
@@ -411,7 +424,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             last_ph = ro.phase;
             fresh = closes;
             if (closes) ++piece;
-            if (++kb == p.KB) kb = i + 1 == o.nfull * p.KB ? static_cast<int>(u0 % p.KB) : 0;
+            if (++kb == p.KB) kb = i + 1 == o.nfull * p.KB ? u0 % p.KB : 0;
         }
         if (last_a >= 0 && elected) gemm::drain_wait(ofree(last_a), last_ph, p.timeout_ns);
     } else if (warp >= L::kWarpConv0) {
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         const int col0 = (ew >> 2) * L::kEpiCols;
         const int row = q * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + L::kDCol0 + col0;
-        const int tail_tile = o.nfull * o.workers + static_cast<int>(u0 / p.KB);
+        const int tail_tile = o.nfull * o.workers + u0 / p.KB;
         const int split_info = u1 > u0 ? gemm::split_info_lane(p, u0, u1, lane) : 0;
         float* sxs = reinterpret_cast<float*>(gbase + L::kScaleOff) + ew * L::kScaleCols;
         // the scales, Y and the workspace may be in use by the preceding grid
@@ -468,7 +481,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         int ps = 0;
         for (int pc = 0; ps < nunits; ++pc) {
             const bool full = pc < o.nfull;
-            const int kb0 = pc == o.nfull ? static_cast<int>(u0 % p.KB) : 0;
+            const int kb0 = pc == o.nfull ? u0 % p.KB : 0;
             const int tile = full ? worker + pc * o.workers : tail_tile + pc - o.nfull;
             const int b = pc % kD;
             int pe = ps + (p.KB - kb0) - 1;
@@ -736,7 +749,8 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
     p.part = reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(a.M, a.K));
     const int y_pairs = a.y_type != QG_FP32 && a.N % 2 == 0 && a.ldy % 2 == 0 &&
                         (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
-    const Out o{a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull};
+    const Out o{a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull,
+                p.G > 0 ? static_cast<int>(p.U / p.G) : 0, p.G > 0 ? static_cast<int>(p.U % p.G) : 0};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
     cfg.blockDim = dim3(L::kThreads);

@@ -162,24 +162,13 @@ __device__ __forceinline__ uint64_t entry_of(float x, uint32_t index) {
 }
 __device__ __forceinline__ uint32_t entry_index(uint64_t e) { return 0xFFFFFFFFu - static_cast<uint32_t>(e); }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ uint32_t cluster_size() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // A word of CTA `rank`'s shared memory at the address `p` has in this CTA's.
-__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
+__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) { return map_to_cta(smem_u32(p), rank); }
 __device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
     float r;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(peer_address(p, rank)) : "memory");
@@ -386,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     grid_dependency_wait();
     const int tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5;
-    const uint32_t S = cluster_size(), rank = cluster_rank();
+    const uint32_t S = cluster_size(), rank = cluster_cta_rank();
     const int64_t m = blockIdx.x / S;
     const uint8_t* row = static_cast<const uint8_t*>(a.logits) + m * a.ld * F::kSize;
 
@@ -548,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             sh.bad = bad ? 1.0f : 0.0f;
         }
         __syncthreads();
-        cluster_arrive();
-        cluster_wait();
+        cluster_arrive_all();
+        cluster_wait_all();
         if (rank == 0) {
             // every warp adds the parts up for itself, lane l holding part l
             const bool has = lane < static_cast<int>(S);
@@ -581,9 +570,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             if (tid == 0) sh.ncand = 0;
         }
         __syncthreads();
-        cluster_arrive();   // nobody's shared memory is read any more
+        cluster_arrive_all();   // nobody's shared memory is read any more
         if (rank != 0) {
-            cluster_wait();
+            cluster_wait_all();
             return;
         }
         if (a.top_k > 0) {
@@ -605,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             }
             __syncthreads();
         }
-        cluster_wait();
+        cluster_wait_all();
     }
 
     // not (a <= b) is also true of a NaN
