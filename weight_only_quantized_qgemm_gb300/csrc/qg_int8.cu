@@ -772,22 +772,30 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
 
 }  // namespace
 
-int int8_tile_rows(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256; }
-
-// The cost of a grid is the units (a tile x 128 of K) of its busiest worker.
-// The whole tiles cost floor(T / workers) tiles; for the tail of r tiles the
-// rule takes the cheapest of
+// The cost of a schedule is the time of its busiest worker, in nanoseconds of
+// units (a tile x 128 of K) and of what a split adds.  The whole tiles cost
+// floor(T / workers) tiles; for the tail of r tiles the rule takes the cheapest
+// of
 //   - one worker a tile: KU units
-//   - k = floor(workers / r) equal pieces of every tile: ceil(KU / k), plus
-//     kSplitUnits for storing, counting and summing partial results
-//   - all workers, pieces that straddle tiles: ceil(r KU / workers), plus
-//     kSplitUnits + kStraddleUnits
-constexpr long long kSplitUnits = 10, kStraddleUnits = 5;
+//   - k = floor(workers / r) equal pieces of every tile: ceil(KU / k) units and
+//     a split (storing, counting and summing partial results)
+//   - all workers, pieces that straddle tiles: ceil(r KU / workers) units, a
+//     split, and half of one more (a worker may end two pieces)
+// A tile has the fewest activation rows that take the batch, up to 64; beyond,
+// 128 or 256, whichever costs less: wide tiles read fewer weights and
+// activations per product (660 ns a unit of twice the work against 380), but
+// a split's partial results are twice as many, summed by half as many CTAs (14
+// us against 6 on 256 x 5120 x 17408).
 constexpr int kMostPieces = 8;
+struct TileCost {
+    int rows;
+    long long unit_ns, split_ns;
+};
+constexpr TileCost kNarrow{0, 370, 3700}, kTile128{128, 380, 6000}, kTile256{256, 660, 14000};
 
-Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
+Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int forced, long long* cost) {
     Schedule s;
-    s.nmma = int8_tile_rows(M);
+    s.nmma = tc.rows;
     const int ctas = int8_ctas(s.nmma);
     const long long tn = (N + 128ll * ctas - 1) / (128 * ctas);
     s.T = static_cast<int>(tn * ((M + s.nmma - 1) / s.nmma));
@@ -800,23 +808,25 @@ Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
     s.nfull = static_cast<int>(s.T / w);
     const long long r = s.T - s.nfull * w;
     long long g = 0;
+    *cost = s.nfull * s.KU * tc.unit_ns;
     if (r > 0) {
+        auto up = [](long long a, long long b) { return (a + b - 1) / b; };
         const long long all = w < r * s.KU ? w : r * s.KU;
-        if (forced > 0) {
-            g = all;
-        } else {
-            auto up = [](long long a, long long b) { return (a + b - 1) / b; };
-            long long best = s.KU;
-            g = r;
-            long long k = w / r;
-            if (k > kMostPieces) k = kMostPieces;
-            if (k > s.KU) k = s.KU;
-            if (k > 1 && up(s.KU, k) + kSplitUnits < best) {
-                best = up(s.KU, k) + kSplitUnits;
-                g = k * r;
-            }
-            if (up(r * s.KU, all) + kSplitUnits + kStraddleUnits < best) g = all;
+        const long long straddle = up(r * s.KU, all) * tc.unit_ns + tc.split_ns + tc.split_ns / 2;
+        long long best = s.KU * tc.unit_ns;
+        g = r;
+        long long k = w / r;
+        if (k > kMostPieces) k = kMostPieces;
+        if (k > s.KU) k = s.KU;
+        if (k > 1 && up(s.KU, k) * tc.unit_ns + tc.split_ns < best) {
+            best = up(s.KU, k) * tc.unit_ns + tc.split_ns;
+            g = k * r;
         }
+        if (straddle < best || forced > 0) {
+            best = straddle;
+            g = all;
+        }
+        *cost += best;
     }
     s.tail_g = static_cast<int>(g);
     s.G = static_cast<int>(s.nfull > 0 ? w : g);
@@ -824,6 +834,19 @@ Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
     s.split = false;
     for (long long c = 1; c < g && !s.split; ++c) s.split = c * (r * s.KU) / g % s.KU != 0;
     return s;
+}
+
+Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
+    long long cost = 0, cost256 = 0;
+    if (M <= 64) {
+        TileCost t = kNarrow;
+        t.rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+        return schedule_with(t, M, N, K, sms, forced, &cost);
+    }
+    const Schedule s = schedule_with(kTile128, M, N, K, sms, forced, &cost);
+    if (M <= 128) return s;
+    const Schedule wide = schedule_with(kTile256, M, N, K, sms, forced, &cost256);
+    return cost256 < cost ? wide : s;
 }
 
 size_t int8_expanded_bytes(int M, int K) {
@@ -859,7 +882,7 @@ cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap&
         case 16: return launch_int8_na<16, false>(a, s, tmW, tmX, c, st);
         case 32: return launch_int8_na<32, false>(a, s, tmW, tmX, c, st);
         case 64: return launch_int8_na<64, false>(a, s, tmW, tmX, c, st);
-        case 128: return launch_int8_na<128, false>(a, s, tmW, tmX, c, st);
+        case 128: return launch_int8_na<128, true>(a, s, tmW, tmX, c, st);
         case 256: return launch_int8_na<256, true>(a, s, tmW, tmX, c, st);
     }
     return cudaErrorInvalidValue;

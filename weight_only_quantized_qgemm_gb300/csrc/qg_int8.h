@@ -18,11 +18,10 @@ struct Int8Args {
     void* ws;
 };
 
-// Activation rows per tile (the MMA's N side) for a batch size, and the CTAs
-// that work on a tile together (2: a CTA pair with a tile of 256 weight rows;
-// a schedule's G then counts pairs).
-int int8_tile_rows(int M);
-inline int int8_ctas(int tile_rows) { return tile_rows > 128 ? 2 : 1; }
+// The CTAs that work on a tile together, for a schedule's activation rows per
+// tile (nmma, the MMA's N side): 2 is a CTA pair with a tile of 256 weight
+// rows, and the schedule's G then counts pairs.
+inline int int8_ctas(int tile_rows) { return tile_rows > 64 ? 2 : 1; }
 
 // The schedule of a shape on `sms` SMs (forced > 0: with that many CTAs, the
 // tail cut evenly over all of them).
