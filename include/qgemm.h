@@ -86,7 +86,7 @@ enum { QG_BF16 = 0, QG_FP16 = 1, QG_FP32 = 2 };
  * without clearing.  The W8A8 kind lays its workspace out differently (wider
  * partial sums): a workspace serves either QG_KIND_W8A8 calls or calls of
  * the other kinds, not both, unless it is zero-filled again in between.
- * QG_KIND_INT8 has a layout of its own too: 16384 bytes of arrival counters
+ * QG_KIND_INT8 has a layout of its own too: 32768 bytes of arrival counters
  * (at the front for every shape), the activations expanded to FP16 (2 M K
  * bytes rounded up to 256), then the partial sums of a schedule that splits
  * tiles (two slots of 512 R bytes for each CTA, R = the rows of a tile: 16,

@@ -116,7 +116,7 @@ def test_every_split_gives_the_same_integers(M, N, K, ctas):
     try:
         ws = q.Workspace()
         y = _call(q, Xq, sx, W, sw, b, torch.float32, ws=ws)
-        assert int(ws.buf[:16384].count_nonzero()) == 0
+        assert int(ws.buf[:32768].count_nonzero()) == 0
         again = _call(q, Xq, sx, W, sw, b, torch.float32, ws=ws)
     finally:
         q.dispatch_clear()

@@ -59,6 +59,9 @@ struct I8Layout {
     static constexpr int kEpiCols = NA / (kEpi / 4);            // columns per epilogue warp
     static constexpr int kWarpConv0 = kWarpEpi0 + kEpi;
     static constexpr int kThreads = 32 * (kWarpConv0 + 4 * kGroups);
+    // slices of an epilogue warp's columns that the CTAs of a split tile sum
+    static constexpr int kSlices = kPair ? kInt8Slices : 1;
+    static constexpr int kSliceCols = kEpiCols / kSlices;
     // per epilogue warp, the activation scales of the columns at hand
     static constexpr int kScaleCols = kEpiCols < 64 ? kEpiCols : 64;
     static constexpr int kWBytes = 128 * 128;
@@ -503,17 +506,20 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 const int c = 32 * h + lane;
                 held[h] = c < L::kEpiCols && m0 + c < p.M ? o.sx[m0 + c] : 0.0f;
             }
-            auto scales_from = [&](int c) {   // of the 16 columns from 16 c (c in ascending order)
-                if ((16 * c) % L::kScaleCols == 0) {
+            int window = -1;   // the columns whose scales are in shared memory
+            auto scales_from = [&](int c) {   // of the 16 columns from 16 c
+                const int at0 = (16 * c) / L::kScaleCols * L::kScaleCols;
+                if (at0 != window) {
+                    window = at0;
                     __syncwarp();
 #pragma unroll
                     for (int h = 0; h < kHeld; ++h) {
-                        const int at = 32 * h + lane - 16 * c;
+                        const int at = 32 * h + lane - at0;
                         if (at >= 0 && at < L::kScaleCols) sxs[at] = held[h];
                     }
                     __syncwarp();
                 }
-                return sxs + (16 * c) % L::kScaleCols;
+                return sxs + 16 * c - at0;
             };
             if (!gemm::warp_wait(dfull(b), (pc / kD) & 1, wc)) break;
             tc_fence_after();
@@ -546,72 +552,88 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 }
                 release();
                 store_packed<L::kEpiCols>(p, n, m0, w);
-            } else {
-                float4* mine = part_slot<NA>(p, cta, which) + (col0 / 4) * 128 + row;
+            } else if (whole) {
 #pragma unroll 1
                 for (int c = 0; c < L::kEpiCols / 16; ++c) {
                     float f[16];
                     load16(c, f);
-                    if (whole) {
-                        store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, f);
-                    } else {
-#pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            __stcg(mine + (4 * c + g) * 128,
-                                   make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
-                    }
+                    store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, f);
                 }
                 release();
-            }
-            if (!whole) {
-                // every lane's partial visible GPU-wide before lane 0's arrival.  A
-                // split tile's counter is indexed by the CTA that holds its first
+            } else {
+                // A piece of a split tile: partial sums to the workspace, a slice
+                // of the warp's columns at a time, each with an arrival counter of
+                // its own; the last of a tile's CTAs to arrive at a slice sums it.
+                // The CTAs start at different slices, so that, ending together,
+                // they are each last at some: one CTA summing all of a tile was
+                // bound by its own reads of L2 (8 to 10 us of a wide tile).
+                //
+                // A counter is indexed by the CTA that holds the tile's first
                 // unit: that CTA's last tile, so no other tile shares it (a pair's
                 // CTAs keep partial sums and counters of their own).
                 const int cf = __shfl_sync(0xffffffffu, split_info, 3 * which);
                 const int cl = __shfl_sync(0xffffffffu, split_info, 3 * which + 1);
                 const int w_first = __shfl_sync(0xffffffffu, split_info, 3 * which + 2);
-                uint32_t* cnt = p.cnt + (cf * L::kCtas + static_cast<int>(rank)) * 8 + ew;
-                __threadfence();
-                __syncwarp();
-                uint32_t prev = 0;
-                if (lane == 0) prev = atomicAdd(cnt, 1u);
-                prev = __shfl_sync(0xffffffffu, prev, 0);
-                if (static_cast<int>(prev) == cl - cf) {
-                    __threadfence();
+                uint32_t* cnt = p.cnt + ((cf * L::kCtas + static_cast<int>(rank)) * 8 + ew) * kInt8Slices;
+                float4* mine = part_slot<NA>(p, cta, which) + (col0 / 4) * 128 + row;
+                const int s0 = (worker - cf) * L::kSlices / (cl - cf + 1);
+                uint32_t last_at = 0;   // slices this CTA is the last to arrive at
 #pragma unroll 1
-                    for (int c = 0; c < L::kEpiCols / 16; ++c) {
-                        float acc[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-                        // four pieces' loads in flight at a time
+                for (int e = 0; e < L::kSlices; ++e) {
+                    const int sl = (s0 + e) % L::kSlices;
 #pragma unroll 1
-                        for (int c4 = cf; c4 <= cl; c4 += 4) {
-                            float4 x[4][4];
+                    for (int c = sl * L::kSliceCols / 16; c < (sl + 1) * L::kSliceCols / 16; ++c) {
+                        float f[16];
+                        load16(c, f);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int c2 = c4 + e;
-                                const float4* src =
-                                    part_slot<NA>(p, c2 * L::kCtas + static_cast<int>(rank), c2 == cf ? w_first : 0) +
-                                    (col0 / 4 + 4 * c) * 128 + row;
-#pragma unroll
-                                for (int g = 0; g < 4; ++g)
-                                    x[e][g] = c2 <= cl ? __ldcg(src + g * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                                for (int g = 0; g < 4; ++g) {
-                                    acc[4 * g + 0] = __fadd_rn(acc[4 * g + 0], x[e][g].x);
-                                    acc[4 * g + 1] = __fadd_rn(acc[4 * g + 1], x[e][g].y);
-                                    acc[4 * g + 2] = __fadd_rn(acc[4 * g + 2], x[e][g].z);
-                                    acc[4 * g + 3] = __fadd_rn(acc[4 * g + 3], x[e][g].w);
-                                }
-                        }
-                        store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, acc);
+                        for (int g = 0; g < 4; ++g)
+                            __stcg(mine + (4 * c + g) * 128,
+                                   make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
                     }
+                    if (e == L::kSlices - 1) release();
+                    // every lane's partial visible GPU-wide before lane 0's arrival
+                    __threadfence();
                     __syncwarp();
-                    if (lane == 0) *cnt = 0u;   // ready for the next call
+                    uint32_t prev = 0;
+                    if (lane == 0) prev = atomicAdd(cnt + sl, 1u);
+                    prev = __shfl_sync(0xffffffffu, prev, 0);
+                    if (static_cast<int>(prev) == cl - cf) last_at |= 1u << sl;
+                }
+                if (last_at) __threadfence();
+#pragma unroll 1
+                for (int c = 0; c < L::kEpiCols / 16; ++c) {
+                    const int sl = 16 * c / L::kSliceCols;
+                    if (!(last_at >> sl & 1u)) continue;
+                    float acc[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
+                    // four pieces' loads in flight at a time
+#pragma unroll 1
+                    for (int c4 = cf; c4 <= cl; c4 += 4) {
+                        float4 x[4][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c2 = c4 + e;
+                            const float4* src =
+                                part_slot<NA>(p, c2 * L::kCtas + static_cast<int>(rank), c2 == cf ? w_first : 0) +
+                                (col0 / 4 + 4 * c) * 128 + row;
+#pragma unroll
+                            for (int g = 0; g < 4; ++g)
+                                x[e][g] = c2 <= cl ? __ldcg(src + g * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) {
+                                acc[4 * g + 0] = __fadd_rn(acc[4 * g + 0], x[e][g].x);
+                                acc[4 * g + 1] = __fadd_rn(acc[4 * g + 1], x[e][g].y);
+                                acc[4 * g + 2] = __fadd_rn(acc[4 * g + 2], x[e][g].z);
+                                acc[4 * g + 3] = __fadd_rn(acc[4 * g + 3], x[e][g].w);
+                            }
+                    }
+                    store16(p, o, n, m0 + 16 * c, scales_from(c), sw, bias, acc);
+                    // its last columns: the slice is ready for the next call
+                    if (lane == 0 && (16 * c + 16) % L::kSliceCols == 0) cnt[sl] = 0u;
                 }
             }
             ps = pe + 1;
@@ -779,19 +801,22 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
 //   - one worker a tile: KU units
 //   - k = floor(workers / r) equal pieces of every tile: ceil(KU / k) units and
 //     a split (storing, counting and summing partial results)
-//   - all workers, pieces that straddle tiles: ceil(r KU / workers) units, a
-//     split, and half of one more (a worker may end two pieces)
+//   - all workers, pieces that straddle tiles: ceil(r KU / workers) units and
+//     two splits a worker
 // A tile has the fewest activation rows that take the batch, up to 64; beyond,
 // 128 or 256, whichever costs less: wide tiles read fewer weights and
-// activations per product (660 ns a unit of twice the work against 380), but
-// a split's partial results are twice as many, summed by half as many CTAs (14
-// us against 6 on 256 x 5120 x 17408).
+// activations per product, but split at a higher price.  Measured (whole tiles
+// / equal pieces / straddling): 256 x 5120 x 17408 at 128 rows 52.8 / - / 44.7
+// us, at 256 rows 81.0 / 42.4 / 49.8; 128 x 6144 x 5120 at 128 rows 19.3 / 17.6
+// / 22.7, at 256 rows 28.9 / 23.5 / 31.6; 1 x 1024 x 5120 at 16 rows 15.9 / 8.4
+// / 8.8.
 constexpr int kMostPieces = 8;
 struct TileCost {
     int rows;
-    long long unit_ns, split_ns;
+    long long unit_ns, split_ns, straddle_ns;
 };
-constexpr TileCost kNarrow{0, 370, 3700}, kTile128{128, 380, 6000}, kTile256{256, 660, 14000};
+constexpr TileCost kTiles[] = {
+    {16, 300, 4000, 7500}, {32, 310, 4000, 7500}, {64, 340, 7500, 10500}, {128, 350, 7500, 14500}, {256, 560, 9500, 24000}};
 
 Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int forced, long long* cost) {
     Schedule s;
@@ -812,7 +837,7 @@ Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int for
     if (r > 0) {
         auto up = [](long long a, long long b) { return (a + b - 1) / b; };
         const long long all = w < r * s.KU ? w : r * s.KU;
-        const long long straddle = up(r * s.KU, all) * tc.unit_ns + tc.split_ns + tc.split_ns / 2;
+        const long long straddle = up(r * s.KU, all) * tc.unit_ns + tc.straddle_ns;
         long long best = s.KU * tc.unit_ns;
         g = r;
         long long k = w / r;
@@ -837,16 +862,12 @@ Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int for
 }
 
 Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
-    long long cost = 0, cost256 = 0;
-    if (M <= 64) {
-        TileCost t = kNarrow;
-        t.rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
-        return schedule_with(t, M, N, K, sms, forced, &cost);
-    }
-    const Schedule s = schedule_with(kTile128, M, N, K, sms, forced, &cost);
+    long long cost = 0, wide_cost = 0;
+    const int t = M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : 3;
+    const Schedule s = schedule_with(kTiles[t], M, N, K, sms, forced, &cost);
     if (M <= 128) return s;
-    const Schedule wide = schedule_with(kTile256, M, N, K, sms, forced, &cost256);
-    return cost256 < cost ? wide : s;
+    const Schedule wide = schedule_with(kTiles[4], M, N, K, sms, forced, &wide_cost);
+    return wide_cost < cost ? wide : s;
 }
 
 size_t int8_expanded_bytes(int M, int K) {
@@ -860,7 +881,7 @@ size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split) {
 
 cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                         const LaunchCtl& c, cudaStream_t st) {
-    if (static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 8 * sizeof(uint32_t) > kInt8CounterBytes) return cudaErrorInvalidValue;
+    if (static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 8 * kInt8Slices * sizeof(uint32_t) > kInt8CounterBytes) return cudaErrorInvalidValue;
     const int K16 = a.K / 16;
     int64_t blocks = (static_cast<int64_t>(a.M) * K16 + 255) / 256;
     if (blocks > 4 * c.num_sms) blocks = 4 * c.num_sms;

@@ -31,7 +31,8 @@ Schedule int8_schedule(int M, int N, int K, int sms, int forced);
 // counters (kInt8CounterBytes, zero between calls, at offset 0 for every
 // shape), the activations as FP16 [M, K], then the split-K partial sums of a
 // schedule that splits tiles (two slots of 128 x s.nmma FP32 per CTA).
-constexpr size_t kInt8CounterBytes = 16384;
+constexpr size_t kInt8CounterBytes = 32768;
+constexpr int kInt8Slices = 2;   // counters of an epilogue warp of a split tile
 size_t int8_expanded_bytes(int M, int K);
 size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split);
 
