@@ -65,20 +65,24 @@ struct I8Layout {
     // per epilogue warp, the activation scales of the columns at hand
     static constexpr int kScaleCols = kEpiCols < 64 ? kEpiCols : 64;
     static constexpr int kWBytes = 128 * 128;
-    // The operand ring: a slot is one unit's A buffer in TMEM (64 columns) and
-    // its activations in shared memory (two boxes of 64 K).  One barrier says
-    // that both are there, one that the unit's MMAs have read them, so that
-    // the MMA warp passes one wait and one commit per unit: each costs it
-    // 0.05 to 0.1 us even when nothing is late (with separate rings, three
-    // waits and three commits a unit, gate/up at 16 rows took 28.0 us).
-    static constexpr int kSlots = 4;
+    // The operand ring: a slot holds one unit's activations in shared memory
+    // (two boxes of 64 K); the unit's A buffer in TMEM (64 columns) is one of
+    // kABufs taken in turn.  One barrier of the slot says that both are there,
+    // one that the unit's MMAs have read them, so that the MMA warp passes one
+    // wait and one commit per unit: each costs it 0.05 to 0.1 us even when
+    // nothing is late (with separate rings, three waits and three commits a
+    // unit, gate/up at 16 rows took 28.0 us).  More slots than A buffers where
+    // they fit: a copy of activations takes most of a microsecond, and with
+    // four slots that set the pace of a CTA (0.3 us a unit).
+    static constexpr int kABufs = 4;
+    static constexpr int kSlots = NA <= 32 ? 8 : NA <= 128 ? 6 : 4;
     static constexpr int kXRows = NA / kCtas;                   // of the tile, in this CTA's shared memory
     static constexpr int kXBox = kXRows * 128;
     static constexpr int kXSlot = 2 * kXBox;
     static constexpr int kWFit = (232448 - 512 - kEpi * kScaleCols * 4 - kSlots * kXSlot) / kWBytes;
     static constexpr int kWStages = (kWFit < 12 ? kWFit : 12) / kGroups * kGroups;
     static constexpr int kD = NA > 128 ? 1 : 2;                 // accumulators, NA columns each
-    static constexpr int kDCol0 = kSlots * 64;
+    static constexpr int kDCol0 = kABufs * 64;
     static constexpr int kXOff = kWStages * kWBytes;
     static constexpr int kBarOff = kXOff + kSlots * kXSlot;
     static constexpr int kNumBars = 2 * kWStages + 2 * kSlots + 2 * kD;
@@ -88,9 +92,10 @@ struct I8Layout {
     static_assert(kDCol0 + kD * NA <= 512, "TMEM columns");
     static_assert(kSmemBytes <= 232448, "shared memory");
     static_assert(kXBox % 1024 == 0, "keep the 1024-byte swizzle alignment");
-    // a weight stage and a slot always belong to one convert group, so that
-    // its parity waits are for the phase after one it has seen
-    static_assert(kWStages % kGroups == 0 && kSlots % kGroups == 0, "ring ownership");
+    // a weight stage, a slot and an A buffer always belong to one convert
+    // group, so that its parity waits are for the phase after one it has seen
+    static_assert(kWStages % kGroups == 0 && kSlots % kGroups == 0 && kABufs % kGroups == 0, "ring ownership");
+    static_assert(kSlots >= kABufs, "a unit's A buffer is free once the unit kABufs before it is done");
     static_assert(kEpiCols % 16 == 0, "epilogue chunks");
 };
 
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p,
                 const Out o) {
     using L = I8Layout<NA, kPair>;
-    constexpr int kWStages = L::kWStages, kSlots = L::kSlots, kD = L::kD;
+    constexpr int kWStages = L::kWStages, kSlots = L::kSlots, kABufs = L::kABufs, kD = L::kD;
     extern __shared__ __align__(1024) uint8_t gbase[];
     const uint32_t base = smem_u32(gbase);
     if (base & 1023u) {   // the swizzle needs the alignment asked for above
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             if (!wait(ofull(ro.slot), ro.phase)) break;
             tc_fence_after();
             const uint32_t dt = tmem + L::kDCol0 + b * NA;
-            const uint32_t at = tmem + ro.slot * 64;
+            const uint32_t at = tmem + (i % kABufs) * 64;
             const uint64_t xd = dx0 + static_cast<uint64_t>((ro.slot * L::kXSlot) >> 4);
             const bool closes = i == nunits - 1 || kb == p.KB - 1;
             if (elected) {
@@ -436,14 +441,18 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         const int row = q * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
         Ring<kWStages> rw(grp);
-        Ring<kSlots> ro(grp);
+        Ring<kSlots> ro(grp);      // the unit's slot
+        Ring<kSlots> done(grp);    // that of the unit kABufs before it, whose A buffer it takes
         for (int i = grp; i < nunits; i += kGroups, rw.step(kGroups), ro.step(kGroups)) {
             if (!gemm::warp_wait(wfull(rw.slot), rw.phase, wc)) break;
             const uint8_t* src = gbase + rw.slot * L::kWBytes + row * 128;
             uint4 c[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
-            if (i >= kSlots && !gemm::warp_wait(ofree(ro.slot), ro.phase ^ 1u, wc)) break;
+            if (i >= kABufs) {
+                if (!gemm::warp_wait(ofree(done.slot), done.phase, wc)) break;
+                done.step(kGroups);
+            }
             __syncwarp();
             tc_fence_after();
 #pragma unroll
@@ -457,7 +466,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                     s8x4_to_f16(w.z, f[8 * e + 4], f[8 * e + 5]);
                     s8x4_to_f16(w.w, f[8 * e + 6], f[8 * e + 7]);
                 }
-                tmem_st_x16(tl + ro.slot * 64 + t * 16, f);
+                tmem_st_x16(tl + (i % kABufs) * 64 + t * 16, f);
             }
             // the loads have returned: the TMEM stores above needed them
             __syncwarp();
