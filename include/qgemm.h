@@ -87,8 +87,8 @@ enum { QG_BF16 = 0, QG_FP16 = 1, QG_FP32 = 2 };
  * partial sums): a workspace serves either QG_KIND_W8A8 calls or calls of
  * the other kinds, not both, unless it is zero-filled again in between.
  * QG_KIND_INT8 has a layout of its own too: 32768 bytes of arrival counters
- * (at the front for every shape), the activations expanded to FP16 (2 M K
- * bytes rounded up to 256), then the partial sums of a schedule that splits
+ * (at the front for every shape), the activations expanded to FP16 (M > 16:
+ * 2 M K bytes rounded up to 256), then the partial sums of a schedule that splits
  * tiles (two slots of 512 R bytes for each CTA, R = the rows of a tile: 16,
  * 32, 64 or 128); its workspace serves INT8 calls of any shape, and no other
  * kind.
@@ -338,10 +338,11 @@ qg_status qg_quantize_act_int8(const void *X, int x_type, int64_t ldx, int8_t *X
  *   M, N, K  1 <= M <= 65536, N >= 1, K % 16 == 0; K == 0 writes the bias
  *            (or zeros) to every row
  *   workspace  at least qg_workspace_bytes(QG_KIND_INT8, M, N, K) bytes,
- *            zero-filled before its first use, 256-byte aligned (every
- *            INT8 call needs one: it holds the activations as FP16)
- * A call launches two kernels: the expansion of the activations, and the
- * GEMM, whose weight stream starts under it.
+ *            zero-filled before its first use, 256-byte aligned (may be NULL
+ *            when that is 0; every call with M > 16 needs one, which holds
+ *            the activations as FP16)
+ * A call with M <= 16 launches one kernel, any other two: the expansion of
+ * the activations, and the GEMM, whose weight stream starts under it.
  */
 qg_status qgemm_w8a8_int8(const int8_t *Xq, int64_t ldxq, const float *X_scale,
                           const int8_t *W, const float *W_scale, const float *bias,

@@ -751,15 +751,16 @@ qg_status qgemm_w8a8_int8(const int8_t* Xq, int64_t ldxq, const float* X_scale, 
     if (K == 0) return launch_int8_bias_rows(a, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
     const SchedEntry& se = cached_schedule(QG_KIND_INT8, M, N, K, d->sms);
     const Schedule s = se.s;
-    if (!workspace || workspace_bytes_ < se.ws || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    if (se.ws > 0 && (!workspace || workspace_bytes_ < se.ws || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return QG_ERR_WORKSPACE;
-    a.ws = workspace;
-    CUtensorMap tmW, tmX;
+    a.ws = se.ws > 0 ? workspace : nullptr;
+    CUtensorMap tmW, tmX{};
     if (!make_tmap(&tmW, W, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<uint64_t>(K), static_cast<uint64_t>(N),
                    static_cast<uint64_t>(K), 128, 128) ||
+        (!int8_inline_x(s) &&
         !make_tmap(&tmX, static_cast<uint8_t*>(workspace) + kInt8CounterBytes, CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                    static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K) * 2, 64,
-                   static_cast<uint32_t>(s.nmma / int8_ctas(s.nmma))))
+                   static_cast<uint32_t>(s.nmma / int8_ctas(s.nmma)))))
         return QG_ERR_CUDA;
     return launch_int8(a, s, tmW, tmX, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }

@@ -20,12 +20,14 @@
 // where the MMA takes its A operand.  Activations are expanded to FP16 once
 // per call by a small kernel in front (they are read by every weight tile;
 // converting them in each CTA would cost NA/128 of the weight conversion and
-// twice the shared memory traffic) and arrive by TMA as the B operand.
+// twice the shared memory traffic) and arrive by TMA as the B operand.  Up to
+// 16 rows two warps of the GEMM expand them instead, which saves a launch.
 //
 // One persistent CTA per SM; warps by role:
 //   warp 0        weight producer (TMA, one 16 KB box per unit)
 //   warp 1        activation producer (TMA, two boxes of 64 K x NA rows a unit),
-//                 after the expansion kernel's completion
+//                 after the expansion kernel's completion; up to 16 rows warps 1
+//                 and 3 load and expand the codes themselves
 //   warp 2        MMA issuer: 8 tcgen05.mma (M = 128, N = NA, K = 16) a unit
 //   warps 4-      epilogue: one per TMEM lane quadrant (two for NA >= 128)
 //   the last 8    convert: two groups of four warps taking alternate units
@@ -48,13 +50,18 @@ using gemm::Cursor;
 using gemm::Params;
 using gemm::Ring;
 
-constexpr int kWarpWProd = 0, kWarpXProd = 1, kWarpMma = 2, kWarpEpi0 = 4;
+constexpr int kWarpWProd = 0, kWarpXProd = 1, kWarpMma = 2, kWarpX2 = 3, kWarpEpi0 = 4;
 constexpr int kGroups = 2;   // convert groups of four warps
 
 // NA activation rows a tile; kPair: a tile is 256 weight rows on a CTA pair.
 template <int NA, bool kPair>
 struct I8Layout {
     static constexpr int kCtas = kPair ? 2 : 1;
+    // up to 16 rows the activations are expanded in the kernel (warps 1 and 3,
+    // alternate units); beyond, by the kernel in front (at 32 rows the two
+    // warps set the pace: 43.7 us against 34.5 on 32 x 32768 x 5120)
+    static constexpr bool kInlineX = NA <= 16;
+    static constexpr int kXChunks = NA * 8 / 32;                // a lane's 16-byte pieces of a unit's codes
     static constexpr int kEpi = NA >= 128 ? 8 : 4;
     static constexpr int kEpiCols = NA / (kEpi / 4);            // columns per epilogue warp
     static constexpr int kWarpConv0 = kWarpEpi0 + kEpi;
@@ -100,6 +107,8 @@ struct I8Layout {
 };
 
 struct Out {
+    const int8_t* xq;
+    int64_t ldxq;
     const float* sx;
     const float* sw;
     const float* bias;
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             if constexpr (kPair) tmem_alloc_pair(smem_u32(tmem_slot), 512);
             else tmem_alloc(smem_u32(tmem_slot), 512);
         }
-        if (warp == kWarpXProd && lane == 0) prefetch_tmap(&tmX);
+        if (!L::kInlineX && warp == kWarpXProd && lane == 0) prefetch_tmap(&tmX);
         tc_fence_before();
         __syncwarp();
         if constexpr (kPair) cluster_sync_all();   // the peer's barriers are set up too
@@ -362,6 +371,50 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
 
     if (warp == kWarpWProd) {
         // done above
+    } else if (L::kInlineX && (warp == kWarpXProd || warp == kWarpX2)) {
+        // Codes of a unit in registers while the unit two before is stored: 16
+        // codes a piece, two 16-byte chunks of FP16 in the swizzled layout the
+        // MMA reads.
+        const int xi = warp == kWarpXProd ? 0 : 1;
+        grid_dependency_wait();
+        Walk cur(p, o, worker, u0);
+        if (xi == 1) cur.step(p, o);
+        auto fetch = [&](int i, uint4 (&x)[L::kXChunks]) {
+#pragma unroll
+            for (int j = 0; j < L::kXChunks; ++j) {
+                const int m = cur.tm * NA + j * 4 + (lane >> 3);
+                const int k = cur.kr * 128 + (lane & 7) * 16;
+                x[j] = i < nunits && m < p.M && k < p.K
+                           ? *reinterpret_cast<const uint4*>(o.xq + static_cast<int64_t>(m) * o.ldxq + k)
+                           : make_uint4(0u, 0u, 0u, 0u);
+            }
+            cur.step(p, o);
+            cur.step(p, o);
+        };
+        uint4 x[L::kXChunks], ahead[L::kXChunks];
+        fetch(xi, x);
+        Ring<kSlots> ro(xi);
+        for (int i = xi; i < nunits; i += 2, ro.step(2)) {
+            fetch(i + 2, ahead);
+            if (i >= kSlots && !gemm::warp_wait(ofree(ro.slot), ro.phase ^ 1u, wc)) break;
+            uint8_t* box = gbase + L::kXOff + ro.slot * L::kXSlot + ((lane & 7) >> 2) * L::kXBox;
+            const int c0 = (lane & 3) * 2;
+#pragma unroll
+            for (int j = 0; j < L::kXChunks; ++j) {
+                const int r = j * 4 + (lane >> 3);
+                uint4 a, b;
+                s8x4_to_f16(x[j].x, a.x, a.y);
+                s8x4_to_f16(x[j].y, a.z, a.w);
+                s8x4_to_f16(x[j].z, b.x, b.y);
+                s8x4_to_f16(x[j].w, b.z, b.w);
+                *reinterpret_cast<uint4*>(box + r * 128 + ((c0 ^ (r & 7)) << 4)) = a;
+                *reinterpret_cast<uint4*>(box + r * 128 + (((c0 + 1) ^ (r & 7)) << 4)) = b;
+                x[j] = ahead[j];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ofull(ro.slot));
+        }
     } else if (warp == kWarpXProd) {
         if (lane == 0) {
             grid_dependency_wait();   // the expansion kernel's output
@@ -663,7 +716,9 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     }
 }
 
-// The activations as FP16 [M, K]: 16 codes (K % 16 == 0) a thread.
+// The activations as FP16 [M, K]: 16 codes (K % 16 == 0) a thread.  The GEMM
+// behind it may start, and stream weights, at once: the grid before this one is
+// done by then, unless the caller allows the overlap.
 __global__ void __launch_bounds__(256) expand_kernel(const int8_t* __restrict__ Xq, int64_t ldxq,
                                                      uint4* __restrict__ out, int M, int K16) {
     grid_dependents_launch();
@@ -777,27 +832,32 @@ cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorM
     p.G = s.tail_g;
     uint8_t* w = static_cast<uint8_t*>(a.ws);
     p.cnt = reinterpret_cast<uint32_t*>(w);
-    p.part = reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(a.M, a.K));
+    p.part = w ? reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(s, a.M, a.K)) : nullptr;
     const int y_pairs = a.y_type != QG_FP32 && a.N % 2 == 0 && a.ldy % 2 == 0 &&
                         (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
-    const Out o{a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull,
+    const Out o{a.Xq, a.ldxq, a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull,
                 p.G > 0 ? static_cast<int>(p.U / p.G) : 0, p.G > 0 ? static_cast<int>(p.U % p.G) : 0};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
     cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kSmemBytes;
     cfg.stream = st;
-    // always overlapped with the expansion kernel in front, which is part of
-    // this call: the weight stream starts under it
+    // always overlapped with the expansion kernel in front, where there is one
+    // (it is part of this call): the weight stream starts under it
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    int n = 0;
+    if (!L::kInlineX || c.overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (kPair) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = kPair ? 2 : 1;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, int8_kernel<NA, kPair>, tmW, tmX, p, o);
 }
 
@@ -879,35 +939,40 @@ Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
     return wide_cost < cost ? wide : s;
 }
 
-size_t int8_expanded_bytes(int M, int K) {
+size_t int8_expanded_bytes(const Schedule& s, int M, int K) {
+    if (int8_inline_x(s)) return 0;
     return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255);
 }
 
 size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split) {
     const size_t part = split ? static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 2 * 128 * s.nmma * sizeof(float) : 0;
-    return kInt8CounterBytes + int8_expanded_bytes(M, K) + part;
+    const size_t x = int8_expanded_bytes(s, M, K);
+    return part + x > 0 ? kInt8CounterBytes + x + part : 0;
 }
 
 cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                         const LaunchCtl& c, cudaStream_t st) {
-    if (static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 8 * kInt8Slices * sizeof(uint32_t) > kInt8CounterBytes) return cudaErrorInvalidValue;
-    const int K16 = a.K / 16;
-    int64_t blocks = (static_cast<int64_t>(a.M) * K16 + 255) / 256;
-    if (blocks > 4 * c.num_sms) blocks = 4 * c.num_sms;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    if (c.overlap) {
+    if (static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 8 * kInt8Slices * sizeof(uint32_t) > kInt8CounterBytes)
+        return cudaErrorInvalidValue;
+    if (!int8_inline_x(s)) {
+        const int K16 = a.K / 16;
+        int64_t blocks = (static_cast<int64_t>(a.M) * K16 + 255) / 256;
+        if (blocks > 4 * c.num_sms) blocks = 4 * c.num_sms;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        // waiting resident for the preceding grid even where the caller did not
+        // ask for overlap took 0.3 us off small calls, but slowed large ones by 3%
+        cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = c.overlap ? 1 : 0;
+        uint4* xf = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.ws) + kInt8CounterBytes);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel, a.Xq, a.ldxq, xf, a.M, K16);
+        if (e != cudaSuccess) return e;
     }
-    uint4* xf = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.ws) + kInt8CounterBytes);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel, a.Xq, a.ldxq, xf, a.M, K16);
-    if (e != cudaSuccess) return e;
     switch (s.nmma) {
         case 16: return launch_int8_na<16, false>(a, s, tmW, tmX, c, st);
         case 32: return launch_int8_na<32, false>(a, s, tmW, tmX, c, st);

@@ -29,16 +29,19 @@ Schedule int8_schedule(int M, int N, int K, int sms, int forced);
 
 // Workspace of a schedule (s.nmma = the tile's activation rows): the arrival
 // counters (kInt8CounterBytes, zero between calls, at offset 0 for every
-// shape), the activations as FP16 [M, K], then the split-K partial sums of a
-// schedule that splits tiles (two slots of 128 x s.nmma FP32 per CTA).
+// shape), the activations as FP16 [M, K] (nothing where the GEMM expands them
+// itself, int8_inline_x), then the split-K partial sums of a schedule that
+// splits tiles (two slots of 128 x s.nmma FP32 per CTA); 0 when it holds neither.
 constexpr size_t kInt8CounterBytes = 32768;
 constexpr int kInt8Slices = 2;   // counters of an epilogue warp of a split tile
-size_t int8_expanded_bytes(int M, int K);
+inline bool int8_inline_x(const Schedule& s) { return s.nmma <= 16; }
+size_t int8_expanded_bytes(const Schedule& s, int M, int K);
 size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split);
 
 // tmW: the weight map ([N, K] bytes, 128 x 128 boxes, 128-byte swizzle);
 // tmX: the expanded activations ([M, K] FP16, boxes of 64 K x the rows of a
-// tile that one CTA holds, s.nmma / int8_ctas).
+// tile that one CTA holds, s.nmma / int8_ctas), not used where the GEMM expands
+// them itself.
 cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                         const LaunchCtl& c, cudaStream_t st);
 cudaError_t launch_quantize_int8(const void* X, int x_type, int64_t ldx, int8_t* Xq, int64_t ldxq, float* Sx, int M,
