@@ -22,23 +22,33 @@
 // of this file's row function: a maximum beyond +-1e8 (or at the floor: a row
 // of nothing but masks), a NaN or +inf, or more than kCap logits at the bound.
 //
-// One CTA per row; rows that are too few for the SMs are split over a cluster
-// of up to 16 CTAs, whose sums and lists rank 0 joins through distributed
-// shared memory (no workspace, no atomics on memory, the same order of sums
-// on every call).
+// A few CTAs per SM walk over the rows.  One warp of a CTA streams them into a
+// ring in shared memory by bulk copies, running on into the next row while the
+// other eight finish one (choosing the alternatives takes about as long as
+// reading 40 KB: 4 us, with nothing on the way from memory when each row had a
+// CTA of its own and registers for its loads).  Rows that are too few for the
+// SMs are split over a cluster of up to 16 CTAs, whose sums and lists rank 0
+// joins through distributed shared memory (no workspace, no atomics on memory,
+// the same order of sums on every call).
+#include <cstddef>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "qg_device.cuh"
+#include "qg_gemm.cuh"
 #include "qg_logprobs.h"
 
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;      // that take logits; one more warp streams them in
 constexpr int kWarps = kThreads / 32;
 constexpr int kPairs = kThreads / 2;
-constexpr int kCap = 1024;         // candidates at the bound
+constexpr int kCtasPerSm = 3;
+constexpr int kStages = 4;         // of the ring, one turn each
+constexpr int kU = 4;              // 16-byte vectors a thread takes in a turn
+constexpr int kTurn = kU * kThreads;
+constexpr int kCap = 512;          // candidates at the bound
 constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -46,11 +56,11 @@ constexpr float kFar = 1e8f;       // a maximum beyond this goes the plain way
 constexpr float kNoRef = -3e38f;   // c before the first logit
 
 template <int kType>
-struct Fmt;   // element unpacking: kE elements in a 16-byte vector, kU vectors a thread has in flight
+struct Fmt;   // element unpacking: kE elements in a 16-byte vector
 
 template <>
 struct Fmt<QG_FP32> {
-    static constexpr int kE = 4, kU = 8, kSize = 4;
+    static constexpr int kE = 4, kSize = 4;
     static constexpr float kFloor = -1e30f;
     __device__ static float at(const void* row, int64_t v) { return static_cast<const float*>(row)[v]; }
     __device__ static uint32_t floor_word(uint32_t w) {
@@ -62,12 +72,13 @@ struct Fmt<QG_FP32> {
         return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
     }
     __device__ static float max_of(uint32_t w) { return __uint_as_float(w); }
-    static constexpr uint32_t kEmpty = 0xFF800000u;   // -inf
+    __device__ static float element(const uint32_t (&w)[4], int e) { return __uint_as_float(w[e]); }
+    static constexpr uint32_t kEmpty = 0xFF800000u;   // words of -inf
 };
 
 template <>
 struct Fmt<QG_BF16> {
-    static constexpr int kE = 8, kU = 4, kSize = 2;
+    static constexpr int kE = 8, kSize = 2;
     static constexpr float kFloor = -1.0003425e30f;   // the bf16 0xF14A
     __device__ static float at(const void* row, int64_t v) {
         return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[v]) << 16);
@@ -89,12 +100,15 @@ struct Fmt<QG_BF16> {
         a = __uint_as_float(w << 16);
         b = __uint_as_float(w & 0xFFFF0000u);
     }
+    __device__ static float element(const uint32_t (&w)[4], int e) {
+        return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+    }
     static constexpr uint32_t kEmpty = 0xFF80FF80u;
 };
 
 template <>
 struct Fmt<QG_FP16> {
-    static constexpr int kE = 8, kU = 4, kSize = 2;
+    static constexpr int kE = 8, kSize = 2;
     static constexpr float kFloor = -65504.0f;
     __device__ static float at(const void* row, int64_t v) { return __half2float(static_cast<const __half*>(row)[v]); }
     __device__ static uint32_t floor_word(uint32_t w) {
@@ -116,6 +130,11 @@ struct Fmt<QG_FP16> {
         float a, b;
         unpack(w, a, b);
         return fmaxf(a, b);
+    }
+    __device__ static float element(const uint32_t (&w)[4], int e) {
+        float a, b;
+        unpack(w[e >> 1], a, b);
+        return e & 1 ? b : a;
     }
     static constexpr uint32_t kEmpty = 0xFC00FC00u;
 };
@@ -194,10 +213,12 @@ struct Sums {
 };
 
 struct Shared {
+    uint64_t full[kStages], empty[kStages];   // of the ring
+    int abort;
     float warp_mx[kWarps];
     float warp_s[kWarps], warp_w[kWarps];
     uint32_t warp_u[kWarps];
-    float pair_mx[kPairs];
+    alignas(16) uint32_t pair_key[kPairs];   // read four at a time
     float bound;
     int flagged[kPairs];
     int nflagged, ncand, nlist;
@@ -210,12 +231,25 @@ struct Shared {
     int slow_ids[kMaxTopK];
 };
 
+// The barrier of the threads that take logits.
+__device__ __forceinline__ void meet() { named_bar_sync(1, kThreads); }
+// The barrier of all threads of a row's cluster.
+__device__ __forceinline__ void cluster_meet() {
+    __syncwarp();
+    cluster_sync_all();
+}
+
+static_assert(offsetof(Shared, pair_key) % 16 == 0 && alignof(Shared) >= 16, "vector reads of the maxima");
+static_assert(offsetof(Shared, full) % 8 == 0 && offsetof(Shared, list) % 8 == 0 && offsetof(Shared, cand) % 8 == 0 &&
+                  offsetof(Shared, joined) % 8 == 0,
+              "barriers and entries");
+
 __device__ __forceinline__ float block_sum(float x, float* buf) {
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    __syncthreads();
+    meet();
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
+    meet();
     float r = 0.0f;
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) r += buf[j];
@@ -224,9 +258,9 @@ __device__ __forceinline__ float block_sum(float x, float* buf) {
 
 __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* buf) {
     x = __reduce_max_sync(0xffffffffu, x);
-    __syncthreads();
+    meet();
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
+    meet();
     uint32_t r = 0u;
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) r = max(r, buf[j]);
@@ -252,9 +286,9 @@ __device__ __noinline__ void top_by_value(const void* row, int V, int k, Shared&
             const int v = v0 + threadIdx.x;
             const bool hit = v < V && order_key(F::at(row, v)) == best;
             const uint32_t mask = __ballot_sync(0xffffffffu, hit);
-            __syncthreads();
+            meet();
             if ((threadIdx.x & 31) == 0) sh.warp_u[threadIdx.x >> 5] = __popc(mask);
-            __syncthreads();
+            meet();
             int before = 0, total = 0;
 #pragma unroll
             for (int j = 0; j < kWarps; ++j) {
@@ -270,7 +304,7 @@ __device__ __noinline__ void top_by_value(const void* row, int V, int k, Shared&
         }
         below = best;
     }
-    __syncthreads();
+    meet();
 }
 
 // A whole row by its definition: maximum, then sums of differences.
@@ -318,21 +352,21 @@ __device__ __forceinline__ float logp_of(float x, float c, float ls) {
 // kU vectors of a thread: their maximum first (moving c where it rose), then
 // their terms, two at a time.
 template <int kType>
-__device__ __forceinline__ void take(const uint4 (&x)[Fmt<kType>::kU], float& mx, float& c, uint64_t& s2, uint64_t& w2) {
+__device__ __forceinline__ void take(const uint4 (&x)[kU], float& mx, float& c, uint64_t& s2, uint64_t& w2) {
     using F = Fmt<kType>;
-    uint32_t u[F::kU * 4];
+    uint32_t u[kU * 4];
 #pragma unroll
-    for (int j = 0; j < F::kU; ++j) {
+    for (int j = 0; j < kU; ++j) {
         u[4 * j + 0] = F::floor_word(x[j].x);
         u[4 * j + 1] = F::floor_word(x[j].y);
         u[4 * j + 2] = F::floor_word(x[j].z);
         u[4 * j + 3] = F::floor_word(x[j].w);
     }
-    uint32_t mw[F::kU * 2];
+    uint32_t mw[kU * 2];
 #pragma unroll
-    for (int j = 0; j < F::kU * 2; ++j) mw[j] = F::max_word(u[2 * j], u[2 * j + 1]);
+    for (int j = 0; j < kU * 2; ++j) mw[j] = F::max_word(u[2 * j], u[2 * j + 1]);
 #pragma unroll
-    for (int n = F::kU; n > 0; n >>= 1)
+    for (int n = kU; n > 0; n >>= 1)
 #pragma unroll
         for (int j = 0; j < n; ++j) mw[j] = F::max_word(mw[j], mw[j + n]);
     const float top = F::max_of(mw[0]);
@@ -351,7 +385,7 @@ __device__ __forceinline__ void take(const uint4 (&x)[Fmt<kType>::kU], float& mx
     const uint64_t l2 = pack2(kLog2e, kLog2e);
     const uint64_t c2 = pack2(-c, -c);
 #pragma unroll
-    for (int j = 0; j < F::kU * 4; j += (F::kE == 4 ? 2 : 1)) {
+    for (int j = 0; j < kU * 4; j += (F::kE == 4 ? 2 : 1)) {
         float a, b;
         if constexpr (F::kE == 4) {
             a = __uint_as_float(u[j]);
@@ -367,17 +401,38 @@ __device__ __forceinline__ void take(const uint4 (&x)[Fmt<kType>::kU], float& mx
     }
 }
 
+// The part of a row that one CTA of its cluster takes: up to 15 bytes of head,
+// vectors of 16 bytes, a tail; vectors [v0, v1) here, the head in the first
+// part and the tail in the last.
 template <int kType>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs a) {
+struct Part {
+    const uint8_t* row;
+    const uint4* vec;
+    int head, tail0, v0, v1, turns;
+    __device__ Part(const LogprobArgs& a, int64_t m, uint32_t rank, uint32_t S) {
+        using F = Fmt<kType>;
+        row = static_cast<const uint8_t*>(a.logits) + m * a.ld * F::kSize;
+        head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / F::kSize;
+        if (head > a.V) head = a.V;
+        const int nv = (a.V - head) / F::kE;
+        v0 = static_cast<int>(static_cast<int64_t>(nv) * rank / S);
+        v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / S);
+        vec = reinterpret_cast<const uint4*>(row + head * F::kSize);
+        tail0 = head + nv * F::kE;
+        turns = (v1 - v0 + kTurn - 1) / kTurn;
+    }
+};
+
+template <int kType>
+__device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32_t rank, uint32_t S, Shared& sh,
+                                         const uint4* ring, int& stage, uint32_t& phase, const WaitCtl& wc) {
     using F = Fmt<kType>;
-    __shared__ Shared sh;
-    grid_dependents_launch();
-    grid_dependency_wait();
     const int tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5;
-    const uint32_t S = cluster_size(), rank = cluster_cta_rank();
-    const int64_t m = blockIdx.x / S;
-    const uint8_t* row = static_cast<const uint8_t*>(a.logits) + m * a.ld * F::kSize;
+    const Part<kType> part(a, m, rank, S);
+    const uint8_t* row = part.row;
+    const uint4* vec = part.vec;
+    const int head = part.head, v0 = part.v0, v1 = part.v1, tail0 = part.tail0;
 
     // the asked tokens' logits, on their way while the row is read
     int64_t tok = -1;
@@ -387,35 +442,35 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
         if (tok >= 0 && tok < a.V) tok_x = F::at(row, tok);
         else tok = -1;
     }
-
-    // a row is up to 15 bytes of head, vectors of 16 bytes, a tail; this CTA
-    // takes vectors [v0, v1), the first one the head and the last one the tail
-    int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / F::kSize;
-    if (head > a.V) head = a.V;
-    const int nv = (a.V - head) / F::kE;
-    const int v0 = static_cast<int>(static_cast<int64_t>(nv) * rank / S);
-    const int v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) / S);
-    const uint4* vec = reinterpret_cast<const uint4*>(row + head * F::kSize);
-    const int tail0 = head + nv * F::kE;
     int lone = -1;   // the index of the head or tail logit this thread takes
     if (rank == 0 && tid < head) lone = tid;
     if (rank == S - 1 && tid >= 32 && tid - 32 < a.V - tail0) lone = tail0 + tid - 32;
+    float lone_x = lone >= 0 ? F::at(row, lone) : 0.0f;
 
     Sums t{-INFINITY, kNoRef, 0.0f, 0.0f};
     uint64_t s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
     const uint4 empty = make_uint4(F::kEmpty, F::kEmpty, F::kEmpty, F::kEmpty);
-    int v = v0 + tid;
-    for (; v + (F::kU - 1) * kThreads < v1; v += F::kU * kThreads) {
-        uint4 x[F::kU];
+    for (int n = 0; n < part.turns; ++n) {
+        // a wait that gives up raises the abort flag and the status; the row
+        // goes on (with what the ring holds), so that every thread meets the others
+        wait_bounded(smem_u32(&sh.full[stage]), phase, wc);
+        const uint4* at = ring + stage * kTurn + tid;
+        const int left = v1 - v0 - n * kTurn - tid;
+        uint4 x[kU];
+        if (left > (kU - 1) * kThreads) {
 #pragma unroll
-        for (int j = 0; j < F::kU; ++j) x[j] = vec[v + j * kThreads];
-        take<kType>(x, t.mx, t.c, s2, w2);
-    }
-    if (v < v1) {
-        uint4 x[F::kU];
+            for (int j = 0; j < kU; ++j) x[j] = at[j * kThreads];
+        } else {
 #pragma unroll
-        for (int j = 0; j < F::kU; ++j) x[j] = v + j * kThreads < v1 ? vec[v + j * kThreads] : empty;
+            for (int j = 0; j < kU; ++j) x[j] = left > j * kThreads ? at[j * kThreads] : empty;
+        }
         take<kType>(x, t.mx, t.c, s2, w2);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
     }
     {
         float s_hi, w_hi;
@@ -424,9 +479,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
         t.s += s_hi;
         t.w += w_hi;
     }
-    float lone_x = 0.0f;
     if (lone >= 0) {
-        lone_x = F::at(row, lone);
         const float x = lone_x < F::kFloor ? F::kFloor : lone_x;   // a NaN passes
         t.mx = fmaxf(t.mx, x);
         const float c2 = ceilf(x * kLog2e);
@@ -439,14 +492,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
 
     // the CTA's maximum and sums, and (for alternatives) the pairs' maxima
     const float pair = fmaxf(t.mx, __shfl_xor_sync(0xffffffffu, t.mx, 1));
-    if ((tid & 1) == 0) sh.pair_mx[tid >> 1] = pair;
+    if ((tid & 1) == 0) sh.pair_key[tid >> 1] = (order_key(pair) & ~(kPairs - 1u)) | (kPairs - 1u - (tid >> 1));
     float mx = pair;
 #pragma unroll
     for (int s = 16; s > 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     if (lane == 0) sh.warp_mx[warp] = mx;
     if (tid == 0) sh.nflagged = sh.ncand = sh.nlist = 0;
     if (tid < kMaxTopK) sh.list[tid] = 0ull;
-    __syncthreads();
+    meet();
     mx = sh.warp_mx[0];
 #pragma unroll
     for (int j = 1; j < kWarps; ++j) mx = fmaxf(mx, sh.warp_mx[j]);
@@ -464,63 +517,86 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
 
     bool bad = false;   // this CTA's list is not to be used
     if (a.top_k > 0) {
-        // the bound: the top_k-th largest of the pairs' maxima
-        if (tid < kPairs) {
-            const float mine = sh.pair_mx[tid];
+        // The bound: the top_k-th largest of the pairs' maxima, by counting, on
+        // their keys with the pair's number in the low bits (which makes them
+        // distinct, and the bound at most that much lower than the maximum).
+        // Each thread counts for one pair against half of them.
+        float bound = mx;
+        if (a.top_k > 1) {
+            const uint32_t mine = sh.pair_key[tid >> 1];
+            const uint4* p4 = reinterpret_cast<const uint4*>(sh.pair_key) + (tid & 1) * (kPairs / 8);
             int above = 0;
-            const float4* p4 = reinterpret_cast<const float4*>(sh.pair_mx);
-#pragma unroll 8
-            for (int j = 0; j < kPairs / 4; ++j) {
-                const float4 o = p4[j];
-                const int at = 4 * j;
-                above += (o.x > mine || (o.x == mine && at < tid)) + (o.y > mine || (o.y == mine && at + 1 < tid)) +
-                         (o.z > mine || (o.z == mine && at + 2 < tid)) + (o.w > mine || (o.w == mine && at + 3 < tid));
+#pragma unroll
+            for (int j = 0; j < kPairs / 8; ++j) {
+                const uint4 o = p4[j];
+                above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
             }
-            if (above == a.top_k - 1) sh.bound = mine;
+            above += __shfl_xor_sync(0xffffffffu, above, 1);
+            if (above == a.top_k - 1)   // both threads of the pair
+                sh.bound = key_value(max(mine & ~(kPairs - 1u), order_key(-INFINITY)));
+            meet();
+            bound = sh.bound;
         }
-        __syncthreads();
-        const float bound = sh.bound;
-        if (tid < kPairs && sh.pair_mx[tid] >= bound) sh.flagged[atomicAdd(&sh.nflagged, 1)] = tid;
+        if (!(tid & 1) && pair >= bound) sh.flagged[atomicAdd(&sh.nflagged, 1)] = tid >> 1;
         auto push = [&](float x, uint32_t index) {
             const int at = atomicAdd(&sh.ncand, 1);
             if (at < kCap) sh.cand[at] = entry_of(x, index);
         };
         if (lone >= 0 && (lone_x < F::kFloor ? F::kFloor : lone_x) >= bound) push(lone_x, lone);
-        __syncthreads();
-        // a warp goes over one pair's vectors: lanes 2i and 2i + 1 its two
-        // threads' vectors of round i
+        meet();
+        // Two threads to a round of a pair's vectors, up to 64 rounds of a pair at
+        // once, and as many pairs at once as that leaves threads for.
         const int nflagged = sh.nflagged;
-        for (int f = warp; f < nflagged; f += kWarps) {
-            const int first = v0 + 2 * sh.flagged[f] + (lane & 1) + (lane >> 1) * kThreads;
-#pragma unroll 4
-            for (int u = first; u < v1; u += 16 * kThreads) {
-                const uint4 x = vec[u];
-                const uint32_t word[4] = {F::floor_word(x.x), F::floor_word(x.y), F::floor_word(x.z), F::floor_word(x.w)};
-                const float top =
-                    F::max_of(F::max_word(F::max_word(word[0], word[1]), F::max_word(word[2], word[3])));
-                if (top >= bound) {
-                    const uint32_t index = head + u * F::kE;
-                    const void* at = vec + u;
+        auto look = [&](const uint4& x, int u) {
+            const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
+            uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < F::kE; ++e) {
-                        const float y = F::at(at, e);
-                        if ((y < F::kFloor ? F::kFloor : y) >= bound) push(y, index + e);
-                    }
+            for (int j = 0; j < 4; ++j) w[j] = F::floor_word(raw[j]);
+            if (F::max_of(F::max_word(F::max_word(w[0], w[1]), F::max_word(w[2], w[3]))) < bound) return;
+            const uint32_t index = head + u * F::kE;
+#pragma unroll
+            for (int e = 0; e < F::kE; ++e) {
+                const float y = F::element(raw, e);
+                if ((y < F::kFloor ? F::kFloor : y) >= bound) push(y, index + e);
+            }
+        };
+        const int rounds = (v1 - v0 + kThreads - 1) / kThreads;
+        int lg = 0;
+        while (lg < 6 && (1 << lg) < rounds) ++lg;
+        const int group = tid >> (lg + 1), groups = kThreads >> (lg + 1);
+        const int r0 = (tid & ((2 << lg) - 1)) >> 1;
+        for (int u0 = v0 + (tid & 1) + r0 * kThreads; u0 < v1; u0 += kThreads << lg) {
+            int f = group;
+            for (; f + 3 * groups < nflagged; f += 4 * groups) {   // four loads in flight
+                uint4 x[4];
+                int u[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[j] = u0 + 2 * sh.flagged[f + j * groups];
+                    x[j] = u[j] < v1 ? vec[u[j]] : empty;
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (u[j] < v1) look(x[j], u[j]);
+            }
+            for (; f < nflagged; f += groups) {
+                const int u = u0 + 2 * sh.flagged[f];
+                if (u < v1) look(vec[u], u);
             }
         }
-        __syncthreads();
+        meet();
         const int n = sh.ncand;
         bad = n > kCap;
         if (!bad)
             for (int i = tid; i < n; i += kThreads) {
                 const uint64_t mine = sh.cand[i];
                 int above = 0;
+#pragma unroll 8
                 for (int j = 0; j < n; ++j) above += sh.cand[j] > mine;
                 if (above < a.top_k) sh.list[above] = mine;
             }
     }
-    __syncthreads();
+    meet();
     Sums r{mx, c, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) {
@@ -536,9 +612,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             sh.sums[3] = r.w;
             sh.bad = bad ? 1.0f : 0.0f;
         }
-        __syncthreads();
-        cluster_arrive_all();
-        cluster_wait_all();
+        meet();
+        cluster_meet();
         if (rank == 0) {
             // every warp adds the parts up for itself, lane l holding part l
             const bool has = lane < static_cast<int>(S);
@@ -569,12 +644,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             }
             if (tid == 0) sh.ncand = 0;
         }
-        __syncthreads();
-        cluster_arrive_all();   // nobody's shared memory is read any more
-        if (rank != 0) {
-            cluster_wait_all();
-            return;
-        }
+        cluster_meet();   // nobody's lists are read any more
+        if (rank != 0) return;
         if (a.top_k > 0) {
             // what reaches the largest of the lists' last entries holds the answer
             uint64_t bound = 0ull;
@@ -584,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
             }
             for (int e = tid; e < static_cast<int>(S) * a.top_k; e += kThreads)
                 if (sh.joined[e] >= bound && sh.joined[e] != 0ull) sh.cand[atomicAdd(&sh.ncand, 1)] = sh.joined[e];
-            __syncthreads();
+            meet();
             const int n = sh.ncand;
             for (int i = tid; i < n; i += kThreads) {
                 const uint64_t mine = sh.cand[i];
@@ -592,9 +663,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
                 for (int j = 0; j < n; ++j) above += sh.cand[j] > mine;
                 if (above < a.top_k) sh.list[above] = mine;
             }
-            __syncthreads();
+            meet();
         }
-        cluster_wait_all();
     }
 
     // not (a <= b) is also true of a NaN
@@ -616,26 +686,88 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobArgs
     }
 }
 
-// CTAs per row: 1 once the rows fill the SMs twice over, else the row is cut
-// into up to 16 parts of at least 2048 logits.
+template <int kType>
+__global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
+    logprobs_kernel(const LogprobArgs a, uint64_t timeout_ns, uint32_t* status) {
+    extern __shared__ __align__(128) uint4 ring[];   // [kStages][kTurn]
+    __shared__ Shared sh;
+    const uint32_t S = cluster_size(), rank = cluster_cta_rank();
+    if (threadIdx.x == kThreads) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), kWarps);
+        }
+        sh.abort = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const WaitCtl wc{timeout_ns, status, &sh.abort};
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int64_t row0 = blockIdx.x / S;
+    const int64_t rows = gridDim.x / S;   // rows in flight; more than one each only where S is 1
+
+    if (threadIdx.x >= kThreads) {
+        if (threadIdx.x == kThreads) {
+            const uint64_t pol = policy_evict_normal();   // what reaches a bound is read again
+            int issued = 0;
+            gemm::Ring<kStages> r(0);
+            bool ok = true;
+            for (int64_t m = row0; m < a.M && ok; m += rows) {
+                const Part<kType> part(a, m, rank, S);
+                for (int n = 0; n < part.turns; ++n, r.step(1)) {
+                    if (issued >= kStages) ok = wait_bounded(smem_u32(&sh.empty[r.slot]), r.phase ^ 1u, wc);
+                    if (!ok) break;
+                    const int v = part.v0 + n * kTurn;
+                    const uint32_t bytes = (part.v1 - v < kTurn ? part.v1 - v : kTurn) * 16u;
+                    const uint32_t bar = smem_u32(&sh.full[r.slot]);
+                    mbar_arrive_expect_tx(bar, bytes);
+                    bulk_load(smem_u32(ring + r.slot * kTurn), part.vec + v, bytes, bar, pol);
+                    ++issued;
+                }
+            }
+            // every copy lands before the CTA may end
+            for (int i = issued - kStages < 0 ? 0 : issued - kStages; i < issued; ++i)
+                gemm::drain_wait(smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, timeout_ns);
+        }
+        if (S > 1) {   // the two meetings of take_row
+            cluster_meet();
+            cluster_meet();
+        }
+        return;
+    }
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int64_t m = row0; m < a.M; m += rows) take_row<kType>(a, m, rank, S, sh, ring, stage, phase, wc);
+}
+
+// CTAs per row: 1 once the rows fill the SMs, else the row is cut into up to
+// 16 parts of at least 2048 logits while their CTAs all run at once.
 int parts_of(int M, int V, int sms) {
     int s = 1;
-    while (s < kMaxCluster && static_cast<int64_t>(M) * s < 2 * sms && V / (2 * s) >= 2048) s *= 2;
+    while (s < kMaxCluster && static_cast<int64_t>(M) * 2 * s <= kCtasPerSm * sms * 3 / 4 && V / (2 * s) >= 2048) s *= 2;
     return s;
 }
 
 template <int kType>
 cudaError_t launch(const LogprobArgs& a, const LaunchCtl& c, cudaStream_t st) {
-    int parts = parts_of(a.M, a.V, c.num_sms);
-    while (static_cast<int64_t>(a.M) * parts > INT32_MAX) parts /= 2;
-    if (parts > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<kType>,
-                                                   cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
+    const int parts = parts_of(a.M, a.V, c.num_sms);
+    const int most = kCtasPerSm * c.num_sms;
+    // A CTA with one part to take needs no more of the ring than its turns (a
+    // part has at most V / parts / kE + 1 vectors); one that runs on into
+    // another row goes round all of it.
+    const int turns = a.V / parts / (kTurn * Fmt<kType>::kE) + 1;
+    const bool one_part = parts > 1 || a.M <= most;
+    const int ring_bytes = (one_part && turns < kStages ? turns : kStages) * kTurn * 16;
+    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<kType>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kStages * kTurn * 16);
+    if (e == cudaSuccess && parts > 8)
+        e = cudaFuncSetAttribute(logprobs_kernel<kType>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.M) * parts);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(parts > 1 ? a.M * parts : a.M < most ? a.M : most));
+    cfg.blockDim = dim3(kThreads + 32);
+    cfg.dynamicSmemBytes = static_cast<size_t>(ring_bytes);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -646,7 +778,7 @@ cudaError_t launch(const LogprobArgs& a, const LaunchCtl& c, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = c.overlap ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<kType>, a);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<kType>, a, c.timeout_ns, c.status);
 }
 
 }  // namespace
