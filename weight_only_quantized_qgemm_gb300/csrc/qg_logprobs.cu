@@ -425,7 +425,8 @@ struct Part {
 
 template <int kType>
 __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32_t rank, uint32_t S, Shared& sh,
-                                         const uint4* ring, int& stage, uint32_t& phase, const WaitCtl& wc) {
+                                         const uint4* ring, bool resident, int& stage, uint32_t& phase,
+                                         const WaitCtl& wc) {
     using F = Fmt<kType>;
     const int tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5;
@@ -546,6 +547,8 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
         meet();
         // Two threads to a round of a pair's vectors, up to 64 rounds of a pair at
         // once, and as many pairs at once as that leaves threads for.
+        // a part that went into the ring without a second turn round it is still there
+        const uint4* from = resident && part.turns <= kStages ? ring - v0 : vec;
         const int nflagged = sh.nflagged;
         auto look = [&](const uint4& x, int u) {
             const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
@@ -573,7 +576,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     u[j] = u0 + 2 * sh.flagged[f + j * groups];
-                    x[j] = u[j] < v1 ? vec[u[j]] : empty;
+                    x[j] = u[j] < v1 ? from[u[j]] : empty;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -581,7 +584,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
             }
             for (; f < nflagged; f += groups) {
                 const int u = u0 + 2 * sh.flagged[f];
-                if (u < v1) look(vec[u], u);
+                if (u < v1) look(from[u], u);
             }
         }
         meet();
@@ -738,7 +741,8 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
     }
     int stage = 0;
     uint32_t phase = 0;
-    for (int64_t m = row0; m < a.M; m += rows) take_row<kType>(a, m, rank, S, sh, ring, stage, phase, wc);
+    for (int64_t m = row0; m < a.M; m += rows) 
+        take_row<kType>(a, m, rank, S, sh, ring, rows >= a.M, stage, phase, wc);
 }
 
 // CTAs per row: 1 once the rows fill the SMs, else the row is cut into up to
