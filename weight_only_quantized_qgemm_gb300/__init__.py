@@ -402,36 +402,34 @@ def qgemm_w8a8(X, W, W_scale, Y=None, workspace=None, stream=None):
 
 
 _dtype_codes = {}
-
-
-def _dtype_code(dtype):
-    """QG_BF16, QG_FP16 or QG_FP32 of a torch dtype, None for any other."""
-    if not _dtype_codes:
-        torch = _torch()
-        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    return _dtype_codes.get(dtype)
-
-
-def _row_ld(t) -> int:
-    """_ld, with the row length for a lone row (whose stride is arbitrary)."""
-    ld = _ld(t)
-    return t.shape[1] if t.shape[0] <= 1 else ld
-
-
 _raw_stream = None
 
 
-def _stream_on(stream, device) -> int:
-    """_stream_ptr for a caller's tensors: the current stream of their device
-    (read without building a stream object: 0.1 us instead of 3 us a call)."""
-    if stream is not None:
-        return _stream_ptr(stream)
+def _lazy():
+    """torch, with what the entry points below look up on every call."""
     global _raw_stream
-    if _raw_stream is None:
-        torch = _torch()
+    torch = _torch()
+    if not _dtype_codes:
+        # the current stream of a device, without building a stream object
+        # (0.1 us instead of 3 us a call)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: int(torch.cuda.current_stream(index).cuda_stream))
-    return _raw_stream(device.index)
+        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})   # QG_BF16, QG_FP16, QG_FP32
+    return torch
+
+
+def _rows(t, what: str):
+    """(rows, columns, row stride) of a 2-D CUDA tensor with unit column
+    stride; a lone row's stride is arbitrary and counts as its length."""
+    if t.dim() != 2:
+        raise ValueError(what + " must be a 2-D tensor")
+    r, c = t.shape
+    ld, step = t.stride()
+    if step != 1 and c > 1:
+        raise ValueError(what + " must have unit stride in its last dimension")
+    if not t.is_cuda:
+        raise ValueError(what + " must be on a CUDA device")
+    return r, c, (ld if r > 1 else c)
 
 
 def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
@@ -443,33 +441,32 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
     int8 [M, K], X_scale float32 [M]).  Xq and X_scale (optional) are written
     in place.
     """
-    torch = _torch()
-    code = _dtype_code(X.dtype)
+    torch = _lazy()
+    code = _dtype_codes.get(X.dtype)
     if code != 0 and code != 1:
         raise TypeError("X must be bfloat16 or float16")
-    ld = _row_ld(X)
-    M, K = X.shape
+    M, K, ld = _rows(X, "X")
     dev = X.device
-    if not X.is_cuda:
-        raise ValueError("X must be on a CUDA device")
     if Xq is None:
         Xq = torch.empty((M, K), dtype=torch.int8, device=dev)
         ldq = K
     else:
         if Xq.dtype != torch.int8:
             raise TypeError("Xq must be int8")
-        if Xq.shape != X.shape or Xq.device != dev:
+        rows, cols, ldq = _rows(Xq, "Xq")
+        if rows != M or cols != K or Xq.device != dev:
             raise ValueError("Xq must be [M, K] on X's device")
-        ldq = _row_ld(Xq)
     if X_scale is None:
         X_scale = torch.empty((M,), dtype=torch.float32, device=dev)
     else:
         if X_scale.dtype != torch.float32 or not X_scale.is_contiguous():
             raise TypeError("X_scale must be contiguous float32")
-        if tuple(X_scale.shape) != (M,) or X_scale.device != dev:
+        if X_scale.shape != (M,) or X_scale.device != dev:
             raise ValueError("X_scale must be [M] on X's device")
-    _check(lib.qg_quantize_act_int8(X.data_ptr(), code, ld, Xq.data_ptr(), ldq, X_scale.data_ptr(), M, K,
-                                    _stream_on(stream, dev)), "qg_quantize_act_int8")
+    st = _raw_stream(dev.index) if stream is None else _stream_ptr(stream)
+    r = lib.qg_quantize_act_int8(X.data_ptr(), code, ld, Xq.data_ptr(), ldq, X_scale.data_ptr(), M, K, st)
+    if r:
+        raise QgemmError(r, "qg_quantize_act_int8")
     return Xq, X_scale
 
 
@@ -483,21 +480,20 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
     float32 [N]; bias (optional): float32 [N].  Y (optional): [M, N] with unit
     column stride, in bfloat16 (the default), float16 or float32 (out_dtype).
     """
-    torch = _torch()
+    torch = _lazy()
     i8, f32 = torch.int8, torch.float32
     if Xq.dtype != i8 or W.dtype != i8:
         raise TypeError("Xq and W must be int8")
     if X_scale.dtype != f32 or W_scale.dtype != f32:
-        raise TypeError("X_scale, W_scale and bias must be float32")
+        raise TypeError("X_scale and W_scale must be float32")
     if not (W.is_contiguous() and X_scale.is_contiguous() and W_scale.is_contiguous()):
-        raise TypeError("W, the scales and bias must be contiguous")
-    ldq = _row_ld(Xq)
-    M, K = Xq.shape
+        raise TypeError("W and the scales must be contiguous")
+    M, K, ldq = _rows(Xq, "Xq")
     N = W.shape[0]
     dev = Xq.device
     if W.shape != (N, K) or X_scale.shape != (M,) or W_scale.shape != (N,):
         raise ValueError("shape mismatch between Xq, X_scale, W and W_scale")
-    if not Xq.is_cuda or W.device != dev or X_scale.device != dev or W_scale.device != dev:
+    if W.device != dev or X_scale.device != dev or W_scale.device != dev:
         raise ValueError("all tensors must be on one CUDA device")
     b = None
     if bias is not None:
@@ -507,22 +503,26 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
             raise ValueError("bias must be [N] on the same device")
         b = bias.data_ptr()
     if Y is None:
-        code = _dtype_code(out_dtype or torch.bfloat16)
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
+        code = _dtype_codes.get(out_dtype)
         if code is None:
             raise TypeError("the output must be bfloat16, float16 or float32")
-        Y = torch.empty((M, N), dtype=out_dtype or torch.bfloat16, device=dev)
+        Y = torch.empty((M, N), dtype=out_dtype, device=dev)
         ldy = N
     else:
-        code = _dtype_code(Y.dtype)
+        code = _dtype_codes.get(Y.dtype)
         if code is None or (out_dtype is not None and Y.dtype != out_dtype):
             raise TypeError("Y must be bfloat16, float16 or float32, as out_dtype says")
-        if Y.shape != (M, N) or Y.device != dev:
+        rows, cols, ldy = _rows(Y, "Y")
+        if rows != M or cols != N or Y.device != dev:
             raise ValueError("Y must be [M, N] on the same device")
-        ldy = _row_ld(Y)
-    st = _stream_on(stream, dev)
+    st = _raw_stream(dev.index) if stream is None else _stream_ptr(stream)
     ws, wsb = _workspace_for(KIND_INT8, M, N, K, workspace, dev, st)
-    _check(lib.qgemm_w8a8_int8(Xq.data_ptr(), ldq, X_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(), b,
-                               Y.data_ptr(), code, ldy, M, N, K, ws, wsb, st), "qgemm_w8a8_int8")
+    r = lib.qgemm_w8a8_int8(Xq.data_ptr(), ldq, X_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(), b,
+                            Y.data_ptr(), code, ldy, M, N, K, ws, wsb, st)
+    if r:
+        raise QgemmError(r, "qgemm_w8a8_int8")
     return Y
 
 
@@ -548,40 +548,43 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
     of -inf and entropy 0; a token outside the vocabulary has -inf; a row with
     a NaN or +inf gives NaN (see include/qgemm.h).
     """
-    torch = _torch()
-    code = _dtype_code(logits.dtype)
+    torch = _lazy()
+    f32, i64 = torch.float32, torch.int64
+    code = _dtype_codes.get(logits.dtype)
     if code is None:
         raise TypeError("logits must be bfloat16, float16 or float32")
-    ld = _row_ld(logits)
-    M, V = logits.shape
+    M, V, ld = _rows(logits, "logits")
     dev = logits.device
-    if not logits.is_cuda or (tokens is not None and tokens.device != dev):
-        raise ValueError("logits and tokens must be on one CUDA device")
     T = ldt = 0
-    tok = token_lp = ent = ids = top = None
+    tok = token_lp = token_p = ent = ent_p = ids = ids_p = top = top_p = None
     if tokens is not None:
-        if tokens.dtype != torch.int64:
+        if tokens.dtype != i64:
             raise TypeError("tokens must be int64")
-        if tokens.dim() not in (1, 2) or tokens.shape[0] != M:
+        if tokens.device != dev:
+            raise ValueError("logits and tokens must be on one CUDA device")
+        shape = tokens.shape
+        if len(shape) not in (1, 2) or shape[0] != M:
             raise ValueError("tokens must be [M] or [M, T]")
-        T = tokens.shape[1] if tokens.dim() == 2 else 1
-        if T > 1 and tokens.stride(1) != 1:
-            tokens = tokens.contiguous()
-        ldt = max(tokens.stride(0), T)
-        if M > 1 and tokens.stride(0) < T:   # an expanded row
+        T = shape[1] if len(shape) == 2 else 1
+        strides = tokens.stride()
+        ldt = strides[0] if M > 1 else T
+        if ldt < T or (T > 1 and strides[1] != 1):   # expanded or transposed
             tokens = tokens.contiguous()
             ldt = T
         tok = tokens.data_ptr()
-        token_lp = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
+        token_lp = torch.empty(shape, dtype=f32, device=dev)
+        token_p = token_lp.data_ptr()
     if entropy:
-        ent = torch.empty((M,), dtype=torch.float32, device=dev)
+        ent = torch.empty((M,), dtype=f32, device=dev)
+        ent_p = ent.data_ptr()
     if top_k > 0:   # a negative one is refused by the library
-        ids = torch.empty((M, top_k), dtype=torch.int64, device=dev)
-        top = torch.empty((M, top_k), dtype=torch.float32, device=dev)
-    _check(lib.qg_logprobs(logits.data_ptr(), code, ld, tok, ldt, T,
-                           token_lp.data_ptr() if token_lp is not None else None,
-                           ent.data_ptr() if entropy else None, top_k, ids.data_ptr() if ids is not None else None,
-                           top.data_ptr() if top is not None else None, M, V, _stream_on(stream, dev)), "qg_logprobs")
+        ids = torch.empty((M, top_k), dtype=i64, device=dev)
+        top = torch.empty((M, top_k), dtype=f32, device=dev)
+        ids_p, top_p = ids.data_ptr(), top.data_ptr()
+    st = _raw_stream(dev.index) if stream is None else _stream_ptr(stream)
+    r = lib.qg_logprobs(logits.data_ptr(), code, ld, tok, ldt, T, token_p, ent_p, top_k, ids_p, top_p, M, V, st)
+    if r:
+        raise QgemmError(r, "qg_logprobs")
     return LogProbs(token_lp, ent, ids, top)
 
 

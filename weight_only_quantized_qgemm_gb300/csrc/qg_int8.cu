@@ -37,6 +37,8 @@
 // share their operands in L2; the tiles that are left are cut over the workers
 // at any K block, and a tile shared by several is summed, in ascending K order
 // of its pieces, by the last to arrive, as in the other kernels.
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -824,8 +826,8 @@ template <int NA, bool kPair>
 cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                            const LaunchCtl& c, cudaStream_t st) {
     using L = I8Layout<NA, kPair>;
-    cudaError_t e =
-        cudaFuncSetAttribute(int8_kernel<NA, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = set_smem_once(configured, int8_kernel<NA, kPair>, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     Params p = gemm::base_params(s, a.Y, a.ldy, a.M, a.N, a.K, nullptr, c);
     p.U = static_cast<long long>(s.T - s.nfull * s.G) * s.KU;   // the tail

@@ -30,6 +30,7 @@
 // SMs are split over a cluster of up to 16 CTAs, whose sums and lists rank 0
 // joins through distributed shared memory (no workspace, no atomics on memory,
 // the same order of sums on every call).
+#include <atomic>
 #include <cstddef>
 
 #include <cuda_bf16.h>
@@ -763,10 +764,10 @@ cudaError_t launch(const LogprobArgs& a, const LaunchCtl& c, cudaStream_t st) {
     const int turns = a.V / parts / (kTurn * Fmt<kType>::kE) + 1;
     const bool one_part = parts > 1 || a.M <= most;
     const int ring_bytes = (one_part && turns < kStages ? turns : kStages) * kTurn * 16;
-    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<kType>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kStages * kTurn * 16);
+    static std::atomic<uint64_t> configured{0}, wide{0};
+    cudaError_t e = set_smem_once(configured, logprobs_kernel<kType>, kStages * kTurn * 16);
     if (e == cudaSuccess && parts > 8)
-        e = cudaFuncSetAttribute(logprobs_kernel<kType>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = set_once(wide, logprobs_kernel<kType>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(parts > 1 ? a.M * parts : a.M < most ? a.M : most));
