@@ -211,21 +211,33 @@ __device__ __forceinline__ void pack16(const float (&v)[16], const float* sx, fl
     }
 }
 
-// Stores COLS packed columns (activation rows m0 ..) of weight row n, two
-// neighbouring weight rows to a 32-bit store: of activation rows m and m + 1
-// the even lane of a pair writes (n, n + 1) of row m and the odd lane (n - 1,
-// n) of row m + 1, which halves the stores of a tile.
+// Stores COLS packed columns (activation rows m0 ..) of weight row n.  pairs:
+// two neighbouring weight rows to a 32-bit store: of activation rows m and
+// m + 1 the even lane of a pair writes (n, n + 1) of row m and the odd lane
+// (n - 1, n) of row m + 1, which halves the stores of a tile.  It needs an even
+// N and row stride and a 4-byte aligned Y; else every value is a store.
 template <int COLS>
-__device__ __forceinline__ void store_packed(const Params& p, int n, int m0, const uint32_t* w) {
-    const int odd = threadIdx.x & 1;
-    const uint32_t sel = odd ? 0x3276u : 0x5410u;
+__device__ __forceinline__ void store_packed(const Params& p, bool pairs, int n, int m0, const uint32_t* w) {
     const int64_t ldy = p.seg[0].ldy;
-    uint16_t* at = static_cast<uint16_t*>(p.seg[0].Y) + (static_cast<int64_t>(m0) + odd) * ldy + (n - odd);
-    const int rows = n < p.N ? p.M - m0 - odd : 0;   // of this lane's; N is even
+    if (pairs) {
+        const int odd = threadIdx.x & 1;
+        const uint32_t sel = odd ? 0x3276u : 0x5410u;
+        uint16_t* at = static_cast<uint16_t*>(p.seg[0].Y) + (static_cast<int64_t>(m0) + odd) * ldy + (n - odd);
+        const int rows = n < p.N ? p.M - m0 - odd : 0;   // of this lane's
+#pragma unroll
+        for (int j = 0; j < COLS / 2; ++j) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 1);
+            if (2 * j < rows) *reinterpret_cast<uint32_t*>(at) = prmt(w[j], other, sel);
+            at += 2 * ldy;
+        }
+        return;
+    }
+    uint16_t* at = static_cast<uint16_t*>(p.seg[0].Y) + static_cast<int64_t>(m0) * ldy + n;
+    const int rows = n < p.N ? p.M - m0 : 0;
 #pragma unroll
     for (int j = 0; j < COLS / 2; ++j) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, w[j], 1);
-        if (2 * j < rows) *reinterpret_cast<uint32_t*>(at) = prmt(w[j], other, sel);
+        if (2 * j < rows) *at = static_cast<uint16_t>(w[j]);
+        if (2 * j + 1 < rows) at[ldy] = static_cast<uint16_t>(w[j] >> 16);
         at += 2 * ldy;
     }
 }
@@ -234,33 +246,21 @@ __device__ __forceinline__ void store_packed(const Params& p, int n, int m0, con
 // in shared memory.
 __device__ __forceinline__ void store16(const Params& p, const Out& o, int n, int m0, const float* sx, float sw, float b,
                                         const float (&v)[16]) {
-    if (o.y_pairs) {
+    if (o.y_type != QG_FP32) {
         uint32_t w[8];
         pack16(v, sx, sw, b, o.y_type, w);
-        store_packed<16>(p, n, m0, w);
+        store_packed<16>(p, o.y_pairs, n, m0, w);
         return;
     }
     float y[16];
     scale16(v, sx, sw, b, y);
-    if (n >= p.N) return;
     const int64_t ldy = p.seg[0].ldy;
-    const int64_t at = static_cast<int64_t>(m0) * ldy + n;
-    const int rows = p.M - m0;
-    if (o.y_type == QG_FP32) {
-        float* Y = static_cast<float*>(p.seg[0].Y) + at;
+    float* at = static_cast<float*>(p.seg[0].Y) + static_cast<int64_t>(m0) * ldy + n;
+    const int rows = n < p.N ? p.M - m0 : 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < rows) Y[j * ldy] = y[j];
-    } else if (o.y_type == QG_BF16) {
-        __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.seg[0].Y) + at;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < rows) Y[j * ldy] = __float2bfloat16_rn(y[j]);
-    } else {
-        __half* Y = static_cast<__half*>(p.seg[0].Y) + at;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < rows) Y[j * ldy] = __float2half_rn(y[j]);
+    for (int j = 0; j < 16; ++j) {
+        if (j < rows) *at = y[j];
+        at += ldy;
     }
 }
 
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
             };
-            if (whole && o.y_pairs) {
+            if (whole && o.y_type != QG_FP32) {
                 // all columns into registers, packed, so that the next tile's
                 // MMAs run under the stores (with one accumulator per pair the
                 // stores held them for 5 us of each tile's 38)
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                     pack16(f, scales_from(c), sw, bias, o.y_type, w + 8 * c);
                 }
                 release();
-                store_packed<L::kEpiCols>(p, n, m0, w);
+                store_packed<L::kEpiCols>(p, o.y_pairs, n, m0, w);
             } else if (whole) {
 #pragma unroll 1
                 for (int c = 0; c < L::kEpiCols / 16; ++c) {

@@ -80,7 +80,7 @@ struct Fmt<QG_FP32> {
 template <>
 struct Fmt<QG_BF16> {
     static constexpr int kE = 8, kSize = 2;
-    static constexpr float kFloor = -1.0003425e30f;   // the bf16 0xF14A
+    static constexpr float kFloor = -0x1.94p99f;   // about -1e30: the bf16 0xF14A
     __device__ static float at(const void* row, int64_t v) {
         return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[v]) << 16);
     }
@@ -199,6 +199,11 @@ __device__ __forceinline__ uint64_t peer_u64(const uint64_t* p, uint32_t rank) {
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(r) : "r"(peer_address(p, rank)) : "memory");
     return r;
 }
+
+// The reference c of logits up to `top`.  Not below that of -kFar: c is then
+// within a few units of top L (its rounding is 2^-24 of it), and a thread or a
+// part with nothing but masks adds 2^-huge = 0 instead of what rounding leaves.
+__device__ __forceinline__ float reference_of(float top) { return ceilf(fmaxf(top, -kFar) * kLog2e); }
 
 // Running sums of one thread (or CTA, or row): maximum, reference c, s and w.
 struct Sums {
@@ -373,7 +378,7 @@ __device__ __forceinline__ void take(const uint4 (&x)[kU], float& mx, float& c, 
     const float top = F::max_of(mw[0]);
     if (top > mx) {
         mx = top;
-        const float c2 = ceilf(top * kLog2e);
+        const float c2 = reference_of(top);
         if (c2 > c) {
             const float d = c - c2;
             const float f = ex2(d);
@@ -484,7 +489,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
     if (lone >= 0) {
         const float x = lone_x < F::kFloor ? F::kFloor : lone_x;   // a NaN passes
         t.mx = fmaxf(t.mx, x);
-        const float c2 = ceilf(x * kLog2e);
+        const float c2 = reference_of(x);
         if (c2 > t.c) t.move_to(c2);
         const float tt = fmaf(x, kLog2e, -t.c);
         const float e = ex2(tt);
@@ -505,7 +510,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
     mx = sh.warp_mx[0];
 #pragma unroll
     for (int j = 1; j < kWarps; ++j) mx = fmaxf(mx, sh.warp_mx[j]);
-    const float c = mx == -INFINITY ? kNoRef : ceilf(mx * kLog2e);   // no logit at all in this CTA's part
+    const float c = reference_of(mx);
     t.move_to(c);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) {
@@ -590,7 +595,9 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
         }
         meet();
         const int n = sh.ncand;
-        bad = n > kCap;
+        // (fewer than asked for in a part that holds them: NaNs, which no bound sees)
+        const int size = (v1 - v0) * F::kE + (rank == 0 ? head : 0) + (rank == S - 1 ? a.V - tail0 : 0);
+        bad = n > kCap || n < (a.top_k < size ? a.top_k : size);
         if (!bad)
             for (int i = tid; i < n; i += kThreads) {
                 const uint64_t mine = sh.cand[i];
@@ -633,7 +640,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             r.mx = top;
-            r.c = ceilf(top * kLog2e);
+            r.c = reference_of(top);
             p.move_to(r.c);
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) {
