@@ -940,7 +940,7 @@ Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int for
     s.max_ctas = static_cast<int>(w * ctas);
     if (w > s.U) w = s.U;
     s.nfull = static_cast<int>(s.T / w);
-    const long long r = s.T - s.nfull * w;
+    long long r = s.T - s.nfull * w;
     long long g = 0;
     *cost = s.nfull * s.KU * tc.unit_ns;
     if (r > 0) {
@@ -961,6 +961,16 @@ Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int for
             g = all;
         }
         *cost += best;
+        // A few rounds of whole tiles on single CTAs: as many workers as keep
+        // all of them busy in every round.  These shapes are bound by memory,
+        // and a last round on part of the SMs does not fill it (32 x 32768 x
+        // 5120: 34.8 us on 152 CTAs, 32.9 on 128; from five rounds on, and on
+        // pairs, which are bound by the tensor cores, it costs up to 1%).
+        if (g == r && ctas == 1 && s.nfull >= 1 && s.nfull <= 3 && forced == 0) {
+            w = up(s.T, s.nfull + 1);
+            s.nfull = static_cast<int>(s.T / w);
+            g = r = s.T - s.nfull * w;
+        }
     }
     s.tail_g = static_cast<int>(g);
     s.G = static_cast<int>(s.nfull > 0 ? w : g);
