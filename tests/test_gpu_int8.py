@@ -262,3 +262,25 @@ def test_refusals():
     assert e.value.code == 3
     with pytest.raises(TypeError):
         q.quantize_act_int8(torch.zeros(4, 64, device=dev))
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 1024, 5120), (48, 1024, 2048), (100, 700, 2048), (400, 1024, 4096)])
+def test_timeout_is_reported_and_the_context_survives(M, N, K):
+    """A weight copy that is never made: every wait runs out, on both CTAs of
+    a pair too, the status says so, and the next call is right."""
+    q = qg()
+    Xq, sx, W, sw, b = _problem(M, N, K, 21)
+    ws = q.Workspace()
+    args = [torch.from_numpy(t).cuda() for t in (Xq, sx, W, sw)]
+    q.qgemm_w8a8_int8(*args, workspace=ws)
+    assert q.last_device_status() == 0
+    q.set_wait_timeout_ns(20_000_000)      # 20 ms
+    q.set_fault_injection(0)               # CTA 0 never loads its first unit
+    try:
+        q.qgemm_w8a8_int8(*args, workspace=ws)
+        assert q.last_device_status() == 5  # QG_ERR_TIMEOUT
+    finally:
+        q.set_fault_injection(-1)
+        q.set_wait_timeout_ns(1_000_000_000)
+    ws.reset()
+    _check(_call(q, Xq, sx, W, sw, b, torch.float32, ws=ws), Xq, sx, W, sw, b, torch.float32)

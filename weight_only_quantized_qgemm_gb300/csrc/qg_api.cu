@@ -163,9 +163,9 @@ int table_lookup(int kind, int M, int N, int K) {
 }
 
 // The schedule of a shape on `sms` SMs, with `forced` > 0 a dispatch-table grid.
-Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
+Int8Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
     if (kind == QG_KIND_INT8) return int8_schedule(M, N, K, sms, forced);
-    Schedule s;
+    Int8Schedule s;
     s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : M <= 16 ? 16 : 32;
     // W8A8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
     s.T = (N + 127) / 128 * (kind == QG_KIND_W8A8 ? (M + s.nmma - 1) / s.nmma : 1);
@@ -212,7 +212,7 @@ Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
 // CTAs of the launch per G of the schedule (2 where G counts CTA pairs).
 int schedule_ctas(int kind, const Schedule& s) { return kind == QG_KIND_INT8 ? int8_ctas(s.nmma) : 1; }
 
-Schedule choose_schedule(int kind, int M, int N, int K, int sms) {
+Int8Schedule choose_schedule(int kind, int M, int N, int K, int sms) {
     return schedule_for(kind, M, N, K, sms, table_lookup(kind, M, N, K));
 }
 
@@ -229,7 +229,7 @@ constexpr int kCacheWays = 8;
 struct SchedEntry {
     int kind = -1, M = 0, N = 0, K = 0, sms = 0;
     uint64_t gen = 0;
-    Schedule s;
+    Int8Schedule s;   // a plain Schedule for the other kinds
     size_t ws = 0;
 };
 
@@ -251,7 +251,7 @@ const SchedEntry& cached_schedule(int kind, int M, int N, int K, int sms) {
     e.gen = gen;
     e.s = choose_schedule(kind, M, N, K, sms);
     e.ws = kind == QG_KIND_W8A8   ? w8a8_workspace_bytes(e.s, schedule_splits(e.s))
-           : kind == QG_KIND_INT8 ? int8_workspace_bytes(e.s, M, K, e.s.split)
+           : kind == QG_KIND_INT8 ? int8_workspace_bytes(e.s, M, K)
                                   : workspace_bytes_uncached(e.s);
     return e;
 }
@@ -750,7 +750,7 @@ qg_status qgemm_w8a8_int8(const int8_t* Xq, int64_t ldxq, const float* X_scale, 
     a.K = K;
     if (K == 0) return launch_int8_bias_rows(a, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
     const SchedEntry& se = cached_schedule(QG_KIND_INT8, M, N, K, d->sms);
-    const Schedule s = se.s;
+    const Int8Schedule s = se.s;
     if (se.ws > 0 && (!workspace || workspace_bytes_ < se.ws || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return QG_ERR_WORKSPACE;
     a.ws = se.ws > 0 ? workspace : nullptr;

@@ -37,13 +37,13 @@
 // share their operands in L2; the tiles that are left are cut over the workers
 // at any K block, and a tile shared by several is summed, in ascending K order
 // of its pieces, by the last to arrive, as in the other kernels.
-#include <atomic>
-
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "qg_gemm.cuh"
 #include "qg_int8.h"
+#include "qg_launch.h"
+#include "qg_pair.cuh"
 
 namespace qg {
 namespace {
@@ -439,14 +439,15 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 }
                 issued = i + 1;
             }
-            // a unit whose MMAs are complete has its copies; after a wait that
-            // gave up some never run, and the drain gives up as well
-            for (int i = issued - kSlots < 0 ? 0 : issued - kSlots; i < issued; ++i)
-                gemm::drain_wait(ofree(i % kSlots), (i / kSlots) & 1, p.timeout_ns);
+            // a unit whose MMAs are complete has its copies, and those before it
+            // theirs; after a wait that gave up they never run, and the drain
+            // gives up as well
+            if (issued > 0)
+                gemm::drain_wait(ofree((issued - 1) % kSlots), ((issued - 1) / kSlots) & 1, p.timeout_ns);
         }
     } else if (warp == kWarpMma && leader) {
         const bool elected = elect_one();
-        constexpr uint32_t idesc = idesc_f16(NA, false, 128 * L::kCtas);
+        constexpr uint32_t idesc = kPair ? idesc_f16_pair(NA) : idesc_f16(NA, false);
         const uint64_t dx0 = smem_desc_sw128(base + L::kXOff);
         auto wait = [&](uint32_t bar, uint32_t parity) {
             if constexpr (kPair) return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, wc)) != 0;
@@ -861,7 +862,7 @@ __global__ void bias_rows_kernel(const float* bias, void* Y, int64_t ldy, int y_
 }
 
 template <int NA, bool kPair>
-cudaError_t launch_int8_na(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
+cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                            const LaunchCtl& c, cudaStream_t st) {
     using L = I8Layout<NA, kPair>;
     static std::atomic<uint64_t> configured{0};
@@ -927,8 +928,8 @@ struct TileCost {
 constexpr TileCost kTiles[] = {
     {16, 300, 4000, 7500}, {32, 310, 4000, 7500}, {64, 340, 7500, 10500}, {128, 350, 7500, 14500}, {256, 560, 9500, 24000}};
 
-Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int forced, long long* cost) {
-    Schedule s;
+Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int forced, long long* cost) {
+    Int8Schedule s;
     s.nmma = tc.rows;
     const int ctas = int8_ctas(s.nmma);
     const long long tn = (N + 128ll * ctas - 1) / (128 * ctas);
@@ -980,12 +981,12 @@ Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int for
     return s;
 }
 
-Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
+Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
     long long cost = 0, wide_cost = 0;
     const int t = M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : 3;
-    const Schedule s = schedule_with(kTiles[t], M, N, K, sms, forced, &cost);
+    const Int8Schedule s = schedule_with(kTiles[t], M, N, K, sms, forced, &cost);
     if (M <= 128) return s;
-    const Schedule wide = schedule_with(kTiles[4], M, N, K, sms, forced, &wide_cost);
+    const Int8Schedule wide = schedule_with(kTiles[4], M, N, K, sms, forced, &wide_cost);
     return wide_cost < cost ? wide : s;
 }
 
@@ -994,13 +995,13 @@ size_t int8_expanded_bytes(const Schedule& s, int M, int K) {
     return (static_cast<size_t>(M) * K * 2 + 255) & ~static_cast<size_t>(255);
 }
 
-size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split) {
-    const size_t part = split ? static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 2 * 128 * s.nmma * sizeof(float) : 0;
+size_t int8_workspace_bytes(const Int8Schedule& s, int M, int K) {
+    const size_t part = s.split ? static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 2 * 128 * s.nmma * sizeof(float) : 0;
     const size_t x = int8_expanded_bytes(s, M, K);
     return part + x > 0 ? kInt8CounterBytes + x + part : 0;
 }
 
-cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
+cudaError_t launch_int8(const Int8Args& a, const Int8Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                         const LaunchCtl& c, cudaStream_t st) {
     if (static_cast<size_t>(s.G) * int8_ctas(s.nmma) * 8 * kInt8Slices * sizeof(uint32_t) > kInt8CounterBytes)
         return cudaErrorInvalidValue;

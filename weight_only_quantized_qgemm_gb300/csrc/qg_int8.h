@@ -23,9 +23,18 @@ struct Int8Args {
 // rows, and the schedule's G then counts pairs.
 inline int int8_ctas(int tile_rows) { return tile_rows > 64 ? 2 : 1; }
 
+// The work of a shape: G workers (CTAs or CTA pairs) run nfull whole tiles
+// each, then tail_g of them share the units of the other T - nfull G tiles;
+// split: a tile is cut.  (The other kinds' schedules leave these at 0.)
+struct Int8Schedule : Schedule {
+    int nfull = 0;
+    int tail_g = 0;
+    bool split = false;
+};
+
 // The schedule of a shape on `sms` SMs (forced > 0: with that many CTAs, the
 // tail cut evenly over all of them).
-Schedule int8_schedule(int M, int N, int K, int sms, int forced);
+Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced);
 
 // Workspace of a schedule (s.nmma = the tile's activation rows): the arrival
 // counters (kInt8CounterBytes, zero between calls, at offset 0 for every
@@ -36,13 +45,13 @@ constexpr size_t kInt8CounterBytes = 32768;
 constexpr int kInt8Slices = 2;   // counters of an epilogue warp of a split tile
 inline bool int8_inline_x(const Schedule& s) { return s.nmma <= 16; }
 size_t int8_expanded_bytes(const Schedule& s, int M, int K);
-size_t int8_workspace_bytes(const Schedule& s, int M, int K, bool split);
+size_t int8_workspace_bytes(const Int8Schedule& s, int M, int K);
 
 // tmW: the weight map ([N, K] bytes, 128 x 128 boxes, 128-byte swizzle);
 // tmX: the expanded activations ([M, K] FP16, boxes of 64 K x the rows of a
 // tile that one CTA holds, s.nmma / int8_ctas), not used where the GEMM expands
 // them itself.
-cudaError_t launch_int8(const Int8Args& a, const Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
+cudaError_t launch_int8(const Int8Args& a, const Int8Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                         const LaunchCtl& c, cudaStream_t st);
 cudaError_t launch_quantize_int8(const void* X, int x_type, int64_t ldx, int8_t* Xq, int64_t ldxq, float* Sx, int M,
                                  int K, const LaunchCtl& c, cudaStream_t st);

@@ -2,7 +2,6 @@
 // units.  Not installed; not part of the public header.
 #pragma once
 
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -24,11 +23,6 @@ struct Schedule {
     int G = 0;        // CTAs
     int nmma = 16;    // MMA N (16 or 32)
     int max_ctas = 0; // CTAs the device holds at once (one per SM): bounds G
-    // INT8 schedules only (qg_int8.cu): G workers run nfull whole tiles each,
-    // then tail_g of them share the units of the other T - nfull G tiles
-    int nfull = 0;
-    int tail_g = 0;
-    bool split = false;   // the tail cuts a tile
 };
 
 // Workspace layout for a schedule that splits tiles: split-K partial sums
@@ -121,25 +115,6 @@ uint32_t* device_status_ptr();
 // True when calls launch with programmatic stream serialization
 // (qg_set_weight_prefetch_overlap).
 bool overlap_enabled();
-
-// Sets a kernel's attribute once per device (`done`: a bit for each of the
-// first 64, set after the call succeeded; a concurrent first call sets it twice,
-// which is harmless).
-template <class Kernel>
-cudaError_t set_once(std::atomic<uint64_t>& done, Kernel kernel, cudaFuncAttribute attribute, int value) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, attribute, value);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-    return e;
-}
-template <class Kernel>
-cudaError_t set_smem_once(std::atomic<uint64_t>& done, Kernel kernel, int bytes) {
-    return set_once(done, kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
 
 inline bool aligned_16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

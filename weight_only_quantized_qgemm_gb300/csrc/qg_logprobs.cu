@@ -30,14 +30,15 @@
 // SMs are split over a cluster of up to 16 CTAs, whose sums and lists rank 0
 // joins through distributed shared memory (no workspace, no atomics on memory,
 // the same order of sums on every call).
-#include <atomic>
 #include <cstddef>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "qg_gemm.cuh"
+#include "qg_launch.h"
 #include "qg_logprobs.h"
+#include "qg_pair.cuh"
 
 namespace qg {
 namespace {
