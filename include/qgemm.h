@@ -87,11 +87,11 @@ enum { QG_BF16 = 0, QG_FP16 = 1, QG_FP32 = 2 };
  * partial sums): a workspace serves either QG_KIND_W8A8 calls or calls of
  * the other kinds, not both, unless it is zero-filled again in between.
  * QG_KIND_INT8 has a layout of its own too: 32768 bytes of arrival counters
- * (at the front for every shape), the activations expanded to FP16 (M > 16:
+ * (at the front for every shape), the activations expanded to FP16 (R > 16:
  * 2 M K bytes rounded up to 256), then the partial sums of a schedule that splits
- * tiles (two slots of 512 R bytes for each CTA, R = the rows of a tile: 16,
- * 32, 64 or 128); its workspace serves INT8 calls of any shape, and no other
- * kind.
+ * tiles (two slots of 512 R bytes for each CTA), with R the activation rows
+ * of the shape's tiles (qg_int8_tile_rows); its workspace serves INT8 calls of
+ * any shape, and no other kind.
  */
 size_t qg_workspace_bytes(int kind, int M, int N, int K);
 
@@ -339,10 +339,11 @@ qg_status qg_quantize_act_int8(const void *X, int x_type, int64_t ldx, int8_t *X
  *            (or zeros) to every row
  *   workspace  at least qg_workspace_bytes(QG_KIND_INT8, M, N, K) bytes,
  *            zero-filled before its first use, 256-byte aligned (may be NULL
- *            when that is 0; every call with M > 16 needs one, which holds
- *            the activations as FP16)
- * A call with M <= 16 launches one kernel, any other two: the expansion of
- * the activations, and the GEMM, whose weight stream starts under it.
+ *            when that is 0)
+ * The output is tiled in 128 or 256 channels x 16, 32, 64, 128 or 256 tokens,
+ * as the schedule rule finds cheapest for the shape.  With tiles of 16 tokens
+ * a call launches one kernel, else two: the expansion of the activations to
+ * FP16 in the workspace, and the GEMM, whose weight stream starts under it.
  */
 qg_status qgemm_w8a8_int8(const int8_t *Xq, int64_t ldxq, const float *X_scale,
                           const int8_t *W, const float *W_scale, const float *bias,
@@ -350,6 +351,13 @@ qg_status qgemm_w8a8_int8(const int8_t *Xq, int64_t ldxq, const float *X_scale,
                           int M, int N, int K,
                           void *workspace, size_t workspace_bytes,
                           struct CUstream_st *stream);
+
+/*
+ * The tokens of a tile (16, 32, 64, 128 or 256) that the schedule rule picks
+ * for a QG_KIND_INT8 shape on a device with `sms` SMs, whatever the dispatch
+ * table holds (host only, no CUDA call; 0 for invalid arguments).
+ */
+int qg_int8_tile_rows(int M, int N, int K, int sms);
 
 /*
  * Log probabilities of given tokens, entropy and top alternatives over rows

@@ -80,6 +80,43 @@ def test_gemm_matches_64_bits(M, N, K, dtype):
     _check(y, Xq, sx, W, sw, b if (M + N) % 2 else None, dtype)
 
 
+WIDTHS = [
+    # M, N, K, tokens of a tile: every width of the kernel, with ragged edges on
+    # every side, few and many tiles a CTA, split tails and odd channel counts
+    (17, 19001, 1040, 32), (24, 49155, 1040, 32), (31, 5001, 5120, 32), (50, 9001, 4112, 32),
+    (64, 17408, 400, 64), (50, 15001, 2064, 64), (172, 4218, 1456, 64), (40, 17283, 1040, 64),
+    (65, 17283, 1040, 128), (128, 17408, 1552, 128), (200, 9000, 2064, 128), (384, 17155, 528, 128),
+    (1000, 2051, 4112, 128), (256, 17283, 1040, 256), (255, 5120, 17408, 256), (513, 17283, 2064, 256),
+    (1000, 5001, 4112, 256), (700, 6001, 1040, 256),
+]
+
+
+@pytest.mark.parametrize("M,N,K,rows", WIDTHS)
+@pytest.mark.parametrize("dtype", list(OUT), ids=["bf16", "fp16", "fp32"])
+def test_every_tile_width(M, N, K, rows, dtype):
+    q = qg()
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert q.int8_tile_rows(M, N, K, 152) == rows
+    if sms != 152:
+        pytest.skip("the widths are those of 152 SMs")
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    Xq = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    W = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.rand(M, generator=g, device="cuda") * 0.05 + 0.003
+    sw = torch.rand(N, generator=g, device="cuda") * 1e-3 + 1e-4
+    b = torch.randn(N, generator=g, device="cuda") if N % 2 else None
+    pad = torch.full((M, N + 6), float("nan"), dtype=dtype, device="cuda")
+    q.qgemm_w8a8_int8(Xq, sx, W, sw, bias=b, Y=pad[:, :N])
+    assert q.last_device_status() == 0
+    assert bool(torch.isnan(pad[:, N:]).all())
+    P = (Xq.double() @ W.double().t()) * sx.double()[:, None] * sw.double()[None, :]   # integers below 2^53: exact
+    ref = P if b is None else P + b.double()[None, :]
+    tol = U * (2 * P.abs() + (0.0 if b is None else b.double().abs()[None, :])) * (1 + 2.0 ** -10)
+    tol = tol + OUT[dtype] * (ref.abs() + tol) + (2.0 ** -25 if dtype == torch.float16 else 1e-38)
+    bad = (pad[:, :N].double() - ref).abs() > tol
+    assert not bool(bad.any()), int(bad.sum())
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 130, 1024), (40, 256, 1024), (300, 256, 1024)])
 def test_integers_are_exact(M, N, K):
     """With unit scales and 32-bit output the result is the integer product
@@ -251,7 +288,8 @@ def test_refusals():
             q.qgemm_w8a8_int8(Xq, bad.get("sx", sx), bad.get("W", W), bad.get("sw", sw), bias=bad.get("b"),
                               out_dtype=bad.get("dt"))
     with pytest.raises(q.QgemmError) as e:
-        q.qgemm_w8a8_int8(torch.zeros(40, 64, dtype=torch.int8, device=dev), torch.ones(40, device=dev), W, sw,
+        q.qgemm_w8a8_int8(torch.zeros(1, 5120, dtype=torch.int8, device=dev), torch.ones(1, device=dev),
+                          torch.zeros(1024, 5120, dtype=torch.int8, device=dev), torch.ones(1024, device=dev),
                           workspace=torch.zeros(256, dtype=torch.uint8, device=dev))
     assert e.value.code == 6
     with pytest.raises(q.QgemmError) as e:   # K % 16

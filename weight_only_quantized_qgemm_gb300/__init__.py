@@ -47,7 +47,7 @@ __all__ = [
     "debug_schedule", "tune_fp8", "tune_lut3", "workspace_bytes_max", "qgemm_bf16", "KIND_BF16", "KIND_FP8_BLOCK", "KIND_LUT3", "STATUS",
     "quantize_act_e4m3", "qgemm_w8a8_block", "qgemm_w8a8", "KIND_W8A8", "MAX_M_W8A8",
     "tune_bf16", "tune_w8a8", "workspace_bytes_max_w8a8",
-    "quantize_act_int8", "qgemm_w8a8_int8", "KIND_INT8", "logprobs", "LogProbs", "MAX_TOP_K",
+    "quantize_act_int8", "qgemm_w8a8_int8", "int8_tile_rows", "KIND_INT8", "logprobs", "LogProbs", "MAX_TOP_K",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -103,6 +103,7 @@ _SIGS = {
     "qg_dispatch_get": (_I, [_I, _I, _I, _I]),
     "qg_dispatch_rule": (_I, [_I, _I, _I, _I, _I]),
     "qg_dispatch_clear": (None, []),
+    "qg_int8_tile_rows": (_I, [_I, _I, _I, _I]),
     "qg_workspace_bytes_max": (_S, [_I]),
     "qg_workspace_bytes_max_w8a8": (_S, [_I, _I]),
     "qg_tune_bf16": (_I, [_P, _L, _P, _I, _P, _L, _P, _I, _I, _I, _P, _S, _I, _P, _P, _P]),
@@ -524,6 +525,13 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
     if r:
         raise QgemmError(r, "qgemm_w8a8_int8")
     return Y
+
+
+def int8_tile_rows(M: int, N: int, K: int, sms: int) -> int:
+    """The tokens of a tile that the schedule rule of :func:`qgemm_w8a8_int8`
+    picks for this shape on a device with `sms` SMs (host only; 0 for invalid
+    arguments)."""
+    return int(lib.qg_int8_tile_rows(M, N, K, sms))
 
 
 MAX_TOP_K = 32

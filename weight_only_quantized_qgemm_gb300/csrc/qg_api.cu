@@ -965,6 +965,11 @@ int qg_dispatch_rule(int kind, int M, int N, int K, int sms) {
     return s.G * schedule_ctas(kind, s);
 }
 
+int qg_int8_tile_rows(int M, int N, int K, int sms) {
+    if (M < 1 || M > max_m(QG_KIND_INT8) || N < 1 || K < 1 || sms < 1) return 0;
+    return int8_schedule(M, N, K, sms, 0).nmma;
+}
+
 void qg_dispatch_clear(void) {
     {
         std::lock_guard<std::mutex> lk(g_table_mu);

@@ -904,29 +904,35 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
 
 }  // namespace
 
-// The cost of a schedule is the time of its busiest worker, in nanoseconds of
-// units (a tile x 128 of K) and of what a split adds.  The whole tiles cost
-// floor(T / workers) tiles; for the tail of r tiles the rule takes the cheapest
-// of
+// The cost of a schedule is the time of its busiest worker, in nanoseconds:
+// what every call takes, units (a tile x 128 of K), and what a split adds.  The
+// whole tiles cost floor(T / workers) tiles; for the tail of r tiles the rule
+// takes the cheapest of
 //   - one worker a tile: KU units
 //   - k = floor(workers / r) equal pieces of every tile: ceil(KU / k) units and
 //     a split (storing, counting and summing partial results)
 //   - all workers, pieces that straddle tiles: ceil(r KU / workers) units and
 //     two splits a worker
-// A tile has the fewest activation rows that take the batch, up to 64; beyond,
-// 128 or 256, whichever costs less: wide tiles read fewer weights and
-// activations per product, but split at a higher price.  Measured (whole tiles
-// / equal pieces / straddling): 256 x 5120 x 17408 at 128 rows 52.8 / - / 44.7
-// us, at 256 rows 81.0 / 42.4 / 49.8; 128 x 6144 x 5120 at 128 rows 19.3 / 17.6
-// / 22.7, at 256 rows 28.9 / 23.5 / 31.6; 1 x 1024 x 5120 at 16 rows 15.9 / 8.4
-// / 8.8.
+// and over the tile widths the one that costs least: wide tiles read fewer
+// weights and activations per product, narrow ones spread a small product over
+// more SMs, split at a lower price, and the narrowest saves a launch (2 us of
+// the constant: the host's time, which bounds small calls).  Measured, whole
+// tiles / equal pieces / straddling: 256 x 5120 x 17408 at 128 rows 52.8 / - /
+// 44.7 us, at 256 rows 81.0 / 42.4 / 49.8; 128 x 6144 x 5120 at 128 rows 19.3 /
+// 17.6 / 22.7, at 256 rows 28.9 / 23.5 / 31.6; 1 x 1024 x 5120 at 16 rows 15.9 /
+// 8.4 / 8.8.  And by width (16, 32, 64, 128, 256 rows): 100 x 1000 x 1008 6.5 /
+// 7.1 / 7.7 / 8.8 / 11.2 us, 172 x 4218 x 1456 15.3 / 12.4 / 9.8 / 10.8 / 13.9, 64
+// x 5120 x 5120 21.1 / 18.0 / 15.5 / 17.2 / 23.3.
 constexpr int kMostPieces = 8;
 struct TileCost {
     int rows;
-    long long unit_ns, split_ns, straddle_ns;
+    long long call_ns, unit_ns, split_ns, straddle_ns;
 };
-constexpr TileCost kTiles[] = {
-    {16, 300, 4000, 7500}, {32, 310, 4000, 7500}, {64, 340, 7500, 10500}, {128, 350, 7500, 14500}, {256, 560, 9500, 24000}};
+constexpr TileCost kTiles[] = {{16, 4000, 305, 4000, 7500},
+                               {32, 6300, 310, 4000, 7500},
+                               {64, 6500, 340, 6500, 10500},
+                               {128, 7700, 350, 7500, 14500},
+                               {256, 8500, 560, 9500, 24000}};
 
 Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int forced, long long* cost) {
     Int8Schedule s;
@@ -943,7 +949,7 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
     s.nfull = static_cast<int>(s.T / w);
     long long r = s.T - s.nfull * w;
     long long g = 0;
-    *cost = s.nfull * s.KU * tc.unit_ns;
+    *cost = tc.call_ns + s.nfull * s.KU * tc.unit_ns;
     if (r > 0) {
         auto up = [](long long a, long long b) { return (a + b - 1) / b; };
         const long long all = w < r * s.KU ? w : r * s.KU;
@@ -975,19 +981,27 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
     }
     s.tail_g = static_cast<int>(g);
     s.G = static_cast<int>(s.nfull > 0 ? w : g);
-    // splits: some worker's part of the tail begins inside a tile
-    s.split = false;
-    for (long long c = 1; c < g && !s.split; ++c) s.split = c * (r * s.KU) / g % s.KU != 0;
     return s;
 }
 
 Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
-    long long cost = 0, wide_cost = 0;
-    const int t = M <= 16 ? 0 : M <= 32 ? 1 : M <= 64 ? 2 : 3;
-    const Int8Schedule s = schedule_with(kTiles[t], M, N, K, sms, forced, &cost);
-    if (M <= 128) return s;
-    const Int8Schedule wide = schedule_with(kTiles[4], M, N, K, sms, forced, &wide_cost);
-    return wide_cost < cost ? wide : s;
+    Int8Schedule best;
+    long long least = 0;
+    int narrower = 0;   // rows of the next narrower tile
+    for (const TileCost& tc : kTiles) {
+        if (narrower >= M) break;   // the narrower one takes the batch as it is
+        narrower = tc.rows;
+        long long cost = 0;
+        const Int8Schedule s = schedule_with(tc, M, N, K, sms, forced, &cost);
+        if (best.T == 0 || cost < least) {
+            best = s;
+            least = cost;
+        }
+    }
+    // splits: some worker's part of the tail begins inside a tile
+    const long long units = (best.T - static_cast<long long>(best.nfull) * best.G) * best.KU;
+    for (long long c = 1; c < best.tail_g && !best.split; ++c) best.split = c * units / best.tail_g % best.KU != 0;
+    return best;
 }
 
 size_t int8_expanded_bytes(const Schedule& s, int M, int K) {
