@@ -119,6 +119,7 @@ struct Out {
     int tn_count, tm_count;   // weight tiles, activation row blocks
     int workers;              // CTAs or CTA pairs
     int nfull;                // whole tiles each worker runs before its part of the tail
+    int early;                // weights may be read before the preceding grid is done
     int tail_q, tail_r;       // the tail's units = tail_q G + tail_r
     // where worker c's part of the tail begins: floor(c U / G), in 32 bits
     __device__ int tail_begin(const Params& p, int c) const { return c * tail_q + c * tail_r / p.G; }
@@ -345,6 +346,9 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         Walk cur(p, o, worker, u0);
         Ring<kWStages> rw(0);
         int issued = 0;
+        // without an expansion kernel in front the preceding grid may still be
+        // writing the weights, unless the caller says it does not
+        if (L::kInlineX && !o.early) grid_dependency_wait();
         auto load_w = [&]() {
             if (skipped(issued)) return;
             mbar_arrive_expect_tx(wfull(rw.slot), L::kWBytes);
@@ -898,20 +902,21 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
     const int y_pairs = a.y_type != QG_FP32 && a.N % 2 == 0 && a.ldy % 2 == 0 &&
                         (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
     const Out o{a.Xq, a.ldxq, a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull,
+                c.overlap ? 1 : 0,
                 p.G > 0 ? static_cast<int>(p.U / p.G) : 0, p.G > 0 ? static_cast<int>(p.U % p.G) : 0};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
     cfg.blockDim = dim3(L::kThreads);
     cfg.dynamicSmemBytes = L::kSmemBytes;
     cfg.stream = st;
-    // always overlapped with the expansion kernel in front, where there is one
-    // (it is part of this call): the weight stream starts under it
+    // Always launched ahead.  Behind the expansion kernel, which is part of this
+    // call, the weight stream starts at once; without one the kernel sets itself
+    // up under the end of the preceding grid, but touches no memory before that
+    // is done (unless the caller allows it for the weights).
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (!L::kInlineX || c.overlap) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    }
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
     if (kPair) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = 2;
