@@ -31,6 +31,7 @@ struct DeviceInfo {
     std::once_flag once;
     int sms = 0;
     uint32_t* status = nullptr;
+    int clusters[kMostClusterPieces + 1] = {};   // of INT8 pairs (int8_cluster_capacity)
     cudaError_t err = cudaSuccess;
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -44,6 +45,7 @@ DeviceInfo* device_info() {
         d->err = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev);
         if (d->err == cudaSuccess)
             d->err = cudaGetSymbolAddress(reinterpret_cast<void**>(&d->status), g_status_word);
+        if (d->err == cudaSuccess) int8_cluster_capacity(d->clusters);
     });
     return d->err == cudaSuccess ? d : nullptr;
 }
@@ -163,8 +165,8 @@ int table_lookup(int kind, int M, int N, int K) {
 }
 
 // The schedule of a shape on `sms` SMs, with `forced` > 0 a dispatch-table grid.
-Int8Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
-    if (kind == QG_KIND_INT8) return int8_schedule(M, N, K, sms, forced);
+Int8Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced, const int* clusters) {
+    if (kind == QG_KIND_INT8) return int8_schedule(M, N, K, sms, forced, clusters);
     Int8Schedule s;
     s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : M <= 16 ? 16 : 32;
     // W8A8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
@@ -213,7 +215,8 @@ Int8Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced) {
 int schedule_ctas(int kind, const Schedule& s) { return kind == QG_KIND_INT8 ? int8_ctas(s.nmma) : 1; }
 
 Int8Schedule choose_schedule(int kind, int M, int N, int K, int sms) {
-    return schedule_for(kind, M, N, K, sms, table_lookup(kind, M, N, K));
+    const DeviceInfo* d = device_info();
+    return schedule_for(kind, M, N, K, sms, table_lookup(kind, M, N, K), d ? d->clusters : int8_nominal_clusters(0));
 }
 
 // True when some tile's units are spread over more than one CTA.
@@ -961,13 +964,13 @@ int qg_dispatch_get(int kind, int M, int N, int K) {
 
 int qg_dispatch_rule(int kind, int M, int N, int K, int sms) {
     if (max_m(kind) == 0 || M < 1 || M > max_m(kind) || N < 1 || K < 1 || sms < 1) return 0;
-    const Schedule s = schedule_for(kind, M, N, K, sms, 0);
+    const Schedule s = schedule_for(kind, M, N, K, sms, 0, int8_nominal_clusters(sms));
     return s.G * schedule_ctas(kind, s);
 }
 
 int qg_int8_tile_rows(int M, int N, int K, int sms) {
     if (M < 1 || M > max_m(QG_KIND_INT8) || N < 1 || K < 1 || sms < 1) return 0;
-    return int8_schedule(M, N, K, sms, 0).nmma;
+    return int8_schedule(M, N, K, sms, 0, int8_nominal_clusters(sms)).nmma;
 }
 
 void qg_dispatch_clear(void) {

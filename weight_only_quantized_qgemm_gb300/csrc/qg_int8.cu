@@ -119,6 +119,7 @@ struct Out {
     int tn_count, tm_count;   // weight tiles, activation row blocks
     int workers;              // CTAs or CTA pairs
     int nfull;                // whole tiles each worker runs before its part of the tail
+    int pieces;               // kClu: the pairs that share a tile
     int early;                // weights may be read before the preceding grid is done
     int tail_q, tail_r;       // the tail's units = tail_q G + tail_r
     // where worker c's part of the tail begins: floor(c U / G), in 32 bits
@@ -276,7 +277,15 @@ __device__ __forceinline__ float4* part_slot(const Params& p, int cta, int which
     return reinterpret_cast<float4*>(p.part) + (static_cast<size_t>(cta) * 2 + which) * (NA / 4) * 128;
 }
 
-template <int NA, bool kPair>
+// Stores and loads of the partial sums that the CTAs of a cluster exchange.
+__device__ __forceinline__ void st_cluster(uint32_t mapped, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mapped), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
+}
+
+// kClu: o.pieces pairs of one cluster run equal pieces of a tile's K range and
+// sum them through distributed shared memory.
+template <int NA, bool kPair, bool kClu>
 __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p,
                 const Out o) {
@@ -303,12 +312,22 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
+    static_assert(!kClu || kPair, "clusters are of pairs");
     // the units of a worker: a CTA, or a pair (both CTAs walk the same ones)
     const int worker = cta / L::kCtas;
-    const uint32_t rank = kPair ? cluster_cta_rank() : 0u;
+    const uint32_t crank = kPair ? cluster_cta_rank() : 0u;
+    const uint32_t rank = crank & 1u;         // in the pair
+    const uint32_t lead = crank - rank;       // the pair's leader's place in the cluster
     const bool leader = rank == 0;
-    const int u0 = worker < p.G ? o.tail_begin(p, worker) : 0;
-    const int u1 = worker < p.G ? o.tail_begin(p, worker + 1) : 0;
+    int u0, u1;
+    if constexpr (kClu) {
+        const int tile = worker / o.pieces, piece = worker - tile * o.pieces;
+        u0 = tile * p.KB + piece * p.KB / o.pieces;
+        u1 = tile * p.KB + (piece + 1) * p.KB / o.pieces;
+    } else {
+        u0 = worker < p.G ? o.tail_begin(p, worker) : 0;
+        u1 = worker < p.G ? o.tail_begin(p, worker + 1) : 0;
+    }
     const int nunits = o.nfull * p.KB + u1 - u0;
     const WaitCtl wc{p.timeout_ns, p.status, abort_flag};
 
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 const int m0 = cur.tm * NA + static_cast<int>(rank) * L::kXRows;
                 if (leader) mbar_arrive_expect_tx(ofull(ro.slot), L::kXSlot * L::kCtas);
                 if constexpr (kPair) {
-                    const uint32_t bar = map_to_cta(ofull(ro.slot), 0);
+                    const uint32_t bar = map_to_cta(ofull(ro.slot), lead);
                     tma_load_2d_pair(dst, &tmX, bar, cur.kr * 128, m0, pol);
                     tma_load_2d_pair(dst + L::kXBox, &tmX, bar, cur.kr * 128 + 64, m0, pol);
                 } else {
@@ -464,7 +483,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             else return gemm::warp_wait(bar, parity, wc);
         };
         auto commit = [&](uint32_t bar) {
-            if constexpr (kPair) tc_commit_pair(bar);
+            if constexpr (kPair) tc_commit_pair(bar, static_cast<uint16_t>(3u << lead));
             else tc_commit(bar);
         };
         // the K block within a tile: whole tiles, then the tail from its first
@@ -541,11 +560,101 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (kPair && !leader) mbar_arrive_cluster(map_to_cta(ofull(ro.slot), 0));
+                if (kPair && !leader) mbar_arrive_cluster(map_to_cta(ofull(ro.slot), lead));
                 else mbar_arrive(ofull(ro.slot));
             }
         }
-    } else if (warp >= kWarpEpi0) {
+    } else if (kClu && warp >= kWarpEpi0) {
+        // One tile piece.  Each piece's pair sums 1/pieces of the tile's columns:
+        // a warp's chunks of 16 columns go to the pieces in order, kC to each.
+        // First every pair is done with its MMAs, and so with its operand rings,
+        // which take the partial sums of the others; then each CTA adds up the
+        // chunks it owns, in piece order.
+        constexpr int kChunks = L::kEpiCols / 16;
+        const int ew = warp - kWarpEpi0;
+        const int q = warp & 3;
+        const int col0 = (ew >> 2) * L::kEpiCols;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + L::kDCol0 + col0;
+        float* sxs = reinterpret_cast<float*>(gbase + L::kScaleOff) + ew * L::kScaleCols;
+        const int pieces = o.pieces;
+        const int piece = static_cast<int>(crank >> 1);
+        const int kC = (kChunks + pieces - 1) / pieces;
+        const int c_lo = piece * kC < kChunks ? piece * kC : kChunks;
+        const int c_hi = c_lo + kC < kChunks ? c_lo + kC : kChunks;
+        // the buffer of piece j's chunk (the lc-th of an owner's), this warp's part
+        auto buffer = [&](int j, int owner, int lc) {
+            return (((j < owner ? j : j - 1) * L::kEpi + ew) * kC + lc) * 2048 + lane * 16;
+        };
+        grid_dependency_wait();   // the scales and Y may be in use by the preceding grid
+        int tn, tm;
+        place_of(o, worker / pieces, tn, tm);
+        const int n = (tn * L::kCtas + static_cast<int>(rank)) * 128 + q * 32 + lane;
+        const int m0 = tm * NA + col0;
+        const float sw = n < p.N ? o.sw[n] : 0.0f;
+        const float bias = o.bias != nullptr && n < p.N ? o.bias[n] : 0.0f;
+        // the scales of the owned columns (at most 64: there are two pieces or more)
+        for (int c = lane; c < (c_hi - c_lo) * 16; c += 32) {
+            const int m = m0 + c_lo * 16 + c;
+            sxs[c] = m < p.M ? o.sx[m] : 0.0f;
+        }
+        const bool ok = gemm::warp_wait(dfull(0), 0, wc);
+        tc_fence_after();
+        auto load16 = [&](int c, float (&f)[16]) {
+            uint32_t v[16];
+            tmem_ld_x16(tl + 16 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+        };
+        __syncwarp();
+        cluster_sync_all();   // every ring is idle
+        if (ok) {
+            // start with the next piece's chunks, so that the CTAs write to
+            // different ones at a time
+#pragma unroll 1
+            for (int e = kC; e < pieces * kC; ++e) {
+                int c = c_lo + e;
+                if (c >= pieces * kC) c -= pieces * kC;
+                if (c >= kChunks) continue;
+                const int owner = c / kC;
+                if (owner == piece) continue;
+                const uint32_t to =
+                    map_to_cta(base + buffer(piece, owner, c - owner * kC), static_cast<uint32_t>(owner) * 2 + rank);
+                float f[16];
+                load16(c, f);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) st_cluster(to + g * 512, f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();   // every partial sum has arrived
+        if (ok) {
+#pragma unroll 1
+            for (int c = c_lo; c < c_hi; ++c) {
+                float own[16], acc[16];
+                load16(c, own);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
+                for (int j = 0; j < pieces; ++j) {
+                    if (j == piece) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[i] = __fadd_rn(acc[i], own[i]);
+                    } else {
+                        const uint8_t* from = gbase + buffer(j, piece, c - c_lo);
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const float4 x = *reinterpret_cast<const float4*>(from + g * 512);
+                            acc[4 * g + 0] = __fadd_rn(acc[4 * g + 0], x.x);
+                            acc[4 * g + 1] = __fadd_rn(acc[4 * g + 1], x.y);
+                            acc[4 * g + 2] = __fadd_rn(acc[4 * g + 2], x.z);
+                            acc[4 * g + 3] = __fadd_rn(acc[4 * g + 3], x.w);
+                        }
+                    }
+                }
+                store16(p, o, n, m0 + 16 * c, sxs + 16 * (c - c_lo), sw, bias, acc);
+            }
+        }
+    } else if (!kClu && warp >= kWarpEpi0) {
         const int ew = warp - kWarpEpi0;
         const int q = warp & 3;
         const int col0 = (ew >> 2) * L::kEpiCols;
@@ -603,7 +712,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (kPair && !leader) mbar_arrive_cluster(map_to_cta(dempty(b), 0));
+                    if (kPair && !leader) mbar_arrive_cluster(map_to_cta(dempty(b), lead));
                     else mbar_arrive(dempty(b));
                 }
             };
@@ -731,6 +840,11 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     }
 
     tc_fence_before();
+    if (kClu && (warp < kWarpEpi0 || warp >= L::kWarpConv0)) {   // the two meetings of the epilogue
+        __syncwarp();
+        cluster_sync_all();
+        cluster_sync_all();
+    }
     // a pair leaves together: the leader's MMAs read both CTAs' operands, and
     // either's threads arrive on the other's barriers
     __syncwarp();
@@ -886,12 +1000,15 @@ __global__ void bias_rows_kernel(const float* bias, void* Y, int64_t ldy, int y_
     }
 }
 
-template <int NA, bool kPair>
+template <int NA, bool kPair, bool kClu = false>
 cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                            const LaunchCtl& c, cudaStream_t st) {
     using L = I8Layout<NA, kPair>;
     static std::atomic<uint64_t> configured{0};
-    cudaError_t e = set_smem_once(configured, int8_kernel<NA, kPair>, L::kSmemBytes);
+    cudaError_t e = set_smem_once(configured, int8_kernel<NA, kPair, kClu>, L::kSmemBytes);
+    static std::atomic<uint64_t> wide{0};
+    if (e == cudaSuccess && kClu && s.pieces > 4)
+        e = set_once(wide, int8_kernel<NA, kPair, kClu>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     Params p = gemm::base_params(s, a.Y, a.ldy, a.M, a.N, a.K, nullptr, c);
     p.U = static_cast<long long>(s.T - s.nfull * s.G) * s.KU;   // the tail
@@ -902,7 +1019,7 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
     const int y_pairs = a.y_type != QG_FP32 && a.N % 2 == 0 && a.ldy % 2 == 0 &&
                         (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
     const Out o{a.Xq, a.ldxq, a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull,
-                c.overlap ? 1 : 0,
+                s.pieces, c.overlap ? 1 : 0,
                 p.G > 0 ? static_cast<int>(p.U / p.G) : 0, p.G > 0 ? static_cast<int>(p.U % p.G) : 0};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
@@ -919,13 +1036,13 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
     attr[n++].val.programmaticStreamSerializationAllowed = 1;
     if (kPair) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.x = kClu ? 2 * static_cast<unsigned>(s.pieces) : 2;
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, int8_kernel<NA, kPair>, tmW, tmX, p, o);
+    return cudaLaunchKernelEx(&cfg, int8_kernel<NA, kPair, kClu>, tmW, tmX, p, o);
 }
 
 }  // namespace
@@ -952,15 +1069,16 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
 constexpr int kMostPieces = 8;
 struct TileCost {
     int rows;
-    long long call_ns, unit_ns, split_ns, straddle_ns;
+    long long call_ns, unit_ns, split_ns, straddle_ns, cluster_ns;
 };
-constexpr TileCost kTiles[] = {{16, 4000, 305, 4000, 7500},
-                               {32, 6300, 310, 4000, 7500},
-                               {64, 6500, 340, 6500, 10500},
-                               {128, 7700, 350, 7500, 14500},
-                               {256, 8500, 560, 9500, 24000}};
+constexpr TileCost kTiles[] = {{16, 4000, 305, 4000, 7500, 0},
+                               {32, 6300, 310, 4000, 7500, 0},
+                               {64, 6500, 340, 6500, 10500, 0},
+                               {128, 7700, 350, 7500, 14500, 3500},
+                               {256, 8500, 560, 9500, 24000, 4500}};
 
-Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int forced, long long* cost) {
+Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int forced, const int* clusters,
+                           long long* cost) {
     Int8Schedule s;
     s.nmma = tc.rows;
     const int ctas = int8_ctas(s.nmma);
@@ -993,6 +1111,15 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
             best = straddle;
             g = all;
         }
+        // equal pieces in clusters of pairs, as many as run at once
+        if (ctas == 2 && s.nfull == 0 && forced == 0) {
+            for (int c = 2; c <= kMostClusterPieces && c <= s.KU; ++c) {
+                if (s.T > clusters[c] || up(s.KU, c) * tc.unit_ns + tc.cluster_ns >= best) continue;
+                best = up(s.KU, c) * tc.unit_ns + tc.cluster_ns;
+                g = static_cast<long long>(c) * r;
+                s.pieces = c;
+            }
+        }
         *cost += best;
         // A few rounds of whole tiles on single CTAs: as many workers as keep
         // all of them busy in every round.  These shapes are bound by memory,
@@ -1010,7 +1137,7 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
     return s;
 }
 
-Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
+Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced, const int* clusters) {
     Int8Schedule best;
     long long least = 0;
     int narrower = 0;   // rows of the next narrower tile
@@ -1018,7 +1145,7 @@ Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
         if (narrower >= M) break;   // the narrower one takes the batch as it is
         narrower = tc.rows;
         long long cost = 0;
-        const Int8Schedule s = schedule_with(tc, M, N, K, sms, forced, &cost);
+        const Int8Schedule s = schedule_with(tc, M, N, K, sms, forced, clusters, &cost);
         if (best.T == 0 || cost < least) {
             best = s;
             least = cost;
@@ -1026,8 +1153,36 @@ Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced) {
     }
     // splits: some worker's part of the tail begins inside a tile
     const long long units = (best.T - static_cast<long long>(best.nfull) * best.G) * best.KU;
-    for (long long c = 1; c < best.tail_g && !best.split; ++c) best.split = c * units / best.tail_g % best.KU != 0;
+    for (long long c = 1; c < best.tail_g && !best.split && best.pieces == 0; ++c) best.split = c * units / best.tail_g % best.KU != 0;
     return best;
+}
+
+// The clusters of 2 c CTAs that a device runs at once, for c pieces a tile (a
+// cluster lies within one of the device's groups of SMs, so that they are fewer
+// than the SMs would hold).
+void int8_cluster_capacity(int (&clusters)[kMostClusterPieces + 1]) {
+    for (int c = 0; c <= kMostClusterPieces; ++c) {
+        clusters[c] = 0;
+        if (c < 2) continue;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * c * 64);
+        cfg.blockDim = dim3(I8Layout<256, true>::kThreads);
+        cfg.dynamicSmemBytes = I8Layout<256, true>::kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2 * c;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const auto kernel = int8_kernel<256, true, true>;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, I8Layout<256, true>::kSmemBytes) ==
+                cudaSuccess &&
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess)
+            clusters[c] = n;
+    }
 }
 
 size_t int8_expanded_bytes(const Schedule& s, int M, int K) {
@@ -1068,8 +1223,12 @@ cudaError_t launch_int8(const Int8Args& a, const Int8Schedule& s, const CUtensor
         case 16: return launch_int8_na<16, false>(a, s, tmW, tmX, c, st);
         case 32: return launch_int8_na<32, false>(a, s, tmW, tmX, c, st);
         case 64: return launch_int8_na<64, false>(a, s, tmW, tmX, c, st);
-        case 128: return launch_int8_na<128, true>(a, s, tmW, tmX, c, st);
-        case 256: return launch_int8_na<256, true>(a, s, tmW, tmX, c, st);
+        case 128:
+            return s.pieces > 1 ? launch_int8_na<128, true, true>(a, s, tmW, tmX, c, st)
+                                : launch_int8_na<128, true>(a, s, tmW, tmX, c, st);
+        case 256:
+            return s.pieces > 1 ? launch_int8_na<256, true, true>(a, s, tmW, tmX, c, st)
+                                : launch_int8_na<256, true>(a, s, tmW, tmX, c, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -30,11 +30,24 @@ struct Int8Schedule : Schedule {
     int nfull = 0;
     int tail_g = 0;
     bool split = false;
+    // > 1: a cluster of this many pairs runs equal pieces of each tile (nfull
+    // is 0, tail_g = G = T * pieces)
+    int pieces = 0;
 };
 
+// Pairs of a cluster that share a tile, at most.
+constexpr int kMostClusterPieces = 5;
+// The clusters of 2 c CTAs that run at once on the current device, for c pieces.
+void int8_cluster_capacity(int (&clusters)[kMostClusterPieces + 1]);
+// The same on a GB300 with all of its 152 SMs, for questions without a device.
+inline const int* int8_nominal_clusters(int sms) {
+    static constexpr int kNone[kMostClusterPieces + 1] = {}, kFull[kMostClusterPieces + 1] = {0, 0, 36, 23, 15, 13};
+    return sms == 152 ? kFull : kNone;
+}
+
 // The schedule of a shape on `sms` SMs (forced > 0: with that many CTAs, the
-// tail cut evenly over all of them).
-Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced);
+// tail cut evenly over all of them); clusters: the capacity for 2 .. pieces.
+Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced, const int* clusters);
 
 // Workspace of a schedule (s.nmma = the tile's activation rows): the arrival
 // counters (kInt8CounterBytes, zero between calls, at offset 0 for every

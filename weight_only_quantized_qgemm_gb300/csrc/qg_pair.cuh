@@ -107,11 +107,12 @@ __device__ __forceinline__ void mma_ts_f16_pair(uint32_t d_tmem, uint32_t a_tmem
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// tc_commit of the pair's operations: arrives once on `bar` in both CTAs.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+// tc_commit of the pair's operations: arrives once on `bar` in both CTAs (mask:
+// their places in the cluster).
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "h"(mask)
         : "memory");
 }
 
