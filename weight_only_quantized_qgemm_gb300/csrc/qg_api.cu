@@ -31,7 +31,7 @@ struct DeviceInfo {
     std::once_flag once;
     int sms = 0;
     uint32_t* status = nullptr;
-    int clusters[kMostClusterPieces + 1] = {};   // of INT8 pairs (int8_cluster_capacity)
+    int clusters[kMostClusterCtas + 1] = {};   // of INT8 CTAs (int8_cluster_capacity)
     cudaError_t err = cudaSuccess;
 };
 DeviceInfo g_dev[kMaxDevices];

@@ -283,8 +283,8 @@ __device__ __forceinline__ void st_cluster(uint32_t mapped, float a, float b, fl
                  : "memory");
 }
 
-// kClu: o.pieces pairs of one cluster run equal pieces of a tile's K range and
-// sum them through distributed shared memory.
+// kClu: o.pieces workers (CTAs or pairs) of one cluster run equal pieces of a
+// tile's K range and sum them through distributed shared memory.
 template <int NA, bool kPair, bool kClu>
 __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     int8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p,
@@ -312,11 +312,10 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
-    static_assert(!kClu || kPair, "clusters are of pairs");
     // the units of a worker: a CTA, or a pair (both CTAs walk the same ones)
     const int worker = cta / L::kCtas;
-    const uint32_t crank = kPair ? cluster_cta_rank() : 0u;
-    const uint32_t rank = crank & 1u;         // in the pair
+    const uint32_t crank = kPair || kClu ? cluster_cta_rank() : 0u;
+    const uint32_t rank = kPair ? crank & 1u : 0u;   // in the pair
     const uint32_t lead = crank - rank;       // the pair's leader's place in the cluster
     const bool leader = rank == 0;
     int u0, u1;
@@ -356,7 +355,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             fence_barrier_init();
         }
         __syncwarp();
-        if constexpr (kPair) cluster_arrive_all();
+        if constexpr (kPair || kClu) cluster_arrive_all();
         else named_bar_arrive(1, L::kThreads);
         grid_dependents_launch();
         // a weight tile serves tm_count tiles: keep it for their re-reads
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         if (lane == 0)
             for (; issued < nunits && issued < kWStages; ++issued, cur.step(p, o), rw.step(1)) load_w();
         __syncwarp();
-        if constexpr (kPair) cluster_wait_all();   // of the arrival above
+        if constexpr (kPair || kClu) cluster_wait_all();   // of the arrival above
         if (lane == 0) {
             for (; issued < nunits; ++issued, cur.step(p, o), rw.step(1)) {
                 if (!wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         if (!L::kInlineX && warp == kWarpXProd && lane == 0) prefetch_tmap(&tmX);
         tc_fence_before();
         __syncwarp();
-        if constexpr (kPair) cluster_sync_all();   // the peer's barriers are set up too
+        if constexpr (kPair || kClu) cluster_sync_all();   // the peer's barriers are set up too
         else named_bar_sync(1, L::kThreads);
         tc_fence_after();
     }
@@ -565,11 +564,14 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             }
         }
     } else if (kClu && warp >= kWarpEpi0) {
-        // One tile piece.  Each piece's pair sums 1/pieces of the tile's columns:
-        // a warp's chunks of 16 columns go to the pieces in order, kC to each.
-        // First every pair is done with its MMAs, and so with its operand rings,
-        // which take the partial sums of the others; then each CTA adds up the
-        // chunks it owns, in piece order.
+        // One tile piece.  Each worker sums 1/pieces of the tile's columns: a
+        // warp's chunks of 16 columns go to the pieces in order, kC to each.
+        // First every worker is done with its MMAs, and so with its operand
+        // rings, which take the partial sums of the others; then each CTA adds up
+        // the chunks it owns, in piece order.  (Partial sums through the workspace
+        // cost 9 us of a 256-row tile, this way 4; 64 x 5120 x 5120 15.2 and 13.5 us.
+        // At 16 rows, where one CTA would sum all of a tile, 1 x 1024 x 5120 took
+        // 7.1 us either way and 8 x 2048 x 8192 8.4 and 9.0: not built.)
         constexpr int kChunks = L::kEpiCols / 16;
         const int ew = warp - kWarpEpi0;
         const int q = warp & 3;
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + L::kDCol0 + col0;
         float* sxs = reinterpret_cast<float*>(gbase + L::kScaleOff) + ew * L::kScaleCols;
         const int pieces = o.pieces;
-        const int piece = static_cast<int>(crank >> 1);
+        const int piece = static_cast<int>(crank) / L::kCtas;
         const int kC = (kChunks + pieces - 1) / pieces;
         const int c_lo = piece * kC < kChunks ? piece * kC : kChunks;
         const int c_hi = c_lo + kC < kChunks ? c_lo + kC : kChunks;
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         const int m0 = tm * NA + col0;
         const float sw = n < p.N ? o.sw[n] : 0.0f;
         const float bias = o.bias != nullptr && n < p.N ? o.bias[n] : 0.0f;
-        // the scales of the owned columns (at most 64: there are two pieces or more)
+        // the scales of the owned columns (at most 64, and at most the warp's)
         for (int c = lane; c < (c_hi - c_lo) * 16; c += 32) {
             const int m = m0 + c_lo * 16 + c;
             sxs[c] = m < p.M ? o.sx[m] : 0.0f;
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
                 const int owner = c / kC;
                 if (owner == piece) continue;
                 const uint32_t to =
-                    map_to_cta(base + buffer(piece, owner, c - owner * kC), static_cast<uint32_t>(owner) * 2 + rank);
+                    map_to_cta(base + buffer(piece, owner, c - owner * kC), static_cast<uint32_t>(owner * L::kCtas) + rank);
                 float f[16];
                 load16(c, f);
 #pragma unroll
@@ -848,7 +850,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     // a pair leaves together: the leader's MMAs read both CTAs' operands, and
     // either's threads arrive on the other's barriers
     __syncwarp();
-    if constexpr (kPair) cluster_sync_all();
+    if constexpr (kPair || kClu) cluster_sync_all();
     else __syncthreads();
     if (warp == kWarpMma) {
         __syncwarp();
@@ -1000,14 +1002,14 @@ __global__ void bias_rows_kernel(const float* bias, void* Y, int64_t ldy, int y_
     }
 }
 
-template <int NA, bool kPair, bool kClu = false>
+template <int NA, bool kPair, bool kClu>
 cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
                            const LaunchCtl& c, cudaStream_t st) {
     using L = I8Layout<NA, kPair>;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = set_smem_once(configured, int8_kernel<NA, kPair, kClu>, L::kSmemBytes);
     static std::atomic<uint64_t> wide{0};
-    if (e == cudaSuccess && kClu && s.pieces > 4)
+    if (e == cudaSuccess && kClu && s.pieces * L::kCtas > 8)
         e = set_once(wide, int8_kernel<NA, kPair, kClu>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     Params p = gemm::base_params(s, a.Y, a.ldy, a.M, a.N, a.K, nullptr, c);
@@ -1034,15 +1036,23 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
     int n = 0;
     attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[n++].val.programmaticStreamSerializationAllowed = 1;
-    if (kPair) {
+    if (kPair || kClu) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = kClu ? 2 * static_cast<unsigned>(s.pieces) : 2;
+        attr[n].val.clusterDim.x = static_cast<unsigned>(L::kCtas * (kClu ? s.pieces : 1));
         attr[n].val.clusterDim.y = 1;
         attr[n++].val.clusterDim.z = 1;
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, int8_kernel<NA, kPair, kClu>, tmW, tmX, p, o);
+}
+
+template <int NA, bool kPair>
+cudaError_t launch_int8_rows(const Int8Args& a, const Int8Schedule& s, const CUtensorMap& tmW, const CUtensorMap& tmX,
+                             const LaunchCtl& c, cudaStream_t st) {
+    if constexpr (NA > 16)
+        if (s.pieces > 1) return launch_int8_na<NA, kPair, true>(a, s, tmW, tmX, c, st);
+    return launch_int8_na<NA, kPair, false>(a, s, tmW, tmX, c, st);
 }
 
 }  // namespace
@@ -1054,6 +1064,8 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
 //   - one worker a tile: KU units
 //   - k = floor(workers / r) equal pieces of every tile: ceil(KU / k) units and
 //     a split (storing, counting and summing partial results)
+//   - k equal pieces of every tile in a cluster, where all clusters run at once:
+//     ceil(KU / k) units and the exchange
 //   - all workers, pieces that straddle tiles: ceil(r KU / workers) units and
 //     two splits a worker
 // and over the tile widths the one that costs least: wide tiles read fewer
@@ -1061,19 +1073,23 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
 // more SMs, split at a lower price, and the narrowest saves a launch (2 us of
 // the constant: the host's time, which bounds small calls).  Measured, whole
 // tiles / equal pieces / straddling: 256 x 5120 x 17408 at 128 rows 52.8 / - /
-// 44.7 us, at 256 rows 81.0 / 42.4 / 49.8; 128 x 6144 x 5120 at 128 rows 19.3 /
-// 17.6 / 22.7, at 256 rows 28.9 / 23.5 / 31.6; 1 x 1024 x 5120 at 16 rows 15.9 /
-// 8.4 / 8.8.  And by width (16, 32, 64, 128, 256 rows): 100 x 1000 x 1008 6.5 /
-// 7.1 / 7.7 / 8.8 / 11.2 us, 172 x 4218 x 1456 15.3 / 12.4 / 9.8 / 10.8 / 13.9, 64
-// x 5120 x 5120 21.1 / 18.0 / 15.5 / 17.2 / 23.3.
+// 44.7 us, at 256 rows 81.0 / 42.4 / 49.8 and 38.6 in clusters; 128 x 6144 x 5120
+// at 128 rows 19.3 / 17.6 / 22.7, at 256 rows 28.9 / 23.5 / 31.6; 64 x 5120 x 5120
+// at 64 rows 19.5 / 15.2 / 18.2 and 13.5; 1 x 1024 x 5120 at 16 rows 14.7 / 7.1 /
+// 8.7 and 7.0; 8 x 2048 x 8192 at 16 rows 22.4 / 8.4 / 9.6 and 9.0.  And by width
+// (16, 32, 64, 128, 256 rows), before clusters: 100 x 1000 x 1008 6.5 / 7.1 / 7.7 /
+// 8.8 / 11.2 us, 172 x 4218 x 1456 15.3 / 12.4 / 9.8 / 10.8 / 13.9, 64 x 5120 x
+// 5120 21.1 / 18.0 / 15.5 / 17.2 / 23.3; with them, 64 x 1024 x 8192 10.4 (16) and
+// 11.2 (64).
 constexpr int kMostPieces = 8;
 struct TileCost {
     int rows;
-    long long call_ns, unit_ns, split_ns, straddle_ns, cluster_ns;
+    long long call_ns, unit_ns, split_ns, straddle_ns;
+    long long cluster_ns;   // of equal pieces in a cluster; 0: not offered
 };
-constexpr TileCost kTiles[] = {{16, 4000, 305, 4000, 7500, 0},
-                               {32, 6300, 310, 4000, 7500, 0},
-                               {64, 6500, 340, 6500, 10500, 0},
+constexpr TileCost kTiles[] = {{16, 4000, 305, 3000, 7500, 0},
+                               {32, 6300, 310, 4000, 7500, 2800},
+                               {64, 6500, 340, 6500, 10500, 3000},
                                {128, 7700, 350, 7500, 14500, 3500},
                                {256, 8500, 560, 9500, 24000, 4500}};
 
@@ -1111,10 +1127,10 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
             best = straddle;
             g = all;
         }
-        // equal pieces in clusters of pairs, as many as run at once
-        if (ctas == 2 && s.nfull == 0 && forced == 0) {
-            for (int c = 2; c <= kMostClusterPieces && c <= s.KU; ++c) {
-                if (s.T > clusters[c] || up(s.KU, c) * tc.unit_ns + tc.cluster_ns >= best) continue;
+        // equal pieces in clusters, as many as run at once
+        if (tc.cluster_ns > 0 && s.nfull == 0 && forced == 0) {
+            for (int c = 2; c * ctas <= kMostClusterCtas && c <= kMostPieces && c <= s.KU; ++c) {
+                if (s.T > clusters[c * ctas] || up(s.KU, c) * tc.unit_ns + tc.cluster_ns >= best) continue;
                 best = up(s.KU, c) * tc.unit_ns + tc.cluster_ns;
                 g = static_cast<long long>(c) * r;
                 s.pieces = c;
@@ -1157,20 +1173,20 @@ Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced, const int* 
     return best;
 }
 
-// The clusters of 2 c CTAs that a device runs at once, for c pieces a tile (a
-// cluster lies within one of the device's groups of SMs, so that they are fewer
-// than the SMs would hold).
-void int8_cluster_capacity(int (&clusters)[kMostClusterPieces + 1]) {
-    for (int c = 0; c <= kMostClusterPieces; ++c) {
+// The clusters of c CTAs that a device runs at once (a cluster lies within one
+// of the device's groups of SMs, so that they are fewer than the SMs would
+// hold).  Every kernel here takes an SM to itself; one is asked for all.
+void int8_cluster_capacity(int (&clusters)[kMostClusterCtas + 1]) {
+    for (int c = 0; c <= kMostClusterCtas; ++c) {
         clusters[c] = 0;
-        if (c < 2) continue;
+        if (c < 2 || (c > 8 && c % 2 != 0)) continue;   // pairs only beyond 8
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * c * 64);
+        cfg.gridDim = dim3(c * 64);
         cfg.blockDim = dim3(I8Layout<256, true>::kThreads);
         cfg.dynamicSmemBytes = I8Layout<256, true>::kSmemBytes;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2 * c;
+        attr[0].val.clusterDim.x = c;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
@@ -1220,15 +1236,11 @@ cudaError_t launch_int8(const Int8Args& a, const Int8Schedule& s, const CUtensor
         if (e != cudaSuccess) return e;
     }
     switch (s.nmma) {
-        case 16: return launch_int8_na<16, false>(a, s, tmW, tmX, c, st);
-        case 32: return launch_int8_na<32, false>(a, s, tmW, tmX, c, st);
-        case 64: return launch_int8_na<64, false>(a, s, tmW, tmX, c, st);
-        case 128:
-            return s.pieces > 1 ? launch_int8_na<128, true, true>(a, s, tmW, tmX, c, st)
-                                : launch_int8_na<128, true>(a, s, tmW, tmX, c, st);
-        case 256:
-            return s.pieces > 1 ? launch_int8_na<256, true, true>(a, s, tmW, tmX, c, st)
-                                : launch_int8_na<256, true>(a, s, tmW, tmX, c, st);
+        case 16: return launch_int8_rows<16, false>(a, s, tmW, tmX, c, st);
+        case 32: return launch_int8_rows<32, false>(a, s, tmW, tmX, c, st);
+        case 64: return launch_int8_rows<64, false>(a, s, tmW, tmX, c, st);
+        case 128: return launch_int8_rows<128, true>(a, s, tmW, tmX, c, st);
+        case 256: return launch_int8_rows<256, true>(a, s, tmW, tmX, c, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -30,23 +30,24 @@ struct Int8Schedule : Schedule {
     int nfull = 0;
     int tail_g = 0;
     bool split = false;
-    // > 1: a cluster of this many pairs runs equal pieces of each tile (nfull
+    // > 1: a cluster of this many workers runs equal pieces of each tile (nfull
     // is 0, tail_g = G = T * pieces)
     int pieces = 0;
 };
 
-// Pairs of a cluster that share a tile, at most.
-constexpr int kMostClusterPieces = 5;
-// The clusters of 2 c CTAs that run at once on the current device, for c pieces.
-void int8_cluster_capacity(int (&clusters)[kMostClusterPieces + 1]);
-// The same on a GB300 with all of its 152 SMs, for questions without a device.
+// CTAs of a cluster that share a tile, at most (five pairs; single CTAs: 8).
+constexpr int kMostClusterCtas = 10;
+// The clusters of c CTAs that run at once on the current device, for each c.
+void int8_cluster_capacity(int (&clusters)[kMostClusterCtas + 1]);
+// The same on a GB300 with 152 SMs, for questions without a device.
 inline const int* int8_nominal_clusters(int sms) {
-    static constexpr int kNone[kMostClusterPieces + 1] = {}, kFull[kMostClusterPieces + 1] = {0, 0, 36, 23, 15, 13};
+    static constexpr int kNone[kMostClusterCtas + 1] = {};
+    static constexpr int kFull[kMostClusterCtas + 1] = {0, 0, 76, 46, 36, 28, 23, 15, 15, 0, 13};
     return sms == 152 ? kFull : kNone;
 }
 
 // The schedule of a shape on `sms` SMs (forced > 0: with that many CTAs, the
-// tail cut evenly over all of them); clusters: the capacity for 2 .. pieces.
+// tail cut evenly over all of them); clusters: the device's capacity by CTAs a cluster.
 Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced, const int* clusters);
 
 // Workspace of a schedule (s.nmma = the tile's activation rows): the arrival
