@@ -272,3 +272,17 @@ def test_refusals():
     with pytest.raises(q.QgemmError):
         q.logprobs(x, top_k=-1)
     assert q.logprobs(torch.zeros(0, 16, device="cuda"), top_k=2).top_ids.shape == (0, 2)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_entropy_of_a_certain_token(dtype):
+    """One logit far above the others: the entropy is 0 within its bound
+    (R (2 + 2 ln V), D counted as 104) and never negative."""
+    q = qg()
+    V = 5003
+    rng = np.random.default_rng(17)
+    x = rng.uniform(-2, 2, (64, V)) + rng.uniform(-300, 300, (64, 1))
+    x[np.arange(64), rng.integers(0, V, 64)] += rng.uniform(110, 400, 64)
+    H = q.logprobs(torch.from_numpy(x).to(DT[dtype]).cuda(), entropy=True).entropy.double().cpu().numpy()
+    R = (4 + 2 * 104 + V / 128 + 32) * U
+    assert (H >= 0).all() and (H <= R * (2 + 2 * math.log(V))).all()

@@ -690,7 +690,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
         const int64_t id = a.tokens[m * a.ldt + i];
         a.token_lp[m * a.T + i] = id < 0 || id >= a.V ? -INFINITY : logp_of(F::at(row, id), r.c, ls);
     }
-    if (a.entropy && tid == 0) a.entropy[m] = ls - kLn2 * (r.w / r.s);
+    if (a.entropy && tid == 0) a.entropy[m] = fmaxf(ls - kLn2 * (r.w / r.s), 0.0f);
     if (tid < a.top_k) {
         const uint64_t e = sh.list[tid];
         a.top_ids[m * a.top_k + tid] = entry_index(e);
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
     }
     int stage = 0;
     uint32_t phase = 0;
-    for (int64_t m = row0; m < a.M; m += rows) 
+    for (int64_t m = row0; m < a.M; m += rows)
         take_row<kType>(a, m, rank, S, sh, ring, rows >= a.M, stage, phase, wc);
 }
 
