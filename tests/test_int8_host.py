@@ -78,6 +78,7 @@ def test_quantiser_argument_validation(qg, args, expect):
     ((FAKE, 0, 99, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),        # ld < V
     ((FAKE, 0, 100, FAKE, 1, 2, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 1),       # ldt < T
     ((FAKE, 0, 0, FAKE, 1, 1, FAKE, FAKE, 0, FAKE, FAKE, 3, 0), 2),           # V == 0
+    ((FAKE, 0, 2 ** 31, FAKE, 1, 1, FAKE, FAKE, 0, FAKE, FAKE, 3, 2 ** 30 + 1), 2),   # a row longer than an index takes
     ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, 33, FAKE, FAKE, 3, 100), 2),      # top_k > 32
     ((FAKE, 0, 100, FAKE, 1, 1, FAKE, FAKE, 9, FAKE, FAKE, 3, 8), 2),         # top_k > V
     ((FAKE + 1, 0, 100, FAKE, 1, 1, FAKE, FAKE, 4, FAKE, FAKE, 3, 100), 3),

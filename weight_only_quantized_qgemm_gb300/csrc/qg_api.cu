@@ -31,7 +31,8 @@ struct DeviceInfo {
     std::once_flag once;
     int sms = 0;
     uint32_t* status = nullptr;
-    int clusters[kMostClusterCtas + 1] = {};   // of INT8 CTAs (int8_cluster_capacity)
+    std::once_flag clusters_once;
+    int clusters[kMostClusterCtas + 1] = {};   // of INT8 CTAs; asked for by the first INT8 schedule
     cudaError_t err = cudaSuccess;
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -45,7 +46,6 @@ DeviceInfo* device_info() {
         d->err = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev);
         if (d->err == cudaSuccess)
             d->err = cudaGetSymbolAddress(reinterpret_cast<void**>(&d->status), g_status_word);
-        if (d->err == cudaSuccess) int8_cluster_capacity(d->clusters);
     });
     return d->err == cudaSuccess ? d : nullptr;
 }
@@ -215,8 +215,13 @@ Int8Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced, co
 int schedule_ctas(int kind, const Schedule& s) { return kind == QG_KIND_INT8 ? int8_ctas(s.nmma) : 1; }
 
 Int8Schedule choose_schedule(int kind, int M, int N, int K, int sms) {
-    const DeviceInfo* d = device_info();
-    return schedule_for(kind, M, N, K, sms, table_lookup(kind, M, N, K), d ? d->clusters : int8_nominal_clusters(0));
+    const int* clusters = nullptr;
+    if (kind == QG_KIND_INT8) {
+        DeviceInfo* d = device_info();
+        if (d) std::call_once(d->clusters_once, [d]() { int8_cluster_capacity(d->clusters); });
+        clusters = d ? d->clusters : int8_nominal_clusters(0);
+    }
+    return schedule_for(kind, M, N, K, sms, table_lookup(kind, M, N, K), clusters);
 }
 
 // True when some tile's units are spread over more than one CTA.
@@ -776,7 +781,8 @@ qg_status qg_logprobs(const void* logits, int type, int64_t ld, const int64_t* t
     if (M == 0 || (T == 0 && !entropy && top_k == 0)) return QG_OK;
     if (!logits || (T > 0 && (!tokens || !token_logprobs)) || (top_k > 0 && (!top_ids || !top_logprobs)))
         return QG_ERR_INVALID_ARG;
-    if (V == 0 || top_k > QG_MAX_TOP_K || top_k > V) return QG_ERR_UNSUPPORTED_SHAPE;
+    // a row is indexed by int, with a CTA's stride to spare
+    if (V == 0 || V > (1 << 30) || top_k > QG_MAX_TOP_K || top_k > V) return QG_ERR_UNSUPPORTED_SHAPE;
     if (ld < V || ldt < T) return QG_ERR_INVALID_ARG;
     const uintptr_t mask = type == QG_FP32 ? 3u : 1u;
     if ((reinterpret_cast<uintptr_t>(logits) & mask) || (reinterpret_cast<uintptr_t>(tokens) & 7u) ||

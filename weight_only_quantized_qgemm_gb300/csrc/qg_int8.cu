@@ -6,9 +6,11 @@
 // sm_103a has no integer kind of tcgen05.mma, so the products run as
 // kind::f16: every value of -128..127 is an FP16 number, every product an
 // integer of at most 2^14, and the FP32 accumulator adds integers exactly
-// while the partial sums stay below 2^24 (always for K <= 1024; beyond that a
-// sum that leaves the range rounds at 2^-24 of its size, far under the output
-// types' steps).  The floor is therefore the FP16 tensor rate for large M and
+// while the partial sums stay below 2^24 (always for K <= 1024; codes of mixed
+// signs stay there far longer).  Beyond, every 16 products drop what lies under
+// the accumulator's last place: measured 1.7e-5 of a sum of 17408 products of
+// one sign and 5.2e-5 of 65536, under half a step of the 16-bit outputs (2^-9
+// and 2^-12 of the value).  The floor is therefore the FP16 tensor rate for large M and
 // the weight bytes, read once as stored, for small M.
 //
 // The output is tiled in 128 weight rows x NA activation rows (NA = the MMA's
@@ -54,6 +56,7 @@ using gemm::Ring;
 
 constexpr int kWarpWProd = 0, kWarpXProd = 1, kWarpMma = 2, kWarpX2 = 3, kWarpEpi0 = 4;
 constexpr int kGroups = 2;   // convert groups of four warps
+constexpr int kMostPieces = 8;   // equal pieces that a tile is cut into
 
 // NA activation rows a tile; kPair: a tile is 256 weight rows on a CTA pair.
 template <int NA, bool kPair>
@@ -119,7 +122,7 @@ struct Out {
     int tn_count, tm_count;   // weight tiles, activation row blocks
     int workers;              // CTAs or CTA pairs
     int nfull;                // whole tiles each worker runs before its part of the tail
-    int pieces;               // kClu: the pairs that share a tile
+    int pieces;               // kClu: the workers that share a tile
     int early;                // weights may be read before the preceding grid is done
     int tail_q, tail_r;       // the tail's units = tail_q G + tail_r
     // where worker c's part of the tail begins: floor(c U / G), in 32 bits
@@ -581,6 +584,9 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         const int pieces = o.pieces;
         const int piece = static_cast<int>(crank) / L::kCtas;
         const int kC = (kChunks + pieces - 1) / pieces;
+        // (pieces - 1) kC <= kChunks + pieces - 2 buffers an epilogue warp
+        static_assert((kChunks + kMostPieces - 2) * L::kEpi * 2048 <= L::kBarOff,
+                      "the others' partial sums fit the rings");
         const int c_lo = piece * kC < kChunks ? piece * kC : kChunks;
         const int c_hi = c_lo + kC < kChunks ? c_lo + kC : kChunks;
         // the buffer of piece j's chunk (the lc-th of an owner's), this warp's part
@@ -1020,8 +1026,8 @@ cudaError_t launch_int8_na(const Int8Args& a, const Int8Schedule& s, const CUten
     p.part = w ? reinterpret_cast<float*>(w + kInt8CounterBytes + int8_expanded_bytes(s, a.M, a.K)) : nullptr;
     const int y_pairs = a.y_type != QG_FP32 && a.N % 2 == 0 && a.ldy % 2 == 0 &&
                         (reinterpret_cast<uintptr_t>(a.Y) & 3u) == 0;
-    const Out o{a.Xq, a.ldxq, a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas), (a.M + NA - 1) / NA, s.G, s.nfull,
-                s.pieces, c.overlap ? 1 : 0,
+    const Out o{a.Xq, a.ldxq, a.Sx, a.Sw, a.bias, a.y_type, y_pairs, (a.N + 128 * L::kCtas - 1) / (128 * L::kCtas),
+                (a.M + NA - 1) / NA, s.G, s.nfull, s.pieces, c.overlap ? 1 : 0,
                 p.G > 0 ? static_cast<int>(p.U / p.G) : 0, p.G > 0 ? static_cast<int>(p.U % p.G) : 0};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(s.G * L::kCtas));
@@ -1081,7 +1087,6 @@ cudaError_t launch_int8_rows(const Int8Args& a, const Int8Schedule& s, const CUt
 // 8.8 / 11.2 us, 172 x 4218 x 1456 15.3 / 12.4 / 9.8 / 10.8 / 13.9, 64 x 5120 x
 // 5120 21.1 / 18.0 / 15.5 / 17.2 / 23.3; with them, 64 x 1024 x 8192 10.4 (16) and
 // 11.2 (64).
-constexpr int kMostPieces = 8;
 struct TileCost {
     int rows;
     long long call_ns, unit_ns, split_ns, straddle_ns;
@@ -1169,7 +1174,8 @@ Int8Schedule int8_schedule(int M, int N, int K, int sms, int forced, const int* 
     }
     // splits: some worker's part of the tail begins inside a tile
     const long long units = (best.T - static_cast<long long>(best.nfull) * best.G) * best.KU;
-    for (long long c = 1; c < best.tail_g && !best.split && best.pieces == 0; ++c) best.split = c * units / best.tail_g % best.KU != 0;
+    for (long long c = 1; c < best.tail_g && !best.split && best.pieces == 0; ++c)
+        best.split = c * units / best.tail_g % best.KU != 0;
     return best;
 }
 
@@ -1198,6 +1204,8 @@ void int8_cluster_capacity(int (&clusters)[kMostClusterCtas + 1]) {
             cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
             cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess)
             clusters[c] = n;
+        else
+            cudaGetLastError();   // not offered; no later call shall find the error
     }
 }
 
