@@ -11,10 +11,10 @@
 // floor first: their 2^t is 0 and 2^t t stays 0 instead of NaN; a NaN passes
 // the floor and spreads to s.
 //
-// The alternatives come from the same pass.  Every pair of threads knows the
-// largest logit it has seen; the k-th largest of these maxima is a bound that
-// at least k logits reach, and only the pairs that reach it (k of them, but
-// for ties) look at their logits again, in L2.  What reaches the bound (about
+// The alternatives come from the same pass.  Every thread knows the largest
+// logit it has seen; the k-th largest of these maxima is a bound that at least
+// k logits reach, and only the logits of the threads that reach it (k of them,
+// but for ties) are looked at again, in L2.  What reaches the bound (about
 // k (1 + k / 256) logits of a row without structure) is ranked by counting.
 // They are ordered on 64-bit keys: the value, then the lower index.
 //
@@ -43,13 +43,14 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256;      // that take logits; one more warp streams them in
+constexpr int kThreads = 128;      // that take logits; one more warp streams them in
 constexpr int kWarps = kThreads / 32;
-constexpr int kPairs = kThreads / 2;
-constexpr int kCtasPerSm = 3;
-constexpr int kStages = 4;         // of the ring, one turn each
-constexpr int kU = 4;              // 16-byte vectors a thread takes in a turn
+constexpr int kCtasPerSm = 5;
+constexpr int kMostStages = 4;     // of the ring, one turn each (stages_of)
+constexpr int kULg = 3;
+constexpr int kU = 1 << kULg;      // 16-byte vectors a thread takes in a turn
 constexpr int kTurn = kU * kThreads;
+constexpr int kSegs = 8;           // stretches of a thread's turns that it keeps the maxima of
 constexpr int kCap = 512;          // candidates at the bound
 constexpr int kMaxCluster = 16;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -188,17 +189,16 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-// A word of CTA `rank`'s shared memory at the address `p` has in this CTA's.
-__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) { return map_to_cta(smem_u32(p), rank); }
-__device__ __forceinline__ float peer_f32(const float* p, uint32_t rank) {
-    float r;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(peer_address(p, rank)) : "memory");
-    return r;
+// Stores to the shared memory of another CTA of the cluster (a mapped address).
+__device__ __forceinline__ void st_peer(uint32_t to, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
 }
-__device__ __forceinline__ uint64_t peer_u64(const uint64_t* p, uint32_t rank) {
-    uint64_t r;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(r) : "r"(peer_address(p, rank)) : "memory");
-    return r;
+__device__ __forceinline__ void st_peer(uint32_t to, float x, float y, float z, float w) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(x), "f"(y), "f"(z), "f"(w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_peer(uint32_t to, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(v) : "memory");
 }
 
 // The reference c of logits up to `top`.  Not below that of -kFar: c is then
@@ -219,21 +219,25 @@ struct Sums {
     }
 };
 
+struct alignas(16) PartSums {
+    Sums sums;
+    float bad;   // the part's list is not to be used
+};
+
 struct Shared {
-    uint64_t full[kStages], empty[kStages];   // of the ring
+    uint64_t full[kMostStages], empty[kMostStages];   // of the ring
     int abort;
     float warp_mx[kWarps];
     float warp_s[kWarps], warp_w[kWarps];
     uint32_t warp_u[kWarps];
-    alignas(16) uint32_t pair_key[kPairs];   // read four at a time
+    alignas(16) uint32_t own_key[kThreads];   // read four at a time
     float bound;
-    int flagged[kPairs];
+    float seg_mx[kSegs][kThreads];
+    uint16_t flagged[kSegs * kThreads];   // seg * kThreads + thread
     int nflagged, ncand, nlist;
-    float sums[4];                        // mx, c, s, w of the CTA; read by rank 0
-    float bad;                            // the CTA's list is not to be used; read by rank 0
-    uint64_t list[kMaxTopK];              // the CTA's best entries, in order; read by rank 0
+    PartSums parts[kMaxCluster];          // of a split row; written by the parts' CTAs, read by rank 0
+    uint64_t list[kMaxTopK];              // the CTA's best entries, in order
     uint64_t cand[kCap];
-    uint64_t joined[kMaxCluster * kMaxTopK];
     uint32_t slow_keys[kMaxTopK];
     int slow_ids[kMaxTopK];
 };
@@ -246,10 +250,10 @@ __device__ __forceinline__ void cluster_meet() {
     cluster_sync_all();
 }
 
-static_assert(offsetof(Shared, pair_key) % 16 == 0 && alignof(Shared) >= 16, "vector reads of the maxima");
-static_assert(offsetof(Shared, full) % 8 == 0 && offsetof(Shared, list) % 8 == 0 && offsetof(Shared, cand) % 8 == 0 &&
-                  offsetof(Shared, joined) % 8 == 0,
-              "barriers and entries");
+static_assert(offsetof(Shared, own_key) % 16 == 0 && alignof(Shared) >= 16, "vector reads of the maxima");
+static_assert(offsetof(Shared, full) % 8 == 0 && offsetof(Shared, parts) % 16 == 0 &&
+                  offsetof(Shared, list) % 8 == 0 && offsetof(Shared, cand) % 8 == 0,
+              "barriers, sums and entries");
 
 __device__ __forceinline__ float block_sum(float x, float* buf) {
 #pragma unroll
@@ -356,10 +360,10 @@ __device__ __forceinline__ float logp_of(float x, float c, float ls) {
     return x < -1e30f ? x : fmaf(fmaf(x, kLog2e, -c), kLn2, -ls);
 }
 
-// kU vectors of a thread: their maximum first (moving c where it rose), then
-// their terms, two at a time.
+// kU vectors of a thread: their maximum first, which is returned (moving c where
+// it rose), then their terms, two at a time.
 template <int kType>
-__device__ __forceinline__ void take(const uint4 (&x)[kU], float& mx, float& c, uint64_t& s2, uint64_t& w2) {
+__device__ __forceinline__ float take(const uint4 (&x)[kU], float& mx, float& c, uint64_t& s2, uint64_t& w2) {
     using F = Fmt<kType>;
     uint32_t u[kU * 4];
 #pragma unroll
@@ -406,6 +410,7 @@ __device__ __forceinline__ void take(const uint4 (&x)[kU], float& mx, float& c, 
         s2 = add2(s2, e2);
         w2 = fma2(e2, t2, w2);
     }
+    return top;
 }
 
 // The part of a row that one CTA of its cluster takes: up to 15 bytes of head,
@@ -432,7 +437,7 @@ struct Part {
 
 template <int kType>
 __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32_t rank, uint32_t S, Shared& sh,
-                                         const uint4* ring, bool resident, int& stage, uint32_t& phase,
+                                         const uint4* ring, uint64_t* joined, int stages, bool resident, int& stage, uint32_t& phase,
                                          const WaitCtl& wc) {
     using F = Fmt<kType>;
     const int tid = threadIdx.x;
@@ -458,6 +463,10 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
     Sums t{-INFINITY, kNoRef, 0.0f, 0.0f};
     uint64_t s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
     const uint4 empty = make_uint4(F::kEmpty, F::kEmpty, F::kEmpty, F::kEmpty);
+    // turns of a stretch, as a power of two
+    int seg_lg = 0;
+    while (kSegs << seg_lg < part.turns) ++seg_lg;
+    float seg = -INFINITY;
     for (int n = 0; n < part.turns; ++n) {
         // a wait that gives up raises the abort flag and the status; the row
         // goes on (with what the ring holds), so that every thread meets the others
@@ -472,10 +481,14 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
 #pragma unroll
             for (int j = 0; j < kU; ++j) x[j] = left > j * kThreads ? at[j * kThreads] : empty;
         }
-        take<kType>(x, t.mx, t.c, s2, w2);
+        seg = fmaxf(seg, take<kType>(x, t.mx, t.c, s2, w2));
+        if (((n + 1) & ((1 << seg_lg) - 1)) == 0 || n + 1 == part.turns) {   // read by this thread only
+            sh.seg_mx[n >> seg_lg][tid] = seg;
+            seg = -INFINITY;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));
-        if (++stage == kStages) {
+        if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -498,12 +511,13 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
         t.w = fmaf(e, tt, t.w);
     }
 
-    // the CTA's maximum and sums, and (for alternatives) the pairs' maxima
-    const float pair = fmaxf(t.mx, __shfl_xor_sync(0xffffffffu, t.mx, 1));
-    if ((tid & 1) == 0) sh.pair_key[tid >> 1] = (order_key(pair) & ~(kPairs - 1u)) | (kPairs - 1u - (tid >> 1));
-    float mx = pair;
+    // the CTA's maximum and sums, and (for alternatives) the threads' maxima
+    const float own = t.mx;
+    const uint32_t key = (order_key(own) & ~(kThreads - 1u)) | (kThreads - 1u - tid);
+    if (a.top_k > 1) sh.own_key[tid] = key;
+    float mx = own;
 #pragma unroll
-    for (int s = 16; s > 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     if (lane == 0) sh.warp_mx[warp] = mx;
     if (tid == 0) sh.nflagged = sh.ncand = sh.nlist = 0;
     if (tid < kMaxTopK) sh.list[tid] = 0ull;
@@ -525,37 +539,35 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
 
     bool bad = false;   // this CTA's list is not to be used
     if (a.top_k > 0) {
-        // The bound: the top_k-th largest of the pairs' maxima, by counting, on
-        // their keys with the pair's number in the low bits (which makes them
+        // The bound: the top_k-th largest of the threads' maxima, by counting, on
+        // their keys with the thread's number in the low bits (which makes them
         // distinct, and the bound at most that much lower than the maximum).
-        // Each thread counts for one pair against half of them.
         float bound = mx;
         if (a.top_k > 1) {
-            const uint32_t mine = sh.pair_key[tid >> 1];
-            const uint4* p4 = reinterpret_cast<const uint4*>(sh.pair_key) + (tid & 1) * (kPairs / 8);
+            const uint4* k4 = reinterpret_cast<const uint4*>(sh.own_key);
             int above = 0;
-#pragma unroll
-            for (int j = 0; j < kPairs / 8; ++j) {
-                const uint4 o = p4[j];
-                above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+#pragma unroll 8
+            for (int j = 0; j < kThreads / 4; ++j) {
+                const uint4 o = k4[j];
+                above += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
             }
-            above += __shfl_xor_sync(0xffffffffu, above, 1);
-            if (above == a.top_k - 1)   // both threads of the pair
-                sh.bound = key_value(max(mine & ~(kPairs - 1u), order_key(-INFINITY)));
+            if (above == a.top_k - 1)
+                sh.bound = key_value(max(key & ~(kThreads - 1u), order_key(-INFINITY)));
             meet();
             bound = sh.bound;
         }
-        if (!(tid & 1) && pair >= bound) sh.flagged[atomicAdd(&sh.nflagged, 1)] = tid >> 1;
+        if (own >= bound)
+            for (int j = 0; j << seg_lg < part.turns; ++j)
+                if (sh.seg_mx[j][tid] >= bound)
+                    sh.flagged[atomicAdd(&sh.nflagged, 1)] = static_cast<uint16_t>(j * kThreads + tid);
         auto push = [&](float x, uint32_t index) {
             const int at = atomicAdd(&sh.ncand, 1);
             if (at < kCap) sh.cand[at] = entry_of(x, index);
         };
         if (lone >= 0 && (lone_x < F::kFloor ? F::kFloor : lone_x) >= bound) push(lone_x, lone);
         meet();
-        // Two threads to a round of a pair's vectors, up to 64 rounds of a pair at
-        // once, and as many pairs at once as that leaves threads for.
         // a part that went into the ring without a second turn round it is still there
-        const uint4* from = resident && part.turns <= kStages ? ring - v0 : vec;
+        const uint4* from = resident && part.turns <= stages ? ring - v0 : vec;
         const int nflagged = sh.nflagged;
         auto look = [&](const uint4& x, int u) {
             const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
@@ -570,29 +582,30 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
                 if ((y < F::kFloor ? F::kFloor : y) >= bound) push(y, index + e);
             }
         };
-        const int rounds = (v1 - v0 + kThreads - 1) / kThreads;
-        int lg = 0;
-        while (lg < 6 && (1 << lg) < rounds) ++lg;
-        const int group = tid >> (lg + 1), groups = kThreads >> (lg + 1);
-        const int r0 = (tid & ((2 << lg) - 1)) >> 1;
-        for (int u0 = v0 + (tid & 1) + r0 * kThreads; u0 < v1; u0 += kThreads << lg) {
-            int f = group;
-            for (; f + 3 * groups < nflagged; f += 4 * groups) {   // four loads in flight
-                uint4 x[4];
-                int u[4];
+        // all vectors of the flagged stretches, spread over the threads
+        const int per_lg = seg_lg + kULg;
+        auto vector_of = [&](int q) {
+            const int f = sh.flagged[q >> per_lg];
+            const int round = ((f / kThreads) << per_lg) + (q & ((1 << per_lg) - 1));
+            return v0 + round * kThreads + f % kThreads;
+        };
+        const int all = nflagged << per_lg;
+        int q = tid;
+        for (; q + 3 * kThreads < all; q += 4 * kThreads) {   // four loads in flight
+            uint4 x[4];
+            int u[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    u[j] = u0 + 2 * sh.flagged[f + j * groups];
-                    x[j] = u[j] < v1 ? from[u[j]] : empty;
-                }
+            for (int j = 0; j < 4; ++j) {
+                u[j] = vector_of(q + j * kThreads);
+                x[j] = u[j] < v1 ? from[u[j]] : empty;
+            }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (u[j] < v1) look(x[j], u[j]);
-            }
-            for (; f < nflagged; f += groups) {
-                const int u = u0 + 2 * sh.flagged[f];
-                if (u < v1) look(from[u], u);
-            }
+            for (int j = 0; j < 4; ++j)
+                if (u[j] < v1) look(x[j], u[j]);
+        }
+        for (; q < all; q += kThreads) {
+            const int u = vector_of(q);
+            if (u < v1) look(from[u], u);
         }
         meet();
         const int n = sh.ncand;
@@ -617,63 +630,61 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
     }
 
     if (S > 1) {
+        // every part's sums and list to rank 0, which has started by then
+        cluster_wait_all();
+        const uint32_t to = map_to_cta(smem_u32(&sh.parts[rank]), 0);
         if (tid == 0) {
-            sh.sums[0] = r.mx;
-            sh.sums[1] = r.c;
-            sh.sums[2] = r.s;
-            sh.sums[3] = r.w;
-            sh.bad = bad ? 1.0f : 0.0f;
+            st_peer(to, r.mx, r.c, r.s, r.w);
+            st_peer(to + 16, bad ? 1.0f : 0.0f);
         }
-        meet();
+        if (tid < a.top_k) st_peer(map_to_cta(smem_u32(joined + rank * a.top_k + tid), 0), sh.list[tid]);
         cluster_meet();
-        if (rank == 0) {
-            // every warp adds the parts up for itself, lane l holding part l
-            const bool has = lane < static_cast<int>(S);
-            Sums p{-INFINITY, kNoRef, 0.0f, 0.0f};
-            bool any_bad = false;
-            if (has) {
-                p = Sums{peer_f32(sh.sums, lane), peer_f32(sh.sums + 1, lane), peer_f32(sh.sums + 2, lane),
-                         peer_f32(sh.sums + 3, lane)};
-                any_bad = peer_f32(&sh.bad, lane) != 0.0f;
-            }
-            bad = __any_sync(0xffffffffu, any_bad);
-            float top = p.mx;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            r.mx = top;
-            r.c = reference_of(top);
-            p.move_to(r.c);
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) {
-                p.s += __shfl_xor_sync(0xffffffffu, p.s, s);
-                p.w += __shfl_xor_sync(0xffffffffu, p.w, s);
-            }
-            r.s = p.s;
-            r.w = p.w;
-            for (int e = tid; e < static_cast<int>(S) * a.top_k; e += kThreads) {
-                const int q = e / a.top_k;
-                sh.joined[e] = peer_u64(sh.list + (e - q * a.top_k), q);
-            }
-            if (tid == 0) sh.ncand = 0;
-        }
-        cluster_meet();   // nobody's lists are read any more
         if (rank != 0) return;
+        // every warp adds the parts up for itself, lane l holding part l
+        const bool has = lane < static_cast<int>(S);
+        Sums p{-INFINITY, kNoRef, 0.0f, 0.0f};
+        if (has) p = sh.parts[lane].sums;
+        bad = __any_sync(0xffffffffu, has && sh.parts[lane].bad != 0.0f);
+        float top = p.mx;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        r.mx = top;
+        r.c = reference_of(top);
+        p.move_to(r.c);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) {
+            p.s += __shfl_xor_sync(0xffffffffu, p.s, s);
+            p.w += __shfl_xor_sync(0xffffffffu, p.w, s);
+        }
+        r.s = p.s;
+        r.w = p.w;
         if (a.top_k > 0) {
-            // what reaches the largest of the lists' last entries holds the answer
-            uint64_t bound = 0ull;
-            for (int q = 0; q < static_cast<int>(S); ++q) {
-                const uint64_t last = sh.joined[q * a.top_k + a.top_k - 1];
-                bound = last > bound ? last : bound;
+            // At least top_k entries reach the q-th largest of the lists' j-th
+            // entries, j q >= top_k, with the smallest j that S lists allow (with
+            // j = top_k, the largest of the last entries, 20 alternatives of 32
+            // rows in 16 parts left 230 entries to rank and took 18.6 us).
+            const int j = (a.top_k + static_cast<int>(S) - 1) / static_cast<int>(S);
+            const int q = (a.top_k + j - 1) / j;
+            const uint64_t mine = has ? joined[lane * a.top_k + j - 1] : 0ull;
+            int above = 0;
+            for (int l = 0; l < static_cast<int>(S); ++l) {
+                const uint64_t other = __shfl_sync(0xffffffffu, mine, l);
+                above += other > mine || (other == mine && l < lane);
             }
+            const uint32_t at = __ballot_sync(0xffffffffu, has && above == q - 1);
+            const uint64_t bound = __shfl_sync(0xffffffffu, mine, __ffs(at) - 1);
+            if (tid == 0) sh.ncand = 0;
+            meet();
             for (int e = tid; e < static_cast<int>(S) * a.top_k; e += kThreads)
-                if (sh.joined[e] >= bound && sh.joined[e] != 0ull) sh.cand[atomicAdd(&sh.ncand, 1)] = sh.joined[e];
+                if (joined[e] >= bound && joined[e] != 0ull) sh.cand[atomicAdd(&sh.ncand, 1)] = joined[e];
             meet();
             const int n = sh.ncand;
             for (int i = tid; i < n; i += kThreads) {
-                const uint64_t mine = sh.cand[i];
-                int above = 0;
-                for (int j = 0; j < n; ++j) above += sh.cand[j] > mine;
-                if (above < a.top_k) sh.list[above] = mine;
+                const uint64_t one = sh.cand[i];
+                int rank_of = 0;
+#pragma unroll 8
+                for (int l = 0; l < n; ++l) rank_of += sh.cand[l] > one;
+                if (rank_of < a.top_k) sh.list[rank_of] = one;
             }
             meet();
         }
@@ -698,14 +709,21 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
     }
 }
 
+__host__ __device__ constexpr uint32_t joined_bytes(uint32_t S, int top_k) {
+    return S > 1 ? (S * static_cast<uint32_t>(top_k) * 8u + 127u) & ~127u : 0u;
+}
+
 template <int kType>
 __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
-    logprobs_kernel(const LogprobArgs a, uint64_t timeout_ns, uint32_t* status) {
-    extern __shared__ __align__(128) uint4 ring[];   // [kStages][kTurn]
+    logprobs_kernel(const LogprobArgs a, int stages, uint64_t timeout_ns, uint32_t* status) {
+    extern __shared__ __align__(128) uint4 dynamic[];   // the lists of a split row's parts, then the ring
     __shared__ Shared sh;
     const uint32_t S = cluster_size(), rank = cluster_cta_rank();
+    uint64_t* joined = reinterpret_cast<uint64_t*>(dynamic);   // [S][top_k]
+    uint4* ring = dynamic + joined_bytes(S, a.top_k) / 16;     // [stages][kTurn]
+    if (S > 1) cluster_arrive_all();   // waited for in front of the first store to a peer
     if (threadIdx.x == kThreads) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1);
             mbar_init(smem_u32(&sh.empty[s]), kWarps);
         }
@@ -722,28 +740,33 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
     if (threadIdx.x >= kThreads) {
         if (threadIdx.x == kThreads) {
             const uint64_t pol = policy_evict_normal();   // what reaches a bound is read again
-            int issued = 0;
-            gemm::Ring<kStages> r(0);
+            int issued = 0, slot = 0;
+            uint32_t turned = 0u;   // parity of the times round the ring
             bool ok = true;
             for (int64_t m = row0; m < a.M && ok; m += rows) {
                 const Part<kType> part(a, m, rank, S);
-                for (int n = 0; n < part.turns; ++n, r.step(1)) {
-                    if (issued >= kStages) ok = wait_bounded(smem_u32(&sh.empty[r.slot]), r.phase ^ 1u, wc);
+                for (int n = 0; n < part.turns; ++n) {
+                    if (issued >= stages) ok = wait_bounded(smem_u32(&sh.empty[slot]), turned ^ 1u, wc);
                     if (!ok) break;
                     const int v = part.v0 + n * kTurn;
                     const uint32_t bytes = (part.v1 - v < kTurn ? part.v1 - v : kTurn) * 16u;
-                    const uint32_t bar = smem_u32(&sh.full[r.slot]);
+                    const uint32_t bar = smem_u32(&sh.full[slot]);
                     mbar_arrive_expect_tx(bar, bytes);
-                    bulk_load(smem_u32(ring + r.slot * kTurn), part.vec + v, bytes, bar, pol);
+                    bulk_load(smem_u32(ring + slot * kTurn), part.vec + v, bytes, bar, pol);
                     ++issued;
+                    if (++slot == stages) {
+                        slot = 0;
+                        turned ^= 1u;
+                    }
                 }
             }
             // every copy lands before the CTA may end
-            for (int i = issued - kStages < 0 ? 0 : issued - kStages; i < issued; ++i)
-                gemm::drain_wait(smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, timeout_ns);
+            for (int i = issued - stages < 0 ? 0 : issued - stages; i < issued; ++i)
+                gemm::drain_wait(smem_u32(&sh.full[i % stages]), (i / stages) & 1, timeout_ns);
         }
-        if (S > 1) {   // the two meetings of take_row
-            cluster_meet();
+        if (S > 1) {   // the two of take_row
+            __syncwarp();
+            cluster_wait_all();
             cluster_meet();
         }
         return;
@@ -751,15 +774,27 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
     int stage = 0;
     uint32_t phase = 0;
     for (int64_t m = row0; m < a.M; m += rows)
-        take_row<kType>(a, m, rank, S, sh, ring, rows >= a.M, stage, phase, wc);
+        take_row<kType>(a, m, rank, S, sh, ring, joined, stages, rows >= a.M, stage, phase, wc);
 }
 
-// CTAs per row: 1 once the rows fill the SMs, else the row is cut into up to
-// 16 parts of at least 2048 logits while their CTAs all run at once.
+// CTAs per row: a power of two up to 16, so that the CTAs are at most two per
+// SM and take 2048 logits or more each.  More of them cost more to launch as
+// clusters and to join than the shorter parts save (32 x 131072 FP32, 20
+// alternatives: 12.3 us in 16 parts, 11.3 in 8, 13.1 in 4; 57 x 131072 BF16, 5:
+// 12.0 in 8, 10.8 in 4; 380 x 8000: 9.5 in 2, 6.1 whole; but 100 x 50000: 10.4 in
+// 4, 10.8 in 2).
 int parts_of(int M, int V, int sms) {
     int s = 1;
-    while (s < kMaxCluster && static_cast<int64_t>(M) * 2 * s <= kCtasPerSm * sms * 3 / 4 && V / (2 * s) >= 2048) s *= 2;
+    while (s < kMaxCluster && static_cast<int64_t>(M) * 2 * s <= 2 * sms && V / (2 * s) >= 2048) s *= 2;
     return s;
+}
+
+// The ring's turns: what an SM's shared memory holds for its CTAs (two turns
+// each where there are four or more, four where there are two: 260 x 160000
+// FP32 38.5 -> 34.2 us, 128 x 131072 BF16, 20 alternatives, 17.5 -> 16.5).
+int stages_of(int64_t ctas, int sms) {
+    const int64_t per_sm = (ctas + sms - 1) / sms;
+    return per_sm <= 2 ? 4 : per_sm == 3 ? 3 : 2;
 }
 
 template <int kType>
@@ -771,16 +806,19 @@ cudaError_t launch(const LogprobArgs& a, const LaunchCtl& c, cudaStream_t st) {
     // another row goes round all of it.
     const int turns = a.V / parts / (kTurn * Fmt<kType>::kE) + 1;
     const bool one_part = parts > 1 || a.M <= most;
-    const int ring_bytes = (one_part && turns < kStages ? turns : kStages) * kTurn * 16;
+    const int64_t ctas = parts > 1 ? static_cast<int64_t>(a.M) * parts : a.M < most ? a.M : most;
+    const int stages = stages_of(ctas, c.num_sms);
+    const int ring_bytes = (one_part && turns < stages ? turns : stages) * kTurn * 16;
     static std::atomic<uint64_t> configured{0}, wide{0};
-    cudaError_t e = set_smem_once(configured, logprobs_kernel<kType>, kStages * kTurn * 16);
+    cudaError_t e = set_smem_once(configured, logprobs_kernel<kType>,
+                                 kMostStages * kTurn * 16 + joined_bytes(kMaxCluster, kMaxTopK));
     if (e == cudaSuccess && parts > 8)
         e = set_once(wide, logprobs_kernel<kType>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(parts > 1 ? a.M * parts : a.M < most ? a.M : most));
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads + 32);
-    cfg.dynamicSmemBytes = static_cast<size_t>(ring_bytes);
+    cfg.dynamicSmemBytes = static_cast<size_t>(ring_bytes) + joined_bytes(parts, a.top_k);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -791,7 +829,7 @@ cudaError_t launch(const LogprobArgs& a, const LaunchCtl& c, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = c.overlap ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<kType>, a, c.timeout_ns, c.status);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<kType>, a, stages, c.timeout_ns, c.status);
 }
 
 }  // namespace
