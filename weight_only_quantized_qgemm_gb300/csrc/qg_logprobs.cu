@@ -14,22 +14,29 @@
 // The alternatives come from the same pass.  Every thread keeps the largest
 // logits of up to eight stretches of its turns; the k-th largest of the maxima of
 // pairs of threads is a bound that at least k logits reach, and only the
-// stretches that reach it (little more than k of them) are looked at again, in L2.  What reaches the bound (about
-// k (1 + k / 256) logits of a row without structure) is ranked by counting.
-// They are ordered on 64-bit keys: the value, then the lower index.
+// stretches that reach it (little more than k of them) are looked at again, in
+// L2.  What reaches the bound (about k (1 + k / 128) logits of a row without
+// structure) is ranked by counting.  They are ordered on 64-bit keys: the value,
+// then the lower index.
 //
 // Rows where this does not hold are worked out by the plain method at the end
 // of this file's row function: a maximum beyond +-1e8 (or at the floor: a row
 // of nothing but masks), a NaN or +inf, or more than kCap logits at the bound.
 //
-// A few CTAs per SM walk over the rows.  One warp of a CTA streams them into a
+// Five CTAs per SM walk over the rows.  One warp of a CTA streams them into a
 // ring in shared memory by bulk copies, running on into the next row while the
-// other eight finish one (choosing the alternatives takes about as long as
-// reading 40 KB: 4 us, with nothing on the way from memory when each row had a
-// CTA of its own and registers for its loads).  Rows that are too few for the
-// SMs are split over a cluster of up to 16 CTAs, whose sums and lists rank 0
-// joins through distributed shared memory (no workspace, no atomics on memory,
-// the same order of sums on every call).
+// other four finish one (under load the end of a row takes 4 us, with nothing on
+// the way from memory when each row had a CTA of its own and registers for its
+// loads).  Many small CTAs, because that end is a chain of block-wide steps and
+// the others' streaming hides it (three CTAs of 256 threads: 177 us for 4096 x
+// 131072 BF16 and 65 for 4096 x 32768, now 158 and 53); turns of eight vectors a
+// thread, because each costs a wait, a maximum and an arrival (of
+// four, 167 against 165 us and 57 against 53 when they were compared).
+// Bound by memory on long rows: 4096 x 131072 BF16 runs at the measured copy
+// rate.  Rows that are too few for the SMs are split over a cluster of up to 16
+// CTAs, which store their sums and lists to rank 0's shared memory, where they
+// are joined (no workspace, no atomics on memory, the same order of sums on every
+// call).
 #include <cstddef>
 
 #include <cuda_bf16.h>
@@ -66,7 +73,8 @@ template <>
 struct Fmt<QG_FP32> {
     static constexpr int kE = 4, kSize = 4;
     static constexpr float kFloor = -1e30f;
-    __device__ static float at(const void* row, int64_t v) { return static_cast<const float*>(row)[v]; }
+    using Word = float;   // of one element, as loaded
+    __device__ static float value(Word w) { return w; }
     __device__ static uint32_t floor_word(uint32_t w) {
         uint32_t r;
         asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(__float_as_uint(kFloor)));
@@ -84,9 +92,8 @@ template <>
 struct Fmt<QG_BF16> {
     static constexpr int kE = 8, kSize = 2;
     static constexpr float kFloor = -0x1.94p99f;   // about -1e30: the bf16 0xF14A
-    __device__ static float at(const void* row, int64_t v) {
-        return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(row)[v]) << 16);
-    }
+    using Word = uint16_t;
+    __device__ static float value(Word w) { return __uint_as_float(static_cast<uint32_t>(w) << 16); }
     __device__ static uint32_t floor_word(uint32_t w) {
         uint32_t r;
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xF14AF14Au));
@@ -114,7 +121,8 @@ template <>
 struct Fmt<QG_FP16> {
     static constexpr int kE = 8, kSize = 2;
     static constexpr float kFloor = -65504.0f;
-    __device__ static float at(const void* row, int64_t v) { return __half2float(static_cast<const __half*>(row)[v]); }
+    using Word = uint16_t;
+    __device__ static float value(Word w) { return __half2float(__ushort_as_half(w)); }
     __device__ static uint32_t floor_word(uint32_t w) {
         uint32_t r;
         asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0xFBFFFBFFu));
@@ -142,6 +150,16 @@ struct Fmt<QG_FP16> {
     }
     static constexpr uint32_t kEmpty = 0xFC00FC00u;
 };
+
+// Element v of a row, as loaded (the conversion at once would wait for the load).
+template <typename F>
+__device__ __forceinline__ typename F::Word word_at(const void* row, int64_t v) {
+    return static_cast<const typename F::Word*>(row)[v];
+}
+template <typename F>
+__device__ __forceinline__ float value_at(const void* row, int64_t v) {
+    return F::value(word_at<F>(row, v));
+}
 
 // ----------------------------------------------------------------- small pieces
 __device__ __forceinline__ float ex2(float x) {
@@ -290,13 +308,13 @@ __device__ __noinline__ void top_by_value(const void* row, int V, int k, Shared&
     while (have < k) {
         uint32_t best = 0u;
         for (int v = threadIdx.x; v < V; v += kThreads) {
-            const uint32_t key = order_key(F::at(row, v));
+            const uint32_t key = order_key(value_at<F>(row, v));
             if (key < below) best = max(best, key);
         }
         best = block_max(best, sh.warp_u);
         for (int v0 = 0; v0 < V && have < k; v0 += kThreads) {
             const int v = v0 + threadIdx.x;
-            const bool hit = v < V && order_key(F::at(row, v)) == best;
+            const bool hit = v < V && order_key(value_at<F>(row, v)) == best;
             const uint32_t mask = __ballot_sync(0xffffffffu, hit);
             meet();
             if ((threadIdx.x & 31) == 0) sh.warp_u[threadIdx.x >> 5] = __popc(mask);
@@ -324,13 +342,13 @@ template <int kType>
 __device__ __noinline__ void plain_row(const LogprobArgs& a, int64_t m, const void* row, Shared& sh) {
     using F = Fmt<kType>;
     uint32_t best = 0u;
-    for (int v = threadIdx.x; v < a.V; v += kThreads) best = max(best, order_key(F::at(row, v)));
+    for (int v = threadIdx.x; v < a.V; v += kThreads) best = max(best, order_key(value_at<F>(row, v)));
     const float mx = key_value(block_max(best, sh.warp_u));
     const bool none = mx == -INFINITY;   // a row with nothing left
     float s = 0.0f, w = 0.0f;
     if (!none)
         for (int v = threadIdx.x; v < a.V; v += kThreads) {
-            const float d = F::at(row, v) - mx;
+            const float d = value_at<F>(row, v) - mx;
             const float e = ex2(d * kLog2e);
             s += e;
             if (e != 0.0f) w += e * d;
@@ -341,7 +359,7 @@ __device__ __noinline__ void plain_row(const LogprobArgs& a, int64_t m, const vo
     for (int t = threadIdx.x; t < a.T; t += kThreads) {
         const int64_t id = a.tokens[m * a.ldt + t];
         const bool in = id >= 0 && id < a.V;
-        a.token_lp[m * a.T + t] = !in || none ? -INFINITY : F::at(row, id) - mx - ls;
+        a.token_lp[m * a.T + t] = !in || none ? -INFINITY : value_at<F>(row, id) - mx - ls;
     }
     if (a.entropy && threadIdx.x == 0) a.entropy[m] = none ? 0.0f : ls - w / s;
     if (a.top_k > 0) {
@@ -452,18 +470,19 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
     // the asked token's logit, on its way while the row is read, and the token
     // of the CTA's next row (its load and the logit's in a row cost 1 us a row)
     int64_t tok = -1;
-    float tok_x = 0.0f;
+    typename F::Word tok_w = 0;
     if (rank == 0 && tid < a.T) {
         if (ahead >= 0 && ahead < a.V) {
             tok = ahead;
-            tok_x = F::at(row, tok);
+            tok_w = word_at<F>(row, tok);
         }
         if (next < a.M) ahead = a.tokens[next * a.ldt + tid];
     }
     int lone = -1;   // the index of the head or tail logit this thread takes
     if (rank == 0 && tid < head) lone = tid;
     if (rank == S - 1 && tid >= 32 && tid - 32 < a.V - tail0) lone = tail0 + tid - 32;
-    float lone_x = lone >= 0 ? F::at(row, lone) : 0.0f;
+    typename F::Word lone_w = 0;
+    if (lone >= 0) lone_w = word_at<F>(row, lone);
 
     Sums t{-INFINITY, kNoRef, 0.0f, 0.0f};
     uint64_t s2 = pack2(0.0f, 0.0f), w2 = pack2(0.0f, 0.0f);
@@ -512,6 +531,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
         t.s += s_hi;
         t.w += w_hi;
     }
+    const float lone_x = F::value(lone_w);
     if (lone >= 0) {
         const float x = lone_x < F::kFloor ? F::kFloor : lone_x;   // a NaN passes
         t.mx = fmaxf(t.mx, x);
@@ -555,8 +575,8 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
         // counting, on their keys with the pair's number in the low bits (which
         // makes them distinct, and the bound at most that much lower than the
         // maximum).  Each thread counts for its pair against half of them (against
-        // the threads' own 128 maxima 1.3 us a row, and 22 logits instead of 24 at
-        // the bound for 20 alternatives).
+        // the threads' own 128 maxima it took 0.7 us more a row under load, for 22
+        // logits instead of 24 at the bound of 20 alternatives).
         float bound = mx;
         if (a.top_k > 1) {
             const uint4* k4 = reinterpret_cast<const uint4*>(sh.pair_key) + (tid & 1) * (kPairs / 8);
@@ -722,10 +742,10 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
         return;
     }
     const float ls = logf(r.s);
-    if (tid < a.T) a.token_lp[m * a.T + tid] = tok < 0 ? -INFINITY : logp_of(tok_x, r.c, ls);
+    if (tid < a.T) a.token_lp[m * a.T + tid] = tok < 0 ? -INFINITY : logp_of(F::value(tok_w), r.c, ls);
     for (int i = tid + kThreads; i < a.T; i += kThreads) {
         const int64_t id = a.tokens[m * a.ldt + i];
-        a.token_lp[m * a.T + i] = id < 0 || id >= a.V ? -INFINITY : logp_of(F::at(row, id), r.c, ls);
+        a.token_lp[m * a.T + i] = id < 0 || id >= a.V ? -INFINITY : logp_of(value_at<F>(row, id), r.c, ls);
     }
     if (a.entropy && tid == 0) a.entropy[m] = fmaxf(ls - kLn2 * (r.w / r.s), 0.0f);
     if (tid < a.top_k) {
