@@ -286,3 +286,40 @@ def test_entropy_of_a_certain_token(dtype):
     H = q.logprobs(torch.from_numpy(x).to(DT[dtype]).cuda(), entropy=True).entropy.double().cpu().numpy()
     R = (4 + 2 * 104 + V / 128 + 32) * U
     assert (H >= 0).all() and (H <= R * (2 + 2 * math.log(V))).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,V,T,k,pad", [
+    (1700, 9001, 2, 7, 3), (800, 20011, 1, 32, 0), (2300, 2003, 1, 20, 5), (4000, 517, 3, 1, 0),   # several rows a CTA
+    (160, 131075, 1, 20, 0), (153, 200000, 1, 32, 8), (460, 70001, 1, 8, 1),                       # many turns a row
+    (150, 40009, 1, 20, 0), (70, 40009, 1, 32, 1), (30, 65539, 1, 20, 0), (12, 131072, 1, 32, 0),  # rows in 2 to 16 parts
+    (17, 2003, 130, 5, 0), (900, 1003, 129, 2, 1),                                                 # more tokens than threads
+])
+def test_many_rows_turns_and_parts(dtype, M, V, T, k, pad):
+    """Against 64 bits on the device, with the bounds above; logits on a coarse
+    grid in every other row, so that the alternatives tie across threads and parts."""
+    x = _logits(M, V, dtype, 3 * M + V, pad)
+    x[::2] = torch.round(x[::2].float() * 2).to(DT[dtype]) / 2
+    x[1::7, :: 3] = -INF
+    g = torch.Generator(device="cuda").manual_seed(M)
+    tok = torch.randint(-1, V + 1, (M, T), generator=g, device="cuda")
+    q = qg()
+    r = q.logprobs(x, tok, top_k=k, entropy=True)
+    assert q.last_device_status() == 0
+    for m0 in range(0, M, 200):
+        d = x[m0:m0 + 200].double()
+        lp = torch.log_softmax(d, dim=1)
+        H = torch.special.entr(lp.exp()).sum(dim=1)
+        low = torch.where(d == -INF, d.amax(dim=1, keepdim=True), d).amin(dim=1)
+        R = ((4 + 2 * (d.amax(dim=1) - low).clamp(max=104) + V / 128 + 32) * U)[:, None]
+        order = torch.sort(d, dim=1, descending=True, stable=True).indices[:, :k]
+        assert torch.equal(r.top_ids[m0:m0 + 200], order)
+        t = tok[m0:m0 + 200]
+        ref = lp.gather(1, t.clamp(0, V - 1)).masked_fill((t < 0) | (t >= V), -INF)
+        for got, want in ((r.top_logprobs[m0:m0 + 200], lp.gather(1, order)), (r.token_logprobs[m0:m0 + 200], ref)):
+            none = want == -INF
+            assert torch.equal(got.double() == -INF, none)
+            err = (got.double() - want).masked_fill(none, 0).abs()
+            assert bool((err <= R + 4 * U * (want.masked_fill(none, 0).abs() + (d.amax(dim=1) - low)[:, None])).all())
+        err = (r.entropy[m0:m0 + 200].double() - H).abs()
+        assert bool((err <= R[:, 0] * (2 + 2 * math.log(V) + 2 * H)).all())

@@ -30,13 +30,12 @@
 // loads).  Many small CTAs, because that end is a chain of block-wide steps and
 // the others' streaming hides it (three CTAs of 256 threads: 177 us for 4096 x
 // 131072 BF16 and 65 for 4096 x 32768, now 158 and 53); turns of eight vectors a
-// thread, because each costs a wait, a maximum and an arrival (of
-// four, 167 against 165 us and 57 against 53 when they were compared).
-// Bound by memory on long rows: 4096 x 131072 BF16 runs at the measured copy
-// rate.  Rows that are too few for the SMs are split over a cluster of up to 16
-// CTAs, which store their sums and lists to rank 0's shared memory, where they
-// are joined (no workspace, no atomics on memory, the same order of sums on every
-// call).
+// thread, because each costs a wait, a maximum and an arrival (of four, 167
+// against 165 us and 57 against 53 when they were compared).  Bound by memory on
+// long rows: 4096 x 131072 BF16 runs at the measured copy rate.  Rows that are too
+// few for the SMs are split over a cluster of up to 16 CTAs, which store their
+// sums and lists to rank 0's shared memory, where they are joined (no workspace,
+// no atomics on memory, the same order of sums on every call).
 #include <cstddef>
 
 #include <cuda_bf16.h>
@@ -457,8 +456,9 @@ struct Part {
 
 template <int kType>
 __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32_t rank, uint32_t S, Shared& sh,
-                                         const uint4* ring, uint64_t* joined, int stages, bool resident, int64_t next, int64_t& ahead, int& stage,
-                                         uint32_t& phase, const WaitCtl& wc) {
+                                         const uint4* ring, uint64_t* joined, int stages, bool resident,
+                                         int64_t next, int64_t& ahead, int& stage, uint32_t& phase,
+                                         const WaitCtl& wc) {
     using F = Fmt<kType>;
     const int tid = threadIdx.x;
     const int lane = tid & 31, warp = tid >> 5;
@@ -836,6 +836,18 @@ int parts_of(int M, int V, int sms) {
     return s;
 }
 
+// CTAs that take whole rows: as many as run at once, unless few of them would
+// take the last round, which reads slower than memory gives; then all take the
+// same number (800 x 131072 BF16: 48.6 us on 760 CTAs, 41.4 on 400; 1600: 77.8 and
+// 76.6 on 534; but 2500 with a third of them in the last round 105 and 112).
+int64_t row_ctas(int M, int sms) {
+    const int64_t most = static_cast<int64_t>(kCtasPerSm) * sms;
+    if (M <= most) return M;
+    const int64_t rounds = (M + most - 1) / most;
+    const int64_t last = M - (rounds - 1) * most;
+    return last * 8 < most ? (M + rounds - 1) / rounds : most;
+}
+
 // The ring's turns: what an SM's shared memory holds for its CTAs (two turns
 // each where there are four or more, four where there are two: 260 x 160000
 // FP32 38.5 -> 34.2 us, 128 x 131072 BF16, 20 alternatives, 17.5 -> 16.5).
@@ -847,13 +859,12 @@ int stages_of(int64_t ctas, int sms) {
 template <int kType>
 cudaError_t launch(const LogprobArgs& a, const LaunchCtl& c, cudaStream_t st) {
     const int parts = parts_of(a.M, a.V, c.num_sms);
-    const int most = kCtasPerSm * c.num_sms;
+    const int64_t ctas = parts > 1 ? static_cast<int64_t>(a.M) * parts : row_ctas(a.M, c.num_sms);
     // A CTA with one part to take needs no more of the ring than its turns (a
     // part has at most V / parts / kE + 1 vectors); one that runs on into
     // another row goes round all of it.
     const int turns = a.V / parts / (kTurn * Fmt<kType>::kE) + 1;
-    const bool one_part = parts > 1 || a.M <= most;
-    const int64_t ctas = parts > 1 ? static_cast<int64_t>(a.M) * parts : a.M < most ? a.M : most;
+    const bool one_part = parts > 1 || a.M == ctas;
     const int stages = stages_of(ctas, c.num_sms);
     const int ring_bytes = (one_part && turns < stages ? turns : stages) * kTurn * 16;
     static std::atomic<uint64_t> configured{0}, wide{0};
