@@ -64,7 +64,8 @@ struct I8Layout {
     static constexpr int kCtas = kPair ? 2 : 1;
     // up to 16 rows the activations are expanded in the kernel (warps 1 and 3,
     // alternate units); beyond, by the kernel in front (at 32 rows the two
-    // warps set the pace: 43.7 us against 34.5 on 32 x 32768 x 5120)
+    // warps set the pace: 43.7 us against 34.5 on 32 x 32768 x 5120; four took 37.9
+    // against 32.5, and eight at 64 rows 29.7 against 21.4 on 64 x 17408 x 5120)
     static constexpr bool kInlineX = NA <= 16;
     static constexpr int kXChunks = NA * 8 / 32;                // a lane's 16-byte pieces of a unit's codes
     static constexpr int kEpi = NA >= 128 ? 8 : 4;
