@@ -13,6 +13,11 @@
 // and 2^-12 of the value).  The floor is therefore the FP16 tensor rate for large M and
 // the weight bytes, read once as stored, for small M.
 //
+// What bounds a narrow tile is neither the conversion nor the copies but the
+// MMAs' reads of A: eight of 128 x 16 from TMEM take 0.29 us however few columns B
+// has (the MMA warp waits 130 cycles of a unit's 600 for its operands, the convert
+// warps wait for an A buffer), which is just above the memory's pace on all SMs.
+//
 // The output is tiled in 128 weight rows x NA activation rows (NA = the MMA's
 // N side); a unit is one tile x one 128-wide K block.  Weights stay 8-bit up
 // to the SM: TMA brings a unit's 128 x 128 bytes into a shared-memory ring
@@ -377,8 +382,17 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
             tma_load_2d(base + rw.slot * L::kWBytes, &tmW, wfull(rw.slot), cur.kr * 128,
                         (cur.tn * L::kCtas + static_cast<int>(rank)) * 128, pol);
         };
+        // The first kFirst copies, and the ring's others once the first has landed:
+        // with all of every CTA's on the way at once, some CTAs waited 6 us for
+        // their first unit, and a CTA is no faster than memory, so that they ended
+        // last (16 x 6144 x 5120 12.1 -> 10.8 us, 64 x 5120 x 17408 26.4 -> 25.0; with
+        // 3, 6 or 8 the same within 3%).
+        constexpr int kFirst = 4;
         if (lane == 0)
-            for (; issued < nunits && issued < kWStages; ++issued, cur.step(p, o), rw.step(1)) load_w();
+            for (; issued < nunits && issued < kWStages; ++issued, cur.step(p, o), rw.step(1)) {
+                if (issued == kFirst && !wait_bounded(wfull(0), 0, wc)) break;
+                load_w();
+            }
         __syncwarp();
         if constexpr (kPair || kClu) cluster_wait_all();   // of the arrival above
         if (lane == 0) {
