@@ -1093,15 +1093,14 @@ cudaError_t launch_int8_rows(const Int8Args& a, const Int8Schedule& s, const CUt
 // weights and activations per product, narrow ones spread a small product over
 // more SMs, split at a lower price, and the narrowest saves a launch (2 us of
 // the constant: the host's time, which bounds small calls).  Measured, whole
-// tiles / equal pieces / straddling: 256 x 5120 x 17408 at 128 rows 52.8 / - /
-// 44.7 us, at 256 rows 81.0 / 42.4 / 49.8 and 38.6 in clusters; 128 x 6144 x 5120
-// at 128 rows 19.3 / 17.6 / 22.7, at 256 rows 28.9 / 23.5 / 31.6; 64 x 5120 x 5120
-// at 64 rows 19.5 / 15.2 / 18.2 and 13.5; 1 x 1024 x 5120 at 16 rows 14.7 / 7.1 /
-// 8.7 and 7.0; 8 x 2048 x 8192 at 16 rows 22.4 / 8.4 / 9.6 and 9.0.  And by width
-// (16, 32, 64, 128, 256 rows), before clusters: 100 x 1000 x 1008 6.5 / 7.1 / 7.7 /
-// 8.8 / 11.2 us, 172 x 4218 x 1456 15.3 / 12.4 / 9.8 / 10.8 / 13.9, 64 x 5120 x
-// 5120 21.1 / 18.0 / 15.5 / 17.2 / 23.3; with them, 64 x 1024 x 8192 10.4 (16) and
-// 11.2 (64).
+// tiles / equal pieces / straddling / clusters: 256 x 5120 x 17408 at 256 rows
+// 81.0 / 42.4 / 49.8 / 38.6 us; 128 x 6144 x 5120 at 128 rows 19.0 / 17.5 / 22.4 /
+// 15.7; 64 x 5120 x 5120 at 64 rows 19.2 / 14.9 / 17.7 / 13.2; 1 x 1024 x 5120 at
+// 16 rows 14.8 / 7.0 / 8.8.  And the best of them by width (16, 32, 64, 128 rows):
+// 100 x 1000 x 1008 5.5 / 7.2 / 7.6 / 8.6 us, 172 x 4218 x 1456 14.5 / 12.0 / 9.2 /
+// 10.1, 64 x 5120 x 5120 20.0 / 16.8 / 13.2 / 14.4, 64 x 1024 x 8192 10.5 / 11.3 /
+// 11.2 / 12.5.  On 17 shapes of 1 to 172 rows the rule's choice took at most 2%
+// more than the best of all widths and forms.
 struct TileCost {
     int rows;
     long long call_ns, unit_ns, split_ns, straddle_ns;
