@@ -323,3 +323,57 @@ def test_many_rows_turns_and_parts(dtype, M, V, T, k, pad):
             assert bool((err <= R + 4 * U * (want.masked_fill(none, 0).abs() + (d.amax(dim=1) - low)[:, None])).all())
         err = (r.entropy[m0:m0 + 200].double() - H).abs()
         assert bool((err <= R[:, 0] * (2 + 2 * math.log(V) + 2 * H)).all())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("mask", [-INF, -1e9, "lowest", 0.5], ids=["inf", "1e9", "lowest", "tied"])
+@pytest.mark.parametrize("M,V,k", [(3, 131072, 8), (1, 20011, 32), (40, 40009, 20), (200, 9001, 5), (900, 5003, 7)])
+def test_few_tokens_left(dtype, mask, M, V, k):
+    """Masks that leave 0 to 40 tokens of a row, fewer than the alternatives
+    asked for in most: the rest are masked ones, lower index first (rows with
+    nothing left among them).  Bounds as above, D over the tokens left."""
+    if mask == "lowest":
+        mask = torch.finfo(DT[dtype]).min
+    if mask == -1e9 and dtype == "fp16":
+        mask = -6e4
+    g = torch.Generator(device="cuda").manual_seed(M + V + k)
+    x = torch.full((M, V), mask, dtype=DT[dtype], device="cuda")
+    left = torch.zeros((M, V), dtype=torch.bool, device="cuda")
+    for m in range(M):
+        n = m % 41
+        left[m, torch.randperm(V, generator=g, device="cuda")[:n]] = True
+    x[left] = torch.randn(int(left.sum()), generator=g, device="cuda").to(DT[dtype])
+    if V % 2:
+        x[:, V - 1] = x[:, 0]   # the last logit ties with the first
+    tok = torch.randint(0, V, (M, 2), generator=g, device="cuda")
+    q = qg()
+    r = q.logprobs(x, tok, top_k=k, entropy=True)
+    assert q.last_device_status() == 0
+    d = x.double()
+    lp = torch.where((d.amax(dim=1) == -INF)[:, None], torch.full_like(d, -INF), torch.log_softmax(d, dim=1))
+    order = torch.sort(d, dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(r.top_ids, order)
+    R = (4 + 2 * 16 + V / 128 + 32) * U   # the tokens left and 0.5 lie within 16 of each other
+    for got, want in ((r.top_logprobs, lp.gather(1, order)), (r.token_logprobs, lp.gather(1, tok))):
+        none = want == -INF
+        assert torch.equal(got.double() == -INF, none)
+        err = (got.double() - want).masked_fill(none, 0).abs()
+        assert bool((err <= R + 4 * U * want.masked_fill(none, 0).abs()).all())
+    H = torch.where(d.amax(dim=1) == -INF, 0.0, torch.special.entr(lp.exp()).sum(dim=1))
+    assert bool(((r.entropy.double() - H).abs() <= R * (2 + 2 * math.log(V) + 2 * H)).all())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_nan_among_ties(dtype):
+    """Rows of ties with a NaN somewhere: NaN throughout, and first in order."""
+    V, k = 40009, 9
+    x = torch.zeros((6, V), dtype=DT[dtype], device="cuda")
+    x[:, 7] = 1.0
+    at = [0, 5, 20000, 39999, 40008, 12345]
+    for m, v in enumerate(at):
+        x[m, v] = float("nan")
+    r = qg().logprobs(x, torch.zeros((6, 1), dtype=torch.int64, device="cuda"), top_k=k, entropy=True)
+    assert bool(torch.isnan(r.entropy).all()) and bool(torch.isnan(r.token_logprobs).all())
+    for m, v in enumerate(at):
+        rest = [i for i in range(k + 2) if i not in (7, v)]
+        assert r.top_ids[m].tolist() == ([v] + [7] + rest)[:k]

@@ -21,7 +21,9 @@
 //
 // Rows where this does not hold are worked out by the plain method at the end
 // of this file's row function: a maximum beyond +-1e8 (or at the floor: a row
-// of nothing but masks), a NaN or +inf, or more than kCap logits at the bound.
+// of nothing but masks), a NaN or +inf, or more than kCap logits above the bound.
+// (More than kCap at the bound, as where masks leave fewer tokens than are asked
+// for, are filled in by index.)
 //
 // Five CTAs per SM walk over the rows.  One warp of a CTA streams them into a
 // ring in shared memory by bulk copies, running on into the next row while the
@@ -249,15 +251,13 @@ struct Shared {
     float warp_s[kWarps], warp_w[kWarps];
     uint32_t warp_u[kWarps];
     alignas(16) uint32_t pair_key[kPairs];   // read four at a time
-    float bound;
+    float bound, tie;   // the bound, and the maximum that it was taken from
     float seg_mx[kSegs][kThreads];
     uint16_t flagged[kSegs * kThreads];   // seg * kThreads + thread
     int nflagged, ncand, nlist;
     PartSums parts[kMaxCluster];          // of a split row; written by the parts' CTAs, read by rank 0
     uint64_t list[kMaxTopK];              // the CTA's best entries, in order
     uint64_t cand[kCap];
-    uint32_t slow_keys[kMaxTopK];
-    int slow_ids[kMaxTopK];
 };
 
 // The barrier of the threads that take logits.
@@ -296,78 +296,177 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* buf) {
     return r;
 }
 
-// ----------------------------------------------------------------- the plain way
-// The top alternatives of a row, one distinct value at a time: the largest key
-// below the previous one, then its occurrences in index order.
+// The part of a row that one CTA of its cluster takes: up to 15 bytes of head,
+// vectors of 16 bytes, a tail; vectors [v0, v1) here, the head in the first
+// part and the tail in the last.
 template <int kType>
-__device__ __noinline__ void top_by_value(const void* row, int V, int k, Shared& sh) {
-    using F = Fmt<kType>;
-    int have = 0;
-    uint64_t below = 1ull << 32;   // keys under this are left
-    while (have < k) {
-        uint32_t best = 0u;
-        for (int v = threadIdx.x; v < V; v += kThreads) {
-            const uint32_t key = order_key(value_at<F>(row, v));
-            if (key < below) best = max(best, key);
-        }
-        best = block_max(best, sh.warp_u);
-        for (int v0 = 0; v0 < V && have < k; v0 += kThreads) {
-            const int v = v0 + threadIdx.x;
-            const bool hit = v < V && order_key(value_at<F>(row, v)) == best;
-            const uint32_t mask = __ballot_sync(0xffffffffu, hit);
-            meet();
-            if ((threadIdx.x & 31) == 0) sh.warp_u[threadIdx.x >> 5] = __popc(mask);
-            meet();
-            int before = 0, total = 0;
-#pragma unroll
-            for (int j = 0; j < kWarps; ++j) {
-                if (j < static_cast<int>(threadIdx.x >> 5)) before += sh.warp_u[j];
-                total += sh.warp_u[j];
-            }
-            const int at = have + before + __popc(mask & ((1u << (threadIdx.x & 31)) - 1u));
-            if (hit && at < k) {
-                sh.slow_keys[at] = best;
-                sh.slow_ids[at] = v;
-            }
-            have += total;
-        }
-        below = best;
+struct Part {
+    const uint8_t* row;
+    const uint4* vec;
+    int head, tail0, v0, v1, turns;
+    __device__ Part(const LogprobArgs& a, uint32_t m, uint32_t rank, uint32_t S) {
+        using F = Fmt<kType>;
+        row = static_cast<const uint8_t*>(a.logits) + int64_t{m} * a.ld * F::kSize;
+        head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / F::kSize;
+        if (head > a.V) head = a.V;
+        const int nv = (a.V - head) / F::kE;
+        const int lg = __ffs(S) - 1;   // S is a power of two
+        v0 = static_cast<int>(static_cast<int64_t>(nv) * rank >> lg);
+        v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) >> lg);
+        vec = reinterpret_cast<const uint4*>(row + head * F::kSize);
+        tail0 = head + nv * F::kE;
+        turns = (v1 - v0 + kTurn - 1) / kTurn;
     }
-    meet();
+};
+
+// A part with its share of the row's head and tail, for the ways that read it
+// again from memory.  They are functions of their own that work it out anew: as
+// part of the one pass they cost that its registers (158 -> 173 us on 4096 x
+// 131072 BF16).
+template <int kType>
+struct WholePart : Part<kType> {
+    int heads, tails;
+    __device__ WholePart(const LogprobArgs& a, uint32_t m, uint32_t rank, uint32_t S)
+        : Part<kType>(a, m, rank, S), heads(rank == 0 ? this->head : 0),
+          tails(rank == S - 1 ? a.V - this->tail0 : 0) {}
+};
+
+// fn(logit, its index) for this thread's share of a part, in no order.
+template <int kType, typename Fn>
+__device__ __forceinline__ void each_logit(const WholePart<kType>& part, Fn fn) {
+    using F = Fmt<kType>;
+    const int tid = threadIdx.x;
+    if (tid < part.heads) fn(value_at<F>(part.row, tid), tid);
+    if (tid < part.tails) fn(value_at<F>(part.row, part.tail0 + tid), part.tail0 + tid);
+#pragma unroll 4
+    for (int u = part.v0 + tid; u < part.v1; u += kThreads) {
+        const uint4 x = part.vec[u];
+        const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < F::kE; ++e) fn(F::element(raw, e), part.head + u * F::kE + e);
+    }
 }
 
+// Appends the largest logits of a part, from those of key `best` down, to the
+// `have` entries of sh.cand until there are k: one distinct value at a time, its
+// occurrences in index order.  Returns the entries there are (fewer than k where
+// the part has no more).
+template <int kType>
+__device__ __forceinline__ int top_from(const WholePart<kType>& part, uint32_t best, int have, int k, Shared& sh) {
+    using F = Fmt<kType>;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    while (have < k && best != 0u) {
+        // hits: a bit per logit from `index` on; the threads' are in index order
+        auto append = [&](uint32_t hits, uint32_t index) {
+            int upto = __popc(hits);
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int before = __shfl_up_sync(0xffffffffu, upto, s);
+                if (lane >= s) upto += before;
+            }
+            meet();
+            if (lane == 31) sh.warp_u[warp] = upto;
+            meet();
+            int at = have + upto - __popc(hits);
+            for (int j = 0; j < kWarps; ++j) {
+                if (j < warp) at += sh.warp_u[j];
+                have += sh.warp_u[j];
+            }
+            for (; hits != 0u && at < k; hits &= hits - 1u, ++at)
+                sh.cand[at] = static_cast<uint64_t>(best) << 32 | (0xFFFFFFFFu - (index + __ffs(hits) - 1));
+        };
+        if (part.heads > 0) append(tid < part.heads && order_key(value_at<F>(part.row, tid)) == best, tid);
+        for (int u0 = part.v0; u0 < part.v1 && have < k; u0 += kThreads) {
+            const int u = u0 + tid;
+            uint32_t hits = 0u;
+            if (u < part.v1) {
+                const uint4 x = part.vec[u];
+                const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < F::kE; ++e) hits |= (order_key(F::element(raw, e)) == best ? 1u : 0u) << e;
+            }
+            append(hits, part.head + u * F::kE);
+        }
+        if (part.tails > 0 && have < k)
+            append(tid < part.tails && order_key(value_at<F>(part.row, part.tail0 + tid)) == best, part.tail0 + tid);
+        if (have >= k) break;
+        uint32_t next = 0u;
+        each_logit(part, [&](float x, int) {
+            const uint32_t key = order_key(x);
+            if (key < best) next = max(next, key);
+        });
+        best = block_max(next, sh.warp_u);
+    }
+    meet();
+    return have < k ? have : k;
+}
+
+// The `need` largest of a part where more than kCap logits reach the bound that
+// was taken from the maximum `tie`, such as masked ones where fewer than top_k
+// are left: what is above the tie, then the tie and the values under it by index
+// (32 x 131072 BF16 with 5 tokens left, 8 asked for: 1650 us with the plain
+// method for such rows, now 22).  Returns the entries in sh.cand; more than kCap or
+// fewer than needed where this fails.
+template <int kType>
+__device__ __noinline__ int top_of_ties(const LogprobArgs& a, uint32_t m, uint32_t rank, uint32_t S, float tie,
+                                        int need, Shared& sh) {
+    const WholePart<kType> part(a, m, rank, S);
+    const uint32_t key = order_key(tie);
+    meet();   // everyone has read the count
+    if (threadIdx.x == 0) sh.ncand = 0;
+    meet();
+    uint32_t best = 0u;   // of the others
+    each_logit(part, [&](float x, int index) {
+        const uint32_t k = order_key(x);
+        if (k > key) {
+            const int at = atomicAdd(&sh.ncand, 1);
+            if (at < kCap) sh.cand[at] = entry_of(x, index);
+        } else {
+            best = max(best, k);
+        }
+    });
+    best = block_max(best, sh.warp_u);
+    const int n = sh.ncand;
+    return n < need ? top_from(part, best, n, need, sh) : n;
+}
+
+// ----------------------------------------------------------------- the plain way
 // A whole row by its definition: maximum, then sums of differences.
 template <int kType>
-__device__ __noinline__ void plain_row(const LogprobArgs& a, int64_t m, const void* row, Shared& sh) {
+__device__ __noinline__ void plain_row(const LogprobArgs& a, uint32_t m, Shared& sh) {
     using F = Fmt<kType>;
+    const WholePart<kType> part(a, m, 0, 1);
     uint32_t best = 0u;
-    for (int v = threadIdx.x; v < a.V; v += kThreads) best = max(best, order_key(value_at<F>(row, v)));
-    const float mx = key_value(block_max(best, sh.warp_u));
+    each_logit(part, [&](float x, int) { best = max(best, order_key(x)); });
+    best = block_max(best, sh.warp_u);
+    const float mx = key_value(best);
     const bool none = mx == -INFINITY;   // a row with nothing left
     float s = 0.0f, w = 0.0f;
     if (!none)
-        for (int v = threadIdx.x; v < a.V; v += kThreads) {
-            const float d = value_at<F>(row, v) - mx;
+        each_logit(part, [&](float x, int) {
+            const float d = x - mx;
             const float e = ex2(d * kLog2e);
             s += e;
             if (e != 0.0f) w += e * d;
-        }
+        });
     s = block_sum(s, sh.warp_s);
     w = block_sum(w, sh.warp_w);
     const float ls = logf(s);
     for (int t = threadIdx.x; t < a.T; t += kThreads) {
-        const int64_t id = a.tokens[m * a.ldt + t];
+        const int64_t id = a.tokens[int64_t{m} * a.ldt + t];
         const bool in = id >= 0 && id < a.V;
-        a.token_lp[m * a.T + t] = !in || none ? -INFINITY : value_at<F>(row, id) - mx - ls;
+        a.token_lp[int64_t{m} * a.T + t] = !in || none ? -INFINITY : value_at<F>(part.row, id) - mx - ls;
     }
     if (a.entropy && threadIdx.x == 0) a.entropy[m] = none ? 0.0f : ls - w / s;
     if (a.top_k > 0) {
-        top_by_value<kType>(row, a.V, a.top_k, sh);
+        top_from(part, best, 0, a.top_k, sh);
         if (threadIdx.x < a.top_k) {
-            a.top_ids[m * a.top_k + threadIdx.x] = sh.slow_ids[threadIdx.x];
-            a.top_lp[m * a.top_k + threadIdx.x] =
-                none ? -INFINITY : key_value(sh.slow_keys[threadIdx.x]) - mx - ls;
+            const uint64_t e = sh.cand[threadIdx.x];
+            a.top_ids[int64_t{m} * a.top_k + threadIdx.x] = entry_index(e);
+            a.top_lp[int64_t{m} * a.top_k + threadIdx.x] =
+                none ? -INFINITY : key_value(static_cast<uint32_t>(e >> 32)) - mx - ls;
         }
+        meet();   // before the next row's candidates
     }
 }
 
@@ -431,33 +530,10 @@ __device__ __forceinline__ float take(const uint4 (&x)[kN], float& mx, float& c,
     return top;
 }
 
-// The part of a row that one CTA of its cluster takes: up to 15 bytes of head,
-// vectors of 16 bytes, a tail; vectors [v0, v1) here, the head in the first
-// part and the tail in the last.
 template <int kType>
-struct Part {
-    const uint8_t* row;
-    const uint4* vec;
-    int head, tail0, v0, v1, turns;
-    __device__ Part(const LogprobArgs& a, int64_t m, uint32_t rank, uint32_t S) {
-        using F = Fmt<kType>;
-        row = static_cast<const uint8_t*>(a.logits) + m * a.ld * F::kSize;
-        head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / F::kSize;
-        if (head > a.V) head = a.V;
-        const int nv = (a.V - head) / F::kE;
-        const int lg = __ffs(S) - 1;   // S is a power of two
-        v0 = static_cast<int>(static_cast<int64_t>(nv) * rank >> lg);
-        v1 = static_cast<int>(static_cast<int64_t>(nv) * (rank + 1) >> lg);
-        vec = reinterpret_cast<const uint4*>(row + head * F::kSize);
-        tail0 = head + nv * F::kE;
-        turns = (v1 - v0 + kTurn - 1) / kTurn;
-    }
-};
-
-template <int kType>
-__device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32_t rank, uint32_t S, Shared& sh,
+__device__ __forceinline__ void take_row(const LogprobArgs& a, uint32_t m, uint32_t rank, uint32_t S, Shared& sh,
                                          const uint4* ring, uint64_t* joined, int stages, bool resident,
-                                         int64_t next, int64_t& ahead, int& stage, uint32_t& phase,
+                                         uint32_t next, int64_t& ahead, int& stage, uint32_t& phase,
                                          const WaitCtl& wc) {
     using F = Fmt<kType>;
     const int tid = threadIdx.x;
@@ -469,14 +545,14 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
 
     // the asked token's logit, on its way while the row is read, and the token
     // of the CTA's next row (its load and the logit's in a row cost 1 us a row)
-    int64_t tok = -1;
+    bool known = false;   // the token lies in the vocabulary
     typename F::Word tok_w = 0;
     if (rank == 0 && tid < a.T) {
         if (ahead >= 0 && ahead < a.V) {
-            tok = ahead;
-            tok_w = word_at<F>(row, tok);
+            known = true;
+            tok_w = word_at<F>(row, ahead);
         }
-        if (next < a.M) ahead = a.tokens[next * a.ldt + tid];
+        if (next < static_cast<uint32_t>(a.M)) ahead = a.tokens[int64_t{next} * a.ldt + tid];
     }
     int lone = -1;   // the index of the head or tail logit this thread takes
     if (rank == 0 && tid < head) lone = tid;
@@ -545,7 +621,8 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
 
     // the CTA's maximum and sums, and (for alternatives) the pairs' maxima
     const float own = t.mx;
-    float mx = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, 1));
+    const float pair = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, 1));
+    float mx = pair;
     const uint32_t key = (order_key(mx) & ~(kPairs - 1u)) | (kPairs - 1u - (tid >> 1));
     if ((tid & 1) == 0) sh.pair_key[tid >> 1] = key;
 #pragma unroll
@@ -587,8 +664,10 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
                 above += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
             }
             above += __shfl_xor_sync(0xffffffffu, above, 1);
-            if (above == a.top_k - 1)   // both threads of the pair
+            if (above == a.top_k - 1) {   // both threads of the pair
                 sh.bound = key_value(max(key & ~(kPairs - 1u), order_key(-INFINITY)));
+                sh.tie = pair;
+            }
             meet();
             bound = sh.bound;
         }
@@ -625,6 +704,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
                 y[e] = F::element(raw, e);
                 hits += (y[e] < F::kFloor ? F::kFloor : y[e]) >= bound;
             }
+            if (*static_cast<volatile int*>(&sh.ncand) > kCap) return;   // too many already
             int at = atomicAdd(&sh.ncand, hits);
 #pragma unroll
             for (int e = 0; e < F::kE; ++e)
@@ -640,7 +720,9 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
             const int round = ((f / kThreads) << per_lg) + (q & ((1 << per_lg) - 1));
             return v0 + round * kThreads + f % kThreads;
         };
-        const int all = nflagged << per_lg;
+        // (a marked stretch holds a logit at the bound or more: more than kCap of
+        // them need no count)
+        const int all = nflagged > kCap ? 0 : nflagged << per_lg;
         for (int q = tid; q < all; q += 4 * kThreads) {   // four loads in flight
             uint4 x[4];
             int u[4];
@@ -654,10 +736,12 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
                 if (u[j] < v1) look(x[j], u[j]);
         }
         meet();
-        const int n = sh.ncand;
-        // (fewer than asked for in a part that holds them: NaNs, which no bound sees)
+        int n = sh.nflagged > kCap ? kCap + 1 : sh.ncand;
         const int size = (v1 - v0) * F::kE + (rank == 0 ? head : 0) + (rank == S - 1 ? a.V - tail0 : 0);
-        bad = n > kCap || n < (a.top_k < size ? a.top_k : size);
+        const int need = a.top_k < size ? a.top_k : size;
+        if (n > kCap) n = top_of_ties<kType>(a, m, rank, S, a.top_k > 1 ? sh.tie : mx, need, sh);
+        // (fewer than asked for: NaNs, which no bound sees)
+        bad = n > kCap || n < need;
         if (!bad)
             for (int i = tid; i < n; i += kThreads) {
                 const uint64_t mine = sh.cand[i];
@@ -738,20 +822,20 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, int64_t m, uint32
 
     // not (a <= b) is also true of a NaN
     if (!(fabsf(r.mx) <= kFar) || r.mx <= F::kFloor + 500.0f || r.s != r.s || bad) {
-        plain_row<kType>(a, m, row, sh);
+        plain_row<kType>(a, m, sh);
         return;
     }
     const float ls = logf(r.s);
-    if (tid < a.T) a.token_lp[m * a.T + tid] = tok < 0 ? -INFINITY : logp_of(F::value(tok_w), r.c, ls);
+    if (tid < a.T) a.token_lp[int64_t{m} * a.T + tid] = known ? logp_of(F::value(tok_w), r.c, ls) : -INFINITY;
     for (int i = tid + kThreads; i < a.T; i += kThreads) {
-        const int64_t id = a.tokens[m * a.ldt + i];
-        a.token_lp[m * a.T + i] = id < 0 || id >= a.V ? -INFINITY : logp_of(value_at<F>(row, id), r.c, ls);
+        const int64_t id = a.tokens[int64_t{m} * a.ldt + i];
+        a.token_lp[int64_t{m} * a.T + i] = id < 0 || id >= a.V ? -INFINITY : logp_of(value_at<F>(row, id), r.c, ls);
     }
     if (a.entropy && tid == 0) a.entropy[m] = fmaxf(ls - kLn2 * (r.w / r.s), 0.0f);
     if (tid < a.top_k) {
         const uint64_t e = sh.list[tid];
-        a.top_ids[m * a.top_k + tid] = entry_index(e);
-        a.top_lp[m * a.top_k + tid] = logp_of(key_value(static_cast<uint32_t>(e >> 32)), r.c, ls);
+        a.top_ids[int64_t{m} * a.top_k + tid] = entry_index(e);
+        a.top_lp[int64_t{m} * a.top_k + tid] = logp_of(key_value(static_cast<uint32_t>(e >> 32)), r.c, ls);
     }
 }
 
@@ -780,8 +864,9 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
     const WaitCtl wc{timeout_ns, status, &sh.abort};
     grid_dependents_launch();
     grid_dependency_wait();
-    const int64_t row0 = blockIdx.x / S;
-    const int64_t rows = gridDim.x / S;   // rows in flight; more than one each only where S is 1
+    const uint32_t row0 = blockIdx.x / S;
+    const uint32_t rows = gridDim.x / S;   // rows in flight; more than one each only where S is 1
+    const uint32_t M = static_cast<uint32_t>(a.M);
 
     if (threadIdx.x >= kThreads) {
         if (threadIdx.x == kThreads) {
@@ -789,7 +874,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
             int issued = 0, slot = 0;
             uint32_t turned = 0u;   // parity of the times round the ring
             bool ok = true;
-            for (int64_t m = row0; m < a.M && ok; m += rows) {
+            for (uint32_t m = row0; m < M && ok; m += rows) {
                 const Part<kType> part(a, m, rank, S);
                 for (int n = 0; n < part.turns; ++n) {
                     if (issued >= stages) ok = wait_bounded(smem_u32(&sh.empty[slot]), turned ^ 1u, wc);
@@ -820,8 +905,8 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm)
     int stage = 0;
     uint32_t phase = 0;
     int64_t ahead = rank == 0 && threadIdx.x < a.T ? a.tokens[row0 * a.ldt + threadIdx.x] : -1;
-    for (int64_t m = row0; m < a.M; m += rows)
-        take_row<kType>(a, m, rank, S, sh, ring, joined, stages, rows >= a.M, m + rows, ahead, stage, phase, wc);
+    for (uint32_t m = row0; m < M; m += rows)
+        take_row<kType>(a, m, rank, S, sh, ring, joined, stages, rows >= M, m + rows, ahead, stage, phase, wc);
 }
 
 // CTAs per row: a power of two up to 16, so that the CTAs are at most two per
