@@ -13,10 +13,10 @@
 // and 2^-12 of the value).  The floor is therefore the FP16 tensor rate for large M and
 // the weight bytes, read once as stored, for small M.
 //
-// What bounds a narrow tile is neither the conversion nor the copies but the
-// MMAs' reads of A: eight of 128 x 16 from TMEM take 0.29 us however few columns B
-// has (the MMA warp waits 130 cycles of a unit's 600 for its operands, the convert
-// warps wait for an A buffer), which is just above the memory's pace on all SMs.
+// What bounds small M is the stream of weights, with 4 to 5 us of start and end
+// around it: 16 x 17408 x 5120 takes 19 us, 14.5 of them at 6.1 TB/s.  Neither the
+// MMAs nor the conversion does (one MMA a unit in place of eight: 19.1 -> 18.8 us,
+// twice as many 19.9; four convert groups in place of two: 19.5 -> 20.0).
 //
 // The output is tiled in 128 weight rows x NA activation rows (NA = the MMA's
 // N side); a unit is one tile x one 128-wide K block.  Weights stay 8-bit up
@@ -61,7 +61,8 @@ using gemm::Ring;
 
 constexpr int kWarpWProd = 0, kWarpXProd = 1, kWarpMma = 2, kWarpX2 = 3, kWarpEpi0 = 4;
 constexpr int kGroups = 2;   // convert groups of four warps
-constexpr int kMostPieces = 8;   // equal pieces that a tile is cut into
+constexpr int kMostPieces = 8;   // equal pieces of a tile in a cluster
+constexpr int kMostSplit = 16;   // pieces of a tile summed through the workspace
 
 // NA activation rows a tile; kPair: a tile is 256 weight rows on a CTA pair.
 template <int NA, bool kPair>
@@ -1083,7 +1084,7 @@ cudaError_t launch_int8_rows(const Int8Args& a, const Int8Schedule& s, const CUt
 // whole tiles cost floor(T / workers) tiles; for the tail of r tiles the rule
 // takes the cheapest of
 //   - one worker a tile: KU units
-//   - k = floor(workers / r) equal pieces of every tile: ceil(KU / k) units and
+//   - k <= floor(workers / r) equal pieces of every tile: ceil(KU / k) units and
 //     a split (storing, counting and summing partial results)
 //   - k equal pieces of every tile in a cluster, where all clusters run at once:
 //     ceil(KU / k) units and the exchange
@@ -1130,26 +1131,33 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
     long long g = 0;
     *cost = tc.call_ns + s.nfull * s.KU * tc.unit_ns;
     if (r > 0) {
+        // no tile in more than kMostSplit pieces, which one CTA sums in turn, and
+        // 0.2 us for each beyond 8 (1 x 128 x 17408 in 8 pieces 10.1 us, in 12 9.2, in
+        // 16 8.7, in 136 21.3; 1 x 1024 x 5120 7.0, 7.6, 8.0)
         auto up = [](long long a, long long b) { return (a + b - 1) / b; };
-        const long long all = w < r * s.KU ? w : r * s.KU;
+        long long all = w < r * s.KU ? w : r * s.KU;
+        if (all > r * kMostSplit && forced == 0) all = r * kMostSplit;
         const long long straddle = up(r * s.KU, all) * tc.unit_ns + tc.straddle_ns;
         long long best = s.KU * tc.unit_ns;
         g = r;
-        long long k = w / r;
-        if (k > kMostPieces) k = kMostPieces;
-        if (k > s.KU) k = s.KU;
-        if (k > 1 && up(s.KU, k) * tc.unit_ns + tc.split_ns < best) {
-            best = up(s.KU, k) * tc.unit_ns + tc.split_ns;
+        for (long long k = 2; k <= w / r && k <= kMostSplit && k <= s.KU; ++k) {
+            const long long cost_k = up(s.KU, k) * tc.unit_ns + tc.split_ns + (k > 8 ? (k - 8) * 200 : 0);
+            if (cost_k >= best) continue;
+            best = cost_k;
             g = k * r;
         }
         if (straddle < best || forced > 0) {
             best = straddle;
             g = all;
         }
-        // equal pieces in clusters, as many as run at once
+        // equal pieces in clusters, as many as run at once; of odd sizes, which share
+        // SM pairs with their neighbours, nine tenths of what the device states (64 x
+        // 8192 with 42 tiles in clusters of 3, of 46: 16.5 us, 45 tiles 19.6, 46 22.0;
+        // even sizes run to the last)
         if (tc.cluster_ns > 0 && s.nfull == 0 && forced == 0) {
             for (int c = 2; c * ctas <= kMostClusterCtas && c <= kMostPieces && c <= s.KU; ++c) {
-                if (s.T > clusters[c * ctas] || up(s.KU, c) * tc.unit_ns + tc.cluster_ns >= best) continue;
+                const int fit = c * ctas % 2 != 0 ? clusters[c * ctas] * 9 / 10 : clusters[c * ctas];
+                if (s.T > fit || up(s.KU, c) * tc.unit_ns + tc.cluster_ns >= best) continue;
                 best = up(s.KU, c) * tc.unit_ns + tc.cluster_ns;
                 g = static_cast<long long>(c) * r;
                 s.pieces = c;
