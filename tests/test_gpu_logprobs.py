@@ -377,3 +377,28 @@ def test_nan_among_ties(dtype):
     for m, v in enumerate(at):
         rest = [i for i in range(k + 2) if i not in (7, v)]
         assert r.top_ids[m].tolist() == ([v] + [7] + rest)[:k]
+
+
+def test_strided_tokens_on_another_stream():
+    """Expanded, transposed and sliced tokens with stream=: their copy is made
+    on that stream.  The current stream is kept busy, so that work left to it
+    would come too late; the tokens' memory was used for other tokens before."""
+    q = qg()
+    V, M = 33333, 6
+    x = _logits(M, V, "bf16", 15)
+    tok = torch.from_numpy(_tokens(M, 3, V)).cuda()
+    forms = [tok[:, :1].expand(M, 3), tok.t().contiguous().t(), tok[:1].expand(M, 3), tok[:, 0]]
+    expect = [q.logprobs(x, f.contiguous(), top_k=7, entropy=True) for f in forms]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    busy = torch.zeros(1 << 28, device="cuda")
+    for stream in (st, st.cuda_stream):
+        for f, want in zip(forms, expect):
+            for _ in range(8):
+                busy.add_(1.0)
+            got = q.logprobs(x, f, top_k=7, entropy=True, stream=stream)
+            st.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    torch.cuda.synchronize()
+    assert q.last_device_status() == 0

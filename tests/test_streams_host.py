@@ -1,0 +1,177 @@
+"""Which stream the entry points' own memory belongs to (no GPU): a call with
+``stream=`` makes its outputs, copies and intermediate tensors on that stream,
+where the kernel that writes or reads them runs.  Tensors, streams and the
+library are stand-ins that record the current stream."""
+import contextlib
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def built():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    import weight_only_quantized_qgemm_gb300 as q
+    return q
+
+
+class Device:
+    def __init__(self, index=0):
+        self.type, self.index = "cuda", index
+
+    def __eq__(self, other):
+        return isinstance(other, Device) and other.index == self.index
+
+    def __hash__(self):
+        return hash(self.index)
+
+
+class Stream:
+    def __init__(self, handle, device=0):
+        self.cuda_stream, self.device_index = int(handle), device
+
+
+class Tensor:
+    def __init__(self, world, shape, dtype, strides=None, device=None):
+        self.world, self.shape, self.dtype = world, tuple(shape), dtype
+        self.device, self.is_cuda = device or Device(), True
+        if strides is None:
+            strides, n = [], 1
+            for s in reversed(self.shape):
+                strides.insert(0, n)
+                n *= s
+        self.strides = tuple(strides)
+        world.made.append((self, world.current.cuda_stream))
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, d=None):
+        return self.strides if d is None else self.strides[d]
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def element_size(self):
+        return 1
+
+    def is_contiguous(self):
+        n = 1
+        for s, t in zip(reversed(self.shape), reversed(self.strides)):
+            if s != 1 and t != n:
+                return False
+            n *= s
+        return True
+
+    def contiguous(self):
+        return self if self.is_contiguous() else Tensor(self.world, self.shape, self.dtype, device=self.device)
+
+    def fill_(self, value):
+        self.world.made.append((self, self.world.current.cuda_stream))
+        return self
+
+    def __getitem__(self, item):
+        return self
+
+    def data_ptr(self):
+        return 0x100000
+
+
+class World:
+    """The stand-in for torch and the library: `made` holds (tensor, stream it
+    was made on), `calls` (entry point, stream that was current, arguments)."""
+
+    def __init__(self):
+        self.current = Stream(0)
+        self.device = 0
+        self.made, self.calls = [], []
+        self.cuda = self
+        self.Stream = Stream
+
+    def __getattr__(self, name):   # dtypes and the like
+        return getattr(torch, name)
+
+    # torch
+    def empty(self, shape, dtype=None, device=None):
+        return Tensor(self, shape, dtype)
+
+    def zeros(self, shape, dtype=None, device=None):
+        return Tensor(self, (shape,) if isinstance(shape, int) else shape, dtype)
+
+    # torch.cuda
+    def current_stream(self, device=None):
+        return self.current
+
+    def current_device(self):
+        return self.device
+
+    def default_stream(self, device=None):
+        return Stream(0)
+
+    def ExternalStream(self, handle, device=None):
+        return Stream(handle)
+
+    def synchronize(self, device=None):
+        pass
+
+    @contextlib.contextmanager
+    def stream(self, s):
+        before, device = self.current, self.device
+        self.current, self.device = s, s.device_index
+        try:
+            yield
+        finally:
+            self.current, self.device = before, device
+
+    # the library
+    def entry(self, name):
+        def call(*args):
+            self.calls.append((name, self.current.cuda_stream, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def world(built, monkeypatch):
+    w = World()
+
+    class Lib:
+        def __getattr__(self, name):
+            return (lambda *a: 4096) if name == "qg_workspace_bytes" else w.entry(name)
+
+    monkeypatch.setattr(built, "lib", Lib())
+    monkeypatch.setattr(built, "_torch", lambda: w)
+    monkeypatch.setattr(built, "_raw_stream", lambda index: w.current.cuda_stream)
+    monkeypatch.setattr(built, "_current_device", lambda: w.device, raising=False)
+    monkeypatch.setattr(built, "_dtype_codes", {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    monkeypatch.setattr(built, "_default_ws", {})
+    monkeypatch.setattr(built, "_ws_need", {})
+    w.q = built
+    return w
+
+
+SIDE = 0x7000
+
+
+def _check_side(w, before, name):
+    """All that was made since `before`, and the call, belong to the side stream."""
+    assert w.calls and w.calls[-1][0] == name and w.calls[-1][2][-1] == SIDE
+    made = w.made[before:]
+    assert made and all(s == SIDE for _, s in made), [(t.shape, s) for t, s in made]
+    assert w.current.cuda_stream == 0, "the caller's stream is current again"
+
+
+@pytest.mark.parametrize("stream", [Stream(SIDE), SIDE], ids=["object", "handle"])
+@pytest.mark.parametrize("strides", [(0, 0), (1, 7), (0, 1)], ids=["expanded", "transposed", "one row of tokens"])
+def test_logprobs_copies_strided_tokens_on_its_stream(world, stream, strides):
+    x = Tensor(world, (7, 100), torch.bfloat16)
+    tokens = Tensor(world, (7, 3), torch.int64, strides=strides)
+    n = len(world.made)
+    world.q.logprobs(x, tokens, top_k=2, entropy=True, stream=stream)
+    copies = [t for t, _ in world.made[n:] if t.dtype == torch.int64 and t.shape == (7, 3)]
+    assert len(copies) == 1
+    _check_side(world, n, "qg_logprobs")

@@ -145,6 +145,21 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_stream(stream, call, *args):
+    """call(*args) with `stream` (a torch stream or a raw handle) as the current
+    one, so that whatever the call allocates, copies or fills belongs to the
+    stream that its kernels run on.  (Made on the caller's stream, a copy would
+    not be ordered with the kernel, and memory of the caller's pool may still be
+    in use by work queued there.)"""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_ptr(stream)
+        # 0 and 1 are the legacy default stream
+        stream = torch.cuda.default_stream() if handle <= 1 else torch.cuda.ExternalStream(handle)
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
 def workspace_bytes(kind: int, M: int, N: int, K: int) -> int:
     """Device workspace a call needs on the current device (may be 0)."""
     return int(lib.qg_workspace_bytes(kind, M, N, K))
@@ -554,8 +569,11 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
     (optional): int64 [M] or [M, T]; top_k: 0 .. MAX_TOP_K and <= V.  A logit
     of -inf is a masked token; a row with nothing left has log probabilities
     of -inf and entropy 0; a token outside the vocabulary has -inf; a row with
-    a NaN or +inf gives NaN (see include/qgemm.h).
+    a NaN or +inf gives NaN (see include/qgemm.h).  With `stream`, the outputs
+    belong to that stream, as if the call were made under torch.cuda.stream(stream).
     """
+    if stream is not None:
+        return _on_stream(stream, logprobs, logits, tokens, top_k, entropy)
     torch = _lazy()
     f32, i64 = torch.float32, torch.int64
     code = _dtype_codes.get(logits.dtype)
@@ -589,7 +607,7 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
         ids = torch.empty((M, top_k), dtype=i64, device=dev)
         top = torch.empty((M, top_k), dtype=f32, device=dev)
         ids_p, top_p = ids.data_ptr(), top.data_ptr()
-    st = _raw_stream(dev.index) if stream is None else _stream_ptr(stream)
+    st = _raw_stream(dev.index)
     r = lib.qg_logprobs(logits.data_ptr(), code, ld, tok, ldt, T, token_p, ent_p, top_k, ids_p, top_p, M, V, st)
     if r:
         raise QgemmError(r, "qg_logprobs")
