@@ -175,3 +175,31 @@ def test_logprobs_copies_strided_tokens_on_its_stream(world, stream, strides):
     copies = [t for t, _ in world.made[n:] if t.dtype == torch.int64 and t.shape == (7, 3)]
     assert len(copies) == 1
     _check_side(world, n, "qg_logprobs")
+
+
+@pytest.mark.parametrize("stream", [Stream(SIDE), SIDE], ids=["object", "handle"])
+def test_int8_outputs_belong_to_the_call_s_stream(world, stream):
+    q = world.q
+    X = Tensor(world, (4, 64), torch.bfloat16)
+    n = len(world.made)
+    q.quantize_act_int8(X, stream=stream)
+    _check_side(world, n, "qg_quantize_act_int8")
+    Xq, W = Tensor(world, (4, 64), torch.int8), Tensor(world, (8, 64), torch.int8)
+    sx, sw = Tensor(world, (4,), torch.float32), Tensor(world, (8,), torch.float32)
+    n = len(world.made)
+    q.qgemm_w8a8_int8(Xq, sx, W, sw, out_dtype=torch.float16, stream=stream)   # Y and its stream's workspace
+    _check_side(world, n, "qgemm_w8a8_int8")
+    assert {t.dtype for t, _ in world.made[n:]} == {torch.float16, torch.uint8}
+    # the same call on the caller's stream has a workspace of its own
+    n = len(world.made)
+    q.qgemm_w8a8_int8(Xq, sx, W, sw)
+    assert [s for _, s in world.made[n:]] == [0, 0]
+
+
+def test_a_stream_of_zero_is_the_default_stream(world):
+    x = Tensor(world, (7, 100), torch.bfloat16)
+    with world.stream(Stream(SIDE)):
+        n = len(world.made)
+        world.q.logprobs(x, entropy=True, stream=0)
+        assert world.calls[-1][2][-1] == 0 and all(s == 0 for _, s in world.made[n:])
+        assert world.current.cuda_stream == SIDE

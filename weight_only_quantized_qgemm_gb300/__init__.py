@@ -455,8 +455,10 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
 
     X: CUDA [M, K] (row stride a multiple of 8, K % 16 == 0).  Returns (Xq
     int8 [M, K], X_scale float32 [M]).  Xq and X_scale (optional) are written
-    in place.
+    in place; with `stream`, those that the call allocates belong to that stream.
     """
+    if stream is not None:
+        return _on_stream(stream, quantize_act_int8, X, Xq, X_scale)
     torch = _lazy()
     code = _dtype_codes.get(X.dtype)
     if code != 0 and code != 1:
@@ -479,7 +481,7 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
             raise TypeError("X_scale must be contiguous float32")
         if X_scale.shape != (M,) or X_scale.device != dev:
             raise ValueError("X_scale must be [M] on X's device")
-    st = _raw_stream(dev.index) if stream is None else _stream_ptr(stream)
+    st = _raw_stream(dev.index)
     r = lib.qg_quantize_act_int8(X.data_ptr(), code, ld, Xq.data_ptr(), ldq, X_scale.data_ptr(), M, K, st)
     if r:
         raise QgemmError(r, "qg_quantize_act_int8")
@@ -495,7 +497,10 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
     :func:`quantize_act_int8` returns them; W: int8 [N, K] contiguous; W_scale:
     float32 [N]; bias (optional): float32 [N].  Y (optional): [M, N] with unit
     column stride, in bfloat16 (the default), float16 or float32 (out_dtype).
+    With `stream`, a Y that the call allocates belongs to that stream.
     """
+    if stream is not None:
+        return _on_stream(stream, qgemm_w8a8_int8, Xq, X_scale, W, W_scale, bias, out_dtype, Y, workspace)
     torch = _lazy()
     i8, f32 = torch.int8, torch.float32
     if Xq.dtype != i8 or W.dtype != i8:
@@ -533,7 +538,7 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
         rows, cols, ldy = _rows(Y, "Y")
         if rows != M or cols != N or Y.device != dev:
             raise ValueError("Y must be [M, N] on the same device")
-    st = _raw_stream(dev.index) if stream is None else _stream_ptr(stream)
+    st = _raw_stream(dev.index)
     ws, wsb = _workspace_for(KIND_INT8, M, N, K, workspace, dev, st)
     r = lib.qgemm_w8a8_int8(Xq.data_ptr(), ldq, X_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(), b,
                             Y.data_ptr(), code, ldy, M, N, K, ws, wsb, st)
