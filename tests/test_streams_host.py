@@ -203,3 +203,35 @@ def test_a_stream_of_zero_is_the_default_stream(world):
         world.q.logprobs(x, entropy=True, stream=0)
         assert world.calls[-1][2][-1] == 0 and all(s == 0 for _, s in world.made[n:])
         assert world.current.cuda_stream == SIDE
+
+
+def _older_calls(w):
+    q, T, K = w.q, lambda *a, **k: Tensor(w, *a, **k), 256
+    bf = lambda r: T((r, K), torch.bfloat16)     # noqa: E731
+    codes = lambda n: (T((n, K), torch.uint8), T((-(-n // 128), 2), torch.float32))   # noqa: E731
+    lut = (T((1 << 14,), torch.uint8), T((8,), torch.float16), T((128, 2), torch.float16), 128)
+    return {
+        "qgemm_fp8_block": lambda st: q.qgemm_fp8_block(bf(4), *codes(128), stream=st),
+        "qgemm_fp8_block_multi": lambda st: q.qgemm_fp8_block_multi(bf(4), [codes(128), codes(200)], stream=st),
+        "qgemm_lut3": lambda st: q.qgemm_lut3(T((4, K), torch.float16), *lut, stream=st),
+        "qgemm_bf16": lambda st: q.qgemm_bf16(bf(4), bf(128), stream=st),
+        "qg_quantize_act_e4m3": lambda st: q.quantize_act_e4m3(bf(4), stream=st),
+        "qgemm_w8a8_block": lambda st: q.qgemm_w8a8(bf(4), *codes(128), stream=st),
+        "qg_debug_fp8_split": lambda st: q.debug_fp8_split(T((3, 128), torch.bfloat16), stream=st),
+        "qg_dequant_lut3": lambda st: q.dequant_lut3(*lut, K, stream=st),
+    }
+
+
+@pytest.mark.parametrize("name", ["qgemm_fp8_block", "qgemm_fp8_block_multi", "qgemm_lut3", "qgemm_bf16",
+                                  "qg_quantize_act_e4m3", "qgemm_w8a8_block", "qg_debug_fp8_split", "qg_dequant_lut3"])
+def test_outputs_of_every_entry_point_belong_to_its_stream(world, monkeypatch, name):
+    monkeypatch.setattr(world.q, "lut3_packed_bytes", lambda N, K: 1 << 14)
+    world.calls.clear()
+    _older_calls(world)[name](SIDE)
+    inputs = [t for t, s in world.made if s == 0]
+    assert all(c[2][-1] == SIDE for c in world.calls) and world.calls[-1][0] == name
+    assert len(world.made) > len(inputs)
+    # what the call made itself: everything that is not one of its inputs
+    outputs = {"qgemm_fp8_block": 2, "qgemm_fp8_block_multi": 3, "qgemm_lut3": 2, "qgemm_bf16": 2,
+               "qg_quantize_act_e4m3": 2, "qgemm_w8a8_block": 4, "qg_debug_fp8_split": 3, "qg_dequant_lut3": 1}
+    assert sum(s == SIDE for _, s in world.made) == outputs[name]

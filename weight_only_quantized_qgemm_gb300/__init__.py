@@ -30,6 +30,10 @@ The names follow the C ABI in ``include/qgemm.h``:
 * :func:`debug_fp8_split` / :func:`dequant_lut3` -- test aids: the FP8
   kernel's activation split and the LUT3 kernel's dequantiser on their own,
   exposed for value-by-value checks.
+
+A call with ``stream=`` (a torch stream or a raw handle) is the call made under
+``torch.cuda.stream(stream)``: its kernels run there, and the tensors that it
+allocates belong to that stream.
 """
 from __future__ import annotations
 
@@ -232,6 +236,8 @@ def qgemm_fp8_block(X, W, W_scale, Y=None, workspace=None, stream=None):
     float8_e4m3fn [N, K] contiguous; W_scale: float32 [ceil(N/128), ceil(K/128)]
     contiguous.  Y (optional): bf16 [M, N] with unit column stride.
     """
+    if stream is not None:
+        return _on_stream(stream, qgemm_fp8_block, X, W, W_scale, Y, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16:
         raise TypeError("X must be bfloat16")
@@ -245,9 +251,9 @@ def qgemm_fp8_block(X, W, W_scale, Y=None, workspace=None, stream=None):
         raise ValueError("shape mismatch between X, W and W_scale")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, X.device, stream)
+    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, X.device)
     _check(lib.qgemm_fp8_block(X.data_ptr(), _ld(X), W.data_ptr(), W_scale.data_ptr(), Y.data_ptr(),
-                               _ld(Y), M, N, K, ws, wsb, _stream_ptr(stream)), "qgemm_fp8_block")
+                               _ld(Y), M, N, K, ws, wsb, _stream_ptr(None)), "qgemm_fp8_block")
     return Y
 
 
@@ -265,6 +271,8 @@ def qgemm_fp8_block_multi(X, weights, Ys=None, workspace=None, stream=None):
     (1 to MAX_SEGMENTS of them, sharing X), in one launch; returns the list of
     Y_j (BF16 [M, N_j]).  Ys (optional): the output tensors, each with unit
     column stride."""
+    if stream is not None:
+        return _on_stream(stream, qgemm_fp8_block_multi, X, weights, Ys, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16:
         raise TypeError("X must be bfloat16")
@@ -285,9 +293,9 @@ def qgemm_fp8_block_multi(X, weights, Ys=None, workspace=None, stream=None):
         outs.append(Y)
         segs[j] = Fp8Segment(W.data_ptr(), S.data_ptr(), Y.data_ptr(), _ld(Y), N)
         rows += -(-N // 128) * 128
-    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, rows, K, workspace, X.device, stream)
+    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, rows, K, workspace, X.device)
     _check(lib.qgemm_fp8_block_multi(X.data_ptr(), _ld(X), ctypes.cast(segs, ctypes.c_void_p), len(weights), M, K,
-                                     ws, wsb, _stream_ptr(stream)), "qgemm_fp8_block_multi")
+                                     ws, wsb, _stream_ptr(None)), "qgemm_fp8_block_multi")
     return outs
 
 
@@ -305,6 +313,8 @@ def qgemm_fp8_block_host(X, W, W_scale, Y=None, X_stage=None, workspace=None, st
     kept when absent.  The call is asynchronous: Y is complete after the
     stream is synchronised.
     """
+    if stream is not None:
+        return _on_stream(stream, qgemm_fp8_block_host, X, W, W_scale, Y, X_stage, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16:
         raise TypeError("X must be bfloat16")
@@ -329,9 +339,9 @@ def qgemm_fp8_block_host(X, W, W_scale, Y=None, X_stage=None, workspace=None, st
                                                              device=W.device)
     elif not X_stage.is_cuda or X_stage.numel() * X_stage.element_size() < M * K * 2:
         raise ValueError("X_stage must be a device buffer of at least M*K bfloat16 elements")
-    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, W.device, stream)
+    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, W.device)
     _check(lib.qgemm_fp8_block_host(X.data_ptr(), _ld(X), W.data_ptr(), W_scale.data_ptr(), Y.data_ptr(),
-                                    _ld(Y), M, N, K, X_stage.data_ptr(), ws, wsb, _stream_ptr(stream)),
+                                    _ld(Y), M, N, K, X_stage.data_ptr(), ws, wsb, _stream_ptr(None)),
            "qgemm_fp8_block_host")
     return Y
 
@@ -342,6 +352,8 @@ def qgemm_lut3(X, Wq, qmap, scales, N: int, Y=None, workspace=None, stream=None)
     X: fp16 CUDA [M, K]; Wq: the packed bytes from :func:`pack_lut3` on the
     device; qmap: fp16 [8]; scales: fp16 [N, K/128] contiguous.
     """
+    if stream is not None:
+        return _on_stream(stream, qgemm_lut3, X, Wq, qmap, scales, N, Y, workspace)
     torch = _torch()
     if X.dtype != torch.float16 or qmap.dtype != torch.float16 or scales.dtype != torch.float16:
         raise TypeError("X, qmap and scales must be float16")
@@ -352,9 +364,9 @@ def qgemm_lut3(X, Wq, qmap, scales, N: int, Y=None, workspace=None, stream=None)
         raise ValueError("packed weights are smaller than pack_lut3 produces for this shape")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.float16, device=X.device)
-    ws, wsb = _workspace_for(KIND_LUT3, M, N, K, workspace, X.device, stream)
+    ws, wsb = _workspace_for(KIND_LUT3, M, N, K, workspace, X.device)
     _check(lib.qgemm_lut3(X.data_ptr(), _ld(X), Wq.data_ptr(), qmap.data_ptr(), scales.data_ptr(),
-                          Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(stream)), "qgemm_lut3")
+                          Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(None)), "qgemm_lut3")
     return Y
 
 
@@ -368,6 +380,8 @@ def quantize_act_e4m3(X, Xq=None, X_scale=None, stream=None):
     float32 [ceil(K/128), ldsx] with ldsx = M rounded up to 32; columns
     [M, ldsx) are 0).  Xq and X_scale (optional) are written in place.
     """
+    if stream is not None:
+        return _on_stream(stream, quantize_act_e4m3, X, Xq, X_scale)
     torch = _torch()
     if X.dtype != torch.bfloat16:
         raise TypeError("X must be bfloat16")
@@ -382,7 +396,7 @@ def quantize_act_e4m3(X, Xq=None, X_scale=None, stream=None):
     if tuple(Xq.shape) != (M, K) or X_scale.shape[0] != KB:
         raise ValueError("shape mismatch between X, Xq and X_scale")
     _check(lib.qg_quantize_act_e4m3(X.data_ptr(), _ld(X), Xq.data_ptr(), _ld(Xq), X_scale.data_ptr(),
-                                    _ld(X_scale), M, K, _stream_ptr(stream)), "qg_quantize_act_e4m3")
+                                    _ld(X_scale), M, K, _stream_ptr(None)), "qg_quantize_act_e4m3")
     return Xq, X_scale
 
 
@@ -390,6 +404,8 @@ def qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=None, workspace=None, stream=Non
     """Y[M, N] = sum over 128-wide K blocks kb of X_scale[kb, m] *
     W_scale[n/128, kb] * (Xq[m, kb] . W[n, kb]) (E4M3 x E4M3, FP32 fold, BF16
     out), with Xq, X_scale as :func:`quantize_act_e4m3` returns them."""
+    if stream is not None:
+        return _on_stream(stream, qgemm_w8a8_block, Xq, X_scale, W, W_scale, Y, workspace)
     torch = _torch()
     if Xq.dtype not in (torch.uint8, torch.float8_e4m3fn) or W.dtype not in (torch.uint8, torch.float8_e4m3fn):
         raise TypeError("Xq and W must hold E4M3 codes (uint8 or float8_e4m3fn)")
@@ -403,9 +419,9 @@ def qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=None, workspace=None, stream=Non
         raise ValueError("shape mismatch between Xq, X_scale, W and W_scale")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=Xq.device)
-    ws, wsb = _workspace_for(KIND_W8A8, M, N, K, workspace, Xq.device, stream)
+    ws, wsb = _workspace_for(KIND_W8A8, M, N, K, workspace, Xq.device)
     _check(lib.qgemm_w8a8_block(Xq.data_ptr(), _ld(Xq), X_scale.data_ptr(), _ld(X_scale), W.data_ptr(),
-                                W_scale.data_ptr(), Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(stream)),
+                                W_scale.data_ptr(), Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(None)),
            "qgemm_w8a8_block")
     return Y
 
@@ -413,8 +429,10 @@ def qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=None, workspace=None, stream=Non
 def qgemm_w8a8(X, W, W_scale, Y=None, workspace=None, stream=None):
     """The W8A8 path from BF16 activations: :func:`quantize_act_e4m3` then
     :func:`qgemm_w8a8_block` (two launches on one stream)."""
-    Xq, X_scale = quantize_act_e4m3(X, stream=stream)
-    return qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=Y, workspace=workspace, stream=stream)
+    if stream is not None:
+        return _on_stream(stream, qgemm_w8a8, X, W, W_scale, Y, workspace)
+    Xq, X_scale = quantize_act_e4m3(X)
+    return qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=Y, workspace=workspace)
 
 
 _dtype_codes = {}
@@ -455,7 +473,7 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
 
     X: CUDA [M, K] (row stride a multiple of 8, K % 16 == 0).  Returns (Xq
     int8 [M, K], X_scale float32 [M]).  Xq and X_scale (optional) are written
-    in place; with `stream`, those that the call allocates belong to that stream.
+    in place.
     """
     if stream is not None:
         return _on_stream(stream, quantize_act_int8, X, Xq, X_scale)
@@ -497,7 +515,6 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
     :func:`quantize_act_int8` returns them; W: int8 [N, K] contiguous; W_scale:
     float32 [N]; bias (optional): float32 [N].  Y (optional): [M, N] with unit
     column stride, in bfloat16 (the default), float16 or float32 (out_dtype).
-    With `stream`, a Y that the call allocates belongs to that stream.
     """
     if stream is not None:
         return _on_stream(stream, qgemm_w8a8_int8, Xq, X_scale, W, W_scale, bias, out_dtype, Y, workspace)
@@ -574,8 +591,7 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
     (optional): int64 [M] or [M, T]; top_k: 0 .. MAX_TOP_K and <= V.  A logit
     of -inf is a masked token; a row with nothing left has log probabilities
     of -inf and entropy 0; a token outside the vocabulary has -inf; a row with
-    a NaN or +inf gives NaN (see include/qgemm.h).  With `stream`, the outputs
-    belong to that stream, as if the call were made under torch.cuda.stream(stream).
+    a NaN or +inf gives NaN (see include/qgemm.h).
     """
     if stream is not None:
         return _on_stream(stream, logprobs, logits, tokens, top_k, entropy)
@@ -625,6 +641,8 @@ def qgemm_bf16(X, W, Y=None, workspace=None, stream=None):
     X: bf16 CUDA [M, K] (row stride a multiple of 8); W: bf16 [N, K]
     contiguous; Y (optional): bf16 [M, N] with unit column stride.
     """
+    if stream is not None:
+        return _on_stream(stream, qgemm_bf16, X, W, Y, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
         raise TypeError("X and W must be bfloat16")
@@ -636,9 +654,9 @@ def qgemm_bf16(X, W, Y=None, workspace=None, stream=None):
         raise ValueError("shape mismatch between X and W")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    ws, wsb = _workspace_for(KIND_BF16, M, N, K, workspace, X.device, stream)
+    ws, wsb = _workspace_for(KIND_BF16, M, N, K, workspace, X.device)
     _check(lib.qgemm_bf16(X.data_ptr(), _ld(X), W.data_ptr(), Y.data_ptr(), _ld(Y), M, N, K, ws, wsb,
-                          _stream_ptr(stream)), "qgemm_bf16")
+                          _stream_ptr(None)), "qgemm_bf16")
     return Y
 
 
@@ -668,6 +686,8 @@ def debug_fp8_split(X, stream=None):
     """The FP8 GEMM's activation split of BF16 X [B, 128] (one 128-wide K
     block per row): returns (hi, lo, e) with hi, lo uint8 E4M3 codes [B, 128]
     and e int32 [B], such that x * 2^e = hi + lo / 16 (see include/qgemm.h)."""
+    if stream is not None:
+        return _on_stream(stream, debug_fp8_split, X)
     torch = _torch()
     if X.dtype != torch.bfloat16 or X.dim() != 2 or X.shape[1] != 128 or not X.is_contiguous():
         raise ValueError("X must be a contiguous bfloat16 [B, 128] tensor")
@@ -675,18 +695,20 @@ def debug_fp8_split(X, stream=None):
     hi = torch.empty((B, 128), dtype=torch.uint8, device=X.device)
     lo = torch.empty((B, 128), dtype=torch.uint8, device=X.device)
     e = torch.empty((B,), dtype=torch.int32, device=X.device)
-    _check(lib.qg_debug_fp8_split(X.data_ptr(), B, hi.data_ptr(), lo.data_ptr(), e.data_ptr(), _stream_ptr(stream)),
+    _check(lib.qg_debug_fp8_split(X.data_ptr(), B, hi.data_ptr(), lo.data_ptr(), e.data_ptr(), _stream_ptr(None)),
            "qg_debug_fp8_split")
     return hi, lo, e
 
 
 def dequant_lut3(Wq, qmap, scales, N: int, K: int, out=None, stream=None):
     """Packed LUT3 weights -> FP16 [N, K], with the LUT3 GEMM's own dequantiser."""
+    if stream is not None:
+        return _on_stream(stream, dequant_lut3, Wq, qmap, scales, N, K, out)
     torch = _torch()
     if out is None:
         out = torch.empty((N, K), dtype=torch.float16, device=Wq.device)
     _check(lib.qg_dequant_lut3(Wq.data_ptr(), qmap.data_ptr(), scales.data_ptr(), out.data_ptr(), N, K,
-                               _stream_ptr(stream)), "qg_dequant_lut3")
+                               _stream_ptr(None)), "qg_dequant_lut3")
     return out
 
 
