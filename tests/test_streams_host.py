@@ -235,3 +235,25 @@ def test_outputs_of_every_entry_point_belong_to_its_stream(world, monkeypatch, n
     outputs = {"qgemm_fp8_block": 2, "qgemm_fp8_block_multi": 3, "qgemm_lut3": 2, "qgemm_bf16": 2,
                "qg_quantize_act_e4m3": 2, "qgemm_w8a8_block": 4, "qg_debug_fp8_split": 3, "qg_dequant_lut3": 1}
     assert sum(s == SIDE for _, s in world.made) == outputs[name]
+
+
+def test_tensors_of_another_device_are_refused(world):
+    """The library launches on the current device: tensors of another one are
+    refused before the call, under a stream of this device too."""
+    q, other = world.q, Device(1)
+
+    def T(*shape, dtype=torch.int8):
+        return Tensor(world, shape, dtype, device=other)
+
+    f = torch.float32
+    for stream in (None, SIDE):
+        for call in (lambda: q.quantize_act_int8(T(4, 64, dtype=torch.bfloat16), stream=stream),
+                     lambda: q.qgemm_w8a8_int8(T(4, 64), T(4, dtype=f), T(8, 64), T(8, dtype=f), stream=stream),
+                     lambda: q.logprobs(T(4, 100, dtype=f), entropy=True, stream=stream)):
+            with pytest.raises(ValueError, match="current CUDA device"):
+                call()
+    assert not world.calls
+    with world.stream(Stream(SIDE, device=1)):   # which makes device 1 current
+        q.logprobs(T(4, 100, dtype=f), entropy=True)
+    q.logprobs(T(4, 100, dtype=f), entropy=True, stream=Stream(SIDE, device=1))
+    assert len(world.calls) == 2

@@ -437,17 +437,19 @@ def qgemm_w8a8(X, W, W_scale, Y=None, workspace=None, stream=None):
 
 _dtype_codes = {}
 _raw_stream = None
+_current_device = None
 
 
 def _lazy():
     """torch, with what the entry points below look up on every call."""
-    global _raw_stream
+    global _raw_stream, _current_device
     torch = _torch()
     if not _dtype_codes:
         # the current stream of a device, without building a stream object
         # (0.1 us instead of 3 us a call)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: int(torch.cuda.current_stream(index).cuda_stream))
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})   # QG_BF16, QG_FP16, QG_FP32
     return torch
 
@@ -463,6 +465,8 @@ def _rows(t, what: str):
         raise ValueError(what + " must have unit stride in its last dimension")
     if not t.is_cuda:
         raise ValueError(what + " must be on a CUDA device")
+    if t.device.index != _current_device():   # where the library launches
+        raise ValueError(what + " must be on the current CUDA device")
     return r, c, (ld if r > 1 else c)
 
 
