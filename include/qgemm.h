@@ -61,7 +61,8 @@ typedef enum {
     QG_OK = 0,
     QG_ERR_INVALID_ARG = 1,       /* null pointer, negative size, ld < row length */
     QG_ERR_UNSUPPORTED_SHAPE = 2, /* M > 32 (65536 for W8A8, INT8), K % 16 (FP8, W8A8, INT8), K % 128 (LUT3)
-                                     or K % 8 (BF16) != 0; log probabilities: V == 0 or > 2^30, top_k > V or
+                                     or K % 8 (BF16) != 0, more than 2^29 tiles
+                                     of 128 x 32 (W8A8) or 128 x 16 (INT8); log probabilities: V == 0 or > 2^30, top_k > V or
                                      > QG_MAX_TOP_K */
     QG_ERR_MISALIGNED = 3,        /* a pointer or row stride breaks the 16-byte rule */
     QG_ERR_CUDA = 4,              /* a CUDA runtime call or kernel launch failed */

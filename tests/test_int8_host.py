@@ -1,5 +1,8 @@
 """Host-side checks of the 8-bit integer and log-probability entry points (no
 GPU): arguments are refused before anything is enqueued."""
+import subprocess
+import sys
+
 import pytest
 
 
@@ -122,3 +125,31 @@ def test_schedule_rule_invariants(qg):
                     assert rows in (16, 32, 64, 128, 256) and (rows < 2 * M or rows == 16)
                     assert 1 <= g <= max(sms, 2) and (rows < 128 or g % 2 == 0), (M, N, K, sms, rows, g)
     assert qg.int8_tile_rows(0, 1, 16, 152) == 0 and qg.int8_tile_rows(1, 1, 16, 0) == 0
+
+
+@pytest.mark.parametrize("kind,M,N,K", [
+    (4, 65536, 2 ** 31 - 1, 16), (4, 65536, 2 ** 30, 5120), (4, 65536, 2 ** 24 + 1, 2 ** 31 - 16), (4, 32769, 2 ** 25, 16),
+    (3, 65536, 2 ** 31 - 1, 16), (3, 65536, 2 ** 30, 5120), (3, 65536, 2 ** 25 + 1, 2 ** 31 - 16), (3, 32769, 2 ** 26, 16),
+])
+def test_too_many_tiles_are_refused(qg, kind, M, N, K):
+    """More than 2^29 tiles (whose number leaves an int): the questions about
+    the schedule answer 0 and none divides by zero.  In a process of its own."""
+    code = (f"import weight_only_quantized_qgemm_gb300 as q; k, s = {kind}, ({M}, {N}, {K})\n"
+            "print([q.dispatch_rule(k, *s, n) for n in (1, 76, 152)], q.workspace_bytes(k, *s), q.dispatch_get(k, *s),\n"
+            "      q.lib.qg_dispatch_set(k, *s, 1), q.int8_tile_rows(*s, 152) if k == 4 else 0)")
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert p.returncode == 0, (p.returncode, p.stderr[-500:])
+    assert p.stdout.split("\n")[0] == "[0, 0, 0] 0 0 2 0"
+
+
+@pytest.mark.parametrize("M,N,K", [(65536, 2 ** 24, 16), (65536, 2 ** 24, 2 ** 20), (65536, 2 ** 24, 2 ** 31 - 16),
+                                   (1, 2 ** 31 - 1, 16), (1, 2 ** 31 - 1, 2 ** 31 - 16)])
+def test_the_most_tiles_have_a_schedule(qg, M, N, K):
+    """At the limit itself, with short and long K, the rule answers as for any
+    shape, with tiles as wide as a long K asks for."""
+    for sms in (1, 76, 152):
+        rows, g = qg.int8_tile_rows(M, N, K, sms), qg.dispatch_rule(qg.KIND_INT8, M, N, K, sms)
+        assert rows == (16 if M == 1 else rows) and rows in (16, 32, 64, 128, 256)
+        assert 1 <= g <= max(sms, 2), (sms, rows, g)
+        if M > 1 and K >= 2 ** 20 and sms > 1:
+            assert rows == 256, (sms, rows)

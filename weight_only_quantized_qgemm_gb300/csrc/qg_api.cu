@@ -164,15 +164,25 @@ int table_lookup(int kind, int M, int N, int K) {
     return 0;
 }
 
+// Tiles are indexed by int, with four arrival counters each (W8A8) to spare:
+// 2^29 of the narrowest ones at most.  Every entry point that builds a schedule
+// asks this first.
+bool too_many_tiles(int kind, int M, int N) {
+    const int64_t rows = kind == QG_KIND_W8A8 ? 32 : kind == QG_KIND_INT8 ? 16 : M;
+    return (static_cast<int64_t>(N) + 127) / 128 * ((M + rows - 1) / rows) > (int64_t(1) << 29);
+}
+
 // The schedule of a shape on `sms` SMs, with `forced` > 0 a dispatch-table grid.
 Int8Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced, const int* clusters) {
     if (kind == QG_KIND_INT8) return int8_schedule(M, N, K, sms, forced, clusters);
     Int8Schedule s;
     s.nmma = kind == QG_KIND_W8A8 ? w8a8_tile_rows(M) : M <= 16 ? 16 : 32;
     // W8A8 tiles are 128 weight rows x nmma activation rows, weight-tile-major
-    s.T = (N + 127) / 128 * (kind == QG_KIND_W8A8 ? (M + s.nmma - 1) / s.nmma : 1);
+    s.T = static_cast<int>((static_cast<int64_t>(N) + 127) / 128) *
+          (kind == QG_KIND_W8A8 ? (M + s.nmma - 1) / s.nmma : 1);
     // one unit = 128 rows x one 128-wide K block (W8A8: two blocks)
-    s.KU = kind == QG_KIND_W8A8 ? (K + 255) / 256 : (K + 127) / 128;
+    const int unit = kind == QG_KIND_W8A8 ? 256 : 128;
+    s.KU = static_cast<int>((static_cast<int64_t>(K) + unit - 1) / unit);
     s.U = static_cast<long long>(s.T) * s.KU;
     const bool unit_bound = kind == QG_KIND_W8A8 || (kind == QG_KIND_FP8_BLOCK && M > 16);
     long long g = sms;
@@ -340,7 +350,7 @@ void workspace_counters(int kind, int M, int N, int K, size_t* offset, size_t* b
     *offset = 0;
     *bytes = 0;
     DeviceInfo* d = device_info();
-    if (!d || M <= 0 || N <= 0 || K <= 0) return;
+    if (!d || M <= 0 || N <= 0 || K <= 0 || too_many_tiles(kind, M, N)) return;
     const SchedEntry& e = cached_schedule(kind, M, N, K, d->sms);
     const Schedule& s = e.s;
     const size_t total = e.ws;
@@ -502,7 +512,7 @@ using namespace qg;
 extern "C" {
 
 size_t qg_workspace_bytes(int kind, int M, int N, int K) {
-    if (M < 1 || N < 1 || K < 1 || M > max_m(kind)) return 0;
+    if (M < 1 || N < 1 || K < 1 || M > max_m(kind) || too_many_tiles(kind, M, N)) return 0;
     DeviceInfo* d = device_info();
     if (!d) return 0;
     return cached_schedule(kind, M, N, K, d->sms).ws;
@@ -672,8 +682,7 @@ qg_status qgemm_w8a8_block(const uint8_t* Xq, int64_t ldxq, const float* X_scale
         return QG_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(W_scale) & 3u) != 0 || (reinterpret_cast<uintptr_t>(Y) & 1u) != 0)
         return QG_ERR_MISALIGNED;
-    // 4 arrival counters per tile, indexed by int
-    if ((static_cast<int64_t>(N) + 127) / 128 * ((M + 31) / 32) > (int64_t(1) << 29)) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (too_many_tiles(QG_KIND_W8A8, M, N)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     if (K == 0) return launch_zero_rows(Y, ldy, M, N, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
@@ -740,8 +749,7 @@ qg_status qgemm_w8a8_int8(const int8_t* Xq, int64_t ldxq, const float* X_scale, 
         (reinterpret_cast<uintptr_t>(W_scale) & 3u) != 0 || (reinterpret_cast<uintptr_t>(bias) & 3u) != 0 ||
         (reinterpret_cast<uintptr_t>(Y) & y_mask) != 0)
         return QG_ERR_MISALIGNED;
-    // tiles are indexed by int
-    if ((static_cast<int64_t>(N) + 127) / 128 * ((M + 15) / 16) > (int64_t(1) << 29)) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (too_many_tiles(QG_KIND_INT8, M, N)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     Int8Args a{};
@@ -922,7 +930,7 @@ qg_status qg_debug_schedule(int kind, int M, int N, int K, int* ctas, int64_t* r
                             cudaStream_t stream) {
     if (max_m(kind) == 0 || kind == QG_KIND_INT8) return QG_ERR_INVALID_ARG;   // INT8: not a plain split of T * KU units
     if (M < 1 || M > max_m(kind) || N < 1 || K < 1 || !ctas) return QG_ERR_INVALID_ARG;
-    if (K % k_multiple(kind) != 0) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (K % k_multiple(kind) != 0 || too_many_tiles(kind, M, N)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     const Schedule s = cached_schedule(kind, M, N, K, d->sms).s;
@@ -937,6 +945,7 @@ qg_status qg_debug_schedule(int kind, int M, int N, int K, int* ctas, int64_t* r
 qg_status qg_dispatch_set(int kind, int M, int N, int K, int ctas) {
     if (max_m(kind) == 0) return QG_ERR_INVALID_ARG;
     if (M < 1 || M > max_m(kind) || N < 1 || K < 1 || ctas < 0) return QG_ERR_INVALID_ARG;
+    if (too_many_tiles(kind, M, N)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     if (ctas > d->sms) return QG_ERR_INVALID_ARG;
@@ -961,7 +970,7 @@ qg_status qg_dispatch_set(int kind, int M, int N, int K, int ctas) {
 }
 
 int qg_dispatch_get(int kind, int M, int N, int K) {
-    if (M < 1 || M > max_m(kind) || N < 1 || K < 1) return 0;
+    if (M < 1 || M > max_m(kind) || N < 1 || K < 1 || too_many_tiles(kind, M, N)) return 0;
     DeviceInfo* d = device_info();
     if (!d) return 0;
     const Schedule& s = cached_schedule(kind, M, N, K, d->sms).s;
@@ -970,12 +979,13 @@ int qg_dispatch_get(int kind, int M, int N, int K) {
 
 int qg_dispatch_rule(int kind, int M, int N, int K, int sms) {
     if (max_m(kind) == 0 || M < 1 || M > max_m(kind) || N < 1 || K < 1 || sms < 1) return 0;
+    if (too_many_tiles(kind, M, N)) return 0;
     const Schedule s = schedule_for(kind, M, N, K, sms, 0, int8_nominal_clusters(sms));
     return s.G * schedule_ctas(kind, s);
 }
 
 int qg_int8_tile_rows(int M, int N, int K, int sms) {
-    if (M < 1 || M > max_m(QG_KIND_INT8) || N < 1 || K < 1 || sms < 1) return 0;
+    if (M < 1 || M > max_m(QG_KIND_INT8) || N < 1 || K < 1 || sms < 1 || too_many_tiles(QG_KIND_INT8, M, N)) return 0;
     return int8_schedule(M, N, K, sms, 0, int8_nominal_clusters(sms)).nmma;
 }
 

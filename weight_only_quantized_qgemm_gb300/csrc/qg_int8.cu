@@ -1120,7 +1120,7 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
     const int ctas = int8_ctas(s.nmma);
     const long long tn = (N + 128ll * ctas - 1) / (128 * ctas);
     s.T = static_cast<int>(tn * ((M + s.nmma - 1) / s.nmma));
-    s.KU = (K + 127) / 128;
+    s.KU = static_cast<int>((static_cast<int64_t>(K) + 127) / 128);
     s.U = static_cast<long long>(s.T) * s.KU;
     long long w = forced > 0 ? (forced + ctas - 1) / ctas : sms / ctas;
     if (w < 1) w = 1;
@@ -1129,7 +1129,7 @@ Int8Schedule schedule_with(const TileCost& tc, int M, int N, int K, int sms, int
     s.nfull = static_cast<int>(s.T / w);
     long long r = s.T - s.nfull * w;
     long long g = 0;
-    *cost = tc.call_ns + s.nfull * s.KU * tc.unit_ns;
+    *cost = tc.call_ns + static_cast<long long>(s.nfull) * s.KU * tc.unit_ns;
     if (r > 0) {
         // no tile in more than kMostSplit pieces, which one CTA sums in turn, and
         // 0.2 us for each beyond 8 (1 x 128 x 17408 in 8 pieces 10.1 us, in 12 9.2, in
