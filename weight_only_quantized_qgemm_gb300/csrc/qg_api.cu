@@ -224,28 +224,25 @@ Int8Schedule schedule_for(int kind, int M, int N, int K, int sms, int forced, co
 // CTAs of the launch per G of the schedule (2 where G counts CTA pairs).
 int schedule_ctas(int kind, const Schedule& s) { return kind == QG_KIND_INT8 ? int8_ctas(s.nmma) : 1; }
 
-Int8Schedule choose_schedule(int kind, int M, int N, int K, int sms) {
-    const int* clusters = nullptr;
-    if (kind == QG_KIND_INT8) {
-        DeviceInfo* d = device_info();
-        if (d) std::call_once(d->clusters_once, [d]() { int8_cluster_capacity(d->clusters); });
-        clusters = d ? d->clusters : int8_nominal_clusters(0);
-    }
-    return schedule_for(kind, M, N, K, sms, table_lookup(kind, M, N, K), clusters);
+// d: of the current device.
+Int8Schedule choose_schedule(int kind, int M, int N, int K, DeviceInfo* d) {
+    if (kind == QG_KIND_INT8) std::call_once(d->clusters_once, [d]() { int8_cluster_capacity(d->clusters); });
+    return schedule_for(kind, M, N, K, d->sms, table_lookup(kind, M, N, K), d->clusters);
 }
 
 // True when some tile's units are spread over more than one CTA.
 bool schedule_splits(const Schedule& s) { return splits(s.U, s.KU, s.G); }
 
-// Per-thread caches of the last few schedules (keyed by kind, shape, SM
-// count and dispatch-table generation) and weight tensor maps (keyed by
-// address and shape, which determine the map): the schedule search walks
-// every CTA boundary and the map encoding is a driver call, both otherwise
-// paid on every GEMM call.
+// Per-thread caches of the last few schedules (keyed by kind, shape, device
+// (its SM count and clusters decide) and dispatch-table generation) and weight
+// tensor maps (keyed by address and shape, which determine the map): the
+// schedule search walks every CTA boundary and the map encoding is a driver
+// call, both otherwise paid on every GEMM call.
 constexpr int kCacheWays = 8;
 
 struct SchedEntry {
-    int kind = -1, M = 0, N = 0, K = 0, sms = 0;
+    int kind = -1, M = 0, N = 0, K = 0;
+    const DeviceInfo* device = nullptr;
     uint64_t gen = 0;
     Int8Schedule s;   // a plain Schedule for the other kinds
     size_t ws = 0;
@@ -253,21 +250,21 @@ struct SchedEntry {
 
 size_t workspace_bytes_uncached(const Schedule& s);
 
-const SchedEntry& cached_schedule(int kind, int M, int N, int K, int sms) {
+const SchedEntry& cached_schedule(int kind, int M, int N, int K, DeviceInfo* d) {
     thread_local SchedEntry cache[kCacheWays];
     thread_local int next = 0;
     const uint64_t gen = g_table_gen.load(std::memory_order_acquire);
     for (const SchedEntry& e : cache)
-        if (e.kind == kind && e.M == M && e.N == N && e.K == K && e.sms == sms && e.gen == gen) return e;
+        if (e.kind == kind && e.M == M && e.N == N && e.K == K && e.device == d && e.gen == gen) return e;
     SchedEntry& e = cache[next];
     next = (next + 1) % kCacheWays;
     e.kind = kind;
     e.M = M;
     e.N = N;
     e.K = K;
-    e.sms = sms;
+    e.device = d;
     e.gen = gen;
-    e.s = choose_schedule(kind, M, N, K, sms);
+    e.s = choose_schedule(kind, M, N, K, d);
     e.ws = kind == QG_KIND_W8A8   ? w8a8_workspace_bytes(e.s, schedule_splits(e.s))
            : kind == QG_KIND_INT8 ? int8_workspace_bytes(e.s, M, K)
                                   : workspace_bytes_uncached(e.s);
@@ -351,7 +348,7 @@ void workspace_counters(int kind, int M, int N, int K, size_t* offset, size_t* b
     *bytes = 0;
     DeviceInfo* d = device_info();
     if (!d || M <= 0 || N <= 0 || K <= 0 || too_many_tiles(kind, M, N)) return;
-    const SchedEntry& e = cached_schedule(kind, M, N, K, d->sms);
+    const SchedEntry& e = cached_schedule(kind, M, N, K, d);
     const Schedule& s = e.s;
     const size_t total = e.ws;
     if (total == 0) return;
@@ -515,7 +512,7 @@ size_t qg_workspace_bytes(int kind, int M, int N, int K) {
     if (M < 1 || N < 1 || K < 1 || M > max_m(kind) || too_many_tiles(kind, M, N)) return 0;
     DeviceInfo* d = device_info();
     if (!d) return 0;
-    return cached_schedule(kind, M, N, K, d->sms).ws;
+    return cached_schedule(kind, M, N, K, d).ws;
 }
 
 size_t qg_workspace_bytes_max(int N) {
@@ -550,7 +547,7 @@ qg_status qgemm_fp8_block(const void* X, int64_t ldx, const uint8_t* W, const fl
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     if (K == 0) return launch_zero_rows(Y, ldy, M, N, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
-    const SchedEntry& se = cached_schedule(QG_KIND_FP8_BLOCK, M, N, K, d->sms);
+    const SchedEntry& se = cached_schedule(QG_KIND_FP8_BLOCK, M, N, K, d);
     const Schedule s = se.s;
     const size_t need = se.ws;
     if (need > 0 && (!workspace || workspace_bytes_ < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
@@ -593,7 +590,7 @@ qg_status qgemm_fp8_block_multi(const void* X, int64_t ldx, const qg_fp8_segment
         return QG_OK;
     }
     const int N = static_cast<int>(rows);
-    const SchedEntry& se = cached_schedule(QG_KIND_FP8_BLOCK, M, N, K, d->sms);
+    const SchedEntry& se = cached_schedule(QG_KIND_FP8_BLOCK, M, N, K, d);
     const Schedule s = se.s;
     const size_t need = se.ws;
     if (need > 0 && (!workspace || workspace_bytes_ < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
@@ -629,7 +626,7 @@ qg_status qgemm_bf16(const void* X, int64_t ldx, const void* W, void* Y, int64_t
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     if (K == 0) return launch_zero_rows(Y, ldy, M, N, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
-    const SchedEntry& se = cached_schedule(QG_KIND_BF16, M, N, K, d->sms);
+    const SchedEntry& se = cached_schedule(QG_KIND_BF16, M, N, K, d);
     const Schedule s = se.s;
     const size_t need = se.ws;
     if (need > 0 && (!workspace || workspace_bytes_ < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
@@ -686,7 +683,7 @@ qg_status qgemm_w8a8_block(const uint8_t* Xq, int64_t ldxq, const float* X_scale
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     if (K == 0) return launch_zero_rows(Y, ldy, M, N, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
-    const SchedEntry& se = cached_schedule(QG_KIND_W8A8, M, N, K, d->sms);
+    const SchedEntry& se = cached_schedule(QG_KIND_W8A8, M, N, K, d);
     const Schedule s = se.s;
     const size_t need = se.ws;
     if (need > 0 && (!workspace || workspace_bytes_ < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
@@ -765,7 +762,7 @@ qg_status qgemm_w8a8_int8(const int8_t* Xq, int64_t ldxq, const float* X_scale, 
     a.N = N;
     a.K = K;
     if (K == 0) return launch_int8_bias_rows(a, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
-    const SchedEntry& se = cached_schedule(QG_KIND_INT8, M, N, K, d->sms);
+    const SchedEntry& se = cached_schedule(QG_KIND_INT8, M, N, K, d);
     const Int8Schedule s = se.s;
     if (se.ws > 0 && (!workspace || workspace_bytes_ < se.ws || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return QG_ERR_WORKSPACE;
@@ -817,7 +814,7 @@ qg_status qgemm_lut3(const void* X, int64_t ldx, const void* Wq, const void* qma
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     if (K == 0) return launch_zero_rows(Y, ldy, M, N, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
-    const SchedEntry& se = cached_schedule(QG_KIND_LUT3, M, N, K, d->sms);
+    const SchedEntry& se = cached_schedule(QG_KIND_LUT3, M, N, K, d);
     const Schedule s = se.s;
     const size_t need = se.ws;
     if (need > 0 && (!workspace || workspace_bytes_ < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
@@ -933,7 +930,7 @@ qg_status qg_debug_schedule(int kind, int M, int N, int K, int* ctas, int64_t* r
     if (K % k_multiple(kind) != 0 || too_many_tiles(kind, M, N)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
-    const Schedule s = cached_schedule(kind, M, N, K, d->sms).s;
+    const Schedule s = cached_schedule(kind, M, N, K, d).s;
     *ctas = s.G;
     if (!ranges || !info) return QG_OK;   // a query of the CTA count only
     if (capacity < s.G) return QG_ERR_INVALID_ARG;
@@ -973,7 +970,7 @@ int qg_dispatch_get(int kind, int M, int N, int K) {
     if (M < 1 || M > max_m(kind) || N < 1 || K < 1 || too_many_tiles(kind, M, N)) return 0;
     DeviceInfo* d = device_info();
     if (!d) return 0;
-    const Schedule& s = cached_schedule(kind, M, N, K, d->sms).s;
+    const Schedule& s = cached_schedule(kind, M, N, K, d).s;
     return s.G * schedule_ctas(kind, s);
 }
 
