@@ -365,7 +365,7 @@ int qg_int8_tile_rows(int M, int N, int K, int sms);
  * Log probabilities of given tokens, entropy and top alternatives over rows
  * of logits, such as an lm_head's output (an addition of this library, with
  * no counterpart in the paper).  With x = logits[m, 0 .. V-1] and
- * p = softmax(x), in FP32 and natural logarithms:
+ * p = softmax(x), in FP32 and natural logarithms (never above 0):
  *   token_logprobs[m * T + t] = ln p[tokens[m * ldt + t]]
  *   entropy[m]                = - sum_v p[v] ln p[v]   (0 ln 0 = 0)
  *   top_ids[m * top_k + j], top_logprobs[m * top_k + j]

@@ -402,3 +402,22 @@ def test_strided_tokens_on_another_stream():
             assert all(torch.equal(a, b) for a, b in zip(got, want))
     torch.cuda.synchronize()
     assert q.last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_no_log_probability_is_above_zero(dtype):
+    """Rows held by one token, at offsets of every kind, whole and split over
+    CTAs: its log probability is 0 within the bound and not above it, so that
+    exp gives no more than 1 and log1p(-exp) no NaN."""
+    q = qg()
+    rng = np.random.default_rng(23)
+    for M, V in ((64, 5003), (500, 700), (3, 70001), (1, 131072)):
+        x = rng.uniform(-2, 2, (M, V)) + rng.uniform(-300, 300, (M, 1))
+        ids = rng.integers(0, V, M)
+        x[np.arange(M), ids] += rng.uniform(30, 400, M)
+        tok = torch.from_numpy(ids).cuda()
+        r = q.logprobs(torch.from_numpy(x).to(DT[dtype]).cuda(), tok, top_k=2, entropy=True)
+        R = (4 + 2 * 104 + V / 128 + 32) * U
+        for lp in (r.token_logprobs, r.top_logprobs[:, 0]):
+            assert bool((lp <= 0).all()) and bool((lp >= -R).all())
+        assert torch.equal(r.top_ids[:, 0], tok) and bool((r.top_logprobs[:, 1] <= 0).all())

@@ -472,9 +472,11 @@ __device__ __noinline__ void plain_row(const LogprobArgs& a, uint32_t m, Shared&
 
 // ----------------------------------------------------------------- one pass
 // ln p of logit x by the row's reference and ln s.  Below -1e30 (where x L may
-// leave the range) both are lost in x: it is its own log probability.
+// leave the range) both are lost in x: it is its own log probability.  Of a token
+// that holds all of the row the roundings of t, 2^t and ln s leave about +-2e-7:
+// not above 0.  (Rows with a NaN do not come here.)
 __device__ __forceinline__ float logp_of(float x, float c, float ls) {
-    return x < -1e30f ? x : fmaf(fmaf(x, kLog2e, -c), kLn2, -ls);
+    return x < -1e30f ? x : fminf(fmaf(fmaf(x, kLog2e, -c), kLn2, -ls), 0.0f);
 }
 
 // kN vectors of a thread: their maximum first, which is returned (moving c where
