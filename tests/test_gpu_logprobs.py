@@ -421,3 +421,22 @@ def test_no_log_probability_is_above_zero(dtype):
         for lp in (r.token_logprobs, r.top_logprobs[:, 0]):
             assert bool((lp <= 0).all()) and bool((lp >= -R).all())
         assert torch.equal(r.top_ids[:, 0], tok) and bool((r.top_logprobs[:, 1] <= 0).all())
+
+
+def test_a_row_alone_and_among_others():
+    """The rows of a batch that is split over more or fewer CTAs a row give the
+    same alternatives, and values within the sums' bound of one another (their
+    order, and so their last bits, depend on the number of rows)."""
+    q = qg()
+    V = 32768
+    x = _logits(400, V, "bf16", 14)
+    tok = torch.from_numpy(_tokens(400, 1, V)).cuda()
+    whole = q.logprobs(x, tok, top_k=5, entropy=True)
+    R = (4 + 2 * 104 + V / 128 + 32) * U
+    for m, n in ((0, 1), (7, 8), (100, 140), (0, 160)):
+        part = q.logprobs(x[m:n], tok[m:n], top_k=5, entropy=True)
+        assert torch.equal(part.top_ids, whole.top_ids[m:n])
+        for a, b in ((part.token_logprobs, whole.token_logprobs[m:n]), (part.top_logprobs, whole.top_logprobs[m:n])):
+            assert bool(((a - b).abs() <= 2 * (R + 4 * U * b.abs())).all())
+        H = whole.entropy[m:n]
+        assert bool(((part.entropy - H).abs() <= 2 * R * (2 + 2 * math.log(V) + 2 * H)).all())
