@@ -42,7 +42,8 @@
  *    status word, release its resources and return; read it with
  *    qg_last_device_status().  After such an error the workspace contents are
  *    undefined and must be zero-filled again before reuse.
- *  - NaN codes (E4M3 0x7F / 0xFF) and non-finite X produce unspecified values.
+ *  - NaN codes (E4M3 0x7F / 0xFF) and non-finite X produce unspecified values
+ *    (qg_quantize_act_int8 marks such rows by a scale of NaN).
  *  - One workspace may serve one in-flight call at a time.
  */
 #ifndef QGEMM_H
@@ -314,7 +315,8 @@ qg_status qgemm_w8a8_block(const uint8_t *Xq, int64_t ldxq, const float *X_scale
  *   Xq       device, int8 [M, ldxq], 16-byte aligned, ldxq >= K, ldxq % 16 == 0
  *   X_scale  device, FP32 [M]
  *   M, K     0 <= M <= 65536, K % 16 == 0 (nothing is written when K == 0)
- * Finite inputs only (the codes of a row with Inf or NaN are unspecified).
+ * A row with Inf or NaN has scale NaN (its codes are unspecified), so that the
+ * GEMM's output for it is NaN.
  */
 qg_status qg_quantize_act_int8(const void *X, int x_type, int64_t ldx, int8_t *Xq, int64_t ldxq,
                                float *X_scale, int M, int K, struct CUstream_st *stream);

@@ -1,0 +1,37 @@
+"""The 8-bit integer path where inputs or the work around it are unusual:
+broken activations."""
+import pytest
+import torch
+
+from gpu_util import qg
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("K", [64, 5120, 40960])
+def test_broken_rows_stay_broken(dtype, K):
+    """A row with a NaN or an infinity has scale NaN, and the GEMM and the
+    scores behind it give NaN for that row and no other."""
+    q = qg()
+    g = torch.Generator(device="cuda").manual_seed(K)
+    X = torch.randn(9, K, generator=g, device="cuda").to(dtype)
+    good = X.clone()
+    X[1, 0] = float("nan")
+    X[2, K - 1] = float("inf")
+    X[3, K // 2] = -float("inf")
+    X[4, 5], X[4, 6] = float("inf"), float("nan")
+    X[5] = float("nan")
+    X[6, 7] = -float("nan")
+    broken = torch.tensor([0, 1, 1, 1, 1, 1, 1, 0, 0], dtype=torch.bool, device="cuda")
+    codes, scale = q.quantize_act_int8(X)
+    assert torch.equal(torch.isnan(scale), broken)
+    c0, s0 = q.quantize_act_int8(good)
+    assert torch.equal(codes[~broken], c0[~broken]) and torch.equal(scale[~broken], s0[~broken])
+    W = torch.randint(-127, 128, (200, K), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.full((200,), 1e-3, device="cuda")
+    y = q.qgemm_w8a8_int8(codes, scale, W, sw, out_dtype=torch.float32)
+    assert torch.equal(torch.isnan(y), broken[:, None].expand_as(y))
+    r = q.logprobs(y, torch.zeros(9, dtype=torch.int64, device="cuda"), top_k=3, entropy=True)
+    for t in (r.token_logprobs, r.entropy, r.top_logprobs[:, 0]):
+        assert torch.equal(torch.isnan(t), broken)

@@ -473,7 +473,8 @@ def _rows(t, what: str):
 def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
     """8-bit integer codes and one FP32 scale per row of BF16 or FP16
     activations: scale = max |x| / 127, code = x * (127 * (1 / max |x|)) rounded
-    half to even (a row whose largest |x| is below 2^-100 has codes 0, scale 1).
+    half to even (a row whose largest |x| is below 2^-100 has codes 0, scale 1;
+    one with a NaN or an infinity has scale NaN).
 
     X: CUDA [M, K] (row stride a multiple of 8, K % 16 == 0).  Returns (Xq
     int8 [M, K], X_scale float32 [M]).  Xq and X_scale (optional) are written

@@ -989,9 +989,13 @@ __global__ void __launch_bounds__(256) quantize_int8_kernel(const uint16_t* __re
     for (int j = 0; j < 8; ++j) mx = max(mx, warp_max[j]);
     float amax, unused;
     unpack2<kBf16>(mx, amax, unused);
-    const bool live = amax >= kTinyMax;
+    // A row with a NaN or an infinity (whose bit patterns order above every
+    // finite magnitude) has scale NaN, which the GEMM carries to its whole output.
+    const bool finite = amax < INFINITY;
+    const bool live = finite && amax >= kTinyMax;
     const float inv = live ? __fmul_rn(127.0f, __frcp_rn(amax)) : 0.0f;
-    if (threadIdx.x == 0) Sx[m] = live ? __fdiv_rn(amax, 127.0f) : 1.0f;
+    if (threadIdx.x == 0)
+        Sx[m] = live ? __fdiv_rn(amax, 127.0f) : finite ? 1.0f : __uint_as_float(0x7FC00000u);
     if constexpr (kVec > 0) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
