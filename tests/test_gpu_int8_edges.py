@@ -1,5 +1,5 @@
 """The 8-bit integer path where inputs or the work around it are unusual:
-broken activations."""
+broken activations, nothing to quantise."""
 import pytest
 import torch
 
@@ -35,3 +35,19 @@ def test_broken_rows_stay_broken(dtype, K):
     r = q.logprobs(y, torch.zeros(9, dtype=torch.int64, device="cuda"), top_k=3, entropy=True)
     for t in (r.token_logprobs, r.entropy, r.top_logprobs[:, 0]):
         assert torch.equal(torch.isnan(t), broken)
+
+
+def test_rows_of_nothing_have_scale_one():
+    """K = 0: a row's largest |x| is that of no values, 0."""
+    q = qg()
+    X = torch.empty(5, 0, dtype=torch.bfloat16, device="cuda")
+    scale = torch.full((5,), 3.0, device="cuda")
+    codes, got = q.quantize_act_int8(X, X_scale=scale)
+    assert got is scale and torch.equal(scale, torch.ones(5, device="cuda")) and tuple(codes.shape) == (5, 0)
+    junk = torch.full((1 << 20,), float("nan"), device="cuda")
+    del junk
+    st = torch.cuda.Stream()
+    for stream in (None, st):
+        _, fresh = q.quantize_act_int8(X, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(fresh, torch.ones(5, device="cuda"))

@@ -257,3 +257,12 @@ def test_tensors_of_another_device_are_refused(world):
         q.logprobs(T(4, 100, dtype=f), entropy=True)
     q.logprobs(T(4, 100, dtype=f), entropy=True, stream=Stream(SIDE, device=1))
     assert len(world.calls) == 2
+
+
+def test_scales_of_rows_of_nothing_are_filled_on_the_call_s_stream(world):
+    X = Tensor(world, (4, 0), torch.bfloat16)
+    n = len(world.made)
+    world.q.quantize_act_int8(X, stream=SIDE)
+    filled = [t for t, _ in world.made[n:] if t.shape == (4,)]
+    assert len(filled) == 2 and filled[0] is filled[1]   # made, then filled
+    assert all(s == SIDE for _, s in world.made[n:])

@@ -504,6 +504,8 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
             raise TypeError("X_scale must be contiguous float32")
         if X_scale.shape != (M,) or X_scale.device != dev:
             raise ValueError("X_scale must be [M] on X's device")
+    if K == 0:   # rows of nothing, which the library leaves alone
+        return Xq, X_scale.fill_(1.0)
     st = _raw_stream(dev.index)
     r = lib.qg_quantize_act_int8(X.data_ptr(), code, ld, Xq.data_ptr(), ldq, X_scale.data_ptr(), M, K, st)
     if r:
