@@ -1,5 +1,5 @@
 """The 8-bit integer path where inputs or the work around it are unusual:
-broken activations, nothing to quantise."""
+broken activations, nothing to quantise, a long kernel in front of the GEMM."""
 import pytest
 import torch
 
@@ -51,3 +51,39 @@ def test_rows_of_nothing_have_scale_one():
         _, fresh = q.quantize_act_int8(X, stream=stream)
         torch.cuda.synchronize()
         assert torch.equal(fresh, torch.ones(5, device="cuda"))
+
+
+@pytest.mark.parametrize("overlap", [False, True], ids=["plain", "overlapped"])
+@pytest.mark.parametrize("M,N,K,rows", [(1, 1024, 5120, 16), (4, 640, 1040, 16), (64, 5120, 5120, 64),
+                                        (256, 5120, 5120, 256)])
+def test_the_wait_limit_does_not_count_the_kernel_in_front(M, N, K, rows, overlap):
+    """A GEMM that starts under a preceding kernel (here of several hundred
+    microseconds on a few SMs, which lets it start at once) gives up on none of
+    its waits for that, with a limit below the kernel's time."""
+    q = qg()
+    assert q.int8_tile_rows(M, N, K, 152) == rows
+    g = torch.Generator(device="cuda").manual_seed(6)
+    Xq = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    W = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    sx, sw = torch.full((M,), 0.01, device="cuda"), torch.full((N,), 1e-3, device="cuda")
+    ws = q.Workspace()
+    expect = q.qgemm_w8a8_int8(Xq, sx, W, sw, workspace=ws)   # which grows it, and so waits for the device
+    logits = torch.zeros((1, 1 << 28), dtype=torch.bfloat16, device="cuda")
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    q.logprobs(logits, entropy=True)
+    start.record()
+    q.logprobs(logits, entropy=True)
+    end.record()
+    end.synchronize()
+    limit_us = 150
+    assert start.elapsed_time(end) * 1e3 > 2 * limit_us, "the kernel in front is too short for this test"
+    q.set_wait_timeout_ns(limit_us * 1000)
+    q.set_weight_prefetch_overlap(overlap)
+    try:
+        q.logprobs(logits, entropy=True)
+        got = q.qgemm_w8a8_int8(Xq, sx, W, sw, workspace=ws)
+        assert q.last_device_status() == 0
+    finally:
+        q.set_weight_prefetch_overlap(False)
+        q.set_wait_timeout_ns(1_000_000_000)
+    assert torch.equal(got, expect)

@@ -340,6 +340,9 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
     const int nunits = o.nfull * p.KB + u1 - u0;
     const WaitCtl wc{p.timeout_ns, p.status, abort_flag};
 
+    // The kernel may start long before the preceding grid is done.  Every warp
+    // waits for that before its first bounded wait for what comes behind it, so
+    // that the preceding grid's time does not count against the limit.
     if (warp == kWarpWProd) {
         // Sets the barriers up, announces them and starts the weight stream at
         // once: it needs nothing else of the CTA's set-up (with the first turn
@@ -398,6 +401,8 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         if constexpr (kPair || kClu) cluster_wait_all();   // of the arrival above
         if (lane == 0) {
             for (; issued < nunits; ++issued, cur.step(p, o), rw.step(1)) {
+                // the first stage that an MMA has to free, through an A buffer
+                if (issued == kWStages + kABufs) grid_dependency_wait();
                 if (!wait_bounded(wempty(rw.slot), rw.phase ^ 1u, wc)) break;
                 load_w();
             }
@@ -506,6 +511,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         };
         // the K block within a tile: whole tiles, then the tail from its first
         int kb = o.nfull > 0 ? 0 : u0 % p.KB;
+        grid_dependency_wait();   // the activations come behind it
         Ring<kSlots> ro(0);
         int piece = 0;
         int last_a = -1;
@@ -546,6 +552,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
         Ring<kWStages> rw(grp);
         Ring<kSlots> ro(grp);      // the unit's slot
         Ring<kSlots> done(grp);    // that of the unit kABufs before it, whose A buffer it takes
+        if (L::kInlineX && !o.early) grid_dependency_wait();   // so do the weights
         for (int i = grp; i < nunits; i += kGroups, rw.step(kGroups), ro.step(kGroups)) {
             if (!gemm::warp_wait(wfull(rw.slot), rw.phase, wc)) break;
             const uint8_t* src = gbase + rw.slot * L::kWBytes + row * 128;
@@ -553,6 +560,7 @@ __global__ void __launch_bounds__(I8Layout<NA, kPair>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) c[j] = *reinterpret_cast<const uint4*>(src + ((j ^ (row & 7)) << 4));
             if (i >= kABufs) {
+                if (i < kABufs + kGroups) grid_dependency_wait();   // MMAs are behind it
                 if (!gemm::warp_wait(ofree(done.slot), done.phase, wc)) break;
                 done.step(kGroups);
             }
