@@ -465,8 +465,6 @@ def _rows(t, what: str):
         raise ValueError(what + " must have unit stride in its last dimension")
     if not t.is_cuda:
         raise ValueError(what + " must be on a CUDA device")
-    if t.device.index != _current_device():   # where the library launches
-        raise ValueError(what + " must be on the current CUDA device")
     return r, c, (ld if r > 1 else c)
 
 
@@ -488,6 +486,9 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
         raise TypeError("X must be bfloat16 or float16")
     M, K, ld = _rows(X, "X")
     dev = X.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
     if Xq is None:
         Xq = torch.empty((M, K), dtype=torch.int8, device=dev)
         ldq = K
@@ -506,7 +507,7 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
             raise ValueError("X_scale must be [M] on X's device")
     if K == 0:   # rows of nothing, which the library leaves alone
         return Xq, X_scale.fill_(1.0)
-    st = _raw_stream(dev.index)
+    st = _raw_stream(index)
     r = lib.qg_quantize_act_int8(X.data_ptr(), code, ld, Xq.data_ptr(), ldq, X_scale.data_ptr(), M, K, st)
     if r:
         raise QgemmError(r, "qg_quantize_act_int8")
@@ -536,6 +537,9 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
     M, K, ldq = _rows(Xq, "Xq")
     N = W.shape[0]
     dev = Xq.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
     if W.shape != (N, K) or X_scale.shape != (M,) or W_scale.shape != (N,):
         raise ValueError("shape mismatch between Xq, X_scale, W and W_scale")
     if W.device != dev or X_scale.device != dev or W_scale.device != dev:
@@ -562,7 +566,7 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
         rows, cols, ldy = _rows(Y, "Y")
         if rows != M or cols != N or Y.device != dev:
             raise ValueError("Y must be [M, N] on the same device")
-    st = _raw_stream(dev.index)
+    st = _raw_stream(index)
     ws, wsb = _workspace_for(KIND_INT8, M, N, K, workspace, dev, st)
     r = lib.qgemm_w8a8_int8(Xq.data_ptr(), ldq, X_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(), b,
                             Y.data_ptr(), code, ldy, M, N, K, ws, wsb, st)
@@ -609,6 +613,9 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
         raise TypeError("logits must be bfloat16, float16 or float32")
     M, V, ld = _rows(logits, "logits")
     dev = logits.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
     T = ldt = 0
     tok = token_lp = token_p = ent = ent_p = ids = ids_p = top = top_p = None
     if tokens is not None:
@@ -635,7 +642,7 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
         ids = torch.empty((M, top_k), dtype=i64, device=dev)
         top = torch.empty((M, top_k), dtype=f32, device=dev)
         ids_p, top_p = ids.data_ptr(), top.data_ptr()
-    st = _raw_stream(dev.index)
+    st = _raw_stream(index)
     r = lib.qg_logprobs(logits.data_ptr(), code, ld, tok, ldt, T, token_p, ent_p, top_k, ids_p, top_p, M, V, st)
     if r:
         raise QgemmError(r, "qg_logprobs")
