@@ -266,3 +266,27 @@ def test_scales_of_rows_of_nothing_are_filled_on_the_call_s_stream(world):
     filled = [t for t, _ in world.made[n:] if t.shape == (4,)]
     assert len(filled) == 2 and filled[0] is filled[1]   # made, then filled
     assert all(s == SIDE for _, s in world.made[n:])
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 16])
+def test_sizes_beyond_32_bits_are_refused(world, big):
+    """The library takes sizes as 32-bit numbers: larger ones would arrive as
+    what is left of them."""
+    q, f = world.q, torch.float32
+
+    def T(*shape, dtype=torch.int8):
+        return Tensor(world, shape, dtype)
+
+    bf = torch.bfloat16
+    for call in (lambda: q.quantize_act_int8(T(big, 64, dtype=bf)),
+                 lambda: q.quantize_act_int8(T(4, big, dtype=bf)),
+                 lambda: q.qgemm_w8a8_int8(T(big, 64), T(big, dtype=f), T(8, 64), T(8, dtype=f)),
+                 lambda: q.qgemm_w8a8_int8(T(4, big), T(4, dtype=f), T(8, big), T(8, dtype=f)),
+                 lambda: q.qgemm_w8a8_int8(T(4, 64), T(4, dtype=f), T(big, 64), T(big, dtype=f)),
+                 lambda: q.logprobs(T(big, 16, dtype=f), entropy=True),
+                 lambda: q.logprobs(T(4, big, dtype=f), entropy=True),
+                 lambda: q.logprobs(T(4, 16, dtype=f), T(4, big, dtype=torch.int64)),
+                 lambda: q.logprobs(T(4, 16, dtype=f), top_k=big)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    assert not world.calls

@@ -468,6 +468,9 @@ def _rows(t, what: str):
     return r, c, (ld if r > 1 else c)
 
 
+_SIZE = "sizes of 2^31 and more are not supported"   # which ctypes would cut to 32 bits
+
+
 def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
     """8-bit integer codes and one FP32 scale per row of BF16 or FP16
     activations: scale = max |x| / 127, code = x * (127 * (1 / max |x|)) rounded
@@ -485,6 +488,8 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
     if code != 0 and code != 1:
         raise TypeError("X must be bfloat16 or float16")
     M, K, ld = _rows(X, "X")
+    if (M | K) >> 31:
+        raise ValueError(_SIZE)
     dev = X.device
     index = dev.index
     if index != _current_device():   # where the library launches
@@ -536,6 +541,8 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
         raise TypeError("W and the scales must be contiguous")
     M, K, ldq = _rows(Xq, "Xq")
     N = W.shape[0]
+    if (M | N | K) >> 31:
+        raise ValueError(_SIZE)
     dev = Xq.device
     index = dev.index
     if index != _current_device():   # where the library launches
@@ -612,6 +619,8 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
     if code is None:
         raise TypeError("logits must be bfloat16, float16 or float32")
     M, V, ld = _rows(logits, "logits")
+    if (M | V) >> 31:
+        raise ValueError(_SIZE)
     dev = logits.device
     index = dev.index
     if index != _current_device():   # where the library launches
@@ -627,6 +636,8 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
         if len(shape) not in (1, 2) or shape[0] != M:
             raise ValueError("tokens must be [M] or [M, T]")
         T = shape[1] if len(shape) == 2 else 1
+        if T >> 31:
+            raise ValueError(_SIZE)
         strides = tokens.stride()
         ldt = strides[0] if M > 1 else T
         if ldt < T or (T > 1 and strides[1] != 1):   # expanded or transposed
@@ -639,6 +650,8 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
         ent = torch.empty((M,), dtype=f32, device=dev)
         ent_p = ent.data_ptr()
     if top_k > 0:   # a negative one is refused by the library
+        if top_k >> 31:
+            raise ValueError(_SIZE)
         ids = torch.empty((M, top_k), dtype=i64, device=dev)
         top = torch.empty((M, top_k), dtype=f32, device=dev)
         ids_p, top_p = ids.data_ptr(), top.data_ptr()
