@@ -1,5 +1,7 @@
 """The 8-bit integer path where inputs or the work around it are unusual:
-broken activations, nothing to quantise, a long kernel in front of the GEMM."""
+broken activations, nothing to quantise, a long kernel in front of the GEMM, one
+workspace for several kinds."""
+import numpy as np
 import pytest
 import torch
 
@@ -87,3 +89,28 @@ def test_the_wait_limit_does_not_count_the_kernel_in_front(M, N, K, rows, overla
         q.set_weight_prefetch_overlap(False)
         q.set_wait_timeout_ns(1_000_000_000)
     assert torch.equal(got, expect)
+
+
+def test_one_workspace_object_serves_every_kind():
+    """Kinds that lay their workspace out differently, in turn on one Workspace."""
+    import workloads as wl
+    q = qg()
+    p = wl.make_fp8_problem(4, 1024, 5120, config_id=50)
+    Xf = torch.from_numpy(p.X.view(np.int16)).view(torch.bfloat16).cuda()
+    Wf, Sf = torch.from_numpy(p.W).cuda(), torch.from_numpy(p.S).cuda()
+    g = torch.Generator(device="cuda").manual_seed(31)
+    X = torch.randn(200, 5120, generator=g, device="cuda").to(torch.bfloat16)
+    Wi = torch.randint(-127, 128, (1024, 5120), generator=g, device="cuda", dtype=torch.int8)
+    si = torch.full((1024,), 1e-3, device="cuda")
+    calls = [lambda ws: q.qgemm_fp8_block(Xf, Wf, Sf, workspace=ws),
+             lambda ws: q.qgemm_w8a8_int8(*q.quantize_act_int8(X), Wi, si, workspace=ws),
+             lambda ws: q.qgemm_w8a8_int8(*q.quantize_act_int8(X[:1]), Wi, si, workspace=ws),
+             lambda ws: q.qgemm_w8a8(X, Wf, Sf, workspace=ws)]
+    for kind, M in ((q.KIND_FP8_BLOCK, 4), (q.KIND_INT8, 200), (q.KIND_INT8, 1), (q.KIND_W8A8, 200)):
+        assert q.workspace_bytes(kind, M, 1024, 5120) > 0
+    expect = [c(q.Workspace()) for c in calls]
+    ws = q.Workspace()
+    for _ in range(3):
+        for c, want in zip(calls, expect):
+            out = c(ws)
+            assert q.last_device_status() == 0 and torch.equal(out, want)

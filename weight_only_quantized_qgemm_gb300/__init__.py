@@ -169,34 +169,47 @@ def workspace_bytes(kind: int, M: int, N: int, K: int) -> int:
     return int(lib.qg_workspace_bytes(kind, M, N, K))
 
 
+# the kinds whose workspaces share a layout: each of these alone, all others together
+_OWN_LAYOUT = (KIND_W8A8, KIND_INT8)
+
+
 class Workspace:
-    """A zero-filled device byte buffer that grows on demand.  Calls leave
-    its arrival counters at zero again (the partial-sum area in front of them
-    is scratch), so one buffer serves any sequence of calls on one stream
-    (calls that may run at the same time, on different streams, need one
-    buffer each).  Growing synchronises the device, so that no call still
-    uses the old buffer and the zero fill has landed before any stream uses
-    the new one."""
+    """Zero-filled device byte buffers that grow on demand, one for each
+    workspace layout (the W8A8 and INT8 kinds have their own, the others share
+    one).  Calls leave their arrival counters at zero again (the rest is
+    scratch), so one Workspace serves any sequence of calls of any kind on one
+    stream (calls that may run at the same time, on different streams, need one
+    each).  Growing synchronises the device, so that no call still uses the old
+    buffer and the zero fill has landed before any stream uses the new one; a
+    captured graph keeps the addresses of the buffers that it was captured with,
+    so give it a Workspace that no larger call grows later.
+
+    ``buf`` is the buffer that was asked for last."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self._bufs = {}
 
-    def get(self, nbytes: int):
+    def get(self, nbytes: int, kind: int = KIND_FP8_BLOCK):
+        """The buffer of the kind's layout, of at least nbytes (None for 0)."""
         torch = _torch()
         if nbytes == 0:
             return None
-        if self.buf is None or self.buf.numel() < nbytes:
+        layout = kind if kind in _OWN_LAYOUT else None
+        buf = self._bufs.get(layout)
+        if buf is None or buf.numel() < nbytes:
             dev = self.device or torch.cuda.current_device()
-            if self.buf is not None:
+            if buf is not None:
                 torch.cuda.synchronize(dev)
-            self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+            buf = self._bufs[layout] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
             torch.cuda.synchronize(dev)
-        return self.buf
+        self.buf = buf
+        return buf
 
     def reset(self):
-        if self.buf is not None:
-            self.buf.zero_()
+        for buf in self._bufs.values():
+            buf.zero_()
 
 
 _default_ws = {}
@@ -213,13 +226,12 @@ def _workspace_for(kind, M, N, K, workspace, device, stream=None):
     if need == 0:
         return None, 0
     if workspace is None:
-        # one default buffer per device, stream (calls on different streams may
-        # overlap) and layout family (the W8A8 and INT8 kinds' differ from the others')
-        key = (device, _stream_ptr(stream), kind if kind in (KIND_W8A8, KIND_INT8) else None)
+        # a default one per device and stream (calls on different streams may overlap)
+        key = (device, _stream_ptr(stream))
         workspace = _default_ws.get(key)
         if workspace is None:
             workspace = _default_ws[key] = Workspace(device)
-    buf = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    buf = workspace.get(need, kind) if isinstance(workspace, Workspace) else workspace
     return buf.data_ptr(), buf.numel() * buf.element_size()
 
 
@@ -801,11 +813,11 @@ def workspace_bytes_max(N: int) -> int:
     return int(lib.qg_workspace_bytes_max(N))
 
 
-def _tune_common(M, N, X, Y_ref, workspace, nbytes=None):
+def _tune_common(M, N, X, Y_ref, workspace, nbytes=None, kind=KIND_FP8_BLOCK):
     if workspace is None:
         workspace = Workspace(X.device)
     need = workspace_bytes_max(N) if nbytes is None else nbytes
-    buf = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    buf = workspace.get(need, kind) if isinstance(workspace, Workspace) else workspace
     return buf, (buf.numel() * buf.element_size() if buf is not None else 0)
 
 
@@ -860,7 +872,7 @@ def tune_w8a8(Xq, X_scale, W_copies, W_scale, calls: int = 100, workspace=None, 
     N = W_copies[0].shape[0]
     Y = torch.empty((M, N), dtype=torch.bfloat16, device=Xq.device)
     Y_ref = torch.empty_like(Y)
-    buf, nb = _tune_common(M, N, Xq, Y_ref, workspace, workspace_bytes_max_w8a8(M, N))
+    buf, nb = _tune_common(M, N, Xq, Y_ref, workspace, workspace_bytes_max_w8a8(M, N), KIND_W8A8)
     ptrs = (ctypes.c_void_p * len(W_copies))(*[w.data_ptr() for w in W_copies])
     g, us = ctypes.c_int(0), ctypes.c_float(0)
     _check(lib.qg_tune_w8a8(Xq.data_ptr(), _ld(Xq), X_scale.data_ptr(), _ld(X_scale),
