@@ -114,3 +114,30 @@ def test_one_workspace_object_serves_every_kind():
         for c, want in zip(calls, expect):
             out = c(ws)
             assert q.last_device_status() == 0 and torch.equal(out, want)
+
+
+def test_a_graph_outlives_its_workspace_s_growth():
+    """A larger call on the Workspace of a captured graph, and other tensors
+    made after it: the replays give what they gave, and write to nothing else."""
+    q = qg()
+    g = torch.Generator(device="cuda").manual_seed(41)
+    W = torch.randint(-127, 128, (1024, 5120), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.full((1024,), 1e-3, device="cuda")
+    small = q.quantize_act_int8(torch.randn(200, 5120, generator=g, device="cuda").to(torch.bfloat16))
+    large = q.quantize_act_int8(torch.randn(4096, 5120, generator=g, device="cuda").to(torch.bfloat16))
+    ws = q.Workspace()
+    want = q.qgemm_w8a8_int8(*small, W, sw, workspace=ws)
+    before = ws.buf.numel()
+    Y = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.qgemm_w8a8_int8(*small, W, sw, Y=Y, workspace=ws)
+    q.qgemm_w8a8_int8(*large, W, sw, workspace=ws)
+    assert ws.buf.numel() > before
+    others = [torch.full((before,), 85, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for _ in range(2):
+        Y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, want) and all(bool((t == 85).all()) for t in others)
+    assert q.last_device_status() == 0

@@ -70,6 +70,9 @@ class Tensor:
     def contiguous(self):
         return self if self.is_contiguous() else Tensor(self.world, self.shape, self.dtype, device=self.device)
 
+    def zero_(self):
+        return self.fill_(0)
+
     def fill_(self, value):
         self.world.made.append((self, self.world.current.cuda_stream))
         return self
@@ -290,3 +293,26 @@ def test_sizes_beyond_32_bits_are_refused(world, big):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
     assert not world.calls
+
+
+def test_a_workspace_keeps_the_buffers_that_it_outgrows(world):
+    """A captured graph holds the addresses of the buffers of its calls: they
+    stay allocated when a larger call needs a new one, and each is at least
+    twice the one before, so that they add up to less than the newest."""
+    import gc
+    import weakref
+    q = world.q
+    ws = q.Workspace()
+    seen, sizes = [], []
+    for n in (1 << 20, (1 << 20) + 1, 3 << 20, 5 << 20, 1 << 24):
+        buf = ws.get(n, q.KIND_INT8)
+        assert buf.numel() >= n
+        if not sizes or buf.numel() != sizes[-1]:
+            sizes.append(buf.numel())
+            seen.append(weakref.ref(buf))
+    del buf
+    world.made.clear()
+    gc.collect()
+    assert len(sizes) > 2 and all(r() is not None for r in seen)
+    assert all(b >= 2 * a for a, b in zip(sizes, sizes[1:]))
+    assert ws.get(64, q.KIND_INT8) is seen[-1]()

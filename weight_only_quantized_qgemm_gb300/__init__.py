@@ -179,17 +179,17 @@ class Workspace:
     one).  Calls leave their arrival counters at zero again (the rest is
     scratch), so one Workspace serves any sequence of calls of any kind on one
     stream (calls that may run at the same time, on different streams, need one
-    each).  Growing synchronises the device, so that no call still uses the old
-    buffer and the zero fill has landed before any stream uses the new one; a
-    captured graph keeps the addresses of the buffers that it was captured with,
-    so give it a Workspace that no larger call grows later.
+    each).  Growing synchronises the device, so that the zero fill has landed
+    before any stream uses the new buffer.  The buffers that it outgrows are
+    kept: captured graphs hold their addresses.  (Each is at least twice the one
+    before, so that they add up to less than the newest.)
 
     ``buf`` is the buffer that was asked for last."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
-        self._bufs = {}
+        self._bufs = {}   # by layout: the buffers so far, the newest last
 
     def get(self, nbytes: int, kind: int = KIND_FP8_BLOCK):
         """The buffer of the kind's layout, of at least nbytes (None for 0)."""
@@ -197,19 +197,19 @@ class Workspace:
         if nbytes == 0:
             return None
         layout = kind if kind in _OWN_LAYOUT else None
-        buf = self._bufs.get(layout)
-        if buf is None or buf.numel() < nbytes:
+        bufs = self._bufs.setdefault(layout, [])
+        if not bufs or bufs[-1].numel() < nbytes:
             dev = self.device or torch.cuda.current_device()
-            if buf is not None:
-                torch.cuda.synchronize(dev)
-            buf = self._bufs[layout] = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+            least = 2 * bufs[-1].numel() if bufs else 1 << 20
+            bufs.append(torch.zeros(max(nbytes, least), dtype=torch.uint8, device=dev))
             torch.cuda.synchronize(dev)
-        self.buf = buf
-        return buf
+        self.buf = bufs[-1]
+        return self.buf
 
     def reset(self):
-        for buf in self._bufs.values():
-            buf.zero_()
+        for bufs in self._bufs.values():
+            for buf in bufs:
+                buf.zero_()
 
 
 _default_ws = {}
