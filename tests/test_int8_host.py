@@ -153,3 +153,12 @@ def test_the_most_tiles_have_a_schedule(qg, M, N, K):
         assert 1 <= g <= max(sms, 2), (sms, rows, g)
         if M > 1 and K >= 2 ** 20 and sms > 1:
             assert rows == 256, (sms, rows)
+
+
+def test_the_binding_s_constants_are_the_header_s(qg):
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(qg.__file__), "..", "include", "qgemm.h")) as f:
+        header = f.read()
+    assert qg.MAX_TOP_K == int(re.search(r"#define QG_MAX_TOP_K (\d+)", header).group(1))
+    assert qg.KIND_INT8 == int(re.search(r"QG_KIND_INT8 = (\d+)", header).group(1))

@@ -254,7 +254,7 @@ struct Shared {
     float bound, tie;   // the bound, and the maximum that it was taken from
     float seg_mx[kSegs][kThreads];
     uint16_t flagged[kSegs * kThreads];   // seg * kThreads + thread
-    int nflagged, ncand, nlist;
+    int nflagged, ncand;
     PartSums parts[kMaxCluster];          // of a split row; written by the parts' CTAs, read by rank 0
     uint64_t list[kMaxTopK];              // the CTA's best entries, in order
     uint64_t cand[kCap];
@@ -268,6 +268,8 @@ __device__ __forceinline__ void cluster_meet() {
     cluster_sync_all();
 }
 
+static_assert(kMaxTopK <= kPairs, "the bound is one of the pairs' maxima");
+static_assert(kMaxCluster * kMaxTopK <= kCap, "the parts' lists fit the candidates");
 static_assert(offsetof(Shared, pair_key) % 16 == 0 && alignof(Shared) >= 16, "vector reads of the maxima");
 static_assert(offsetof(Shared, full) % 8 == 0 && offsetof(Shared, parts) % 16 == 0 &&
                   offsetof(Shared, list) % 8 == 0 && offsetof(Shared, cand) % 8 == 0,
@@ -630,7 +632,7 @@ __device__ __forceinline__ void take_row(const LogprobArgs& a, uint32_t m, uint3
 #pragma unroll
     for (int s = 16; s > 1; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
     if (lane == 0) sh.warp_mx[warp] = mx;
-    if (tid == 0) sh.nflagged = sh.ncand = sh.nlist = 0;
+    if (tid == 0) sh.nflagged = sh.ncand = 0;
     if (tid < kMaxTopK) sh.list[tid] = 0ull;
     meet();
     mx = sh.warp_mx[0];

@@ -5,7 +5,7 @@
 
 namespace qg {
 
-constexpr int kMaxTopK = 32;
+constexpr int kMaxTopK = QG_MAX_TOP_K;
 
 struct LogprobArgs {
     const void* logits;        // [M, ld] of type
