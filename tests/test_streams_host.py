@@ -102,6 +102,9 @@ class World:
     def empty(self, shape, dtype=None, device=None):
         return Tensor(self, shape, dtype)
 
+    def empty_like(self, t):
+        return Tensor(self, t.shape, t.dtype)
+
     def zeros(self, shape, dtype=None, device=None):
         return Tensor(self, (shape,) if isinstance(shape, int) else shape, dtype)
 
@@ -316,3 +319,50 @@ def test_a_workspace_keeps_the_buffers_that_it_outgrows(world):
     assert len(sizes) > 2 and all(r() is not None for r in seen)
     assert all(b >= 2 * a for a, b in zip(sizes, sizes[1:]))
     assert ws.get(64, q.KIND_INT8) is seen[-1]()
+
+
+def test_the_current_stream_is_not_switched_to(world, monkeypatch):
+    """stream= the current one: nothing to switch, which costs the host as much
+    as a small call."""
+    q = world.q
+    x = Tensor(world, (4, 64), torch.bfloat16)
+    for current in (Stream(SIDE), Stream(0)):
+        with world.stream(current):
+            with monkeypatch.context() as mp:
+                mp.setattr(world, "stream", None, raising=False)
+                for stream in (current, current.cuda_stream):
+                    q.quantize_act_int8(x, stream=stream)
+                    q.logprobs(x, entropy=True, stream=stream)
+                    q.qgemm_bf16(x, Tensor(world, (128, 64), torch.bfloat16), stream=stream)
+                    assert world.calls[-1][2][-1] == current.cuda_stream
+    # the default streams of two devices have one handle
+    y = Tensor(world, (4, 64), torch.bfloat16, device=Device(1))
+    q.logprobs(y, entropy=True, stream=Stream(0, device=1))
+    assert world.device == 0
+
+
+def test_calls_with_all_outputs_given_hand_the_stream_on(world, monkeypatch):
+    q = world.q
+
+    def T(*shape, dtype=torch.bfloat16):
+        return Tensor(world, shape, dtype)
+
+    X, W, i8, f = T(4, 256), T(128, 256), torch.int8, torch.float32
+    codes = T(128, 256, dtype=torch.uint8), T(1, 2, dtype=f)
+    Xq, sx = T(4, 256, dtype=i8), T(4, dtype=f)
+    ws = q.Workspace()
+    for kind in (q.KIND_FP8_BLOCK, q.KIND_W8A8, q.KIND_INT8):
+        ws.get(4096, kind)
+    n = len(world.made)
+    monkeypatch.setattr(world, "stream", None, raising=False)
+    for call in (lambda st: q.qgemm_fp8_block(X, *codes, Y=X, workspace=ws, stream=st),
+                 lambda st: q.qgemm_fp8_block_multi(X, [codes], Ys=[X], workspace=ws, stream=st),
+                 lambda st: q.qgemm_bf16(X, W, Y=X, workspace=ws, stream=st),
+                 lambda st: q.quantize_act_int8(X, Xq, sx, stream=st),
+                 lambda st: q.qgemm_w8a8_int8(Xq, sx, Xq, sx, Y=T4, workspace=ws, stream=st)):
+        T4 = Tensor(world, (4, 4), torch.bfloat16)
+        n += 1
+        for st in (Stream(SIDE), SIDE):
+            call(st)
+            assert world.calls[-1][2][-1] == SIDE
+    assert len(world.made) == n

@@ -137,16 +137,35 @@ def _check(code: int, where: str) -> None:
         raise QgemmError(code, where)
 
 
+_dtype_codes = {}
+_raw_stream = None       # the current stream of a device, as a raw handle
+_current_device = None
+
+
 def _torch():
+    """torch, with what the entry points look up on every call."""
+    global _raw_stream, _current_device
     import torch
+    if _raw_stream is None:
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        # without building a stream object (0.1 us instead of 3 us a call)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: int(torch.cuda.current_stream(index).cuda_stream))
+        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})   # QG_BF16, QG_FP16, QG_FP32
     return torch
 
 
 def _stream_ptr(stream) -> int:
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        _torch()
+        return _raw_stream(_current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _elsewhere(stream) -> bool:
+    """True when `stream` is not the current stream of the current device."""
+    return _stream_ptr(stream) != _stream_ptr(None) or \
+        getattr(stream, "device_index", None) not in (None, _current_device())
 
 
 def _on_stream(stream, call, *args):
@@ -154,7 +173,8 @@ def _on_stream(stream, call, *args):
     one, so that whatever the call allocates, copies or fills belongs to the
     stream that its kernels run on.  (Made on the caller's stream, a copy would
     not be ordered with the kernel, and memory of the caller's pool may still be
-    in use by work queued there.)"""
+    in use by work queued there.)  It costs the host 9 us, so that calls with
+    nothing to make, all outputs given, hand the stream on instead."""
     torch = _torch()
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream_ptr(stream)
@@ -248,7 +268,7 @@ def qgemm_fp8_block(X, W, W_scale, Y=None, workspace=None, stream=None):
     float8_e4m3fn [N, K] contiguous; W_scale: float32 [ceil(N/128), ceil(K/128)]
     contiguous.  Y (optional): bf16 [M, N] with unit column stride.
     """
-    if stream is not None:
+    if stream is not None and Y is None and _elsewhere(stream):
         return _on_stream(stream, qgemm_fp8_block, X, W, W_scale, Y, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16:
@@ -263,9 +283,9 @@ def qgemm_fp8_block(X, W, W_scale, Y=None, workspace=None, stream=None):
         raise ValueError("shape mismatch between X, W and W_scale")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, X.device)
+    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, X.device, stream)
     _check(lib.qgemm_fp8_block(X.data_ptr(), _ld(X), W.data_ptr(), W_scale.data_ptr(), Y.data_ptr(),
-                               _ld(Y), M, N, K, ws, wsb, _stream_ptr(None)), "qgemm_fp8_block")
+                               _ld(Y), M, N, K, ws, wsb, _stream_ptr(stream)), "qgemm_fp8_block")
     return Y
 
 
@@ -283,7 +303,7 @@ def qgemm_fp8_block_multi(X, weights, Ys=None, workspace=None, stream=None):
     (1 to MAX_SEGMENTS of them, sharing X), in one launch; returns the list of
     Y_j (BF16 [M, N_j]).  Ys (optional): the output tensors, each with unit
     column stride."""
-    if stream is not None:
+    if stream is not None and Ys is None and _elsewhere(stream):
         return _on_stream(stream, qgemm_fp8_block_multi, X, weights, Ys, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16:
@@ -305,9 +325,9 @@ def qgemm_fp8_block_multi(X, weights, Ys=None, workspace=None, stream=None):
         outs.append(Y)
         segs[j] = Fp8Segment(W.data_ptr(), S.data_ptr(), Y.data_ptr(), _ld(Y), N)
         rows += -(-N // 128) * 128
-    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, rows, K, workspace, X.device)
+    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, rows, K, workspace, X.device, stream)
     _check(lib.qgemm_fp8_block_multi(X.data_ptr(), _ld(X), ctypes.cast(segs, ctypes.c_void_p), len(weights), M, K,
-                                     ws, wsb, _stream_ptr(None)), "qgemm_fp8_block_multi")
+                                     ws, wsb, _stream_ptr(stream)), "qgemm_fp8_block_multi")
     return outs
 
 
@@ -325,7 +345,7 @@ def qgemm_fp8_block_host(X, W, W_scale, Y=None, X_stage=None, workspace=None, st
     kept when absent.  The call is asynchronous: Y is complete after the
     stream is synchronised.
     """
-    if stream is not None:
+    if stream is not None and (Y is None or X_stage is None) and _elsewhere(stream):
         return _on_stream(stream, qgemm_fp8_block_host, X, W, W_scale, Y, X_stage, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16:
@@ -351,9 +371,9 @@ def qgemm_fp8_block_host(X, W, W_scale, Y=None, X_stage=None, workspace=None, st
                                                              device=W.device)
     elif not X_stage.is_cuda or X_stage.numel() * X_stage.element_size() < M * K * 2:
         raise ValueError("X_stage must be a device buffer of at least M*K bfloat16 elements")
-    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, W.device)
+    ws, wsb = _workspace_for(KIND_FP8_BLOCK, M, N, K, workspace, W.device, stream)
     _check(lib.qgemm_fp8_block_host(X.data_ptr(), _ld(X), W.data_ptr(), W_scale.data_ptr(), Y.data_ptr(),
-                                    _ld(Y), M, N, K, X_stage.data_ptr(), ws, wsb, _stream_ptr(None)),
+                                    _ld(Y), M, N, K, X_stage.data_ptr(), ws, wsb, _stream_ptr(stream)),
            "qgemm_fp8_block_host")
     return Y
 
@@ -364,7 +384,7 @@ def qgemm_lut3(X, Wq, qmap, scales, N: int, Y=None, workspace=None, stream=None)
     X: fp16 CUDA [M, K]; Wq: the packed bytes from :func:`pack_lut3` on the
     device; qmap: fp16 [8]; scales: fp16 [N, K/128] contiguous.
     """
-    if stream is not None:
+    if stream is not None and Y is None and _elsewhere(stream):
         return _on_stream(stream, qgemm_lut3, X, Wq, qmap, scales, N, Y, workspace)
     torch = _torch()
     if X.dtype != torch.float16 or qmap.dtype != torch.float16 or scales.dtype != torch.float16:
@@ -376,9 +396,9 @@ def qgemm_lut3(X, Wq, qmap, scales, N: int, Y=None, workspace=None, stream=None)
         raise ValueError("packed weights are smaller than pack_lut3 produces for this shape")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.float16, device=X.device)
-    ws, wsb = _workspace_for(KIND_LUT3, M, N, K, workspace, X.device)
+    ws, wsb = _workspace_for(KIND_LUT3, M, N, K, workspace, X.device, stream)
     _check(lib.qgemm_lut3(X.data_ptr(), _ld(X), Wq.data_ptr(), qmap.data_ptr(), scales.data_ptr(),
-                          Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(None)), "qgemm_lut3")
+                          Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(stream)), "qgemm_lut3")
     return Y
 
 
@@ -392,7 +412,7 @@ def quantize_act_e4m3(X, Xq=None, X_scale=None, stream=None):
     float32 [ceil(K/128), ldsx] with ldsx = M rounded up to 32; columns
     [M, ldsx) are 0).  Xq and X_scale (optional) are written in place.
     """
-    if stream is not None:
+    if stream is not None and (Xq is None or X_scale is None) and _elsewhere(stream):
         return _on_stream(stream, quantize_act_e4m3, X, Xq, X_scale)
     torch = _torch()
     if X.dtype != torch.bfloat16:
@@ -408,7 +428,7 @@ def quantize_act_e4m3(X, Xq=None, X_scale=None, stream=None):
     if tuple(Xq.shape) != (M, K) or X_scale.shape[0] != KB:
         raise ValueError("shape mismatch between X, Xq and X_scale")
     _check(lib.qg_quantize_act_e4m3(X.data_ptr(), _ld(X), Xq.data_ptr(), _ld(Xq), X_scale.data_ptr(),
-                                    _ld(X_scale), M, K, _stream_ptr(None)), "qg_quantize_act_e4m3")
+                                    _ld(X_scale), M, K, _stream_ptr(stream)), "qg_quantize_act_e4m3")
     return Xq, X_scale
 
 
@@ -416,7 +436,7 @@ def qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=None, workspace=None, stream=Non
     """Y[M, N] = sum over 128-wide K blocks kb of X_scale[kb, m] *
     W_scale[n/128, kb] * (Xq[m, kb] . W[n, kb]) (E4M3 x E4M3, FP32 fold, BF16
     out), with Xq, X_scale as :func:`quantize_act_e4m3` returns them."""
-    if stream is not None:
+    if stream is not None and Y is None and _elsewhere(stream):
         return _on_stream(stream, qgemm_w8a8_block, Xq, X_scale, W, W_scale, Y, workspace)
     torch = _torch()
     if Xq.dtype not in (torch.uint8, torch.float8_e4m3fn) or W.dtype not in (torch.uint8, torch.float8_e4m3fn):
@@ -431,9 +451,9 @@ def qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=None, workspace=None, stream=Non
         raise ValueError("shape mismatch between Xq, X_scale, W and W_scale")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=Xq.device)
-    ws, wsb = _workspace_for(KIND_W8A8, M, N, K, workspace, Xq.device)
+    ws, wsb = _workspace_for(KIND_W8A8, M, N, K, workspace, Xq.device, stream)
     _check(lib.qgemm_w8a8_block(Xq.data_ptr(), _ld(Xq), X_scale.data_ptr(), _ld(X_scale), W.data_ptr(),
-                                W_scale.data_ptr(), Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(None)),
+                                W_scale.data_ptr(), Y.data_ptr(), _ld(Y), M, N, K, ws, wsb, _stream_ptr(stream)),
            "qgemm_w8a8_block")
     return Y
 
@@ -441,29 +461,10 @@ def qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=None, workspace=None, stream=Non
 def qgemm_w8a8(X, W, W_scale, Y=None, workspace=None, stream=None):
     """The W8A8 path from BF16 activations: :func:`quantize_act_e4m3` then
     :func:`qgemm_w8a8_block` (two launches on one stream)."""
-    if stream is not None:
+    if stream is not None and _elsewhere(stream):
         return _on_stream(stream, qgemm_w8a8, X, W, W_scale, Y, workspace)
     Xq, X_scale = quantize_act_e4m3(X)
     return qgemm_w8a8_block(Xq, X_scale, W, W_scale, Y=Y, workspace=workspace)
-
-
-_dtype_codes = {}
-_raw_stream = None
-_current_device = None
-
-
-def _lazy():
-    """torch, with what the entry points below look up on every call."""
-    global _raw_stream, _current_device
-    torch = _torch()
-    if not _dtype_codes:
-        # the current stream of a device, without building a stream object
-        # (0.1 us instead of 3 us a call)
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-            (lambda index: int(torch.cuda.current_stream(index).cuda_stream))
-        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-        _dtype_codes.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})   # QG_BF16, QG_FP16, QG_FP32
-    return torch
 
 
 def _rows(t, what: str):
@@ -493,9 +494,9 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
     int8 [M, K], X_scale float32 [M]).  Xq and X_scale (optional) are written
     in place.
     """
-    if stream is not None:
+    if stream is not None and (Xq is None or X_scale is None) and _elsewhere(stream):
         return _on_stream(stream, quantize_act_int8, X, Xq, X_scale)
-    torch = _lazy()
+    torch = _torch()
     code = _dtype_codes.get(X.dtype)
     if code != 0 and code != 1:
         raise TypeError("X must be bfloat16 or float16")
@@ -523,8 +524,10 @@ def quantize_act_int8(X, Xq=None, X_scale=None, stream=None):
         if X_scale.shape != (M,) or X_scale.device != dev:
             raise ValueError("X_scale must be [M] on X's device")
     if K == 0:   # rows of nothing, which the library leaves alone
+        if stream is not None and _elsewhere(stream):
+            return _on_stream(stream, quantize_act_int8, X, Xq, X_scale)
         return Xq, X_scale.fill_(1.0)
-    st = _raw_stream(index)
+    st = _raw_stream(index) if stream is None else _stream_ptr(stream)
     r = lib.qg_quantize_act_int8(X.data_ptr(), code, ld, Xq.data_ptr(), ldq, X_scale.data_ptr(), M, K, st)
     if r:
         raise QgemmError(r, "qg_quantize_act_int8")
@@ -541,9 +544,9 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
     float32 [N]; bias (optional): float32 [N].  Y (optional): [M, N] with unit
     column stride, in bfloat16 (the default), float16 or float32 (out_dtype).
     """
-    if stream is not None:
+    if stream is not None and Y is None and _elsewhere(stream):
         return _on_stream(stream, qgemm_w8a8_int8, Xq, X_scale, W, W_scale, bias, out_dtype, Y, workspace)
-    torch = _lazy()
+    torch = _torch()
     i8, f32 = torch.int8, torch.float32
     if Xq.dtype != i8 or W.dtype != i8:
         raise TypeError("Xq and W must be int8")
@@ -585,7 +588,7 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
         rows, cols, ldy = _rows(Y, "Y")
         if rows != M or cols != N or Y.device != dev:
             raise ValueError("Y must be [M, N] on the same device")
-    st = _raw_stream(index)
+    st = _raw_stream(index) if stream is None else _stream_ptr(stream)
     ws, wsb = _workspace_for(KIND_INT8, M, N, K, workspace, dev, st)
     r = lib.qgemm_w8a8_int8(Xq.data_ptr(), ldq, X_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(), b,
                             Y.data_ptr(), code, ldy, M, N, K, ws, wsb, st)
@@ -623,9 +626,9 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
     of -inf and entropy 0; a token outside the vocabulary has -inf; a row with
     a NaN or +inf gives NaN (see include/qgemm.h).
     """
-    if stream is not None:
+    if stream is not None and _elsewhere(stream):
         return _on_stream(stream, logprobs, logits, tokens, top_k, entropy)
-    torch = _lazy()
+    torch = _torch()
     f32, i64 = torch.float32, torch.int64
     code = _dtype_codes.get(logits.dtype)
     if code is None:
@@ -680,7 +683,7 @@ def qgemm_bf16(X, W, Y=None, workspace=None, stream=None):
     X: bf16 CUDA [M, K] (row stride a multiple of 8); W: bf16 [N, K]
     contiguous; Y (optional): bf16 [M, N] with unit column stride.
     """
-    if stream is not None:
+    if stream is not None and Y is None and _elsewhere(stream):
         return _on_stream(stream, qgemm_bf16, X, W, Y, workspace)
     torch = _torch()
     if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
@@ -693,9 +696,9 @@ def qgemm_bf16(X, W, Y=None, workspace=None, stream=None):
         raise ValueError("shape mismatch between X and W")
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
-    ws, wsb = _workspace_for(KIND_BF16, M, N, K, workspace, X.device)
+    ws, wsb = _workspace_for(KIND_BF16, M, N, K, workspace, X.device, stream)
     _check(lib.qgemm_bf16(X.data_ptr(), _ld(X), W.data_ptr(), Y.data_ptr(), _ld(Y), M, N, K, ws, wsb,
-                          _stream_ptr(None)), "qgemm_bf16")
+                          _stream_ptr(stream)), "qgemm_bf16")
     return Y
 
 
@@ -725,7 +728,7 @@ def debug_fp8_split(X, stream=None):
     """The FP8 GEMM's activation split of BF16 X [B, 128] (one 128-wide K
     block per row): returns (hi, lo, e) with hi, lo uint8 E4M3 codes [B, 128]
     and e int32 [B], such that x * 2^e = hi + lo / 16 (see include/qgemm.h)."""
-    if stream is not None:
+    if stream is not None and _elsewhere(stream):
         return _on_stream(stream, debug_fp8_split, X)
     torch = _torch()
     if X.dtype != torch.bfloat16 or X.dim() != 2 or X.shape[1] != 128 or not X.is_contiguous():
@@ -741,13 +744,13 @@ def debug_fp8_split(X, stream=None):
 
 def dequant_lut3(Wq, qmap, scales, N: int, K: int, out=None, stream=None):
     """Packed LUT3 weights -> FP16 [N, K], with the LUT3 GEMM's own dequantiser."""
-    if stream is not None:
+    if stream is not None and out is None and _elsewhere(stream):
         return _on_stream(stream, dequant_lut3, Wq, qmap, scales, N, K, out)
     torch = _torch()
     if out is None:
         out = torch.empty((N, K), dtype=torch.float16, device=Wq.device)
     _check(lib.qg_dequant_lut3(Wq.data_ptr(), qmap.data_ptr(), scales.data_ptr(), out.data_ptr(), N, K,
-                               _stream_ptr(None)), "qg_dequant_lut3")
+                               _stream_ptr(stream)), "qg_dequant_lut3")
     return out
 
 
