@@ -366,3 +366,13 @@ def test_calls_with_all_outputs_given_hand_the_stream_on(world, monkeypatch):
             call(st)
             assert world.calls[-1][2][-1] == SIDE
     assert len(world.made) == n
+
+
+def test_tuners_buffers_belong_to_their_stream(world, monkeypatch):
+    q = world.q
+    monkeypatch.setattr(q, "workspace_bytes_max", lambda N: 4096)
+    monkeypatch.setattr(q, "workspace_bytes_max_w8a8", lambda M, N: 4096)
+    X, W = Tensor(world, (4, 256), torch.bfloat16), Tensor(world, (128, 256), torch.bfloat16)
+    n = len(world.made)
+    q.tune_bf16(X, [W], stream=SIDE)
+    _check_side(world, n, "qg_tune_bf16")

@@ -799,6 +799,8 @@ def dispatch_clear() -> None:
 def debug_schedule(kind: int, M: int, N: int, K: int, stream=None):
     """The device's work split of a shape: (ranges int64 [G, 2], info int32
     [G, 6]) as numpy arrays (see include/qgemm.h)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(stream, debug_schedule, kind, M, N, K)
     torch = _torch()
     g = ctypes.c_int(0)
     _check(lib.qg_debug_schedule(kind, M, N, K, ctypes.byref(g), None, None, 0, None), "qg_debug_schedule")
@@ -806,7 +808,7 @@ def debug_schedule(kind: int, M: int, N: int, K: int, stream=None):
     ranges = torch.empty((G, 2), dtype=torch.int64, device="cuda")
     info = torch.empty((G, 6), dtype=torch.int32, device="cuda")
     _check(lib.qg_debug_schedule(kind, M, N, K, ctypes.byref(g), ranges.data_ptr(), info.data_ptr(), G,
-                                 _stream_ptr(stream)), "qg_debug_schedule")
+                                 _stream_ptr(None)), "qg_debug_schedule")
     torch.cuda.synchronize()
     return ranges.cpu().numpy(), info.cpu().numpy()
 
@@ -828,6 +830,8 @@ def tune_fp8(X, W_copies, W_scale, calls: int = 200, workspace=None, stream=None
     """Exactness-gated tuning of the dispatch table for the shape of X and W
     (see qg_tune_fp8 in include/qgemm.h).  W_copies: equal E4M3 weight
     tensors the timed calls rotate over.  Returns (grid, us per call)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(stream, tune_fp8, X, W_copies, W_scale, calls, workspace)
     torch = _torch()
     M, K = X.shape
     N = W_copies[0].shape[0]
@@ -839,7 +843,7 @@ def tune_fp8(X, W_copies, W_scale, calls: int = 200, workspace=None, stream=None
     _check(lib.qg_tune_fp8(X.data_ptr(), _ld(X), ctypes.cast(ptrs, ctypes.c_void_p), len(W_copies),
                            W_scale.data_ptr(), Y.data_ptr(), N, Y_ref.data_ptr(), M, N, K,
                            buf.data_ptr() if buf is not None else None, nb, calls, ctypes.byref(g), ctypes.byref(us),
-                           _stream_ptr(stream)), "qg_tune_fp8")
+                           _stream_ptr(None)), "qg_tune_fp8")
     _ws_need.clear()
     return g.value, us.value
 
@@ -852,6 +856,8 @@ def workspace_bytes_max_w8a8(M: int, N: int) -> int:
 
 def tune_bf16(X, W_copies, calls: int = 200, workspace=None, stream=None):
     """As tune_fp8 for the dense BF16 GEMM (W_copies: equal BF16 weights)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(stream, tune_bf16, X, W_copies, calls, workspace)
     torch = _torch()
     M, K = X.shape
     N = W_copies[0].shape[0]
@@ -862,7 +868,7 @@ def tune_bf16(X, W_copies, calls: int = 200, workspace=None, stream=None):
     g, us = ctypes.c_int(0), ctypes.c_float(0)
     _check(lib.qg_tune_bf16(X.data_ptr(), _ld(X), ctypes.cast(ptrs, ctypes.c_void_p), len(W_copies), Y.data_ptr(),
                             N, Y_ref.data_ptr(), M, N, K, buf.data_ptr() if buf is not None else None, nb, calls,
-                            ctypes.byref(g), ctypes.byref(us), _stream_ptr(stream)), "qg_tune_bf16")
+                            ctypes.byref(g), ctypes.byref(us), _stream_ptr(None)), "qg_tune_bf16")
     _ws_need.clear()
     return g.value, us.value
 
@@ -870,6 +876,8 @@ def tune_bf16(X, W_copies, calls: int = 200, workspace=None, stream=None):
 def tune_w8a8(Xq, X_scale, W_copies, W_scale, calls: int = 100, workspace=None, stream=None):
     """As tune_fp8 for the W8A8 GEMM on quantised activations (Xq, X_scale as
     quantize_act_e4m3 returns them; W_copies: equal E4M3 weights)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(stream, tune_w8a8, Xq, X_scale, W_copies, W_scale, calls, workspace)
     torch = _torch()
     M, K = Xq.shape
     N = W_copies[0].shape[0]
@@ -881,13 +889,15 @@ def tune_w8a8(Xq, X_scale, W_copies, W_scale, calls: int = 100, workspace=None, 
     _check(lib.qg_tune_w8a8(Xq.data_ptr(), _ld(Xq), X_scale.data_ptr(), _ld(X_scale),
                             ctypes.cast(ptrs, ctypes.c_void_p), len(W_copies), W_scale.data_ptr(), Y.data_ptr(), N,
                             Y_ref.data_ptr(), M, N, K, buf.data_ptr() if buf is not None else None, nb, calls,
-                            ctypes.byref(g), ctypes.byref(us), _stream_ptr(stream)), "qg_tune_w8a8")
+                            ctypes.byref(g), ctypes.byref(us), _stream_ptr(None)), "qg_tune_w8a8")
     _ws_need.clear()
     return g.value, us.value
 
 
 def tune_lut3(X, Wq_copies, qmap, scales, N: int, calls: int = 200, workspace=None, stream=None):
     """As tune_fp8 for the 3-bit LUT GEMM (Wq_copies: equal packed weights)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(stream, tune_lut3, X, Wq_copies, qmap, scales, N, calls, workspace)
     torch = _torch()
     M, K = X.shape
     Y = torch.empty((M, N), dtype=torch.float16, device=X.device)
@@ -898,6 +908,6 @@ def tune_lut3(X, Wq_copies, qmap, scales, N: int, calls: int = 200, workspace=No
     _check(lib.qg_tune_lut3(X.data_ptr(), _ld(X), ctypes.cast(ptrs, ctypes.c_void_p), len(Wq_copies),
                             qmap.data_ptr(), scales.data_ptr(), Y.data_ptr(), N, Y_ref.data_ptr(), M, N, K,
                             buf.data_ptr() if buf is not None else None, nb, calls, ctypes.byref(g),
-                            ctypes.byref(us), _stream_ptr(stream)), "qg_tune_lut3")
+                            ctypes.byref(us), _stream_ptr(None)), "qg_tune_lut3")
     _ws_need.clear()
     return g.value, us.value
