@@ -543,6 +543,11 @@ def qgemm_w8a8_int8(Xq, X_scale, W, W_scale, bias=None, out_dtype=None, Y=None, 
     :func:`quantize_act_int8` returns them; W: int8 [N, K] contiguous; W_scale:
     float32 [N]; bias (optional): float32 [N].  Y (optional): [M, N] with unit
     column stride, in bfloat16 (the default), float16 or float32 (out_dtype).
+
+    The products are summed in FP32: exactly while every partial sum stays below
+    2^24 in magnitude (always for K <= 1024, with codes of mixed signs far
+    longer), beyond that with up to 2^-23 of the sum lost, towards zero, every 16
+    products (see include/qgemm.h).
     """
     if stream is not None and Y is None and _elsewhere(stream):
         return _on_stream(stream, qgemm_w8a8_int8, Xq, X_scale, W, W_scale, bias, out_dtype, Y, workspace)
