@@ -463,8 +463,9 @@ qg_status qg_dequant_lut3(const void *Wq, const void *qmap, const void *scales,
  *
  * qg_dispatch_set: ctas in 1 .. SM count of the current device sets the
  *   entry (a grid larger than the shape's work units is cut to their
- *   number); ctas == 0 removes it.  M in 1..32 (1..65536 for QG_KIND_W8A8
- *   and QG_KIND_INT8).
+ *   number; QG_KIND_INT8 rounds it up to an even one where the shape's tiles
+ *   run on CTA pairs); ctas == 0 removes it.  M in 1..32 (1..65536 for
+ *   QG_KIND_W8A8 and QG_KIND_INT8).
  * qg_dispatch_get: the grid the next call of the shape launches on the
  *   current device (0 for invalid arguments).
  * qg_dispatch_rule: the grid the built-in cost rule picks for the shape on
