@@ -396,6 +396,155 @@ qg_status qg_logprobs(const void *logits, int type, int64_t ld,
                       int M, int V, struct CUstream_st *stream);
 
 /*
+ * Layers of experts: a router sends every token to top_k of E experts, whose
+ * feed-forward products run on the rows of the tokens that chose them.  The
+ * rows of all experts together are ordered by expert, then by token; offsets
+ * says where each expert's begin.  Neither is ever needed on the host, so that
+ * a captured call serves any routing.  A layer is
+ *
+ *   qg_moe_route             logits [M, E] -> experts, weights, offsets, rows
+ *   qg_quantize_rows_e4m3    X [M, K], rows -> codes and scales of the M top_k rows
+ *   qgemm_w8a8_grouped       gate and up products of every expert, [., 2 F]
+ *   qg_quantize_rows_e4m3    gated, with num_rows = offsets + E -> codes of [., F]
+ *   qgemm_w8a8_grouped       down product
+ *   qg_moe_combine           back to [M, H]
+ *
+ * (additions of this library, with no counterpart in the paper).
+ */
+#define QG_MAX_EXPERTS 1024
+
+/* Scores of qg_moe_route. */
+enum { QG_SCORE_SOFTMAX = 0, QG_SCORE_SIGMOID = 1 };
+
+/*
+ * Router.  For every token m, in FP32: the score of expert e is
+ *   s[e] = softmax(logits[m])[e]  or  1 / (1 + exp(-logits[m, e])),
+ * the top_k experts are those of the largest s[e] + bias[e] (without a bias in
+ * the order of the logits), ties to the lower index, and their weights are
+ *   w = s[e] * scale / (sum of s over the chosen ones)   (renormalize != 0)
+ *   w = s[e] * scale                                     (else).
+ * Which experts are chosen does not depend on rounding: scores with a bias that
+ * lie closer than their FP32 error are compared in 64 bits.
+ *   logits   device, QG_BF16, QG_FP16 or QG_FP32 [M, ld], ld >= E.  -inf: the
+ *            expert is masked for this token (as is one whose bias is -inf or NaN)
+ *   bias     device, FP32 [E], or NULL
+ *   experts  device, int32 [M, top_k]: in order; -1 where fewer than top_k are left
+ *   weights  device, FP32 [M, top_k]; 0 beside a -1.  A token with a NaN or +inf
+ *            logit is routed nowhere, with weights of NaN
+ *   offsets  device, int32 [E + 1]: the rows of expert e are offsets[e] ..
+ *            offsets[e + 1] - 1, in the order of the tokens
+ *   rows     device, int32 [M, top_k]: the row of each choice; -1 beside a -1
+ *   M, E, top_k   0 <= M <= 2^20, 1 <= E <= QG_MAX_EXPERTS, 1 <= top_k <= E, 32
+ *   workspace     of qg_moe_route_workspace_bytes(M, E) bytes, 16-byte aligned, scratch
+ *                 (nothing is expected in it)
+ * With M = 0 only offsets are written (zeros).
+ */
+size_t qg_moe_route_workspace_bytes(int M, int E);
+qg_status qg_moe_route(const void *logits, int type, int64_t ld, const float *bias, int score, int renormalize,
+                       float scale, int top_k, int32_t *experts, float *weights, int32_t *offsets, int32_t *rows,
+                       int M, int E, void *workspace, size_t workspace_bytes, struct CUstream_st *stream);
+
+/*
+ * E4M3 codes and scales of rows, as qg_quantize_act_e4m3 (the same codes and
+ * scales bit for bit), with three additions:
+ *   gated != 0    row m has 2 K columns, a gate and a value: what is quantised is
+ *                 silu(X[m, k]) * X[m, K + k], silu(g) = g / (1 + exp(-g)), in FP32
+ *   rows          device, int32 [M, top_k], or NULL: row m's codes and scales go to
+ *                 rows rows[m, 0 .. top_k - 1] of the output (one outside 0 ..
+ *                 out_rows - 1: nowhere) instead of row m
+ *   num_rows      device, one int32, or NULL: only rows m < *num_rows are read
+ * Output rows that nothing goes to are left as they were, codes and scales both.
+ *   X        device, QG_BF16 or QG_FP16 [M, ldx], 16-byte aligned, ldx >= K (gated:
+ *            2 K), ldx % 8 == 0
+ *   Xq       device, E4M3 codes [out_rows, ldxq], 16-byte aligned, ldxq >= K, ldxq % 16 == 0
+ *   X_scale  device, FP32 [ceil(K/128), ldsx], 16-byte aligned, ldsx >= out_rows,
+ *            ldsx % 4 == 0
+ *   M, out_rows, K   0 <= M <= 2^22, 0 <= out_rows < 2^31, K % 16 == 0, 1 <= top_k <= 32
+ */
+qg_status qg_quantize_rows_e4m3(const void *X, int x_type, int64_t ldx, int gated, const int32_t *rows, int top_k,
+                                const int32_t *num_rows, uint8_t *Xq, int64_t ldxq, float *X_scale, int64_t ldsx,
+                                int M, int out_rows, int K, struct CUstream_st *stream);
+
+/*
+ * W8A8 block-scaled GEMM grouped by expert: for the rows r of each expert e,
+ * offsets[e] <= r < offsets[e + 1],
+ *   Y[r, n] = sum over 128-wide K blocks kb of X_scale[kb, r] * W_scale[e, n/128, kb]
+ *             * (sum over k in kb of Xq[r, k] * W[e, n, k])
+ * with FP32 sums, as qgemm_w8a8_block for each expert on its own.  Rows in front
+ * of offsets[0] and from offsets[E] on are left as they were; groups may be empty.
+ *   Xq       device, E4M3 codes [R, ldxq], 16-byte aligned, ldxq >= K, ldxq % 16 == 0
+ *   X_scale  device, FP32 [ceil(K/128), ldsx], ldsx >= R
+ *   W        device, E4M3 codes [E, N, K], contiguous, 16-byte aligned
+ *   W_scale  device, FP32 [E, ceil(N/128), ceil(K/128)], contiguous
+ *   offsets  device, int32 [E + 1], ascending, within 0 .. R (entries that are not
+ *            are taken as the nearest that are)
+ *   Y        device, QG_BF16, QG_FP16 or QG_FP32 [R, ldy], ldy >= N
+ *   R, E, N, K   0 <= R <= 2^24, 1 <= E <= QG_MAX_EXPERTS, E N < 2^31, K % 16 == 0
+ *   workspace    of qg_workspace_bytes_grouped(R, E) bytes, 256-byte aligned,
+ *                zero-filled before its first use and left so that the next call
+ *                of any shape can use it; its layout is that of this kind alone
+ * Neither the tiling nor the split of the work depends on anything but R, E, N,
+ * K and offsets: equal calls give equal bits.
+ */
+size_t qg_workspace_bytes_grouped(int R, int E);
+qg_status qgemm_w8a8_grouped(const uint8_t *Xq, int64_t ldxq, const float *X_scale, int64_t ldsx, const uint8_t *W,
+                             const float *W_scale, const int32_t *offsets, void *Y, int y_type, int64_t ldy, int R,
+                             int E, int N, int K, void *workspace, size_t workspace_bytes,
+                             struct CUstream_st *stream);
+
+/*
+ * The experts' results back to the tokens:
+ *   out[m, k] = sum over j of weights[m, j] * Y[rows[m, j], k]  (+ residual[m, k])
+ * in FP32, in the order of j, rounded once.  A row outside 0 .. R - 1 counts as
+ * zeros.
+ *   Y, residual (or NULL), out   device, QG_BF16, QG_FP16 or QG_FP32 (type), row
+ *            strides ldy, ldr, ldo >= K; out may be residual
+ *   rows, weights   device, int32 and FP32 [M, top_k]
+ *   M, R, K, top_k  0 <= M <= 2^22, 0 <= R < 2^31, 1 <= top_k <= 32
+ */
+qg_status qg_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *rows, const float *weights, int top_k,
+                         const void *residual, int64_t ldr, void *out, int64_t ldo, int M, int R, int K,
+                         struct CUstream_st *stream);
+
+#define QG_MAX_DRAFTS 31
+
+/*
+ * Verification of drafted tokens against the target's probabilities (an
+ * addition of this library, with no counterpart in the paper).  Sequence b has
+ * lengths[b] <= G drafted tokens d_0, d_1, ...; p_j is the softmax of target row
+ * (b, j), q_j that of draft row (b, j), both in FP32.
+ *   - The drafts are kept in order while uniform[b, j] * q_j(d_j) < p_j(d_j);
+ *     accepted[b] = n is how many are.
+ *   - One more token follows: with n < lengths[b] the v of the largest
+ *     max(p_n(v) - q_n(v), 0) / noise[b, v] (of p_n(v) / noise[b, v] where that is
+ *     0 for every v), with n = lengths[b] that of the largest p_n(v) / noise[b, v];
+ *     ties to the lower v.  With uniform in [0, 1) and exponential noise the tokens
+ *     are distributed as the target's own.
+ *   - tokens_out[b]: the n kept drafts, the token that follows, then -1.
+ * draft NULL: the drafts are certain (q_j is 1 at d_j).  uniform and noise both
+ * NULL: greedy, a draft is kept while it is the largest logit of its target row,
+ * and the largest of row n follows (draft must be NULL).
+ *   target      device, [B, G + 1, V] of type (QG_BF16, QG_FP16 or QG_FP32), strides
+ *               t_seq and t_row in elements, t_row >= V; as the tokens are drawn from
+ *               them: divided by the temperature, with -inf where a filter leaves a
+ *               token out
+ *   draft       device, [B, G, V] of the same type, strides d_seq and d_row, or NULL
+ *   tokens      device, int64 [B, ldt]; one outside 0 .. V - 1 is never kept
+ *   uniform     device, FP32 [B, ldu];  noise  device, FP32 [B, ldn], positive (a 0
+ *               makes a ratio of infinity, a negative one is never drawn)
+ *   lengths     device, int32 [B] (cut to 0 .. G), or NULL: all G
+ *   accepted    device, int32 [B];  tokens_out  device, int64 [B, G + 1]
+ *   B, G, V     0 <= B <= 65536, 0 <= G <= QG_MAX_DRAFTS, 1 <= V <= 2^30
+ * A row with a NaN or +inf (greedy: a NaN is never the largest), or with nothing
+ * but -inf, keeps no draft, and the token drawn from it is -1.  Rows behind a
+ * sequence's length are not read.
+ */
+qg_status qg_verify_drafts(const void *target, int type, int64_t t_seq, int64_t t_row, const void *draft,
+                           int64_t d_seq, int64_t d_row, const int64_t *tokens, int64_t ldt, const float *uniform,
+                           int64_t ldu, const float *noise, int64_t ldn, const int32_t *lengths, int32_t *accepted,
+                           int64_t *tokens_out, int B, int G, int V, struct CUstream_st *stream);
+
+/*
  * Packed size, in bytes, of an [N, K] 3-bit code matrix:
  * ceil(N/128) * ceil(K/256) * 16384.
  */

@@ -26,6 +26,12 @@ The names follow the C ABI in ``include/qgemm.h``:
   FP16 or FP32 output, optional bias.
 * :func:`logprobs` -- over rows of logits: log probabilities of given tokens,
   entropy and the top alternatives.
+* :func:`verify_drafts` -- drafted tokens against the target's probabilities:
+  how many are kept, and the token that follows.
+* :func:`moe_route`, :func:`quantize_rows_e4m3`, :func:`qgemm_w8a8_grouped`,
+  :func:`moe_combine` -- layers of experts: router and order by expert, E4M3
+  activations on the experts' rows (or of silu(gate) * up), the W8A8 GEMM grouped
+  by expert, and the weighted sum back to the tokens.
 * :func:`pack_lut3` / :func:`unpack_lut3` -- offline nibble packer (host).
 * :func:`debug_fp8_split` / :func:`dequant_lut3` -- test aids: the FP8
   kernel's activation split and the LUT3 kernel's dequantiser on their own,
@@ -52,6 +58,8 @@ __all__ = [
     "quantize_act_e4m3", "qgemm_w8a8_block", "qgemm_w8a8", "KIND_W8A8", "MAX_M_W8A8",
     "tune_bf16", "tune_w8a8", "workspace_bytes_max_w8a8",
     "quantize_act_int8", "qgemm_w8a8_int8", "int8_tile_rows", "KIND_INT8", "logprobs", "LogProbs", "MAX_TOP_K",
+    "moe_route", "MoeRoute", "quantize_rows_e4m3", "qgemm_w8a8_grouped", "moe_combine", "MAX_EXPERTS", "KIND_GROUPED",
+    "verify_drafts", "DraftCheck", "MAX_DRAFTS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -62,6 +70,7 @@ KIND_LUT3 = 1
 KIND_BF16 = 2
 KIND_W8A8 = 3
 KIND_INT8 = 4
+KIND_GROUPED = 5   # of Workspace only: the grouped GEMM has no schedule on the host
 MAX_M_W8A8 = 65536
 STATUS = {
     0: "QG_OK", 1: "QG_ERR_INVALID_ARG", 2: "QG_ERR_UNSUPPORTED_SHAPE", 3: "QG_ERR_MISALIGNED",
@@ -98,6 +107,13 @@ _SIGS = {
     "qg_quantize_act_int8": (_I, [_P, _I, _L, _P, _L, _P, _I, _I, _P]),
     "qgemm_w8a8_int8": (_I, [_P, _L, _P, _P, _P, _P, _P, _I, _L, _I, _I, _I, _P, _S, _P]),
     "qg_logprobs": (_I, [_P, _I, _L, _P, _L, _I, _P, _P, _I, _P, _P, _I, _I, _P]),
+    "qg_moe_route_workspace_bytes": (_S, [_I, _I]),
+    "qg_moe_route": (_I, [_P, _I, _L, _P, _I, _I, ctypes.c_float, _I, _P, _P, _P, _P, _I, _I, _P, _S, _P]),
+    "qg_quantize_rows_e4m3": (_I, [_P, _I, _L, _I, _P, _I, _P, _P, _L, _P, _L, _I, _I, _I, _P]),
+    "qg_workspace_bytes_grouped": (_S, [_I, _I]),
+    "qgemm_w8a8_grouped": (_I, [_P, _L, _P, _L, _P, _P, _P, _P, _I, _L, _I, _I, _I, _I, _P, _S, _P]),
+    "qg_moe_combine": (_I, [_P, _I, _L, _P, _P, _I, _P, _L, _P, _L, _I, _I, _I, _P]),
+    "qg_verify_drafts": (_I, [_P, _I, _L, _L, _P, _L, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _I, _I, _P]),
     "qg_lut3_packed_bytes": (_S, [_I, _I]),
     "pack_lut3": (_I, [_P, _P, _I, _I]),
     "unpack_lut3": (_I, [_P, _P, _I, _I]),
@@ -190,13 +206,14 @@ def workspace_bytes(kind: int, M: int, N: int, K: int) -> int:
 
 
 # the kinds whose workspaces share a layout: each of these alone, all others together
-_OWN_LAYOUT = (KIND_W8A8, KIND_INT8)
+_ROUTE = -1   # the router's scratch, which nothing expects to be zero
+_OWN_LAYOUT = (KIND_W8A8, KIND_INT8, KIND_GROUPED, _ROUTE)
 
 
 class Workspace:
     """Zero-filled device byte buffers that grow on demand, one for each
-    workspace layout (the W8A8 and INT8 kinds have their own, the others share
-    one).  Calls leave their arrival counters at zero again (the rest is
+    workspace layout (the W8A8, INT8 and grouped kinds have their own, the others
+    share one).  Calls leave their arrival counters at zero again (the rest is
     scratch), so one Workspace serves any sequence of calls of any kind on one
     stream (calls that may run at the same time, on different streams, need one
     each).  Growing synchronises the device, so that the zero fill has landed
@@ -680,6 +697,375 @@ def logprobs(logits, tokens=None, top_k: int = 0, entropy: bool = False, stream=
     if r:
         raise QgemmError(r, "qg_logprobs")
     return LogProbs(token_lp, ent, ids, top)
+
+
+MAX_EXPERTS = 1024
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class MoeRoute(NamedTuple):
+    """What :func:`moe_route` returns."""
+    experts: Any   # int32 [M, top_k]
+    weights: Any   # float32 [M, top_k]
+    offsets: Any   # int32 [E + 1]
+    rows: Any      # int32 [M, top_k]
+
+
+def _workspace_of(kind, key, ask, workspace, device, stream):
+    """The workspace of a call whose need `ask` says (kept by key)."""
+    need = _ws_need.get(key)
+    if need is None:
+        need = _ws_need[key] = int(ask())
+    if need == 0:
+        return None, 0
+    if workspace is None:
+        at = (device, stream)
+        workspace = _default_ws.get(at)
+        if workspace is None:
+            workspace = _default_ws[at] = Workspace(device)
+    buf = workspace.get(need, kind) if isinstance(workspace, Workspace) else workspace
+    return buf.data_ptr(), buf.numel() * buf.element_size()
+
+
+def _vector(t, dtype, n, dev, what: str):
+    """The address of a contiguous tensor of n elements."""
+    if t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(what + " must be contiguous " + str(dtype).replace("torch.", ""))
+    if t.numel() != n or t.device != dev:
+        raise ValueError(f"{what} must have {n} elements on the same device")
+    return t.data_ptr()
+
+
+def moe_route(logits, top_k: int, score: str = "softmax", bias=None, renormalize: bool = True, scale: float = 1.0,
+              workspace=None, stream=None) -> MoeRoute:
+    """Router of a layer of experts: for every token (row of logits [M, E], bf16,
+    fp16 or fp32) the top_k experts by score, their weights, and the order of all
+    choices by expert.
+
+    score: "softmax" or "sigmoid" of the logits; bias (optional, float32 [E]) is
+    added for the choice alone.  Ties go to the lower index; -inf masks an expert.
+    weights: the scores over their sum (renormalize) times scale.  Expert e's rows
+    are offsets[e] .. offsets[e + 1] - 1, in the order of the tokens; rows[m, j] is
+    the row of token m's j-th choice.  Where fewer than top_k experts are left,
+    experts and rows are -1 and the weight 0; a token with a NaN or +inf logit is
+    routed nowhere, with weights of NaN.
+    """
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(stream, moe_route, logits, top_k, score, bias, renormalize, scale, workspace)
+    torch = _torch()
+    code = _dtype_codes.get(logits.dtype)
+    if code is None:
+        raise TypeError("logits must be bfloat16, float16 or float32")
+    kind = _SCORES.get(score)
+    if kind is None:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    M, E, ld = _rows(logits, "logits")
+    if (M | E | top_k) >> 31:
+        raise ValueError(_SIZE)
+    dev = logits.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
+    b = None if bias is None else _vector(bias, torch.float32, E, dev, "bias")
+    i32 = torch.int32
+    experts = torch.empty((M, top_k), dtype=i32, device=dev)
+    weights = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+    offsets = torch.empty((E + 1,), dtype=i32, device=dev)
+    rows = torch.empty((M, top_k), dtype=i32, device=dev)
+    st = _raw_stream(index)
+    ws, wsb = _workspace_of(_ROUTE, (_ROUTE, M, E, dev), lambda: lib.qg_moe_route_workspace_bytes(M, E), workspace, dev, st)
+    r = lib.qg_moe_route(logits.data_ptr(), code, ld, b, kind, 1 if renormalize else 0, scale, top_k,
+                         experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), M, E, ws, wsb, st)
+    if r:
+        raise QgemmError(r, "qg_moe_route")
+    return MoeRoute(experts, weights, offsets, rows)
+
+
+def quantize_rows_e4m3(X, gated: bool = False, rows=None, num_rows=None, out_rows=None, Xq=None, X_scale=None,
+                       stream=None):
+    """E4M3 codes and FP32 scales per (row, 128 columns), as
+    :func:`quantize_act_e4m3` makes them, of the rows that a layer of experts needs.
+
+    X: bf16 or fp16 CUDA [M, K] (row stride a multiple of 8, K % 16 == 0); gated:
+    [M, 2 K], and silu(X[:, :K]) * X[:, K:] is quantised.  rows (optional, int32
+    [M, top_k] as :func:`moe_route` returns it): row m goes to rows rows[m, :] of the
+    output (-1: nowhere), of out_rows rows (M * top_k when absent).  num_rows
+    (optional, int32, one element on the device, e.g. ``route.offsets[-1:]``): only
+    the rows before it are read.  Output rows that nothing goes to are left as they
+    were.  Returns (Xq uint8 [out_rows, K], X_scale float32 [ceil(K/128), ldsx]) with
+    ldsx = out_rows rounded up to 32.  Xq and X_scale (optional) are written in place.
+    """
+    if stream is not None and (Xq is None or X_scale is None) and _elsewhere(stream):
+        return _on_stream(stream, quantize_rows_e4m3, X, gated, rows, num_rows, out_rows, Xq, X_scale)
+    torch = _torch()
+    code = _dtype_codes.get(X.dtype)
+    if code != 0 and code != 1:
+        raise TypeError("X must be bfloat16 or float16")
+    M, K, ld = _rows(X, "X")
+    if gated:
+        if K % 2:
+            raise ValueError("gated: X must have an even number of columns")
+        K //= 2
+    dev = X.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
+    top_k, at, n = 0, None, None
+    if rows is not None:
+        if rows.dim() != 2 or rows.shape[0] != M:
+            raise ValueError("rows must be [M, top_k]")
+        top_k = rows.shape[1]
+        at = _vector(rows, torch.int32, M * top_k, dev, "rows")
+    if num_rows is not None:
+        n = _vector(num_rows, torch.int32, 1, dev, "num_rows")
+    if out_rows is None:
+        out_rows = Xq.shape[0] if Xq is not None else M if rows is None else M * top_k
+    if (M | K | out_rows) >> 31:
+        raise ValueError(_SIZE)
+    KB = -(-K // 128)
+    if Xq is None:
+        Xq = torch.empty((out_rows, K), dtype=torch.uint8, device=dev)
+        ldq = K
+    else:
+        if Xq.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError("Xq must be uint8 or float8_e4m3fn")
+        r, c, ldq = _rows(Xq, "Xq")
+        if r != out_rows or c != K or Xq.device != dev:
+            raise ValueError("Xq must be [out_rows, K] on X's device")
+    if X_scale is None:
+        X_scale = torch.empty((KB, max(32, -(-out_rows // 32) * 32)), dtype=torch.float32, device=dev)
+        lds = X_scale.shape[1]
+    else:
+        if X_scale.dtype != torch.float32:
+            raise TypeError("X_scale must be float32")
+        r, c, lds = _rows(X_scale, "X_scale")
+        if r != KB or c < out_rows or X_scale.device != dev:
+            raise ValueError("X_scale must be [ceil(K/128), out_rows or more] on X's device")
+    if rows is not None and top_k == 0:   # rows that go nowhere
+        return Xq, X_scale
+    st = _raw_stream(index) if stream is None else _stream_ptr(stream)
+    r = lib.qg_quantize_rows_e4m3(X.data_ptr(), code, ld, 1 if gated else 0, at, top_k, n, Xq.data_ptr(), ldq,
+                                  X_scale.data_ptr(), lds, M, out_rows, K, st)
+    if r:
+        raise QgemmError(r, "qg_quantize_rows_e4m3")
+    return Xq, X_scale
+
+
+def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None, workspace=None, stream=None):
+    """:func:`qgemm_w8a8_block` grouped by expert: for the rows r of each expert e,
+    offsets[e] <= r < offsets[e + 1], Y[r] = dequant(Xq[r]) . dequant(W[e])^T with
+    FP32 sums per 128-wide K block.
+
+    Xq: uint8 (E4M3 codes) or float8_e4m3fn CUDA [R, K] (row stride a multiple of
+    16) and X_scale: float32 [ceil(K/128), R or more] as :func:`quantize_rows_e4m3`
+    returns them; W: uint8 or float8_e4m3fn [E, N, K] contiguous; W_scale: float32
+    [E, ceil(N/128), ceil(K/128)] contiguous; offsets: int32 [E + 1] on the device.
+    Y (optional): [R, N] with unit column stride, in bfloat16 (the default), float16
+    or float32 (out_dtype).  Rows of no expert are left as they were.
+    """
+    if stream is not None and Y is None and _elsewhere(stream):
+        return _on_stream(stream, qgemm_w8a8_grouped, Xq, X_scale, W, W_scale, offsets, out_dtype, Y, workspace)
+    torch = _torch()
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    if Xq.dtype not in codes or W.dtype not in codes:
+        raise TypeError("Xq and W must hold E4M3 codes (uint8 or float8_e4m3fn)")
+    f32 = torch.float32
+    if X_scale.dtype != f32 or W_scale.dtype != f32:
+        raise TypeError("X_scale and W_scale must be float32")
+    if not (W.is_contiguous() and W_scale.is_contiguous()):
+        raise TypeError("W and W_scale must be contiguous")
+    R, K, ldq = _rows(Xq, "Xq")
+    sr, sc, lds = _rows(X_scale, "X_scale")
+    if sr == 1:
+        lds = sc
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K]")
+    E, N, WK = W.shape
+    if (R | E | N | K) >> 31:
+        raise ValueError(_SIZE)
+    KB = -(-K // 128)
+    if WK != K or sr != KB or sc < R or W_scale.shape != (E, -(-N // 128), KB):
+        raise ValueError("shape mismatch between Xq, X_scale, W and W_scale")
+    dev = Xq.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
+    if W.device != dev or X_scale.device != dev or W_scale.device != dev:
+        raise ValueError("all tensors must be on one CUDA device")
+    off = _vector(offsets, torch.int32, E + 1, dev, "offsets")
+    if Y is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
+        code = _dtype_codes.get(out_dtype)
+        if code is None:
+            raise TypeError("the output must be bfloat16, float16 or float32")
+        Y = torch.empty((R, N), dtype=out_dtype, device=dev)
+        ldy = N
+    else:
+        code = _dtype_codes.get(Y.dtype)
+        if code is None or (out_dtype is not None and Y.dtype != out_dtype):
+            raise TypeError("Y must be bfloat16, float16 or float32, as out_dtype says")
+        r, c, ldy = _rows(Y, "Y")
+        if r != R or c != N or Y.device != dev:
+            raise ValueError("Y must be [R, N] on the same device")
+    st = _raw_stream(index) if stream is None else _stream_ptr(stream)
+    ws, wsb = _workspace_of(KIND_GROUPED, (KIND_GROUPED, R, E, dev), lambda: lib.qg_workspace_bytes_grouped(R, E), workspace,
+                            dev, st)
+    r = lib.qgemm_w8a8_grouped(Xq.data_ptr(), ldq, X_scale.data_ptr(), lds, W.data_ptr(), W_scale.data_ptr(), off,
+                               Y.data_ptr(), code, ldy, R, E, N, K, ws, wsb, st)
+    if r:
+        raise QgemmError(r, "qgemm_w8a8_grouped")
+    return Y
+
+
+def moe_combine(Y, rows, weights, residual=None, out=None, stream=None):
+    """out[m] = sum over j of weights[m, j] * Y[rows[m, j]] (+ residual[m]) in FP32,
+    rounded once: the experts' results back to the tokens.
+
+    Y: bf16, fp16 or fp32 CUDA [R, K]; rows: int32 and weights: float32 [M, top_k] as
+    :func:`moe_route` returns them (a row of -1 counts as zeros); residual (optional)
+    and out (optional): [M, K] of Y's type, which may be the same tensor.
+    """
+    if stream is not None and out is None and _elsewhere(stream):
+        return _on_stream(stream, moe_combine, Y, rows, weights, residual, out)
+    torch = _torch()
+    code = _dtype_codes.get(Y.dtype)
+    if code is None:
+        raise TypeError("Y must be bfloat16, float16 or float32")
+    R, K, ldy = _rows(Y, "Y")
+    if rows.dim() != 2:
+        raise ValueError("rows must be [M, top_k]")
+    M, top_k = rows.shape
+    if (M | K | R) >> 31:
+        raise ValueError(_SIZE)
+    dev = Y.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
+    at = _vector(rows, torch.int32, M * top_k, dev, "rows")
+    w = _vector(weights, torch.float32, M * top_k, dev, "weights")
+    res, ldr = None, K
+    if residual is not None:
+        if residual.dtype != Y.dtype:
+            raise TypeError("residual must have Y's type")
+        r, c, ldr = _rows(residual, "residual")
+        if r != M or c != K or residual.device != dev:
+            raise ValueError("residual must be [M, K] on the same device")
+        res = residual.data_ptr()
+    if out is None:
+        out = torch.empty((M, K), dtype=Y.dtype, device=dev)
+        ldo = K
+    else:
+        if out.dtype != Y.dtype:
+            raise TypeError("out must have Y's type")
+        r, c, ldo = _rows(out, "out")
+        if r != M or c != K or out.device != dev:
+            raise ValueError("out must be [M, K] on the same device")
+    st = _raw_stream(index) if stream is None else _stream_ptr(stream)
+    r = lib.qg_moe_combine(Y.data_ptr(), code, ldy, at, w, top_k, res, ldr, out.data_ptr(), ldo, M, R, K, st)
+    if r:
+        raise QgemmError(r, "qg_moe_combine")
+    return out
+
+
+MAX_DRAFTS = 31
+
+
+class DraftCheck(NamedTuple):
+    """What :func:`verify_drafts` returns."""
+    accepted: Any   # int32 [B]: drafts that are kept
+    tokens: Any     # int64 [B, G + 1]: those, the token that follows, then -1
+
+
+def _batch_rows(t, what: str):
+    """(sequences, rows, columns, sequence stride, row stride) of a 3-D CUDA tensor
+    with unit column stride; strides of lone sequences and rows do not count."""
+    if t.dim() != 3:
+        raise ValueError(what + " must be a 3-D tensor")
+    b, r, c = t.shape
+    sb, sr, step = t.stride()
+    if step != 1 and c > 1:
+        raise ValueError(what + " must have unit stride in its last dimension")
+    if not t.is_cuda:
+        raise ValueError(what + " must be on a CUDA device")
+    return b, r, c, (sb if b > 1 else 0), (sr if r > 1 else c)
+
+
+def verify_drafts(target_logits, draft_tokens, draft_logits=None, uniform=None, noise=None, lengths=None,
+                  stream=None) -> DraftCheck:
+    """Drafted tokens against the target's probabilities, from given random numbers.
+
+    target_logits: bf16, fp16 or fp32 CUDA [B, G + 1, V] (unit column stride), as
+    tokens are drawn from them (divided by the temperature, -inf where a filter
+    leaves a token out); draft_tokens: int64 [B, G], G <= MAX_DRAFTS; draft_logits
+    (optional): [B, G, V] of the same type that the drafts were drawn from; without
+    it they count as certain.  uniform: float32 [B, G] in [0, 1), noise: float32 [B, V]
+    exponential.  lengths (optional): int32 [B], how many drafts a sequence has.
+
+    Drafts are kept while uniform * q(d) < p(d); the next token is drawn from
+    max(p - q, 0) at the first that is not kept, from p behind the last one, as the
+    largest ratio of probability to noise.  Without uniform and noise: greedy, drafts
+    are kept while they are the largest logit, and the largest follows.  (A row with
+    a NaN, +inf or nothing left keeps no draft and yields -1; see include/qgemm.h.)
+    """
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(stream, verify_drafts, target_logits, draft_tokens, draft_logits, uniform, noise, lengths)
+    torch = _torch()
+    code = _dtype_codes.get(target_logits.dtype)
+    if code is None:
+        raise TypeError("target_logits must be bfloat16, float16 or float32")
+    B, rows, V, t_seq, t_row = _batch_rows(target_logits, "target_logits")
+    G = rows - 1
+    if G < 0:
+        raise ValueError("target_logits must have a row for each draft and one more")
+    if (B | V) >> 31 or G >> 31:
+        raise ValueError(_SIZE)
+    dev = target_logits.device
+    index = dev.index
+    if index != _current_device():   # where the library launches
+        raise ValueError("the tensors must be on the current CUDA device")
+    if draft_tokens.dtype != torch.int64:
+        raise TypeError("draft_tokens must be int64")
+    if draft_tokens.shape != (B, G):
+        raise ValueError("draft_tokens must be [B, G], target_logits [B, G + 1, V]")
+    if draft_tokens.device != dev:
+        raise ValueError("all tensors must be on one CUDA device")
+    if not draft_tokens.is_contiguous():
+        draft_tokens = draft_tokens.contiguous()
+    if (uniform is None) != (noise is None):
+        raise ValueError("uniform and noise belong together")
+    d, d_seq, d_row = None, 0, V
+    if draft_logits is not None:
+        if noise is None:
+            raise ValueError("draft_logits need uniform and noise")
+        if draft_logits.dtype != target_logits.dtype:
+            raise TypeError("draft_logits must have target_logits' type")
+        b, r, c, d_seq, d_row = _batch_rows(draft_logits, "draft_logits")
+        if (b, r, c) != (B, G, V) or draft_logits.device != dev:
+            raise ValueError("draft_logits must be [B, G, V] on the same device")
+        d = draft_logits.data_ptr() if G > 0 else None
+    u = z = n = None
+    ldu, ldn = G, V
+    if noise is not None:
+        f32 = torch.float32
+        if uniform.dtype != f32 or noise.dtype != f32:
+            raise TypeError("uniform and noise must be float32")
+        r, c, ldu = _rows(uniform, "uniform")
+        r2, c2, ldn = _rows(noise, "noise")
+        if (r, c) != (B, G) or (r2, c2) != (B, V) or uniform.device != dev or noise.device != dev:
+            raise ValueError("uniform must be [B, G] and noise [B, V] on the same device")
+        z = noise.data_ptr()
+        u = uniform.data_ptr() if G > 0 else z   # not read without drafts
+    if lengths is not None:
+        n = _vector(lengths, torch.int32, B, dev, "lengths")
+    accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    tokens = torch.empty((B, G + 1), dtype=torch.int64, device=dev)
+    st = _raw_stream(index)
+    r = lib.qg_verify_drafts(target_logits.data_ptr(), code, t_seq, t_row, d, d_seq, d_row, draft_tokens.data_ptr(), G,
+                             u, ldu, z, ldn, n, accepted.data_ptr(), tokens.data_ptr(), B, G, V, st)
+    if r:
+        raise QgemmError(r, "qg_verify_drafts")
+    return DraftCheck(accepted, tokens)
 
 
 def qgemm_bf16(X, W, Y=None, workspace=None, stream=None):

@@ -10,10 +10,13 @@
 #include <cuda_fp16.h>
 
 #include "../../include/qgemm.h"
+#include "qg_experts.h"
 #include "qg_gemm.cuh"
+#include "qg_grouped.h"
 #include "qg_int8.h"
 #include "qg_internal.h"
 #include "qg_logprobs.h"
+#include "qg_verify.h"
 #include "qg_w8a8.h"
 
 namespace qg {
@@ -798,6 +801,155 @@ qg_status qg_logprobs(const void* logits, int type, int64_t ld, const int64_t* t
     if (!d) return QG_ERR_CUDA;
     const LogprobArgs a{logits, type, ld, tokens, ldt, T, token_logprobs, entropy, top_k, top_ids, top_logprobs, M, V};
     return launch_logprobs(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+size_t qg_moe_route_workspace_bytes(int M, int E) {
+    if (M < 0 || M > (1 << 20) || E < 1 || E > QG_MAX_EXPERTS) return 0;
+    DeviceInfo* d = device_info();
+    return d ? route_workspace_bytes(M, E, d->sms) : 0;
+}
+
+qg_status qg_moe_route(const void* logits, int type, int64_t ld, const float* bias, int score, int renormalize,
+                       float scale, int top_k, int32_t* experts, float* weights, int32_t* offsets, int32_t* rows,
+                       int M, int E, void* workspace, size_t workspace_bytes_, cudaStream_t stream) {
+    if (M < 0 || E < 0 || top_k < 1 || (type != QG_BF16 && type != QG_FP16 && type != QG_FP32) ||
+        (score != QG_SCORE_SOFTMAX && score != QG_SCORE_SIGMOID))
+        return QG_ERR_INVALID_ARG;
+    if (!offsets || (M > 0 && (!logits || !experts || !weights || !rows))) return QG_ERR_INVALID_ARG;
+    if (M > (1 << 20) || E < 1 || E > QG_MAX_EXPERTS || top_k > E || top_k > 32) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (ld < E) return QG_ERR_INVALID_ARG;
+    const uintptr_t mask = type == QG_FP32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(logits) & mask) || (reinterpret_cast<uintptr_t>(bias) & 3u) ||
+        (reinterpret_cast<uintptr_t>(experts) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u) || (reinterpret_cast<uintptr_t>(rows) & 3u))
+        return QG_ERR_MISALIGNED;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    const size_t need = route_workspace_bytes(M, E, d->sms);
+    if (need > 0 && (!workspace || workspace_bytes_ < need || !aligned16(workspace))) return QG_ERR_WORKSPACE;
+    const RouteArgs a{logits,  type,    ld,   bias, score, renormalize, scale, top_k,
+                      experts, weights, offsets, rows, M,     E,           workspace};
+    return launch_route(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+qg_status qg_quantize_rows_e4m3(const void* X, int x_type, int64_t ldx, int gated, const int32_t* rows, int top_k,
+                                const int32_t* num_rows, uint8_t* Xq, int64_t ldxq, float* X_scale, int64_t ldsx,
+                                int M, int out_rows, int K, cudaStream_t stream) {
+    if (M < 0 || K < 0 || out_rows < 0 || (x_type != QG_BF16 && x_type != QG_FP16) || (rows && top_k < 1))
+        return QG_ERR_INVALID_ARG;
+    if (M == 0 || K == 0 || out_rows == 0) return QG_OK;
+    if (!X || !Xq || !X_scale) return QG_ERR_INVALID_ARG;
+    if (M > (1 << 22) || K % 16 != 0 || (rows && top_k > 32)) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (ldx < (gated ? 2 * static_cast<int64_t>(K) : K) || ldxq < K || ldsx < out_rows) return QG_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(Xq) || !aligned16(X_scale) || ldx % 8 != 0 || ldxq % 16 != 0 || ldsx % 4 != 0 ||
+        (reinterpret_cast<uintptr_t>(rows) & 3u) || (reinterpret_cast<uintptr_t>(num_rows) & 3u))
+        return QG_ERR_MISALIGNED;
+    // a warp's jobs (M spans of 256 columns, eight to a CTA) are the grid
+    if (static_cast<int64_t>(M) * ((K + 255) / 256) > (int64_t(1) << 33)) return QG_ERR_UNSUPPORTED_SHAPE;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    const QuantizeRowsArgs a{X,  x_type, ldx, gated != 0, rows, top_k, num_rows, Xq, ldxq, X_scale, ldsx,
+                             M, out_rows, K};
+    return launch_quantize_rows(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+size_t qg_workspace_bytes_grouped(int R, int E) {
+    if (R < 1 || R > (1 << 24) || E < 1 || E > QG_MAX_EXPERTS) return 0;
+    DeviceInfo* d = device_info();
+    return d ? grouped_workspace_bytes(R, E, d->sms) : 0;
+}
+
+qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_scale, int64_t ldsx, const uint8_t* W,
+                             const float* W_scale, const int32_t* offsets, void* Y, int y_type, int64_t ldy, int R,
+                             int E, int N, int K, void* workspace, size_t workspace_bytes_, cudaStream_t stream) {
+    if (R < 0 || E < 0 || N < 0 || K < 0 || (y_type != QG_BF16 && y_type != QG_FP16 && y_type != QG_FP32))
+        return QG_ERR_INVALID_ARG;
+    if (R == 0 || E == 0 || N == 0) return QG_OK;
+    if (!Y || !offsets || (K > 0 && (!Xq || !X_scale || !W || !W_scale))) return QG_ERR_INVALID_ARG;
+    if (R > (1 << 24) || E > QG_MAX_EXPERTS || K % 16 != 0 || static_cast<int64_t>(E) * N >= (int64_t(1) << 31) - 256)
+        return QG_ERR_UNSUPPORTED_SHAPE;
+    if (ldxq < K || ldy < N || ldsx < R) return QG_ERR_INVALID_ARG;
+    const uintptr_t y_mask = y_type == QG_FP32 ? 3u : 1u;
+    // without a K there is nothing of Xq and W to be aligned
+    if ((K > 0 && (!aligned16(Xq) || !aligned16(W) || ldxq % 16 != 0)) ||
+        (reinterpret_cast<uintptr_t>(X_scale) & 3u) || (reinterpret_cast<uintptr_t>(W_scale) & 3u) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u) || (reinterpret_cast<uintptr_t>(Y) & y_mask))
+        return QG_ERR_MISALIGNED;
+    const int nt = grouped_tile_rows(R, E);
+    // tiles are counted in 32 bits
+    if ((static_cast<int64_t>(R) / nt + E) * ((N + 127) / 128) > (int64_t(1) << 30)) return QG_ERR_UNSUPPORTED_SHAPE;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    GroupedArgs a{};
+    a.Sx = X_scale;
+    a.ldsx = ldsx;
+    a.S = W_scale;
+    a.offsets = offsets;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.y_type = y_type;
+    a.R = R;
+    a.E = E;
+    a.N = N;
+    a.K = K;
+    if (K == 0) return launch_grouped_zero(a, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+    const size_t need = grouped_workspace_bytes(R, E, d->sms);
+    if (need > 0 && (!workspace || workspace_bytes_ < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return QG_ERR_WORKSPACE;
+    a.ws = need > 0 ? workspace : nullptr;
+    const CUtensorMap* tmW =
+        cached_tmap(W, static_cast<uint64_t>(K), static_cast<uint64_t>(E) * static_cast<uint64_t>(N), kMapFp8Weights);
+    if (!tmW) return QG_ERR_CUDA;
+    CUtensorMap tmX;
+    if (!make_tmap(&tmX, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<uint64_t>(K), static_cast<uint64_t>(R),
+                   static_cast<uint64_t>(ldxq), 128, static_cast<uint32_t>(nt / grouped_ctas(nt))))
+        return QG_ERR_CUDA;
+    return launch_grouped(a, *tmW, tmX, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+qg_status qg_moe_combine(const void* Y, int type, int64_t ldy, const int32_t* rows, const float* weights, int top_k,
+                         const void* residual, int64_t ldr, void* out, int64_t ldo, int M, int R, int K,
+                         cudaStream_t stream) {
+    if (M < 0 || R < 0 || K < 0 || top_k < 1 || (type != QG_BF16 && type != QG_FP16 && type != QG_FP32))
+        return QG_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) return QG_OK;
+    if ((R > 0 && !Y) || !rows || !weights || !out) return QG_ERR_INVALID_ARG;
+    if (M > (1 << 22) || top_k > 32 || static_cast<int64_t>(M) * K > (int64_t(1) << 38)) return QG_ERR_UNSUPPORTED_SHAPE;
+    if ((R > 0 && ldy < K) || (residual && ldr < K) || ldo < K) return QG_ERR_INVALID_ARG;
+    const uintptr_t mask = type == QG_FP32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(Y) & mask) || (reinterpret_cast<uintptr_t>(residual) & mask) ||
+        (reinterpret_cast<uintptr_t>(out) & mask) || (reinterpret_cast<uintptr_t>(rows) & 3u) ||
+        (reinterpret_cast<uintptr_t>(weights) & 3u))
+        return QG_ERR_MISALIGNED;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    const CombineArgs a{Y, type, ldy, rows, weights, top_k, residual, ldr, out, ldo, M, R, K};
+    return launch_combine(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+qg_status qg_verify_drafts(const void* target, int type, int64_t t_seq, int64_t t_row, const void* draft,
+                           int64_t d_seq, int64_t d_row, const int64_t* tokens, int64_t ldt, const float* uniform,
+                           int64_t ldu, const float* noise, int64_t ldn, const int32_t* lengths, int32_t* accepted,
+                           int64_t* tokens_out, int B, int G, int V, cudaStream_t stream) {
+    if (B < 0 || G < 0 || V < 0 || (type != QG_BF16 && type != QG_FP16 && type != QG_FP32)) return QG_ERR_INVALID_ARG;
+    if (B == 0) return QG_OK;
+    if (!target || !accepted || !tokens_out || (G > 0 && !tokens)) return QG_ERR_INVALID_ARG;
+    // greedy, or both kinds of random numbers (without drafts no uniform is read)
+    if ((noise == nullptr) != (uniform == nullptr) || (draft && !noise)) return QG_ERR_INVALID_ARG;
+    if (B > 65536 || G > QG_MAX_DRAFTS || V < 1 || V > (1 << 30)) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (t_row < V || t_seq < 0 || ldt < G || (draft && (d_row < V || d_seq < 0)) || (uniform && (ldu < G || ldn < V)))
+        return QG_ERR_INVALID_ARG;
+    const uintptr_t mask = type == QG_FP32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(target) & mask) || (reinterpret_cast<uintptr_t>(draft) & mask) ||
+        (reinterpret_cast<uintptr_t>(tokens) & 7u) || (reinterpret_cast<uintptr_t>(uniform) & 3u) ||
+        (reinterpret_cast<uintptr_t>(noise) & 3u) || (reinterpret_cast<uintptr_t>(lengths) & 3u) ||
+        (reinterpret_cast<uintptr_t>(accepted) & 3u) || (reinterpret_cast<uintptr_t>(tokens_out) & 7u))
+        return QG_ERR_MISALIGNED;
+    DeviceInfo* d = device_info();
+    if (!d) return QG_ERR_CUDA;
+    const VerifyArgs a{target, t_seq, t_row, draft,   d_seq,    d_row,      type, tokens, ldt, uniform,
+                       ldu,    noise, ldn,   lengths, accepted, tokens_out, B,    G,      V};
+    return launch_verify(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
 qg_status qgemm_lut3(const void* X, int64_t ldx, const void* Wq, const void* qmap, const void* scales, void* Y,

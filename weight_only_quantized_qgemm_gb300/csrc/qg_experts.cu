@@ -1,0 +1,589 @@
+// What a layer of experts needs around its grouped products, for sm_103a: the
+// router, the quantiser that copies a token's activations to its experts' rows
+// (or applies the gate between an expert's two products), and the weighted sum
+// of the experts' results.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qg_device.cuh"
+#include "qg_experts.h"
+#include "qg_launch.h"
+
+namespace qg {
+namespace {
+
+template <int kType>
+__device__ __forceinline__ float to_f32(const void* p, int64_t i) {
+    if (kType == QG_FP32) return static_cast<const float*>(p)[i];
+    if (kType == QG_BF16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+    return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+// Launched ahead of the preceding grid's end: every kernel here waits for it
+// before it touches memory.
+cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream_t st, cudaLaunchAttribute* attr) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// ----------------------------------------------------------------- router
+// A warp takes a token: lane l holds experts l, l + 32, ...  Of the choices'
+// order by expert, then by token, each CTA knows its own part: a warp counts its
+// tokens' choices by expert, the counts of a CTA's warps add up in order, and
+// with more than one CTA a second kernel adds the counts of the CTAs in front.
+// (Counting, not atomics, so that the order is that of the tokens on every call.)
+//
+// Without a bias the order of the scores is that of the logits, which are
+// compared as they are.  With one the scores decide that are next to another,
+// and 32 bits are not enough for those: where the chosen ones, or the last one
+// and the next, lie closer than the scores' error, the token is done again in 64.
+constexpr int kRouteWarps = 16;
+constexpr float kNear = 4e-6f;   // relative to max(1, |score|); the scores are good to 1e-6 of it
+
+// A value's bits as a whole number that orders like it (never 0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);   // -0 as 0
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+    const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return b ^ (static_cast<uint64_t>(static_cast<int64_t>(b) >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = w > v ? w : v;
+    }
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The k + more largest keys above 0, in order (ties to the lower expert): lane j
+// receives the j-th one's expert (-1: none left) and its key.
+template <class Key, int PL>
+__device__ __forceinline__ void choose(Key (&key)[PL], int n, int lane, int& expert, Key& at) {
+    expert = -1;
+    at = 0;
+    for (int j = 0; j < n; ++j) {
+        Key best = 0;
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                bi = i;
+            }
+        const Key top = warp_max(best);
+        if (top == 0) return;
+        const int e = static_cast<int>(
+            __reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(bi * 32 + lane) : 0xffffffffu));
+        if (lane == (e & 31)) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                if (i == e >> 5) key[i] = 0;
+        }
+        if (lane == j) {
+            expert = e;
+            at = top;
+        }
+    }
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// One token: lane j < k receives its j-th expert (-1: none) and the weight.
+template <int kType, int PL>
+__device__ __forceinline__ void route_token(const RouteArgs& a, const void* row, int lane, int& expert, float& weight) {
+    float v[PL];
+    float top = -INFINITY;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        const int e = i * 32 + lane;
+        v[i] = e < a.E ? to_f32<kType>(row, e) : -INFINITY;
+        top = fmaxf(top, v[i]);
+        bad |= !(v[i] < INFINITY);   // NaN or +inf
+    }
+    if (__any_sync(0xffffffffu, bad)) {   // routed nowhere, and the weights say so
+        expert = -1;
+        weight = __uint_as_float(0x7FC00000u);
+        return;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int k = a.top_k;
+    const bool soft = a.score == QG_SCORE_SOFTMAX;
+    uint32_t key[PL], at;
+    float total = 0.0f;   // of the softmax, where it is needed
+    if (soft && (a.bias != nullptr || !a.renormalize)) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) total += expf(v[i] - top);
+        total = warp_sum(total);
+    }
+    if (a.bias == nullptr) {
+#pragma unroll
+        for (int i = 0; i < PL; ++i) key[i] = v[i] > -INFINITY ? order_key(v[i]) : 0u;
+        choose(key, k, lane, expert, at);
+    } else {
+        bool near = false;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            const int e = i * 32 + lane;
+            const float s = soft ? expf(v[i] - top) / total : 1.0f / (1.0f + expf(-v[i]));
+            const float by = s + (e < a.E ? a.bias[e] : 0.0f);
+            key[i] = v[i] > -INFINITY && by > -INFINITY ? order_key(by) : 0u;   // a NaN is above nothing
+        }
+        // k < 32: the next one too; k = 32 is done again whenever one is left
+        choose(key, k < 32 ? k + 1 : 32, lane, expert, at);
+        const uint32_t next = __shfl_down_sync(0xffffffffu, at, 1);
+        if (lane < (k < 32 ? k : 31) && next != 0u) {
+            const float x = key_value(at);
+            near = !(x - key_value(next) > kNear * fmaxf(1.0f, fabsf(x)));
+        }
+        if (k == 32) {
+            bool left = false;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) left |= key[i] != 0u;
+            near |= left;
+        }
+        if (__any_sync(0xffffffffu, near)) {
+            uint64_t wide[PL], wat;
+            double sum = 1.0;
+            if (soft) {
+                sum = 0.0;
+#pragma unroll 1
+                for (int i = 0; i < PL; ++i) {
+                    const int e = i * 32 + lane;
+                    if (e < a.E) sum += exp(static_cast<double>(to_f32<kType>(row, e)) - static_cast<double>(top));
+                }
+                sum = warp_sum(sum);
+            }
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const int e = i * 32 + lane;
+                wide[i] = 0;
+                if (e < a.E && v[i] > -INFINITY) {
+                    const double x = v[i];
+                    const double s = soft ? exp(x - static_cast<double>(top)) / sum : 1.0 / (1.0 + exp(-x));
+                    const double by = s + static_cast<double>(a.bias[e]);
+                    if (by > -INFINITY) wide[i] = order_key(by);
+                }
+            }
+            choose(wide, k, lane, expert, wat);
+        }
+        if (lane >= k) expert = -1;
+    }
+    // the weights, from the chosen logits
+    float w = 0.0f;
+    if (expert >= 0) {
+        const float x = to_f32<kType>(row, expert);
+        w = soft ? expf(x - top) : 1.0f / (1.0f + expf(-x));
+    }
+    const float sum = a.renormalize ? warp_sum(w) : soft ? total : 1.0f;
+    weight = sum > 0.0f ? w * (a.scale / sum) : 0.0f;
+}
+
+// Tokens of a CTA and of a warp.
+__host__ __device__ inline int route_ctas(int M, int sms) {
+    // up to four tokens a warp one CTA does it all: the second launch costs more
+    return M <= 4 * kRouteWarps ? 1 : (M + kRouteWarps - 1) / kRouteWarps < sms ? (M + kRouteWarps - 1) / kRouteWarps : sms;
+}
+
+// where[e] = the exclusive prefix over the experts of total[e] (each a CTA's or
+// the whole call's), total in shared memory; all threads of the CTA.
+__device__ __forceinline__ void prefix_experts(const int* total, int* where, int E) {
+    if (threadIdx.x < 32) {
+        int before = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + static_cast<int>(threadIdx.x);
+            const int mine = e < E ? total[e] : 0;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int other = __shfl_up_sync(0xffffffffu, upto, o);
+                if (static_cast<int>(threadIdx.x) >= o) upto += other;
+            }
+            if (e < E) where[e] = before + upto - mine;
+            before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        if (threadIdx.x == 0) where[E] = before;
+    }
+    __syncthreads();
+}
+
+template <int kType, int PL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a, int chunk) {
+    extern __shared__ int route_smem[];
+    int* count = route_smem;                        // [warps][E]
+    int* total = route_smem + kRouteWarps * a.E;    // [E]
+    int* where = total + a.E;                       // [E + 1]
+    grid_dependents_launch();
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < kRouteWarps * a.E; i += kRouteWarps * 32) count[i] = 0;
+    grid_dependency_wait();
+    __syncthreads();
+    // contiguous tokens to a CTA, and of those to a warp
+    const int c0 = blockIdx.x * chunk;
+    const int c1 = c0 + chunk < a.M ? c0 + chunk : a.M;
+    const int each = (chunk + kRouteWarps - 1) / kRouteWarps;
+    const int t0 = c0 + warp * each;
+    const int t1 = t0 + each < c1 ? t0 + each : c1;
+    int* mine = count + warp * a.E;
+    const int64_t size = kType == QG_FP32 ? 4 : 2;
+    for (int m = t0; m < t1; ++m) {
+        int expert;
+        float weight;
+        route_token<kType, PL>(a, static_cast<const uint8_t*>(a.logits) + m * a.ld * size, lane, expert, weight);
+        if (lane < a.top_k) {
+            const int64_t at = static_cast<int64_t>(m) * a.top_k + lane;
+            a.experts[at] = expert;
+            a.weights[at] = weight;
+            a.rows[at] = expert >= 0 ? mine[expert]++ : -1;   // among this warp's; a token's experts differ
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kRouteWarps * 32) {
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kRouteWarps; ++w) {
+            const int n = count[w * a.E + e];
+            count[w * a.E + e] = sum;
+            sum += n;
+        }
+        total[e] = sum;
+        if (gridDim.x > 1) static_cast<int*>(a.ws)[static_cast<int64_t>(blockIdx.x) * a.E + e] = sum;
+    }
+    __syncthreads();
+    if (gridDim.x == 1) {
+        prefix_experts(total, where, a.E);
+        for (int e = threadIdx.x; e <= a.E; e += kRouteWarps * 32) a.offsets[e] = where[e];
+    }
+    for (int64_t i = static_cast<int64_t>(t0) * a.top_k + lane; i < static_cast<int64_t>(t1) * a.top_k; i += 32) {
+        const int e = a.experts[i];
+        if (e >= 0) a.rows[i] += mine[e] + (gridDim.x == 1 ? where[e] : 0);
+    }
+}
+
+// Behind route_kernel on several CTAs: where each expert's rows begin, and the
+// rows of this CTA's choices, from all CTAs' counts.
+constexpr int kPlaceThreads = 512;
+__global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs a, int chunk) {
+    extern __shared__ int route_smem[];
+    int* total = route_smem;            // [E]: of all CTAs
+    int* front = total + a.E;           // [E]: of the CTAs in front
+    int* where = front + a.E;           // [E + 1]
+    grid_dependents_launch();
+    for (int e = threadIdx.x; e < 2 * a.E; e += kPlaceThreads) total[e] = 0;
+    grid_dependency_wait();
+    __syncthreads();
+    const int* table = static_cast<const int*>(a.ws);
+    const int ctas = gridDim.x;
+    // threads in parts of E, each part a share of the CTAs; whole numbers, so that
+    // the order of the additions does not show
+    const int parts = a.E <= kPlaceThreads ? kPlaceThreads / a.E : 1;
+    for (int i = threadIdx.x; i < parts * a.E; i += kPlaceThreads) {
+        const int e = i % a.E, part = i / a.E;
+        const int b0 = part * ctas / parts, b1 = (part + 1) * ctas / parts;
+        int all = 0, before = 0;
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b) {
+            const int n = __ldcg(table + static_cast<int64_t>(b) * a.E + e);
+            all += n;
+            before += b < static_cast<int>(blockIdx.x) ? n : 0;
+        }
+        atomicAdd(total + e, all);
+        atomicAdd(front + e, before);
+    }
+    __syncthreads();
+    prefix_experts(total, where, a.E);
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= a.E; e += kPlaceThreads) a.offsets[e] = where[e];
+    const int c0 = blockIdx.x * chunk;
+    const int c1 = c0 + chunk < a.M ? c0 + chunk : a.M;
+    for (int64_t i = static_cast<int64_t>(c0) * a.top_k + threadIdx.x; i < static_cast<int64_t>(c1) * a.top_k;
+         i += kPlaceThreads) {
+        const int e = __ldcg(a.experts + i);
+        if (e >= 0) a.rows[i] = __ldcg(a.rows + i) + where[e] + front[e];
+    }
+}
+
+template <int kType, int PL>
+cudaError_t launch_route_pl(const RouteArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    const int ctas = route_ctas(a.M, c.num_sms);
+    const int chunk = a.M > 0 ? (a.M + ctas - 1) / ctas : 1;
+    cudaLaunchAttribute attr;
+    const size_t smem = (kRouteWarps + 2) * a.E * sizeof(int) + sizeof(int);
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = set_smem_once(configured, route_kernel<kType, PL>, (kRouteWarps + 2) * 32 * PL * 4 + 4);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = config(static_cast<unsigned>(ctas), kRouteWarps * 32, smem, st, &attr);
+    e = cudaLaunchKernelEx(&cfg, route_kernel<kType, PL>, a, chunk);
+    if (e != cudaSuccess || ctas == 1) return e;
+    cfg = config(static_cast<unsigned>(ctas), kPlaceThreads, (3 * a.E + 1) * sizeof(int), st, &attr);
+    return cudaLaunchKernelEx(&cfg, route_place_kernel, a, chunk);
+}
+
+template <int kType>
+cudaError_t launch_route_type(const RouteArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    if (a.E <= 64) return launch_route_pl<kType, 2>(a, c, st);
+    if (a.E <= 128) return launch_route_pl<kType, 4>(a, c, st);
+    if (a.E <= 256) return launch_route_pl<kType, 8>(a, c, st);
+    if (a.E <= 512) return launch_route_pl<kType, 16>(a, c, st);
+    return launch_route_pl<kType, 32>(a, c, st);
+}
+
+// ----------------------------------------------------------------- row quantiser
+// A half warp takes a block of 128 columns of a row, eight of them a lane: their
+// maximum, the scale, eight codes, which go to every one of the row's places.  A
+// warp walks over its row in steps of 256 columns.
+template <bool kBf16>
+__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (kBf16) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// silu(g) u in 32 bits: g u / (1 + e^-g).  The exponential is good to
+// 2^-22 + |g| 2^-24, the reciprocal to 2^-23: far below an E4M3 step (2^-4).
+__device__ __forceinline__ float gate(float g, float u) {
+    float e, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
+}
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+constexpr int kQuantWarps = 8;
+
+template <bool kBf16, bool kGated>
+__global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const QuantizeRowsArgs a, int steps, int spans) {
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    // a span: `steps` steps of 256 columns of one row
+    const int64_t job = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5);
+    const int64_t m = job / spans;
+    int live = a.M;
+    if (a.num_rows != nullptr) {
+        const int n = __ldcg(a.num_rows);
+        live = n < live ? n : live;
+    }
+    if (m >= live) return;
+    const int span = static_cast<int>(job - m * spans);
+    const uint16_t* x = static_cast<const uint16_t*>(a.X) + m * a.ldx;
+    // the row's places: lane j holds the j-th (out of range: none)
+    int place = lane == 0 ? static_cast<int>(m) : -1;
+    int places = 1;
+    if (a.rows != nullptr) {
+        places = a.top_k;
+        place = lane < places ? __ldcg(a.rows + m * a.top_k + lane) : -1;
+    }
+    if (place >= a.out_rows) place = -1;
+    for (int s = 0; s < steps; ++s) {
+        const int k0 = (span * steps + s) * 256 + lane * 8;
+        if (k0 - lane * 8 >= a.K) break;
+        const bool in = k0 < a.K;   // K is a multiple of 16: all eight or none
+        float v[8];
+        uint4 w = make_uint4(0u, 0u, 0u, 0u), w2 = w;
+        if (in) {
+            w = *reinterpret_cast<const uint4*>(x + k0);
+            if (kGated) w2 = *reinterpret_cast<const uint4*>(x + a.K + k0);
+        }
+        widen8<kBf16>(w, v);
+        if (kGated) {
+            float u[8];
+            widen8<kBf16>(w2, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = gate(v[i], u[i]);
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], sc);
+        const uint2 codes = make_uint2(codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7]));
+        for (int j = 0; j < places; ++j) {
+            const int r = __shfl_sync(0xffffffffu, place, j);
+            if (r < 0 || !in) continue;
+            *reinterpret_cast<uint2*>(a.Xq + r * a.ldxq + k0) = codes;
+            if ((lane & 15) == 0) a.Sx[(k0 >> 7) * a.ldsx + r] = sc;
+        }
+    }
+}
+
+// ----------------------------------------------------------------- combination
+// A thread takes eight neighbouring columns of a token (one where the tensors
+// do not allow vectors) and sums them over the token's experts in their order.
+template <int kType>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
+    if (kType == QG_FP32) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+        widen8<kType == QG_BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i), x);
+    }
+}
+template <int kType>
+__device__ __forceinline__ uint32_t narrow2(float a, float b) {
+    if (kType == QG_BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+constexpr int kCombineThreads = 256;
+
+template <int kType, bool kVec>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a, int pieces) {
+    constexpr int kW = kVec ? 8 : 1;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int64_t job = static_cast<int64_t>(blockIdx.x) * kCombineThreads + threadIdx.x;
+    const int64_t m = job / pieces;
+    if (m >= a.M) return;
+    const int64_t k0 = (job - m * pieces) * kW;
+    float acc[kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+        float w[8];
+        float x[8][kW];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kW; ++i) x[j][i] = 0.0f;
+            if (j0 + j >= a.top_k) continue;
+            const int r = a.rows[m * a.top_k + j0 + j];
+            w[j] = a.weights[m * a.top_k + j0 + j];
+            if (r < 0 || r >= a.R) continue;   // no expert: zeros (a weight of NaN shows all the same)
+            if constexpr (kVec) load8<kType>(a.Y, r * a.ldy + k0, x[j]);
+            else x[j][0] = to_f32<kType>(a.Y, r * a.ldy + k0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < kW; ++i) acc[i] = __fmaf_rn(w[j], x[j][i], acc[i]);
+    }
+    if (a.residual != nullptr) {
+        float x[8];
+        if constexpr (kVec) load8<kType>(a.residual, m * a.ldr + k0, x);
+        else x[0] = to_f32<kType>(a.residual, m * a.ldr + k0);
+#pragma unroll
+        for (int i = 0; i < kW; ++i) acc[i] += x[i];
+    }
+    const int64_t at = m * a.ldo + k0;
+    if constexpr (kVec) {
+        if (kType == QG_FP32) {
+            float* o = static_cast<float*>(a.out) + at;
+            *reinterpret_cast<float4*>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            *reinterpret_cast<float4*>(o + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) =
+                make_uint4(narrow2<kType>(acc[0], acc[1]), narrow2<kType>(acc[2], acc[3]),
+                           narrow2<kType>(acc[4], acc[5]), narrow2<kType>(acc[6], acc[7]));
+        }
+    } else if (kType == QG_FP32) {
+        static_cast<float*>(a.out)[at] = acc[0];
+    } else {
+        static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(narrow2<kType>(acc[0], 0.0f));
+    }
+}
+
+template <int kType>
+cudaError_t launch_combine_type(const CombineArgs& a, cudaStream_t st) {
+    const int size = kType == QG_FP32 ? 4 : 2;
+    auto fits = [&](const void* p, int64_t ld) { return p == nullptr || (aligned_16(p) && ld * size % 16 == 0); };
+    const bool vec = a.K % 8 == 0 && fits(a.Y, a.ldy) && fits(a.out, a.ldo) && fits(a.residual, a.ldr);
+    const int pieces = vec ? a.K / 8 : a.K;
+    const int64_t blocks = (static_cast<int64_t>(a.M) * pieces + kCombineThreads - 1) / kCombineThreads;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kCombineThreads, 0, st, &attr);
+    if (vec) return cudaLaunchKernelEx(&cfg, combine_kernel<kType, true>, a, pieces);
+    return cudaLaunchKernelEx(&cfg, combine_kernel<kType, false>, a, pieces);
+}
+
+}  // namespace
+
+size_t route_workspace_bytes(int M, int E, int sms) {
+    const int ctas = route_ctas(M, sms);
+    return ctas > 1 ? static_cast<size_t>(ctas) * E * sizeof(int) : 0;
+}
+
+cudaError_t launch_route(const RouteArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    switch (a.type) {
+        case QG_BF16: return launch_route_type<QG_BF16>(a, c, st);
+        case QG_FP16: return launch_route_type<QG_FP16>(a, c, st);
+        case QG_FP32: return launch_route_type<QG_FP32>(a, c, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_quantize_rows(const QuantizeRowsArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    const int all = (a.K + 255) / 256;   // steps of a row
+    const int steps = 2;
+    const int spans = (all + steps - 1) / steps;
+    const int64_t blocks = (static_cast<int64_t>(a.M) * spans + kQuantWarps - 1) / kQuantWarps;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kQuantWarps * 32, 0, st, &attr);
+    if (a.x_type == QG_BF16)
+        return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, true>, a, steps, spans)
+                       : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, false>, a, steps, spans);
+    return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, true>, a, steps, spans)
+                   : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, false>, a, steps, spans);
+}
+
+cudaError_t launch_combine(const CombineArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    switch (a.type) {
+        case QG_BF16: return launch_combine_type<QG_BF16>(a, st);
+        case QG_FP16: return launch_combine_type<QG_FP16>(a, st);
+        case QG_FP32: return launch_combine_type<QG_FP32>(a, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace qg

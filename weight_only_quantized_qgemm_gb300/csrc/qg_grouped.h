@@ -1,0 +1,35 @@
+// Internal interface of the grouped W8A8 GEMM (qg_grouped.cu) for the C ABI.
+#pragma once
+
+#include "qg_internal.h"
+
+namespace qg {
+
+struct GroupedArgs {
+    const float* Sx;          // [ceil(K/128), ldsx]
+    int64_t ldsx;
+    const float* S;           // [E, ceil(N/128), ceil(K/128)]
+    const int32_t* offsets;   // device [E + 1]
+    void* Y;                  // [R, ldy] of y_type
+    int64_t ldy;
+    int y_type;
+    int R, E, N, K;
+    void* ws;
+};
+
+// The rows of a tile (the MMA's N side) for R rows over E experts, and the CTAs
+// that work on a tile together (2: a pair with a tile of 256 weight rows).
+int grouped_tile_rows(int R, int E);
+inline int grouped_ctas(int tile_rows) { return tile_rows > 64 ? 2 : 1; }
+
+size_t grouped_workspace_bytes(int R, int E, int sms);
+
+// tmW: the weights as one [E * N, K] matrix of bytes, 128 x 128 boxes, 128-byte
+// swizzle; tmX: the activations ([R, K] bytes, boxes of 128 K x the tile's
+// rows that one CTA holds).
+cudaError_t launch_grouped(const GroupedArgs& a, const CUtensorMap& tmW, const CUtensorMap& tmX, const LaunchCtl& c,
+                           cudaStream_t st);
+// Zeros in rows [0, offsets[E]) of Y: the K = 0 product.
+cudaError_t launch_grouped_zero(const GroupedArgs& a, cudaStream_t st);
+
+}  // namespace qg

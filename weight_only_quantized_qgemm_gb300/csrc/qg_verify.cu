@@ -1,0 +1,404 @@
+// Verification of drafted tokens against the target's probabilities, for sm_103a.
+//
+// With p_j the softmax of the target's row j and q_j that of the draft's row
+// (a certain draft: 1 at the drafted token), the drafts d_0, d_1, ... of a
+// sequence are kept in order while u_j q_j(d_j) < p_j(d_j).  At the first one that
+// is not kept (row n) the token is drawn from max(p_n - q_n, 0), behind the last
+// one from p_n: the largest weight[v] / noise[v] with exponential random noise,
+// which draws v with probability weight[v] / sum.  (A race needs no sum of the
+// weights and no ordered scan over the vocabulary, and two implementations draw
+// the same token unless the two largest ratios are as close as their rounding.)
+// Greedy: drafts are kept while they are the target's largest logit, and the
+// last token is that of row n.
+//
+// A cluster of CTAs takes a sequence, each CTA a slice of the vocabulary:
+//   1. over all rows, one pass: the maximum and the sum of exponentials of the
+//      slice (greedy: the largest logit and its index), a warp at a time on a
+//      stretch of a row; the CTAs' parts are read through distributed shared
+//      memory by all of them, so that each knows n;
+//   2. the race over the slice of row n (read again, from L2 in the main);
+//   3. the first CTA compares the winners.
+// All sums have a fixed order.  Bound by memory: every logit is read once, and two
+// rows of a sequence a second time with the noise.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qg_launch.h"
+#include "qg_pair.cuh"
+#include "qg_verify.h"
+
+namespace qg {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMostRows = 2 * QG_MAX_DRAFTS + 1;
+constexpr int kMostCtas = 16;
+constexpr int kParts = 8;          // stretches of a row's slice, at most
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int kType>
+struct Elem;
+template <>
+struct Elem<QG_BF16> {
+    static constexpr int kSize = 2;
+    static __device__ __forceinline__ float at(const void* p, int64_t i) {
+        return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+    }
+    static __device__ __forceinline__ void wide(uint32_t w, float* x) {
+        x[0] = __uint_as_float(w << 16);
+        x[1] = __uint_as_float(w & 0xFFFF0000u);
+    }
+};
+template <>
+struct Elem<QG_FP16> {
+    static constexpr int kSize = 2;
+    static __device__ __forceinline__ float at(const void* p, int64_t i) {
+        return __half2float(static_cast<const __half*>(p)[i]);
+    }
+    static __device__ __forceinline__ void wide(uint32_t w, float* x) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        x[0] = f.x;
+        x[1] = f.y;
+    }
+};
+template <>
+struct Elem<QG_FP32> {
+    static constexpr int kSize = 4;
+    static __device__ __forceinline__ float at(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+    static __device__ __forceinline__ void wide(uint32_t w, float* x) { x[0] = __uint_as_float(w); }
+};
+
+__device__ __forceinline__ float ex2(float t) {
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e;
+}
+
+// e^d for d <= 0, with the product's rounding carried along: within 2^-22 of it
+// at any distance from the maximum (a rounded d log2 e alone costs |d| 2^-24).
+__device__ __forceinline__ float exp_near(float d) {
+    const float t = __fmul_rn(d, kLog2e);
+    const float lo = __fmaf_rn(d, kLog2e, -t) + d * 1.925963033e-8f;   // the product's rest, and log2 e's
+    const float e = ex2(t);
+    return d > -150.0f ? __fmaf_rn(e, lo * 0.6931471806f, e) : 0.0f;
+}
+
+// A part of a row: its maximum and sum of exponentials about it; greedy: the
+// maximum and its first index (as bits).
+struct Part {
+    float m, s;
+};
+
+// Exact zero for s where nothing is left; NaN and +inf spread to s.
+__device__ __forceinline__ Part join(Part a, Part b) {
+    const float m = fmaxf(a.m, b.m);
+    const float s = (a.m > -INFINITY ? a.s * ex2((a.m - m) * kLog2e) : a.s) +
+                    (b.m > -INFINITY ? b.s * ex2((b.m - m) * kLog2e) : b.s);
+    return Part{m, s};
+}
+__device__ __forceinline__ Part join_greedy(Part a, Part b) {
+    const bool second = b.m > a.m || (b.m == a.m && __float_as_uint(b.s) < __float_as_uint(a.s));
+    return second ? b : a;
+}
+
+// One value into a running part (greedy).
+__device__ __forceinline__ void see_greedy(Part& p, float x, int v) {
+    if (x > p.m) {   // indices ascend in a lane, so the first stays
+        p.m = x;
+        p.s = __uint_as_float(static_cast<uint32_t>(v));
+    }
+}
+
+template <int kCount>
+__device__ __forceinline__ void see(Part& p, const float (&x)[kCount]) {
+    float m = p.m;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) m = fmaxf(m, x[i]);
+    float s = p.m > -INFINITY ? p.s * ex2((p.m - m) * kLog2e) : p.s;
+    const float c = m > -INFINITY ? m : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) s += ex2((x[i] - c) * kLog2e);
+    p.m = m;
+    p.s = s;
+}
+
+// The slice [v0, v1) of a row, by one warp: scalars up to the first 16-byte
+// boundary and behind the last, vectors in between.
+template <int kType, bool kGreedy>
+__device__ __forceinline__ Part scan_row(const void* row, int v0, int v1, int lane) {
+    using El = Elem<kType>;
+    constexpr int kVec = 16 / El::kSize;
+    Part p{-INFINITY, kGreedy ? __uint_as_float(0x7FFFFFFFu) : 0.0f};
+    const uint8_t* base = static_cast<const uint8_t*>(row);
+    const uintptr_t first = reinterpret_cast<uintptr_t>(base) + static_cast<int64_t>(v0) * El::kSize;
+    const int head = static_cast<int>(((16 - (first & 15u)) & 15u) / El::kSize);
+    const int a0 = v0 + head < v1 ? v0 + head : v1;
+    const int nvec = (v1 - a0) / kVec;
+    const int a1 = a0 + nvec * kVec;
+    auto one = [&](int v) {
+        const float x[1] = {El::at(row, v)};
+        if constexpr (kGreedy) see_greedy(p, x[0], v);
+        else see(p, x);
+    };
+    for (int v = v0 + lane; v < a0; v += 32) one(v);
+    const uint4* vec = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(a0) * El::kSize);
+    constexpr int kU = 4;   // loads in flight
+    for (int i = lane; i < nvec; i += 32 * kU) {
+        uint4 w[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (i + 32 * u < nvec) w[u] = vec[i + 32 * u];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            if (i + 32 * u >= nvec) break;
+            float x[kVec];
+            const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) El::wide(ws[e], x + e * (kVec / 4));
+            if constexpr (kGreedy) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) see_greedy(p, x[e], a0 + (i + 32 * u) * kVec + e);
+            } else {
+                see(p, x);
+            }
+        }
+    }
+    for (int v = a1 + lane; v < v1; v += 32) one(v);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Part q{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)};
+        p = kGreedy ? join_greedy(p, q) : join(p, q);
+    }
+    return p;
+}
+
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(map_to_cta(smem_u32(p), rank)) : "memory");
+    return v;
+}
+
+// A candidate of the race: the larger ratio, then the lower index.
+struct Best {
+    float ratio;
+    int v;
+};
+__device__ __forceinline__ Best better(Best a, Best b) {
+    return b.ratio > a.ratio || (b.ratio == a.ratio && b.v < a.v) ? b : a;
+}
+
+template <int kType, bool kGreedy>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, int ctas) {
+    using El = Elem<kType>;
+    __shared__ Part parts[kMostRows][kParts];
+    __shared__ Part mine[kMostRows];        // this CTA's slice
+    __shared__ Part all[kMostRows];         // the whole rows
+    __shared__ Best best[2][kWarps];        // of max(p - q, 0), of p
+    __shared__ Best winner[2];
+    __shared__ int kept;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % ctas;
+    const int b = blockIdx.x / ctas;
+    const bool sampled = !kGreedy && a.draft != nullptr;
+    int length = a.G;
+    if (a.lengths != nullptr) {
+        length = a.lengths[b];
+        length = length < 0 ? 0 : length > a.G ? a.G : length;
+    }
+    // rows 0 .. length of the target, then 0 .. length - 1 of the draft
+    const int trows = length + 1;
+    const int rows = trows + (sampled ? length : 0);
+    auto row_at = [&](int r) -> const void* {
+        const uint8_t* p = r < trows ? static_cast<const uint8_t*>(a.target) + (b * a.t_seq + r * a.t_row) * El::kSize
+                                     : static_cast<const uint8_t*>(a.draft) + (b * a.d_seq + (r - trows) * a.d_row) * El::kSize;
+        return p;
+    };
+    // slices and stretches end at multiples of 32 elements, so that rows that
+    // are aligned stay so
+    auto cut = [](int64_t n, int i, int of) { return static_cast<int>((n + 31) / 32 * i / of * 32); };
+    const int v0 = cut(a.V, rank, ctas);
+    int v1 = cut(a.V, rank + 1, ctas);
+    if (v1 > a.V) v1 = a.V;
+    const int slice = v1 - v0;
+    int pieces = slice / 4096;
+    pieces = pieces < 1 ? 1 : pieces > kParts ? kParts : pieces;
+    for (int i = warp; i < rows * pieces; i += kWarps) {
+        const int r = i / pieces, s = i - r * pieces;
+        int s1 = v0 + cut(slice, s + 1, pieces);
+        if (s1 > v1) s1 = v1;
+        const Part p = scan_row<kType, kGreedy>(row_at(r), v0 + cut(slice, s, pieces), s1, lane);
+        if (lane == 0) parts[r][s] = p;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < rows; r += kThreads) {
+        Part p = parts[r][0];
+        for (int s = 1; s < pieces; ++s) p = kGreedy ? join_greedy(p, parts[r][s]) : join(p, parts[r][s]);
+        mine[r] = p;
+    }
+    __syncthreads();
+    cluster_sync_all();
+    for (int r = threadIdx.x; r < rows; r += kThreads) {
+        Part p = mine[r];
+        if (ctas > 1) {
+            p = Part{ld_cluster(&mine[r].m, 0), ld_cluster(&mine[r].s, 0)};
+            for (int c = 1; c < ctas; ++c) {
+                const Part o{ld_cluster(&mine[r].m, static_cast<uint32_t>(c)), ld_cluster(&mine[r].s, static_cast<uint32_t>(c))};
+                p = kGreedy ? join_greedy(p, o) : join(p, o);
+            }
+        }
+        all[r] = p;
+    }
+    __syncthreads();
+    // which drafts are kept: a lane a draft
+    if (warp == 0) {
+        bool keep = false;
+        if (lane < length) {
+            const int64_t d = a.tokens[b * a.ldt + lane];
+            if constexpr (kGreedy) {
+                keep = d == static_cast<int64_t>(__float_as_uint(all[lane].s)) && all[lane].m > -INFINITY;
+            } else if (d >= 0 && d < a.V) {
+                const Part t = all[lane];
+                const float p = exp_near(El::at(row_at(lane), d) - t.m) / t.s;
+                float q = 1.0f;
+                if (sampled) {
+                    const Part s = all[trows + lane];
+                    q = exp_near(El::at(row_at(trows + lane), d) - s.m) / s.s;
+                }
+                keep = a.uniform[b * a.ldu + lane] * q < p;
+            }
+        }
+        const uint32_t not_kept = ~__ballot_sync(0xffffffffu, keep);
+        const int n = not_kept == 0u ? 32 : __ffs(static_cast<int>(not_kept)) - 1;   // the first draft that is not kept
+        if (lane == 0) kept = n;
+    }
+    __syncthreads();
+    const int n = kept;
+    if constexpr (!kGreedy) {
+        const Part t = all[n];
+        const void* trow = row_at(n);
+        const bool drafted = n < length;
+        const Part s = drafted && sampled ? all[trows + n] : Part{0.0f, 1.0f};
+        const void* drow = drafted && sampled ? row_at(trows + n) : nullptr;
+        const int64_t d = drafted && !sampled ? a.tokens[b * a.ldt + n] : -1;   // the certain draft
+        const float pr = 1.0f / t.s, qr = 1.0f / s.s;
+        const float* noise = a.noise + b * a.ldn;
+        // [0]: max(p - q, 0); [1]: p, for a row where that is 0 everywhere
+        Best top[2] = {{0.0f, 0x7FFFFFFF}, {0.0f, 0x7FFFFFFF}};
+        auto enter = [&](int v, float x, float y, float e) {
+            const float p = exp_near(x - t.m) * pr;
+            float q = 0.0f;
+            if (drow != nullptr) q = exp_near(y - s.m) * qr;
+            else if (v == d) q = 1.0f;
+            const float w = p - q;
+            if (w > 0.0f && w > top[0].ratio * e * 0.999999f) {
+                const float ratio = __fdiv_rn(w, e);
+                if (ratio > top[0].ratio) top[0] = Best{ratio, v};
+            }
+            if (drafted && p > 0.0f && p > top[1].ratio * e * 0.999999f) {
+                const float ratio = __fdiv_rn(p, e);
+                if (ratio > top[1].ratio) top[1] = Best{ratio, v};
+            }
+        };
+        // indices ascend in a thread, so the first of equals stays
+        constexpr int kU = 4;
+        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads * kU) {
+            float x[kU], y[kU], e[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int w = v + kThreads * u;
+                x[u] = y[u] = e[u] = 0.0f;
+                if (w >= v1) continue;
+                x[u] = El::at(trow, w);
+                if (drow != nullptr) y[u] = El::at(drow, w);
+                e[u] = noise[w];
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (v + kThreads * u < v1) enter(v + kThreads * u, x[u], y[u], e[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top[i] = better(top[i], Best{__shfl_xor_sync(0xffffffffu, top[i].ratio, o),
+                                             __shfl_xor_sync(0xffffffffu, top[i].v, o)});
+            if (lane == 0) best[i][warp] = top[i];
+        }
+        __syncthreads();
+        if (threadIdx.x < 2) {
+            Best w = best[threadIdx.x][0];
+            for (int i = 1; i < kWarps; ++i) w = better(w, best[threadIdx.x][i]);
+            winner[threadIdx.x] = w;
+        }
+        __syncthreads();
+        cluster_sync_all();
+    }
+    if (rank == 0) {
+        int64_t last = -1;
+        if constexpr (kGreedy) {
+            if (all[n].m > -INFINITY) last = static_cast<int64_t>(__float_as_uint(all[n].s));
+        } else if (threadIdx.x <= static_cast<unsigned>(a.G)) {
+            Best w[2];
+            for (int i = 0; i < 2; ++i) {
+                w[i] = winner[i];
+                for (int c = 1; c < ctas; ++c) {
+                    const float ratio = ld_cluster(&winner[i].ratio, static_cast<uint32_t>(c));
+                    const float v = ld_cluster(reinterpret_cast<const float*>(&winner[i].v), static_cast<uint32_t>(c));
+                    w[i] = better(w[i], Best{ratio, static_cast<int>(__float_as_uint(v))});
+                }
+            }
+            const Best u = w[0].v != 0x7FFFFFFF ? w[0] : w[1];
+            if (u.v != 0x7FFFFFFF) last = u.v;
+        }
+        const int j = static_cast<int>(threadIdx.x);
+        if (j <= a.G) a.out[static_cast<int64_t>(b) * (a.G + 1) + j] = j < n ? a.tokens[b * a.ldt + j] : j == n ? last : -1;
+        if (j == 0) a.accepted[b] = n;
+    }
+    cluster_sync_all();   // nobody leaves while its shared memory is read
+}
+
+template <int kType, bool kGreedy>
+cudaError_t launch(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    static std::atomic<uint64_t> wide{0};
+    cudaError_t e = set_once(wide, verify_kernel<kType, kGreedy>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    // CTAs of a sequence: about two for every SM, none with less than 2048 of the vocabulary
+    int ctas = kMostCtas;
+    while (ctas > 1 && (static_cast<int64_t>(ctas) * a.B > 2 * c.num_sms || a.V / ctas < 2048)) ctas /= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.B * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<kType, kGreedy>, a, ctas);
+}
+
+template <int kType>
+cudaError_t launch_type(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    return a.uniform == nullptr ? launch<kType, true>(a, c, st) : launch<kType, false>(a, c, st);
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    switch (a.type) {
+        case QG_BF16: return launch_type<QG_BF16>(a, c, st);
+        case QG_FP16: return launch_type<QG_FP16>(a, c, st);
+        case QG_FP32: return launch_type<QG_FP32>(a, c, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace qg
