@@ -473,7 +473,7 @@ qg_status qg_quantize_rows_e4m3(const void *X, int x_type, int64_t ldx, int gate
  * with FP32 sums, as qgemm_w8a8_block for each expert on its own.  Rows in front
  * of offsets[0] and from offsets[E] on are left as they were; groups may be empty.
  *   Xq       device, E4M3 codes [R, ldxq], 16-byte aligned, ldxq >= K, ldxq % 16 == 0
- *   X_scale  device, FP32 [ceil(K/128), ldsx], ldsx >= R
+ *   X_scale  device, FP32 [ceil(K/128), ldsx], 16-byte aligned, ldsx >= R, ldsx % 4 == 0
  *   W        device, E4M3 codes [E, N, K], contiguous, 16-byte aligned
  *   W_scale  device, FP32 [E, ceil(N/128), ceil(K/128)], contiguous
  *   offsets  device, int32 [E + 1], ascending, within 0 .. R (entries that are not

@@ -871,9 +871,8 @@ qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_sca
     if (ldxq < K || ldy < N || ldsx < R) return QG_ERR_INVALID_ARG;
     const uintptr_t y_mask = y_type == QG_FP32 ? 3u : 1u;
     // without a K there is nothing of Xq and W to be aligned
-    if ((K > 0 && (!aligned16(Xq) || !aligned16(W) || ldxq % 16 != 0)) ||
-        (reinterpret_cast<uintptr_t>(X_scale) & 3u) || (reinterpret_cast<uintptr_t>(W_scale) & 3u) ||
-        (reinterpret_cast<uintptr_t>(offsets) & 3u) || (reinterpret_cast<uintptr_t>(Y) & y_mask))
+    if ((K > 0 && (!aligned16(Xq) || !aligned16(W) || !aligned16(X_scale) || ldxq % 16 != 0 || ldsx % 4 != 0)) ||
+        (reinterpret_cast<uintptr_t>(W_scale) & 3u) || (reinterpret_cast<uintptr_t>(offsets) & 3u) || (reinterpret_cast<uintptr_t>(Y) & y_mask))
         return QG_ERR_MISALIGNED;
     const int nt = grouped_tile_rows(R, E);
     // tiles are counted in 32 bits
@@ -902,7 +901,7 @@ qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_sca
     if (!tmW) return QG_ERR_CUDA;
     CUtensorMap tmX;
     if (!make_tmap(&tmX, Xq, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<uint64_t>(K), static_cast<uint64_t>(R),
-                   static_cast<uint64_t>(ldxq), 128, static_cast<uint32_t>(nt / grouped_ctas(nt))))
+                   static_cast<uint64_t>(ldxq), 128, static_cast<uint32_t>(grouped_box_rows(nt))))
         return QG_ERR_CUDA;
     return launch_grouped(a, *tmW, tmX, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }

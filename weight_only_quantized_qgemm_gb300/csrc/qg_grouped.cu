@@ -11,21 +11,32 @@
 // factors (activation scale x weight scale, one per row of the activations) and
 // adds to FP32 outer sums in registers, as the ungrouped kernel does.
 //
-// The output is tiled in 128 weight rows (256 on a CTA pair) x up to NT rows of
-// one expert.  A tile's MMA is as wide as its rows (rounded up to 16 or 32), so that a
-// ragged group costs the tensor cores only its rows; columns of TMEM and of the
-// activation boxes beyond them hold other rows' values, which nothing stores.
-// Every CTA lists the experts that hold rows, with the tiles in front of each,
-// at its start; workers then take tiles worker, worker + workers, ..., so that
-// those in flight share an expert's weights and activations in L2.
+// Few rows an expert (W): a tile is 128 weight rows, on the MMA's M side, x up to NT
+// rows of one expert on its N side, which is as wide as the tile's rows (rounded
+// up to 16).  Columns of TMEM and of the activation boxes beyond them hold other
+// rows' values, which nothing stores.  Bound by the weights' bytes.
+//
+// Many rows (T): a tile is 256 rows of one expert on the M side of a CTA pair's
+// MMAs x 256 weight rows.  A fold lane then is a row and needs one factor a K
+// block; with the weights on the M side it needs a factor for each of its columns,
+// whose way out of shared memory took longer than the MMAs.  The pair's MMAs of a K
+// block take 512 cycles, a third of a unit's round of barriers beside them: MMAs,
+// commit, fold (two waits, two loads of 64 columns, the products), release, the
+// issuer's wait.  Two accumulators of 256 columns are all that TMEM holds, so the
+// round sets the pace: 456 ns a unit at K = 16384, 2.8 PFLOP/s (374 without the
+// copies' power and traffic, 347 without the MMAs).
+//
+// Every CTA lists the experts that hold rows, with the tiles in front of each, at
+// its start; workers then take tiles worker, worker + workers, ..., so that those
+// in flight share an expert's weights and activations in L2.
 //
 // One persistent CTA (or pair) per SM; warps by role:
 //   warp 0     producer: a unit's weight and activation boxes into one stage of
 //              the ring, one barrier for all of them
-//   warp 2     MMA issuer (the pair's first CTA)
-//   warp 3     factors: sx * s of the unit's rows into shared memory, the scales
-//              fetched some units ahead
-//   warps 4-   fold and epilogue: one per TMEM lane quadrant (two in a pair)
+//   warp 1     MMA issuer (T: warps 1 and 2 of the pair's first CTA take alternate
+//              units; a K block is summed on its own, so that they need no order)
+//   warp 3     the activation scales of a unit into a ring of their own
+//   warps 4-   fold and epilogue: one per TMEM lane quadrant (T: two)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,9 +50,17 @@ namespace {
 
 using gemm::Ring;
 
-constexpr int kWarpProd = 0, kWarpMma = 2, kWarpFactor = 3, kWarpFold0 = 4;
+constexpr int kWarpProd = 0, kWarpMma = 1, kWarpScales = 3, kWarpFold0 = 4;
 constexpr int kMaxExperts = QG_MAX_EXPERTS;
-constexpr int kAhead = 4;   // units whose scales the factor warp fetches ahead
+
+// The experts that hold rows (the groups), in order.  Their rows follow one
+// another, so that a group ends where the next one begins: the entry behind the
+// last says where the rows and the tiles end.
+struct Groups {
+    int2 at[kMaxExperts + 1];        // first row, tiles in front
+    uint16_t expert[kMaxExperts];
+    int count, tiles;
+};
 
 template <int NT, bool kPair>
 struct GLayout {
@@ -51,29 +70,40 @@ struct GLayout {
     static constexpr int kBlk = kPair ? 1 : 2;
     static constexpr int kXRows = NT / kCtas;              // activation rows in this CTA's shared memory
     static constexpr int kWBox = 128 * 128;
-    static constexpr int kXBox = kXRows * 128;
+    static constexpr int kXBlock = kXRows * 128;           // a K block's activations
     static constexpr int kXOff = kBlk * kWBox;             // in a stage, behind the weights
-    static constexpr int kStage = kBlk * (kWBox + kXBox);
+    static constexpr int kStage = kBlk * (kWBox + kXBlock);
     static constexpr int kFit = 512 / (kBlk * NT);
     static constexpr int kBufs = kFit < 4 ? kFit : 4;      // accumulator sets (kBlk x NT columns each)
+    // MMA issuers, each with accumulator sets of its own (alternate units)
+    static constexpr int kIssuers = kPair ? 2 : 1;
+    static constexpr int kTabBytes = (sizeof(Groups) + 15) / 16 * 16;
     static constexpr int kFold = kPair ? 8 : 4;            // fold warps
     static constexpr int kCols = NT / (kFold / 4);         // columns of a fold warp
     static constexpr int kThreads = 32 * (kWarpFold0 + kFold);
-    static constexpr int kGSlot = kBlk * NT * 4;           // factors of a unit
-    static constexpr int kOutWarp = 16 * 64;               // a fold warp's 16 rows x 32 weight rows of 16 bits
-    static constexpr int kFixed = kMaxExperts * 16 + kBufs * kGSlot + kFold * kOutWarp + 512;
-    static constexpr int kStages = (232448 - kFixed) / kStage;
+    // The ring of activation scales: of a block, the tile's rows from a multiple of
+    // four on (bulk copies start and end at 16 bytes)
+    static constexpr int kSSlots = kPair ? 4 : 8;
+    static constexpr int kSRow = (NT + 4) * 4;
+    static constexpr int kSSlot = kBlk * kSRow;
+    static constexpr int kOutWarp = (kPair ? 32 : 16) * 64;   // a fold warp's 32 (16) rows x 32 weight rows of 16 bits
+    static constexpr int kFixed = kTabBytes + kSSlots * kSSlot + kFold * kOutWarp + 512;
+    static constexpr int kStages = (232448 - kFixed) / kStage / kIssuers * kIssuers;
     static constexpr int kTabOff = kStages * kStage;
-    static constexpr int kGOff = kTabOff + kMaxExperts * 16;
-    static constexpr int kOutOff = kGOff + kBufs * kGSlot;
+    static constexpr int kSOff = kTabOff + kTabBytes;
+    static constexpr int kOutOff = kSOff + kSSlots * kSSlot;
     static constexpr int kBarOff = kOutOff + kFold * kOutWarp;
-    static constexpr int kNumBars = 2 * kStages + 3 * kBufs;
+    static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 2 * kSSlots;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmemBytes = kMiscOff + 32;
     static_assert(kSmemBytes <= 232448, "shared memory");
     static_assert(kBufs >= 2 && kBufs * kBlk * NT <= 512, "TMEM columns");
-    static_assert(kXBox % 1024 == 0 && kStage % 1024 == 0, "keep the 1024-byte swizzle alignment");
-    static_assert(kCols % 16 == 0 && kXRows % 8 == 0, "fragments");
+    static_assert(kXBlock % 1024 == 0 && kStage % 1024 == 0, "keep the 1024-byte swizzle alignment");
+    static_assert(kCols % 16 == 0, "fragments");
+    // a set and a stage always belong to one issuer, whose parity waits are then for
+    // the phase after one that it has seen
+    static_assert(kBufs % kIssuers == 0 && kStages % kIssuers == 0, "ring ownership");
+    static_assert(kSRow % 16 == 0 && kOutOff % 16 == 0 && kNumBars * 8 <= 512 - 32, "alignment, barriers");
 };
 
 struct GParams {
@@ -84,7 +114,7 @@ struct GParams {
     void* Y;
     int64_t ldy;
     int y_type;
-    int y_vec;        // a 16-bit Y that takes 16-byte stores
+    int y_vec;        // Y takes 16-byte stores
     int R, E, N, KB;  // KB: K blocks of 128
     int KU;           // units a tile
     int sn;           // blocks of 128 weight rows (the scales' rows of an expert)
@@ -106,18 +136,20 @@ __device__ __forceinline__ void mma_ss_f8_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
-// 16 lanes x 8 C columns (C = 2 or 4 groups): lane t holds, of group g, columns
-// 2 (t % 4) and the next of rows t / 4 (v[4g], v[4g + 1]) and t / 4 + 8 (v[4g + 2],
-// v[4g + 3]).  A lane so meets a quarter of the columns, and of their factors.
+// 16 lanes x 4 C columns (C = 4 or 8 groups of four): lane t holds, of group j,
+// column 4 j + t % 4 of rows t / 4 (v[2j]) and t / 4 + 8 (v[2j + 1]).  A lane so meets
+// a quarter of the columns, and of their scales: with a row to a lane (32x32b)
+// every lane reads all of them, and a K block of 256 columns takes eight warps
+// 586 cycles; 463 this way, and 590 with 16x256b, which reads TMEM at half the rate.
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr)
                  : "memory");
 }
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
@@ -135,12 +167,50 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t v0, uint32_t
         : "r"(v0), "r"(v1), "f"(f0), "f"(f1));
 }
 
+__device__ __forceinline__ void fma2(uint64_t& a, uint32_t v0, uint32_t v1, uint64_t f) {
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(a) : "r"(v0), "r"(v1), "l"(f));
+}
+__device__ __forceinline__ uint64_t twice(float f) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(f));
+    return r;
+}
+
+// Each thread of the warp reads 64 consecutive 32-bit columns of its own lane.
+__device__ __forceinline__ void tmem_ld_x64(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, "
+        "%38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, "
+        "%60, %61, %62, %63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+          "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+          "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+          "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+
 // Four 8 x 8 matrices of 16-bit values, transposed on the way: row j of matrix i
 // goes to the address of lane 8 i + j.
 __device__ __forceinline__ void stmatrix_t4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
                  "r"(c), "r"(d)
                  : "memory");
+}
+
+// Registers between the warpgroups of a block: every warp of one executes it.
+template <int kRegs>
+__device__ __forceinline__ void regs_more() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_fewer() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __device__ __forceinline__ uint32_t pack_out(float lo, float hi, int y_type) {
@@ -152,11 +222,45 @@ __device__ __forceinline__ uint32_t pack_out(float lo, float hi, int y_type) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// An expert that holds rows: its first row, how many, the tiles in front of it
-// in the grid's order, its number.
-struct Group {
-    int row0, rows, tile0, expert;
-};
+// Bounded waits of this kernel.  The timer is read only once a wait has slept
+// for 20 us, since most are short.  wait_on is for the fold, which a unit's chain
+// of wait, loads, release bounds: no vote on the outcome, no call around which the
+// sums would have to be saved.  A wait that gives up just returns, as does every
+// later one; the sums are then worthless, and the tile loop ends.
+__device__ __forceinline__ bool wait_here(uint32_t bar, uint32_t parity, const WaitCtl& c) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*c.abort) return false;
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    const uint64_t t0 = globaltimer();
+    for (uint32_t it = 0; it < (1u << 26); ++it) {
+        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+        if (*c.abort) return false;
+        if (globaltimer() - t0 > c.timeout_ns) break;
+    }
+    raise_abort(c, kDevTimeout);
+    return false;
+}
+__device__ __forceinline__ bool warp_wait_here(uint32_t bar, uint32_t parity, const WaitCtl& c) {
+    return __all_sync(0xffffffffu, wait_here(bar, parity, c));
+}
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, const WaitCtl& c) { wait_here(bar, parity, c); }
+__device__ __forceinline__ bool aborted(const WaitCtl& c) { return __any_sync(0xffffffffu, *c.abort != 0); }
+
+// One lane's arrival without a branch around it.
+__device__ __forceinline__ void arrive_if(bool yes, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 st;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar),
+                 "r"(static_cast<uint32_t>(yes))
+                 : "memory");
+}
+// On a barrier of the pair's leader (a mapped address); it carries no memory, as
+// mbar_arrive_cluster.
+__device__ __forceinline__ void arrive_cluster_if(bool yes, uint32_t mapped) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(mapped),
+                 "r"(static_cast<uint32_t>(yes))
+                 : "memory");
+}
 
 // Where tile t lies.  The groups are in ascending order of their tiles.
 template <int NT, int kCtas>
@@ -164,39 +268,52 @@ struct Place {
     int g;            // the group
     int expert;
     int row0, rows;   // of the tile
+    bool several;     // the group has more row tiles than this
     int n0;           // first weight row of this CTA
     int nb;           // its block of 128 weight rows
-    __device__ void enter(const Group* tab, int groups, int t, int tn_count, int rank) {
+    __device__ void enter(const Groups& tab, int t, int tn_count, int rank) {
         // the last group whose tiles begin at or before t
-        int lo = g, hi = groups - 1;
-        if (lo < hi && tab[lo + 1].tile0 <= t) {
+        int lo = g, hi = tab.count - 1;
+        if (tab.at[lo + 1].y <= t) {
+            ++lo;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (tab[mid].tile0 <= t) lo = mid;
+                if (tab.at[mid].y <= t) lo = mid;
                 else hi = mid - 1;
             }
             g = lo;
         }
-        const Group q = tab[g];
-        expert = q.expert;
-        const int tm_count = (q.rows + NT - 1) / NT;
-        const int j = t - q.tile0;
+        const int2 q = tab.at[g];
+        const int group_rows = tab.at[g + 1].x - q.x;
+        expert = tab.expert[g];
+        several = group_rows > NT;
+        const int tm_count = (group_rows + NT - 1) / NT;
+        const int j = t - q.y;
         const int tn = j / tm_count;   // a weight tile's row tiles are neighbours: its re-reads come from L2
         const int tm = j - tn * tm_count;
-        row0 = q.row0 + tm * NT;
-        rows = q.rows - tm * NT < NT ? q.rows - tm * NT : NT;
+        row0 = q.x + tm * NT;
+        rows = group_rows - tm * NT < NT ? group_rows - tm * NT : NT;
         nb = tn * kCtas + rank;
         n0 = nb * 128;
     }
-    // the MMA's N side: a multiple of 16, on a pair of 32 (16 from each CTA)
-    __device__ int width() const { return kCtas == 2 ? (rows + 31) & ~31 : (rows + 15) & ~15; }
+    // The rows (of the tile's share of this CTA) whose scales it needs.
+    __device__ void scale_rows(int rank, int R, int& first, int& count) const {
+        first = row0;
+        count = rows;
+        if (kCtas == 2) {   // its half of a pair's tile, as far as the rows go
+            first += rank * (NT / 2);
+            count = R - first < NT / 2 ? (R > first ? R - first : 0) : NT / 2;
+        }
+    }
+    // W: the MMA's N side
+    __device__ int width() const { return (rows + 15) & ~15; }
 };
 
 // The table of the groups and the number of tiles, by one warp.  Offsets are
 // taken as they are meant (ascending, from 0 to R); what breaks that is cut so
 // that no row lies outside the tensors and none is in two groups.
 template <int NT>
-__device__ __forceinline__ void list_groups(const GParams& p, Group* tab, int* groups, int* tiles, int lane) {
+__device__ __forceinline__ void list_groups(const GParams& p, Groups& tab, int lane) {
     int first = __ldcg(p.offsets);
     int end_before = first < 0 ? 0 : first > p.R ? p.R : first;
     int ngroups = 0, ntiles = 0;
@@ -231,16 +348,20 @@ __device__ __forceinline__ void list_groups(const GParams& p, Group* tab, int* g
                 if (lane >= o) upto += other;
             }
             const uint32_t active = __ballot_sync(0xffffffffu, rows > 0);
-            if (rows > 0)
-                tab[ngroups + __popc(active & ((1u << lane) - 1u))] = Group{begin, rows, ntiles + upto - mine, e};
+            if (rows > 0) {
+                const int i = ngroups + __popc(active & ((1u << lane) - 1u));
+                tab.at[i] = make_int2(begin, ntiles + upto - mine);
+                tab.expert[i] = static_cast<uint16_t>(e);
+            }
             ngroups += __popc(active);
             ntiles += __shfl_sync(0xffffffffu, upto, 31);
             end_before = __shfl_sync(0xffffffffu, end, 31);
         }
     }
     if (lane == 0) {
-        *groups = ngroups;
-        *tiles = ntiles;
+        tab.at[ngroups] = make_int2(end_before, ntiles);
+        tab.count = ngroups;
+        tab.tiles = ntiles;
     }
 }
 
@@ -259,13 +380,15 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
     const uint32_t bar0 = base + L::kBarOff;
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (kStages + s); };
-    auto dfull = [&](int b) { return bar0 + 8u * (2 * kStages + b); };
-    auto dempty = [&](int b) { return bar0 + 8u * (2 * kStages + kBufs + b); };
-    auto fempty = [&](int b) { return bar0 + 8u * (2 * kStages + 2 * kBufs + b); };
-    const Group* tab = reinterpret_cast<const Group*>(gbase + L::kTabOff);
+    constexpr int kBarD = 2 * kStages;
+    auto dfull = [&](int b) { return bar0 + 8u * (kBarD + b); };
+    auto dempty = [&](int b) { return bar0 + 8u * (kBarD + kBufs + b); };
+    auto sfull = [&](int s) { return bar0 + 8u * (kBarD + 2 * kBufs + s); };
+    auto sempty = [&](int s) { return bar0 + 8u * (kBarD + 2 * kBufs + L::kSSlots + s); };
+    Groups& tab = *reinterpret_cast<Groups*>(gbase + L::kTabOff);
     int* misc = reinterpret_cast<int*>(gbase + L::kMiscOff);
     volatile int* abort_flag = misc + 1;
-    auto factors_at = [&](int b) { return reinterpret_cast<float*>(gbase + L::kGOff + b * L::kGSlot); };
+    auto scales_at = [&](int s) { return reinterpret_cast<const float*>(gbase + L::kSOff + s * L::kSSlot); };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -284,9 +407,12 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
             mbar_init(empty(s), 1);   // commit: the unit's MMAs are complete
         }
         for (int b = 0; b < kBufs; ++b) {
-            mbar_init(dfull(b), 2);                   // commit, and the factor warp
+            mbar_init(dfull(b), 1);                   // commit
             mbar_init(dempty(b), kFold * L::kCtas);   // every fold warp: to the MMA issuer
-            mbar_init(fempty(b), kFold);              // this CTA's: to its factor warp
+        }
+        for (int s = 0; s < L::kSSlots; ++s) {
+            mbar_init(sfull(s), 1);
+            mbar_init(sempty(s), kFold);   // this CTA's
         }
         *abort_flag = 0;
         fence_barrier_init();
@@ -298,16 +424,23 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
     }
     grid_dependents_launch();
     grid_dependency_wait();
-    if (warp == kWarpFactor)
-        list_groups<NT>(p, reinterpret_cast<Group*>(gbase + L::kTabOff), misc + 2, misc + 3, lane);
+    if (warp == kWarpScales)
+        list_groups<NT>(p, tab, lane);
     tc_fence_before();
     __syncwarp();
     if constexpr (kPair) cluster_sync_all();   // the peer's barriers are set up too
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = static_cast<uint32_t>(misc[0]);
-    const int groups = misc[2], tiles = misc[3];
+    const int tiles = tab.tiles;
 
+    if (warp < kWarpFold0) {
+    // 128 outer sums a fold lane: of the launch's 384 x 168 registers, 256 x 224 +
+    // 128 x 56
+    if constexpr (kPair) {
+        static_assert(L::kThreads == 384 && 256 * 224 + 128 * 56 <= 384 * 168, "registers");
+        regs_fewer<56>();
+    }
     if (warp == kWarpProd) {
         if (lane == 0) {
             const uint64_t keep = policy_evict_last(), once = policy_evict_first();
@@ -317,14 +450,14 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
             int i = 0;
             bool ok = true;
             for (int t = worker; ok && t < tiles; t += p.workers) {
-                at.enter(tab, groups, t, p.tn, rank);
+                at.enter(tab, t, p.tn, rank);
                 // a weight tile of several row tiles is read again soon
-                const uint64_t pol_w = tab[at.g].rows > NT ? keep : once;
+                const uint64_t pol_w = at.several ? keep : once;
                 const int wrow = at.expert * p.N + at.n0;
-                const int xrow = at.row0 + (kPair ? rank * (at.width() >> 1) : 0);
+                const int xrow = at.row0 + rank * L::kXRows;
                 for (int ku = 0; ku < p.KU; ++ku, ++i, rs.step(1)) {
                     if (i >= kStages) {
-                        ok = wait_bounded(empty(rs.slot), rs.phase ^ 1u, wc);
+                        ok = wait_here(empty(rs.slot), rs.phase ^ 1u, wc);
                         if (!ok) break;
                     }
                     if (blockIdx.x == 0 && i == p.fault_unit) continue;   // failure-path test hook
@@ -336,10 +469,10 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                         const int k0 = (ku * kBlk + b) * 128;
                         if constexpr (kPair) {
                             tma_load_2d_pair(dst + b * L::kWBox, &tmW, bar, k0, wrow, pol_w);
-                            tma_load_2d_pair(dst + L::kXOff + b * L::kXBox, &tmX, bar, k0, xrow, keep);
+                            tma_load_2d_pair(dst + L::kXOff + b * L::kXBlock, &tmX, bar, k0, xrow, keep);
                         } else {
                             tma_load_2d(dst + b * L::kWBox, &tmW, bar, k0, wrow, pol_w);
-                            tma_load_2d(dst + L::kXOff + b * L::kXBox, &tmX, bar, k0, xrow, keep);
+                            tma_load_2d(dst + L::kXOff + b * L::kXBlock, &tmX, bar, k0, xrow, keep);
                         }
                     }
                 }
@@ -349,233 +482,341 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
             // gives up as well
             if (i > 0) gemm::drain_wait(empty((i - 1) % kStages), ((i - 1) / kStages) & 1, p.timeout_ns);
         }
-    } else if (warp == kWarpMma && leader) {
+    } else if (warp < kWarpMma + L::kIssuers && leader) {
+        const int issuer = warp - kWarpMma;
+        constexpr uint32_t kDescT = (idesc_f8_e4m3(256) & ~(31u << 24)) | (static_cast<uint32_t>(256 >> 4) << 24);
         const bool elected = elect_one();
         const uint64_t d0 = smem_desc_sw128(base);
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-            if constexpr (kPair) return __all_sync(0xffffffffu, wait_bounded_cluster(bar, parity, wc)) != 0;
-            else return gemm::warp_wait(bar, parity, wc);
-        };
         auto commit = [&](uint32_t bar) {
             if constexpr (kPair) tc_commit_pair(bar, static_cast<uint16_t>(3u));
             else tc_commit(bar);
         };
-        Ring<kStages> rs(0);
-        Ring<kBufs> rb(0);
+        Ring<kStages> rs(issuer);
+        Ring<kBufs> rb(issuer);
         Pl at;
         at.g = 0;
-        int i = 0;
+        int i = issuer, last = -1, ku = issuer;   // the unit, the last one issued, the unit's place in its tile
         bool ok = true;
         for (int t = worker; ok && t < tiles; t += p.workers) {
-            at.enter(tab, groups, t, p.tn, rank);
-            uint32_t idesc = idesc_f8_e4m3(at.width());
-            if constexpr (kPair) idesc = (idesc & ~(31u << 24)) | (static_cast<uint32_t>(256 >> 4) << 24);
-            for (int ku = 0; ku < p.KU; ++ku, ++i, rs.step(1), rb.step(1)) {
-                ok = wait(full(rs.slot), rs.phase);
-                if (ok && i >= kBufs) ok = wait(dempty(rb.slot), rb.phase ^ 1u);
+            at.enter(tab, t, p.tn, rank);
+            const uint32_t idesc = kPair ? kDescT : idesc_f8_e4m3(at.width());
+            // the places in a stage of the operands of the M and the N side
+            constexpr uint32_t m_off = kPair ? L::kXOff : 0, n_off = kPair ? 0 : L::kXOff;
+            for (; ku < p.KU; ku += L::kIssuers, i += L::kIssuers, rs.step(L::kIssuers), rb.step(L::kIssuers)) {
+                // On a pair, too, the arrivals carry no memory of the arriving threads
+                // (TMA writes, which the MMA reads, and TMEM accesses ordered by
+                // tcgen05.fence), so that the waits need no cluster scope.
+                ok = warp_wait_here(full(rs.slot), rs.phase, wc);
+                if (ok && i >= kBufs) ok = warp_wait_here(dempty(rb.slot), rb.phase ^ 1u, wc);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t ad = d0 + static_cast<uint64_t>((rs.slot * L::kStage) >> 4);
-                const uint64_t bd = ad + static_cast<uint64_t>(L::kXOff >> 4);
+                const uint64_t stage = d0 + static_cast<uint64_t>((rs.slot * L::kStage) >> 4);
                 if (elected) {
 #pragma unroll
                     for (int b = 0; b < kBlk; ++b) {
                         const uint32_t dt = tmem + (rb.slot * kBlk + b) * NT;
-                        const uint64_t adb = ad + static_cast<uint64_t>((b * L::kWBox) >> 4);
-                        const uint64_t bdb = bd + static_cast<uint64_t>((b * L::kXBox) >> 4);
+                        // several blocks a unit: weights, then activations (W alone)
+                        const uint64_t ad = stage + ((m_off + b * L::kWBox) >> 4);
+                        const uint64_t bd = stage + ((n_off + b * L::kXBlock) >> 4);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            if constexpr (kPair) mma_ss_f8_pair(dt, adb + 2 * j, bdb + 2 * j, idesc, j > 0 ? 1u : 0u);
-                            else mma_ss_f8(dt, adb + 2 * j, bdb + 2 * j, idesc, j > 0 ? 1u : 0u);
+                            if constexpr (kPair) mma_ss_f8_pair(dt, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
+                            else mma_ss_f8(dt, ad + 2 * j, bd + 2 * j, idesc, j > 0 ? 1u : 0u);
                         }
                     }
-                    commit(empty(rs.slot));
                     commit(dfull(rb.slot));
+                    commit(empty(rs.slot));
                 }
                 __syncwarp();
+                last = i;
             }
+            ku -= p.KU;
         }
-        if (i > 0 && elected) gemm::drain_wait(empty((i - 1) % kStages), ((i - 1) / kStages) & 1, p.timeout_ns);
-    } else if (warp == kWarpFactor) {
-        // Lane l has columns l, l + 32, ... of the tile; their scales are fetched
-        // kAhead units before they are used (a load takes longer than a unit).
-        constexpr int kHeld = (kBlk * NT + 31) / 32;
-        float held[kAhead][kHeld];
-        float sw[kAhead][kBlk];
-        Pl at;
-        at.g = 0;
-        int t = worker, ku = 0;
-        bool live = t < tiles;
-        if (live) at.enter(tab, groups, t, p.tn, rank);
-        auto fetch = [&](float (&h)[kHeld], float (&w)[kBlk]) {
-            if (!live) return;
-            const float* srow = p.S + (static_cast<int64_t>(at.expert) * p.sn + at.nb) * p.KB;
-#pragma unroll
-            for (int b = 0; b < kBlk; ++b) {
-                const int kb = ku * kBlk + b;
-                w[b] = kb < p.KB && at.nb < p.sn ? __ldg(srow + kb) : 0.0f;
-            }
-#pragma unroll
-            for (int c = 0; c < kHeld; ++c) {
-                const int col = c * 32 + lane;
-                const int b = kBlk == 1 ? 0 : col / NT;
-                const int j = kBlk == 1 ? col : col % NT;
-                const int kb = ku * kBlk + b;
-                h[c] = b < kBlk && kb < p.KB && j < at.rows
-                           ? __ldcg(p.Sx + static_cast<int64_t>(kb) * p.ldsx + at.row0 + j)
-                           : 0.0f;
-            }
-            if (++ku == p.KU) {
-                ku = 0;
-                t += p.workers;
-                live = t < tiles;
-                if (live) at.enter(tab, groups, t, p.tn, rank);
-            }
-        };
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) fetch(held[a], sw[a]);
-        const int mine = worker < tiles ? (tiles - worker + p.workers - 1) / p.workers * p.KU : 0;
-        Ring<kBufs> rb(0);
-        bool ok = true;
-        for (int i0 = 0; ok && i0 < mine; i0 += kAhead) {
-#pragma unroll
-            for (int a = 0; a < kAhead; ++a) {
-                const int i = i0 + a;
-                if (i >= mine) break;
-                if (i >= kBufs) {
-                    ok = gemm::warp_wait(fempty(rb.slot), rb.phase ^ 1u, wc);
-                    if (!ok) break;
+        if (last >= 0 && elected) gemm::drain_wait(empty(last % kStages), (last / kStages) & 1, p.timeout_ns);
+    } else if (warp == kWarpScales) {
+        // The scales of this CTA's rows of each unit, by bulk copies: loads to
+        // registers, however far ahead, held up a warp's other waits (290 ns a unit).
+        if (lane == 0) {
+            const uint64_t keep = policy_evict_last();
+            Ring<L::kSSlots> rs(0);
+            Pl at;
+            at.g = 0;
+            int i = 0;
+            bool ok = true;
+            for (int t = worker; ok && t < tiles; t += p.workers) {
+                at.enter(tab, t, p.tn, rank);
+                int first, rows;
+                at.scale_rows(rank, p.R, first, rows);
+                const float* from = p.Sx + (first & ~3);
+                const uint32_t bytes = rows > 0 ? ((first & 3) + rows + 3) / 4 * 16 : 0;
+                for (int ku = 0; ku < p.KU; ++ku, ++i, rs.step(1)) {
+                    if (i >= L::kSSlots) {
+                        ok = wait_here(sempty(rs.slot), rs.phase ^ 1u, wc);
+                        if (!ok) break;
+                    }
+                    const int nblk = kBlk == 1 || ku * kBlk + 2 <= p.KB ? kBlk : 1;
+                    mbar_arrive_expect_tx(sfull(rs.slot), bytes * nblk);
+                    for (int b = 0; b < nblk && bytes > 0; ++b)
+                        bulk_load(base + L::kSOff + rs.slot * L::kSSlot + b * L::kSRow,
+                                  from + static_cast<int64_t>(ku * kBlk + b) * p.ldsx, bytes, sfull(rs.slot), keep);
                 }
-                float* f = factors_at(rb.slot);
-#pragma unroll
-                for (int c = 0; c < kHeld; ++c) {
-                    const int col = c * 32 + lane;
-                    const int b = kBlk == 1 ? 0 : col / NT;
-                    const int j = kBlk == 1 ? col : col % NT;
-                    // in the order in which a fold lane reads them (fold below)
-                    if (b < kBlk)
-                        f[b * NT + (j & ~15) + ((j & 7) >> 1) * 4 + ((j >> 3) & 1) * 2 + (j & 1)] =
-                            __fmul_rn(held[a][c], b == 0 ? sw[a][0] : sw[a][kBlk - 1]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(dfull(rb.slot));
-                rb.step(1);
-                fetch(held[a], sw[a]);
             }
+            // the copies of the last turn of the ring (earlier ones were waited for by the fold)
+            for (int j = i > L::kSSlots ? i - L::kSSlots : 0; j < i; ++j)
+                gemm::drain_wait(sfull(j % L::kSSlots), (j / L::kSSlots) & 1, p.timeout_ns);
         }
-    } else if (warp >= kWarpFold0) {
+    }
+    } else {
+        if constexpr (kPair) regs_more<224>();
         const int fw = warp - kWarpFold0;
         const int q = warp & 3;
-        const int col0 = (fw >> 2) * kCols;
-        const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + col0;
+        const int g = fw >> 2;            // columns g kCols ..
+        const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + g * kCols;
         uint8_t* out = gbase + L::kOutOff + fw * L::kOutWarp;
         constexpr int kChunk = kCols < 32 ? kCols : 32;   // columns of a TMEM load
         Ring<kBufs> rb(0);
+        Ring<L::kSSlots> rg(0);
         Pl at;
         at.g = 0;
-        bool ok = true;
-        for (int t = worker; ok && t < tiles; t += p.workers) {
-            at.enter(tab, groups, t, p.tn, rank);
-            const int cols = at.width() - col0;   // of this warp that the MMA writes; <= 0: none
-            float acc[2][kCols / 8][4];
+        // W: [rows 0-15, 16-31][column group of 4][row, row + 8]; T: [column]
+        float acc[kCols];
+        const uint32_t to_issuer = kPair && !leader ? map_to_cta(dempty(0), 0) : dempty(0);
+        auto release = [&]() {   // the accumulators have been read
+            tc_fence_before();
+            __syncwarp();
+            if constexpr (kPair) arrive_cluster_if(lane == 0, to_issuer + 8u * rb.slot);
+            else arrive_if(lane == 0, to_issuer + 8u * rb.slot);
+        };
+        // The weight scales of the tile's block of rows: lane l holds those of unit
+        // u0 + l, of 32 units at a time, fetched 32 units (or an epilogue) ahead.
+        float sw[kBlk], sw_next[kBlk];
+        auto fetch = [&](const Pl& x, int u0) {
+            int nb = kPair ? x.nb - rank + g : x.nb;
+            nb = nb < p.sn ? nb : p.sn - 1;
+            const float* from = p.S + (static_cast<int64_t>(x.expert) * p.sn + nb) * p.KB;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int b = 0; b < kBlk; ++b) {
+                const int kb = (u0 + lane) * kBlk + b;
+                sw_next[b] = kb < p.KB ? __ldg(from + kb) : 0.0f;
+            }
+        };
+        auto next_scales = [&](int ku) {   // at the beginning of a unit
+            if ((ku & 31) == 0) {
 #pragma unroll
-                for (int g = 0; g < kCols / 8; ++g)
+                for (int b = 0; b < kBlk; ++b) sw[b] = sw_next[b];
+                if (ku + 32 < p.KU) fetch(at, ku + 32);
+            }
+        };
+        if (worker < tiles) {
+            at.enter(tab, worker, p.tn, rank);
+            fetch(at, 0);
+        }
+        for (int t = worker; t < tiles && !aborted(wc); t += p.workers) {
+            at.enter(tab, t, p.tn, rank);
+            auto fetch_next_tile = [&]() {
+                if (t + p.workers >= tiles) return;
+                Pl x = at;
+                x.enter(tab, t + p.workers, p.tn, rank);
+                fetch(x, 0);
+            };
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[h][g][e] = 0.0f;
-            for (int ku = 0; ku < p.KU; ++ku, rb.step(1)) {
-                ok = gemm::warp_wait(dfull(rb.slot), rb.phase, wc);
-                if (!ok) break;
-                tc_fence_after();
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+            if constexpr (kPair) {
+                // ------------------------------------------------ T: a lane is a row, with one factor a unit
+                const int nb = at.nb - rank + g;   // the columns' block of weight rows
+                uint64_t sums[kCols / 2];   // two columns each
 #pragma unroll
-                for (int b = 0; b < kBlk; ++b) {
-                    const float* f = factors_at(rb.slot) + b * NT + col0 + (lane & 3) * 4;
-                    const uint32_t tb = tl + (rb.slot * kBlk + b) * NT;
+                for (int i = 0; i < kCols / 2; ++i) sums[i] = 0ull;
+                for (int ku = 0; ku < p.KU; ++ku, rb.step(1), rg.step(1)) {
+                    next_scales(ku);
+                    wait_on(sfull(rg.slot), rg.phase, wc);
+                    const float f = __fmul_rn(scales_at(rg.slot)[(at.row0 & 3) + q * 32 + lane],
+                                              __shfl_sync(0xffffffffu, sw[0], ku & 31));
+                    arrive_if(lane == 0, sempty(rg.slot));
+                    const uint64_t f2 = twice(f);
+                    wait_on(dfull(rb.slot), rb.phase, wc);
+                    tc_fence_after();
+                    // 64 columns a load: two are on their way by turns in the two warps of
+                    // a scheduler (of 32, or the next one under the products, the sums
+                    // spilled: 530 and 572 ns a unit against 456)
 #pragma unroll
-                    for (int c = 0; c < kCols / kChunk; ++c) {
-                        if (c * kChunk >= cols) break;
-                        uint32_t v0[kChunk / 2], v1[kChunk / 2];
-                        tmem_ld_frag(tb + c * kChunk, v0);
-                        tmem_ld_frag(tb + (16u << 16) + c * kChunk, v1);
-                        float4 g4[kChunk / 16];
-#pragma unroll
-                        for (int e = 0; e < kChunk / 16; ++e)
-                            g4[e] = *reinterpret_cast<const float4*>(f + c * kChunk + e * 16);
+                    for (int c = 0; c < kCols / 64; ++c) {
+                        uint32_t x[64];
+                        tmem_ld_x64(tl + rb.slot * NT + c * 64, x);
                         tmem_wait_ld();
+                        if (c + 1 == kCols / 64) release();   // ahead of the last products
 #pragma unroll
-                        for (int e = 0; e < kChunk / 8; ++e) {
-                            const float fa = e & 1 ? g4[e / 2].z : g4[e / 2].x;
-                            const float fb = e & 1 ? g4[e / 2].w : g4[e / 2].y;
-                            float* a0 = acc[0][c * (kChunk / 8) + e];
-                            float* a1 = acc[1][c * (kChunk / 8) + e];
-                            fma2(a0[0], a0[1], v0[4 * e], v0[4 * e + 1], fa, fb);
-                            fma2(a0[2], a0[3], v0[4 * e + 2], v0[4 * e + 3], fa, fb);
-                            fma2(a1[0], a1[1], v1[4 * e], v1[4 * e + 1], fa, fb);
-                            fma2(a1[2], a1[3], v1[4 * e + 2], v1[4 * e + 3], fa, fb);
+                        for (int j = 0; j < 32; ++j) fma2(sums[c * 32 + j], x[2 * j], x[2 * j + 1], f2);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kCols / 2; ++i) {
+                    acc[2 * i] = __uint_as_float(static_cast<uint32_t>(sums[i]));
+                    acc[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(sums[i] >> 32));
+                }
+                fetch_next_tile();
+                // its columns: the 128 weight rows of block nb, in order
+                const int n0 = nb * 128;
+                const int here = at.rows - rank * 128 - q * 32;   // rows of this warp that exist
+                if (n0 >= p.N || here <= 0) continue;
+                if (p.y_type != QG_FP32 && p.y_vec) {
+                    // 32 columns at a time through the warp's shared memory (16-byte
+                    // chunks of a row exchanged so that neither side meets bank
+                    // conflicts), so that a store covers whole sectors of eight rows
+                    // (a lane's own row, 16 bytes in each of 32 rows a store: 3.6 us a tile)
+                    uint8_t* st = out + lane * 64;
+                    const int swap = (lane >> 1) & 3;
+                    const int r0 = lane >> 2, chunk = lane & 3;
+                    uint16_t* y = static_cast<uint16_t*>(p.Y) +
+                                  (static_cast<int64_t>(at.row0) + rank * 128 + q * 32 + r0) * p.ldy + n0 + chunk * 8;
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float* v = acc + c * 32 + e * 8;
+                            *reinterpret_cast<uint4*>(st + ((e ^ swap) << 4)) =
+                                make_uint4(pack_out(v[0], v[1], p.y_type), pack_out(v[2], v[3], p.y_type),
+                                           pack_out(v[4], v[5], p.y_type), pack_out(v[6], v[7], p.y_type));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 8 + r0;
+                            const uint4 w = *reinterpret_cast<const uint4*>(out + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+                            if (r < here && n0 + c * 32 + chunk * 8 < p.N)
+                                *reinterpret_cast<uint4*>(y + i * 8 * p.ldy + c * 32) = w;
+                        }
+                        __syncwarp();
+                    }
+                } else if (lane < here) {
+                    const int64_t row = static_cast<int64_t>(at.row0) + rank * 128 + q * 32 + lane;
+                    if (p.y_type == QG_FP32) {
+                        float* y = static_cast<float*>(p.Y) + row * p.ldy + n0;
+#pragma unroll
+                        for (int j = 0; j < kCols; j += 4) {
+                            if (p.y_vec) {
+                                if (n0 + j < p.N)
+                                    *reinterpret_cast<float4*>(y + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (n0 + j + e < p.N) y[j + e] = acc[j + e];
+                            }
+                        }
+                    } else {
+                        uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + n0;
+#pragma unroll
+                        for (int j = 0; j < kCols; j += 2) {
+                            const uint32_t w = pack_out(acc[j], acc[j + 1], p.y_type);
+                            if (n0 + j < p.N) y[j] = static_cast<uint16_t>(w);
+                            if (n0 + j + 1 < p.N) y[j + 1] = static_cast<uint16_t>(w >> 16);
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (kPair && !leader) mbar_arrive_cluster(map_to_cta(dempty(rb.slot), 0));
-                    else mbar_arrive(dempty(rb.slot));
-                    mbar_arrive(fempty(rb.slot));
-                }
-            }
-            if (!ok) break;
-            // ------------------------------------------------ the tile's outputs
-            const int nw = at.n0 + q * 32;          // the warp's first weight row
-            const int rows = at.rows - col0;        // of this warp's columns that exist
-            if (nw >= p.N || rows <= 0) continue;
-            const int64_t r0 = at.row0 + col0;
-            if (p.y_type == QG_FP32) {
-                float* y = static_cast<float*>(p.Y) + r0 * p.ldy + nw + (lane >> 2);
+            } else {
+            // ---------------------------------------------------- W: a lane is a weight row
+            const int cols = at.width() - g * kCols;   // of this warp that the MMA writes; <= 0: none
+            const int chunks = cols <= 0 ? 0 : cols >= kCols ? kCols / kChunk : (cols + kChunk - 1) / kChunk;
+            for (int ku = 0; ku < p.KU; ++ku, rb.step(1), rg.step(1)) {
+                next_scales(ku);
+                wait_on(sfull(rg.slot), rg.phase, wc);
+                wait_on(dfull(rb.slot), rb.phase, wc);
+                tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < kCols / 8; ++g)
+                for (int b = 0; b < kBlk; ++b) {
+                    // a column beyond the tile's rows takes whatever the slot holds
+                    const float* f = scales_at(rg.slot) + b * (L::kSRow / 4) + (at.row0 & 3) + g * kCols + (lane & 3);
+                    const float w = __shfl_sync(0xffffffffu, sw[b], ku & 31);
+                    // the second block of a last unit may lie past K: 0, whatever the slot holds
+                    const bool there = kBlk == 1 || ku * kBlk + b < p.KB;
+                    const uint32_t tb = tl + (rb.slot * kBlk + b) * NT;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = 8 * g + 2 * (lane & 3) + (e & 1);
-                        const int dn = 8 * (e >> 1);
-                        if (j < rows && nw + dn + (lane >> 2) < p.N) y[j * p.ldy + dn] = acc[e >> 2][g][e & 3];
+                    for (int c = 0; c < kCols / kChunk; ++c) {
+                        if (c >= chunks) break;
+                        uint32_t x[2][kChunk / 2];
+                        tmem_ld_frag(tb + c * kChunk, x[0]);
+                        tmem_ld_frag(tb + (16u << 16) + c * kChunk, x[1]);
+                        float ff[kChunk / 4];
+#pragma unroll
+                        for (int e = 0; e < kChunk / 4; ++e) ff[e] = f[c * kChunk + e * 4];
+                        tmem_wait_ld();
+                        if (b == kBlk - 1 && c + 1 >= chunks) release();   // ahead of the last products
+#pragma unroll
+                        for (int e = 0; e < kChunk / 4; ++e) {
+                            const float m = there ? __fmul_rn(ff[e], w) : 0.0f;
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                float* o = acc + r * (kCols / 2) + 2 * (c * (kChunk / 4) + e);
+                                fma2(o[0], o[1], x[r][2 * e], x[r][2 * e + 1], m, m);
+                            }
+                        }
                     }
-                continue;
-            }
-            // 16 bits: 16 rows of Y at a time through the warp's shared memory, as
-            // [row][32 weight rows] with the 16-byte chunks of a row exchanged so
-            // that neither side meets bank conflicts
-            const uint32_t so = smem_u32(out);
-            const uint32_t st_at = so + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
-#pragma unroll
-            for (int g = 0; g < kCols / 16; ++g) {
-                if (16 * g >= rows) break;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float* a0 = acc[0][2 * g + e];
-                    const float* a1 = acc[1][2 * g + e];
-                    stmatrix_t4(st_at + e * 512, pack_out(a0[0], a0[1], p.y_type), pack_out(a0[2], a0[3], p.y_type),
-                                pack_out(a1[0], a1[1], p.y_type), pack_out(a1[2], a1[3], p.y_type));
                 }
+                if (chunks == 0) release();
                 __syncwarp();
-                if (p.y_vec) {
+                arrive_if(lane == 0, sempty(rg.slot));   // the scales have been read, too
+            }
+            fetch_next_tile();
+            const int nw = at.n0 + q * 32;          // the warp's first weight row
+            const int rows = at.rows - g * kCols;   // of this warp's columns that exist
+            if (nw >= p.N || rows <= 0) continue;
+            {
+                const int64_t r0 = at.row0 + g * kCols;
+                // (row group r, column group j)
+                auto sum = [&](int r, int j) { return acc + r * (kCols / 2) + 2 * j; };
+                if (p.y_type == QG_FP32) {
+                    float* y = static_cast<float*>(p.Y) + r0 * p.ldy + nw + (lane >> 2);
+#pragma unroll
+                    for (int j4 = 0; j4 < kCols / 4; ++j4) {
+                        const int j = 4 * j4 + (lane & 3);
+                        if (4 * j4 >= rows) break;
+                        if (j < rows) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (nw + 8 * e + (lane >> 2) < p.N) y[j * p.ldy + 8 * e] = sum(e >> 1, j4)[e & 1];
+                        }
+                    }
+                    continue;
+                }
+                // 16 bits: 16 rows of Y at a time through the warp's shared memory, as
+                // [row][32 weight rows] with the 16-byte chunks of a row exchanged so
+                // that neither side meets bank conflicts.  Columns 2 c and 2 c + 1 of a
+                // lane's 8 x 8 matrices are rows c and c + 4 of the eight.
+                const int mrow = ((lane & 7) >> 1) + (lane & 1) * 4;
+                const uint32_t st_at = smem_u32(out) + mrow * 64 + (((lane >> 3) ^ ((mrow >> 1) & 3)) << 4);
+#pragma unroll
+                for (int j16 = 0; j16 < kCols / 16; ++j16) {
+                    if (16 * j16 >= rows) break;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = e * 8 + (lane >> 2);
-                        const uint4 x = *reinterpret_cast<const uint4*>(out + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-                        const int n = nw + (lane & 3) * 8;
-                        if (16 * g + r < rows && n < p.N)
-                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.Y) + (r0 + 16 * g + r) * p.ldy + n) = x;
+                        const float *a0 = sum(0, 4 * j16 + 2 * e), *a1 = a0 + 2;
+                        const float *b0 = sum(1, 4 * j16 + 2 * e), *b1 = b0 + 2;
+                        stmatrix_t4(st_at + e * 512, pack_out(a0[0], a1[0], p.y_type), pack_out(a0[1], a1[1], p.y_type),
+                                    pack_out(b0[0], b1[0], p.y_type), pack_out(b0[1], b1[1], p.y_type));
                     }
-                } else {
-                    const int n = nw + lane;
+                    __syncwarp();
+                    if (p.y_vec) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = e * 8 + (lane >> 2);
+                            const uint4 x =
+                                *reinterpret_cast<const uint4*>(out + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                            const int n = nw + (lane & 3) * 8;
+                            if (16 * j16 + r < rows && n < p.N)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.Y) + (r0 + 16 * j16 + r) * p.ldy + n) = x;
+                        }
+                    } else {
+                        const int n = nw + lane;
 #pragma unroll 1
-                    for (int r = 0; r < 16 && 16 * g + r < rows; ++r)
-                        if (n < p.N)
-                            static_cast<uint16_t*>(p.Y)[(r0 + 16 * g + r) * p.ldy + n] = *reinterpret_cast<const uint16_t*>(
-                                out + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+                        for (int r = 0; r < 16 && 16 * j16 + r < rows; ++r)
+                            if (n < p.N)
+                                static_cast<uint16_t*>(p.Y)[(r0 + 16 * j16 + r) * p.ldy + n] =
+                                    *reinterpret_cast<const uint16_t*>(
+                                        out + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+            }
             }
         }
     }
@@ -621,7 +862,7 @@ cudaError_t launch_grouped_nt(const GroupedArgs& a, const CUtensorMap& tmW, cons
     p.Y = a.Y;
     p.ldy = a.ldy;
     p.y_type = a.y_type;
-    p.y_vec = a.y_type != QG_FP32 && a.N % 8 == 0 && a.ldy % 8 == 0 && aligned_16(a.Y);
+    p.y_vec = a.N % 8 == 0 && a.ldy % 8 == 0 && aligned_16(a.Y);
     p.R = a.R;
     p.E = a.E;
     p.N = a.N;

@@ -17,16 +17,18 @@ struct GroupedArgs {
     void* ws;
 };
 
-// The rows of a tile (the MMA's N side) for R rows over E experts, and the CTAs
-// that work on a tile together (2: a pair with a tile of 256 weight rows).
+// The rows of a tile for R rows over E experts (more than 64: on a CTA pair, with
+// 256 weight rows).
 int grouped_tile_rows(int R, int E);
-inline int grouped_ctas(int tile_rows) { return tile_rows > 64 ? 2 : 1; }
 
 size_t grouped_workspace_bytes(int R, int E, int sms);
 
+// Activation rows of a copy (a pair's CTAs hold half of a tile's rows each).
+inline int grouped_box_rows(int tile_rows) { return tile_rows > 64 ? tile_rows / 2 : tile_rows; }
+
 // tmW: the weights as one [E * N, K] matrix of bytes, 128 x 128 boxes, 128-byte
-// swizzle; tmX: the activations ([R, K] bytes, boxes of 128 K x the tile's
-// rows that one CTA holds).
+// swizzle; tmX: the activations ([R, K] bytes, boxes of 128 K x
+// grouped_box_rows).
 cudaError_t launch_grouped(const GroupedArgs& a, const CUtensorMap& tmW, const CUtensorMap& tmX, const LaunchCtl& c,
                            cudaStream_t st);
 // Zeros in rows [0, offsets[E]) of Y: the K = 0 product.
