@@ -391,6 +391,15 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
+// x / s, rounded to nearest, from r, the rounded 1 / s: one correction of the
+// product by its remainder (Markstein's theorem; s normal, and its reciprocal, and
+// x / s of at most 448).  A division of every element took most of the kernel's
+// time (issue slots 83 % busy).
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+}
+
 constexpr int kQuantWarps = 8;
 
 template <bool kBf16, bool kGated>
@@ -440,8 +449,14 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const Q
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const float sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+        if (sc > 1e-30f) {
+            const float r = __frcp_rn(sc);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], sc);
+            for (int i = 0; i < 8; ++i) v[i] = quotient(v[i], sc, r);
+        } else {   // a reciprocal or a remainder would not be a normal number
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], sc);
+        }
         const uint2 codes = make_uint2(codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7]));
         for (int j = 0; j < places; ++j) {
             const int r = __shfl_sync(0xffffffffu, place, j);
@@ -455,15 +470,27 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const Q
 // ----------------------------------------------------------------- combination
 // A thread takes eight neighbouring columns of a token (one where the tensors
 // do not allow vectors) and sums them over the token's experts in their order.
-template <int kType>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
-    if (kType == QG_FP32) {
-        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        widen8<kType == QG_BF16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i), x);
-    }
+// Bound by memory.
+__device__ __forceinline__ uint4 load16(const void* p, int64_t byte) {
+    return *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + byte);
+}
+// The same where `there`, else zeros.  Volatile, so that the compiler leaves a
+// batch of them in front of the first use (with branches around plain loads it
+// waited for each: 374 us for 8191 x 8 x 5120).
+__device__ __forceinline__ uint4 load16_if(bool there, const void* p, int64_t byte) {
+    uint4 v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+                 "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                 "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+                 : "l"(static_cast<const uint8_t*>(p) + byte), "r"(static_cast<uint32_t>(there))
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void widen8(const uint4& a, const uint4& b, float (&x)[8]) {
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
 }
 template <int kType>
 __device__ __forceinline__ uint32_t narrow2(float a, float b) {
@@ -475,50 +502,77 @@ __device__ __forceinline__ uint32_t narrow2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-constexpr int kCombineThreads = 256;
+// A CTA takes a part of one token's columns.  The rows' loads are all on their way
+// before the first is used: eight experts' at a time, without branches between
+// them (a row that is not there reads row 0, and counts as zeros).
+constexpr int kCombineThreads = 320;
 
 template <int kType, bool kVec>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a, int pieces) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs a, int parts) {
     constexpr int kW = kVec ? 8 : 1;
+    constexpr int kLoads = kVec && kType == QG_FP32 ? 2 : 1;   // 16-byte loads of a thread's columns
     grid_dependents_launch();
     grid_dependency_wait();
-    const int64_t job = static_cast<int64_t>(blockIdx.x) * kCombineThreads + threadIdx.x;
-    const int64_t m = job / pieces;
-    if (m >= a.M) return;
-    const int64_t k0 = (job - m * pieces) * kW;
+    const int m = static_cast<int>(blockIdx.x / static_cast<unsigned>(parts));
+    const int part = static_cast<int>(blockIdx.x - static_cast<unsigned>(m) * parts);
+    const int k0 = (part * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * kW;
+    if (k0 >= a.K) return;
+    const int32_t* rows = a.rows + static_cast<int64_t>(m) * a.top_k;
+    const float* weights = a.weights + static_cast<int64_t>(m) * a.top_k;
     float acc[kW];
 #pragma unroll
     for (int i = 0; i < kW; ++i) acc[i] = 0.0f;
     for (int j0 = 0; j0 < a.top_k; j0 += 8) {
         float w[8];
-        float x[8][kW];
+        int r[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            w[j] = 0.0f;
+            const bool in = j0 + j < a.top_k;
+            r[j] = in ? rows[j0 + j] : -1;
+            w[j] = in ? weights[j0 + j] : 0.0f;
+        }
+        uint4 raw[8][kLoads];
+        float one[8];
 #pragma unroll
-            for (int i = 0; i < kW; ++i) x[j][i] = 0.0f;
-            if (j0 + j >= a.top_k) continue;
-            const int r = a.rows[m * a.top_k + j0 + j];
-            w[j] = a.weights[m * a.top_k + j0 + j];
-            if (r < 0 || r >= a.R) continue;   // no expert: zeros (a weight of NaN shows all the same)
-            if constexpr (kVec) load8<kType>(a.Y, r * a.ldy + k0, x[j]);
-            else x[j][0] = to_f32<kType>(a.Y, r * a.ldy + k0);
+        for (int j = 0; j < 8; ++j) {
+            const bool there = r[j] >= 0 && r[j] < a.R;
+            const int64_t at = (there ? r[j] : 0) * a.ldy + k0;
+            if constexpr (kVec) {
+#pragma unroll
+                for (int l = 0; l < kLoads; ++l)
+                    raw[j][l] = load16_if(there, a.Y, at * (kType == QG_FP32 ? 4 : 2) + 16 * l);
+            } else {
+                one[j] = there ? to_f32<kType>(a.Y, at) : 0.0f;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (kVec) {
+                float x[8];
+                if constexpr (kType == QG_FP32) widen8(raw[j][0], raw[j][1], x);
+                else widen8<kType == QG_BF16>(raw[j][0], x);
 #pragma unroll
-            for (int i = 0; i < kW; ++i) acc[i] = __fmaf_rn(w[j], x[j][i], acc[i]);
+                for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(w[j], x[i], acc[i]);   // a weight of NaN shows all the same
+            } else {
+                acc[0] = __fmaf_rn(w[j], one[j], acc[0]);
+            }
+        }
     }
     if (a.residual != nullptr) {
-        float x[8];
-        if constexpr (kVec) load8<kType>(a.residual, m * a.ldr + k0, x);
-        else x[0] = to_f32<kType>(a.residual, m * a.ldr + k0);
+        const int64_t at = m * a.ldr + k0;
+        if constexpr (kVec) {
+            float x[8];
+            if constexpr (kType == QG_FP32) widen8(load16(a.residual, at * 4), load16(a.residual, at * 4 + 16), x);
+            else widen8<kType == QG_BF16>(load16(a.residual, at * 2), x);
 #pragma unroll
-        for (int i = 0; i < kW; ++i) acc[i] += x[i];
+            for (int i = 0; i < 8; ++i) acc[i] += x[i];
+        } else {
+            acc[0] += to_f32<kType>(a.residual, at);
+        }
     }
     const int64_t at = m * a.ldo + k0;
     if constexpr (kVec) {
-        if (kType == QG_FP32) {
+        if constexpr (kType == QG_FP32) {
             float* o = static_cast<float*>(a.out) + at;
             *reinterpret_cast<float4*>(o) = make_float4(acc[0], acc[1], acc[2], acc[3]);
             *reinterpret_cast<float4*>(o + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -527,7 +581,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
                 make_uint4(narrow2<kType>(acc[0], acc[1]), narrow2<kType>(acc[2], acc[3]),
                            narrow2<kType>(acc[4], acc[5]), narrow2<kType>(acc[6], acc[7]));
         }
-    } else if (kType == QG_FP32) {
+    } else if constexpr (kType == QG_FP32) {
         static_cast<float*>(a.out)[at] = acc[0];
     } else {
         static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(narrow2<kType>(acc[0], 0.0f));
@@ -540,11 +594,14 @@ cudaError_t launch_combine_type(const CombineArgs& a, cudaStream_t st) {
     auto fits = [&](const void* p, int64_t ld) { return p == nullptr || (aligned_16(p) && ld * size % 16 == 0); };
     const bool vec = a.K % 8 == 0 && fits(a.Y, a.ldy) && fits(a.out, a.ldo) && fits(a.residual, a.ldr);
     const int pieces = vec ? a.K / 8 : a.K;
-    const int64_t blocks = (static_cast<int64_t>(a.M) * pieces + kCombineThreads - 1) / kCombineThreads;
+    // equal parts of a row, in whole warps
+    const int parts = (pieces + kCombineThreads - 1) / kCombineThreads;
+    const int threads = ((pieces + parts - 1) / parts + 31) / 32 * 32;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kCombineThreads, 0, st, &attr);
-    if (vec) return cudaLaunchKernelEx(&cfg, combine_kernel<kType, true>, a, pieces);
-    return cudaLaunchKernelEx(&cfg, combine_kernel<kType, false>, a, pieces);
+    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(static_cast<int64_t>(a.M) * parts),
+                                          static_cast<unsigned>(threads), 0, st, &attr);
+    if (vec) return cudaLaunchKernelEx(&cfg, combine_kernel<kType, true>, a, parts);
+    return cudaLaunchKernelEx(&cfg, combine_kernel<kType, false>, a, parts);
 }
 
 }  // namespace

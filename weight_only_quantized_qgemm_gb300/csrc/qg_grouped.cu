@@ -659,58 +659,64 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                 const int n0 = nb * 128;
                 const int here = at.rows - rank * 128 - q * 32;   // rows of this warp that exist
                 if (n0 >= p.N || here <= 0) continue;
-                if (p.y_type != QG_FP32 && p.y_vec) {
-                    // 32 columns at a time through the warp's shared memory (16-byte
-                    // chunks of a row exchanged so that neither side meets bank
-                    // conflicts), so that a store covers whole sectors of eight rows
-                    // (a lane's own row, 16 bytes in each of 32 rows a store: 3.6 us a tile)
-                    uint8_t* st = out + lane * 64;
-                    const int swap = (lane >> 1) & 3;
+                // 64 bytes of a row at a time through the warp's shared memory (16-byte
+                // chunks exchanged so that neither side meets bank conflicts), so that
+                // a store covers whole sectors of eight rows (a lane's own row, 16 bytes
+                // in each of 32 rows a store: 3.6 us a tile; this way 1.5)
+                uint8_t* st = out + lane * 64;
+                const int swap = (lane >> 1) & 3;
+                const int64_t first_row = static_cast<int64_t>(at.row0) + rank * 128 + q * 32;
+                if (p.y_type != QG_FP32) {
                     const int r0 = lane >> 2, chunk = lane & 3;
-                    uint16_t* y = static_cast<uint16_t*>(p.Y) +
-                                  (static_cast<int64_t>(at.row0) + rank * 128 + q * 32 + r0) * p.ldy + n0 + chunk * 8;
+                    uint16_t* y = static_cast<uint16_t*>(p.Y) + first_row * p.ldy + n0;
 #pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) {
+                    for (int c = 0; c < kCols; c += 32) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float* v = acc + c * 32 + e * 8;
+                            const float* v = acc + c + e * 8;
                             *reinterpret_cast<uint4*>(st + ((e ^ swap) << 4)) =
                                 make_uint4(pack_out(v[0], v[1], p.y_type), pack_out(v[2], v[3], p.y_type),
                                            pack_out(v[4], v[5], p.y_type), pack_out(v[6], v[7], p.y_type));
                         }
                         __syncwarp();
+                        if (p.y_vec) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = i * 8 + r0;
-                            const uint4 w = *reinterpret_cast<const uint4*>(out + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
-                            if (r < here && n0 + c * 32 + chunk * 8 < p.N)
-                                *reinterpret_cast<uint4*>(y + i * 8 * p.ldy + c * 32) = w;
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = i * 8 + r0;
+                                const uint4 w =
+                                    *reinterpret_cast<const uint4*>(out + r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+                                if (r < here && n0 + c + chunk * 8 < p.N)
+                                    *reinterpret_cast<uint4*>(y + r * p.ldy + c + chunk * 8) = w;
+                            }
+                        } else if (n0 + c + lane < p.N) {
+#pragma unroll 4
+                            for (int r = 0; r < 32; ++r)
+                                if (r < here)
+                                    y[r * p.ldy + c + lane] = *reinterpret_cast<const uint16_t*>(
+                                        out + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
                         }
                         __syncwarp();
                     }
-                } else if (lane < here) {
-                    const int64_t row = static_cast<int64_t>(at.row0) + rank * 128 + q * 32 + lane;
-                    if (p.y_type == QG_FP32) {
-                        float* y = static_cast<float*>(p.Y) + row * p.ldy + n0;
+                } else {
+                    const int r0 = lane >> 4, col = lane & 15;
+                    float* y = static_cast<float*>(p.Y) + first_row * p.ldy + n0;
 #pragma unroll
-                        for (int j = 0; j < kCols; j += 4) {
-                            if (p.y_vec) {
-                                if (n0 + j < p.N)
-                                    *reinterpret_cast<float4*>(y + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-                            } else {
+                    for (int c = 0; c < kCols; c += 16) {
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (n0 + j + e < p.N) y[j + e] = acc[j + e];
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float4*>(st + ((e ^ swap) << 4)) =
+                                make_float4(acc[c + 4 * e], acc[c + 4 * e + 1], acc[c + 4 * e + 2], acc[c + 4 * e + 3]);
+                        __syncwarp();
+                        if (n0 + c + col < p.N) {
+#pragma unroll 4
+                            for (int i = 0; i < 16; ++i) {
+                                const int r = 2 * i + r0;
+                                if (r < here)
+                                    y[r * p.ldy + c + col] = *reinterpret_cast<const float*>(
+                                        out + r * 64 + (((col >> 2) ^ ((r >> 1) & 3)) << 4) + (col & 3) * 4);
                             }
                         }
-                    } else {
-                        uint16_t* y = static_cast<uint16_t*>(p.Y) + row * p.ldy + n0;
-#pragma unroll
-                        for (int j = 0; j < kCols; j += 2) {
-                            const uint32_t w = pack_out(acc[j], acc[j + 1], p.y_type);
-                            if (n0 + j < p.N) y[j] = static_cast<uint16_t>(w);
-                            if (n0 + j + 1 < p.N) y[j + 1] = static_cast<uint16_t>(w >> 16);
-                        }
+                        __syncwarp();
                     }
                 }
             } else {
