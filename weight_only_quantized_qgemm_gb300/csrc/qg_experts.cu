@@ -401,41 +401,47 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 }
 
 constexpr int kQuantWarps = 8;
+constexpr int kQuantCtas = 6;   // per SM
 
+// Resident warps walk over jobs (256 columns of a row), the next job's loads on
+// their way while this one's codes are worked out.
 template <bool kBf16, bool kGated>
-__global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const QuantizeRowsArgs a, int steps, int spans) {
+__global__ void __launch_bounds__(kQuantWarps * 32, kQuantCtas)
+    quantize_rows_kernel(const QuantizeRowsArgs a, int steps) {
     grid_dependents_launch();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    // a span: `steps` steps of 256 columns of one row
-    const int64_t job = static_cast<int64_t>(blockIdx.x) * kQuantWarps + (threadIdx.x >> 5);
-    const int64_t m = job / spans;
     int live = a.M;
     if (a.num_rows != nullptr) {
         const int n = __ldcg(a.num_rows);
         live = n < live ? n : live;
     }
-    if (m >= live) return;
-    const int span = static_cast<int>(job - m * spans);
-    const uint16_t* x = static_cast<const uint16_t*>(a.X) + m * a.ldx;
-    // the row's places: lane j holds the j-th (out of range: none)
-    int place = lane == 0 ? static_cast<int>(m) : -1;
-    int places = 1;
-    if (a.rows != nullptr) {
-        places = a.top_k;
-        place = lane < places ? __ldcg(a.rows + m * a.top_k + lane) : -1;
-    }
-    if (place >= a.out_rows) place = -1;
-    for (int s = 0; s < steps; ++s) {
-        const int k0 = (span * steps + s) * 256 + lane * 8;
-        if (k0 - lane * 8 >= a.K) break;
-        const bool in = k0 < a.K;   // K is a multiple of 16: all eight or none
-        float v[8];
-        uint4 w = make_uint4(0u, 0u, 0u, 0u), w2 = w;
-        if (in) {
-            w = *reinterpret_cast<const uint4*>(x + k0);
-            if (kGated) w2 = *reinterpret_cast<const uint4*>(x + a.K + k0);
+    const unsigned warps = gridDim.x * kQuantWarps;
+    const unsigned first = blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
+    // (row, step of the row) of a job, stepped without divisions
+    const int dm = static_cast<int>(warps / static_cast<unsigned>(steps));
+    const int ds = static_cast<int>(warps - static_cast<unsigned>(dm) * steps);
+    int m = static_cast<int>(first / static_cast<unsigned>(steps));
+    int s = static_cast<int>(first - static_cast<unsigned>(m) * steps);
+    const int places = a.rows != nullptr ? a.top_k : 1;
+    uint4 w, w2;
+    int place;   // lane j holds the row's j-th place (out of range: none)
+    auto fetch = [&]() {
+        w = w2 = make_uint4(0u, 0u, 0u, 0u);
+        place = -1;
+        if (m >= live) return;
+        const int k0 = s * 256 + lane * 8;
+        const uint16_t* x = static_cast<const uint16_t*>(a.X) + m * a.ldx + k0;
+        if (k0 < a.K) {   // K is a multiple of 16: all eight or none
+            w = *reinterpret_cast<const uint4*>(x);
+            if (kGated) w2 = *reinterpret_cast<const uint4*>(x + a.K);
         }
+        if (a.rows == nullptr) place = m;
+        else if (lane < places) place = __ldcg(a.rows + static_cast<int64_t>(m) * places + lane);
+    };
+    fetch();
+    while (m < live) {
+        float v[8];
         widen8<kBf16>(w, v);
         if (kGated) {
             float u[8];
@@ -443,6 +449,15 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const Q
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = gate(v[i], u[i]);
         }
+        const int k0 = s * 256 + lane * 8;
+        const int to = place < a.out_rows ? place : -1;
+        m += dm;
+        s += ds;
+        if (s >= steps) {
+            s -= steps;
+            ++m;
+        }
+        fetch();
         float amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
@@ -458,11 +473,13 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_rows_kernel(const Q
             for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], sc);
         }
         const uint2 codes = make_uint2(codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7]));
+        uint8_t* q = a.Xq + k0;
+        float* scale = a.Sx + (k0 >> 7) * a.ldsx;
         for (int j = 0; j < places; ++j) {
-            const int r = __shfl_sync(0xffffffffu, place, j);
-            if (r < 0 || !in) continue;
-            *reinterpret_cast<uint2*>(a.Xq + r * a.ldxq + k0) = codes;
-            if ((lane & 15) == 0) a.Sx[(k0 >> 7) * a.ldsx + r] = sc;
+            const int r = __shfl_sync(0xffffffffu, to, j);
+            if (r < 0 || k0 >= a.K) continue;
+            *reinterpret_cast<uint2*>(q + r * a.ldxq) = codes;
+            if ((lane & 15) == 0) scale[r] = sc;
         }
     }
 }
@@ -621,17 +638,18 @@ cudaError_t launch_route(const RouteArgs& a, const LaunchCtl& c, cudaStream_t st
 }
 
 cudaError_t launch_quantize_rows(const QuantizeRowsArgs& a, const LaunchCtl& c, cudaStream_t st) {
-    const int all = (a.K + 255) / 256;   // steps of a row
-    const int steps = 2;
-    const int spans = (all + steps - 1) / steps;
-    const int64_t blocks = (static_cast<int64_t>(a.M) * spans + kQuantWarps - 1) / kQuantWarps;
+    const int steps = (a.K + 255) / 256;   // of a row
+    const int64_t jobs = static_cast<int64_t>(a.M) * steps;
+    const int64_t most = static_cast<int64_t>(c.num_sms) * kQuantCtas;
+    const int64_t blocks = (jobs + kQuantWarps - 1) / kQuantWarps;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(blocks), kQuantWarps * 32, 0, st, &attr);
+    const cudaLaunchConfig_t cfg =
+        config(static_cast<unsigned>(blocks < most ? blocks : most), kQuantWarps * 32, 0, st, &attr);
     if (a.x_type == QG_BF16)
-        return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, true>, a, steps, spans)
-                       : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, false>, a, steps, spans);
-    return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, true>, a, steps, spans)
-                   : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, false>, a, steps, spans);
+        return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, true>, a, steps)
+                       : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, false>, a, steps);
+    return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, true>, a, steps)
+                   : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, false>, a, steps);
 }
 
 cudaError_t launch_combine(const CombineArgs& a, const LaunchCtl& c, cudaStream_t st) {

@@ -12,14 +12,23 @@
 // last token is that of row n.
 //
 // A cluster of CTAs takes a sequence, each CTA a slice of the vocabulary:
-//   1. over all rows, one pass: the maximum and the sum of exponentials of the
-//      slice (greedy: the largest logit and its index), a warp at a time on a
+//   1. over all rows, one pass: the sum of exponentials of the slice about a
+//      reference (greedy: the largest logit and its index), a warp at a time on a
 //      stretch of a row; the CTAs' parts are read through distributed shared
 //      memory by all of them, so that each knows n;
-//   2. the race over the slice of row n (read again, from L2 in the main);
+//   2. the race over the slice of row n (read again, from L2 in the main).  Most
+//      tokens are out by one exponential: probability over noise below the best
+//      so far;
 //   3. the first CTA compares the winners.
 // All sums have a fixed order.  Bound by memory: every logit is read once, and two
 // rows of a sequence a second time with the noise.
+//
+// The sums: with L = log2 e and c a whole number that follows the largest x L from
+// below (by at most 32), s = sum 2^(x L - c): a term is one fma with one rounding,
+// one ex2 and one addition, and c moves only when a term would pass 2^32, so that
+// no maximum is carried along.  Where c is no exact number near x L (beyond
+// 2^23: logits of +-6e6, among them rows of a type's lowest value) or nothing is
+// left, the row is done again about its maximum.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,7 +39,8 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostRows = 2 * QG_MAX_DRAFTS + 1;
 constexpr int kMostCtas = 16;
@@ -49,6 +59,10 @@ struct Elem<QG_BF16> {
         x[0] = __uint_as_float(w << 16);
         x[1] = __uint_as_float(w & 0xFFFF0000u);
     }
+    static __device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        wide(w.x, x), wide(w.y, x + 2), wide(w.z, x + 4), wide(w.w, x + 6);
+    }
 };
 template <>
 struct Elem<QG_FP16> {
@@ -61,12 +75,21 @@ struct Elem<QG_FP16> {
         x[0] = f.x;
         x[1] = f.y;
     }
+    static __device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        wide(w.x, x), wide(w.y, x + 2), wide(w.z, x + 4), wide(w.w, x + 6);
+    }
 };
 template <>
 struct Elem<QG_FP32> {
     static constexpr int kSize = 4;
     static __device__ __forceinline__ float at(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
     static __device__ __forceinline__ void wide(uint32_t w, float* x) { x[0] = __uint_as_float(w); }
+    static __device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
+        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
 };
 
 __device__ __forceinline__ float ex2(float t) {
@@ -123,13 +146,45 @@ __device__ __forceinline__ void see(Part& p, const float (&x)[kCount]) {
     p.s = s;
 }
 
+// A part of a row about c: s = sum 2^(x L - c).
+constexpr float kNoRef = -1e30f;      // nothing seen
+constexpr float kMostRef = 8388608.0f;
+struct Sum {
+    float c, s;
+};
+__device__ __forceinline__ Sum join(Sum a, Sum b) {
+    const float c = fmaxf(a.c, b.c);
+    return Sum{c, a.s * ex2(a.c - c) + b.s * ex2(b.c - c)};
+}
+template <int kCount>
+__device__ __forceinline__ void see(Sum& p, const float (&x)[kCount]) {
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i < kCount; ++i) m = fmaxf(m, x[i]);
+    if (m * kLog2e > p.c + 32.0f) {
+        const float c = ceilf(m * kLog2e);
+        p.s *= ex2(p.c - c);
+        p.c = c;
+    }
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) s += ex2(__fmaf_rn(x[i], kLog2e, -p.c));
+    p.s += s;
+}
+// The same about the maximum m' = c ln 2 (rounded): s' = s 2^(c - m' L).
+__device__ __forceinline__ Part about_max(Sum a) {
+    const float m = a.c * 0.6931471806f;
+    return Part{m, a.s * ex2(-__fmaf_rn(m, kLog2e, -a.c))};
+}
+
 // The slice [v0, v1) of a row, by one warp: scalars up to the first 16-byte
-// boundary and behind the last, vectors in between.
-template <int kType, bool kGreedy>
-__device__ __forceinline__ Part scan_row(const void* row, int v0, int v1, int lane) {
+// boundary and behind the last, vectors in between.  kHow: kSum, kMax (about the
+// maximum) or kGreedy.
+constexpr int kSum = 0, kMax = 1, kGreedyScan = 2;
+template <int kType, int kHow, class State>
+__device__ __forceinline__ State scan_row(const void* row, int v0, int v1, int lane, State p) {
     using El = Elem<kType>;
     constexpr int kVec = 16 / El::kSize;
-    Part p{-INFINITY, kGreedy ? __uint_as_float(0x7FFFFFFFu) : 0.0f};
     const uint8_t* base = static_cast<const uint8_t*>(row);
     const uintptr_t first = reinterpret_cast<uintptr_t>(base) + static_cast<int64_t>(v0) * El::kSize;
     const int head = static_cast<int>(((16 - (first & 15u)) & 15u) / El::kSize);
@@ -138,33 +193,48 @@ __device__ __forceinline__ Part scan_row(const void* row, int v0, int v1, int la
     const int a1 = a0 + nvec * kVec;
     auto one = [&](int v) {
         const float x[1] = {El::at(row, v)};
-        if constexpr (kGreedy) see_greedy(p, x[0], v);
+        if constexpr (kHow == kGreedyScan) see_greedy(p, x[0], v);
         else see(p, x);
     };
     for (int v = v0 + lane; v < a0; v += 32) one(v);
     const uint4* vec = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(a0) * El::kSize);
+    auto take = [&](const uint4& w, int i) {
+        float x[kVec];
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) El::wide(ws[e], x + e * (kVec / 4));
+        if constexpr (kHow == kGreedyScan) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) see_greedy(p, x[e], a0 + i * kVec + e);
+        } else {
+            see(p, x);
+        }
+    };
     constexpr int kU = 4;   // loads in flight
-    for (int i = lane; i < nvec; i += 32 * kU) {
+    int i = lane;
+    for (; i + 32 * (kU - 1) < nvec; i += 32 * kU) {
         uint4 w[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-            if (i + 32 * u < nvec) w[u] = vec[i + 32 * u];
+        for (int u = 0; u < kU; ++u) w[u] = __ldcg(vec + i + 32 * u);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (i + 32 * u >= nvec) break;
-            float x[kVec];
-            const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) El::wide(ws[e], x + e * (kVec / 4));
-            if constexpr (kGreedy) {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) see_greedy(p, x[e], a0 + (i + 32 * u) * kVec + e);
-            } else {
-                see(p, x);
-            }
-        }
+        for (int u = 0; u < kU; ++u) take(w[u], i + 32 * u);
     }
+    for (; i < nvec; i += 32) take(vec[i], i);
     for (int v = a1 + lane; v < v1; v += 32) one(v);
+    return p;
+}
+template <int kType>
+__device__ __forceinline__ Sum scan_sum(const void* row, int v0, int v1, int lane) {
+    Sum p = scan_row<kType, kSum>(row, v0, v1, lane, Sum{kNoRef, 0.0f});
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        p = join(p, Sum{__shfl_xor_sync(0xffffffffu, p.c, o), __shfl_xor_sync(0xffffffffu, p.s, o)});
+    return p;
+}
+template <int kType, bool kGreedy>
+__device__ __forceinline__ Part scan_max(const void* row, int v0, int v1, int lane) {
+    Part p = scan_row<kType, kGreedy ? kGreedyScan : kMax>(
+        row, v0, v1, lane, Part{-INFINITY, kGreedy ? __uint_as_float(0x7FFFFFFFu) : 0.0f});
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const Part q{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)};
@@ -189,14 +259,14 @@ __device__ __forceinline__ Best better(Best a, Best b) {
 }
 
 template <int kType, bool kGreedy>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const VerifyArgs a, int ctas) {
     using El = Elem<kType>;
     __shared__ Part parts[kMostRows][kParts];
     __shared__ Part mine[kMostRows];        // this CTA's slice
     __shared__ Part all[kMostRows];         // the whole rows
-    __shared__ Best best[2][kWarps];        // of max(p - q, 0), of p
-    __shared__ Best winner[2];
-    __shared__ int kept;
+    __shared__ Best best[kWarps];
+    __shared__ Best winner, winner_p;       // of max(p - q, 0), or of p
+    __shared__ int kept, odd_rows;
     grid_dependents_launch();
     grid_dependency_wait();
     const int warp = threadIdx.x >> 5;
@@ -224,35 +294,83 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, in
     int v1 = cut(a.V, rank + 1, ctas);
     if (v1 > a.V) v1 = a.V;
     const int slice = v1 - v0;
-    int pieces = slice / 4096;
+    int pieces = slice / 2048;
     pieces = pieces < 1 ? 1 : pieces > kParts ? kParts : pieces;
-    for (int i = warp; i < rows * pieces; i += kWarps) {
-        const int r = i / pieces, s = i - r * pieces;
-        int s1 = v0 + cut(slice, s + 1, pieces);
+    auto stretch = [&](int i, int& r, int& piece, int& s0, int& s1) {
+        r = i / pieces;
+        piece = i - r * pieces;
+        s0 = v0 + cut(slice, piece, pieces);
+        s1 = v0 + cut(slice, piece + 1, pieces);
         if (s1 > v1) s1 = v1;
-        const Part p = scan_row<kType, kGreedy>(row_at(r), v0 + cut(slice, s, pieces), s1, lane);
-        if (lane == 0) parts[r][s] = p;
+    };
+    // the CTAs' parts of a row, in their order
+    auto of_all = [&](int r, auto joined) {
+        Part p = ctas > 1 ? Part{ld_cluster(&mine[r].m, 0), ld_cluster(&mine[r].s, 0)} : mine[r];
+        for (int c = 1; c < ctas; ++c)
+            p = joined(p, Part{ld_cluster(&mine[r].m, static_cast<uint32_t>(c)), ld_cluster(&mine[r].s, static_cast<uint32_t>(c))});
+        return p;
+    };
+    auto join_sums = [](Part a, Part b) {
+        const Sum s = join(Sum{a.m, a.s}, Sum{b.m, b.s});
+        return Part{s.c, s.s};
+    };
+    auto join_maxima = [](Part a, Part b) { return kGreedy ? join_greedy(a, b) : join(a, b); };
+    if (threadIdx.x == 0) odd_rows = 0;
+    for (int i = warp; i < rows * pieces; i += kWarps) {
+        int r, piece, s0, s1;
+        stretch(i, r, piece, s0, s1);
+        Part p;
+        if constexpr (kGreedy) {
+            p = scan_max<kType, true>(row_at(r), s0, s1, lane);
+        } else {
+            const Sum q = scan_sum<kType>(row_at(r), s0, s1, lane);
+            p = Part{q.c, q.s};
+        }
+        if (lane == 0) parts[r][piece] = p;
     }
     __syncthreads();
     for (int r = threadIdx.x; r < rows; r += kThreads) {
         Part p = parts[r][0];
-        for (int s = 1; s < pieces; ++s) p = kGreedy ? join_greedy(p, parts[r][s]) : join(p, parts[r][s]);
+        for (int i = 1; i < pieces; ++i) p = kGreedy ? join_greedy(p, parts[r][i]) : join_sums(p, parts[r][i]);
         mine[r] = p;
     }
     __syncthreads();
     cluster_sync_all();
     for (int r = threadIdx.x; r < rows; r += kThreads) {
-        Part p = mine[r];
-        if (ctas > 1) {
-            p = Part{ld_cluster(&mine[r].m, 0), ld_cluster(&mine[r].s, 0)};
-            for (int c = 1; c < ctas; ++c) {
-                const Part o{ld_cluster(&mine[r].m, static_cast<uint32_t>(c)), ld_cluster(&mine[r].s, static_cast<uint32_t>(c))};
-                p = kGreedy ? join_greedy(p, o) : join(p, o);
-            }
+        if constexpr (kGreedy) {
+            all[r] = of_all(r, join_maxima);
+        } else {
+            const Part p = of_all(r, join_sums);
+            const bool fine = fabsf(p.m) <= kMostRef && p.s < INFINITY;
+            all[r] = fine ? about_max(Sum{p.m, p.s}) : Part{0.0f, -1.0f};
+            if (!fine) atomicOr(&odd_rows, 1);
         }
-        all[r] = p;
     }
     __syncthreads();
+    if constexpr (!kGreedy) {
+        if (odd_rows) {   // the same in all CTAs of the cluster
+            cluster_sync_all();   // every part has been read
+            for (int i = warp; i < rows * pieces; i += kWarps) {
+                int r, piece, s0, s1;
+                stretch(i, r, piece, s0, s1);
+                if (all[r].s >= 0.0f) continue;
+                const Part p = scan_max<kType, false>(row_at(r), s0, s1, lane);
+                if (lane == 0) parts[r][piece] = p;
+            }
+            __syncthreads();
+            for (int r = threadIdx.x; r < rows; r += kThreads) {
+                if (all[r].s >= 0.0f) continue;
+                Part p = parts[r][0];
+                for (int i = 1; i < pieces; ++i) p = join(p, parts[r][i]);
+                mine[r] = p;
+            }
+            __syncthreads();
+            cluster_sync_all();
+            for (int r = threadIdx.x; r < rows; r += kThreads)
+                if (!(all[r].s >= 0.0f)) all[r] = of_all(r, join_maxima);
+            __syncthreads();
+        }
+    }
     // which drafts are kept: a lane a draft
     if (warp == 0) {
         bool keep = false;
@@ -277,6 +395,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, in
     }
     __syncthreads();
     const int n = kept;
+    int64_t last = -1;   // the token that follows
     if constexpr (!kGreedy) {
         const Part t = all[n];
         const void* trow = row_at(n);
@@ -286,74 +405,88 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyArgs a, in
         const int64_t d = drafted && !sampled ? a.tokens[b * a.ldt + n] : -1;   // the certain draft
         const float pr = 1.0f / t.s, qr = 1.0f / s.s;
         const float* noise = a.noise + b * a.ldn;
-        // [0]: max(p - q, 0); [1]: p, for a row where that is 0 everywhere
-        Best top[2] = {{0.0f, 0x7FFFFFFF}, {0.0f, 0x7FFFFFFF}};
-        auto enter = [&](int v, float x, float y, float e) {
-            const float p = exp_near(x - t.m) * pr;
-            float q = 0.0f;
-            if (drow != nullptr) q = exp_near(y - s.m) * qr;
-            else if (v == d) q = 1.0f;
-            const float w = p - q;
-            if (w > 0.0f && w > top[0].ratio * e * 0.999999f) {
-                const float ratio = __fdiv_rn(w, e);
-                if (ratio > top[0].ratio) top[0] = Best{ratio, v};
-            }
-            if (drafted && p > 0.0f && p > top[1].ratio * e * 0.999999f) {
-                const float ratio = __fdiv_rn(p, e);
-                if (ratio > top[1].ratio) top[1] = Best{ratio, v};
-            }
-        };
-        // indices ascend in a thread, so the first of equals stays
-        constexpr int kU = 4;
-        for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads * kU) {
-            float x[kU], y[kU], e[kU];
+        const float cut_off = pr * 1.0001f;   // the exponential below is good to 2^-20
+        // The race of max(p - q, 0), or of p (for a row where that is 0 everywhere).
+        auto race = [&](bool with_q, Best& result) {
+            Best top{0.0f, 0x7FFFFFFF};
+            // indices ascend in a thread, so the first of equals stays
+            auto enter = [&](int v, float x, float y, float e) {
+                if (!(ex2((x - t.m) * kLog2e) * cut_off > top.ratio * e * 0.9999f)) return;
+                const float p = exp_near(x - t.m) * pr;
+                float q = 0.0f;
+                if (with_q) {
+                    if (drow != nullptr) q = exp_near(y - s.m) * qr;
+                    else if (v == d) q = 1.0f;
+                }
+                const float w = p - q;
+                if (w > 0.0f) {
+                    const float ratio = __fdiv_rn(w, e);
+                    if (ratio > top.ratio) top = Best{ratio, v};
+                }
+            };
+            constexpr int kVec = 8;
+            const bool vectors = ((reinterpret_cast<uintptr_t>(trow) | reinterpret_cast<uintptr_t>(drow) |
+                                   reinterpret_cast<uintptr_t>(noise)) & 15u) == 0;
+            int v_done = v0;
+            if (vectors) {   // slices begin at multiples of 32
+                const int nvec = (v1 - v0) / kVec;
+                v_done = v0 + nvec * kVec;
+                for (int i = threadIdx.x; i < nvec; i += kThreads) {
+                    const int v = v0 + i * kVec;
+                    float x[kVec], y[kVec], e[kVec];
+                    El::load8(trow, v, x);
+                    if (with_q && drow != nullptr) El::load8(drow, v, y);
+                    Elem<QG_FP32>::load8(noise, v, e);
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int w = v + kThreads * u;
-                x[u] = y[u] = e[u] = 0.0f;
-                if (w >= v1) continue;
-                x[u] = El::at(trow, w);
-                if (drow != nullptr) y[u] = El::at(drow, w);
-                e[u] = noise[w];
-            }
-#pragma unroll
-            for (int u = 0; u < kU; ++u)
-                if (v + kThreads * u < v1) enter(v + kThreads * u, x[u], y[u], e[u]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                top[i] = better(top[i], Best{__shfl_xor_sync(0xffffffffu, top[i].ratio, o),
-                                             __shfl_xor_sync(0xffffffffu, top[i].v, o)});
-            if (lane == 0) best[i][warp] = top[i];
-        }
-        __syncthreads();
-        if (threadIdx.x < 2) {
-            Best w = best[threadIdx.x][0];
-            for (int i = 1; i < kWarps; ++i) w = better(w, best[threadIdx.x][i]);
-            winner[threadIdx.x] = w;
-        }
-        __syncthreads();
-        cluster_sync_all();
-    }
-    if (rank == 0) {
-        int64_t last = -1;
-        if constexpr (kGreedy) {
-            if (all[n].m > -INFINITY) last = static_cast<int64_t>(__float_as_uint(all[n].s));
-        } else if (threadIdx.x <= static_cast<unsigned>(a.G)) {
-            Best w[2];
-            for (int i = 0; i < 2; ++i) {
-                w[i] = winner[i];
-                for (int c = 1; c < ctas; ++c) {
-                    const float ratio = ld_cluster(&winner[i].ratio, static_cast<uint32_t>(c));
-                    const float v = ld_cluster(reinterpret_cast<const float*>(&winner[i].v), static_cast<uint32_t>(c));
-                    w[i] = better(w[i], Best{ratio, static_cast<int>(__float_as_uint(v))});
+                    for (int j = 0; j < kVec; ++j) enter(v + j, x[j], drow != nullptr ? y[j] : 0.0f, e[j]);
                 }
             }
-            const Best u = w[0].v != 0x7FFFFFFF ? w[0] : w[1];
-            if (u.v != 0x7FFFFFFF) last = u.v;
-        }
+            constexpr int kU = 4;
+            for (int v = v_done + static_cast<int>(threadIdx.x); v < v1; v += kThreads * kU) {
+                float x[kU], y[kU], e[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int w = v + kThreads * u < v1 ? v + kThreads * u : v;
+                    x[u] = El::at(trow, w);
+                    y[u] = with_q && drow != nullptr ? El::at(drow, w) : 0.0f;
+                    e[u] = noise[w];
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (v + kThreads * u < v1) enter(v + kThreads * u, x[u], y[u], e[u]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = better(top, Best{__shfl_xor_sync(0xffffffffu, top.ratio, o), __shfl_xor_sync(0xffffffffu, top.v, o)});
+            __syncthreads();   // `best` may still be read from the race before
+            if (lane == 0) best[warp] = top;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                Best w = best[0];
+                for (int i = 1; i < kWarps; ++i) w = better(w, best[i]);
+                result = w;
+            }
+            __syncthreads();
+            cluster_sync_all();
+            // of all CTAs, known to each
+            Best w = result;
+            if (ctas > 1 && lane < ctas) {
+                w.ratio = ld_cluster(&result.ratio, static_cast<uint32_t>(lane));
+                w.v = static_cast<int>(
+                    __float_as_uint(ld_cluster(reinterpret_cast<const float*>(&result.v), static_cast<uint32_t>(lane))));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                w = better(w, Best{__shfl_xor_sync(0xffffffffu, w.ratio, o), __shfl_xor_sync(0xffffffffu, w.v, o)});
+            return Best{__shfl_sync(0xffffffffu, w.ratio, 0), __shfl_sync(0xffffffffu, w.v, 0)};
+        };
+        Best w = race(drafted, winner);
+        if (drafted && w.v == 0x7FFFFFFF) w = race(false, winner_p);
+        if (w.v != 0x7FFFFFFF) last = w.v;
+    }
+    if (rank == 0) {
+        if constexpr (kGreedy)
+            if (all[n].m > -INFINITY) last = static_cast<int64_t>(__float_as_uint(all[n].s));
         const int j = static_cast<int>(threadIdx.x);
         if (j <= a.G) a.out[static_cast<int64_t>(b) * (a.G + 1) + j] = j < n ? a.tokens[b * a.ldt + j] : j == n ? last : -1;
         if (j == 0) a.accepted[b] = n;
@@ -366,9 +499,9 @@ cudaError_t launch(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
     static std::atomic<uint64_t> wide{0};
     cudaError_t e = set_once(wide, verify_kernel<kType, kGreedy>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    // CTAs of a sequence: about two for every SM, none with less than 2048 of the vocabulary
+    // CTAs of a sequence: as many as run at once, none with less than 2048 of the vocabulary
     int ctas = kMostCtas;
-    while (ctas > 1 && (static_cast<int64_t>(ctas) * a.B > 2 * c.num_sms || a.V / ctas < 2048)) ctas /= 2;
+    while (ctas > 1 && (static_cast<int64_t>(ctas) * a.B > kCtasPerSm * c.num_sms || a.V / ctas < 2048)) ctas /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B * ctas));
     cfg.blockDim = dim3(kThreads);
