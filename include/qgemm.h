@@ -480,17 +480,12 @@ qg_status qg_quantize_rows_e4m3(const void *X, int x_type, int64_t ldx, int gate
  *            are taken as the nearest that are)
  *   Y        device, QG_BF16, QG_FP16 or QG_FP32 [R, ldy], ldy >= N
  *   R, E, N, K   0 <= R <= 2^24, 1 <= E <= QG_MAX_EXPERTS, E N < 2^31, K % 16 == 0
- *   workspace    of qg_workspace_bytes_grouped(R, E) bytes, 256-byte aligned,
- *                zero-filled before its first use and left so that the next call
- *                of any shape can use it; its layout is that of this kind alone
- * Neither the tiling nor the split of the work depends on anything but R, E, N,
- * K and offsets: equal calls give equal bits.
+ * Tiles are not split along K, so that no workspace is needed and a row's result
+ * does not depend on the other rows' values.
  */
-size_t qg_workspace_bytes_grouped(int R, int E);
 qg_status qgemm_w8a8_grouped(const uint8_t *Xq, int64_t ldxq, const float *X_scale, int64_t ldsx, const uint8_t *W,
                              const float *W_scale, const int32_t *offsets, void *Y, int y_type, int64_t ldy, int R,
-                             int E, int N, int K, void *workspace, size_t workspace_bytes,
-                             struct CUstream_st *stream);
+                             int E, int N, int K, struct CUstream_st *stream);
 
 /*
  * The experts' results back to the tokens:
@@ -535,14 +530,18 @@ qg_status qg_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *ro
  *   lengths     device, int32 [B] (cut to 0 .. G), or NULL: all G
  *   accepted    device, int32 [B];  tokens_out  device, int64 [B, G + 1]
  *   B, G, V     0 <= B <= 65536, 0 <= G <= QG_MAX_DRAFTS, 1 <= V <= 2^30
+ *   workspace   of qg_verify_drafts_workspace_bytes(B, G, V) bytes (0 for few
+ *               sequences), 16-byte aligned, scratch (nothing is expected in it)
  * A row with a NaN or +inf (greedy: a NaN is never the largest), or with nothing
  * but -inf, keeps no draft, and the token drawn from it is -1.  Rows behind a
  * sequence's length are not read.
  */
+size_t qg_verify_drafts_workspace_bytes(int B, int G, int V);
 qg_status qg_verify_drafts(const void *target, int type, int64_t t_seq, int64_t t_row, const void *draft,
                            int64_t d_seq, int64_t d_row, const int64_t *tokens, int64_t ldt, const float *uniform,
                            int64_t ldu, const float *noise, int64_t ldn, const int32_t *lengths, int32_t *accepted,
-                           int64_t *tokens_out, int B, int G, int V, struct CUstream_st *stream);
+                           int64_t *tokens_out, int B, int G, int V, void *workspace, size_t workspace_bytes,
+                           struct CUstream_st *stream);
 
 /*
  * Packed size, in bytes, of an [N, K] 3-bit code matrix:

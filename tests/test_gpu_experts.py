@@ -257,7 +257,7 @@ def grouped_reference(Xq, Xs, W, Ws, off):
     return y, mass
 
 
-def check_grouped(q, sizes, N, K, dtype, seed=1, extra=0, first=0, pad_y=0, pad_x=0, workspace=None):
+def check_grouped(q, sizes, N, K, dtype, seed=1, extra=0, first=0, pad_y=0, pad_x=0):
     Xq, Xs, W, Ws, off = grouped_problem(sizes, N, K, seed, extra, first)
     R = Xq.shape[0]
     if pad_x:
@@ -267,7 +267,7 @@ def check_grouped(q, sizes, N, K, dtype, seed=1, extra=0, first=0, pad_y=0, pad_
     else:
         x = Xq
     Y = torch.full((R, N + pad_y), -1234.0, dtype=DTYPES[dtype], device="cuda")
-    q.qgemm_w8a8_grouped(x, Xs, W, Ws, off, Y=Y[:, :N], workspace=workspace)
+    q.qgemm_w8a8_grouped(x, Xs, W, Ws, off, Y=Y[:, :N])
     assert q.last_device_status() == 0
     ref, mass = grouped_reference(Xq, Xs, W, Ws, off)
     live = ~torch.isnan(ref[:, 0]) if N else torch.zeros(R, dtype=torch.bool, device="cuda")

@@ -58,7 +58,7 @@ __all__ = [
     "quantize_act_e4m3", "qgemm_w8a8_block", "qgemm_w8a8", "KIND_W8A8", "MAX_M_W8A8",
     "tune_bf16", "tune_w8a8", "workspace_bytes_max_w8a8",
     "quantize_act_int8", "qgemm_w8a8_int8", "int8_tile_rows", "KIND_INT8", "logprobs", "LogProbs", "MAX_TOP_K",
-    "moe_route", "MoeRoute", "quantize_rows_e4m3", "qgemm_w8a8_grouped", "moe_combine", "MAX_EXPERTS", "KIND_GROUPED",
+    "moe_route", "MoeRoute", "quantize_rows_e4m3", "qgemm_w8a8_grouped", "moe_combine", "MAX_EXPERTS",
     "verify_drafts", "DraftCheck", "MAX_DRAFTS",
 ]
 
@@ -70,7 +70,6 @@ KIND_LUT3 = 1
 KIND_BF16 = 2
 KIND_W8A8 = 3
 KIND_INT8 = 4
-KIND_GROUPED = 5   # of Workspace only: the grouped GEMM has no schedule on the host
 MAX_M_W8A8 = 65536
 STATUS = {
     0: "QG_OK", 1: "QG_ERR_INVALID_ARG", 2: "QG_ERR_UNSUPPORTED_SHAPE", 3: "QG_ERR_MISALIGNED",
@@ -110,10 +109,10 @@ _SIGS = {
     "qg_moe_route_workspace_bytes": (_S, [_I, _I]),
     "qg_moe_route": (_I, [_P, _I, _L, _P, _I, _I, ctypes.c_float, _I, _P, _P, _P, _P, _I, _I, _P, _S, _P]),
     "qg_quantize_rows_e4m3": (_I, [_P, _I, _L, _I, _P, _I, _P, _P, _L, _P, _L, _I, _I, _I, _P]),
-    "qg_workspace_bytes_grouped": (_S, [_I, _I]),
-    "qgemm_w8a8_grouped": (_I, [_P, _L, _P, _L, _P, _P, _P, _P, _I, _L, _I, _I, _I, _I, _P, _S, _P]),
+    "qgemm_w8a8_grouped": (_I, [_P, _L, _P, _L, _P, _P, _P, _P, _I, _L, _I, _I, _I, _I, _P]),
     "qg_moe_combine": (_I, [_P, _I, _L, _P, _P, _I, _P, _L, _P, _L, _I, _I, _I, _P]),
-    "qg_verify_drafts": (_I, [_P, _I, _L, _L, _P, _L, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _I, _I, _P]),
+    "qg_verify_drafts_workspace_bytes": (_S, [_I, _I, _I]),
+    "qg_verify_drafts": (_I, [_P, _I, _L, _L, _P, _L, _L, _P, _L, _P, _L, _P, _L, _P, _P, _P, _I, _I, _I, _P, _S, _P]),
     "qg_lut3_packed_bytes": (_S, [_I, _I]),
     "pack_lut3": (_I, [_P, _P, _I, _I]),
     "unpack_lut3": (_I, [_P, _P, _I, _I]),
@@ -206,14 +205,13 @@ def workspace_bytes(kind: int, M: int, N: int, K: int) -> int:
 
 
 # the kinds whose workspaces share a layout: each of these alone, all others together
-_ROUTE = -1   # the router's scratch, which nothing expects to be zero
-_OWN_LAYOUT = (KIND_W8A8, KIND_INT8, KIND_GROUPED, _ROUTE)
+_OWN_LAYOUT = (KIND_W8A8, KIND_INT8)
 
 
 class Workspace:
     """Zero-filled device byte buffers that grow on demand, one for each
-    workspace layout (the W8A8, INT8 and grouped kinds have their own, the others
-    share one).  Calls leave their arrival counters at zero again (the rest is
+    workspace layout (the W8A8 and INT8 kinds have their own, the others share
+    one).  Calls leave their arrival counters at zero again (the rest is
     scratch), so one Workspace serves any sequence of calls of any kind on one
     stream (calls that may run at the same time, on different streams, need one
     each).  Growing synchronises the device, so that the zero fill has landed
@@ -711,20 +709,25 @@ class MoeRoute(NamedTuple):
     rows: Any      # int32 [M, top_k]
 
 
-def _workspace_of(kind, key, ask, workspace, device, stream):
-    """The workspace of a call whose need `ask` says (kept by key)."""
-    need = _ws_need.get(key)
+_scratch_need = {}
+
+
+def _scratch(key, ask, workspace, device):
+    """(tensor to keep until the call is made, address, bytes) of the scratch memory
+    of a call, whose need `ask` says (kept by key).  Nothing is expected in it, so
+    that without a workspace every call has some of its own, from PyTorch's
+    allocator: calls of other streams and captured graphs share none."""
+    need = _scratch_need.get(key)
     if need is None:
-        need = _ws_need[key] = int(ask())
+        need = _scratch_need[key] = int(ask())
     if need == 0:
-        return None, 0
+        return None, None, 0
     if workspace is None:
-        at = (device, stream)
-        workspace = _default_ws.get(at)
-        if workspace is None:
-            workspace = _default_ws[at] = Workspace(device)
-    buf = workspace.get(need, kind) if isinstance(workspace, Workspace) else workspace
-    return buf.data_ptr(), buf.numel() * buf.element_size()
+        torch = _torch()
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        buf = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+    return buf, buf.data_ptr(), buf.numel() * buf.element_size()
 
 
 def _vector(t, dtype, n, dev, what: str):
@@ -773,7 +776,7 @@ def moe_route(logits, top_k: int, score: str = "softmax", bias=None, renormalize
     offsets = torch.empty((E + 1,), dtype=i32, device=dev)
     rows = torch.empty((M, top_k), dtype=i32, device=dev)
     st = _raw_stream(index)
-    ws, wsb = _workspace_of(_ROUTE, (_ROUTE, M, E, dev), lambda: lib.qg_moe_route_workspace_bytes(M, E), workspace, dev, st)
+    buf, ws, wsb = _scratch(("route", M, E, index), lambda: lib.qg_moe_route_workspace_bytes(M, E), workspace, dev)
     r = lib.qg_moe_route(logits.data_ptr(), code, ld, b, kind, 1 if renormalize else 0, scale, top_k,
                          experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), M, E, ws, wsb, st)
     if r:
@@ -851,7 +854,7 @@ def quantize_rows_e4m3(X, gated: bool = False, rows=None, num_rows=None, out_row
     return Xq, X_scale
 
 
-def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None, workspace=None, stream=None):
+def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None, stream=None):
     """:func:`qgemm_w8a8_block` grouped by expert: for the rows r of each expert e,
     offsets[e] <= r < offsets[e + 1], Y[r] = dequant(Xq[r]) . dequant(W[e])^T with
     FP32 sums per 128-wide K block.
@@ -864,7 +867,7 @@ def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None,
     or float32 (out_dtype).  Rows of no expert are left as they were.
     """
     if stream is not None and Y is None and _elsewhere(stream):
-        return _on_stream(stream, qgemm_w8a8_grouped, Xq, X_scale, W, W_scale, offsets, out_dtype, Y, workspace)
+        return _on_stream(stream, qgemm_w8a8_grouped, Xq, X_scale, W, W_scale, offsets, out_dtype, Y)
     torch = _torch()
     codes = (torch.uint8, torch.float8_e4m3fn)
     if Xq.dtype not in codes or W.dtype not in codes:
@@ -909,10 +912,8 @@ def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None,
         if r != R or c != N or Y.device != dev:
             raise ValueError("Y must be [R, N] on the same device")
     st = _raw_stream(index) if stream is None else _stream_ptr(stream)
-    ws, wsb = _workspace_of(KIND_GROUPED, (KIND_GROUPED, R, E, dev), lambda: lib.qg_workspace_bytes_grouped(R, E), workspace,
-                            dev, st)
     r = lib.qgemm_w8a8_grouped(Xq.data_ptr(), ldq, X_scale.data_ptr(), lds, W.data_ptr(), W_scale.data_ptr(), off,
-                               Y.data_ptr(), code, ldy, R, E, N, K, ws, wsb, st)
+                               Y.data_ptr(), code, ldy, R, E, N, K, st)
     if r:
         raise QgemmError(r, "qgemm_w8a8_grouped")
     return Y
@@ -992,7 +993,7 @@ def _batch_rows(t, what: str):
 
 
 def verify_drafts(target_logits, draft_tokens, draft_logits=None, uniform=None, noise=None, lengths=None,
-                  stream=None) -> DraftCheck:
+                  workspace=None, stream=None) -> DraftCheck:
     """Drafted tokens against the target's probabilities, from given random numbers.
 
     target_logits: bf16, fp16 or fp32 CUDA [B, G + 1, V] (unit column stride), as
@@ -1009,7 +1010,8 @@ def verify_drafts(target_logits, draft_tokens, draft_logits=None, uniform=None, 
     a NaN, +inf or nothing left keeps no draft and yields -1; see include/qgemm.h.)
     """
     if stream is not None and _elsewhere(stream):
-        return _on_stream(stream, verify_drafts, target_logits, draft_tokens, draft_logits, uniform, noise, lengths)
+        return _on_stream(stream, verify_drafts, target_logits, draft_tokens, draft_logits, uniform, noise, lengths,
+                          workspace)
     torch = _torch()
     code = _dtype_codes.get(target_logits.dtype)
     if code is None:
@@ -1061,8 +1063,10 @@ def verify_drafts(target_logits, draft_tokens, draft_logits=None, uniform=None, 
     accepted = torch.empty((B,), dtype=torch.int32, device=dev)
     tokens = torch.empty((B, G + 1), dtype=torch.int64, device=dev)
     st = _raw_stream(index)
+    buf, ws, wsb = _scratch(("drafts", B, G, V, index), lambda: lib.qg_verify_drafts_workspace_bytes(B, G, V),
+                            workspace, dev)
     r = lib.qg_verify_drafts(target_logits.data_ptr(), code, t_seq, t_row, d, d_seq, d_row, draft_tokens.data_ptr(), G,
-                             u, ldu, z, ldn, n, accepted.data_ptr(), tokens.data_ptr(), B, G, V, st)
+                             u, ldu, z, ldn, n, accepted.data_ptr(), tokens.data_ptr(), B, G, V, ws, wsb, st)
     if r:
         raise QgemmError(r, "qg_verify_drafts")
     return DraftCheck(accepted, tokens)

@@ -853,15 +853,9 @@ qg_status qg_quantize_rows_e4m3(const void* X, int x_type, int64_t ldx, int gate
     return launch_quantize_rows(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
-size_t qg_workspace_bytes_grouped(int R, int E) {
-    if (R < 1 || R > (1 << 24) || E < 1 || E > QG_MAX_EXPERTS) return 0;
-    DeviceInfo* d = device_info();
-    return d ? grouped_workspace_bytes(R, E, d->sms) : 0;
-}
-
 qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_scale, int64_t ldsx, const uint8_t* W,
                              const float* W_scale, const int32_t* offsets, void* Y, int y_type, int64_t ldy, int R,
-                             int E, int N, int K, void* workspace, size_t workspace_bytes_, cudaStream_t stream) {
+                             int E, int N, int K, cudaStream_t stream) {
     if (R < 0 || E < 0 || N < 0 || K < 0 || (y_type != QG_BF16 && y_type != QG_FP16 && y_type != QG_FP32))
         return QG_ERR_INVALID_ARG;
     if (R == 0 || E == 0 || N == 0) return QG_OK;
@@ -892,10 +886,6 @@ qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_sca
     a.N = N;
     a.K = K;
     if (K == 0) return launch_grouped_zero(a, stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
-    const size_t need = grouped_workspace_bytes(R, E, d->sms);
-    if (need > 0 && (!workspace || workspace_bytes_ < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
-        return QG_ERR_WORKSPACE;
-    a.ws = need > 0 ? workspace : nullptr;
     const CUtensorMap* tmW =
         cached_tmap(W, static_cast<uint64_t>(K), static_cast<uint64_t>(E) * static_cast<uint64_t>(N), kMapFp8Weights);
     if (!tmW) return QG_ERR_CUDA;
@@ -926,10 +916,17 @@ qg_status qg_moe_combine(const void* Y, int type, int64_t ldy, const int32_t* ro
     return launch_combine(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
+size_t qg_verify_drafts_workspace_bytes(int B, int G, int V) {
+    if (B < 1 || B > 65536 || G < 0 || G > QG_MAX_DRAFTS || V < 1 || V > (1 << 30)) return 0;
+    DeviceInfo* d = device_info();
+    return d ? verify_workspace_bytes(B, G, V, d->sms) : 0;
+}
+
 qg_status qg_verify_drafts(const void* target, int type, int64_t t_seq, int64_t t_row, const void* draft,
                            int64_t d_seq, int64_t d_row, const int64_t* tokens, int64_t ldt, const float* uniform,
                            int64_t ldu, const float* noise, int64_t ldn, const int32_t* lengths, int32_t* accepted,
-                           int64_t* tokens_out, int B, int G, int V, cudaStream_t stream) {
+                           int64_t* tokens_out, int B, int G, int V, void* workspace, size_t workspace_bytes_,
+                           cudaStream_t stream) {
     if (B < 0 || G < 0 || V < 0 || (type != QG_BF16 && type != QG_FP16 && type != QG_FP32)) return QG_ERR_INVALID_ARG;
     if (B == 0) return QG_OK;
     if (!target || !accepted || !tokens_out || (G > 0 && !tokens)) return QG_ERR_INVALID_ARG;
@@ -946,8 +943,10 @@ qg_status qg_verify_drafts(const void* target, int type, int64_t t_seq, int64_t 
         return QG_ERR_MISALIGNED;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
+    const size_t need = verify_workspace_bytes(B, G, V, d->sms);
+    if (need > 0 && (!workspace || workspace_bytes_ < need || !aligned16(workspace))) return QG_ERR_WORKSPACE;
     const VerifyArgs a{target, t_seq, t_row, draft,   d_seq,    d_row,      type, tokens, ldt, uniform,
-                       ldu,    noise, ldn,   lengths, accepted, tokens_out, B,    G,      V};
+                       ldu,    noise, ldn,   lengths, accepted, tokens_out, B,    G,      V,   workspace};
     return launch_verify(a, launch_ctl(d), stream) == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 

@@ -77,13 +77,12 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// The k + more largest keys above 0, in order (ties to the lower expert): lane j
-// receives the j-th one's expert (-1: none left) and its key.
+// The largest keys above 0, the j0-th to the one in front of the j1-th, in order
+// (ties to the lower expert), taken out of `key`: lane j receives the j-th one's
+// expert and its key, and keeps what it had where none is left.
 template <class Key, int PL>
-__device__ __forceinline__ void choose(Key (&key)[PL], int n, int lane, int& expert, Key& at) {
-    expert = -1;
-    at = 0;
-    for (int j = 0; j < n; ++j) {
+__device__ __forceinline__ void choose(Key (&key)[PL], int j0, int j1, int lane, int& expert, Key& at) {
+    for (int j = j0; j < j1; ++j) {
         Key best = 0;
         int bi = 0;
 #pragma unroll
@@ -112,6 +111,12 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// Whether two sums, x's not below y's, may be in another order in 64 bits.
+__device__ __forceinline__ bool nearly(uint32_t x, uint32_t y) {
+    const float a = key_value(x);
+    return !(a - key_value(y) > kNear * fmaxf(1.0f, fabsf(a)));
+}
+
 // One token: lane j < k receives its j-th expert (-1: none) and the weight.
 template <int kType, int PL>
 __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row, int lane, int& expert, float& weight) {
@@ -134,7 +139,8 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int k = a.top_k;
     const bool soft = a.score == QG_SCORE_SOFTMAX;
-    uint32_t key[PL], at;
+    uint32_t key[PL], at = 0u;
+    expert = -1;
     float total = 0.0f;   // of the softmax, where it is needed
     if (soft && (a.bias != nullptr || !a.renormalize)) {
 #pragma unroll
@@ -144,7 +150,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
     if (a.bias == nullptr) {
 #pragma unroll
         for (int i = 0; i < PL; ++i) key[i] = v[i] > -INFINITY ? order_key(v[i]) : 0u;
-        choose(key, k, lane, expert, at);
+        choose(key, 0, k, lane, expert, at);
     } else {
         bool near = false;
 #pragma unroll
@@ -155,42 +161,68 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
             key[i] = v[i] > -INFINITY && by > -INFINITY ? order_key(by) : 0u;   // a NaN is above nothing
         }
         // k < 32: the next one too; k = 32 is done again whenever one is left
-        choose(key, k < 32 ? k + 1 : 32, lane, expert, at);
+        choose(key, 0, k < 32 ? k + 1 : 32, lane, expert, at);
         const uint32_t next = __shfl_down_sync(0xffffffffu, at, 1);
-        if (lane < (k < 32 ? k : 31) && next != 0u) {
-            const float x = key_value(at);
-            near = !(x - key_value(next) > kNear * fmaxf(1.0f, fabsf(x)));
-        }
-        if (k == 32) {
-            bool left = false;
+        if (lane < (k < 32 ? k : 31) && next != 0u) near = nearly(at, next);
+        auto any_left = [&]() {
+            uint32_t left = 0u;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) left |= key[i] != 0u;
-            near |= left;
-        }
+            for (int i = 0; i < PL; ++i) left |= key[i];
+            return __any_sync(0xffffffffu, left != 0u);
+        };
+        if (k == 32) near |= any_left();
         if (__any_sync(0xffffffffu, near)) {
-            uint64_t wide[PL], wat;
-            double sum = 1.0;
-            if (soft) {
-                sum = 0.0;
+            // The 32 largest sums in 64 bits, one a lane, unless those behind them may
+            // belong among the first k as well.
+            choose(key, k < 32 ? k + 1 : 32, 32, lane, expert, at);
+            const uint32_t last = __shfl_sync(0xffffffffu, at, 31), kth = __shfl_sync(0xffffffffu, at, k - 1);
+            if (!soft && (last == 0u || !any_left() || !nearly(kth, last))) {
+                uint64_t wide = 0;
+                if (at != 0u) {
+                    const double x = to_f32<kType>(row, expert);
+                    const double by = 1.0 / (1.0 + exp(-x)) + static_cast<double>(a.bias[expert]);
+                    if (by > -INFINITY) wide = order_key(by);
+                }
+                int rank = 0;
+                for (int i = 0; i < 32; ++i) {
+                    const uint64_t w = __shfl_sync(0xffffffffu, wide, i);
+                    const int e = __shfl_sync(0xffffffffu, expert, i);
+                    rank += w > wide || (w == wide && e < expert) ? 1 : 0;
+                }
+                if (wide == 0) rank = 32;
+                int mine = -1;
+                for (int i = 0; i < 32; ++i) {
+                    const int r = __shfl_sync(0xffffffffu, rank, i);
+                    const int e = __shfl_sync(0xffffffffu, expert, i);
+                    if (r == lane) mine = e;
+                }
+                expert = mine;
+            } else {
+                uint64_t wide[PL], wat = 0;
+                double sum = 1.0;
+                if (soft) {
+                    sum = 0.0;
 #pragma unroll 1
+                    for (int i = 0; i < PL; ++i) {
+                        const int e = i * 32 + lane;
+                        if (e < a.E) sum += exp(static_cast<double>(to_f32<kType>(row, e)) - static_cast<double>(top));
+                    }
+                    sum = warp_sum(sum);
+                }
+#pragma unroll
                 for (int i = 0; i < PL; ++i) {
                     const int e = i * 32 + lane;
-                    if (e < a.E) sum += exp(static_cast<double>(to_f32<kType>(row, e)) - static_cast<double>(top));
+                    wide[i] = 0;
+                    if (e < a.E && v[i] > -INFINITY) {
+                        const double x = v[i];
+                        const double s = soft ? exp(x - static_cast<double>(top)) / sum : 1.0 / (1.0 + exp(-x));
+                        const double by = s + static_cast<double>(a.bias[e]);
+                        if (by > -INFINITY) wide[i] = order_key(by);
+                    }
                 }
-                sum = warp_sum(sum);
+                expert = -1;
+                choose(wide, 0, k, lane, expert, wat);
             }
-#pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                const int e = i * 32 + lane;
-                wide[i] = 0;
-                if (e < a.E && v[i] > -INFINITY) {
-                    const double x = v[i];
-                    const double s = soft ? exp(x - static_cast<double>(top)) / sum : 1.0 / (1.0 + exp(-x));
-                    const double by = s + static_cast<double>(a.bias[e]);
-                    if (by > -INFINITY) wide[i] = order_key(by);
-                }
-            }
-            choose(wide, k, lane, expert, wat);
         }
         if (lane >= k) expert = -1;
     }
@@ -209,6 +241,10 @@ __host__ __device__ inline int route_ctas(int M, int sms) {
     // up to four tokens a warp one CTA does it all: the second launch costs more
     return M <= 4 * kRouteWarps ? 1 : (M + kRouteWarps - 1) / kRouteWarps < sms ? (M + kRouteWarps - 1) / kRouteWarps : sms;
 }
+
+// The CTAs' counts by expert: 16 bits each (a CTA has at most 2^20 / 64 tokens, each
+// of which takes an expert once), in rows of whole 16 bytes.
+__host__ __device__ inline int route_pitch(int E) { return (E + 7) / 8 * 8; }
 
 // where[e] = the exclusive prefix over the experts of total[e] (each a CTA's or
 // the whole call's), total in shared memory; all threads of the CTA.
@@ -274,7 +310,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             sum += n;
         }
         total[e] = sum;
-        if (gridDim.x > 1) static_cast<int*>(a.ws)[static_cast<int64_t>(blockIdx.x) * a.E + e] = sum;
+        if (gridDim.x > 1)
+            static_cast<uint16_t*>(a.ws)[static_cast<int64_t>(blockIdx.x) * route_pitch(a.E) + e] = static_cast<uint16_t>(sum);
     }
     __syncthreads();
     if (gridDim.x == 1) {
@@ -299,23 +336,44 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
     for (int e = threadIdx.x; e < 2 * a.E; e += kPlaceThreads) total[e] = 0;
     grid_dependency_wait();
     __syncthreads();
-    const int* table = static_cast<const int*>(a.ws);
+    // A thread adds up eight experts over a share of the CTAs, sixteen of their
+    // rows on the way at a time (a value a thread and load: 13 us).  Whole numbers, so
+    // that the order of the additions does not show.
+    const uint4* table = static_cast<const uint4*>(a.ws);
     const int ctas = gridDim.x;
-    // threads in parts of E, each part a share of the CTAs; whole numbers, so that
-    // the order of the additions does not show
-    const int parts = a.E <= kPlaceThreads ? kPlaceThreads / a.E : 1;
-    for (int i = threadIdx.x; i < parts * a.E; i += kPlaceThreads) {
-        const int e = i % a.E, part = i / a.E;
+    const int groups = route_pitch(a.E) / 8;
+    const int parts = kPlaceThreads / groups;   // groups <= 128
+    const int g = threadIdx.x % groups, part = threadIdx.x / groups;
+    if (part < parts) {
         const int b0 = part * ctas / parts, b1 = (part + 1) * ctas / parts;
-        int all = 0, before = 0;
-#pragma unroll 8
-        for (int b = b0; b < b1; ++b) {
-            const int n = __ldcg(table + static_cast<int64_t>(b) * a.E + e);
-            all += n;
-            before += b < static_cast<int>(blockIdx.x) ? n : 0;
+        int all[8] = {}, before[8] = {};
+        for (int b = b0; b < b1; b += 16) {
+            uint4 w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                w[i] = b + i < b1 ? __ldcg(table + static_cast<int64_t>(b + i) * groups + g) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                const bool front_of = b + i < static_cast<int>(blockIdx.x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int lo = static_cast<int>(u[e] & 0xFFFFu), hi = static_cast<int>(u[e] >> 16);
+                    all[2 * e] += lo;
+                    all[2 * e + 1] += hi;
+                    before[2 * e] += front_of ? lo : 0;
+                    before[2 * e + 1] += front_of ? hi : 0;
+                }
+            }
         }
-        atomicAdd(total + e, all);
-        atomicAdd(front + e, before);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = 8 * g + i;
+            if (e < a.E) {
+                atomicAdd(total + e, all[i]);
+                atomicAdd(front + e, before[i]);
+            }
+        }
     }
     __syncthreads();
     prefix_experts(total, where, a.E);
@@ -356,9 +414,8 @@ cudaError_t launch_route_type(const RouteArgs& a, const LaunchCtl& c, cudaStream
 }
 
 // ----------------------------------------------------------------- row quantiser
-// A half warp takes a block of 128 columns of a row, eight of them a lane: their
-// maximum, the scale, eight codes, which go to every one of the row's places.  A
-// warp walks over its row in steps of 256 columns.
+// Eight lanes take a block of 128 columns of a row: its maximum, the scale, sixteen
+// codes each, which go to every one of the row's places.
 template <bool kBf16>
 __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -376,11 +433,13 @@ __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
 }
 
 // silu(g) u in 32 bits: g u / (1 + e^-g).  The exponential is good to
-// 2^-22 + |g| 2^-24, the reciprocal to 2^-23: far below an E4M3 step (2^-4).
+// 2^-22 + |g| 2^-24, the reciprocal to 2^-23: far below an E4M3 step (2^-4).  With
+// subnormals as zeros (an e^-g below 2^-126 is nothing beside 1), each is one
+// instruction; without, they took 40 % of the kernel's.
 __device__ __forceinline__ float gate(float g, float u) {
     float e, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return g * r * u;
 }
 
@@ -401,11 +460,12 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 }
 
 constexpr int kQuantWarps = 8;
-constexpr int kQuantCtas = 6;   // per SM
+constexpr int kQuantCtas = 4;   // per SM
 
-// Resident warps walk over jobs (256 columns of a row), the next job's loads on
-// their way while this one's codes are worked out.
-template <bool kBf16, bool kGated>
+// Resident warps walk over jobs (512 columns of a row, 16 of them a lane, so that a
+// lane's codes are one 16-byte store and eight lanes share a block), the next
+// job's loads on their way while this one's codes are worked out.
+template <bool kBf16, bool kGated, bool kPlaces>
 __global__ void __launch_bounds__(kQuantWarps * 32, kQuantCtas)
     quantize_rows_kernel(const QuantizeRowsArgs a, int steps) {
     grid_dependents_launch();
@@ -423,33 +483,40 @@ __global__ void __launch_bounds__(kQuantWarps * 32, kQuantCtas)
     const int ds = static_cast<int>(warps - static_cast<unsigned>(dm) * steps);
     int m = static_cast<int>(first / static_cast<unsigned>(steps));
     int s = static_cast<int>(first - static_cast<unsigned>(m) * steps);
-    const int places = a.rows != nullptr ? a.top_k : 1;
-    uint4 w, w2;
+    const int places = kPlaces ? a.top_k : 1;
+    uint4 w[2], w2[2];
     int place;   // lane j holds the row's j-th place (out of range: none)
     auto fetch = [&]() {
-        w = w2 = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[h] = w2[h] = make_uint4(0u, 0u, 0u, 0u);
         place = -1;
         if (m >= live) return;
-        const int k0 = s * 256 + lane * 8;
+        const int k0 = s * 512 + lane * 16;
         const uint16_t* x = static_cast<const uint16_t*>(a.X) + m * a.ldx + k0;
-        if (k0 < a.K) {   // K is a multiple of 16: all eight or none
-            w = *reinterpret_cast<const uint4*>(x);
-            if (kGated) w2 = *reinterpret_cast<const uint4*>(x + a.K);
+        if (k0 < a.K) {   // K is a multiple of 16: all of them or none
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                w[h] = reinterpret_cast<const uint4*>(x)[h];
+                if (kGated) w2[h] = reinterpret_cast<const uint4*>(x + a.K)[h];
+            }
         }
-        if (a.rows == nullptr) place = m;
+        if (!kPlaces) place = m;
         else if (lane < places) place = __ldcg(a.rows + static_cast<int64_t>(m) * places + lane);
     };
     fetch();
     while (m < live) {
-        float v[8];
-        widen8<kBf16>(w, v);
-        if (kGated) {
-            float u[8];
-            widen8<kBf16>(w2, u);
+        float v[2][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = gate(v[i], u[i]);
+        for (int h = 0; h < 2; ++h) {
+            widen8<kBf16>(w[h], v[h]);
+            if (kGated) {
+                float u[8];
+                widen8<kBf16>(w2[h], u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[h][i] = gate(v[h][i], u[i]);
+            }
         }
-        const int k0 = s * 256 + lane * 8;
+        const int k0 = s * 512 + lane * 16;
         const int to = place < a.out_rows ? place : -1;
         m += dm;
         s += ds;
@@ -460,28 +527,55 @@ __global__ void __launch_bounds__(kQuantWarps * 32, kQuantCtas)
         fetch();
         float amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(v[0][i]), fabsf(v[1][i])));
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+        for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float sc = quotient(amax, 448.0f, 1.0f / 448.0f);
         if (sc > 1e-30f) {
             const float r = __frcp_rn(sc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = quotient(v[i], sc, r);
+            for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = quotient(v[i >> 3][i & 7], sc, r);
         } else {   // a reciprocal or a remainder would not be a normal number
+            sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], sc);
+            for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __fdiv_rn(v[i >> 3][i & 7], sc);
         }
-        const uint2 codes = make_uint2(codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7]));
+        const uint4 codes =
+            make_uint4(codes4(v[0][0], v[0][1], v[0][2], v[0][3]), codes4(v[0][4], v[0][5], v[0][6], v[0][7]),
+                       codes4(v[1][0], v[1][1], v[1][2], v[1][3]), codes4(v[1][4], v[1][5], v[1][6], v[1][7]));
         uint8_t* q = a.Xq + k0;
         float* scale = a.Sx + (k0 >> 7) * a.ldsx;
-        for (int j = 0; j < places; ++j) {
-            const int r = __shfl_sync(0xffffffffu, to, j);
-            if (r < 0 || k0 >= a.K) continue;
-            *reinterpret_cast<uint2*>(q + r * a.ldxq) = codes;
-            if ((lane & 15) == 0) scale[r] = sc;
+        const bool in = k0 < a.K;
+        if constexpr (!kPlaces) {
+            if (in && to >= 0) *reinterpret_cast<uint4*>(q + to * a.ldxq) = codes;
+            if (in && to >= 0 && (lane & 7) == 0) scale[to] = sc;
+        } else {
+            // four places at a time; the scale of a block by its eight lanes, a place each
+#pragma unroll 1
+            for (int j0 = 0; j0 < places; j0 += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = __shfl_sync(0xffffffffu, to, j0 + j);   // -1 from `places` on
+                    if (in && r >= 0) *reinterpret_cast<uint4*>(q + r * a.ldxq) = codes;
+                }
+            }
+#pragma unroll 1
+            for (int j0 = 0; j0 < places; j0 += 8) {
+                const int r = __shfl_sync(0xffffffffu, to, j0 + (lane & 7));
+                // of a block that is there (its first column decides)
+                if ((k0 & ~127) < a.K && r >= 0) scale[r] = sc;
+            }
         }
     }
+}
+
+template <bool kBf16>
+cudaError_t launch_quantize_type(const cudaLaunchConfig_t& cfg, const QuantizeRowsArgs& a, int steps) {
+    if (a.gated)
+        return a.rows != nullptr ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<kBf16, true, true>, a, steps)
+                                 : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<kBf16, true, false>, a, steps);
+    return a.rows != nullptr ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<kBf16, false, true>, a, steps)
+                             : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<kBf16, false, false>, a, steps);
 }
 
 // ----------------------------------------------------------------- combination
@@ -625,7 +719,7 @@ cudaError_t launch_combine_type(const CombineArgs& a, cudaStream_t st) {
 
 size_t route_workspace_bytes(int M, int E, int sms) {
     const int ctas = route_ctas(M, sms);
-    return ctas > 1 ? static_cast<size_t>(ctas) * E * sizeof(int) : 0;
+    return ctas > 1 ? static_cast<size_t>(ctas) * route_pitch(E) * sizeof(uint16_t) : 0;
 }
 
 cudaError_t launch_route(const RouteArgs& a, const LaunchCtl& c, cudaStream_t st) {
@@ -638,18 +732,14 @@ cudaError_t launch_route(const RouteArgs& a, const LaunchCtl& c, cudaStream_t st
 }
 
 cudaError_t launch_quantize_rows(const QuantizeRowsArgs& a, const LaunchCtl& c, cudaStream_t st) {
-    const int steps = (a.K + 255) / 256;   // of a row
+    const int steps = (a.K + 511) / 512;   // of a row
     const int64_t jobs = static_cast<int64_t>(a.M) * steps;
     const int64_t most = static_cast<int64_t>(c.num_sms) * kQuantCtas;
     const int64_t blocks = (jobs + kQuantWarps - 1) / kQuantWarps;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg =
         config(static_cast<unsigned>(blocks < most ? blocks : most), kQuantWarps * 32, 0, st, &attr);
-    if (a.x_type == QG_BF16)
-        return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, true>, a, steps)
-                       : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<true, false>, a, steps);
-    return a.gated ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, true>, a, steps)
-                   : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<false, false>, a, steps);
+    return a.x_type == QG_BF16 ? launch_quantize_type<true>(cfg, a, steps) : launch_quantize_type<false>(cfg, a, steps);
 }
 
 cudaError_t launch_combine(const CombineArgs& a, const LaunchCtl& c, cudaStream_t st) {

@@ -907,8 +907,6 @@ int grouped_tile_rows(int R, int E) {
     return mean <= 8 ? 16 : mean <= 48 ? 64 : 256;
 }
 
-size_t grouped_workspace_bytes(int R, int E, int sms) { return 0; }
-
 cudaError_t launch_grouped(const GroupedArgs& a, const CUtensorMap& tmW, const CUtensorMap& tmX, const LaunchCtl& c,
                            cudaStream_t st) {
     switch (grouped_tile_rows(a.R, a.E)) {

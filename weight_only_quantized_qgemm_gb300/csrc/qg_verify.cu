@@ -16,10 +16,12 @@
 //      reference (greedy: the largest logit and its index), a warp at a time on a
 //      stretch of a row; the CTAs' parts are read through distributed shared
 //      memory by all of them, so that each knows n;
-//   2. the race over the slice of row n (read again, from L2 in the main).  Most
-//      tokens are out by one exponential: probability over noise below the best
-//      so far;
+//   2. the race over the slice of row n (read again, from L2 in the main);
 //   3. the first CTA compares the winners.
+// With many sequences the pass over the rows is a kernel of its own, in front: the
+// clusters that a sequence's rows would need leave SMs idle (of eight CTAs, 120 to
+// 128 of 152 are used), and one grid of warps over all stretches does not.
+//
 // All sums have a fixed order.  Bound by memory: every logit is read once, and two
 // rows of a sequence a second time with the noise.
 //
@@ -59,9 +61,15 @@ struct Elem<QG_BF16> {
         x[0] = __uint_as_float(w << 16);
         x[1] = __uint_as_float(w & 0xFFFF0000u);
     }
-    static __device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        wide(w.x, x), wide(w.y, x + 2), wide(w.z, x + 4), wide(w.w, x + 6);
+    // eight values as they lie in memory (at a multiple of 16 bytes)
+    struct Raw8 {
+        uint4 a;
+    };
+    static __device__ __forceinline__ Raw8 load8(const void* p, int64_t i) {
+        return Raw8{*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i)};
+    }
+    static __device__ __forceinline__ void wide8(const Raw8& r, float (&x)[8]) {
+        wide(r.a.x, x), wide(r.a.y, x + 2), wide(r.a.z, x + 4), wide(r.a.w, x + 6);
     }
 };
 template <>
@@ -75,9 +83,15 @@ struct Elem<QG_FP16> {
         x[0] = f.x;
         x[1] = f.y;
     }
-    static __device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-        wide(w.x, x), wide(w.y, x + 2), wide(w.z, x + 4), wide(w.w, x + 6);
+    // eight values as they lie in memory (at a multiple of 16 bytes)
+    struct Raw8 {
+        uint4 a;
+    };
+    static __device__ __forceinline__ Raw8 load8(const void* p, int64_t i) {
+        return Raw8{*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i)};
+    }
+    static __device__ __forceinline__ void wide8(const Raw8& r, float (&x)[8]) {
+        wide(r.a.x, x), wide(r.a.y, x + 2), wide(r.a.z, x + 4), wide(r.a.w, x + 6);
     }
 };
 template <>
@@ -85,16 +99,23 @@ struct Elem<QG_FP32> {
     static constexpr int kSize = 4;
     static __device__ __forceinline__ float at(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
     static __device__ __forceinline__ void wide(uint32_t w, float* x) { x[0] = __uint_as_float(w); }
-    static __device__ __forceinline__ void load8(const void* p, int64_t i, float (&x)[8]) {
-        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + 4);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    struct Raw8 {
+        uint4 a, b;
+    };
+    static __device__ __forceinline__ Raw8 load8(const void* p, int64_t i) {
+        const uint4* w = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+        return Raw8{w[0], w[1]};
+    }
+    static __device__ __forceinline__ void wide8(const Raw8& r, float (&x)[8]) {
+        const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(u[i]);
     }
 };
 
 __device__ __forceinline__ float ex2(float t) {
     float e;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));   // below 2^-126: 0
     return e;
 }
 
@@ -231,6 +252,12 @@ __device__ __forceinline__ Sum scan_sum(const void* row, int v0, int v1, int lan
         p = join(p, Sum{__shfl_xor_sync(0xffffffffu, p.c, o), __shfl_xor_sync(0xffffffffu, p.s, o)});
     return p;
 }
+__device__ __forceinline__ int length_of(const VerifyArgs& a, int b) {
+    if (a.lengths == nullptr) return a.G;
+    const int n = a.lengths[b];
+    return n < 0 ? 0 : n > a.G ? a.G : n;
+}
+
 template <int kType, bool kGreedy>
 __device__ __forceinline__ Part scan_max(const void* row, int v0, int v1, int lane) {
     Part p = scan_row<kType, kGreedy ? kGreedyScan : kMax>(
@@ -258,8 +285,51 @@ __device__ __forceinline__ Best better(Best a, Best b) {
     return b.ratio > a.ratio || (b.ratio == a.ratio && b.v < a.v) ? b : a;
 }
 
+// Stretches of this many elements are a warp's work where the rows have a kernel of
+// their own.
+constexpr int kStretch = 2048;
+inline int verify_stretches(int V) { return (V + kStretch - 1) / kStretch; }
+
+// The parts of all rows by stretch: parts[(b (2 G + 1) + r) stretches + i].
 template <int kType, bool kGreedy>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const VerifyArgs a, int ctas) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_rows_kernel(const VerifyArgs a, int stretches, float2* out) {
+    using El = Elem<kType>;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const bool sampled = !kGreedy && a.draft != nullptr;
+    const int most = sampled ? 2 * a.G + 1 : a.G + 1;   // rows of a sequence
+    const int64_t all = static_cast<int64_t>(a.B) * most * stretches;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < all;
+         i += static_cast<int64_t>(gridDim.x) * kWarps) {
+        const int64_t row = i / stretches;
+        const int piece = static_cast<int>(i - row * stretches);
+        const int b = static_cast<int>(row / most);
+        const int r = static_cast<int>(row - static_cast<int64_t>(b) * most);
+        const int length = length_of(a, b);
+        const bool of_target = r <= a.G;
+        if (of_target ? r > length : r - (a.G + 1) >= length) continue;
+        const uint8_t* p = of_target
+                               ? static_cast<const uint8_t*>(a.target) + (b * a.t_seq + r * a.t_row) * El::kSize
+                               : static_cast<const uint8_t*>(a.draft) + (b * a.d_seq + (r - a.G - 1) * a.d_row) * El::kSize;
+        const int s0 = piece * kStretch;
+        const int s1 = s0 + kStretch < a.V ? s0 + kStretch : a.V;
+        float2 v;
+        if constexpr (kGreedy) {
+            const Part q = scan_max<kType, true>(p, s0, s1, lane);
+            v = make_float2(q.m, q.s);
+        } else {
+            const Sum q = scan_sum<kType>(p, s0, s1, lane);
+            v = make_float2(q.c, q.s);
+        }
+        if (lane == 0) out[(static_cast<int64_t>(b) * (2 * a.G + 1) + r) * stretches + piece] = v;
+    }
+}
+
+// kApart: the rows' parts come from verify_rows_kernel.
+template <int kType, bool kGreedy, bool kApart>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    verify_kernel(const VerifyArgs a, int ctas, int stretches, const float2* given) {
     using El = Elem<kType>;
     __shared__ Part parts[kMostRows][kParts];
     __shared__ Part mine[kMostRows];        // this CTA's slice
@@ -274,11 +344,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     const int rank = blockIdx.x % ctas;
     const int b = blockIdx.x / ctas;
     const bool sampled = !kGreedy && a.draft != nullptr;
-    int length = a.G;
-    if (a.lengths != nullptr) {
-        length = a.lengths[b];
-        length = length < 0 ? 0 : length > a.G ? a.G : length;
-    }
+    const int length = length_of(a, b);
     // rows 0 .. length of the target, then 0 .. length - 1 of the draft
     const int trows = length + 1;
     const int rows = trows + (sampled ? length : 0);
@@ -316,34 +382,57 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     };
     auto join_maxima = [](Part a, Part b) { return kGreedy ? join_greedy(a, b) : join(a, b); };
     if (threadIdx.x == 0) odd_rows = 0;
-    for (int i = warp; i < rows * pieces; i += kWarps) {
-        int r, piece, s0, s1;
-        stretch(i, r, piece, s0, s1);
-        Part p;
+    // the whole row's sums (greedy: its maximum) from all parts
+    auto enter_row = [&](int r, Part p) {
         if constexpr (kGreedy) {
-            p = scan_max<kType, true>(row_at(r), s0, s1, lane);
+            all[r] = p;
         } else {
-            const Sum q = scan_sum<kType>(row_at(r), s0, s1, lane);
-            p = Part{q.c, q.s};
-        }
-        if (lane == 0) parts[r][piece] = p;
-    }
-    __syncthreads();
-    for (int r = threadIdx.x; r < rows; r += kThreads) {
-        Part p = parts[r][0];
-        for (int i = 1; i < pieces; ++i) p = kGreedy ? join_greedy(p, parts[r][i]) : join_sums(p, parts[r][i]);
-        mine[r] = p;
-    }
-    __syncthreads();
-    cluster_sync_all();
-    for (int r = threadIdx.x; r < rows; r += kThreads) {
-        if constexpr (kGreedy) {
-            all[r] = of_all(r, join_maxima);
-        } else {
-            const Part p = of_all(r, join_sums);
             const bool fine = fabsf(p.m) <= kMostRef && p.s < INFINITY;
             all[r] = fine ? about_max(Sum{p.m, p.s}) : Part{0.0f, -1.0f};
             if (!fine) atomicOr(&odd_rows, 1);
+        }
+    };
+    if constexpr (kApart) {
+        __syncthreads();   // odd_rows
+        for (int r = warp; r < rows; r += kWarps) {
+            const int at = r < trows ? r : a.G + 1 + r - trows;
+            const float2* from = given + (static_cast<int64_t>(b) * (2 * a.G + 1) + at) * stretches;
+            Part p{kGreedy ? -INFINITY : kNoRef, kGreedy ? __uint_as_float(0x7FFFFFFFu) : 0.0f};
+            for (int i = lane; i < stretches; i += 32) {
+                const float2 v = __ldcg(from + i);
+                p = kGreedy ? join_greedy(p, Part{v.x, v.y}) : join_sums(p, Part{v.x, v.y});
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const Part q{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)};
+                p = kGreedy ? join_greedy(p, q) : join_sums(p, q);
+            }
+            if (lane == 0) enter_row(r, p);
+        }
+    } else {
+        for (int i = warp; i < rows * pieces; i += kWarps) {
+            int r, piece, s0, s1;
+            stretch(i, r, piece, s0, s1);
+            Part p;
+            if constexpr (kGreedy) {
+                p = scan_max<kType, true>(row_at(r), s0, s1, lane);
+            } else {
+                const Sum q = scan_sum<kType>(row_at(r), s0, s1, lane);
+                p = Part{q.c, q.s};
+            }
+            if (lane == 0) parts[r][piece] = p;
+        }
+        __syncthreads();
+        for (int r = threadIdx.x; r < rows; r += kThreads) {
+            Part p = parts[r][0];
+            for (int i = 1; i < pieces; ++i) p = kGreedy ? join_greedy(p, parts[r][i]) : join_sums(p, parts[r][i]);
+            mine[r] = p;
+        }
+        __syncthreads();
+        cluster_sync_all();
+        for (int r = threadIdx.x; r < rows; r += kThreads) {
+            if constexpr (kGreedy) enter_row(r, of_all(r, join_maxima));
+            else enter_row(r, of_all(r, join_sums));
         }
     }
     __syncthreads();
@@ -405,13 +494,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
         const int64_t d = drafted && !sampled ? a.tokens[b * a.ldt + n] : -1;   // the certain draft
         const float pr = 1.0f / t.s, qr = 1.0f / s.s;
         const float* noise = a.noise + b * a.ldn;
-        const float cut_off = pr * 1.0001f;   // the exponential below is good to 2^-20
         // The race of max(p - q, 0), or of p (for a row where that is 0 everywhere).
+        // Eight tokens a lane at a time: bounds of their ratios from quick
+        // probabilities (good to kSlack of p), then the exact ratio where a token's
+        // upper bound reaches the largest lower one that the warp has seen, which
+        // few do.  (Each lane against its own best: some lane of 32 had one for
+        // almost every token, and the race took 20 us of 62.)
+        constexpr float kSlack = 2e-5f;
+        const float tl = t.m * kLog2e, sl = s.m * kLog2e;
         auto race = [&](bool with_q, Best& result) {
             Best top{0.0f, 0x7FFFFFFF};
-            // indices ascend in a thread, so the first of equals stays
-            auto enter = [&](int v, float x, float y, float e) {
-                if (!(ex2((x - t.m) * kLog2e) * cut_off > top.ratio * e * 0.9999f)) return;
+            float reach = 0.0f;
+            auto exact = [&](int v, float x, float y, float e) {
                 const float p = exp_near(x - t.m) * pr;
                 float q = 0.0f;
                 if (with_q) {
@@ -421,8 +515,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                 const float w = p - q;
                 if (w > 0.0f) {
                     const float ratio = __fdiv_rn(w, e);
+                    // indices ascend in a thread, so the first of equals stays
                     if (ratio > top.ratio) top = Best{ratio, v};
                 }
+            };
+            // tokens v, v + step, ... (those from v1 on do not count)
+            auto enter = [&](int v, int step, const float (&x)[8], const float (&y)[8], const float (&e)[8]) {
+                float high[8];
+                float low = reach;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p = ex2(__fmaf_rn(x[j], kLog2e, -tl)) * pr;
+                    float w = p;
+                    if (with_q) {
+                        if (drow != nullptr) w -= ex2(__fmaf_rn(y[j], kLog2e, -sl)) * qr;
+                        else if (v + j * step == d) w -= 1.0f;
+                    }
+                    float r;
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e[j]));
+                    const bool in = v + j * step < v1 && r > 0.0f;
+                    high[j] = in ? __fmaf_rn(kSlack, p, w) * r : -1.0f;
+                    low = fmaxf(low, in ? __fmaf_rn(-kSlack, p, w) * r : 0.0f);
+                }
+                reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(low)));   // not negative
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (high[j] >= reach) exact(v + j * step, x[j], y[j], e[j]);
             };
             constexpr int kVec = 8;
             const bool vectors = ((reinterpret_cast<uintptr_t>(trow) | reinterpret_cast<uintptr_t>(drow) |
@@ -431,29 +549,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
             if (vectors) {   // slices begin at multiples of 32
                 const int nvec = (v1 - v0) / kVec;
                 v_done = v0 + nvec * kVec;
-                for (int i = threadIdx.x; i < nvec; i += kThreads) {
-                    const int v = v0 + i * kVec;
-                    float x[kVec], y[kVec], e[kVec];
-                    El::load8(trow, v, x);
-                    if (with_q && drow != nullptr) El::load8(drow, v, y);
-                    Elem<QG_FP32>::load8(noise, v, e);
+                // loads of several turns on the way at a time
+                constexpr int kTurns = El::kSize == 4 ? 1 : 2;
+                for (int i0 = 32 * warp; i0 < nvec; i0 += kThreads * kTurns) {
+                    typename El::Raw8 xr[kTurns], yr[kTurns];
+                    Elem<QG_FP32>::Raw8 er[kTurns];
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) enter(v + j, x[j], drow != nullptr ? y[j] : 0.0f, e[j]);
+                    for (int u = 0; u < kTurns; ++u) {
+                        int i = i0 + lane + kThreads * u;
+                        i = i < nvec ? i : nvec - 1;
+                        xr[u] = El::load8(trow, v0 + i * kVec);
+                        yr[u] = El::load8(with_q && drow != nullptr ? drow : trow, v0 + i * kVec);
+                        er[u] = Elem<QG_FP32>::load8(noise, v0 + i * kVec);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kTurns; ++u) {
+                        const int i = i0 + lane + kThreads * u;
+                        float x[kVec], y[kVec], e[kVec];
+                        El::wide8(xr[u], x);
+                        El::wide8(yr[u], y);
+                        Elem<QG_FP32>::wide8(er[u], e);
+                        enter(i < nvec ? v0 + i * kVec : v1, 1, x, y, e);
+                    }
                 }
             }
-            constexpr int kU = 4;
-            for (int v = v_done + static_cast<int>(threadIdx.x); v < v1; v += kThreads * kU) {
-                float x[kU], y[kU], e[kU];
+            for (int v = v_done + 32 * warp; v < v1; v += kThreads * kVec) {
+                float x[kVec], y[kVec], e[kVec];
 #pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int w = v + kThreads * u < v1 ? v + kThreads * u : v;
+                for (int u = 0; u < kVec; ++u) {
+                    int w = v + lane + kThreads * u;
+                    w = w < v1 ? w : v1 - 1;
                     x[u] = El::at(trow, w);
                     y[u] = with_q && drow != nullptr ? El::at(drow, w) : 0.0f;
                     e[u] = noise[w];
                 }
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    if (v + kThreads * u < v1) enter(v + kThreads * u, x[u], y[u], e[u]);
+                enter(v + lane, kThreads, x, y, e);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
@@ -494,12 +624,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     cluster_sync_all();   // nobody leaves while its shared memory is read
 }
 
-template <int kType, bool kGreedy>
-cudaError_t launch(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
+template <int kType, bool kGreedy, bool kApart>
+cudaError_t launch_clusters(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
     static std::atomic<uint64_t> wide{0};
-    cudaError_t e = set_once(wide, verify_kernel<kType, kGreedy>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaError_t e = set_once(wide, verify_kernel<kType, kGreedy, kApart>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    // CTAs of a sequence: as many as run at once, none with less than 2048 of the vocabulary
+    // CTAs of a sequence: as many as run at once, none with less than 2048 of the
+    // vocabulary (a power of two: clusters of 7 leave a third of the SMs idle)
     int ctas = kMostCtas;
     while (ctas > 1 && (static_cast<int64_t>(ctas) * a.B > kCtasPerSm * c.num_sms || a.V / ctas < 2048)) ctas /= 2;
     cudaLaunchConfig_t cfg = {};
@@ -515,7 +646,28 @@ cudaError_t launch(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<kType, kGreedy>, a, ctas);
+    return cudaLaunchKernelEx(&cfg, verify_kernel<kType, kGreedy, kApart>, a, ctas, verify_stretches(a.V),
+                              static_cast<const float2*>(a.ws));
+}
+
+template <int kType, bool kGreedy>
+cudaError_t launch(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
+    if (verify_workspace_bytes(a.B, a.G, a.V, c.num_sms) == 0) return launch_clusters<kType, kGreedy, false>(a, c, st);
+    const int stretches = verify_stretches(a.V);
+    const int64_t warps = static_cast<int64_t>(a.B) * (2 * a.G + 1) * stretches;
+    const int64_t most = static_cast<int64_t>(c.num_sms) * kCtasPerSm, blocks = (warps + kWarps - 1) / kWarps;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, verify_rows_kernel<kType, kGreedy>, a, stretches, static_cast<float2*>(a.ws));
+    return e != cudaSuccess ? e : launch_clusters<kType, kGreedy, true>(a, c, st);
 }
 
 template <int kType>
@@ -524,6 +676,12 @@ cudaError_t launch_type(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st
 }
 
 }  // namespace
+
+// 0: the clusters pass over the rows themselves (few sequences: one launch less)
+size_t verify_workspace_bytes(int B, int G, int V, int sms) {
+    if (static_cast<int64_t>(B) * kMostCtas <= 2 * sms || V < 4 * kStretch) return 0;
+    return static_cast<size_t>(B) * (2 * G + 1) * verify_stretches(V) * sizeof(float2);
+}
 
 cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st) {
     switch (a.type) {

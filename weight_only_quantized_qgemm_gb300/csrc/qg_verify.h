@@ -21,7 +21,10 @@ struct VerifyArgs {
     int32_t* accepted;        // [B]
     int64_t* out;             // [B, G + 1]
     int B, G, V;
+    void* ws;
 };
+
+size_t verify_workspace_bytes(int B, int G, int V, int sms);
 
 cudaError_t launch_verify(const VerifyArgs& a, const LaunchCtl& c, cudaStream_t st);
 
