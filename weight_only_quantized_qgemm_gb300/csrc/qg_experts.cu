@@ -45,8 +45,16 @@ cudaLaunchConfig_t config(unsigned grid, unsigned block, size_t smem, cudaStream
 // compared as they are.  With one the scores decide that are next to another,
 // and 32 bits are not enough for those: where the chosen ones, or the last one
 // and the next, lie closer than the scores' error, the token is done again in 64.
-constexpr int kRouteWarps = 16;
-constexpr float kNear = 4e-6f;   // relative to max(1, |score|); the scores are good to 1e-6 of it
+// Warps of a CTA, one CTA on an SM: as many as the registers for PL experts a lane
+// allow (a token is a chain of reductions, of which 16 warps hide too little).
+template <int PL>
+constexpr int kRouteWarps = PL <= 16 ? 32 : 16;
+inline int route_warps(int E) { return E <= 512 ? 32 : 16; }
+// How near, relative to max(1, |sum|).  The quick sigmoid's e^-x is good to 2^-22 +
+// |x| 2^-24, of which s (1 - s) shows in s, its sum with 1 and its reciprocal to 2^-24
+// and 2^-23, the sum with the bias to another 2^-24: less than 4e-7 for each of two.
+// Softmax: the common total of up to 37 roundings comes on top.
+constexpr float kNearSigmoid = 1e-6f, kNearSoftmax = 6e-6f;
 
 // A value's bits as a whole number that orders like it (never 0).
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -111,15 +119,79 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// Whether two sums, x's not below y's, may be in another order in 64 bits.
-__device__ __forceinline__ bool nearly(uint32_t x, uint32_t y) {
-    const float a = key_value(x);
-    return !(a - key_value(y) > kNear * fmaxf(1.0f, fabsf(a)));
+// The `want` largest keys above 0 and whatever else reaches the want-th largest of
+// the lanes' maxima (which at least that many do), in order: lane j receives the
+// j-th one's expert (-1: none) and key.  Returns how many they are; more than 32: too
+// many for this, nothing was done.  A few more than `want` in general, which are
+// ranked by counting: half the instructions of taking them out one by one.
+template <int PL>
+__device__ __forceinline__ int sorted_largest(const uint32_t (&key)[PL], int want, int lane, uint2* held, int& expert,
+                                              uint32_t& at, uint32_t& bound) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < PL; ++i) best = best > key[i] ? best : key[i];
+    bound = 1u;
+    for (int seen = 0; seen < want;) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top == 0u) {   // fewer lanes than that hold any
+            bound = 1u;
+            break;
+        }
+        bound = top;
+        seen += __popc(__ballot_sync(0xffffffffu, best == top));
+        if (best == top) best = 0u;
+    }
+    const uint32_t before = (1u << lane) - 1u;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+        const bool in = key[i] >= bound;
+        const uint32_t all = __ballot_sync(0xffffffffu, in);
+        const int place = n + __popc(all & before);
+        if (in && place < 32) held[place] = make_uint2(key[i], static_cast<uint32_t>(i * 32 + lane));
+        n += __popc(all);
+    }
+    if (n > 32) return n;
+    __syncwarp();
+    const uint2 mine = lane < n ? held[lane] : make_uint2(0u, 0xffffffffu);
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const uint2 o = held[i];
+        rank += o.x > mine.x || (o.x == mine.x && o.y < mine.y) ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < n) held[rank] = mine;
+    __syncwarp();
+    const uint2 now = lane < n ? held[lane] : make_uint2(0u, 0xffffffffu);
+    __syncwarp();   // `held` serves the next token
+    expert = static_cast<int>(now.y);
+    at = now.x;
+    return n;
 }
 
-// One token: lane j < k receives its j-th expert (-1: none) and the weight.
+// Whether two sums, x's not below y's, may be in another order in 64 bits.
+__device__ __forceinline__ bool nearly(uint32_t x, uint32_t y, float near) {
+    const float a = key_value(x);
+    return !(a - key_value(y) > near * fmaxf(1.0f, fabsf(a)));
+}
+
+__device__ __forceinline__ float quick_exp(float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+    return e;
+}
+__device__ __forceinline__ float quick_reciprocal(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// One token: lane j < k receives its j-th expert (-1: none) and the weight.  held: 32
+// pairs of the warp's own.
 template <int kType, int PL>
-__device__ __forceinline__ void route_token(const RouteArgs& a, const void* row, int lane, int& expert, float& weight) {
+__device__ __forceinline__ void route_token(const RouteArgs& a, const void* row, int lane, uint2* held, int& expert,
+                                            float& weight) {
     float v[PL];
     float top = -INFINITY;
     bool bad = false;
@@ -127,6 +199,9 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
     for (int i = 0; i < PL; ++i) {
         const int e = i * 32 + lane;
         v[i] = e < a.E ? to_f32<kType>(row, e) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
         top = fmaxf(top, v[i]);
         bad |= !(v[i] < INFINITY);   // NaN or +inf
     }
@@ -135,12 +210,13 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
         weight = __uint_as_float(0x7FC00000u);
         return;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int k = a.top_k;
     const bool soft = a.score == QG_SCORE_SOFTMAX;
-    uint32_t key[PL], at = 0u;
-    expert = -1;
+    if (soft) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    uint32_t key[PL], at = 0u, bound;
     float total = 0.0f;   // of the softmax, where it is needed
     if (soft && (a.bias != nullptr || !a.renormalize)) {
 #pragma unroll
@@ -150,82 +226,91 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
     if (a.bias == nullptr) {
 #pragma unroll
         for (int i = 0; i < PL; ++i) key[i] = v[i] > -INFINITY ? order_key(v[i]) : 0u;
-        choose(key, 0, k, lane, expert, at);
+        if (sorted_largest(key, k, lane, held, expert, at, bound) > 32) {
+            expert = -1;
+            choose(key, 0, k, lane, expert, at);
+        }
     } else {
-        bool near = false;
+        const float unit = soft ? 1.0f / total : 1.0f;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
             const int e = i * 32 + lane;
-            const float s = soft ? expf(v[i] - top) / total : 1.0f / (1.0f + expf(-v[i]));
-            const float by = s + (e < a.E ? a.bias[e] : 0.0f);
+            const float s = soft ? quick_exp(v[i] - top) * unit : quick_reciprocal(1.0f + quick_exp(-v[i]));
+            const float by = s + (e < a.E ? __ldg(a.bias + e) : 0.0f);
             key[i] = v[i] > -INFINITY && by > -INFINITY ? order_key(by) : 0u;   // a NaN is above nothing
         }
-        // k < 32: the next one too; k = 32 is done again whenever one is left
-        choose(key, 0, k < 32 ? k + 1 : 32, lane, expert, at);
-        const uint32_t next = __shfl_down_sync(0xffffffffu, at, 1);
-        if (lane < (k < 32 ? k : 31) && next != 0u) near = nearly(at, next);
-        auto any_left = [&]() {
-            uint32_t left = 0u;
+        // the next one behind the chosen too
+        const int n = sorted_largest(key, k < 32 ? k + 1 : 32, lane, held, expert, at, bound);
+        const float margin = soft ? kNearSoftmax : kNearSigmoid;
+        bool wide_all = n > 32;
+        if (!wide_all) {
+            const uint32_t next = __shfl_down_sync(0xffffffffu, at, 1), kth = __shfl_sync(0xffffffffu, at, k - 1);
+            bool near = lane < (k < 32 ? k : 31) && next != 0u && nearly(at, next, margin);
+            if (k == 32) {   // no lane holds the next one
 #pragma unroll
-            for (int i = 0; i < PL; ++i) left |= key[i];
-            return __any_sync(0xffffffffu, left != 0u);
-        };
-        if (k == 32) near |= any_left();
-        if (__any_sync(0xffffffffu, near)) {
-            // The 32 largest sums in 64 bits, one a lane, unless those behind them may
-            // belong among the first k as well.
-            choose(key, k < 32 ? k + 1 : 32, 32, lane, expert, at);
-            const uint32_t last = __shfl_sync(0xffffffffu, at, 31), kth = __shfl_sync(0xffffffffu, at, k - 1);
-            if (!soft && (last == 0u || !any_left() || !nearly(kth, last))) {
-                uint64_t wide = 0;
-                if (at != 0u) {
-                    const double x = to_f32<kType>(row, expert);
-                    const double by = 1.0 / (1.0 + exp(-x)) + static_cast<double>(a.bias[expert]);
-                    if (by > -INFINITY) wide = order_key(by);
-                }
-                int rank = 0;
-                for (int i = 0; i < 32; ++i) {
-                    const uint64_t w = __shfl_sync(0xffffffffu, wide, i);
-                    const int e = __shfl_sync(0xffffffffu, expert, i);
-                    rank += w > wide || (w == wide && e < expert) ? 1 : 0;
-                }
-                if (wide == 0) rank = 32;
-                int mine = -1;
-                for (int i = 0; i < 32; ++i) {
-                    const int r = __shfl_sync(0xffffffffu, rank, i);
-                    const int e = __shfl_sync(0xffffffffu, expert, i);
-                    if (r == lane) mine = e;
-                }
-                expert = mine;
-            } else {
-                uint64_t wide[PL], wat = 0;
-                double sum = 1.0;
-                if (soft) {
-                    sum = 0.0;
-#pragma unroll 1
-                    for (int i = 0; i < PL; ++i) {
-                        const int e = i * 32 + lane;
-                        if (e < a.E) sum += exp(static_cast<double>(to_f32<kType>(row, e)) - static_cast<double>(top));
-                    }
-                    sum = warp_sum(sum);
-                }
+                for (int i = 0; i < PL; ++i) near |= key[i] != 0u && key[i] < bound && nearly(kth, key[i], margin);
+            }
+            if (__any_sync(0xffffffffu, near)) {
+                // The sums that may belong among the first k in 64 bits, as far as lanes
+                // hold them all.
+                bool more = soft;   // whose total would have to be in 64 bits, too
 #pragma unroll
-                for (int i = 0; i < PL; ++i) {
-                    const int e = i * 32 + lane;
-                    wide[i] = 0;
-                    if (e < a.E && v[i] > -INFINITY) {
-                        const double x = v[i];
-                        const double s = soft ? exp(x - static_cast<double>(top)) / sum : 1.0 / (1.0 + exp(-x));
-                        const double by = s + static_cast<double>(a.bias[e]);
-                        if (by > -INFINITY) wide[i] = order_key(by);
+                for (int i = 0; i < PL; ++i) more |= key[i] != 0u && key[i] < bound && nearly(kth, key[i], margin);
+                wide_all = __any_sync(0xffffffffu, more);
+                if (!wide_all) {
+                    const bool in = at != 0u && (lane < k || nearly(kth, at, margin));
+                    const int m = __popc(__ballot_sync(0xffffffffu, in));   // the first m lanes
+                    uint64_t wide = 0;
+                    if (in) {
+                        const double x = to_f32<kType>(row, expert);
+                        const double by = 1.0 / (1.0 + exp(-x)) + static_cast<double>(a.bias[expert]);
+                        if (by > -INFINITY) wide = order_key(by);
                     }
+                    int rank = 0;
+                    for (int i = 0; i < m; ++i) {
+                        const uint64_t w = __shfl_sync(0xffffffffu, wide, i);
+                        const int e = __shfl_sync(0xffffffffu, expert, i);
+                        rank += w > wide || (w == wide && e < expert) ? 1 : 0;
+                    }
+                    if (wide == 0) rank = 32;
+                    int mine = -1;
+                    for (int i = 0; i < m; ++i) {
+                        const int r = __shfl_sync(0xffffffffu, rank, i);
+                        const int e = __shfl_sync(0xffffffffu, expert, i);
+                        if (r == lane) mine = e;
+                    }
+                    expert = mine;
                 }
-                expert = -1;
-                choose(wide, 0, k, lane, expert, wat);
             }
         }
-        if (lane >= k) expert = -1;
+        if (wide_all) {
+            uint64_t wide[PL], wat = 0;
+            double sum = 1.0;
+            if (soft) {
+                sum = 0.0;
+#pragma unroll 1
+                for (int i = 0; i < PL; ++i) {
+                    const int e = i * 32 + lane;
+                    if (e < a.E) sum += exp(static_cast<double>(to_f32<kType>(row, e)) - static_cast<double>(top));
+                }
+                sum = warp_sum(sum);
+            }
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const int e = i * 32 + lane;
+                wide[i] = 0;
+                if (e < a.E && v[i] > -INFINITY) {
+                    const double x = v[i];
+                    const double s = soft ? exp(x - static_cast<double>(top)) / sum : 1.0 / (1.0 + exp(-x));
+                    const double by = s + static_cast<double>(a.bias[e]);
+                    if (by > -INFINITY) wide[i] = order_key(by);
+                }
+            }
+            expert = -1;
+            choose(wide, 0, k, lane, expert, wat);
+        }
     }
+    if (lane >= k) expert = -1;
     // the weights, from the chosen logits
     float w = 0.0f;
     if (expert >= 0) {
@@ -237,9 +322,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
 }
 
 // Tokens of a CTA and of a warp.
-__host__ __device__ inline int route_ctas(int M, int sms) {
-    // up to four tokens a warp one CTA does it all: the second launch costs more
-    return M <= 4 * kRouteWarps ? 1 : (M + kRouteWarps - 1) / kRouteWarps < sms ? (M + kRouteWarps - 1) / kRouteWarps : sms;
+inline int route_ctas(int M, int E, int sms) {
+    // up to a token a warp one CTA does it all (64 tokens, 256 experts: 10.4 us; over
+    // eight CTAs with the second launch 8.7)
+    const int warps = route_warps(E), ctas = (M + 7) / 8;
+    return M <= warps ? 1 : ctas < sms ? ctas : sms;
 }
 
 // The CTAs' counts by expert: 16 bits each (a CTA has at most 2^20 / 64 tokens, each
@@ -268,22 +355,28 @@ __device__ __forceinline__ void prefix_experts(const int* total, int* where, int
     __syncthreads();
 }
 
+constexpr int kHeldTokens = 4;   // of a warp
+
 template <int kType, int PL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a, int chunk) {
+__global__ void __launch_bounds__(kRouteWarps<PL> * 32) route_kernel(const RouteArgs a, int chunk) {
+    constexpr int kWarps = kRouteWarps<PL>;
     extern __shared__ int route_smem[];
     int* count = route_smem;                        // [warps][E]
-    int* total = route_smem + kRouteWarps * a.E;    // [E]
+    int* total = route_smem + kWarps * a.E;    // [E]
     int* where = total + a.E;                       // [E + 1]
+    // a warp's choices, where they are few: expert, and place among the warp's
+    __shared__ ushort2 held[kWarps][kHeldTokens][32];
+    __shared__ uint2 sorting[kWarps][32];
     grid_dependents_launch();
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < kRouteWarps * a.E; i += kRouteWarps * 32) count[i] = 0;
+    for (int i = threadIdx.x; i < kWarps * a.E; i += kWarps * 32) count[i] = 0;
     grid_dependency_wait();
     __syncthreads();
     // contiguous tokens to a CTA, and of those to a warp
     const int c0 = blockIdx.x * chunk;
     const int c1 = c0 + chunk < a.M ? c0 + chunk : a.M;
-    const int each = (chunk + kRouteWarps - 1) / kRouteWarps;
+    const int each = (chunk + kWarps - 1) / kWarps;
     const int t0 = c0 + warp * each;
     const int t1 = t0 + each < c1 ? t0 + each : c1;
     int* mine = count + warp * a.E;
@@ -291,23 +384,32 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     for (int m = t0; m < t1; ++m) {
         int expert;
         float weight;
-        route_token<kType, PL>(a, static_cast<const uint8_t*>(a.logits) + m * a.ld * size, lane, expert, weight);
+        route_token<kType, PL>(a, static_cast<const uint8_t*>(a.logits) + m * a.ld * size, lane, sorting[warp], expert, weight);
         if (lane < a.top_k) {
             const int64_t at = static_cast<int64_t>(m) * a.top_k + lane;
             a.experts[at] = expert;
             a.weights[at] = weight;
-            a.rows[at] = expert >= 0 ? mine[expert]++ : -1;   // among this warp's; a token's experts differ
+            // its place among the warp's choices of the expert; a token's experts differ
+            const int place = expert >= 0 ? mine[expert]++ : -1;
+            if (each <= kHeldTokens) held[warp][m - t0][lane] = make_ushort2(static_cast<uint16_t>(expert), static_cast<uint16_t>(place));
+            else a.rows[at] = place;
         }
         __syncwarp();
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kRouteWarps * 32) {
+    for (int e = threadIdx.x; e < a.E; e += kWarps * 32) {
         int sum = 0;
+        constexpr int kBatch = 16;   // loads on the way at a time
 #pragma unroll
-        for (int w = 0; w < kRouteWarps; ++w) {
-            const int n = count[w * a.E + e];
-            count[w * a.E + e] = sum;
-            sum += n;
+        for (int w0 = 0; w0 < kWarps; w0 += kBatch) {
+            int n[kBatch];
+#pragma unroll
+            for (int w = 0; w < kBatch; ++w) n[w] = count[(w0 + w) * a.E + e];
+#pragma unroll
+            for (int w = 0; w < kBatch; ++w) {
+                count[(w0 + w) * a.E + e] = sum;
+                sum += n[w];
+            }
         }
         total[e] = sum;
         if (gridDim.x > 1)
@@ -316,7 +418,16 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     __syncthreads();
     if (gridDim.x == 1) {
         prefix_experts(total, where, a.E);
-        for (int e = threadIdx.x; e <= a.E; e += kRouteWarps * 32) a.offsets[e] = where[e];
+        for (int e = threadIdx.x; e <= a.E; e += kWarps * 32) a.offsets[e] = where[e];
+    }
+    if (each <= kHeldTokens) {
+        for (int m = t0; m < t1; ++m) {
+            if (lane >= a.top_k) continue;
+            const ushort2 h = held[warp][m - t0][lane];
+            a.rows[static_cast<int64_t>(m) * a.top_k + lane] =
+                h.x == 0xFFFFu ? -1 : h.y + mine[h.x] + (gridDim.x == 1 ? where[h.x] : 0);
+        }
+        return;
     }
     for (int64_t i = static_cast<int64_t>(t0) * a.top_k + lane; i < static_cast<int64_t>(t1) * a.top_k; i += 32) {
         const int e = a.experts[i];
@@ -326,36 +437,33 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
 
 // Behind route_kernel on several CTAs: where each expert's rows begin, and the
 // rows of this CTA's choices, from all CTAs' counts.
-constexpr int kPlaceThreads = 512;
+constexpr int kPlaceThreads = 1024;
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteArgs a, int chunk) {
     extern __shared__ int route_smem[];
     int* total = route_smem;            // [E]: of all CTAs
     int* front = total + a.E;           // [E]: of the CTAs in front
     int* where = front + a.E;           // [E + 1]
     grid_dependents_launch();
-    for (int e = threadIdx.x; e < 2 * a.E; e += kPlaceThreads) total[e] = 0;
     grid_dependency_wait();
-    __syncthreads();
-    // A thread adds up eight experts over a share of the CTAs, sixteen of their
-    // rows on the way at a time (a value a thread and load: 13 us).  Whole numbers, so
-    // that the order of the additions does not show.
+    // A warp adds up eight experts at a time, a lane a share of the CTAs.
     const uint4* table = static_cast<const uint4*>(a.ws);
     const int ctas = gridDim.x;
     const int groups = route_pitch(a.E) / 8;
-    const int parts = kPlaceThreads / groups;   // groups <= 128
-    const int g = threadIdx.x % groups, part = threadIdx.x / groups;
-    if (part < parts) {
-        const int b0 = part * ctas / parts, b1 = (part + 1) * ctas / parts;
+    const int lane = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < groups; g += kPlaceThreads / 32) {
         int all[8] = {}, before[8] = {};
-        for (int b = b0; b < b1; b += 16) {
-            uint4 w[16];
+        constexpr int kBatch = 5;   // loads on the way at a time: of up to 160 CTAs, all
+        for (int b0 = lane; b0 < ctas; b0 += 32 * kBatch) {
+            uint4 w[kBatch];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                w[i] = b + i < b1 ? __ldcg(table + static_cast<int64_t>(b + i) * groups + g) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < kBatch; ++i) {
+                const int b = b0 + 32 * i;
+                w[i] = b < ctas ? __ldcg(table + static_cast<int64_t>(b) * groups + g) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kBatch; ++i) {
                 const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                const bool front_of = b + i < static_cast<int>(blockIdx.x);
+                const bool front_of = b0 + 32 * i < static_cast<int>(blockIdx.x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int lo = static_cast<int>(u[e] & 0xFFFFu), hi = static_cast<int>(u[e] >> 16);
@@ -369,9 +477,10 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = 8 * g + i;
-            if (e < a.E) {
-                atomicAdd(total + e, all[i]);
-                atomicAdd(front + e, before[i]);
+            const int t = __reduce_add_sync(0xffffffffu, all[i]), f = __reduce_add_sync(0xffffffffu, before[i]);
+            if (lane == 0 && e < a.E) {
+                total[e] = t;
+                front[e] = f;
             }
         }
     }
@@ -390,14 +499,14 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteA
 
 template <int kType, int PL>
 cudaError_t launch_route_pl(const RouteArgs& a, const LaunchCtl& c, cudaStream_t st) {
-    const int ctas = route_ctas(a.M, c.num_sms);
+    const int ctas = route_ctas(a.M, a.E, c.num_sms);
     const int chunk = a.M > 0 ? (a.M + ctas - 1) / ctas : 1;
     cudaLaunchAttribute attr;
-    const size_t smem = (kRouteWarps + 2) * a.E * sizeof(int) + sizeof(int);
+    const size_t smem = (kRouteWarps<PL> + 2) * a.E * sizeof(int) + sizeof(int);
     static std::atomic<uint64_t> configured{0};
-    cudaError_t e = set_smem_once(configured, route_kernel<kType, PL>, (kRouteWarps + 2) * 32 * PL * 4 + 4);
+    cudaError_t e = set_smem_once(configured, route_kernel<kType, PL>, (kRouteWarps<PL> + 2) * 32 * PL * 4 + 4);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = config(static_cast<unsigned>(ctas), kRouteWarps * 32, smem, st, &attr);
+    cudaLaunchConfig_t cfg = config(static_cast<unsigned>(ctas), kRouteWarps<PL> * 32, smem, st, &attr);
     e = cudaLaunchKernelEx(&cfg, route_kernel<kType, PL>, a, chunk);
     if (e != cudaSuccess || ctas == 1) return e;
     cfg = config(static_cast<unsigned>(ctas), kPlaceThreads, (3 * a.E + 1) * sizeof(int), st, &attr);
@@ -718,7 +827,7 @@ cudaError_t launch_combine_type(const CombineArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t route_workspace_bytes(int M, int E, int sms) {
-    const int ctas = route_ctas(M, sms);
+    const int ctas = route_ctas(M, E, sms);
     return ctas > 1 ? static_cast<size_t>(ctas) * route_pitch(E) * sizeof(uint16_t) : 0;
 }
 
