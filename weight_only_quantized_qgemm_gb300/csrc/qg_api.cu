@@ -868,7 +868,7 @@ qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_sca
     if ((K > 0 && (!aligned16(Xq) || !aligned16(W) || !aligned16(X_scale) || ldxq % 16 != 0 || ldsx % 4 != 0)) ||
         (reinterpret_cast<uintptr_t>(W_scale) & 3u) || (reinterpret_cast<uintptr_t>(offsets) & 3u) || (reinterpret_cast<uintptr_t>(Y) & y_mask))
         return QG_ERR_MISALIGNED;
-    const int nt = grouped_tile_rows(R, E);
+    const int nt = grouped_tile_rows(R, E, K);
     // tiles are counted in 32 bits
     if ((static_cast<int64_t>(R) / nt + E) * ((N + 127) / 128) > (int64_t(1) << 30)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();

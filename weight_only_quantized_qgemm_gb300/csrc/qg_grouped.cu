@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
         const int g = fw >> 2;            // columns g kCols ..
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + g * kCols;
         uint8_t* out = gbase + L::kOutOff + fw * L::kOutWarp;
-        constexpr int kChunk = kCols < 32 ? kCols : 32;   // columns of a TMEM load
+        constexpr int kChunk = kCols % 32 == 0 ? 32 : 16;   // columns of a TMEM load
+        static_assert(kCols % kChunk == 0, "whole loads");
         Ring<kBufs> rb(0);
         Ring<L::kSSlots> rg(0);
         Pl at;
@@ -902,15 +903,28 @@ cudaError_t launch_grouped_nt(const GroupedArgs& a, const CUtensorMap& tmW, cons
 
 }  // namespace
 
-int grouped_tile_rows(int R, int E) {
+// By the mean number of rows of an expert, as far as the host knows it.  Narrow
+// tiles fold fewer columns that hold nothing, wide ones read a large group's
+// weights fewer times, and the pair's tiles win from where the MMAs count, on a short
+// K later (an epilogue a few units).  Measured in us for 16 / 32 / 64 / 256 rows a
+// tile, groups of unlike sizes (the largest five times the mean):
+//   rows      64 experts, 4096 x 2048    16 experts, 2048 x 5120   20 experts, 1003 x 1040
+//     8       81 /  81 /  82 / 114       27 / 28 / 30 / 39         10 / 10 / 11 / 16
+//    12       89 /  80 /  83 / 116       31 / 27 / 30 / 39         11 / 12 / 12 / 16
+//    24      111 /  92 /  89 / 117       39 / 33 / 29 / 40         14 / 13 / 15 / 23
+//    48      176 / 125 / 114 / 120       54 / 41 / 42 / 41         18 / 17 / 17 / 25
+//    64      224 / 153 / 137 / 127       70 / 50 / 45 / 42         21 / 18 / 18 / 26
+//    96      312 / 210 / 177 / 132       94 / 59 / 58 / 41         28 / 23 / 25 / 26
+int grouped_tile_rows(int R, int E, int K) {
     const int64_t mean = R / E;
-    return mean <= 8 ? 16 : mean <= 48 ? 64 : 256;
+    return mean <= 10 ? 16 : mean <= 20 ? 32 : mean <= (K < 2048 ? 96 : 52) ? 64 : 256;
 }
 
 cudaError_t launch_grouped(const GroupedArgs& a, const CUtensorMap& tmW, const CUtensorMap& tmX, const LaunchCtl& c,
                            cudaStream_t st) {
-    switch (grouped_tile_rows(a.R, a.E)) {
+    switch (grouped_tile_rows(a.R, a.E, a.K)) {
         case 16: return launch_grouped_nt<16, false>(a, tmW, tmX, c, st);
+        case 32: return launch_grouped_nt<32, false>(a, tmW, tmX, c, st);
         case 64: return launch_grouped_nt<64, false>(a, tmW, tmX, c, st);
         default: return launch_grouped_nt<256, true>(a, tmW, tmX, c, st);
     }
