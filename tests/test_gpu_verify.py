@@ -219,3 +219,84 @@ def test_distribution_is_the_targets(q):
     want = torch.softmax(t[0, 0].double(), dim=0) * B
     seen = torch.bincount(got.tokens[:, 0], minlength=V).double()
     assert float(((seen - want) ** 2 / want).sum()) < 60
+
+
+# sequences enough that the rows' sums come from a kernel of their own
+MANY = [(24, 3, 20011), (64, 5, 9000), (20, 31, 8192), (130, 1, 8193), (40, 0, 12000)]
+
+
+@pytest.mark.parametrize("B,G,V", MANY)
+@pytest.mark.parametrize("dtype,pad", [("bf16", 0), ("bf16", 3), ("fp16", 8), ("fp32", 1), ("fp32", 4)])
+def test_many_sequences(q, B, G, V, dtype, pad):
+    t, d, tok, u, e = problem(B, G, V, dtype, B + G * 5 + V, pad)
+    lengths = torch.randint(-1, G + 2, (B,), device="cuda", dtype=torch.int32)
+    check(q, t, tok, draft=d, uniform=u, noise=e)
+    check(q, t, tok, draft=d, uniform=u, noise=e, lengths=lengths)
+    if G:
+        tok = torch.where(torch.rand(B, G, device="cuda") < 0.7, t[:, :G].float().argmax(dim=2), tok)
+    check(q, t, tok, uniform=u, noise=e, lengths=lengths)
+    check(q, t, tok, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_odd_rows_of_many_sequences(q, dtype):
+    B, G, V = 30, 2, 9001
+    t, d, tok, u, e = problem(B, G, V, dtype, 5, 7)
+    keep = torch.rand(V, device="cuda") < 0.01
+    keep[:4] = True
+    t[0] = torch.where(keep, t[0], -math.inf)
+    d[1] = torch.where(keep, d[1], -math.inf)
+    t[2, 0] = -math.inf
+    t[3, 1, 17] = math.nan
+    t[4, 0, V - 1] = math.inf
+    d[5, 0] = -math.inf
+    d[6, 1, 3] = math.nan
+    t[7] = torch.where(keep, t[7], torch.finfo(DTYPES[dtype]).min)
+    tok[8, 0], tok[9, 1] = -5, V
+    tok[10, 0] = 7
+    t[10, 0, 7] = -math.inf
+    d[10, 0, 7] = -math.inf
+    t[11, 2] = math.nan
+    check(q, t, tok, draft=d, uniform=u, noise=e, most_unsure=0.2)
+    check(q, t, tok, uniform=u, noise=e, most_unsure=0.2)
+    check(q, t, tok, most_unsure=0.2)
+    # the same sequences a few at a time, which one kernel does alone
+    whole = q.verify_drafts(t, tok, d, u, e)
+    for a in range(0, B, 5):
+        part = q.verify_drafts(t[a:a + 5], tok[a:a + 5], d[a:a + 5], u[a:a + 5], e[a:a + 5])
+        assert torch.equal(part.accepted, whole.accepted[a:a + 5])
+
+
+@pytest.mark.parametrize("B", [2, 40])
+@pytest.mark.parametrize("V", [257, 9000])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_rows_of_the_lowest_value(q, B, V, dtype):
+    """All logits equal, as low (or as high) as the type goes: every token is as
+    likely, so that the race goes to the least noise."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    e = torch.empty(B, V, device="cuda").exponential_(generator=g)
+    tok = torch.zeros((B, 1), dtype=torch.int64, device="cuda")
+    u = torch.full((B, 1), 0.5, device="cuda")
+    for value in (torch.finfo(DTYPES[dtype]).min, torch.finfo(DTYPES[dtype]).max):
+        t = torch.full((B, 2, V), value, dtype=DTYPES[dtype], device="cuda")
+        got = q.verify_drafts(t[:, :1], tok[:, :0], None, u[:, :0], e)
+        assert got.tokens[:, 0].tolist() == e.argmin(dim=1).tolist()
+        # a draft of the same rows is kept, a certain one at 1 / V is not
+        got = q.verify_drafts(t, tok, t[:, :1], u, e)
+        assert got.accepted.tolist() == [1] * B and got.tokens[:, 1].tolist() == e.argmin(dim=1).tolist()
+        got = q.verify_drafts(t, tok, None, u, e)
+        assert got.accepted.tolist() == [0] * B
+        assert got.tokens[:, 0].tolist() == (e[:, 1:].argmin(dim=1) + 1).tolist()
+
+
+@pytest.mark.parametrize("B", [3, 24])
+def test_far_logits(q, B):
+    """Rows whose largest logit lies far from 0, where a logit's neighbours are
+    whole numbers apart."""
+    V = 9000
+    t, d, tok, u, e = problem(B, 2, V, "fp32", B)
+    shift = torch.tensor([8e6, -7e6, 1e3], device="cuda").repeat(B // 3)[:, None, None]
+    t, d = (t * 4).round() + shift, (d * 4).round() - shift
+    check(q, t, tok, draft=d, uniform=u, noise=e)
+    check(q, t, tok, uniform=u, noise=e)
+    check(q, t, tok)

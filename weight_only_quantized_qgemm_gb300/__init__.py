@@ -724,7 +724,7 @@ def _scratch(key, ask, workspace, device):
         return None, None, 0
     if workspace is None:
         torch = _torch()
-        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        buf = torch.empty((need,), dtype=torch.uint8, device=device)
     else:
         buf = workspace.get(need) if isinstance(workspace, Workspace) else workspace
     return buf, buf.data_ptr(), buf.numel() * buf.element_size()

@@ -501,7 +501,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // few do.  (Each lane against its own best: some lane of 32 had one for
         // almost every token, and the race took 20 us of 62.)
         constexpr float kSlack = 2e-5f;
-        const float tl = t.m * kLog2e, sl = s.m * kLog2e;
         auto race = [&](bool with_q, Best& result) {
             Best top{0.0f, 0x7FFFFFFF};
             float reach = 0.0f;
@@ -525,10 +524,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 float low = reach;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float p = ex2(__fmaf_rn(x[j], kLog2e, -tl)) * pr;
+                    const float p = ex2((x[j] - t.m) * kLog2e) * pr;   // t.m may be near a type's lowest value
                     float w = p;
                     if (with_q) {
-                        if (drow != nullptr) w -= ex2(__fmaf_rn(y[j], kLog2e, -sl)) * qr;
+                        if (drow != nullptr) w -= ex2((y[j] - s.m) * kLog2e) * qr;
                         else if (v + j * step == d) w -= 1.0f;
                     }
                     float r;
@@ -549,28 +548,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (vectors) {   // slices begin at multiples of 32
                 const int nvec = (v1 - v0) / kVec;
                 v_done = v0 + nvec * kVec;
-                // loads of several turns on the way at a time
-                constexpr int kTurns = El::kSize == 4 ? 1 : 2;
-                for (int i0 = 32 * warp; i0 < nvec; i0 += kThreads * kTurns) {
-                    typename El::Raw8 xr[kTurns], yr[kTurns];
-                    Elem<QG_FP32>::Raw8 er[kTurns];
-#pragma unroll
-                    for (int u = 0; u < kTurns; ++u) {
-                        int i = i0 + lane + kThreads * u;
-                        i = i < nvec ? i : nvec - 1;
-                        xr[u] = El::load8(trow, v0 + i * kVec);
-                        yr[u] = El::load8(with_q && drow != nullptr ? drow : trow, v0 + i * kVec);
-                        er[u] = Elem<QG_FP32>::load8(noise, v0 + i * kVec);
-                    }
-#pragma unroll
-                    for (int u = 0; u < kTurns; ++u) {
-                        const int i = i0 + lane + kThreads * u;
-                        float x[kVec], y[kVec], e[kVec];
-                        El::wide8(xr[u], x);
-                        El::wide8(yr[u], y);
-                        Elem<QG_FP32>::wide8(er[u], e);
-                        enter(i < nvec ? v0 + i * kVec : v1, 1, x, y, e);
-                    }
+                for (int i0 = 32 * warp; i0 < nvec; i0 += kThreads) {
+                    const int i = i0 + lane < nvec ? i0 + lane : nvec - 1;
+                    float x[kVec], y[kVec], e[kVec];
+                    const typename El::Raw8 xr = El::load8(trow, v0 + i * kVec);
+                    const typename El::Raw8 yr = El::load8(with_q && drow != nullptr ? drow : trow, v0 + i * kVec);
+                    const Elem<QG_FP32>::Raw8 er = Elem<QG_FP32>::load8(noise, v0 + i * kVec);
+                    El::wide8(xr, x);
+                    El::wide8(yr, y);
+                    Elem<QG_FP32>::wide8(er, e);
+                    enter(i0 + lane < nvec ? v0 + i * kVec : v1, 1, x, y, e);
                 }
             }
             for (int v = v_done + 32 * warp; v < v1; v += kThreads * kVec) {
