@@ -64,8 +64,10 @@ typedef enum {
     QG_ERR_UNSUPPORTED_SHAPE = 2, /* M > 32 (65536 for W8A8, INT8), K % 16 (FP8, W8A8, INT8), K % 128 (LUT3)
                                      or K % 8 (BF16) != 0, more than 2^29 tiles
                                      of 128 x 32 (W8A8) or 128 x 16 (INT8); log probabilities: V == 0 or > 2^30, top_k > V or
-                                     > QG_MAX_TOP_K */
-    QG_ERR_MISALIGNED = 3,        /* a pointer or row stride breaks the 16-byte rule */
+                                     > QG_MAX_TOP_K; layers of experts and drafts: beyond the
+                                     bounds that stand at each call */
+    QG_ERR_MISALIGNED = 3,        /* a pointer or row stride breaks the 16-byte rule (or, where a
+                                     call asks for no more, its elements' alignment) */
     QG_ERR_CUDA = 4,              /* a CUDA runtime call or kernel launch failed */
     QG_ERR_TIMEOUT = 5,           /* a bounded in-kernel wait ran out */
     QG_ERR_WORKSPACE = 6          /* workspace missing or smaller than qg_workspace_bytes */
@@ -421,7 +423,8 @@ enum { QG_SCORE_SOFTMAX = 0, QG_SCORE_SIGMOID = 1 };
  *   s[e] = softmax(logits[m])[e]  or  1 / (1 + exp(-logits[m, e])),
  * the top_k experts are those of the largest s[e] + bias[e] (without a bias in
  * the order of the logits), ties to the lower index, and their weights are
- *   w = s[e] * scale / (sum of s over the chosen ones)   (renormalize != 0)
+ *   w = s[e] * scale / (sum of s over the chosen ones)   (renormalize != 0; 0 where
+ *       all chosen scores are below 2^-995)
  *   w = s[e] * scale                                     (else).
  * Which experts are chosen does not depend on rounding: scores with a bias that
  * lie closer than their FP32 error are compared in 64 bits.
@@ -436,7 +439,8 @@ enum { QG_SCORE_SOFTMAX = 0, QG_SCORE_SIGMOID = 1 };
  *   rows     device, int32 [M, top_k]: the row of each choice; -1 beside a -1
  *   M, E, top_k   0 <= M <= 2^20, 1 <= E <= QG_MAX_EXPERTS, 1 <= top_k <= E, 32
  *   workspace     of qg_moe_route_workspace_bytes(M, E) bytes, 16-byte aligned, scratch
- *                 (nothing is expected in it)
+ *                 (nothing is expected in it; calls that may run at the same time, of
+ *                 captured graphs too, need one each)
  * With M = 0 only offsets are written (zeros).
  */
 size_t qg_moe_route_workspace_bytes(int M, int E);
@@ -459,7 +463,8 @@ qg_status qg_moe_route(const void *logits, int type, int64_t ld, const float *bi
  *   Xq       device, E4M3 codes [out_rows, ldxq], 16-byte aligned, ldxq >= K, ldxq % 16 == 0
  *   X_scale  device, FP32 [ceil(K/128), ldsx], 16-byte aligned, ldsx >= out_rows,
  *            ldsx % 4 == 0
- *   M, out_rows, K   0 <= M <= 2^22, 0 <= out_rows < 2^31, K % 16 == 0, 1 <= top_k <= 32
+ *   M, out_rows, K   0 <= M <= 2^22, 0 <= out_rows < 2^31, K % 16 == 0, K <= 2^30,
+ *            1 <= top_k <= 32
  */
 qg_status qg_quantize_rows_e4m3(const void *X, int x_type, int64_t ldx, int gated, const int32_t *rows, int top_k,
                                 const int32_t *num_rows, uint8_t *Xq, int64_t ldxq, float *X_scale, int64_t ldsx,
@@ -479,7 +484,8 @@ qg_status qg_quantize_rows_e4m3(const void *X, int x_type, int64_t ldx, int gate
  *   offsets  device, int32 [E + 1], ascending, within 0 .. R (entries that are not
  *            are taken as the nearest that are)
  *   Y        device, QG_BF16, QG_FP16 or QG_FP32 [R, ldy], ldy >= N
- *   R, E, N, K   0 <= R <= 2^24, 1 <= E <= QG_MAX_EXPERTS, E N < 2^31, K % 16 == 0
+ *   R, E, N, K   0 <= R <= 2^24, 1 <= E <= QG_MAX_EXPERTS, E N < 2^31 - 256,
+ *            K % 16 == 0, K <= 2^30
  * Tiles are not split along K, so that no workspace is needed and a row's result
  * does not depend on the other rows' values.
  */
@@ -495,7 +501,8 @@ qg_status qgemm_w8a8_grouped(const uint8_t *Xq, int64_t ldxq, const float *X_sca
  *   Y, residual (or NULL), out   device, QG_BF16, QG_FP16 or QG_FP32 (type), row
  *            strides ldy, ldr, ldo >= K; out may be residual
  *   rows, weights   device, int32 and FP32 [M, top_k]
- *   M, R, K, top_k  0 <= M <= 2^22, 0 <= R < 2^31, 1 <= top_k <= 32
+ *   M, R, K, top_k  0 <= M <= 2^22, 0 <= R < 2^31, K <= 2^30, M K <= 2^38,
+ *            1 <= top_k <= 32
  */
 qg_status qg_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *rows, const float *weights, int top_k,
                          const void *residual, int64_t ldr, void *out, int64_t ldo, int M, int R, int K,
@@ -531,7 +538,7 @@ qg_status qg_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *ro
  *   accepted    device, int32 [B];  tokens_out  device, int64 [B, G + 1]
  *   B, G, V     0 <= B <= 65536, 0 <= G <= QG_MAX_DRAFTS, 1 <= V <= 2^30
  *   workspace   of qg_verify_drafts_workspace_bytes(B, G, V) bytes (0 for few
- *               sequences), 16-byte aligned, scratch (nothing is expected in it)
+ *               sequences), 16-byte aligned, scratch as qg_moe_route's
  * A row with a NaN or +inf (greedy: a NaN is never the largest), or with nothing
  * but -inf, keeps no draft, and the token drawn from it is -1.  Rows behind a
  * sequence's length are not read.

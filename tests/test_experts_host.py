@@ -65,6 +65,7 @@ def test_route_argument_validation(qg, args, expect):
     ((FAKE, 0, 512, 0, FAKE, 2, None, FAKE, 512, FAKE, 32, 8, 16, 504), 2),
     ((FAKE, 0, 512, 0, FAKE, 33, None, FAKE, 512, FAKE, 32, 8, 16, 512), 2),
     ((FAKE, 0, 512, 0, FAKE, 2, None, FAKE, 512, FAKE, 32, 2 ** 22 + 1, 16, 512), 2),
+    ((FAKE, 0, 2 ** 31, 0, FAKE, 2, None, FAKE, 2 ** 31, FAKE, 32, 8, 16, 2 ** 30 + 16), 2),
     ((FAKE + 8, 0, 512, 0, FAKE, 2, None, FAKE, 512, FAKE, 32, 8, 16, 512), 3),
     ((FAKE, 0, 516, 0, FAKE, 2, None, FAKE, 512, FAKE, 32, 8, 16, 512), 3),
     ((FAKE, 0, 512, 0, FAKE, 2, None, FAKE, 520, FAKE, 32, 8, 16, 512), 3),
@@ -93,6 +94,7 @@ def test_row_quantiser_argument_validation(qg, args, expect):
     ((FAKE, 512, FAKE, 36, FAKE, FAKE, FAKE, FAKE, 0, 256, 40, 8, 256, 512), 1),   # ldsx < R
     ((FAKE, 512, FAKE, 64, FAKE, FAKE, FAKE, FAKE, 0, 255, 40, 8, 256, 512), 1),
     ((FAKE, 520, FAKE, 64, FAKE, FAKE, FAKE, FAKE, 0, 256, 40, 8, 256, 520), 2),
+    ((FAKE, 2 ** 31, FAKE, 64, FAKE, FAKE, FAKE, FAKE, 0, 256, 40, 8, 256, 2 ** 31 - 16), 2),
     ((FAKE, 512, FAKE, 64, FAKE, FAKE, FAKE, FAKE, 0, 256, 40, 1025, 256, 512), 2),
     ((FAKE, 512, FAKE, 2 ** 25, FAKE, FAKE, FAKE, FAKE, 0, 256, 2 ** 24 + 1, 8, 256, 512), 2),
     ((FAKE, 512, FAKE, 64, FAKE, FAKE, FAKE, FAKE, 0, 2 ** 31, 40, 8, 2 ** 28, 512), 2),   # E N = 2^31
@@ -127,6 +129,7 @@ def test_grouped_argument_validation(qg, args, expect):
     ((FAKE, 0, 256, FAKE, FAKE, 33, None, 0, FAKE, 256, 8, 16, 256), 2),
     ((FAKE, 0, 256, FAKE, FAKE, 2, None, 0, FAKE, 256, 2 ** 22 + 1, 16, 256), 2),
     ((FAKE, 0, 2 ** 30, FAKE, FAKE, 2, None, 0, FAKE, 2 ** 30, 2 ** 10, 16, 2 ** 29), 2),
+    ((FAKE, 0, 2 ** 31, FAKE, FAKE, 2, None, 0, FAKE, 2 ** 31, 1, 16, BIG), 2),
     ((FAKE + 1, 0, 256, FAKE, FAKE, 2, None, 0, FAKE, 256, 8, 16, 256), 3),
     ((FAKE, 2, 256, FAKE, FAKE, 2, FAKE + 2, 256, FAKE, 256, 8, 16, 256), 3),
     ((FAKE, 0, 256, FAKE + 2, FAKE, 2, None, 0, FAKE, 256, 8, 16, 256), 3),

@@ -391,3 +391,41 @@ def test_combine_strides(q):
     ref = (Y[:, 3:67].double().reshape(6, 2, 64) * w.double()[:, :, None]).sum(dim=1)
     assert bool(((out[:, 1:65].double() - ref).abs() <= 2.0 ** -22 * ref.abs() + 1e-6).all())
     assert bool((out[:, 0] == 9).all()) and bool((out[:, 65:] == 9).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_chosen_scores_far_from_one(q, dtype, score):
+    """Renormalized weights are ratios, however small the scores are: a bias keeps the
+    largest logit out, and the sigmoids of the others are below what 32 bits hold."""
+    M, E, k = 40, 50, 5
+    g = gen(12)
+    logits = torch.randn(M, E, generator=g, device="cuda") * 3
+    logits -= torch.tensor([0.0, 55.0, 62.0, 90.0, 105.0, 400.0, 600.0, 2000.0], device="cuda").repeat(M // 8)[:, None]
+    logits[:, 0] = 50.0
+    bias = torch.zeros(E, device="cuda")
+    bias[0] = -math.inf
+    check_route(q, logits.to(DTYPES[dtype]), k, score=score, bias=bias)
+    check_route(q, logits[:, 1:].to(DTYPES[dtype]), k, score=score, scale=2.5)
+
+
+def test_workspaces_of_calls_with_counters_stay_clean(q):
+    """One Workspace for scratch memory and for a GEMM whose workspace has to be zero
+    before its first use."""
+    ws = q.Workspace()
+    M, E = 20000, 1024
+    logits = torch.randn(M, E, device="cuda")
+    a, b = q.moe_route(logits, 4, workspace=ws), q.moe_route(logits, 4)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    B, G, V = 2000, 4, 8192
+    target = torch.randn(B, G + 1, V, device="cuda").to(torch.bfloat16)
+    tok = target[:, :G].float().argmax(dim=2)
+    q.verify_drafts(target, tok, workspace=ws)
+    scratch = ws.buf
+    assert scratch.numel() >= B * (2 * G + 1) * (V // 2048) * 8
+    buf = ws.get(1 << 16)
+    assert buf.data_ptr() != scratch.data_ptr() and not bool(buf.any())
+    with pytest.raises(ValueError):
+        q.moe_route(logits, 4, workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(q.QgemmError):
+        q.moe_route(logits, 4, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))

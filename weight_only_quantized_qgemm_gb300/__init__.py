@@ -205,13 +205,14 @@ def workspace_bytes(kind: int, M: int, N: int, K: int) -> int:
 
 
 # the kinds whose workspaces share a layout: each of these alone, all others together
-_OWN_LAYOUT = (KIND_W8A8, KIND_INT8)
+_SCRATCH = "scratch"   # of calls that keep no counters
+_OWN_LAYOUT = (KIND_W8A8, KIND_INT8, _SCRATCH)
 
 
 class Workspace:
     """Zero-filled device byte buffers that grow on demand, one for each
-    workspace layout (the W8A8 and INT8 kinds have their own, the others share
-    one).  Calls leave their arrival counters at zero again (the rest is
+    workspace layout (the W8A8 and INT8 kinds and calls with scratch memory alone
+    have their own, the others share one).  Calls leave their arrival counters at zero again (the rest is
     scratch), so one Workspace serves any sequence of calls of any kind on one
     stream (calls that may run at the same time, on different streams, need one
     each).  Growing synchronises the device, so that the zero fill has landed
@@ -726,7 +727,9 @@ def _scratch(key, ask, workspace, device):
         torch = _torch()
         buf = torch.empty((need,), dtype=torch.uint8, device=device)
     else:
-        buf = workspace.get(need) if isinstance(workspace, Workspace) else workspace
+        buf = workspace.get(need, _SCRATCH) if isinstance(workspace, Workspace) else workspace
+        if buf.device != device or not buf.is_contiguous():
+            raise ValueError("the workspace must be contiguous, on the tensors' device")
     return buf, buf.data_ptr(), buf.numel() * buf.element_size()
 
 
@@ -751,7 +754,9 @@ def moe_route(logits, top_k: int, score: str = "softmax", bias=None, renormalize
     are offsets[e] .. offsets[e + 1] - 1, in the order of the tokens; rows[m, j] is
     the row of token m's j-th choice.  Where fewer than top_k experts are left,
     experts and rows are -1 and the weight 0; a token with a NaN or +inf logit is
-    routed nowhere, with weights of NaN.
+    routed nowhere, with weights of NaN.  workspace (optional, a :class:`Workspace` or
+    uint8 tensor): scratch memory, which calls that may run at the same time must not
+    share; without one every call makes its own.
     """
     if stream is not None and _elsewhere(stream):
         return _on_stream(stream, moe_route, logits, top_k, score, bias, renormalize, scale, workspace)
@@ -1008,6 +1013,7 @@ def verify_drafts(target_logits, draft_tokens, draft_logits=None, uniform=None, 
     largest ratio of probability to noise.  Without uniform and noise: greedy, drafts
     are kept while they are the largest logit, and the largest follows.  (A row with
     a NaN, +inf or nothing left keeps no draft and yields -1; see include/qgemm.h.)
+    workspace: as :func:`moe_route`'s.
     """
     if stream is not None and _elsewhere(stream):
         return _on_stream(stream, verify_drafts, target_logits, draft_tokens, draft_logits, uniform, noise, lengths,

@@ -839,13 +839,11 @@ qg_status qg_quantize_rows_e4m3(const void* X, int x_type, int64_t ldx, int gate
         return QG_ERR_INVALID_ARG;
     if (M == 0 || K == 0 || out_rows == 0) return QG_OK;
     if (!X || !Xq || !X_scale) return QG_ERR_INVALID_ARG;
-    if (M > (1 << 22) || K % 16 != 0 || (rows && top_k > 32)) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (M > (1 << 22) || K % 16 != 0 || K > (1 << 30) || (rows && top_k > 32)) return QG_ERR_UNSUPPORTED_SHAPE;
     if (ldx < (gated ? 2 * static_cast<int64_t>(K) : K) || ldxq < K || ldsx < out_rows) return QG_ERR_INVALID_ARG;
     if (!aligned16(X) || !aligned16(Xq) || !aligned16(X_scale) || ldx % 8 != 0 || ldxq % 16 != 0 || ldsx % 4 != 0 ||
         (reinterpret_cast<uintptr_t>(rows) & 3u) || (reinterpret_cast<uintptr_t>(num_rows) & 3u))
         return QG_ERR_MISALIGNED;
-    // a warp's jobs (M spans of 256 columns, eight to a CTA) are the grid
-    if (static_cast<int64_t>(M) * ((K + 255) / 256) > (int64_t(1) << 33)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
     const QuantizeRowsArgs a{X,  x_type, ldx, gated != 0, rows, top_k, num_rows, Xq, ldxq, X_scale, ldsx,
@@ -860,7 +858,7 @@ qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_sca
         return QG_ERR_INVALID_ARG;
     if (R == 0 || E == 0 || N == 0) return QG_OK;
     if (!Y || !offsets || (K > 0 && (!Xq || !X_scale || !W || !W_scale))) return QG_ERR_INVALID_ARG;
-    if (R > (1 << 24) || E > QG_MAX_EXPERTS || K % 16 != 0 || static_cast<int64_t>(E) * N >= (int64_t(1) << 31) - 256)
+    if (R > (1 << 24) || E > QG_MAX_EXPERTS || K % 16 != 0 || K > (1 << 30) || static_cast<int64_t>(E) * N >= (int64_t(1) << 31) - 256)
         return QG_ERR_UNSUPPORTED_SHAPE;
     if (ldxq < K || ldy < N || ldsx < R) return QG_ERR_INVALID_ARG;
     const uintptr_t y_mask = y_type == QG_FP32 ? 3u : 1u;
@@ -903,7 +901,7 @@ qg_status qg_moe_combine(const void* Y, int type, int64_t ldy, const int32_t* ro
         return QG_ERR_INVALID_ARG;
     if (M == 0 || K == 0) return QG_OK;
     if ((R > 0 && !Y) || !rows || !weights || !out) return QG_ERR_INVALID_ARG;
-    if (M > (1 << 22) || top_k > 32 || static_cast<int64_t>(M) * K > (int64_t(1) << 38)) return QG_ERR_UNSUPPORTED_SHAPE;
+    if (M > (1 << 22) || K > (1 << 30) || top_k > 32 || static_cast<int64_t>(M) * K > (int64_t(1) << 38)) return QG_ERR_UNSUPPORTED_SHAPE;
     if ((R > 0 && ldy < K) || (residual && ldr < K) || ldo < K) return QG_ERR_INVALID_ARG;
     const uintptr_t mask = type == QG_FP32 ? 3u : 1u;
     if ((reinterpret_cast<uintptr_t>(Y) & mask) || (reinterpret_cast<uintptr_t>(residual) & mask) ||

@@ -311,12 +311,20 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
         }
     }
     if (lane >= k) expert = -1;
-    // the weights, from the chosen logits
-    float w = 0.0f;
-    if (expert >= 0) {
-        const float x = to_f32<kType>(row, expert);
-        w = soft ? expf(x - top) : 1.0f / (1.0f + expf(-x));
+    // The weights, from the chosen logits.  Renormalized ones are ratios: about the
+    // largest of the chosen, whose scores a bias (or sigmoids of low logits) may leave
+    // anywhere below 1, down to where 64 bits hold none.
+    const float x = expert >= 0 ? to_f32<kType>(row, expert) : 0.0f;
+    float from = top;
+    bool about = soft, nothing = false;
+    if (a.renormalize) {
+        const uint32_t most = __reduce_max_sync(0xffffffffu, expert >= 0 ? order_key(x) : 0u);
+        from = most != 0u ? key_value(most) : 0.0f;
+        nothing = (soft ? from - top : from) < -690.0f;
+        about = soft || from < -60.0f;   // where sigmoids are exponentials, which 32 bits may not hold
     }
+    float w = 0.0f;
+    if (expert >= 0 && !nothing) w = about ? expf(x - from) : 1.0f / (1.0f + expf(-x));
     const float sum = a.renormalize ? warp_sum(w) : soft ? total : 1.0f;
     weight = sum > 0.0f ? w * (a.scale / sum) : 0.0f;
 }
