@@ -14,7 +14,8 @@
 // Few rows an expert (W): a tile is 128 weight rows, on the MMA's M side, x up to NT
 // rows of one expert on its N side, which is as wide as the tile's rows (rounded
 // up to 16).  Columns of TMEM and of the activation boxes beyond them hold other
-// rows' values, which nothing stores.  Bound by the weights' bytes.
+// rows' values, which nothing stores.  Bound by the weights' bytes: 64 tokens x 8 of
+// 128 experts, 2048 x 5120, 174 us (7 TB/s of the experts that hold rows).
 //
 // Many rows (T): a tile is 256 rows of one expert on the M side of a CTA pair's
 // MMAs x 256 weight rows.  A fold lane then is a row and needs one factor a K
