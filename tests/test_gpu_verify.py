@@ -300,3 +300,22 @@ def test_far_logits(q, B):
     check(q, t, tok, draft=d, uniform=u, noise=e)
     check(q, t, tok, uniform=u, noise=e)
     check(q, t, tok)
+
+
+@pytest.mark.parametrize("B", [8, 24])
+@pytest.mark.parametrize("V,pad", [(8200, 0), (9001, 3), (100, 0)])
+def test_noise_at_its_ends(q, B, V, pad):
+    t, d, tok, u, e = problem(B, 2, V, "bf16", V + B, pad)
+    for b in range(0, B, 8):
+        e[b, [17, 90, V - 1]] = 0.0           # ratios of infinity: the lowest index
+        e[b + 1, 55] = 1e-42                  # a subnormal one
+        e[b + 2, ::2] = math.inf              # a ratio of 0: never drawn
+        e[b + 3, 1::2] = math.nan
+        e[b + 4, ::3] *= -1.0
+        e[b + 5] = math.inf
+        e[b + 6] *= 1e30
+        e[b + 7] *= 1e-30
+    check(q, t, tok, draft=d, uniform=u, noise=e, most_unsure=0.2)
+    check(q, t, tok, uniform=u, noise=e, most_unsure=0.2)
+    none = q.verify_drafts(t, tok, d, u, e).tokens[5::8]
+    assert all(-1 in row for row in none.tolist())

@@ -24,9 +24,9 @@
 //
 // All sums have a fixed order.  Bound by memory: every logit is read once, and two
 // rows of a sequence a second time with the noise.  64 x 6 rows of 131072 with their
-// drafts: 52 us, 30 of them the pass over the rows (184 MB of BF16 at most, 152 with
-// these lengths: 5-6 TB/s under its exponentials), the rest the clusters' start, the
-// race (67 MB) and the joins; 1 x 5 x 32768: 9.7 us, latency.
+// drafts: 46.5 us, of them 27 the pass over the rows (152 MB of BF16, a third of the
+// sequences with fewer drafts: 5.6 TB/s under exponentials), 13 the race (67 MB), the rest the clusters'
+// start and the joins; 1 x 5 x 32768: 9.9 us, latency.
 //
 // The sums: with L = log2 e and c a whole number that follows the largest x L from
 // below (by at most 32), s = sum 2^(x L - c): a term is one fma with one rounding,
@@ -36,6 +36,8 @@
 // left, the row is done again about its maximum.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "qg_launch.h"
 #include "qg_pair.cuh"
@@ -122,6 +124,12 @@ __device__ __forceinline__ float ex2(float t) {
     return e;
 }
 
+__device__ __forceinline__ float lg2(float t) {
+    float l;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(l) : "f"(t));
+    return l;
+}
+
 // e^d for d <= 0, with the product's rounding carried along: within 2^-22 of it
 // at any distance from the maximum (a rounded d log2 e alone costs |d| 2^-24).
 __device__ __forceinline__ float exp_near(float d) {
@@ -201,10 +209,26 @@ __device__ __forceinline__ Part about_max(Sum a) {
     return Part{m, a.s * ex2(-__fmaf_rn(m, kLog2e, -a.c))};
 }
 
+constexpr int kSum = 0, kMax = 1, kGreedyScan = 2;   // kMax: about the maximum
+// Sixteen bytes of a row, the elements from v on.
+template <int kType, int kHow, class State>
+__device__ __forceinline__ void take(State& p, const uint4& w, int v) {
+    using El = Elem<kType>;
+    constexpr int kVec = 16 / El::kSize;
+    float x[kVec];
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) El::wide(ws[e], x + e * (kVec / 4));
+    if constexpr (kHow == kGreedyScan) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) see_greedy(p, x[e], v + e);
+    } else {
+        see(p, x);
+    }
+}
+
 // The slice [v0, v1) of a row, by one warp: scalars up to the first 16-byte
-// boundary and behind the last, vectors in between.  kHow: kSum, kMax (about the
-// maximum) or kGreedy.
-constexpr int kSum = 0, kMax = 1, kGreedyScan = 2;
+// boundary and behind the last, vectors in between.
 template <int kType, int kHow, class State>
 __device__ __forceinline__ State scan_row(const void* row, int v0, int v1, int lane, State p) {
     using El = Elem<kType>;
@@ -222,18 +246,6 @@ __device__ __forceinline__ State scan_row(const void* row, int v0, int v1, int l
     };
     for (int v = v0 + lane; v < a0; v += 32) one(v);
     const uint4* vec = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(a0) * El::kSize);
-    auto take = [&](const uint4& w, int i) {
-        float x[kVec];
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) El::wide(ws[e], x + e * (kVec / 4));
-        if constexpr (kHow == kGreedyScan) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) see_greedy(p, x[e], a0 + i * kVec + e);
-        } else {
-            see(p, x);
-        }
-    };
     constexpr int kU = 4;   // loads in flight
     int i = lane;
     for (; i + 32 * (kU - 1) < nvec; i += 32 * kU) {
@@ -241,19 +253,31 @@ __device__ __forceinline__ State scan_row(const void* row, int v0, int v1, int l
 #pragma unroll
         for (int u = 0; u < kU; ++u) w[u] = __ldcg(vec + i + 32 * u);
 #pragma unroll
-        for (int u = 0; u < kU; ++u) take(w[u], i + 32 * u);
+        for (int u = 0; u < kU; ++u) take<kType, kHow>(p, w[u], a0 + (i + 32 * u) * kVec);
     }
-    for (; i < nvec; i += 32) take(vec[i], i);
+    for (; i < nvec; i += 32) take<kType, kHow>(p, vec[i], a0 + i * kVec);
     for (int v = a1 + lane; v < v1; v += 32) one(v);
     return p;
 }
-template <int kType>
-__device__ __forceinline__ Sum scan_sum(const void* row, int v0, int v1, int lane) {
-    Sum p = scan_row<kType, kSum>(row, v0, v1, lane, Sum{kNoRef, 0.0f});
+// Of all lanes.
+__device__ __forceinline__ Sum warp_join(Sum p) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         p = join(p, Sum{__shfl_xor_sync(0xffffffffu, p.c, o), __shfl_xor_sync(0xffffffffu, p.s, o)});
     return p;
+}
+template <bool kGreedy>
+__device__ __forceinline__ Part warp_join(Part p) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const Part q{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)};
+        p = kGreedy ? join_greedy(p, q) : join(p, q);
+    }
+    return p;
+}
+template <int kType>
+__device__ __forceinline__ Sum scan_sum(const void* row, int v0, int v1, int lane) {
+    return warp_join(scan_row<kType, kSum>(row, v0, v1, lane, Sum{kNoRef, 0.0f}));
 }
 __device__ __forceinline__ int length_of(const VerifyArgs& a, int b) {
     if (a.lengths == nullptr) return a.G;
@@ -263,14 +287,8 @@ __device__ __forceinline__ int length_of(const VerifyArgs& a, int b) {
 
 template <int kType, bool kGreedy>
 __device__ __forceinline__ Part scan_max(const void* row, int v0, int v1, int lane) {
-    Part p = scan_row<kType, kGreedy ? kGreedyScan : kMax>(
-        row, v0, v1, lane, Part{-INFINITY, kGreedy ? __uint_as_float(0x7FFFFFFFu) : 0.0f});
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const Part q{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o)};
-        p = kGreedy ? join_greedy(p, q) : join(p, q);
-    }
-    return p;
+    return warp_join<kGreedy>(scan_row<kType, kGreedy ? kGreedyScan : kMax>(
+        row, v0, v1, lane, Part{-INFINITY, kGreedy ? __uint_as_float(0x7FFFFFFFu) : 0.0f}));
 }
 
 __device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
@@ -293,39 +311,97 @@ __device__ __forceinline__ Best better(Best a, Best b) {
 constexpr int kStretch = 2048;
 inline int verify_stretches(int V) { return (V + kStretch - 1) / kStretch; }
 
-// The parts of all rows by stretch: parts[(b (2 G + 1) + r) stretches + i].
+// The parts of all rows by stretch: parts[(b (2 G + 1) + r) stretches + i].  Warps walk
+// over the stretches, the loads of the next four vectors (of the next stretch) on
+// their way while four are summed, and while a stretch's lanes are joined.
 template <int kType, bool kGreedy>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_rows_kernel(const VerifyArgs a, int stretches, float2* out) {
     using El = Elem<kType>;
+    using State = std::conditional_t<kGreedy, Part, Sum>;
+    constexpr int kHow = kGreedy ? kGreedyScan : kSum;
+    constexpr int kVec = 16 / El::kSize;
+    constexpr int kU = 4;
+    constexpr int kTurns = kStretch / (32 * kVec * kU);
+    static_assert(kTurns * 32 * kVec * kU == kStretch, "whole turns");
     grid_dependents_launch();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const bool sampled = !kGreedy && a.draft != nullptr;
     const int most = sampled ? 2 * a.G + 1 : a.G + 1;   // rows of a sequence
-    const int64_t all = static_cast<int64_t>(a.B) * most * stretches;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); i < all;
-         i += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t row = i / stretches;
-        const int piece = static_cast<int>(i - row * stretches);
-        const int b = static_cast<int>(row / most);
-        const int r = static_cast<int>(row - static_cast<int64_t>(b) * most);
-        const int length = length_of(a, b);
-        const bool of_target = r <= a.G;
-        if (of_target ? r > length : r - (a.G + 1) >= length) continue;
-        const uint8_t* p = of_target
-                               ? static_cast<const uint8_t*>(a.target) + (b * a.t_seq + r * a.t_row) * El::kSize
-                               : static_cast<const uint8_t*>(a.draft) + (b * a.d_seq + (r - a.G - 1) * a.d_row) * El::kSize;
-        const int s0 = piece * kStretch;
-        const int s1 = s0 + kStretch < a.V ? s0 + kStretch : a.V;
-        float2 v;
-        if constexpr (kGreedy) {
-            const Part q = scan_max<kType, true>(p, s0, s1, lane);
-            v = make_float2(q.m, q.s);
-        } else {
-            const Sum q = scan_sum<kType>(p, s0, s1, lane);
-            v = make_float2(q.c, q.s);
+    const int rows = a.B * most;
+    const int warps = gridDim.x * kWarps, first = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    // the next stretch, stepped without divisions
+    const int drow = warps / stretches, dpiece = warps - drow * stretches;
+    int row = first / stretches, piece = first - row * stretches;
+    auto step = [&]() {
+        row += drow;
+        piece += dpiece;
+        if (piece >= stretches) {
+            piece -= stretches;
+            ++row;
         }
-        if (lane == 0) out[(static_cast<int64_t>(b) * (2 * a.G + 1) + r) * stretches + piece] = v;
+    };
+    // an open stretch: its row, place and part
+    const uint8_t* p = nullptr;
+    int s0 = 0;
+    float2* to = nullptr;
+    bool whole = false;   // in whole vectors, all there
+    uint4 w[kU];
+    auto load = [&](int turn, uint4 (&x)[kU]) {
+        const uint4* vec = reinterpret_cast<const uint4*>(p + static_cast<int64_t>(s0) * El::kSize) + turn * 32 * kU + lane;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) x[u] = __ldcg(vec + 32 * u);
+    };
+    auto open = [&](uint4 (&x)[kU]) {   // the next one that counts, from (row, piece) on
+        for (; row < rows; step()) {
+            const int b = row / most, r = row - b * most;
+            const int length = length_of(a, b);
+            const bool of_target = r <= a.G;
+            if (of_target ? r > length : r - (a.G + 1) >= length) continue;
+            p = of_target ? static_cast<const uint8_t*>(a.target) + (b * a.t_seq + r * a.t_row) * El::kSize
+                          : static_cast<const uint8_t*>(a.draft) + (b * a.d_seq + (r - a.G - 1) * a.d_row) * El::kSize;
+            s0 = piece * kStretch;
+            to = out + (static_cast<int64_t>(b) * (2 * a.G + 1) + r) * stretches + piece;
+            whole = a.V - s0 >= kStretch && (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+            if (whole) load(0, x);
+            step();
+            return true;
+        }
+        return false;
+    };
+    auto none = [] {
+        if constexpr (kGreedy) return Part{-INFINITY, __uint_as_float(0x7FFFFFFFu)};
+        else return Sum{kNoRef, 0.0f};
+    };
+    bool there = open(w);
+    while (there) {
+        float2* const at = to;
+        State sum = none();
+        if (whole) {
+            const int v = s0 + lane * kVec;
+#pragma unroll
+            for (int t = 0; t < kTurns; ++t) {
+                uint4 x[kU];
+                if (t + 1 < kTurns) load(t + 1, x);
+                else there = open(x);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) take<kType, kHow>(sum, w[u], v + (t * kU + u) * 32 * kVec);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) w[u] = x[u];
+            }
+        } else {
+            sum = scan_row<kType, kHow>(p, s0, a.V - s0 < kStretch ? a.V : s0 + kStretch, lane, sum);
+            there = open(w);
+        }
+        float2 part;
+        if constexpr (kGreedy) {
+            sum = warp_join<true>(sum);
+            part = make_float2(sum.m, sum.s);
+        } else {
+            sum = warp_join(sum);
+            part = make_float2(sum.c, sum.s);
+        }
+        if (lane == 0) *at = part;
     }
 }
 
@@ -498,12 +574,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const float pr = 1.0f / t.s, qr = 1.0f / s.s;
         const float* noise = a.noise + b * a.ldn;
         // The race of max(p - q, 0), or of p (for a row where that is 0 everywhere).
-        // Eight tokens a lane at a time: bounds of their ratios from quick
-        // probabilities (good to kSlack of p), then the exact ratio where a token's
-        // upper bound reaches the largest lower one that the warp has seen, which
-        // few do.  (Each lane against its own best: some lane of 32 had one for
-        // almost every token, and the race took 20 us of 62.)
-        constexpr float kSlack = 2e-5f;
+        // Eight tokens a lane at a time: quick probabilities, good to kSlack of p, and
+        // whether a token may reach the largest ratio that the warp has seen (w >= reach
+        // noise, with the slack); if one of any lane may, the exact ratios of those
+        // that may.  Few turns of a warp have any.  (Bounds of every ratio by a
+        // reciprocal, and the largest of them every turn: 49.8 us for 64 x 6 x 131072
+        // against 46.5.)
+        //   kSlack: t = fma(x - m, L, -log2 s), |t| <= 126, is within 126 2^-24 of the sum,
+        // and x - m, L and log2 s add 110 2^-24, 110 2^-26 and 50 2^-24 to it: 1.7e-5, as
+        // a factor 1.2e-5; ex2 and the exact one's own 2^-20 on top.  kTiny: below 2^-126
+        // a quick probability is 0.
+        constexpr float kSlack = 2e-5f, kTiny = 0x1p-120f;
+        const float tl = -lg2(t.s), sl = -lg2(s.s);
         auto race = [&](bool with_q, Best& result) {
             Best top{0.0f, 0x7FFFFFFF};
             float reach = 0.0f;
@@ -521,57 +603,74 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (ratio > top.ratio) top = Best{ratio, v};
                 }
             };
-            // tokens v, v + step, ... (those from v1 on do not count)
+            // tokens v, v + step, ... (one with a noise of NaN does not count)
             auto enter = [&](int v, int step, const float (&x)[8], const float (&y)[8], const float (&e)[8]) {
-                float high[8];
-                float low = reach;
+                float w[8], high[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float p = ex2((x[j] - t.m) * kLog2e) * pr;   // t.m may be near a type's lowest value
-                    float w = p;
+                    const float p = ex2(__fmaf_rn(x[j] - t.m, kLog2e, tl));
+                    w[j] = p;
                     if (with_q) {
-                        if (drow != nullptr) w -= ex2((y[j] - s.m) * kLog2e) * qr;
-                        else if (v + j * step == d) w -= 1.0f;
+                        if (drow != nullptr) w[j] -= ex2(__fmaf_rn(y[j] - s.m, kLog2e, sl));
+                        else if (v + j * step == d) w[j] -= 1.0f;
                     }
-                    float r;
-                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e[j]));
-                    const bool in = v + j * step < v1 && r > 0.0f;
-                    high[j] = in ? __fmaf_rn(kSlack, p, w) * r : -1.0f;
-                    low = fmaxf(low, in ? __fmaf_rn(-kSlack, p, w) * r : 0.0f);
+                    high[j] = __fmaf_rn(kSlack, p, w[j]);
                 }
-                reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(low)));   // not negative
+                if (reach == 0.0f) {   // at first: what some token has at least
+                    float low = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (high[j] >= reach) exact(v + j * step, x[j], y[j], e[j]);
+                    for (int j = 0; j < 8; ++j) {
+                        float r;
+                        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e[j]));
+                        const float least = __fmaf_rn(2.0f, w[j], -high[j]) * r;   // w - kSlack p
+                        if (r > 0.0f && r < INFINITY) low = fmaxf(low, least);
+                    }
+                    reach = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(low)));   // not negative
+                }
+                bool may = false;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) may |= high[j] >= __fmaf_rn(reach, e[j], -kTiny);
+                if (__any_sync(0xffffffffu, may)) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (high[j] >= __fmaf_rn(reach, e[j], -kTiny)) exact(v + j * step, x[j], y[j], e[j]);
+                    reach = fmaxf(reach, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top.ratio))));
+                }
             };
             constexpr int kVec = 8;
             const bool vectors = ((reinterpret_cast<uintptr_t>(trow) | reinterpret_cast<uintptr_t>(drow) |
                                    reinterpret_cast<uintptr_t>(noise)) & 15u) == 0;
+            const float nan = __uint_as_float(0x7FC00000u);
             int v_done = v0;
             if (vectors) {   // slices begin at multiples of 32
                 const int nvec = (v1 - v0) / kVec;
                 v_done = v0 + nvec * kVec;
                 for (int i0 = 32 * warp; i0 < nvec; i0 += kThreads) {
-                    const int i = i0 + lane < nvec ? i0 + lane : nvec - 1;
+                    const bool in = i0 + lane < nvec;
+                    const int v = v0 + (in ? i0 + lane : nvec - 1) * kVec;
                     float x[kVec], y[kVec], e[kVec];
-                    const typename El::Raw8 xr = El::load8(trow, v0 + i * kVec);
-                    const typename El::Raw8 yr = El::load8(with_q && drow != nullptr ? drow : trow, v0 + i * kVec);
-                    const Elem<QG_FP32>::Raw8 er = Elem<QG_FP32>::load8(noise, v0 + i * kVec);
+                    const typename El::Raw8 xr = El::load8(trow, v);
+                    const typename El::Raw8 yr = El::load8(with_q && drow != nullptr ? drow : trow, v);
+                    const Elem<QG_FP32>::Raw8 er = Elem<QG_FP32>::load8(noise, v);
                     El::wide8(xr, x);
                     El::wide8(yr, y);
                     Elem<QG_FP32>::wide8(er, e);
-                    enter(i0 + lane < nvec ? v0 + i * kVec : v1, 1, x, y, e);
+                    if (!in) {
+#pragma unroll
+                        for (int j = 0; j < kVec; ++j) e[j] = nan;
+                    }
+                    enter(v, 1, x, y, e);
                 }
             }
             for (int v = v_done + 32 * warp; v < v1; v += kThreads * kVec) {
                 float x[kVec], y[kVec], e[kVec];
 #pragma unroll
                 for (int u = 0; u < kVec; ++u) {
-                    int w = v + lane + kThreads * u;
-                    w = w < v1 ? w : v1 - 1;
+                    const int at = v + lane + kThreads * u;
+                    const int w = at < v1 ? at : v1 - 1;
                     x[u] = El::at(trow, w);
                     y[u] = with_q && drow != nullptr ? El::at(drow, w) : 0.0f;
-                    e[u] = noise[w];
+                    e[u] = at < v1 ? noise[w] : nan;
                 }
                 enter(v + lane, kThreads, x, y, e);
             }
