@@ -429,3 +429,25 @@ def test_workspaces_of_calls_with_counters_stay_clean(q):
         q.moe_route(logits, 4, workspace=torch.empty(1 << 20, dtype=torch.uint8))
     with pytest.raises(q.QgemmError):
         q.moe_route(logits, 4, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("K", [128, 208, 3696])
+def test_quantize_zeros_of_either_sign(q, dtype, K):
+    """Codes of -0 are -0's, in blocks with and without other values."""
+    M = 50
+    g = gen(K)
+    X = torch.randn(M, K, generator=g, device="cuda")
+    zero = torch.where(torch.rand(M, K, generator=g, device="cuda") < 0.5, 0.0, -0.0)
+    X = torch.where(torch.rand(M, K, generator=g, device="cuda") < 0.3, zero, X)
+    X[::3, :128] = zero[::3, :128]
+    X = X.to(DTYPES[dtype])
+    Xq, Xs = q.quantize_rows_e4m3(X)
+    want_q, want_s = q.quantize_act_e4m3(X) if dtype == "bf16" else (None, None)
+    blocks = X.float().split(128, dim=1)
+    scale = torch.stack([torch.where(b.abs().amax(dim=1) > 0, b.abs().amax(dim=1) / torch.tensor(448.0, device="cuda"), 1.0)
+                         for b in blocks])
+    codes = torch.cat([(b / s[:, None]).to(torch.float8_e4m3fn).view(torch.uint8) for b, s in zip(blocks, scale)], dim=1)
+    assert torch.equal(Xq, codes) and torch.equal(Xs[:, :M], scale)
+    if want_q is not None:
+        assert torch.equal(Xq, want_q) and torch.equal(Xs[:, :M], want_s[:, :M])

@@ -573,10 +573,10 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 // x / s, rounded to nearest, from r, the rounded 1 / s: one correction of the
 // product by its remainder (Markstein's theorem; s normal, and its reciprocal, and
 // x / s of at most 448).  A division of every element took most of the kernel's
-// time (issue slots 83 % busy).
+// time (issue slots 83 % busy).  With these signs a -0 stays one.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
     const float q = __fmul_rn(x, r);
-    return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+    return __fmaf_rn(__fmaf_rn(q, s, -x), -r, q);
 }
 
 constexpr int kQuantWarps = 8;
@@ -653,12 +653,13 @@ __global__ void __launch_bounds__(kQuantWarps * 32, kQuantCtas)
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float sc = quotient(amax, 448.0f, 1.0f / 448.0f);
+        if (!(amax > 0.0f)) sc = 1.0f;   // blocks of zeros, and those past K
         if (sc > 1e-30f) {
             const float r = __frcp_rn(sc);
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = quotient(v[i >> 3][i & 7], sc, r);
         } else {   // a reciprocal or a remainder would not be a normal number
-            sc = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+            sc = __fdiv_rn(amax, 448.0f);
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __fdiv_rn(v[i >> 3][i & 7], sc);
         }
