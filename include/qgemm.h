@@ -488,7 +488,11 @@ qg_status qg_quantize_rows_e4m3(const void *X, int x_type, int64_t ldx, int gate
  *            K % 16 == 0, K <= 2^30
  * Tiles are not split along K, so that no workspace is needed and a row's result
  * does not depend on the other rows' values.
+ * qg_grouped_tile_rows: the rows of a tile (16, 32, 64, or 256 on a pair of CTAs) that
+ * the call takes on a device with `sms` SMs (host only, no CUDA call; 0 for invalid
+ * arguments).
  */
+int qg_grouped_tile_rows(int R, int E, int N, int K, int sms);
 qg_status qgemm_w8a8_grouped(const uint8_t *Xq, int64_t ldxq, const float *X_scale, int64_t ldsx, const uint8_t *W,
                              const float *W_scale, const int32_t *offsets, void *Y, int y_type, int64_t ldy, int R,
                              int E, int N, int K, struct CUstream_st *stream);

@@ -316,3 +316,14 @@ def test_sizes_beyond_32_bits_are_refused(world, big):   # noqa: F811
         with pytest.raises(ValueError, match="2\\^31"):
             call()
     assert not world.calls
+
+
+def test_grouped_tile_rows(qg):
+    """Few rows take narrow tiles, many a pair's; invalid shapes none."""
+    rows = [qg.grouped_tile_rows(64 * n, 64, 4096, 2048, 152) for n in (1, 8, 16, 48, 96, 1000)]
+    assert rows == sorted(rows) and rows[0] == 16 and rows[-1] == 256
+    # few tiles: narrow ones, which fill more of the device
+    assert qg.grouped_tile_rows(200, 4, 870, 6432, 152) < qg.grouped_tile_rows(200 * 50, 200, 870, 6432, 152)
+    for bad in ((0, 4, 64, 64, 152), (4, 0, 64, 64, 152), (4, 1025, 64, 64, 152), (4, 4, 0, 64, 152), (4, 4, 64, 60, 152),
+                (4, 4, 64, 0, 152), (4, 4, 64, 64, 1), (2 ** 24 + 1, 4, 64, 64, 152)):
+        assert qg.grouped_tile_rows(*bad) == 0

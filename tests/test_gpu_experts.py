@@ -451,3 +451,44 @@ def test_quantize_zeros_of_either_sign(q, dtype, K):
     assert torch.equal(Xq, codes) and torch.equal(Xs[:, :M], scale)
     if want_q is not None:
         assert torch.equal(Xq, want_q) and torch.equal(Xs[:, :M], want_s[:, :M])
+
+
+# (rows of a tile, sizes, N, K): every form of the grouped GEMM, on groups that fill a
+# tile, end inside one, and hold nothing
+FORMS = [(16, [5, 0, 16, 17, 1, 9, 40], 1003, 1040), (16, [3] * 40, 264, 528), (16, [5, 0, 16, 17, 1, 9, 40], 96, 144),
+         (32, [40, 33, 1, 0, 32, 31] * 4, 1003, 1040), (32, [40, 33, 1, 0, 32, 31] * 4, 640, 2048),
+         (64, [60, 64, 65, 1, 0, 130, 33, 40] * 6, 1003, 1040), (64, [60, 64, 65, 1, 0, 130, 33, 40] * 6, 264, 528),
+         (64, [64] * 60, 2041, 272), (32, [64] * 60, 96, 144),
+         (256, [256, 255, 257, 1, 0, 31, 500, 33, 700] * 3, 1003, 1040), (256, [1500, 3000, 1], 2041, 272),
+         (256, [256, 255, 257, 1, 0, 31, 500, 33, 700] * 3, 264, 528), (256, [1500, 3000, 1], 640, 2048)]
+
+
+@pytest.mark.parametrize("rows,sizes,N,K", FORMS, ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_grouped_forms(q, rows, sizes, N, K, dtype):
+    """Outputs that take stores of 16, 4 and 2 bytes, and strided ones; rows of no
+    expert in front of the groups and behind them."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert q.grouped_tile_rows(sum(sizes), len(sizes), N, K, sms) == rows
+    check_grouped(q, sizes, N, K, dtype)
+    check_grouped(q, sizes, N, K, dtype, extra=3, first=2, pad_y=2, pad_x=16)
+    check_grouped(q, sizes, N, K, dtype, extra=1, pad_y=1)
+
+
+@pytest.mark.parametrize("rows,sizes", [(16, [5, 2]), (32, [30, 31] * 20), (64, [64, 60] * 40), (256, [700, 300] * 10)],
+                         ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
+def test_a_wait_that_runs_out_in_every_form(q, rows, sizes):
+    """A load that is left out: the status says so, and the next call is right."""
+    assert q.grouped_tile_rows(sum(sizes), len(sizes), 512, 2048, 152) == rows
+    Xq, Xs, W, Ws, off = grouped_problem(sizes, 512, 2048, 3)
+    assert q.last_device_status() == 0
+    q.set_wait_timeout_ns(20_000_000)
+    for unit in (0, 5):
+        q.set_fault_injection(unit)
+        try:
+            q.qgemm_w8a8_grouped(Xq, Xs, W, Ws, off)
+            assert q.last_device_status() == 5
+        finally:
+            q.set_fault_injection(-1)
+    q.set_wait_timeout_ns(1_000_000_000)
+    check_grouped(q, sizes, 512, 2048, "bf16")

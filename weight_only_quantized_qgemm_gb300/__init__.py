@@ -58,7 +58,7 @@ __all__ = [
     "quantize_act_e4m3", "qgemm_w8a8_block", "qgemm_w8a8", "KIND_W8A8", "MAX_M_W8A8",
     "tune_bf16", "tune_w8a8", "workspace_bytes_max_w8a8",
     "quantize_act_int8", "qgemm_w8a8_int8", "int8_tile_rows", "KIND_INT8", "logprobs", "LogProbs", "MAX_TOP_K",
-    "moe_route", "MoeRoute", "quantize_rows_e4m3", "qgemm_w8a8_grouped", "moe_combine", "MAX_EXPERTS",
+    "moe_route", "MoeRoute", "quantize_rows_e4m3", "qgemm_w8a8_grouped", "grouped_tile_rows", "moe_combine", "MAX_EXPERTS",
     "verify_drafts", "DraftCheck", "MAX_DRAFTS",
 ]
 
@@ -123,6 +123,7 @@ _SIGS = {
     "qg_dispatch_rule": (_I, [_I, _I, _I, _I, _I]),
     "qg_dispatch_clear": (None, []),
     "qg_int8_tile_rows": (_I, [_I, _I, _I, _I]),
+    "qg_grouped_tile_rows": (_I, [_I, _I, _I, _I, _I]),
     "qg_workspace_bytes_max": (_S, [_I]),
     "qg_workspace_bytes_max_w8a8": (_S, [_I, _I]),
     "qg_tune_bf16": (_I, [_P, _L, _P, _I, _P, _L, _P, _I, _I, _I, _P, _S, _I, _P, _P, _P]),
@@ -922,6 +923,12 @@ def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None,
     if r:
         raise QgemmError(r, "qgemm_w8a8_grouped")
     return Y
+
+
+def grouped_tile_rows(R: int, E: int, N: int, K: int, sms: int) -> int:
+    """The rows of a tile that :func:`qgemm_w8a8_grouped` takes for this shape on a
+    device with `sms` SMs (host only; 0 for invalid arguments)."""
+    return int(lib.qg_grouped_tile_rows(R, E, N, K, sms))
 
 
 def moe_combine(Y, rows, weights, residual=None, out=None, stream=None):

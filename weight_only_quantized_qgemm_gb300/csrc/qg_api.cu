@@ -866,11 +866,11 @@ qg_status qgemm_w8a8_grouped(const uint8_t* Xq, int64_t ldxq, const float* X_sca
     if ((K > 0 && (!aligned16(Xq) || !aligned16(W) || !aligned16(X_scale) || ldxq % 16 != 0 || ldsx % 4 != 0)) ||
         (reinterpret_cast<uintptr_t>(W_scale) & 3u) || (reinterpret_cast<uintptr_t>(offsets) & 3u) || (reinterpret_cast<uintptr_t>(Y) & y_mask))
         return QG_ERR_MISALIGNED;
-    const int nt = grouped_tile_rows(R, E, K);
-    // tiles are counted in 32 bits
-    if ((static_cast<int64_t>(R) / nt + E) * ((N + 127) / 128) > (int64_t(1) << 30)) return QG_ERR_UNSUPPORTED_SHAPE;
+    // tiles (of 16 rows at least) are counted in 32 bits
+    if ((static_cast<int64_t>(R) / 16 + E) * ((N + 127) / 128) > (int64_t(1) << 30)) return QG_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* d = device_info();
     if (!d) return QG_ERR_CUDA;
+    const int nt = grouped_tile_rows(R, E, N, K, d->sms);
     GroupedArgs a{};
     a.Sx = X_scale;
     a.ldsx = ldsx;
@@ -1127,6 +1127,11 @@ int qg_dispatch_rule(int kind, int M, int N, int K, int sms) {
     if (too_many_tiles(kind, M, N)) return 0;
     const Schedule s = schedule_for(kind, M, N, K, sms, 0, int8_nominal_clusters(sms));
     return s.G * schedule_ctas(kind, s);
+}
+
+int qg_grouped_tile_rows(int R, int E, int N, int K, int sms) {
+    if (R < 1 || R > (1 << 24) || E < 1 || E > QG_MAX_EXPERTS || N < 1 || K < 1 || K % 16 != 0 || sms < 2) return 0;
+    return grouped_tile_rows(R, E, N, K, sms);
 }
 
 int qg_int8_tile_rows(int M, int N, int K, int sms) {

@@ -41,6 +41,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
+
 #include "qg_gemm.cuh"
 #include "qg_grouped.h"
 #include "qg_launch.h"
@@ -918,26 +920,47 @@ cudaError_t launch_grouped_nt(const GroupedArgs& a, const CUtensorMap& tmW, cons
 
 }  // namespace
 
-// By the mean number of rows of an expert, as far as the host knows it.  Narrow
-// tiles fold fewer columns that hold nothing, wide ones read a large group's
-// weights fewer times, and the pair's tiles win from where the MMAs count, on a short
-// K later (an epilogue a few units).  Measured in us for 16 / 32 / 64 / 256 rows a
-// tile, groups of unlike sizes (the largest five times the mean):
-//   rows      64 experts, 4096 x 2048    16 experts, 2048 x 5120   20 experts, 1003 x 1040
-//     8       81 /  81 /  82 / 114       27 / 28 / 30 / 39         10 / 10 / 11 / 16
-//    12       89 /  80 /  83 / 116       31 / 27 / 30 / 39         11 / 12 / 12 / 16
-//    24      111 /  92 /  89 / 117       39 / 33 / 29 / 40         14 / 13 / 15 / 23
-//    48      176 / 125 / 114 / 120       54 / 41 / 42 / 41         18 / 17 / 17 / 25
-//    64      224 / 153 / 137 / 127       70 / 50 / 45 / 42         21 / 18 / 18 / 26
-//    96      312 / 210 / 177 / 132       94 / 59 / 58 / 41         28 / 23 / 25 / 26
-int grouped_tile_rows(int R, int E, int K) {
-    const int64_t mean = R / E;
-    return mean <= 10 ? 16 : mean <= 20 ? 32 : mean <= (K < 2048 ? 96 : 52) ? 64 : 256;
+// The host knows R and E, not the groups: experts of about R / E rows each, the last
+// tile of a group half full.  Narrow tiles fold fewer columns that hold nothing and
+// fill the SMs with few rows, wide ones read a large group's weights fewer times,
+// and the pair's have the quickest K blocks and the longest epilogue, on 256 weight
+// rows.  A tile's time is K blocks times `block` and `ends` beside them (us); waves count
+// half as whole ones, since unlike tiles even out.  The figures are fitted to 120
+// shapes in all four forms (R 2 to 65536, 2 to 256 experts, N 65 to 8000, K 128 to
+// 7100) with 14 % of scatter; chosen by them, those take 0.2 % more time than with the best
+// of the four for each, and 220 other shapes 0.6 % (by the mean number of rows
+// alone, 10 / 20 / 52: 2.6 and 4.5 %).  Of the unlike sides, us for 16 / 32 / 64 / 256:
+//   64 experts, 4096 x 2048:   8 rows 81 / 81 / 82 / 114, 24 rows 111 / 92 / 89 / 117, 96
+//   rows 312 / 210 / 177 / 132;  21 experts of 46 rows, 337 x 5072: 23 / 15 / 19 / 24;
+//   3 of 480, 216 x 2240: - / 9 / 11 / 15
+int grouped_tile_rows(int R, int E, int N, int K, int sms) {
+    struct Form {
+        int rows, channels;
+        double block, ends;
+    };
+    constexpr Form kForms[] = {{16, 128, 0.21, 1.0}, {32, 128, 0.20, 1.5}, {64, 128, 0.30, 1.5}, {256, 256, 0.37, 3.4}};
+    const double groups = R < E ? R : E;
+    const int blocks = (K + 127) / 128;
+    int best = 0;
+    double least = 0.0;
+    for (const Form& f : kForms) {
+        const double tn = (static_cast<int64_t>(N) + f.channels - 1) / f.channels;
+        const bool several = 2 * static_cast<int64_t>(R) > static_cast<int64_t>(f.rows) * E;
+        const double tiles = tn * (several ? R / static_cast<double>(f.rows) + 0.5 * groups : groups);
+        const double x = tiles / (sms * 128 / f.channels);
+        const double waves = x <= 1.0 ? 1.0 : 0.5 * (x + std::ceil(x));
+        const double us = waves * (blocks * f.block + f.ends);
+        if (best == 0 || us < least) {
+            best = f.rows;
+            least = us;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_grouped(const GroupedArgs& a, const CUtensorMap& tmW, const CUtensorMap& tmX, const LaunchCtl& c,
                            cudaStream_t st) {
-    switch (grouped_tile_rows(a.R, a.E, a.K)) {
+    switch (grouped_tile_rows(a.R, a.E, a.N, a.K, c.num_sms)) {
         case 16: return launch_grouped_nt<16, false>(a, tmW, tmX, c, st);
         case 32: return launch_grouped_nt<32, false>(a, tmW, tmX, c, st);
         case 64: return launch_grouped_nt<64, false>(a, tmW, tmX, c, st);

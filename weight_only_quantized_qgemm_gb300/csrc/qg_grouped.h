@@ -16,9 +16,8 @@ struct GroupedArgs {
     int R, E, N, K;
 };
 
-// The rows of a tile for R rows over E experts (more than 64: on a CTA pair, with
-// 256 weight rows).
-int grouped_tile_rows(int R, int E, int K);
+// The rows of a tile (more than 64: on a CTA pair, with 256 weight rows).
+int grouped_tile_rows(int R, int E, int N, int K, int sms);
 
 // Activation rows of a copy (a pair's CTAs hold half of a tile's rows each).
 inline int grouped_box_rows(int tile_rows) { return tile_rows > 64 ? tile_rows / 2 : tile_rows; }
