@@ -59,6 +59,7 @@ struct Elem;
 template <>
 struct Elem<QG_BF16> {
     static constexpr int kSize = 2;
+    static constexpr uint32_t kLowest = 0xFF80FF80u;   // -inf in every place
     static __device__ __forceinline__ float at(const void* p, int64_t i) {
         return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
     }
@@ -80,6 +81,7 @@ struct Elem<QG_BF16> {
 template <>
 struct Elem<QG_FP16> {
     static constexpr int kSize = 2;
+    static constexpr uint32_t kLowest = 0xFC00FC00u;   // -inf in every place
     static __device__ __forceinline__ float at(const void* p, int64_t i) {
         return __half2float(static_cast<const __half*>(p)[i]);
     }
@@ -102,6 +104,7 @@ struct Elem<QG_FP16> {
 template <>
 struct Elem<QG_FP32> {
     static constexpr int kSize = 4;
+    static constexpr uint32_t kLowest = 0xFF800000u;   // -inf in every place
     static __device__ __forceinline__ float at(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
     static __device__ __forceinline__ void wide(uint32_t w, float* x) { x[0] = __uint_as_float(w); }
     struct Raw8 {
@@ -228,7 +231,8 @@ __device__ __forceinline__ void take(State& p, const uint4& w, int v) {
 }
 
 // The slice [v0, v1) of a row, by one warp: scalars up to the first 16-byte
-// boundary and behind the last, vectors in between.
+// boundary and behind the last, vectors in between, four and the scalars on their way
+// at a time.
 template <int kType, int kHow, class State>
 __device__ __forceinline__ State scan_row(const void* row, int v0, int v1, int lane, State p) {
     using El = Elem<kType>;
@@ -239,24 +243,29 @@ __device__ __forceinline__ State scan_row(const void* row, int v0, int v1, int l
     const int a0 = v0 + head < v1 ? v0 + head : v1;
     const int nvec = (v1 - a0) / kVec;
     const int a1 = a0 + nvec * kVec;
-    auto one = [&](int v) {
-        const float x[1] = {El::at(row, v)};
-        if constexpr (kHow == kGreedyScan) see_greedy(p, x[0], v);
-        else see(p, x);
-    };
-    for (int v = v0 + lane; v < a0; v += 32) one(v);
-    const uint4* vec = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(a0) * El::kSize);
-    constexpr int kU = 4;   // loads in flight
-    int i = lane;
-    for (; i + 32 * (kU - 1) < nvec; i += 32 * kU) {
+    float front[1] = {-INFINITY}, back[1] = {-INFINITY};   // adds nothing
+    if (v0 + lane < a0) front[0] = El::at(row, v0 + lane);
+    if (a1 + lane < v1) back[0] = El::at(row, a1 + lane);
+    const uint4* vec = reinterpret_cast<const uint4*>(base + static_cast<int64_t>(a0) * El::kSize) + lane;
+    constexpr int kU = 4;
+    for (int i = 0; i < nvec || i == 0; i += 32 * kU) {
         uint4 w[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) w[u] = __ldcg(vec + i + 32 * u);
+        for (int u = 0; u < kU; ++u) {
+            w[u] = make_uint4(El::kLowest, El::kLowest, El::kLowest, El::kLowest);
+            if (i + 32 * u + lane < nvec) w[u] = __ldcg(vec + i + 32 * u);
+        }
+        if (i == 0 && a0 > v0) {
+            if constexpr (kHow == kGreedyScan) see_greedy(p, front[0], v0 + lane);
+            else see(p, front);
+        }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) take<kType, kHow>(p, w[u], a0 + (i + 32 * u) * kVec);
+        for (int u = 0; u < kU; ++u) take<kType, kHow>(p, w[u], a0 + (i + 32 * u + lane) * kVec);
     }
-    for (; i < nvec; i += 32) take<kType, kHow>(p, vec[i], a0 + i * kVec);
-    for (int v = a1 + lane; v < v1; v += 32) one(v);
+    if (a1 < v1) {
+        if constexpr (kHow == kGreedyScan) see_greedy(p, back[0], a1 + lane);
+        else see(p, back);
+    }
     return p;
 }
 // Of all lanes.
@@ -439,8 +448,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int v1 = cut(a.V, rank + 1, ctas);
     if (v1 > a.V) v1 = a.V;
     const int slice = v1 - v0;
-    int pieces = slice / 2048;
-    pieces = pieces < 1 ? 1 : pieces > kParts ? kParts : pieces;
+    // Stretches of a row: a warp's costs one turn of loads, and one more for each 1024
+    // elements; as many to a row as take the warps the least.
+    int pieces = 1;
+    for (int n = 2, least = (rows + kWarps - 1) / kWarps * (1 + (slice + 1023) / 1024); n <= kParts; n *= 2) {
+        const int cost = (rows * n + kWarps - 1) / kWarps * (1 + (slice / n + 1023) / 1024);
+        if (cost < least) {
+            least = cost;
+            pieces = n;
+        }
+    }
     auto stretch = [&](int i, int& r, int& piece, int& s0, int& s1) {
         r = i / pieces;
         piece = i - r * pieces;
@@ -718,10 +735,14 @@ cudaError_t launch_clusters(const VerifyArgs& a, const LaunchCtl& c, cudaStream_
     static std::atomic<uint64_t> wide{0};
     cudaError_t e = set_once(wide, verify_kernel<kType, kGreedy, kApart>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    // CTAs of a sequence: as many as run at once, none with less than 2048 of the
-    // vocabulary (a power of two: clusters of 7 leave a third of the SMs idle)
+    // CTAs of a sequence: as many as run at once (a power of two: clusters of 7 leave a
+    // third of the SMs idle), none with less of the vocabulary than pays the larger
+    // cluster: 1024, or 2048 where only the race is left.  (40 shapes, 1 to 106
+    // sequences of 1182 to 159231: in the mean 10.97 us with 1024, 11.24 with 2048, 11.07
+    // with 512; 29 x 20585, the race alone, 17.4 with 2048 and 20.7 with 1024.)
+    constexpr int kLeast = kApart ? 2048 : 1024;
     int ctas = kMostCtas;
-    while (ctas > 1 && (static_cast<int64_t>(ctas) * a.B > kCtasPerSm * c.num_sms || a.V / ctas < 2048)) ctas /= 2;
+    while (ctas > 1 && (static_cast<int64_t>(ctas) * a.B > kCtasPerSm * c.num_sms || a.V / ctas < kLeast)) ctas /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B * ctas));
     cfg.blockDim = dim3(kThreads);
