@@ -597,10 +597,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // that may.  Few turns of a warp have any.  (Bounds of every ratio by a
         // reciprocal, and the largest of them every turn: 49.8 us for 64 x 6 x 131072
         // against 46.5.)
-        //   kSlack: t = fma(x - m, L, -log2 s), |t| <= 126, is within 126 2^-24 of the sum,
-        // and x - m, L and log2 s add 110 2^-24, 110 2^-26 and 50 2^-24 to it: 1.7e-5, as
-        // a factor 1.2e-5; ex2 and the exact one's own 2^-20 on top.  kTiny: below 2^-126
-        // a quick probability is 0.
+        //   kSlack: the exact probability has the same x - m.  Against it the quick one's
+        // exponent t = fma(x - m, L, -log2 s), |t| <= 126, is off by its rounding (2^-18), by
+        // L's (|x - m| <= 110: 2.1e-6) and by log2 s's (2^-19): with the ex2 and the exact
+        // one's rest 6e-6 as a factor, of p and of a q below p.  kTiny: below 2^-126 a
+        // quick probability is 0.
         constexpr float kSlack = 2e-5f, kTiny = 0x1p-120f;
         const float tl = -lg2(t.s), sl = -lg2(s.s);
         auto race = [&](bool with_q, Best& result) {
