@@ -253,3 +253,65 @@ def test_example_runs(capsys, monkeypatch):
     assert ex.main() == 0
     out = capsys.readouterr().out
     assert "of 16 experts" in out and "drafts kept" in out
+
+
+FIRST = """
+import torch, weight_only_quantized_qgemm_gb300 as q
+torch.cuda.set_device(0)
+E, M, K, N = 16, 700, 256, 272
+logits, x = torch.randn(M, E, device="cuda"), torch.randn(M, K, device="cuda").to(torch.bfloat16)
+W = torch.randint(0, 120, (E, N, K), device="cuda", dtype=torch.uint8)
+S = torch.rand(E, -(-N // 128), K // 128, device="cuda")
+t = torch.randn(40, 3, 9000, device="cuda")
+tok, u, z = t[:, :2].argmax(dim=2), torch.rand(40, 2, device="cuda"), torch.rand(40, 9000, device="cuda") + 0.1
+def step():
+    r = q.moe_route(logits, 2)
+    codes, scales = q.quantize_rows_e4m3(x, rows=r.rows)
+    y = q.qgemm_w8a8_grouped(codes, scales, W, S, r.offsets)
+    return q.moe_combine(y, r.rows, r.weights), *q.verify_drafts(t, tok, None, u, z)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+assert q.last_device_status() == 0
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    import subprocess
+    import sys
+    out = subprocess.run([sys.executable, "-c", FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "same" in out.stdout, out.stderr[-2000:]
+
+
+def test_threads_on_streams_of_their_own(q):
+    """Two host threads, each with a stream, inputs and sizes of its own."""
+    import threading
+    layer = [make_layer(8, 512, 256, 2, 21), make_layer(12, 256, 144, 4, 22)]
+    inputs = [torch.randn(m, h, device="cuda").to(torch.bfloat16) for m, h in ((90, 512), (2000, 256))]
+    logits = [torch.randn(30, 4, 9000, device="cuda"), torch.randn(3, 2, 5000, device="cuda")]
+    tokens = [t[:, :-1].argmax(dim=2) for t in logits]
+    want = [(layer[i](inputs[i]), *q.verify_drafts(logits[i], tokens[i])) for i in range(2)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = (layer[i](inputs[i]), *q.verify_drafts(logits[i], tokens[i]))
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                    wrong.append(i)
+        except Exception as e:   # noqa: BLE001
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and q.last_device_status() == 0
