@@ -24,8 +24,8 @@
 // block take 512 cycles, a third of a unit's round of barriers beside them: MMAs,
 // commit, fold (two waits, two loads of 64 columns, the products), release, the
 // issuer's wait.  Two accumulators of 256 columns are all that TMEM holds, so the
-// round sets the pace: 456 ns a unit at K = 16384, 2.8 PFLOP/s (374 without the
-// copies' power and traffic, 347 without the MMAs).
+// round sets the pace: 440 ns a unit at K = 16384, 2.9 PFLOP/s (at 456, 374 without
+// the copies' power and traffic, 347 without the MMAs).
 //
 // Every CTA lists the experts that hold rows, with the tiles in front of each, at
 // its start; workers then take tiles worker, worker + workers, ..., so that those
@@ -90,12 +90,14 @@ struct GLayout {
     static constexpr int kSRow = (NT + 4) * 4;
     static constexpr int kSSlot = kBlk * kSRow;
     static constexpr int kOutWarp = (kPair ? 32 : 16) * 64;   // a fold warp's 32 (16) rows x 32 weight rows of 16 bits
-    static constexpr int kFixed = kTabBytes + kSSlots * kSSlot + kFold * kOutWarp + 512;
+    static constexpr int kSpots = 16;                      // places of tiles
+    static constexpr int kFixed = kTabBytes + kSSlots * kSSlot + kFold * kOutWarp + kSpots * 16 + 512;
     static constexpr int kStages = (232448 - kFixed) / kStage / kIssuers * kIssuers;
     static constexpr int kTabOff = kStages * kStage;
     static constexpr int kSOff = kTabOff + kTabBytes;
     static constexpr int kOutOff = kSOff + kSSlots * kSSlot;
-    static constexpr int kBarOff = kOutOff + kFold * kOutWarp;
+    static constexpr int kSpotOff = kOutOff + kFold * kOutWarp;
+    static constexpr int kBarOff = kSpotOff + kSpots * 16;
     static constexpr int kNumBars = 2 * kStages + 2 * kBufs + 2 * kSSlots;
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
     static constexpr int kSmemBytes = kMiscOff + 32;
@@ -103,6 +105,9 @@ struct GLayout {
     static_assert(kBufs >= 2 && kBufs * kBlk * NT <= 512, "TMEM columns");
     static_assert(kXBlock % 1024 == 0 && kStage % 1024 == 0, "keep the 1024-byte swizzle alignment");
     static_assert(kCols % 16 == 0, "fragments");
+    // the fold reads a tile's place and the next one's, the warp that writes them is up
+    // to kSSlots tiles in front of it
+    static_assert(kSpots >= kSSlots + 2, "places");
     // a set and a stage always belong to one issuer, whose parity waits are then for
     // the phase after one that it has seen
     static_assert(kBufs % kIssuers == 0 && kStages % kIssuers == 0, "ring ownership");
@@ -440,6 +445,7 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
     Groups& tab = *reinterpret_cast<Groups*>(gbase + L::kTabOff);
     int* misc = reinterpret_cast<int*>(gbase + L::kMiscOff);
     volatile int* abort_flag = misc + 1;
+    int4* spots = reinterpret_cast<int4*>(gbase + L::kSpotOff);   // first row, rows, expert, block of 128 weight rows
     auto scales_at = [&](int s) { return reinterpret_cast<const float*>(gbase + L::kSOff + s * L::kSSlot); };
 
     const int warp = threadIdx.x >> 5;
@@ -476,8 +482,10 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
     }
     grid_dependents_launch();
     grid_dependency_wait();
-    if (warp == kWarpScales)
+    if (warp == kWarpScales) {
+        if (lane < L::kSpots) spots[lane] = make_int4(0, 0, 0, 0);   // valid for a fold that gave up waiting
         list_groups<NT>(p, tab, lane);
+    }
     tc_fence_before();
     __syncwarp();
     if constexpr (kPair) cluster_sync_all();   // the peer's barriers are set up too
@@ -550,7 +558,7 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
         int i = issuer, last = -1, ku = issuer;   // the unit, the last one issued, the unit's place in its tile
         bool ok = true;
         for (int t = worker; ok && t < tiles; t += p.workers) {
-            at.enter(tab, t, p.tn, rank);
+            if constexpr (!kPair) at.enter(tab, t, p.tn, rank);
             const uint32_t idesc = kPair ? kDescT : idesc_f8_e4m3(at.width());
             // the places in a stage of the operands of the M and the N side
             constexpr uint32_t m_off = kPair ? L::kXOff : 0, n_off = kPair ? 0 : L::kXOff;
@@ -588,14 +596,16 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
     } else if (warp == kWarpScales) {
         // The scales of this CTA's rows of each unit, by bulk copies: loads to
         // registers, however far ahead, held up a warp's other waits (290 ns a unit).
+        // And the tiles' places, which took the fold 1300 cycles a tile to work out (19 x
+        // 1024 rows, 2048 x 512: 38.6 us, 35.2 this way; 64 x 60, 2048 x 1024: 33.5, 29.6).
         if (lane == 0) {
             const uint64_t keep = policy_evict_last();
             Ring<L::kSSlots> rs(0);
             Pl at;
             at.g = 0;
-            int i = 0;
+            int i = 0, n = 0;
             bool ok = true;
-            for (int t = worker; ok && t < tiles; t += p.workers) {
+            for (int t = worker; ok && t < tiles; t += p.workers, ++n) {
                 at.enter(tab, t, p.tn, rank);
                 int first, rows;
                 at.scale_rows(rank, p.R, first, rows);
@@ -606,6 +616,7 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                         ok = wait_here(sempty(rs.slot), rs.phase ^ 1u, wc);
                         if (!ok) break;
                     }
+                    if (ku == 0) spots[n % L::kSpots] = make_int4(at.row0, at.rows, at.expert, at.nb);
                     const int nblk = kBlk == 1 || ku * kBlk + 2 <= p.KB ? kBlk : 1;
                     mbar_arrive_expect_tx(sfull(rs.slot), bytes * nblk);
                     for (int b = 0; b < nblk && bytes > 0; ++b)
@@ -629,8 +640,11 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
         static_assert(kCols % kChunk == 0, "whole loads");
         Ring<kBufs> rb(0);
         Ring<L::kSSlots> rg(0);
-        Pl at;
-        at.g = 0;
+        struct {
+            int row0, rows, expert, nb;
+            __device__ void enter(const int4& s) { row0 = s.x, rows = s.y, expert = s.z, nb = s.w; }
+        } at{};
+        int n = 0;   // tiles so far
         // W: [rows 0-15, 16-31][column group of 4][row, row + 8]; T: [column]
         float acc[kCols];
         const uint32_t to_issuer = kPair && !leader ? map_to_cta(dempty(0), 0) : dempty(0);
@@ -643,10 +657,10 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
         // The weight scales of the tile's block of rows: lane l holds those of unit
         // u0 + l, of 32 units at a time, fetched 32 units (or an epilogue) ahead.
         float sw[kBlk], sw_next[kBlk];
-        auto fetch = [&](const Pl& x, int u0) {
-            int nb = kPair ? x.nb - rank + g : x.nb;
+        auto fetch = [&](int expert, int block, int u0) {
+            int nb = kPair ? block - rank + g : block;
             nb = nb < p.sn ? nb : p.sn - 1;
-            const float* from = p.S + (static_cast<int64_t>(x.expert) * p.sn + nb) * p.KB;
+            const float* from = p.S + (static_cast<int64_t>(expert) * p.sn + nb) * p.KB;
 #pragma unroll
             for (int b = 0; b < kBlk; ++b) {
                 const int kb = (u0 + lane) * kBlk + b;
@@ -657,21 +671,20 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
             if ((ku & 31) == 0) {
 #pragma unroll
                 for (int b = 0; b < kBlk; ++b) sw[b] = sw_next[b];
-                if (ku + 32 < p.KU) fetch(at, ku + 32);
+                if (ku + 32 < p.KU) fetch(at.expert, at.nb, ku + 32);
             }
         };
-        if (worker < tiles) {
-            at.enter(tab, worker, p.tn, rank);
-            fetch(at, 0);
-        }
+        // a tile's place is there with the scales of its first unit
+        auto fetch_tile = [&](int t) {
+            if (t >= tiles) return;
+            wait_on(sfull(rg.slot), rg.phase, wc);
+            const int4 s = spots[n % L::kSpots];
+            fetch(s.z, s.w, 0);
+        };
+        fetch_tile(worker);
         for (int t = worker; t < tiles && !aborted(wc); t += p.workers) {
-            at.enter(tab, t, p.tn, rank);
-            auto fetch_next_tile = [&]() {
-                if (t + p.workers >= tiles) return;
-                Pl x = at;
-                x.enter(tab, t + p.workers, p.tn, rank);
-                fetch(x, 0);
-            };
+            at.enter(spots[n % L::kSpots]);
+            ++n;
 #pragma unroll
             for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
             if constexpr (kPair) {
@@ -707,7 +720,7 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                     acc[2 * i] = __uint_as_float(static_cast<uint32_t>(sums[i]));
                     acc[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(sums[i] >> 32));
                 }
-                fetch_next_tile();
+                fetch_tile(t + p.workers);
                 // its columns: the 128 weight rows of block nb, in order
                 const int n0 = nb * 128;
                 const int here = at.rows - rank * 128 - q * 32;   // rows of this warp that exist
@@ -753,7 +766,7 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                 }
             } else {
             // ---------------------------------------------------- W: a lane is a weight row
-            const int cols = at.width() - g * kCols;   // of this warp that the MMA writes; <= 0: none
+            const int cols = ((at.rows + 15) & ~15) - g * kCols;   // of this warp that the MMA writes; <= 0: none
             const int chunks = cols <= 0 ? 0 : cols >= kCols ? kCols / kChunk : (cols + kChunk - 1) / kChunk;
             for (int ku = 0; ku < p.KU; ++ku, rb.step(1), rg.step(1)) {
                 next_scales(ku);
@@ -794,8 +807,8 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                 __syncwarp();
                 arrive_if(lane == 0, sempty(rg.slot));   // the scales have been read, too
             }
-            fetch_next_tile();
-            const int nw = at.n0 + q * 32;          // the warp's first weight row
+            fetch_tile(t + p.workers);
+            const int nw = at.nb * 128 + q * 32;    // the warp's first weight row
             const int rows = at.rows - g * kCols;   // of this warp's columns that exist
             if (nw >= p.N || rows <= 0) continue;
             {
@@ -929,7 +942,8 @@ cudaError_t launch_grouped_nt(const GroupedArgs& a, const CUtensorMap& tmW, cons
 // shapes in all four forms (R 2 to 65536, 2 to 256 experts, N 65 to 8000, K 128 to
 // 7100) with 14 % of scatter; chosen by them, those take 0.2 % more time than with the best
 // of the four for each, and 220 other shapes 0.6 % (by the mean number of rows
-// alone, 10 / 20 / 52: 2.6 and 4.5 %).  Of the unlike sides, us for 16 / 32 / 64 / 256:
+// alone, 10 / 20 / 52: 2.6 and 4.5 %; with the places worked out by the scales' warp
+// since then, 0.5 and 0.7 %).  Of the unlike sides, us for 16 / 32 / 64 / 256:
 //   64 experts, 4096 x 2048:   8 rows 81 / 81 / 82 / 114, 24 rows 111 / 92 / 89 / 117, 96
 //   rows 312 / 210 / 177 / 132;  21 experts of 46 rows, 337 x 5072: 23 / 15 / 19 / 24;
 //   3 of 480, 216 x 2240: - / 9 / 11 / 15
