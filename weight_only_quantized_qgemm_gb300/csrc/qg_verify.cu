@@ -24,9 +24,9 @@
 //
 // All sums have a fixed order.  Bound by memory: every logit is read once, and two
 // rows of a sequence a second time with the noise.  64 x 6 rows of 131072 with their
-// drafts: 46.5 us, of them 27 the pass over the rows (152 MB of BF16, a third of the
+// drafts: 45.7 us, of them 27 the pass over the rows (152 MB of BF16, a third of the
 // sequences with fewer drafts: 5.6 TB/s under exponentials), 13 the race (67 MB), the rest the clusters'
-// start and the joins; 1 x 5 x 32768: 9.9 us, latency.
+// start and the joins; 1 x 5 x 32768: 9.7 us, latency.
 //
 // The sums: with L = log2 e and c a whole number that follows the largest x L from
 // below (by at most 32), s = sum 2^(x L - c): a term is one fma with one rounding,
@@ -201,10 +201,26 @@ __device__ __forceinline__ void see(Sum& p, const float (&x)[kCount]) {
         p.s *= ex2(p.c - c);
         p.c = c;
     }
-    float s = 0.0f;
+    if constexpr (kCount == 1) {
+        p.s += ex2(__fmaf_rn(x[0], kLog2e, -p.c));
+    } else {   // two terms an instruction: the pass is bound by what it issues
+        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kCount; ++i) s += ex2(__fmaf_rn(x[i], kLog2e, -p.c));
-    p.s += s;
+        for (int i = 0; i < kCount; i += 2) {
+            float t0, t1;
+            asm("{\n\t.reg .b64 v, l, c, t;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 l, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+                "fma.rn.f32x2 t, v, l, c;\n\tmov.b64 {%0, %1}, t;\n\t}"
+                : "=f"(t0), "=f"(t1)
+                : "f"(x[i]), "f"(x[i + 1]), "f"(kLog2e), "f"(-p.c));
+            t0 = ex2(t0);
+            t1 = ex2(t1);
+            asm("{\n\t.reg .b64 a, t;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\tadd.rn.f32x2 a, a, t;\n\t"
+                "mov.b64 {%0, %1}, a;\n\t}"
+                : "+f"(s0), "+f"(s1)
+                : "f"(t0), "f"(t1));
+        }
+        p.s += s0 + s1;
+    }
 }
 // The same about the maximum m' = c ln 2 (rounded): s' = s 2^(c - m' L).
 __device__ __forceinline__ Part about_max(Sum a) {
