@@ -514,7 +514,10 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                 // a weight tile of several row tiles is read again soon
                 const uint64_t pol_w = at.several ? keep : once;
                 const int wrow = at.expert * p.N + at.n0;
-                const int xrow = at.row0 + rank * L::kXRows;
+                // a half of a pair's tile that holds no row: zeros from behind the last row,
+                // which cost no traffic and little power (76 x 128 rows, 4096 x 8192: 487 us,
+                // 458 with them)
+                const int xrow = rank * L::kXRows < at.rows ? at.row0 + rank * L::kXRows : p.R;
                 for (int ku = 0; ku < p.KU; ++ku, ++i, rs.step(1)) {
                     if (i >= kStages) {
                         ok = wait_here(empty(rs.slot), rs.phase ^ 1u, wc);
