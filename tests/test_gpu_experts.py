@@ -492,3 +492,27 @@ def test_a_wait_that_runs_out_in_every_form(q, rows, sizes):
             q.set_fault_injection(-1)
     q.set_wait_timeout_ns(1_000_000_000)
     check_grouped(q, sizes, 512, 2048, "bf16")
+
+
+# one or two K blocks a tile, and more than the 32 units whose weight scales are held at a time
+@pytest.mark.parametrize("rows,sizes,N,K",
+                         [(256, [1500, 3000, 1] * 4, 2056, 16), (256, [1500, 3000, 1] * 4, 2056, 128),
+                          (256, [1500, 3000, 1] * 4, 2056, 144), (256, [700, 900] * 6, 640, 4368),
+                          (256, [700, 900, 30] * 6, 700, 8336), (32, [5, 17], 200, 8464),
+                          (32, [30, 31] * 20, 520, 8464), (64, [64, 60] * 40, 520, 8464), (64, [64, 60] * 40, 300, 16),
+                          (64, [30, 31, 20] * 40, 300, 128), (16, [3, 4] * 40, 300, 16), (16, [3, 4] * 40, 300, 272)],
+                         ids=lambda v: f"{len(v)}x{max(v)}" if isinstance(v, list) else str(v))
+def test_grouped_short_and_long_k(q, rows, sizes, N, K):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert q.grouped_tile_rows(sum(sizes), len(sizes), N, K, sms) == rows
+    check_grouped(q, sizes, N, K, "bf16")
+
+
+def test_grouped_rows_of_a_full_device(q):
+    """The largest number of experts, some with a row, some with many tiles."""
+    E = q.MAX_EXPERTS
+    g = gen(4)
+    sizes = torch.randint(0, 4, (E,), generator=g, device="cuda")
+    sizes[[0, 17, E - 1]] = torch.tensor([300, 0, 700], device="cuda")
+    check_grouped(q, sizes.tolist(), 264, 272, "bf16")
+    check_grouped(q, (sizes * 40).tolist(), 264, 272, "bf16")
