@@ -182,7 +182,7 @@ def test_values_beside_a_group_do_not_reach_it(q, rows):
     assert bool((Y[end:] == 7.0).all())
 
 
-@pytest.mark.parametrize("sizes", [[5, 2], [30, 31], [700, 300]], ids=["16 rows", "64 rows", "pairs"])
+@pytest.mark.parametrize("sizes", [[5, 2], [30, 31], [700, 300]], ids=lambda s: f"{max(s)} rows")
 def test_a_wait_that_runs_out_is_reported(q, sizes):
     """A weight load that is left out: the status says so, and the next call is right."""
     Xq, Xs, W, Ws, off = grouped_problem(sizes, 512, 2048, 3)
