@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
                     wait_on(sfull(rg.slot), rg.phase, wc);
                     const float f = __fmul_rn(scales_at(rg.slot)[(at.row0 & 3) + q * 32 + lane],
                                               __shfl_sync(0xffffffffu, sw[0], ku & 31));
+                    __syncwarp();   // every lane has read its factor: a shuffle orders no memory
                     arrive_if(lane == 0, sempty(rg.slot));
                     const uint64_t f2 = twice(f);
                     wait_on(dfull(rb.slot), rb.phase, wc);
