@@ -874,10 +874,21 @@ __global__ void __launch_bounds__(GLayout<NT, kPair>::kThreads, 1)
     }
 }
 
+// Zeros in the rows of the groups, which follow one another: from the first offset to
+// the largest, cut as list_groups cuts them.
 __global__ void zero_group_rows_kernel(const int32_t* offsets, int E, int R, void* Y, int64_t ldy, int y_type, int N) {
-    int rows = offsets[E];
-    rows = rows > R ? R : rows;
-    const int64_t total = rows > 0 ? static_cast<int64_t>(rows) * N : 0;
+    __shared__ int last;
+    int first = offsets[0];
+    first = first < 0 ? 0 : first > R ? R : first;
+    if (threadIdx.x == 0) last = first;
+    __syncthreads();
+    for (int e = 1 + static_cast<int>(threadIdx.x); e <= E; e += static_cast<int>(blockDim.x)) {
+        const int end = offsets[e];
+        atomicMax(&last, end > R ? R : end);
+    }
+    __syncthreads();
+    Y = static_cast<uint8_t*>(Y) + first * ldy * (y_type == QG_FP32 ? 4 : 2);
+    const int64_t total = static_cast<int64_t>(last - first) * N;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; t < total;
          t += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t at = t / N * ldy + t % N;

@@ -27,7 +27,7 @@ inline int grouped_box_rows(int tile_rows) { return tile_rows > 64 ? tile_rows /
 // grouped_box_rows).
 cudaError_t launch_grouped(const GroupedArgs& a, const CUtensorMap& tmW, const CUtensorMap& tmX, const LaunchCtl& c,
                            cudaStream_t st);
-// Zeros in rows [0, offsets[E]) of Y: the K = 0 product.
+// Zeros in the rows of the groups: the K = 0 product.
 cudaError_t launch_grouped_zero(const GroupedArgs& a, cudaStream_t st);
 
 }  // namespace qg
