@@ -1,0 +1,52 @@
+"""Host side of the experts' operators at the ends of what their contracts allow
+(no GPU)."""
+import pytest
+import torch
+
+from test_streams_host import Tensor, built, world  # noqa: F401
+
+
+class Part(Tensor):
+    """A stand-in for the first columns of a tensor whose memory ends after `floats`."""
+
+    def __init__(self, w, shape, strides, floats):
+        super().__init__(w, shape, torch.float32, strides=strides)
+        self.floats = floats
+
+    def storage_offset(self):
+        return 0
+
+    def untyped_storage(self):
+        return self
+
+    def nbytes(self):
+        return 4 * self.floats
+
+
+@pytest.mark.parametrize("K,shape,strides,floats,pitch", [
+    (128, (1, 37), (64, 1), 64, 40),      # the first columns of a padded row
+    (128, (1, 37), (37, 1), 40, 40),      # a lone row's stride does not count
+    (128, (1, 40), (40, 1), 40, 40),
+    (128, (1, 64), (64, 1), 64, 40),
+    (256, (2, 37), (64, 1), 128, 64),
+    (256, (2, 37), (64, 1), 104, 64),
+])
+def test_scales_without_their_padding(world, K, shape, strides, floats, pitch):   # noqa: F811
+    q, u8 = world.q, torch.uint8
+    q.qgemm_w8a8_grouped(Tensor(world, (37, K), u8), Part(world, shape, strides, floats), Tensor(world, (2, 8, K), u8),
+                         Tensor(world, (2, 1, K // 128), torch.float32), Tensor(world, (3,), torch.int32))
+    name, _, args = world.calls[-1]
+    assert name == "qgemm_w8a8_grouped" and args[3] == pitch
+    q.quantize_rows_e4m3(Tensor(world, (37, K), torch.bfloat16), X_scale=Part(world, shape, strides, floats))
+    name, _, args = world.calls[-1]
+    assert name == "qg_quantize_rows_e4m3" and args[10] == pitch
+
+
+@pytest.mark.parametrize("K,shape,strides,floats", [(128, (1, 37), (37, 1), 37), (128, (1, 37), (37, 1), 39),
+                                                    (256, (2, 37), (64, 1), 101), (256, (2, 37), (64, 1), 103)])
+def test_scales_whose_memory_ends_at_once_are_refused(world, K, shape, strides, floats):   # noqa: F811
+    q, u8 = world.q, torch.uint8
+    with pytest.raises(ValueError, match="multiple of 4"):
+        q.qgemm_w8a8_grouped(Tensor(world, (37, K), u8), Part(world, shape, strides, floats), Tensor(world, (2, 8, K), u8),
+                             Tensor(world, (2, 1, K // 128), torch.float32), Tensor(world, (3,), torch.int32))
+    assert not world.calls

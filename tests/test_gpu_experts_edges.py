@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_util import qg
-from test_gpu_experts import DTYPES
+from test_gpu_experts import DTYPES, gen, offsets_of
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,29 @@ def test_grouped_without_k_and_many_experts(q):
                              torch.empty(E, 5, 0, dtype=torch.uint8, device="cuda"), torch.empty(E, 1, 0, device="cuda"),
                              off.cuda(), Y=Y)
         assert Y[:, 0].tolist() == [3.0] * 2 + [0.0] * 7 + [3.0] * 3
+
+
+@pytest.mark.parametrize("K", [16, 128, 144, 256])
+@pytest.mark.parametrize("rows", [1, 37, 300])
+def test_the_first_columns_of_scales(q, K, rows):
+    """The quantiser's scales without their padding, in one row of scales and in several."""
+    g = gen(K + rows)
+    sizes = [rows, 0, 6]
+    R = sum(sizes)
+    X = torch.randn(R, K, generator=g, device="cuda").to(torch.bfloat16)
+    codes, scales = q.quantize_rows_e4m3(X)
+    W = torch.randint(0, 120, (3, 72, K), generator=g, device="cuda", dtype=torch.uint8)
+    Ws = torch.rand(3, 1, -(-K // 128), generator=g, device="cuda")
+    off = offsets_of(sizes)
+    want = q.qgemm_w8a8_grouped(codes, scales, W, Ws, off)
+    assert torch.equal(q.qgemm_w8a8_grouped(codes, scales[:, :R], W, Ws, off), want)
+    if R % 4:   # nothing behind the last scale
+        bare = torch.empty((scales.shape[0] - 1) * scales.shape[1] + R, device="cuda")
+        bare = bare.as_strided((scales.shape[0], R), (scales.shape[1], 1))
+        bare.copy_(scales[:, :R])
+        with pytest.raises(ValueError, match="multiple of 4"):
+            q.qgemm_w8a8_grouped(codes, bare, W, Ws, off)
+    # written in place, and nothing beside them
+    kept = torch.full_like(scales, -7.0)
+    again, out = q.quantize_rows_e4m3(X, X_scale=kept[:, :R])
+    assert torch.equal(out, scales[:, :R]) and torch.equal(again, codes) and bool((kept[:, R:] == -7.0).all())

@@ -802,7 +802,8 @@ def quantize_rows_e4m3(X, gated: bool = False, rows=None, num_rows=None, out_row
     (optional, int32, one element on the device, e.g. ``route.offsets[-1:]``): only
     the rows before it are read.  Output rows that nothing goes to are left as they
     were.  Returns (Xq uint8 [out_rows, K], X_scale float32 [ceil(K/128), ldsx]) with
-    ldsx = out_rows rounded up to 32.  Xq and X_scale (optional) are written in place.
+    ldsx = out_rows rounded up to 32.  Xq and X_scale (optional: [ceil(K/128), out_rows
+    or more], row stride a multiple of 4) are written in place.
     """
     if stream is not None and (Xq is None or X_scale is None) and _elsewhere(stream):
         return _on_stream(stream, quantize_rows_e4m3, X, gated, rows, num_rows, out_rows, Xq, X_scale)
@@ -850,6 +851,8 @@ def quantize_rows_e4m3(X, gated: bool = False, rows=None, num_rows=None, out_row
         r, c, lds = _rows(X_scale, "X_scale")
         if r != KB or c < out_rows or X_scale.device != dev:
             raise ValueError("X_scale must be [ceil(K/128), out_rows or more] on X's device")
+        if r == 1:   # no row behind it: any stride does
+            lds = -(-out_rows // 4) * 4
     if rows is not None and top_k == 0:   # rows that go nowhere
         return Xq, X_scale
     st = _raw_stream(index) if stream is None else _stream_ptr(stream)
@@ -866,9 +869,10 @@ def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None,
     FP32 sums per 128-wide K block.
 
     Xq: uint8 (E4M3 codes) or float8_e4m3fn CUDA [R, K] (row stride a multiple of
-    16) and X_scale: float32 [ceil(K/128), R or more] as :func:`quantize_rows_e4m3`
-    returns them; W: uint8 or float8_e4m3fn [E, N, K] contiguous; W_scale: float32
-    [E, ceil(N/128), ceil(K/128)] contiguous; offsets: int32 [E + 1] on the device.
+    16) and X_scale: float32 [ceil(K/128), R or more] (row stride a multiple of 4) as
+    :func:`quantize_rows_e4m3` returns them, or its first R columns; W: uint8 or
+    float8_e4m3fn [E, N, K] contiguous; W_scale: float32 [E, ceil(N/128), ceil(K/128)]
+    contiguous; offsets: int32 [E + 1] on the device.
     Y (optional): [R, N] with unit column stride, in bfloat16 (the default), float16
     or float32 (out_dtype).  Rows of no expert are left as they were.
     """
@@ -885,8 +889,6 @@ def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None,
         raise TypeError("W and W_scale must be contiguous")
     R, K, ldq = _rows(Xq, "Xq")
     sr, sc, lds = _rows(X_scale, "X_scale")
-    if sr == 1:
-        lds = sc
     if W.dim() != 3:
         raise ValueError("W must be [E, N, K]")
     E, N, WK = W.shape
@@ -895,6 +897,12 @@ def qgemm_w8a8_grouped(Xq, X_scale, W, W_scale, offsets, out_dtype=None, Y=None,
     KB = -(-K // 128)
     if WK != K or sr != KB or sc < R or W_scale.shape != (E, -(-N // 128), KB):
         raise ValueError("shape mismatch between Xq, X_scale, W and W_scale")
+    fours = -(-R // 4) * 4   # the scales are read by fours
+    if sr == 1:   # no row behind it: any stride does
+        lds = fours
+    if sc < fours and 0 < sr and \
+            X_scale.untyped_storage().nbytes() < 4 * (X_scale.storage_offset() + (sr - 1) * lds + fours):
+        raise ValueError("X_scale's memory must reach up to a multiple of 4 columns")
     dev = Xq.device
     index = dev.index
     if index != _current_device():   # where the library launches
