@@ -50,3 +50,21 @@ def test_scales_whose_memory_ends_at_once_are_refused(world, K, shape, strides, 
         q.qgemm_w8a8_grouped(Tensor(world, (37, K), u8), Part(world, shape, strides, floats), Tensor(world, (2, 8, K), u8),
                              Tensor(world, (2, 1, K // 128), torch.float32), Tensor(world, (3,), torch.int32))
     assert not world.calls
+
+
+@pytest.mark.parametrize("sms", [1, 2, 3, 7, 8, 15, 16, 17, 64, 152])
+def test_the_router_s_counts_fit_16_bits(built, sms):   # noqa: F811
+    """A CTA's tokens, whatever the number of SMs: their counts by expert, of 16 bits,
+    would wrap."""
+    import ctypes
+    need = built.lib["_ZN2qg21route_workspace_bytesEiii"]   # qg::route_workspace_bytes(M, E, sms)
+    need.restype, need.argtypes = ctypes.c_size_t, [ctypes.c_int] * 3
+    for E in (8, 256, 1024):
+        for M in [1, 16, 17, 32, 33, 1000, 65535, 65536, 2 * 65535, 2 * 65535 + 1, 17 * 2 ** 15, 2 ** 20 - 1, 2 ** 20]:
+            table = need(M, E, sms)
+            ctas = table // (2 * E)   # E is a multiple of 8
+            assert table == 2 * E * ctas
+            if ctas:
+                assert 1 < ctas <= M and -(-M // ctas) < 2 ** 16
+            else:      # one CTA, whose counts have 32 bits
+                assert M < 65536 or sms == 1

@@ -332,16 +332,20 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, const void* row,
     weight = sum > 0.0f ? w * (a.scale / sum) : 0.0f;
 }
 
-// Tokens of a CTA and of a warp.
+// The CTAs' counts by expert have 16 bits, and a token takes an expert once: so many
+// tokens a CTA at most, which a device of few SMs would pass.
+constexpr int kMostTokens = 0xFFFF;
+
 inline int route_ctas(int M, int E, int sms) {
     // up to a token a warp one CTA does it all (64 tokens, 256 experts: 10.4 us; over
     // eight CTAs with the second launch 8.7)
-    const int warps = route_warps(E), ctas = (M + 7) / 8;
-    return M <= warps ? 1 : ctas < sms ? ctas : sms;
+    if (M <= route_warps(E)) return 1;
+    const int most = (M + 7) / 8, least = (M + kMostTokens - 1) / kMostTokens;
+    const int ctas = most < sms ? most : sms;
+    return ctas < least ? least : ctas;
 }
 
-// The CTAs' counts by expert: 16 bits each (a CTA has at most 2^20 / 64 tokens, each
-// of which takes an expert once), in rows of whole 16 bytes.
+// The table of the counts: rows of whole 16 bytes.
 __host__ __device__ inline int route_pitch(int E) { return (E + 7) / 8 * 8; }
 
 // where[e] = the exclusive prefix over the experts of total[e] (each a CTA's or
