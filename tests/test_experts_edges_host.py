@@ -68,3 +68,22 @@ def test_the_router_s_counts_fit_16_bits(built, sms):   # noqa: F811
                 assert 1 < ctas <= M and -(-M // ctas) < 2 ** 16
             else:      # one CTA, whose counts have 32 bits
                 assert M < 65536 or sms == 1
+
+
+def test_what_is_kept_of_sizes_stays_small(world):   # noqa: F811
+    """The scratch memory's size is kept for sizes that come again, not for every one ever seen."""
+    q, i64 = world.q, torch.int64
+    q._scratch_need.clear()
+    most = 0
+    for n in range(1, 2500):
+        q.moe_route(Tensor(world, (n, 64), torch.float32), 4)
+        q.verify_drafts(Tensor(world, (n, 2, 100), torch.float32), Tensor(world, (n, 1), i64))
+        most = max(most, len(q._scratch_need))
+    assert 2 <= most <= 2048
+    assert sum(name in ("qg_moe_route", "qg_verify_drafts") for name, _, _ in world.calls) == 2 * 2499
+    world.calls.clear()
+    q._scratch_need.clear()
+    for _ in range(3):
+        q.moe_route(Tensor(world, (5, 64), torch.float32), 4)
+    assert [c[0] for c in world.calls] == ["qg_moe_route_workspace_bytes"] + 3 * ["qg_moe_route"]
+    q._scratch_need.clear()

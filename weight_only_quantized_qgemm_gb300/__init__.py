@@ -711,7 +711,8 @@ class MoeRoute(NamedTuple):
     rows: Any      # int32 [M, top_k]
 
 
-_scratch_need = {}
+_scratch_need = {}   # of the sizes seen lately
+_MOST_NEEDS = 1024   # prompts have many lengths: then it starts anew
 
 
 def _scratch(key, ask, workspace, device):
@@ -721,6 +722,8 @@ def _scratch(key, ask, workspace, device):
     allocator: calls of other streams and captured graphs share none."""
     need = _scratch_need.get(key)
     if need is None:
+        if len(_scratch_need) >= _MOST_NEEDS:
+            _scratch_need.clear()
         need = _scratch_need[key] = int(ask())
     if need == 0:
         return None, None, 0
