@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_util import qg
-from test_gpu_experts import DTYPES, gen, offsets_of
+from test_gpu_experts import DTYPES, gen, offsets_of, silu_mul
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,33 @@ def test_the_first_columns_of_scales(q, K, rows):
     kept = torch.full_like(scales, -7.0)
     again, out = q.quantize_rows_e4m3(X, X_scale=kept[:, :R])
     assert torch.equal(out, scales[:, :R]) and torch.equal(again, codes) and bool((kept[:, R:] == -7.0).all())
+
+
+# ----------------------------------------------------------------- row quantiser
+@pytest.mark.parametrize("dtype,gates", [("bf16", [-80.0, -86.5, -87.0, -87.5, -88.0, -88.5]),
+                                         ("fp16", [-80.0, -87.25, -87.375, -87.5, -88.0, -88.5, -88.6875])])
+@pytest.mark.parametrize("up", [1.0, 1e4, 1e37])
+def test_gates_that_let_next_to_nothing_through(q, dtype, gates, up):
+    """Down to where the formula's exponential passes FP32 (g = -88.7): the product
+    counts where the value is large, or the block holds nothing larger."""
+    if dtype == "fp16" and up > 6e4:
+        up = 6e4
+    g = gen(len(gates))
+    M, K = len(gates), 256
+    X = torch.empty((M, 2 * K), device="cuda")
+    X[:, :K] = torch.tensor(gates, device="cuda")[:, None]
+    X[:, K:] = torch.randn(M, K, generator=g, device="cuda").clamp(-1, 1) * up
+    X = X.to(DTYPES[dtype])
+    codes, scales = q.quantize_rows_e4m3(X, gated=True)
+    v = silu_mul(X).view(M, K // 128, 128)
+    amax = v.abs().amax(dim=2)
+    s = scales[:, :M].t().double()
+    # |g| <= 88.7: the exponent's product with log2 e is off by 2^-18 and 128 x 1.4e-8 (of
+    # the constant), times ln 2: 4e-6; exponential, reciprocal and products 6e-7; a
+    # subnormal scale has 20 bits at least (amax > 1e-37), half a step 2^-20
+    tol = 2.0 ** -17
+    assert bool((amax > 1e-37).all())
+    assert bool(((s * 448 - amax).abs() <= tol * amax).all())
+    ref = v / s[:, :, None]
+    off = (codes.view(torch.float8_e4m3fn).double().view_as(v) - ref).abs()
+    assert bool((off <= (2.0 ** -4 + tol) * ref.abs() + 2.0 ** -10).all())

@@ -559,12 +559,15 @@ __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
 // silu(g) u in 32 bits: g u / (1 + e^-g).  The exponential is good to
 // 2^-22 + |g| 2^-24, the reciprocal to 2^-23: far below an E4M3 step (2^-4).  With
 // subnormals as zeros (an e^-g below 2^-126 is nothing beside 1), each is one
-// instruction; without, they took 40 % of the kernel's.
+// instruction; without, they took 40 % of the kernel's.  The reciprocal is that of a
+// quarter of the sum, and a quarter of g is taken (exact: g has 16 bits), so that it
+// stays normal up to the sum's overflow at g = -88.7; at 4 2^-126 a gate of -87.4 would
+// let nothing through, however large u is.
 __device__ __forceinline__ float gate(float g, float u) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * u;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmaf_rn(e, 0.25f, 0.25f)));
+    return 0.25f * g * r * u;
 }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
@@ -592,7 +595,7 @@ constexpr int kQuantCtas = 4;
 // Resident warps walk over jobs (512 columns of a row, 16 of them a lane, so that a
 // lane's codes are one 16-byte store and eight lanes share a block), the next
 // job's loads on their way while this one's codes are worked out.  Bound by
-// memory: the gate on 32763 x 2 x 2048 50.7 us (6.7 TB/s, the copy rate); 4096 x 5120
+// memory: the gate on 32763 x 2 x 2048 51 us (6.6 TB/s, 0.97 of the copy rate); 4096 x 5120
 // to eight rows each 40 us (5.4 TB/s: scattered rows of 5 KB and, 3 us of it, scales).
 template <bool kBf16, bool kGated, bool kPlaces>
 __global__ void __launch_bounds__(kQuantWarps * 32, kQuantCtas)
