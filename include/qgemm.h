@@ -455,7 +455,8 @@ qg_status qg_moe_route(const void *logits, int type, int64_t ld, const float *bi
  *                 silu(X[m, k]) * X[m, K + k], silu(g) = g / (1 + exp(-g)), in FP32
  *   rows          device, int32 [M, top_k], or NULL: row m's codes and scales go to
  *                 rows rows[m, 0 .. top_k - 1] of the output (one outside 0 ..
- *                 out_rows - 1: nowhere) instead of row m
+ *                 out_rows - 1: nowhere) instead of row m; no output row may be
+ *                 named by two rows of X
  *   num_rows      device, one int32, or NULL: only rows m < *num_rows are read
  * Output rows that nothing goes to are left as they were, codes and scales both.
  *   X        device, QG_BF16 or QG_FP16 [M, ldx], 16-byte aligned, ldx >= K (gated:
@@ -503,7 +504,8 @@ qg_status qgemm_w8a8_grouped(const uint8_t *Xq, int64_t ldxq, const float *X_sca
  * in FP32, in the order of j, rounded once.  A row outside 0 .. R - 1 counts as
  * zeros.
  *   Y, residual (or NULL), out   device, QG_BF16, QG_FP16 or QG_FP32 (type), row
- *            strides ldy, ldr, ldo >= K; out may be residual
+ *            strides ldy, ldr, ldo >= K; out may be residual, but share no memory
+ *            with Y
  *   rows, weights   device, int32 and FP32 [M, top_k]
  *   M, R, K, top_k  0 <= M <= 2^22, 0 <= R < 2^31, K <= 2^30, M K <= 2^38,
  *            1 <= top_k <= 32

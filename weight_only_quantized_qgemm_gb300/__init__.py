@@ -948,7 +948,7 @@ def moe_combine(Y, rows, weights, residual=None, out=None, stream=None):
 
     Y: bf16, fp16 or fp32 CUDA [R, K]; rows: int32 and weights: float32 [M, top_k] as
     :func:`moe_route` returns them (a row of -1 counts as zeros); residual (optional)
-    and out (optional): [M, K] of Y's type, which may be the same tensor.
+    and out (optional): [M, K] of Y's type, which may be the same tensor, apart from Y.
     """
     if stream is not None and out is None and _elsewhere(stream):
         return _on_stream(stream, moe_combine, Y, rows, weights, residual, out)

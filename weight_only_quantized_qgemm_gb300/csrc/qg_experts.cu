@@ -587,9 +587,9 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 }
 
 constexpr int kQuantWarps = 8;
-// CTAs per SM, 2 / 3 / 4 / 5 / 6: 41 / 45 / 40.5 / 42 / 45 us for 4096 x 5120 to eight
-// rows each, 62 / 57 / 50.7 / 54 / 67 for the gate on 32763 x 2 x 2048 (from 5 on
-// registers are spilled).
+// CTAs per SM: as many as spill no registers (from 5 on they do).  Two shapes with 2 /
+// 3 / 4 / 5 / 6: 41 / 45 / 40.5 / 42 / 45 us for 4096 x 5120 to eight rows each, 62 / 57 /
+// 50.7 / 54 / 67 for the gate on 32763 x 2 x 2048.
 constexpr int kQuantCtas = 4;
 
 // Resident warps walk over jobs (512 columns of a row, 16 of them a lane, so that a

@@ -234,7 +234,7 @@ __device__ __forceinline__ uint32_t pack_out(float lo, float hi, int y_type) {
 // chunks of a row exchanged by (row / 2) % 4, so that neither side meets bank
 // conflicts: the first `here` rows and `bytes` bytes of each, kWord at a time (a warp
 // covers 64 bytes of 2 kWord / 4 rows a store), eight loads in front of their stores.
-// (19 x 1024 rows, 512 x N, BF16: N = 2048 39 us, 2044 40, 2041 46; FP32 51, 53, 58.
+// (19 x 1024 rows, 512 x N, BF16: N = 2048 35 us, 2044 37, 2041 43; FP32 48, 50, 61.
 // With a load and a multiplied address in front of each store of an element: 74.)
 template <int kWord>
 struct Word {
