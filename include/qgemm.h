@@ -546,8 +546,8 @@ qg_status qg_moe_combine(const void *Y, int type, int64_t ldy, const int32_t *ro
  *   workspace   of qg_verify_drafts_workspace_bytes(B, G, V) bytes (0 for few
  *               sequences), 16-byte aligned, scratch as qg_moe_route's
  * A row with a NaN or +inf (greedy: a NaN is never the largest), or with nothing
- * but -inf, keeps no draft, and the token drawn from it is -1.  Rows behind a
- * sequence's length are not read.
+ * but -inf, keeps no draft, and the token drawn from it is -1 (from p_n where it is
+ * the draft's row that is such a one).  Rows behind a sequence's length are not read.
  */
 size_t qg_verify_drafts_workspace_bytes(int B, int G, int V);
 qg_status qg_verify_drafts(const void *target, int type, int64_t t_seq, int64_t t_row, const void *draft,

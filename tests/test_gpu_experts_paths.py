@@ -140,3 +140,24 @@ def test_lone_sequences_that_are_decided(q, B, G, V, kind, dtype):
         if compared >= 3:
             return
     assert compared >= 3
+
+
+@pytest.mark.parametrize("B", [5, 25])
+def test_draft_rows_that_say_nothing(q, B):
+    """A draft's row with a NaN or +inf, or with nothing but -inf, keeps no draft, and the
+    token is drawn from the target's row alone."""
+    t, d, tok, u, e = problem(B, 2, 9000, "fp32", 3)
+    tok[:, 0] = t[:, 0].argmax(dim=1)
+    u[:, 0] = 0.0
+    d[0, 0, 8999] = math.nan
+    d[1, 0] = -math.inf
+    d[2, 0, 5] = math.inf
+    d[3, 0] = math.nan
+    got = q.verify_drafts(t, tok, d, u, e)
+    p = torch.softmax(t[:, 0].double(), dim=1) / e.double()
+    top = p.topk(2, dim=1)
+    for b in range(4):
+        assert int(got.accepted[b]) == 0
+        if float(top.values[b, 0]) * (1 - 2.0 ** -18) > float(top.values[b, 1]):
+            assert int(got.tokens[b, 0]) == int(top.indices[b, 0])
+    assert bool((got.accepted[4:] >= 1).all())

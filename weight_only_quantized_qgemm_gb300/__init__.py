@@ -801,7 +801,8 @@ def quantize_rows_e4m3(X, gated: bool = False, rows=None, num_rows=None, out_row
     X: bf16 or fp16 CUDA [M, K] (row stride a multiple of 8, K % 16 == 0); gated:
     [M, 2 K], and silu(X[:, :K]) * X[:, K:] is quantised.  rows (optional, int32
     [M, top_k] as :func:`moe_route` returns it): row m goes to rows rows[m, :] of the
-    output (-1: nowhere), of out_rows rows (M * top_k when absent).  num_rows
+    output (-1: nowhere; no place may be named by two rows), of out_rows rows (M * top_k
+    when absent).  num_rows
     (optional, int32, one element on the device, e.g. ``route.offsets[-1:]``): only
     the rows before it are read.  Output rows that nothing goes to are left as they
     were.  Returns (Xq uint8 [out_rows, K], X_scale float32 [ceil(K/128), ldsx]) with
